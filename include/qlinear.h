@@ -466,6 +466,98 @@ ql_status ql_device_status_detail(ql_stream_t stream, uint32_t* flags, uint64_t*
  * A debugging build: slower, same results for in-range programs. 0 otherwise. */
 int ql_bounds_checked(void);
 
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (E2M1): casts and products.
+ *
+ * Formats (groups lie along a row, the reduction axis of the products):
+ *   QL_FP4_NV  groups of 16 with an E4M3 scale s = E4M3(amax / (6 t)) held in
+ *              [2^-9, 448], and one fp32 scale t > 0 per tensor (a device
+ *              pointer; NULL is 1). An element stands for E2M1 * s * t.
+ *   QL_FP4_MX  groups of 32 with a power of two s = 2^ceil(log2(amax / 6)),
+ *              exponent held in [-127, 127] and stored as UE8M0. No t.
+ * E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and E4M3 are rounded to nearest,
+ * ties to even; x / (s t) is correctly rounded first (t >= 2^-60). A group that
+ * holds an infinity or a NaN is NaN in every product.
+ *
+ * Layouts:
+ *   codes   bytes [rows][ld], element 2j in the low half of byte j; ld a
+ *           multiple of 16 bytes, rows 16-byte aligned; the unused half byte
+ *           of an odd number of columns is zero
+ *   scales  uint8 blocks of 128 rows x 4 groups, [ceil(rows/128)]
+ *           [ceil(groups/4)][512]: row r, group g of a block at byte
+ *           (r % 32) * 16 + (r / 32) * 4 + g; 16-byte aligned. Bytes of groups
+ *           past the last are zero; bytes of rows past the last are unspecified.
+ *   experts rows sorted by expert, offsets int32 [experts + 1] on the device:
+ *           expert e has rows [offsets[e], offsets[e+1]) of [0, m). A row-wise
+ *           cast starts a new 128-row scale block with every expert; a
+ *           column-wise cast starts every expert's columns (its rows) on a
+ *           multiple of 256 and fills up with zeros. Offsets are read on the
+ *           device, so nothing waits for them; offsets out of order or outside
+ *           [0, m] are clamped by the products and make ql_device_status return
+ *           QL_ERR_INVALID_ARG. At most 512 experts.
+ * ------------------------------------------------------------------------- */
+#define QL_FP4_NV 0
+#define QL_FP4_MX 1
+
+/* Bytes of the scales of a cast of `rows` rows and k columns; experts > 0: of a
+ * row-wise cast by expert. -1 for an unknown format or a negative size. */
+int64_t fp4_scale_bytes(int64_t rows, int64_t k, int fmt, int experts);
+/* Columns that the codes of a column-wise cast of m rows have room for: m
+ * rounded up to 128; with experts > 0 what any split of m rows over them needs,
+ * which is then also the cast's number of columns (its scale blocks run over
+ * all of them). */
+int64_t fp4_column_extent(int64_t m, int experts);
+
+/* *scale = the least power of two t with max|x| <= 2688 t (2688 = 6 * 448), at
+ * least 2^-80; NaN if x holds an infinity or a NaN. x [m, k], any strides. */
+ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k, int64_t x_stride_m,
+                           int64_t x_stride_k, float* scale, ql_stream_t stream);
+
+/* Casts the rows of x [batch, m, k] (any strides): q [batch * m][ldq], sf one
+ * set of scale blocks per batch entry. With offsets (batch must be 1) the scale
+ * blocks are by expert; rows of no expert get neither codes nor scales. */
+ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
+                   int64_t x_stride_m, int64_t x_stride_k, int fmt, const float* scale, uint8_t* q, int64_t ldq,
+                   uint8_t* sf, const int32_t* offsets, int experts, ql_stream_t stream);
+
+/* Casts x [batch, m, k] (contiguous rows) along its rows and along its columns
+ * from one read: (q_rows, sf_rows) as fp4_cast, and (q_cols, sf_cols) the cast
+ * of x^T: codes [batch * k][ldc], ldc >= fp4_column_extent(m, experts) / 2.
+ * q_rows and sf_rows may both be NULL. */
+ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
+                        int64_t x_stride_m, int fmt, const float* scale, uint8_t* q_rows, int64_t ldr,
+                        uint8_t* sf_rows, uint8_t* q_cols, int64_t ldc, uint8_t* sf_cols, const int32_t* offsets,
+                        int experts, ql_stream_t stream);
+
+/* out [m, k] = the values that codes and scales of one cast (no experts) stand
+ * for, as fp32 or rounded once to bf16; row stride ldo. */
+ql_status fp4_dequant(const uint8_t* q, int64_t ldq, const uint8_t* sf, int fmt, const float* scale, int64_t m,
+                      int64_t k, void* out, ql_dtype out_dtype, int64_t ldo, ql_stream_t stream);
+
+/* D [m, n] = X W^T: X [m, k], W [n, k] row-wise casts of one format, scales
+ * x_scale and w_scale (device, NULL is 1); fp32 accumulation, D bf16 or fp32
+ * (fp32: accumulate != 0 adds to D). */
+ql_status gemm_fp4_nt(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale, const uint8_t* w,
+                      int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, ql_dtype d_dtype,
+                      int64_t ldd, int64_t m, int64_t n, int64_t k, int accumulate, ql_stream_t stream);
+
+/* Experts: rows [offsets[e], offsets[e+1]) of D [m, n] = the same rows of X
+ * times W[e]^T. X [m, k] cast with the offsets, W [experts, n, k] cast as a
+ * batch. Rows of no expert are not written. k == 0 is refused. */
+ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale,
+                             const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt,
+                             void* d, ql_dtype d_dtype, int64_t ldd, const int32_t* offsets, int experts, int64_t m,
+                             int64_t n, int64_t k, ql_stream_t stream);
+
+/* Experts' weight gradient: D[e] [m, n] (+)= Y_e^T X_e over expert e's rows of
+ * the `tokens` rows. y and x are column-wise casts by expert of Y [tokens, m]
+ * and X [tokens, n]: codes [m][ldy], [n][ldx]. D fp32 [experts * m][ldd]. The
+ * D of an expert without rows is zero (unchanged with accumulate). */
+ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sfy, const float* y_scale,
+                                const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale, int fmt,
+                                float* d, int64_t ldd, const int32_t* offsets, int experts, int64_t tokens, int64_t m,
+                                int64_t n, int accumulate, ql_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,8 @@
 #include "../../include/qlinear.h"
 #include "bounds.cuh"
 #include "cast.cuh"
+#include "fp4.cuh"
+#include "fp4_gemm.cuh"
 #include "gemm.cuh"
 
 namespace {
@@ -130,6 +132,37 @@ ql_status gemm_common(const uint8_t* a, int64_t lda, const void* sfa, int64_t sa
         L.drecip = fp8out->drecip;
     }
     return from_cuda(ql::launch_gemm(L, st, effective_sms(di)));
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit operators: shared argument checks and the launch of a product.
+// ---------------------------------------------------------------------------
+constexpr int64_t kInt31 = int64_t(1) << 31;
+
+// Codes of `rows` rows of `k` columns: alignment and row stride.
+ql_status fp4_operand(const uint8_t* q, int64_t ld, const uint8_t* sf, int64_t k) {
+    if (q == nullptr || sf == nullptr || ld < (k + 1) / 2) return QL_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(sf) || ld % 16 != 0) return QL_ERR_ALIGNMENT;
+    return QL_OK;
+}
+
+int64_t fp4_row_blocks(int64_t rows, int experts) { return (rows + 127) / 128 + (experts > 0 ? experts : 0); }
+
+// A launch of the product described by `a` (operands checked, sizes positive).
+ql_status fp4_product(ql::Fp4GemmArgs& a, cudaStream_t st) {
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    a.dev_status = di.status;
+    a.wait_limit_ns = static_cast<uint64_t>(g_wait_limit_ms.load()) * 1000000ull;
+    a.stall_producer = g_stall_producer.load();
+    const int sms = effective_sms(di);
+    const int path = g_gemm_path.load();
+    // 256 x 256 tiles on CTA pairs when there is one for every other pair of
+    // SMs; narrower tiles on one SM otherwise
+    const int64_t per = a.form == ql::kFp4RagRows ? (a.m / a.experts > 0 ? a.m / a.experts : 1) : a.m;
+    const int64_t tiles = ((per + 255) / 256) * ((a.n + 255) / 256) * (a.form == ql::kFp4Plain ? 1 : a.experts);
+    const bool pair = path == 3 || (path != 2 && path != 4 && per > 128 && tiles >= sms / 4);
+    return from_cuda(pair ? ql::launch_fp4_gemm_pair(a, st, sms) : ql::launch_fp4_gemm(a, st, sms));
 }
 
 // ---------------------------------------------------------------------------
@@ -557,6 +590,249 @@ size_t ql_gemm_workspace_size(int64_t m, int64_t n, int64_t k) {
     (void)n;
     (void)k;
     return 0;
+}
+
+int64_t fp4_scale_bytes(int64_t rows, int64_t k, int fmt, int experts) {
+    if (rows < 0 || k < 0 || (fmt != QL_FP4_NV && fmt != QL_FP4_MX)) return -1;
+    return fp4_row_blocks(rows, experts) * ql::fp4_kblocks(k, fmt) * ql::kFp4SfBlock;
+}
+
+int64_t fp4_column_extent(int64_t m, int experts) {
+    if (experts <= 0) return (m + 127) / 128 * 128;
+    return ((m + ql::kFp4KAlign - 1) / ql::kFp4KAlign + experts) * ql::kFp4KAlign;
+}
+
+ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k, int64_t x_stride_m,
+                           int64_t x_stride_k, float* scale, ql_stream_t stream) {
+    if (m < 0 || k < 0 || scale == nullptr || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
+    if (x == nullptr && m > 0 && k > 0) return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    return from_cuda(ql::launch_fp4_tensor_scale(x, x_dtype == QL_BF16, m, k, x_stride_m, x_stride_k, scale,
+                                                 reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+}
+
+ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
+                   int64_t x_stride_m, int64_t x_stride_k, int fmt, const float* scale, uint8_t* q, int64_t ldq,
+                   uint8_t* sf, const int32_t* offsets, int experts, ql_stream_t stream) {
+    if (batch < 0 || m < 0 || k < 0 || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
+    if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
+    if (offsets != nullptr && (batch != 1 || experts < 1)) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || k >= kInt31 || batch >= kInt31 || batch * m >= kInt31 ||
+        (offsets != nullptr && experts > ql::kFp4MaxExperts))
+        return QL_ERR_UNSUPPORTED;
+    if (batch == 0 || m == 0 || k == 0) return QL_OK;
+    if (x == nullptr) return QL_ERR_INVALID_ARG;
+    if (ql_status s = fp4_operand(q, ldq, sf, k); s != QL_OK) return s;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::Fp4CastArgs a{};
+    a.x = x;
+    a.is_bf16 = x_dtype == QL_BF16;
+    a.m = batch * m;
+    a.k = k;
+    a.sxm = x_stride_m;
+    a.sxk = x_stride_k;
+    a.seg_rows = m;
+    a.sxseg = x_stride_b;
+    a.fmt = fmt;
+    a.tscale = fmt == QL_FP4_NV ? scale : nullptr;
+    a.q = q;
+    a.ldq = ldq;
+    a.sf = sf;
+    a.offsets = offsets;
+    a.num_experts = experts;
+    a.sf_row_blocks = offsets != nullptr ? fp4_row_blocks(m, experts) : batch * ((m + 127) / 128);
+    a.dev_status = di.status;
+    return from_cuda(ql::launch_fp4_cast(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+}
+
+ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
+                        int64_t x_stride_m, int fmt, const float* scale, uint8_t* q_rows, int64_t ldr,
+                        uint8_t* sf_rows, uint8_t* q_cols, int64_t ldc, uint8_t* sf_cols, const int32_t* offsets,
+                        int experts, ql_stream_t stream) {
+    if (batch < 0 || m < 0 || k < 0 || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
+    if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
+    if (offsets != nullptr && (batch != 1 || experts < 1)) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || k >= kInt31 || batch >= 65536 || (offsets != nullptr && experts > ql::kFp4MaxExperts))
+        return QL_ERR_UNSUPPORTED;
+    if (batch == 0 || m == 0 || k == 0) return QL_OK;
+    if (x == nullptr || (q_rows == nullptr) != (sf_rows == nullptr)) return QL_ERR_INVALID_ARG;
+    const int64_t kpad = fp4_column_extent(m, offsets != nullptr ? experts : 0);
+    if (kpad / 128 >= 65536) return QL_ERR_UNSUPPORTED;
+    if (q_rows != nullptr)
+        if (ql_status s = fp4_operand(q_rows, ldr, sf_rows, k); s != QL_OK) return s;
+    if (ql_status s = fp4_operand(q_cols, ldc, sf_cols, kpad); s != QL_OK) return s;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::Fp4DualArgs a{};
+    a.x = x;
+    a.is_bf16 = x_dtype == QL_BF16;
+    a.batch = batch;
+    a.m = m;
+    a.k = k;
+    a.sxb = x_stride_b;
+    a.sxm = x_stride_m;
+    a.fmt = fmt;
+    a.tscale = fmt == QL_FP4_NV ? scale : nullptr;
+    a.qr = q_rows;
+    a.ldr = ldr;
+    a.sqrb = m * ldr;
+    a.sfr = sf_rows;
+    a.sfr_row_blocks = fp4_row_blocks(m, offsets != nullptr ? experts : 0);
+    a.ssrb = a.sfr_row_blocks * ql::fp4_kblocks(k, fmt) * ql::kFp4SfBlock;
+    a.qc = q_cols;
+    a.ldc = ldc;
+    a.sqcb = k * ldc;
+    a.sfc = sf_cols;
+    a.sscb = (k + 127) / 128 * ql::fp4_kblocks(offsets != nullptr ? kpad : m, fmt) * ql::kFp4SfBlock;
+    a.offsets = offsets;
+    a.num_experts = experts;
+    a.kpad = kpad;
+    a.dev_status = di.status;
+    return from_cuda(ql::launch_fp4_cast_dual(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ql_status fp4_dequant(const uint8_t* q, int64_t ldq, const uint8_t* sf, int fmt, const float* scale, int64_t m,
+                      int64_t k, void* out, ql_dtype out_dtype, int64_t ldo, ql_stream_t stream) {
+    if (m < 0 || k < 0 || (fmt != QL_FP4_NV && fmt != QL_FP4_MX)) return QL_ERR_INVALID_ARG;
+    if (out_dtype != QL_BF16 && out_dtype != QL_F32) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || k >= kInt31) return QL_ERR_UNSUPPORTED;
+    if (m == 0 || k == 0) return QL_OK;
+    if (out == nullptr || ldo < k) return QL_ERR_INVALID_ARG;
+    if (ql_status s = fp4_operand(q, ldq, sf, k); s != QL_OK) return s;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::Fp4DequantArgs a{};
+    a.q = q;
+    a.ldq = ldq;
+    a.sf = sf;
+    a.fmt = fmt;
+    a.tscale = fmt == QL_FP4_NV ? scale : nullptr;
+    a.m = m;
+    a.k = k;
+    a.out = out;
+    a.out_bf16 = out_dtype == QL_BF16;
+    a.ldo = ldo;
+    a.dev_status = di.status;
+    return from_cuda(ql::launch_fp4_dequant(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+}
+
+static ql_status fp4_gemm_common(ql::Fp4GemmArgs& a, const int32_t* offsets, int experts, ql_dtype d_dtype,
+                                 int accumulate, ql_stream_t stream) {
+    if (a.fmt != QL_FP4_NV && a.fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
+    if (d_dtype != QL_BF16 && d_dtype != QL_F32) return QL_ERR_INVALID_ARG;
+    if (accumulate && d_dtype != QL_F32) return QL_ERR_INVALID_ARG;
+    if (a.d == nullptr || a.ldd < a.n) return QL_ERR_INVALID_ARG;
+    if (ql_status s = fp4_operand(a.x, a.ldx, a.sfx, a.k); s != QL_OK) return s;
+    if (ql_status s = fp4_operand(a.w, a.ldw, a.sfw, a.k); s != QL_OK) return s;
+    if (a.fmt == QL_FP4_MX) a.tx = a.tw = nullptr;
+    a.offsets = offsets;
+    a.experts = experts;
+    a.out_f32 = d_dtype == QL_F32;
+    a.accumulate = accumulate ? 1 : 0;
+    return fp4_product(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ql_status gemm_fp4_nt(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale, const uint8_t* w,
+                      int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, ql_dtype d_dtype,
+                      int64_t ldd, int64_t m, int64_t n, int64_t k, int accumulate, ql_stream_t stream) {
+    if (m < 0 || n < 0 || k < 0) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || n >= kInt31 || k >= kInt31) return QL_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return QL_OK;
+    if (k == 0) {
+        if (d == nullptr || ldd < n || (d_dtype != QL_BF16 && d_dtype != QL_F32) || (accumulate && d_dtype != QL_F32))
+            return QL_ERR_INVALID_ARG;
+        if (accumulate) return QL_OK;
+        const size_t es = d_dtype == QL_F32 ? 4 : 2;
+        return from_cuda(cudaMemset2DAsync(d, static_cast<size_t>(ldd) * es, 0, static_cast<size_t>(n) * es,
+                                           static_cast<size_t>(m), reinterpret_cast<cudaStream_t>(stream)));
+    }
+    ql::Fp4GemmArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.sfx = sfx;
+    a.tx = x_scale;
+    a.x_row_blocks = (m + 127) / 128;
+    a.w = w;
+    a.ldw = ldw;
+    a.sfw = sfw;
+    a.tw = w_scale;
+    a.fmt = fmt;
+    a.form = ql::kFp4Plain;
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.d = d;
+    a.ldd = ldd;
+    return fp4_gemm_common(a, nullptr, 0, d_dtype, accumulate, stream);
+}
+
+ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale,
+                             const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt,
+                             void* d, ql_dtype d_dtype, int64_t ldd, const int32_t* offsets, int experts, int64_t m,
+                             int64_t n, int64_t k, ql_stream_t stream) {
+    if (m < 0 || n < 0 || k < 0 || experts < 1) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || n >= kInt31 || k >= kInt31 || experts > ql::kFp4MaxExperts || experts * n >= kInt31)
+        return QL_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return QL_OK;
+    if (k == 0) return QL_ERR_UNSUPPORTED;
+    if (offsets == nullptr) return QL_ERR_INVALID_ARG;
+    ql::Fp4GemmArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.sfx = sfx;
+    a.tx = x_scale;
+    a.x_row_blocks = fp4_row_blocks(m, experts);
+    a.w = w;
+    a.ldw = ldw;
+    a.sfw = sfw;
+    a.tw = w_scale;
+    a.fmt = fmt;
+    a.form = ql::kFp4RagRows;
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.rows = m;
+    a.d = d;
+    a.ldd = ldd;
+    return fp4_gemm_common(a, offsets, experts, d_dtype, 0, stream);
+}
+
+ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sfy, const float* y_scale,
+                                const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale, int fmt,
+                                float* d, int64_t ldd, const int32_t* offsets, int experts, int64_t tokens, int64_t m,
+                                int64_t n, int accumulate, ql_stream_t stream) {
+    if (m < 0 || n < 0 || tokens < 0 || experts < 1) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || n >= kInt31 || tokens >= kInt31 / 2 || experts > ql::kFp4MaxExperts || experts * m >= kInt31)
+        return QL_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return QL_OK;
+    if (tokens == 0) {
+        if (d == nullptr || ldd < n) return QL_ERR_INVALID_ARG;
+        if (accumulate) return QL_OK;
+        return from_cuda(cudaMemset2DAsync(d, static_cast<size_t>(ldd) * 4, 0, static_cast<size_t>(n) * 4,
+                                           static_cast<size_t>(experts * m), reinterpret_cast<cudaStream_t>(stream)));
+    }
+    if (offsets == nullptr) return QL_ERR_INVALID_ARG;
+    ql::Fp4GemmArgs a{};
+    a.x = y;
+    a.ldx = ldy;
+    a.sfx = sfy;
+    a.tx = y_scale;
+    a.x_row_blocks = (m + 127) / 128;
+    a.w = x;
+    a.ldw = ldx;
+    a.sfw = sfx;
+    a.tw = x_scale;
+    a.fmt = fmt;
+    a.form = ql::kFp4RagK;
+    a.m = m;
+    a.n = n;
+    a.k = fp4_column_extent(tokens, experts);
+    a.rows = tokens;
+    a.d = d;
+    a.ldd = ldd;
+    return fp4_gemm_common(a, offsets, experts, QL_F32, accumulate, stream);
 }
 
 ql_status ql_set_num_sms(int num_sms) {

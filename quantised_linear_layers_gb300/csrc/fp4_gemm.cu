@@ -1,0 +1,369 @@
+// 4-bit product on one SM per tile (fp4_gemm.cuh), for few rows of D, narrow
+// tiles and experts with few rows each.
+//
+// The tile is 128 columns of D by NT rows: W's rows take the tensor core's 128
+// lanes and X's rows its N side, so that a single token costs one 16-wide
+// instruction and no lane idles, and a tile's rows can end anywhere: the
+// accumulator's lanes are D's columns, so one store instruction of a warp
+// writes 32 neighbouring columns of one row, and rows past a tile's end are
+// simply not stored. With few rows the time is the stream of W from HBM, with
+// many tiles the tensor core's; a K stage is 256 columns (128 bytes) of both
+// operands and their scale blocks, all by TMA onto one barrier.
+//
+// With too few tiles for the SMs a cluster of 2, 4 or 8 CTAs takes one tile,
+// each a part of K; the fp32 partial tiles meet in shared memory, and each CTA
+// sums and stores its share of the rows in the CTAs' order.
+//
+// Roles (256 threads): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
+// stage's scales into tensor memory, then up to four instructions of K = 64),
+// warps 4-7 epilogue. Two accumulators and two scale slots in tensor memory:
+// the slot of stage i is written when the instructions of stage i - 2, whose
+// completion frees that stage's shared memory, are done.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "bounds.cuh"
+#include "common.cuh"
+#include "fp4.cuh"
+#include "fp4_gemm.cuh"
+#include "gemm.cuh"
+
+namespace ql {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int TW = 128;
+
+template <int NT, int FMT>
+struct Cfg {
+    static constexpr int kWords = FMT == kFp4Nv ? 4 : 2;          // scale blocks along a stage
+    static constexpr int kStageW = TW * 128;
+    static constexpr int kStageX = NT * 128;
+    static constexpr int kStageSf = kWords * kFp4SfBlock;         // per operand
+    static constexpr int kBytes = kStageW + kStageX + 2 * kStageSf;
+    static constexpr int kSlot = 8 * kWords;                      // tensor-memory columns of a stage's scales
+    static constexpr int kSfCol = NT < 32 ? 64 : 2 * NT;          // accumulators at 0 and NT
+    static constexpr int kTmem = kSfCol + 2 * kSlot <= 128 ? 128 : (kSfCol + 2 * kSlot <= 256 ? 256 : 512);
+    static constexpr int kMisc = 2304;                            // barriers, offsets
+    static constexpr int kMaxStages = (232448 - 1024 - kMisc) / kBytes;
+    static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
+    static constexpr int kOffX = kStages * kStageW;
+    static constexpr int kOffSfw = kOffX + kStages * kStageX;
+    static constexpr int kOffSfx = kOffSfw + kStages * kStageSf;
+    static constexpr int kOffBar = kOffSfx + kStages * kStageSf;
+    static constexpr int kOffOff = kOffBar + 192;
+    static constexpr int kSmem = kOffBar + kMisc + 1024;
+    static_assert((2 * kStages + 5) * 8 + 16 <= 192, "barriers");
+    static_assert(192 + (kFp4MaxExperts + 1) * 4 <= kMisc, "offsets");
+    static_assert(kStageX % 1024 == 0 && kSmem <= 232448, "shared memory");
+    static_assert(NT * TW * 4 <= kOffSfw, "partial tile fits in the operand ring");
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl)) != 0;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool OUT_F32>
+__device__ __forceinline__ void store_one(const Fp4GemmParams& p, int64_t at, float v) {
+    if constexpr (OUT_F32) {
+        float* d = static_cast<float*>(p.d) + at;
+        *d = p.accumulate ? *d + v : v;
+    } else {
+        static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
+    }
+}
+
+template <int NT, int FMT, bool OUT_F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_sfx, const __grid_constant__ CUtensorMap map_sfw,
+                    const Fp4GemmParams p) {
+    using C = Cfg<NT, FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint64_t* empty = full + C::kStages;
+    uint64_t* tfull = empty + C::kStages;       // [2]
+    uint64_t* tempty = tfull + 2;               // [2]
+    uint64_t* done_bar = tempty + 2;
+    uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(done_bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
+    int* s_off = reinterpret_cast<int*>(smem + C::kOffOff);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = static_cast<int>(cluster_nctarank());
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int first = static_cast<int>(cluster_id_x()), step = static_cast<int>(num_clusters_x());
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < 2; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 128); }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    pdl_launch_dependents();
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_sfx);
+        tma_prefetch_desc(&map_sfw);
+    }
+    if (warp == 1) { tmem_alloc(tmem_base_sm, C::kTmem); tmem_relinquish(); }
+    pdl_wait_prior();
+    if (warp == 2 && p.form != kFp4Plain) fp4_load_offsets(s_off, p);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_base_sm;
+    const WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
+
+    Fp4Walk<NT, TW> walk;
+    Fp4Tile t;
+    // this CTA's stages of a tile: [k_lo, k_hi) of its steps of 256
+    auto stages = [&](int& lo, int& hi) {
+        const int kb = (t.k64 + 3) >> 2;
+        lo = static_cast<int>(static_cast<int64_t>(rank) * kb / split);
+        hi = static_cast<int>(static_cast<int64_t>(rank + 1) * kb / split);
+    };
+
+    if (warp == 0) {
+        if (elect_one()) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int i = first; ok && walk.get(i, p, s_off, t) && !p.stall_producer; i += step) {
+                int lo, hi;
+                stages(lo, hi);
+                for (int kb = lo; kb < hi; ++kb, ++it) {
+                    const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
+                    if (!mbar_wait(&empty[s], ph ^ 1u, ctl)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&full[s], C::kBytes);
+                    const int x = (t.k0 + kb) * 128, kblk = (t.k0 + kb) * C::kWords;
+                    tma_load_2d(smem + s * C::kStageW, &map_w, &full[s], x, t.w_row);
+                    tma_load_2d(smem + C::kOffSfw + s * C::kStageSf, &map_sfw, &full[s], 0, (t.w_blk * p.kblocks + kblk) * 4);
+                    tma_load_2d(smem + C::kOffX + s * C::kStageX, &map_x, &full[s], x, t.x_row);
+                    tma_load_2d(smem + C::kOffSfx + s * C::kStageSf, &map_sfx, &full[s], 0, (t.x_blk * p.kblocks + kblk) * 4);
+                }
+            }
+            if (!ok) {
+                const uint32_t from = it > static_cast<uint32_t>(C::kStages) ? it - C::kStages : 0u;
+                for (uint32_t j = from; j < it; ++j)
+                    mbar_wait_drain(&full[j % C::kStages], (j / C::kStages) & 1u, p.wait_limit_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            uint32_t it = 0, tc = 0;
+            bool ok = true;
+            for (int i = first; ok && walk.get(i, p, s_off, t); i += step) {
+                int lo, hi;
+                stages(lo, hi);
+                if (hi <= lo) continue;
+                const uint32_t as = tc & 1u;
+                if (!mbar_wait(&tempty[as], ((tc >> 1) & 1u) ^ 1u, ctl)) { ok = false; break; }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + as * NT;
+                const uint32_t x_col = NT < 128 ? static_cast<uint32_t>(t.x_sub >> 5) : 0u;
+                for (int kb = lo; kb < hi; ++kb, ++it) {
+                    const uint32_t s = it % C::kStages;
+                    if (it >= 2) {
+                        const uint32_t j = it - 2;
+                        if (!mbar_wait(&empty[j % C::kStages], (j / C::kStages) & 1u, ctl)) { ok = false; break; }
+                    }
+                    if (!mbar_wait(&full[s], (it / C::kStages) & 1u, ctl)) { ok = false; break; }
+                    tc_fence_after_sync();
+                    const uint32_t sfw = tmem_base + C::kSfCol + (it & 1u) * C::kSlot;
+                    const uint32_t sfx = sfw + 4 * C::kWords;
+                    const uint32_t pw = smem_addr(smem + C::kOffSfw + s * C::kStageSf);
+                    const uint32_t px = smem_addr(smem + C::kOffSfx + s * C::kStageSf);
+#pragma unroll
+                    for (int j = 0; j < C::kWords; ++j) {
+                        tmem_cp_32x128b_warpx4(sfw + 4 * j, rows16_desc(pw + j * kFp4SfBlock));
+                        tmem_cp_32x128b_warpx4(sfx + 4 * j, rows16_desc(px + j * kFp4SfBlock));
+                    }
+                    const uint64_t dw = sw128_kmajor_desc(smem_addr(smem + s * C::kStageW));
+                    const uint64_t dx = sw128_kmajor_desc(smem_addr(smem + C::kOffX + s * C::kStageX));
+                    const int steps = t.k64 - 4 * kb;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= steps) break;
+                        const int word = FMT == kFp4Nv ? j : j >> 1;
+                        const uint32_t byte = FMT == kFp4Nv ? 0u : 2u * (j & 1);
+                        mma_fp4<FMT, false>(d_tmem, dw + 2 * j, dx + 2 * j, idesc_fp4<FMT>(TW, NT, byte), sfw + 4 * word,
+                                            sfx + 4 * word + x_col, (kb > lo || j > 0) ? 1u : 0u);
+                    }
+                    mma_commit(&empty[s]);
+                }
+                if (!ok) break;
+                mma_commit(&tfull[as]);
+                ++tc;
+            }
+            mma_commit(done_bar);
+            mbar_wait_drain(done_bar, 0, p.wait_limit_ns);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int q = warp & 3;
+        const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
+        uint32_t tc = 0;
+        for (int i = first; walk.get(i, p, s_off, t); i += step) {
+            int lo, hi;
+            stages(lo, hi);
+            const bool any = hi > lo;
+            const uint32_t as = tc & 1u;
+            if (any) {
+                if (!warp_wait(&tfull[as], (tc >> 1) & 1u, ctl)) break;
+                tc_fence_after_sync();
+                ++tc;
+            }
+            const int col = t.col + q * 32 + lane;
+            const int rows = t.rows < NT ? t.rows : NT;
+            float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+            for (int c0 = 0; c0 < NT; c0 += 16) {
+                if (c0 >= rows) break;
+                uint32_t r[16];
+                if (any) {
+                    tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + as * NT + c0, r);
+                    tmem_wait_ld(r);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int row = c0 + j;
+                    if (split > 1) part[row * TW + q * 32 + lane] = __uint_as_float(r[j]);
+                    else if (row < rows && col < p.n)
+                        store_one<OUT_F32>(p, static_cast<int64_t>(t.d_row + row) * p.ldd + col, __uint_as_float(r[j]) * alpha);
+                }
+            }
+            tc_fence_before_sync();
+            if (any) mbar_arrive(&tempty[as]);
+        }
+    }
+    if (split > 1) {
+        // one tile per cluster: the partial tiles are in every CTA's shared memory
+        __syncwarp();
+        cluster_sync_all();
+        Fp4Walk<NT, TW> again;
+        if (warp >= 4 && again.get(first, p, s_off, t) && !*abort_flag) {
+            const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
+            const int at = (warp & 3) * 32 + lane, col = t.col + at;
+            const int rows = t.rows < NT ? t.rows : NT;
+            const int lo = rows * rank / split, hi = rows * (rank + 1) / split;
+            for (int row = lo; row < hi; ++row) {
+                float v = 0.0f;
+                for (int r = 0; r < split; ++r)
+                    v += ld_cluster_f32(mapa_shared(smem + (row * TW + at) * 4, static_cast<uint32_t>(r)));
+                if (col < p.n) store_one<OUT_F32>(p, static_cast<int64_t>(t.d_row + row) * p.ldd + col, v * alpha);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, C::kTmem);
+    }
+}
+
+template <int NT, int FMT, bool OUT_F32>
+cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
+    using C = Cfg<NT, FMT>;
+    Fp4GemmParams p{};
+    fp4_fill_params(a, p);
+    p.tiles_x = static_cast<int>((a.m + NT - 1) / NT);
+    p.tiles_w = static_cast<int>((a.n + TW - 1) / TW);
+    p.group_x = 16;
+    CUtensorMap mx, mw, msx, msw;
+    const int64_t kbytes = (a.k + 1) / 2;
+    const int64_t we = a.form == kFp4RagRows ? a.experts : 1;
+    if (!fp4_codes_map(&mx, a.x, a.m, kbytes, a.ldx, NT) || !fp4_codes_map(&mw, a.w, a.n * we, kbytes, a.ldw, TW) ||
+        !fp4_scales_map(&msx, a.sfx, a.x_row_blocks * p.kblocks, a.fmt) ||
+        !fp4_scales_map(&msw, a.sfw, we * p.w_row_blocks * p.kblocks, a.fmt))
+        return cudaErrorInvalidValue;
+    auto kern = fp4_gemm_kernel<NT, FMT, OUT_F32>;
+    if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmem); e != cudaSuccess) return e;
+    int64_t tiles = static_cast<int64_t>(p.tiles_x) * p.tiles_w;
+    if (a.form == kFp4RagRows) tiles = (a.m / NT + (a.experts < a.m ? a.experts : a.m)) * p.tiles_w;
+    if (a.form == kFp4RagK) tiles *= a.experts;
+    int split = 1;
+    if (a.form == kFp4Plain) {
+        const int64_t kb = (a.k + 255) / 256;
+        while (split < 8 && tiles * split * 2 <= num_sms && kb >= split * 4) split *= 2;
+    }
+    const int64_t most = split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(most * split), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, mx, mw, msx, msw, p);
+}
+
+template <int NT>
+cudaError_t launch_n(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
+    if (a.fmt == kFp4Nv)
+        return a.out_f32 ? launch_t<NT, kFp4Nv, true>(a, st, num_sms) : launch_t<NT, kFp4Nv, false>(a, st, num_sms);
+    return a.out_f32 ? launch_t<NT, kFp4Mx, true>(a, st, num_sms) : launch_t<NT, kFp4Mx, false>(a, st, num_sms);
+}
+
+}  // namespace
+
+bool fp4_codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t kbytes, int64_t ld, int box_rows) {
+    return encode_kmajor_map(map, q, rows, kbytes, ld, box_rows);
+}
+
+bool fp4_scales_map(CUtensorMap* map, const uint8_t* sf, int64_t blocks, int fmt) {
+    return encode_2d_map(map, sf, CU_TENSOR_MAP_DATA_TYPE_UINT8, blocks * 4, 128, 128, fmt == kFp4Nv ? 16 : 8, 128, 0);
+}
+
+void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
+    p.form = a.form;
+    p.fmt = a.fmt;
+    p.experts = a.experts;
+    p.m = static_cast<int>(a.m);
+    p.n = static_cast<int>(a.n);
+    p.k64 = static_cast<int>((a.k + 63) / 64);
+    p.rows = static_cast<int>(a.rows);
+    p.kblocks = static_cast<int>(fp4_kblocks(a.k, a.fmt));
+    p.w_row_blocks = static_cast<int>((a.n + 127) / 128);
+    p.x_row_blocks = static_cast<int>(a.x_row_blocks);
+    p.offsets = a.offsets;
+    p.tx = a.tx;
+    p.tw = a.tw;
+    p.d = a.d;
+    p.ldd = a.ldd;
+    p.accumulate = a.accumulate;
+    p.dev_status = a.dev_status;
+    p.wait_limit_ns = a.wait_limit_ns;
+    p.stall_producer = a.stall_producer;
+}
+
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
+    if (a.form == kFp4Plain && a.m <= 16) return launch_n<16>(a, st, num_sms);
+    if (a.form == kFp4Plain && a.m <= 64) return launch_n<64>(a, st, num_sms);
+    return launch_n<128>(a, st, num_sms);
+}
+
+}  // namespace ql

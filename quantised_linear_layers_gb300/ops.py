@@ -21,6 +21,7 @@ LIB_PATH = os.environ.get("QL_LIBRARY") or os.path.join(_HERE, "libqlinear.so")
 QL_BF16, QL_F32 = 0, 1
 SF_FP32, SF_UE8M0, SF_PACKED_UE8M0 = 0, 1, 2
 CAST_RECIP_OF_SCALE = 0x100
+FP4_NV, FP4_MX = 0, 1
 
 _lock = threading.Lock()
 _lib = None
@@ -47,6 +48,18 @@ _SIGS = {
                                _i64, _i64, _i64, _int, _vp],
     "gemm_fp8_nn_bf16": [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp, _i64,
                          _i64, _i64, _i64, _vp],
+    "fp4_scale_bytes": [_i64, _i64, _int, _int],
+    "fp4_column_extent": [_i64, _int],
+    "fp4_tensor_scale": [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp],
+    "fp4_cast": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _vp, _int, _vp],
+    "fp4_cast_dual": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _int,
+                      _vp],
+    "fp4_dequant": [_vp, _i64, _vp, _int, _vp, _i64, _i64, _vp, _int, _i64, _vp],
+    "gemm_fp4_nt": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _int, _vp],
+    "gemm_fp4_nt_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _int, _i64, _vp, _int, _i64, _i64,
+                           _i64, _vp],
+    "gemm_fp4_wgrad_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64,
+                              _int, _vp],
     "ql_cast_gemm_host_workspace_size": [_i64, _i64, _i64, _int],
     "ql_cast_gemm_host": [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp, _i64, _i64, _i64, _i64, _i64,
                           _vp, _sz, _vp],
@@ -88,6 +101,8 @@ def load_library(path: str = LIB_PATH):
             lib.ql_status_string.restype = ctypes.c_char_p
             lib.ql_gemm_workspace_size.restype = _sz
             lib.ql_cast_gemm_host_workspace_size.restype = _sz
+            lib.fp4_scale_bytes.restype = _i64
+            lib.fp4_column_extent.restype = _i64
             _lib = lib
     return _lib
 
@@ -425,6 +440,229 @@ def cast_gemm_host(x_host: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor, fmt
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(b))
     _check("ql_cast_gemm_host", st)
     return out_host
+
+
+# ---------------------------------------------------------------------------
+# Microscaled 4-bit floating point
+# ---------------------------------------------------------------------------
+class FP4Tensor:
+    """A matrix (or a batch of them) in 4 bits, as a cast left it: codes ``q``
+    (uint8 [batch * rows, bytes]), scale blocks ``sf``, the tensor's scale
+    ``scale`` (fp32 [1], or None for 1), its format and its sizes; ``cols`` is
+    the reduction axis. ``offsets`` are the row ranges of the experts it was cast
+    by (``by_cols``: its columns are the experts' rows, each from a multiple of
+    256 on). The layouts are in include/qlinear.h."""
+
+    __slots__ = ("q", "sf", "scale", "fmt", "batch", "rows", "cols", "offsets", "by_cols")
+
+    def __init__(self, q, sf, scale, fmt, batch, rows, cols, offsets=None, by_cols=False):
+        self.q, self.sf, self.scale, self.fmt = q, sf, scale, fmt
+        self.batch, self.rows, self.cols = batch, rows, cols
+        self.offsets, self.by_cols = offsets, by_cols
+
+    def tensors(self):
+        """The tensors that hold it, for autograd to save."""
+        return self.q, self.sf, self.scale, self.offsets
+
+    def with_tensors(self, q, sf, scale, offsets):
+        return FP4Tensor(q, sf, scale, self.fmt, self.batch, self.rows, self.cols, offsets, self.by_cols)
+
+
+def _fp4_group(fmt: int) -> int:
+    if fmt == FP4_NV:
+        return 16
+    if fmt == FP4_MX:
+        return 32
+    raise ValueError("fmt must be FP4_NV or FP4_MX")
+
+
+def _fp4_sf(batch: int, row_blocks: int, k: int, fmt: int, device) -> torch.Tensor:
+    words = _ceil(k, 4 * _fp4_group(fmt))
+    return torch.empty(max(batch * row_blocks * words, 1) * 512, dtype=torch.uint8, device=device)
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _fp4_input(x: torch.Tensor, fmt: int, tensor_scale, offsets):
+    """(batch, m, k, stride between batch entries, experts) of a cast's input, checked."""
+    _fp4_group(fmt)
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dim() == 3:
+        batch, m, k = x.shape
+        sb = x.stride(0)
+    elif x.dim() == 2:
+        (m, k), batch, sb = x.shape, 1, 0
+    else:
+        raise ValueError("x must be 2-D or a batch of 2-D matrices")
+    if tensor_scale is not None:
+        if fmt != FP4_NV:
+            raise ValueError("only FP4_NV has a tensor scale")
+        if tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1 or tensor_scale.device != x.device:
+            raise ValueError("tensor_scale must be one fp32 value on x's device")
+    experts = 0
+    if offsets is not None:
+        experts = _fp4_experts(offsets, x.device)
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D with offsets")
+    return batch, m, k, sb, experts
+
+
+def _fp4_experts(offsets: torch.Tensor, device) -> int:
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.shape[0] < 2 \
+            or offsets.device != device:
+        raise ValueError("offsets must be a contiguous int32 [experts + 1] tensor on x's device")
+    return offsets.shape[0] - 1
+
+
+def fp4_tensor_scale(x: torch.Tensor) -> torch.Tensor:
+    """The FP4_NV scale of a tensor (any 2-D or 3-D strides, fp32 [1]): the least
+    power of two t with max|x| <= 2688 t, at least 2^-80; a power of two leaves
+    every group's scale s * t exact. NaN if x has an infinity or a NaN."""
+    if x.dim() == 3:
+        if x.stride(0) != x.shape[1] * x.stride(1):
+            x = x.contiguous()
+        x = x.as_strided((x.shape[0] * x.shape[1], x.shape[2]), (x.stride(1), x.stride(2)))
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a 2-D or 3-D CUDA tensor")
+    out = torch.empty(1, dtype=torch.float32, device=x.device)
+    st = load_library().fp4_tensor_scale(x.data_ptr(), _dtype_code(x), x.shape[0], x.shape[1], x.stride(0), x.stride(1),
+                                         out.data_ptr(), _stream(x))
+    _check("fp4_tensor_scale", st)
+    return out
+
+
+def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | None = None,
+             offsets: torch.Tensor | None = None) -> FP4Tensor:
+    """Casts the rows of x [m, k] or [batch, m, k] (bf16 or fp32, any strides) to
+    4 bits. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and
+    the cast is the operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
+    batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
+    q = torch.empty((batch * m, _ceil(max(k, 1), 32) * 16), dtype=torch.uint8, device=x.device)
+    sf = _fp4_sf(batch, _ceil(m, 128) + experts, k, fmt, x.device)
+    st = load_library().fp4_cast(
+        x.data_ptr(), _dtype_code(x), batch, m, k, sb, x.stride(-2), x.stride(-1), fmt, _ptr(tensor_scale),
+        q.data_ptr(), q.stride(0), sf.data_ptr(), _ptr(offsets), experts, _stream(x))
+    _check("fp4_cast", st)
+    return FP4Tensor(q, sf, tensor_scale, fmt, batch, m, k, offsets)
+
+
+def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | None = None,
+                  offsets: torch.Tensor | None = None, rows: bool = True):
+    """Casts x [m, k] or [batch, m, k] (contiguous rows) along its rows and along
+    its columns from one read: (cast of x, cast of x^T). The second is the
+    operand of products that sum over x's rows; with ``offsets`` each expert's rows
+    are columns of their own there (``gemm_fp4_wgrad_ragged``). ``rows=False``
+    leaves the first out (None)."""
+    batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
+    if x.stride(-1) != 1 and k > 1:
+        raise ValueError("x must have contiguous rows")
+    kpad = int(load_library().fp4_column_extent(m, experts))
+    qc = torch.empty((batch * k, max(kpad, 128) // 2), dtype=torch.uint8, device=x.device)
+    sfc = _fp4_sf(batch, _ceil(k, 128), kpad if experts else m, fmt, x.device)
+    q = sf = None
+    if rows:
+        q = torch.empty((batch * m, _ceil(max(k, 1), 32) * 16), dtype=torch.uint8, device=x.device)
+        sf = _fp4_sf(batch, _ceil(m, 128) + experts, k, fmt, x.device)
+    st = load_library().fp4_cast_dual(
+        x.data_ptr(), _dtype_code(x), batch, m, k, sb, x.stride(-2), fmt, _ptr(tensor_scale),
+        _ptr(q), q.stride(0) if rows else 0, _ptr(sf), qc.data_ptr(), qc.stride(0), sfc.data_ptr(), _ptr(offsets),
+        experts, _stream(x))
+    _check("fp4_cast_dual", st)
+    return (FP4Tensor(q, sf, tensor_scale, fmt, batch, m, k, offsets) if rows else None,
+            FP4Tensor(qc, sfc, tensor_scale, fmt, batch, k, m, offsets, by_cols=offsets is not None))
+
+
+def fp4_dequant(a: FP4Tensor, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values [rows, cols] that a cast stands for (bf16 or fp32)."""
+    if a.batch != 1 or a.offsets is not None:
+        raise ValueError("fp4_dequant takes the cast of one matrix")
+    if out is None:
+        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.q.device)
+    if tuple(out.shape) != (a.rows, a.cols) or (a.cols > 1 and out.stride(1) != 1):
+        raise ValueError("out must be [rows, cols] with contiguous rows")
+    st = load_library().fp4_dequant(
+        a.q.data_ptr(), a.q.stride(0), a.sf.data_ptr(), a.fmt, _ptr(a.scale), a.rows, a.cols, out.data_ptr(),
+        _dtype_code(out), max(out.stride(0), a.cols), _stream(out))
+    _check("fp4_dequant", st)
+    return out
+
+
+def _fp4_pair(x: FP4Tensor, w: FP4Tensor):
+    if x.fmt != w.fmt:
+        raise ValueError("the operands' formats differ")
+    if x.cols != w.cols:
+        raise ValueError("the operands must share K")
+    if x.q.device != w.q.device:
+        raise ValueError("the operands must be on one device")
+
+
+def _fp4_out(out, shape, dtype, device, accumulate):
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs an existing out")
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != tuple(shape) \
+            or out.device != device or (out.shape[-1] > 1 and out.stride(-1) != 1):
+        raise ValueError(f"out must be bf16 or fp32 {tuple(shape)} with contiguous rows on the operands' device")
+    if accumulate and out.dtype != torch.float32:
+        raise ValueError("accumulate needs an fp32 out")
+    return out
+
+
+def gemm_fp4_nt(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                accumulate: bool = False) -> torch.Tensor:
+    """D [m, n] (+)= X W^T of two row-wise casts of one format: X [m, k], W [n, k];
+    D bf16 or fp32 (accumulate: fp32)."""
+    _fp4_pair(x, w)
+    if x.batch != 1 or w.batch != 1 or x.offsets is not None or w.offsets is not None:
+        raise ValueError("gemm_fp4_nt takes casts of one matrix each")
+    out = _fp4_out(out, (x.rows, w.rows), dtype, x.q.device, accumulate)
+    st = load_library().gemm_fp4_nt(
+        x.q.data_ptr(), x.q.stride(0), x.sf.data_ptr(), _ptr(x.scale), w.q.data_ptr(), w.q.stride(0), w.sf.data_ptr(),
+        _ptr(w.scale), x.fmt, out.data_ptr(), _dtype_code(out), max(out.stride(0), w.rows), x.rows, w.rows, x.cols,
+        int(bool(accumulate)), _stream(out))
+    _check("gemm_fp4_nt", st)
+    return out
+
+
+def gemm_fp4_nt_ragged(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = None,
+                       dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Experts' products: rows offsets[e] .. offsets[e+1] of D [m, n] are those
+    rows of X [m, k] times W[e]^T; X cast with the offsets, W [experts, n, k] cast
+    as a batch. Rows of no expert are left unwritten in ``out``."""
+    _fp4_pair(x, w)
+    if x.offsets is None or x.by_cols or w.offsets is not None or w.batch != x.offsets.shape[0] - 1:
+        raise ValueError("x must be cast by expert and w hold one matrix per expert")
+    out = _fp4_out(out, (x.rows, w.rows), dtype, x.q.device, False)
+    st = load_library().gemm_fp4_nt_ragged(
+        x.q.data_ptr(), x.q.stride(0), x.sf.data_ptr(), _ptr(x.scale), w.q.data_ptr(), w.q.stride(0), w.sf.data_ptr(),
+        _ptr(w.scale), x.fmt, out.data_ptr(), _dtype_code(out), max(out.stride(0), w.rows), x.offsets.data_ptr(),
+        w.batch, x.rows, w.rows, x.cols, _stream(out))
+    _check("gemm_fp4_nt_ragged", st)
+    return out
+
+
+def gemm_fp4_wgrad_ragged(y: FP4Tensor, x: FP4Tensor, out: torch.Tensor | None = None,
+                          accumulate: bool = False) -> torch.Tensor:
+    """Experts' weight gradients D [experts, m, n] (+)= Y_e^T X_e, fp32, from the
+    column-wise casts of Y [tokens, m] and X [tokens, n] by the same offsets. An
+    expert without rows gets zeros."""
+    _fp4_pair(y, x)
+    if not y.by_cols or not x.by_cols or y.offsets.shape != x.offsets.shape:
+        raise ValueError("both operands must be column-wise casts by the same experts")
+    experts = y.offsets.shape[0] - 1
+    out = _fp4_out(out, (experts, y.rows, x.rows), torch.float32, y.q.device, accumulate)
+    if out.dtype != torch.float32 or not out.is_contiguous():
+        raise ValueError("out must be contiguous fp32")
+    st = load_library().gemm_fp4_wgrad_ragged(
+        y.q.data_ptr(), y.q.stride(0), y.sf.data_ptr(), _ptr(y.scale), x.q.data_ptr(), x.q.stride(0), x.sf.data_ptr(),
+        _ptr(x.scale), y.fmt, out.data_ptr(), x.rows, y.offsets.data_ptr(), experts, y.cols, y.rows, x.rows,
+        int(bool(accumulate)), _stream(out))
+    _check("gemm_fp4_wgrad_ragged", st)
+    return out
 
 
 def set_num_sms(n: int) -> None:
