@@ -35,6 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int TW = 128;
+constexpr int kMaxSplit = 8;
 
 template <int NT, int FMT>
 struct Cfg {
@@ -64,9 +65,11 @@ struct Cfg {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl)) != 0;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
     return v;
 }
 
@@ -77,6 +80,83 @@ __device__ __forceinline__ void store_one(const Fp4GemmParams& p, int64_t at, fl
         *d = p.accumulate ? *d + v : v;
     } else {
         static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
+    }
+}
+
+// Sixteen rows of one column of D (the first `rows` of them). The whole case
+// has no branch between its stores: a lone warp per scheduler would otherwise
+// wait out every address and conversion (measured 100 cycles a row).
+template <bool OUT_F32>
+__device__ __forceinline__ void store_rows(const Fp4GemmParams& p, int64_t at, int rows, const uint32_t (&r)[16],
+                                           float alpha) {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) * alpha;
+    if (rows >= 16) {
+        if constexpr (OUT_F32) {
+            float* d = static_cast<float*>(p.d) + at;
+            if (p.accumulate) {
+                const float* s = d;
+#pragma unroll
+                for (int j = 0; j < 16; ++j, s += p.ldd) v[j] += *s;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j, d += p.ldd) *d = v[j];
+        } else {
+            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + at;
+#pragma unroll
+            for (int j = 0; j < 16; ++j, d += p.ldd) *d = __float2bfloat16_rn(v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, at += p.ldd)
+            if (j < rows) store_one<OUT_F32>(p, at, v[j]);
+    }
+}
+
+// This CTA's share of the rows of a tile split along K: the CTAs' partial
+// tiles (fp32 [NT][128] at the same offset of each CTA's shared memory) added
+// in the CTAs' order. A thread takes four columns of a row and has the loads of
+// kAhead rows in flight.
+template <int NT, bool OUT_F32>
+__device__ __forceinline__ void sum_parts(uint32_t part, const Fp4GemmParams& p, const Fp4Tile& t, int rank, int split) {
+    constexpr int kAhead = 4, kRowsPer = kThreads / 32;
+    const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
+    const int c4 = (threadIdx.x & 31) * 4, col = t.col + c4;
+    const int rows = t.rows < NT ? t.rows : NT;
+    const int lo = rows * rank / split, hi = rows * (rank + 1) / split;
+    if (col >= p.n) return;
+    for (int r0 = lo + static_cast<int>(threadIdx.x >> 5); r0 < hi; r0 += kRowsPer * kAhead) {
+        float4 v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < split; ++s) {
+            uint32_t base;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base) : "r"(part), "r"(s));
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int row = r0 + j * kRowsPer;
+                if (row >= hi) continue;
+                const float4 o = ld_cluster_f32x4(base + (row * TW + c4) * 4);
+                v[j].x += o.x; v[j].y += o.y; v[j].z += o.z; v[j].w += o.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int row = r0 + j * kRowsPer;
+            if (row >= hi) continue;
+            const int64_t at = static_cast<int64_t>(t.d_row + row) * p.ldd + col;
+            const float f[4] = {v[j].x * alpha, v[j].y * alpha, v[j].z * alpha, v[j].w * alpha};
+            if (!OUT_F32 && p.vec_store && col + 4 <= p.n) {
+                const __nv_bfloat162 h0 = __floats2bfloat162_rn(f[0], f[1]), h1 = __floats2bfloat162_rn(f[2], f[3]);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.d) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < p.n) store_one<OUT_F32>(p, at + e, f[e]);
+            }
+        }
     }
 }
 
@@ -238,12 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = 0u;
                 }
+                if (split > 1) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int row = c0 + j;
-                    if (split > 1) part[row * TW + q * 32 + lane] = __uint_as_float(r[j]);
-                    else if (row < rows && col < p.n)
-                        store_one<OUT_F32>(p, static_cast<int64_t>(t.d_row + row) * p.ldd + col, __uint_as_float(r[j]) * alpha);
+                    for (int j = 0; j < 16; ++j) part[(c0 + j) * TW + q * 32 + lane] = __uint_as_float(r[j]);
+                } else if (col < p.n) {
+                    store_rows<OUT_F32>(p, static_cast<int64_t>(t.d_row + c0) * p.ldd + col, rows - c0, r, alpha);
                 }
             }
             tc_fence_before_sync();
@@ -255,18 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         cluster_sync_all();
         Fp4Walk<NT, TW> again;
-        if (warp >= 4 && again.get(first, p, s_off, t) && !*abort_flag) {
-            const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
-            const int at = (warp & 3) * 32 + lane, col = t.col + at;
-            const int rows = t.rows < NT ? t.rows : NT;
-            const int lo = rows * rank / split, hi = rows * (rank + 1) / split;
-            for (int row = lo; row < hi; ++row) {
-                float v = 0.0f;
-                for (int r = 0; r < split; ++r)
-                    v += ld_cluster_f32(mapa_shared(smem + (row * TW + at) * 4, static_cast<uint32_t>(r)));
-                if (col < p.n) store_one<OUT_F32>(p, static_cast<int64_t>(t.d_row + row) * p.ldd + col, v * alpha);
-            }
-        }
+        if (again.get(first, p, s_off, t) && !*abort_flag)
+            sum_parts<NT, OUT_F32>(smem_addr(smem), p, t, rank, split);
         __syncwarp();
         cluster_sync_all();
     }
@@ -286,6 +355,7 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     p.tiles_x = static_cast<int>((a.m + NT - 1) / NT);
     p.tiles_w = static_cast<int>((a.n + TW - 1) / TW);
     p.group_x = 16;
+    p.vec_store = (reinterpret_cast<uintptr_t>(a.d) & 7u) == 0 && a.ldd % 4 == 0;
     CUtensorMap mx, mw, msx, msw;
     const int64_t kbytes = (a.k + 1) / 2;
     const int64_t we = a.form == kFp4RagRows ? a.experts : 1;
@@ -301,7 +371,7 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     int split = 1;
     if (a.form == kFp4Plain) {
         const int64_t kb = (a.k + 255) / 256;
-        while (split < 8 && tiles * split * 2 <= num_sms && kb >= split * 4) split *= 2;
+        while (split < kMaxSplit && tiles * split * 2 <= num_sms && kb >= split * 4) split *= 2;
     }
     const int64_t most = split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms);
     cudaLaunchConfig_t cfg = {};

@@ -66,7 +66,7 @@ struct Fp4GemmParams {
     int64_t ldd;
     int accumulate;
     int tma_d;                   // whole 32-row pieces leave through TMA tile stores
-    int vec_store;               // 16-byte stores along D's rows
+    int vec_store;               // bf16 D: 8-byte stores of four columns
     uint32_t* dev_status;
     uint64_t wait_limit_ns;
     int stall_producer;
