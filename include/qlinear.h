@@ -549,6 +549,19 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
                              void* d, ql_dtype d_dtype, int64_t ldd, const int32_t* offsets, int experts, int64_t m,
                              int64_t n, int64_t k, ql_stream_t stream);
 
+/* The forward call: casts X [m, k] (bf16 or fp32, contiguous rows, row stride
+ * x_stride_m) and multiplies, D [m, n] bf16 = X W^T, or by expert with offsets
+ * (W [experts, n, k]). Equal to fp4_cast and gemm_fp4_nt / gemm_fp4_nt_ragged;
+ * up to 16 rows are cast inside the product, in one launch and without a
+ * workspace. fp4_linear_workspace_size bytes of device memory, 16-byte aligned,
+ * are needed otherwise (0: none); they may be reused once the stream is past
+ * the call. */
+size_t fp4_linear_workspace_size(int64_t m, int64_t k, int fmt, int experts);
+ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, const float* x_scale, const uint8_t* w,
+                     int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
+                     const int32_t* offsets, int experts, int64_t m, int64_t n, int64_t k, void* workspace,
+                     size_t workspace_bytes, ql_stream_t stream);
+
 /* Experts' weight gradient: D[e] [m, n] (+)= Y_e^T X_e over expert e's rows of
  * the `tokens` rows. y and x are column-wise casts by expert of Y [tokens, m]
  * and X [tokens, n]: codes [m][ldy], [n][ldx]. D fp32 [experts * m][ldd]. The

@@ -161,7 +161,7 @@ ql_status fp4_product(ql::Fp4GemmArgs& a, cudaStream_t st) {
     // SMs; narrower tiles on one SM otherwise
     const int64_t per = a.form == ql::kFp4RagRows ? (a.m / a.experts > 0 ? a.m / a.experts : 1) : a.m;
     const int64_t tiles = ((per + 255) / 256) * ((a.n + 255) / 256) * (a.form == ql::kFp4Plain ? 1 : a.experts);
-    const bool pair = path == 3 || (path != 2 && path != 4 && per > 128 && tiles >= sms / 4);
+    const bool pair = a.xr == nullptr && (path == 3 || (path != 2 && path != 4 && per > 128 && tiles >= sms / 4));
     return from_cuda(pair ? ql::launch_fp4_gemm_pair(a, st, sms) : ql::launch_fp4_gemm(a, st, sms));
 }
 
@@ -797,6 +797,60 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
     a.d = d;
     a.ldd = ldd;
     return fp4_gemm_common(a, offsets, experts, d_dtype, 0, stream);
+}
+
+size_t fp4_linear_workspace_size(int64_t m, int64_t k, int fmt, int experts) {
+    if (m <= ql::kFp4CastRows || k <= 0 || (fmt != QL_FP4_NV && fmt != QL_FP4_MX)) return 0;
+    return static_cast<size_t>(m) * ((k + 31) / 32 * 16) + static_cast<size_t>(fp4_scale_bytes(m, k, fmt, experts));
+}
+
+ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, const float* x_scale, const uint8_t* w,
+                     int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
+                     const int32_t* offsets, int experts, int64_t m, int64_t n, int64_t k, void* workspace,
+                     size_t workspace_bytes, ql_stream_t stream) {
+    if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
+    if (x_dtype != QL_BF16 && x_dtype != QL_F32) return QL_ERR_INVALID_ARG;
+    const int64_t ldq = (k + 31) / 32 * 16;
+    uint8_t* q = static_cast<uint8_t*>(workspace);
+    if (m > ql::kFp4CastRows || m <= 0 || n <= 0 || k <= 0) {
+        if (m > 0 && n > 0 && k > 0 && (workspace == nullptr ||
+                                        workspace_bytes < fp4_linear_workspace_size(m, k, fmt, offsets ? experts : 0)))
+            return QL_ERR_INVALID_ARG;
+        uint8_t* sf = q == nullptr ? nullptr : q + m * ldq;
+        if (ql_status s = fp4_cast(x, x_dtype, 1, m, k, 0, x_stride_m, 1, fmt, x_scale, q, ldq, sf, offsets, experts,
+                                   stream);
+            s != QL_OK)
+            return s;
+        return offsets == nullptr
+                   ? gemm_fp4_nt(q, ldq, sf, x_scale, w, ldw, sfw, w_scale, fmt, d, QL_BF16, ldd, m, n, k, 0, stream)
+                   : gemm_fp4_nt_ragged(q, ldq, sf, x_scale, w, ldw, sfw, w_scale, fmt, d, QL_BF16, ldd, offsets,
+                                        experts, m, n, k, stream);
+    }
+    if (n >= kInt31 || k >= kInt31) return QL_ERR_UNSUPPORTED;
+    if (offsets != nullptr && experts < 1) return QL_ERR_INVALID_ARG;
+    if (offsets != nullptr && (experts > ql::kFp4MaxExperts || experts * n >= kInt31)) return QL_ERR_UNSUPPORTED;
+    if (x == nullptr || d == nullptr || ldd < n) return QL_ERR_INVALID_ARG;
+    if (ql_status s = fp4_operand(w, ldw, sfw, k); s != QL_OK) return s;
+    ql::Fp4GemmArgs a{};
+    a.xr = x;
+    a.xr_bf16 = x_dtype == QL_BF16;
+    a.sxr = x_stride_m;
+    a.tx = fmt == QL_FP4_NV ? x_scale : nullptr;
+    a.w = w;
+    a.ldw = ldw;
+    a.sfw = sfw;
+    a.tw = fmt == QL_FP4_NV ? w_scale : nullptr;
+    a.fmt = fmt;
+    a.form = offsets == nullptr ? ql::kFp4Plain : ql::kFp4RagRows;
+    a.offsets = offsets;
+    a.experts = offsets == nullptr ? 0 : experts;
+    a.rows = m;
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.d = d;
+    a.ldd = ldd;
+    return fp4_product(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sfy, const float* y_scale,

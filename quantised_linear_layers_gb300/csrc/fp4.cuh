@@ -198,6 +198,78 @@ __device__ __forceinline__ uint2 fp4_codes16(const float (&x)[16], const Fp4Scal
     if (!g.finite) o = make_uint2(0u, 0u);
     return o;
 }
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// Sixteen consecutive elements of a row as they lie in memory.
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+    uint4 u[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        u[0] = __ldg(reinterpret_cast<const uint4*>(p));
+        u[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0, 0, 0, 0); }
+    // element by element, `n` of them (0 .. 16), `s` elements apart
+    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int64_t s, int n) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t lo = 0, hi = 0;
+            if (2 * i < n) lo = __bfloat16_as_ushort(p[(2 * i) * s]);
+            if (2 * i + 1 < n) hi = __bfloat16_as_ushort(p[(2 * i + 1) * s]);
+            w[i] = lo | (hi << 16);
+        }
+        u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    __device__ __forceinline__ float amax() const {
+        const uint32_t k = 0x7FFF7FFFu;
+        uint32_t m = bf16x2_max_nan(bf16x2_max_nan(u[0].x & k, u[0].y & k), bf16x2_max_nan(u[0].z & k, u[0].w & k));
+        m = bf16x2_max_nan(m, bf16x2_max_nan(bf16x2_max_nan(u[1].x & k, u[1].y & k),
+                                             bf16x2_max_nan(u[1].z & k, u[1].w & k)));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ void values(float (&v)[16]) const {
+        unpack8(u[0], v);
+        unpack8(u[1], v + 8);
+    }
+};
+template <>
+struct Raw16<float> {
+    float f[16];
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(f + 4 * i) = __ldg(reinterpret_cast<const float4*>(p) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+    }
+    __device__ __forceinline__ void load_some(const float* p, int64_t s, int n) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = i < n ? p[i * s] : 0.0f;
+    }
+    __device__ __forceinline__ float amax() const {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(f[i]));
+        return m;
+    }
+    __device__ __forceinline__ void values(float (&v)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f[i];
+    }
+};
 #endif
 
 }  // namespace ql

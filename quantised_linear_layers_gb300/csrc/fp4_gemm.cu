@@ -14,7 +14,12 @@
 // each a part of K; the fp32 partial tiles meet in shared memory, and each CTA
 // sums and stores its share of the rows in the CTAs' order.
 //
-// Roles (256 threads): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
+// Up to 16 rows of X (kFp4CastRows) can come as they are, bf16 or fp32: eight
+// more warps then cast them into the stages, one warp per stage, and the call
+// is a single launch. Every CTA repeats the cast of its part of K, 16 x 1792
+// elements at K = 7168, while its weights are on their way.
+//
+// Roles (256 threads, 512 with the cast): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
 // stage's scales into tensor memory, then up to four instructions of K = 64),
 // warps 4-7 epilogue. Two accumulators and two scale slots in tensor memory:
 // the slot of stage i is written when the instructions of stage i - 2, whose
@@ -23,6 +28,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "bounds.cuh"
 #include "common.cuh"
@@ -34,6 +41,7 @@ namespace ql {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCastWarps = 8;
 constexpr int TW = 128;
 constexpr int kMaxSplit = 8;
 
@@ -160,12 +168,54 @@ __device__ __forceinline__ void sum_parts(uint32_t part, const Fp4GemmParams& p,
     }
 }
 
-template <int NT, int FMT, bool OUT_F32>
-__global__ void __launch_bounds__(kThreads, 1)
+// One stage of X cast in place of its copy: rows [0, rows) of 256 columns from
+// column c0 on, codes in the 128-byte swizzle the tensor core reads, scale bytes
+// in a scale block's order. A lane has 16 columns of a row, a warp two rows.
+template <typename T, int FMT>
+__device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, int rows, int c0, uint8_t* codes,
+                                           uint8_t* sf, const Fp4Tensor& tn) {
+    constexpr int kAhead = 4;                    // rows / 2 in flight
+    const int lane = static_cast<int>(threadIdx.x & 31), cg = lane & 15;
+    const int c = c0 + cg * 16;
+    const T* x = static_cast<const T*>(p.xr) + static_cast<int64_t>(x_row) * p.sxr;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h * 2 * kAhead >= rows) break;
+        Raw16<T> raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = (h * kAhead + i) * 2 + (lane >> 4);
+            if (r >= rows || c >= p.k) raw[i].zero();
+            else if (p.xr_vec && c + 16 <= p.k) raw[i].load(x + r * p.sxr + c);
+            else raw[i].load_some(x + r * p.sxr + c, 1, p.k - c < 16 ? p.k - c : 16);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = (h * kAhead + i) * 2 + (lane >> 4);
+            if ((h * kAhead + i) * 2 >= rows) break;
+            float amax = raw[i].amax();
+            if constexpr (FMT == kFp4Mx) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            const Fp4Scale g = fp4_scale<FMT>(amax, tn);
+            float v[16];
+            raw[i].values(v);
+            *reinterpret_cast<uint2*>(codes + r * 128 + (((cg >> 1) ^ (r & 7)) << 4) + (cg & 1) * 8) = fp4_codes16<FMT>(v, g);
+            const int gi = FMT == kFp4Nv ? cg : cg >> 1;
+            if (FMT == kFp4Nv || (cg & 1) == 0) {
+                const bool live = c0 + gi * fp4_group(FMT) < p.k;
+                sf[(gi >> 2) * kFp4SfBlock + r * 16 + (gi & 3)] = live ? static_cast<uint8_t>(g.byte) : 0;
+            }
+        }
+    }
+}
+
+// T: void when X's codes are copied, else the type of X to cast.
+template <int NT, int FMT, bool OUT_F32, typename T>
+__global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads + 32 * kCastWarps, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_sfx, const __grid_constant__ CUtensorMap map_sfw,
                     const Fp4GemmParams p) {
     using C = Cfg<NT, FMT>;
+    constexpr bool kCast = !std::is_void<T>::value;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -183,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = static_cast<int>(cluster_id_x()), step = static_cast<int>(num_clusters_x());
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], kCast ? 2 : 1); mbar_init(&empty[s], 1); }
         for (int s = 0; s < 2; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 128); }
         mbar_init(done_bar, 1);
         *abort_flag = 0;
@@ -191,10 +241,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_launch_dependents();
     if (warp == 0 && lane == 0) {
-        tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
-        tma_prefetch_desc(&map_sfx);
         tma_prefetch_desc(&map_sfw);
+        if constexpr (!kCast) {
+            tma_prefetch_desc(&map_x);
+            tma_prefetch_desc(&map_sfx);
+        }
+        if (p.form == kFp4Plain && first < p.tiles_x * p.tiles_w) {
+            // the first tile's part of W into L2 while the previous kernel ends
+            // (a prefetch, not a load: that kernel may still be writing W)
+            Fp4Walk<NT, TW> ahead;
+            Fp4Tile f = {};
+            ahead.get(first, p, s_off, f);
+            const int kb = (f.k64 + 3) >> 2;
+            const int lo = rank * kb / split, hi = (rank + 1) * kb / split;
+            for (int i = lo; i < hi && i < lo + p.ahead; ++i) tma_prefetch_l2_2d(&map_w, i * 128, f.w_row);
+        }
     }
     if (warp == 1) { tmem_alloc(tmem_base_sm, C::kTmem); tmem_relinquish(); }
     pdl_wait_prior();
@@ -206,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const WaitCtl ctl{abort_flag, p.dev_status, p.wait_limit_ns};
 
     Fp4Walk<NT, TW> walk;
-    Fp4Tile t;
+    Fp4Tile t = {};
     // this CTA's stages of a tile: [k_lo, k_hi) of its steps of 256
     auto stages = [&](int& lo, int& hi) {
         const int kb = (t.k64 + 3) >> 2;
@@ -224,12 +286,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = lo; kb < hi; ++kb, ++it) {
                     const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
                     if (!mbar_wait(&empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[s], C::kBytes);
+                    mbar_arrive_expect_tx(&full[s], kCast ? C::kStageW + C::kStageSf : C::kBytes);
                     const int x = (t.k0 + kb) * 128, kblk = (t.k0 + kb) * C::kWords;
                     tma_load_2d(smem + s * C::kStageW, &map_w, &full[s], x, t.w_row);
                     tma_load_2d(smem + C::kOffSfw + s * C::kStageSf, &map_sfw, &full[s], 0, (t.w_blk * p.kblocks + kblk) * 4);
-                    tma_load_2d(smem + C::kOffX + s * C::kStageX, &map_x, &full[s], x, t.x_row);
-                    tma_load_2d(smem + C::kOffSfx + s * C::kStageSf, &map_sfx, &full[s], 0, (t.x_blk * p.kblocks + kblk) * 4);
+                    if constexpr (!kCast) {
+                        tma_load_2d(smem + C::kOffX + s * C::kStageX, &map_x, &full[s], x, t.x_row);
+                        tma_load_2d(smem + C::kOffSfx + s * C::kStageSf, &map_sfx, &full[s], 0,
+                                    (t.x_blk * p.kblocks + kblk) * 4);
+                    }
                 }
             }
             if (!ok) {
@@ -290,6 +355,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_drain(done_bar, 0, p.wait_limit_ns);
         }
         __syncwarp();
+    } else if (warp >= 8) {
+        if constexpr (kCast) {
+            const Fp4Tensor tn = fp4_tensor(p.tx);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int i = first; ok && walk.get(i, p, s_off, t); i += step) {
+                int lo, hi;
+                stages(lo, hi);
+                const int rows = t.rows < NT ? t.rows : NT;
+                for (int kb = lo; kb < hi; ++kb, ++it) {
+                    if (static_cast<int>(it % kCastWarps) != warp - 8) continue;
+                    const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
+                    if (!warp_wait(&empty[s], ph ^ 1u, ctl)) { ok = false; break; }
+                    cast_stage<T, FMT>(p, t.x_row, rows, kb * 256, smem + C::kOffX + s * C::kStageX,
+                                       smem + C::kOffSfx + s * C::kStageSf, tn);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
+                }
+            }
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         const int q = warp & 3;
         const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
@@ -334,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         cluster_sync_all();
         Fp4Walk<NT, TW> again;
-        if (again.get(first, p, s_off, t) && !*abort_flag)
+        if (warp < 8 && again.get(first, p, s_off, t) && !*abort_flag)
             sum_parts<NT, OUT_F32>(smem_addr(smem), p, t, rank, split);
         __syncwarp();
         cluster_sync_all();
@@ -347,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int NT, int FMT, bool OUT_F32>
+template <int NT, int FMT, bool OUT_F32, typename T = void>
 cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     using C = Cfg<NT, FMT>;
     Fp4GemmParams p{};
@@ -359,11 +446,21 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     CUtensorMap mx, mw, msx, msw;
     const int64_t kbytes = (a.k + 1) / 2;
     const int64_t we = a.form == kFp4RagRows ? a.experts : 1;
-    if (!fp4_codes_map(&mx, a.x, a.m, kbytes, a.ldx, NT) || !fp4_codes_map(&mw, a.w, a.n * we, kbytes, a.ldw, TW) ||
-        !fp4_scales_map(&msx, a.sfx, a.x_row_blocks * p.kblocks, a.fmt) ||
+    constexpr bool kCast = !std::is_void<T>::value;
+    if constexpr (kCast) {
+        p.xr = a.xr;
+        p.sxr = a.sxr;
+        p.k = static_cast<int>(a.k);
+        p.xr_vec = (reinterpret_cast<uintptr_t>(a.xr) & 15u) == 0 && (a.sxr * (a.xr_bf16 ? 2 : 4)) % 16 == 0;
+        mx = msx = CUtensorMap{};
+    } else if (!fp4_codes_map(&mx, a.x, a.m, kbytes, a.ldx, NT) ||
+               !fp4_scales_map(&msx, a.sfx, a.x_row_blocks * p.kblocks, a.fmt)) {
+        return cudaErrorInvalidValue;
+    }
+    if (!fp4_codes_map(&mw, a.w, a.n * we, kbytes, a.ldw, TW) ||
         !fp4_scales_map(&msw, a.sfw, we * p.w_row_blocks * p.kblocks, a.fmt))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_kernel<NT, FMT, OUT_F32>;
+    auto kern = fp4_gemm_kernel<NT, FMT, OUT_F32, T>;
     if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmem); e != cudaSuccess) return e;
     int64_t tiles = static_cast<int64_t>(p.tiles_x) * p.tiles_w;
     if (a.form == kFp4RagRows) tiles = (a.m / NT + (a.experts < a.m ? a.experts : a.m)) * p.tiles_w;
@@ -373,10 +470,13 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
         const int64_t kb = (a.k + 255) / 256;
         while (split < kMaxSplit && tiles * split * 2 <= num_sms && kb >= split * 4) split *= 2;
     }
+    // at most 64 MB of W ahead over the grid, well inside L2
+    const int64_t grid = (split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms)) * split;
+    p.ahead = static_cast<int>((int64_t(64) << 20) / (grid * C::kStageW));
     const int64_t most = split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(most * split), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(kCast ? kThreads + 32 * kCastWarps : kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -431,6 +531,13 @@ void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
+    if (a.xr != nullptr) {
+        if (a.xr_bf16)
+            return a.fmt == kFp4Nv ? launch_t<kFp4CastRows, kFp4Nv, false, __nv_bfloat16>(a, st, num_sms)
+                                   : launch_t<kFp4CastRows, kFp4Mx, false, __nv_bfloat16>(a, st, num_sms);
+        return a.fmt == kFp4Nv ? launch_t<kFp4CastRows, kFp4Nv, false, float>(a, st, num_sms)
+                               : launch_t<kFp4CastRows, kFp4Mx, false, float>(a, st, num_sms);
+    }
     if (a.form == kFp4Plain && a.m <= 16) return launch_n<16>(a, st, num_sms);
     if (a.form == kFp4Plain && a.m <= 64) return launch_n<64>(a, st, num_sms);
     return launch_n<128>(a, st, num_sms);

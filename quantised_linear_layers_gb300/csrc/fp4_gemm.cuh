@@ -42,7 +42,10 @@ struct Fp4GemmArgs {
     int64_t ldd;
     bool out_f32;
     int accumulate;
-    int path;                    // 0 by size, 1 one SM per tile, 2 CTA pairs, 3 split along K
+    // X not cast yet (m <= kFp4CastRows): the product casts it itself
+    const void* xr;
+    bool xr_bf16;
+    int64_t sxr;                 // elements between its rows
     uint32_t* dev_status;
     uint64_t wait_limit_ns;
     int stall_producer;
@@ -70,7 +73,14 @@ struct Fp4GemmParams {
     uint32_t* dev_status;
     uint64_t wait_limit_ns;
     int stall_producer;
+    const void* xr;              // X before the cast (the kernel's casting form)
+    int64_t sxr;
+    int k, xr_vec;               // columns; rows start on 16 bytes
+    int ahead;                   // stages of W brought into L2 before the previous kernel ends
 };
+
+// Largest m whose X the product casts itself.
+constexpr int kFp4CastRows = 16;
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);

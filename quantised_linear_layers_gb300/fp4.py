@@ -75,7 +75,7 @@ def _need_wt(w: FP4Weight) -> ops.FP4Tensor:
 def forward(x: torch.Tensor, w: FP4Weight, x_scale: torch.Tensor | None = None,
             out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [T, out] = X [T, in] W^T (bf16)."""
-    return ops.gemm_fp4_nt(ops.fp4_cast(x, w.fmt, x_scale), w.w, out=out)
+    return ops.fp4_linear(x, w.w, x_scale, out=out)
 
 
 def forward_saving(x: torch.Tensor, w: FP4Weight):
@@ -97,13 +97,13 @@ def backward(dy: torch.Tensor, w: FP4Weight, x_cols: ops.FP4Tensor, need_dx: boo
 
 def dgrad(dy: torch.Tensor, w: FP4Weight, out: torch.Tensor | None = None) -> torch.Tensor:
     """dX [T, in] = dY [T, out] W (bf16)."""
-    return ops.gemm_fp4_nt(ops.fp4_cast(dy, w.fmt, _scale(dy, w.fmt)), _need_wt(w), out=out)
+    return ops.fp4_linear(dy, _need_wt(w), _scale(dy, w.fmt), out=out)
 
 
 def experts_forward(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight, x_scale: torch.Tensor | None = None,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [T, out]: rows offsets[e] .. offsets[e+1] of X [T, in] times W[e]^T (bf16)."""
-    return ops.gemm_fp4_nt_ragged(ops.fp4_cast(x, w.fmt, x_scale, offsets), w.w, out=out)
+    return ops.fp4_linear(x, w.w, x_scale, offsets, out=out)
 
 
 def experts_forward_saving(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight):
@@ -139,14 +139,14 @@ class _FP4Fn(torch.autograd.Function):
             ctx.x_cols = None
             return _forward(x, offsets, w4)
         y, cols = forward_saving(x, w4) if offsets is None else experts_forward_saving(x, offsets, w4)
-        ctx.x_cols = cols.with_tensors(None, None, None, None)
-        ctx.save_for_backward(offsets, *cols.tensors())
+        ctx.save_for_backward(offsets, cols.buf, cols.scale)
+        ctx.x_cols = cols.set_tensors(None, None, None)
         return y
 
     @staticmethod
     def backward(ctx, dy):
         w4, module = ctx.w4, ctx.module
-        offsets, *cols = ctx.saved_tensors
+        offsets = ctx.saved_tensors[0]
         dy = dy.contiguous()
         if ctx.x_cols is None:
             if not ctx.needs_input_grad[0]:
@@ -154,9 +154,11 @@ class _FP4Fn(torch.autograd.Function):
             if offsets is None:
                 dx = dgrad(dy, w4)
             else:
-                dx = ops.gemm_fp4_nt_ragged(ops.fp4_cast(dy, w4.fmt, _scale(dy, w4.fmt), offsets), _need_wt(w4))
+                dx = ops.fp4_linear(dy, _need_wt(w4), _scale(dy, w4.fmt), offsets)
             return dx.to(ctx.x_dtype), None, None, None, None
-        x_cols = ctx.x_cols.with_tensors(*cols)
+        _, buf, scale = ctx.saved_tensors
+        cols = ctx.x_cols
+        x_cols = ops.FP4Tensor(buf, cols.ld, scale, cols.fmt, cols.batch, cols.rows, cols.cols, offsets, cols.by_cols)
         main = module.main_grad
         kw = dict(need_dx=ctx.needs_input_grad[0], dw_out=main, accumulate=main is not None)
         dx, dw = backward(dy, w4, x_cols, **kw) if offsets is None else experts_backward(dy, offsets, w4, x_cols, **kw)

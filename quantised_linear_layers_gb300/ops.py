@@ -58,6 +58,8 @@ _SIGS = {
     "gemm_fp4_nt": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _int, _vp],
     "gemm_fp4_nt_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _int, _i64, _vp, _int, _i64, _i64,
                            _i64, _vp],
+    "fp4_linear_workspace_size": [_i64, _i64, _int, _int],
+    "fp4_linear": [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp],
     "gemm_fp4_wgrad_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64,
                               _int, _vp],
     "ql_cast_gemm_host_workspace_size": [_i64, _i64, _i64, _int],
@@ -89,6 +91,8 @@ class QLError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Load libqlinear.so (raises if it is missing: no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -101,6 +105,7 @@ def load_library(path: str = LIB_PATH):
             lib.ql_status_string.restype = ctypes.c_char_p
             lib.ql_gemm_workspace_size.restype = _sz
             lib.ql_cast_gemm_host_workspace_size.restype = _sz
+            lib.fp4_linear_workspace_size.restype = _sz
             lib.fp4_scale_bytes.restype = _i64
             lib.fp4_column_extent.restype = _i64
             _lib = lib
@@ -123,6 +128,10 @@ def _dtype_code(x: torch.Tensor) -> int:
     if x.dtype == torch.float32:
         return QL_F32
     raise TypeError(f"input must be bfloat16 or float32, got {x.dtype}")
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 def _bytes8(t: torch.Tensor) -> torch.Tensor:
@@ -446,55 +455,66 @@ def cast_gemm_host(x_host: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor, fmt
 # Microscaled 4-bit floating point
 # ---------------------------------------------------------------------------
 class FP4Tensor:
-    """A matrix (or a batch of them) in 4 bits, as a cast left it: codes ``q``
-    (uint8 [batch * rows, bytes]), scale blocks ``sf``, the tensor's scale
-    ``scale`` (fp32 [1], or None for 1), its format and its sizes; ``cols`` is
-    the reduction axis. ``offsets`` are the row ranges of the experts it was cast
-    by (``by_cols``: its columns are the experts' rows, each from a multiple of
-    256 on). The layouts are in include/qlinear.h."""
+    """A matrix (or a batch of them) in 4 bits, as a cast left it: codes and scale
+    blocks in one buffer ``buf`` (``q``: uint8 [batch * rows, ld]; ``sf``), the
+    tensor's scale ``scale`` (fp32 [1], or None for 1), its format and its sizes;
+    ``cols`` is the reduction axis. ``offsets`` are the row ranges of the experts
+    it was cast by (``by_cols``: its columns are the experts' rows, each from a
+    multiple of 256 on). The layouts are in include/qlinear.h."""
 
-    __slots__ = ("q", "sf", "scale", "fmt", "batch", "rows", "cols", "offsets", "by_cols")
+    __slots__ = ("buf", "ld", "scale", "fmt", "batch", "rows", "cols", "offsets", "by_cols", "device", "q_ptr", "sf_ptr",
+                 "scale_ptr")
 
-    def __init__(self, q, sf, scale, fmt, batch, rows, cols, offsets=None, by_cols=False):
-        self.q, self.sf, self.scale, self.fmt = q, sf, scale, fmt
-        self.batch, self.rows, self.cols = batch, rows, cols
-        self.offsets, self.by_cols = offsets, by_cols
+    def __init__(self, buf, ld, scale, fmt, batch, rows, cols, offsets=None, by_cols=False):
+        self.ld, self.fmt, self.batch, self.rows, self.cols, self.by_cols = ld, fmt, batch, rows, cols, by_cols
+        self.set_tensors(buf, scale, offsets)
 
-    def tensors(self):
-        """The tensors that hold it, for autograd to save."""
-        return self.q, self.sf, self.scale, self.offsets
+    def set_tensors(self, buf, scale, offsets):
+        """The tensors that hold it (``buf``, ``scale``, ``offsets``; None or not), as autograd saved them."""
+        self.buf, self.scale, self.offsets = buf, scale, offsets
+        self.scale_ptr = None if scale is None else scale.data_ptr()
+        if buf is not None:
+            self.device = buf.device
+            self.q_ptr = buf.data_ptr()
+            self.sf_ptr = self.q_ptr + self.batch * self.rows * self.ld
+        return self
 
-    def with_tensors(self, q, sf, scale, offsets):
-        return FP4Tensor(q, sf, scale, self.fmt, self.batch, self.rows, self.cols, offsets, self.by_cols)
+    @property
+    def q(self) -> torch.Tensor:
+        n = self.batch * self.rows
+        return self.buf[:n * self.ld].view(n, self.ld)
 
-
-def _fp4_group(fmt: int) -> int:
-    if fmt == FP4_NV:
-        return 16
-    if fmt == FP4_MX:
-        return 32
-    raise ValueError("fmt must be FP4_NV or FP4_MX")
-
-
-def _fp4_sf(batch: int, row_blocks: int, k: int, fmt: int, device) -> torch.Tensor:
-    words = _ceil(k, 4 * _fp4_group(fmt))
-    return torch.empty(max(batch * row_blocks * words, 1) * 512, dtype=torch.uint8, device=device)
+    @property
+    def sf(self) -> torch.Tensor:
+        return self.buf[self.batch * self.rows * self.ld:]
 
 
-def _ptr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
+_FP4_WORD = {FP4_NV: 64, FP4_MX: 128}       # columns of a scale block
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _fp4_buf(batch: int, rows: int, ld: int, row_blocks: int, kcols: int, fmt: int, device) -> torch.Tensor:
+    """Room for codes and scale blocks (ld is a multiple of 16, so both are aligned)."""
+    return torch.empty(batch * (rows * ld + row_blocks * -(-kcols // _FP4_WORD[fmt]) * 512), dtype=torch.uint8,
+                       device=device)
 
 
 def _fp4_input(x: torch.Tensor, fmt: int, tensor_scale, offsets):
-    """(batch, m, k, stride between batch entries, experts) of a cast's input, checked."""
-    _fp4_group(fmt)
+    """(type code, batch, m, k, stride between batch entries, experts) of a cast's input, checked."""
+    if fmt not in _FP4_WORD:
+        raise ValueError("fmt must be FP4_NV or FP4_MX")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dim() == 3:
+    dim = x.dim()
+    if dim == 2:
+        m, k = x.shape
+        batch, sb = 1, 0
+    elif dim == 3:
         batch, m, k = x.shape
         sb = x.stride(0)
-    elif x.dim() == 2:
-        (m, k), batch, sb = x.shape, 1, 0
     else:
         raise ValueError("x must be 2-D or a batch of 2-D matrices")
     if tensor_scale is not None:
@@ -505,9 +525,9 @@ def _fp4_input(x: torch.Tensor, fmt: int, tensor_scale, offsets):
     experts = 0
     if offsets is not None:
         experts = _fp4_experts(offsets, x.device)
-        if x.dim() != 2:
+        if dim != 2:
             raise ValueError("x must be 2-D with offsets")
-    return batch, m, k, sb, experts
+    return _dtype_code(x), batch, m, k, sb, experts
 
 
 def _fp4_experts(offsets: torch.Tensor, device) -> int:
@@ -521,16 +541,19 @@ def fp4_tensor_scale(x: torch.Tensor) -> torch.Tensor:
     """The FP4_NV scale of a tensor (any 2-D or 3-D strides, fp32 [1]): the least
     power of two t with max|x| <= 2688 t, at least 2^-80; a power of two leaves
     every group's scale s * t exact. NaN if x has an infinity or a NaN."""
-    if x.dim() == 3:
-        if x.stride(0) != x.shape[1] * x.stride(1):
-            x = x.contiguous()
-        x = x.as_strided((x.shape[0] * x.shape[1], x.shape[2]), (x.stride(1), x.stride(2)))
-    if x.dim() != 2 or not x.is_cuda:
+    dim = x.dim()
+    if dim not in (2, 3) or not x.is_cuda:
         raise ValueError("x must be a 2-D or 3-D CUDA tensor")
+    m, k = x.shape[-2], x.shape[-1]
+    if dim == 3:
+        if x.stride(0) != m * x.stride(1):
+            x = x.contiguous()
+        m *= x.shape[0]
     out = torch.empty(1, dtype=torch.float32, device=x.device)
-    st = load_library().fp4_tensor_scale(x.data_ptr(), _dtype_code(x), x.shape[0], x.shape[1], x.stride(0), x.stride(1),
-                                         out.data_ptr(), _stream(x))
-    _check("fp4_tensor_scale", st)
+    st = load_library().fp4_tensor_scale(x.data_ptr(), _dtype_code(x), m, k, x.stride(-2), x.stride(-1), out.data_ptr(),
+                                         _raw_stream(x.device))
+    if st:
+        _check("fp4_tensor_scale", st)
     return out
 
 
@@ -539,14 +562,16 @@ def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | No
     """Casts the rows of x [m, k] or [batch, m, k] (bf16 or fp32, any strides) to
     4 bits. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and
     the cast is the operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
-    batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
-    q = torch.empty((batch * m, _ceil(max(k, 1), 32) * 16), dtype=torch.uint8, device=x.device)
-    sf = _fp4_sf(batch, _ceil(m, 128) + experts, k, fmt, x.device)
+    code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
+    ld = -(-k // 32) * 16 or 16
+    dev = x.device
+    a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld, tensor_scale, fmt, batch, m, k, offsets)
     st = load_library().fp4_cast(
-        x.data_ptr(), _dtype_code(x), batch, m, k, sb, x.stride(-2), x.stride(-1), fmt, _ptr(tensor_scale),
-        q.data_ptr(), q.stride(0), sf.data_ptr(), _ptr(offsets), experts, _stream(x))
-    _check("fp4_cast", st)
-    return FP4Tensor(q, sf, tensor_scale, fmt, batch, m, k, offsets)
+        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), x.stride(-1), fmt, a.scale_ptr, a.q_ptr, ld, a.sf_ptr,
+        _ptr(offsets), experts, _raw_stream(dev))
+    if st:
+        _check("fp4_cast", st)
+    return a
 
 
 def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | None = None,
@@ -556,37 +581,37 @@ def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor
     operand of products that sum over x's rows; with ``offsets`` each expert's rows
     are columns of their own there (``gemm_fp4_wgrad_ragged``). ``rows=False``
     leaves the first out (None)."""
-    batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
+    code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
     if x.stride(-1) != 1 and k > 1:
         raise ValueError("x must have contiguous rows")
-    kpad = int(load_library().fp4_column_extent(m, experts))
-    qc = torch.empty((batch * k, max(kpad, 128) // 2), dtype=torch.uint8, device=x.device)
-    sfc = _fp4_sf(batch, _ceil(k, 128), kpad if experts else m, fmt, x.device)
-    q = sf = None
+    dev = x.device
+    kpad = (-(-m // 256) + experts) * 256 if experts else (-(-m // 128) * 128 or 128)   # fp4_column_extent
+    c = FP4Tensor(_fp4_buf(batch, k, kpad // 2, -(-k // 128), kpad if experts else m, fmt, dev), kpad // 2, tensor_scale,
+                  fmt, batch, k, m, offsets, experts > 0)
+    a = None
     if rows:
-        q = torch.empty((batch * m, _ceil(max(k, 1), 32) * 16), dtype=torch.uint8, device=x.device)
-        sf = _fp4_sf(batch, _ceil(m, 128) + experts, k, fmt, x.device)
+        ld = -(-k // 32) * 16 or 16
+        a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld, tensor_scale, fmt, batch, m, k,
+                      offsets)
     st = load_library().fp4_cast_dual(
-        x.data_ptr(), _dtype_code(x), batch, m, k, sb, x.stride(-2), fmt, _ptr(tensor_scale),
-        _ptr(q), q.stride(0) if rows else 0, _ptr(sf), qc.data_ptr(), qc.stride(0), sfc.data_ptr(), _ptr(offsets),
-        experts, _stream(x))
-    _check("fp4_cast_dual", st)
-    return (FP4Tensor(q, sf, tensor_scale, fmt, batch, m, k, offsets) if rows else None,
-            FP4Tensor(qc, sfc, tensor_scale, fmt, batch, k, m, offsets, by_cols=offsets is not None))
+        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), fmt, c.scale_ptr, a.q_ptr if rows else None,
+        a.ld if rows else 0, a.sf_ptr if rows else None, c.q_ptr, c.ld, c.sf_ptr, _ptr(offsets), experts,
+        _raw_stream(dev))
+    if st:
+        _check("fp4_cast_dual", st)
+    return a, c
 
 
 def fp4_dequant(a: FP4Tensor, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values [rows, cols] that a cast stands for (bf16 or fp32)."""
     if a.batch != 1 or a.offsets is not None:
         raise ValueError("fp4_dequant takes the cast of one matrix")
-    if out is None:
-        out = torch.empty((a.rows, a.cols), dtype=dtype, device=a.q.device)
-    if tuple(out.shape) != (a.rows, a.cols) or (a.cols > 1 and out.stride(1) != 1):
-        raise ValueError("out must be [rows, cols] with contiguous rows")
+    out = _fp4_out(out, (a.rows, a.cols), dtype, a.device, False)
     st = load_library().fp4_dequant(
-        a.q.data_ptr(), a.q.stride(0), a.sf.data_ptr(), a.fmt, _ptr(a.scale), a.rows, a.cols, out.data_ptr(),
-        _dtype_code(out), max(out.stride(0), a.cols), _stream(out))
-    _check("fp4_dequant", st)
+        a.q_ptr, a.ld, a.sf_ptr, a.fmt, a.scale_ptr, a.rows, a.cols, out.data_ptr(), _dtype_code(out),
+        max(out.stride(0), a.cols), _raw_stream(a.device))
+    if st:
+        _check("fp4_dequant", st)
     return out
 
 
@@ -595,7 +620,7 @@ def _fp4_pair(x: FP4Tensor, w: FP4Tensor):
         raise ValueError("the operands' formats differ")
     if x.cols != w.cols:
         raise ValueError("the operands must share K")
-    if x.q.device != w.q.device:
+    if x.device != w.device:
         raise ValueError("the operands must be on one device")
 
 
@@ -619,12 +644,13 @@ def gemm_fp4_nt(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = None, dty
     _fp4_pair(x, w)
     if x.batch != 1 or w.batch != 1 or x.offsets is not None or w.offsets is not None:
         raise ValueError("gemm_fp4_nt takes casts of one matrix each")
-    out = _fp4_out(out, (x.rows, w.rows), dtype, x.q.device, accumulate)
+    out = _fp4_out(out, (x.rows, w.rows), dtype, x.device, accumulate)
     st = load_library().gemm_fp4_nt(
-        x.q.data_ptr(), x.q.stride(0), x.sf.data_ptr(), _ptr(x.scale), w.q.data_ptr(), w.q.stride(0), w.sf.data_ptr(),
-        _ptr(w.scale), x.fmt, out.data_ptr(), _dtype_code(out), max(out.stride(0), w.rows), x.rows, w.rows, x.cols,
-        int(bool(accumulate)), _stream(out))
-    _check("gemm_fp4_nt", st)
+        x.q_ptr, x.ld, x.sf_ptr, x.scale_ptr, w.q_ptr, w.ld, w.sf_ptr, w.scale_ptr, x.fmt, out.data_ptr(),
+        _dtype_code(out), max(out.stride(0), w.rows), x.rows, w.rows, x.cols, 1 if accumulate else 0,
+        _raw_stream(x.device))
+    if st:
+        _check("gemm_fp4_nt", st)
     return out
 
 
@@ -636,12 +662,49 @@ def gemm_fp4_nt_ragged(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = No
     _fp4_pair(x, w)
     if x.offsets is None or x.by_cols or w.offsets is not None or w.batch != x.offsets.shape[0] - 1:
         raise ValueError("x must be cast by expert and w hold one matrix per expert")
-    out = _fp4_out(out, (x.rows, w.rows), dtype, x.q.device, False)
+    out = _fp4_out(out, (x.rows, w.rows), dtype, x.device, False)
     st = load_library().gemm_fp4_nt_ragged(
-        x.q.data_ptr(), x.q.stride(0), x.sf.data_ptr(), _ptr(x.scale), w.q.data_ptr(), w.q.stride(0), w.sf.data_ptr(),
-        _ptr(w.scale), x.fmt, out.data_ptr(), _dtype_code(out), max(out.stride(0), w.rows), x.offsets.data_ptr(),
-        w.batch, x.rows, w.rows, x.cols, _stream(out))
-    _check("gemm_fp4_nt_ragged", st)
+        x.q_ptr, x.ld, x.sf_ptr, x.scale_ptr, w.q_ptr, w.ld, w.sf_ptr, w.scale_ptr, x.fmt, out.data_ptr(),
+        _dtype_code(out), max(out.stride(0), w.rows), x.offsets.data_ptr(), w.batch, x.rows, w.rows, x.cols,
+        _raw_stream(x.device))
+    if st:
+        _check("gemm_fp4_nt_ragged", st)
+    return out
+
+
+def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = None,
+               offsets: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The forward call, cast and product in one: D [m, n] bf16 = X W^T of
+    x [m, k] (bf16 or fp32) and a cast W [n, k]; with ``offsets`` (int32
+    [experts + 1]) by expert, W [experts, n, k]. Equal to ``fp4_cast`` followed by
+    ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 16 rows take one launch."""
+    if x.dim() == 2 and x.stride(1) != 1 and x.shape[1] > 1:
+        x = x.contiguous()
+    code, batch, m, k, _, experts = _fp4_input(x, w.fmt, x_scale, offsets)
+    dev = x.device
+    if x.dim() != 2 or k != w.cols or dev != w.device:
+        raise ValueError("x must be [m, k] with w's k, on w's device")
+    if w.offsets is not None or w.batch != (experts or 1):
+        raise ValueError("w must be the cast of one matrix, or of one per expert with offsets")
+    n = w.rows
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        ldd = n
+    else:
+        out = _fp4_out(out, (m, n), torch.bfloat16, dev, False)
+        if out.dtype != torch.bfloat16:
+            raise ValueError("out must be bf16")
+        ldd = max(out.stride(0), n)
+    lib = load_library()
+    size, ws = 0, None
+    if m > 16:
+        size = lib.fp4_linear_workspace_size(m, k, w.fmt, experts)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    st = lib.fp4_linear(
+        x.data_ptr(), code, x.stride(0), _ptr(x_scale), w.q_ptr, w.ld, w.sf_ptr, w.scale_ptr, w.fmt, out.data_ptr(), ldd,
+        _ptr(offsets), experts, m, n, k, _ptr(ws), size, _raw_stream(dev))
+    if st:
+        _check("fp4_linear", st)
     return out
 
 
@@ -654,14 +717,14 @@ def gemm_fp4_wgrad_ragged(y: FP4Tensor, x: FP4Tensor, out: torch.Tensor | None =
     if not y.by_cols or not x.by_cols or y.offsets.shape != x.offsets.shape:
         raise ValueError("both operands must be column-wise casts by the same experts")
     experts = y.offsets.shape[0] - 1
-    out = _fp4_out(out, (experts, y.rows, x.rows), torch.float32, y.q.device, accumulate)
+    out = _fp4_out(out, (experts, y.rows, x.rows), torch.float32, y.device, accumulate)
     if out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be contiguous fp32")
     st = load_library().gemm_fp4_wgrad_ragged(
-        y.q.data_ptr(), y.q.stride(0), y.sf.data_ptr(), _ptr(y.scale), x.q.data_ptr(), x.q.stride(0), x.sf.data_ptr(),
-        _ptr(x.scale), y.fmt, out.data_ptr(), x.rows, y.offsets.data_ptr(), experts, y.cols, y.rows, x.rows,
-        int(bool(accumulate)), _stream(out))
-    _check("gemm_fp4_wgrad_ragged", st)
+        y.q_ptr, y.ld, y.sf_ptr, y.scale_ptr, x.q_ptr, x.ld, x.sf_ptr, x.scale_ptr, y.fmt, out.data_ptr(), x.rows,
+        y.offsets.data_ptr(), experts, y.cols, y.rows, x.rows, 1 if accumulate else 0, _raw_stream(y.device))
+    if st:
+        _check("gemm_fp4_wgrad_ragged", st)
     return out
 
 

@@ -318,6 +318,56 @@ def test_gradients_against_differences(ops, fp4, fmt):
     assert torch.equal(dx.double(), exact_dx.float().bfloat16().double())
 
 
+@FMTS
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 4096, 7168), (3, 300, 515), (16, 257, 2048), (16, 128, 96), (9, 640, 4099),
+                                   (17, 300, 515), (200, 300, 1000)])
+def test_forward_call_equals_cast_and_product(ops, m, n, k, dtype, fmt):
+    """Bit for bit, also where the product casts X itself (up to 16 rows), for rows that start anywhere."""
+    big, w = acts(m, k + 3, seed=m + k, dtype=dtype), acts(n, k, seed=n, mul=0.02)
+    b = ops.fp4_cast(w, fmt, ops.fp4_tensor_scale(w) if fmt == 0 else None)
+    t = torch.tensor([0.25], device="cuda") if fmt == 0 else None
+    for x in (big[:, :k].contiguous(), big[:, 1:k + 1], big[:, 3:].t().contiguous().t()):
+        for scale in (None, t):
+            want = ops.gemm_fp4_nt(ops.fp4_cast(x, fmt, scale), b)
+            assert torch.equal(ops.fp4_linear(x, b, scale), want)
+            if m <= 16:
+                check(want, ref.values(np64(x), fmt, 1.0 if scale is None else 0.25),
+                      ref.values(np64(w), fmt, 1.0 if b.scale is None else float(b.scale)))
+    out = torch.full((m, n + 5), -7.0, dtype=torch.bfloat16, device="cuda")
+    ops.fp4_linear(x, b, out=out[:, 2:n + 2])
+    assert torch.equal(out[:, 2:n + 2], ops.fp4_linear(x, b)) and bool((out[:, :2] == -7).all()) and bool((out[:, n + 2:] == -7).all())
+
+
+@FMTS
+@pytest.mark.parametrize("offs", [[0, 1], [0, 3, 3, 7, 16], [2, 2, 5, 6], [0, 9, 25], [0, 100, 100, 331]],
+                         ids=["1", "16", "6", "25", "331"])
+def test_forward_call_by_expert(ops, offs, fmt):
+    m, n, k, e = offs[-1], 300, 515, len(offs) - 1
+    x, w = acts(m, k, seed=1), acts(e, n, k, seed=2, mul=0.02)
+    off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    b = ops.fp4_cast(w, fmt)
+    want = torch.full((m, n), -7.0, dtype=torch.bfloat16, device="cuda")
+    ops.gemm_fp4_nt_ragged(ops.fp4_cast(x, fmt, offsets=off), b, out=want)
+    got = torch.full_like(want, -7.0)
+    ops.fp4_linear(x, b, offsets=off, out=got)
+    assert torch.equal(got, want)
+    xv = ref.values(np64(x), fmt)
+    for i, (lo, hi) in enumerate(zip(offs[:-1], offs[1:])):
+        if hi > lo:
+            check(got[lo:hi], xv[lo:hi], ref.values(np64(w[i]), fmt))
+
+
+@FMTS
+def test_forward_call_non_finite(ops, fmt):
+    x, w = acts(7, 640, seed=1), acts(300, 640, seed=2)
+    x[2, 100], x[5, 639] = float("nan"), float("-inf")
+    d = ops.fp4_linear(x, ops.fp4_cast(w, fmt))
+    bad = torch.zeros((7, 300), dtype=torch.bool, device="cuda")
+    bad[2], bad[5] = True, True
+    assert torch.equal(torch.isnan(d), bad)
+
+
 def test_side_stream_and_graph(ops, fp4):
     x, w = acts(48, 512, seed=1), acts(384, 512, seed=2)
     w4 = fp4.FP4Weight(w, 0, dgrad=False)
@@ -351,6 +401,8 @@ def test_time_out_is_reported(ops):
             assert ops.device_status() == 5
             ops.gemm_fp4_nt_ragged(ra, rb)
             assert ops.device_status() == 5
+            ops.fp4_linear(acts(9, 512, seed=1), b)
+            assert ops.device_status() == 5
     finally:
         ops.test_stall_gemm_producer(False)
         ops.set_wait_limit_ms(2000)
@@ -370,12 +422,15 @@ def test_refusals(ops, fp4):
                 lambda: ops.fp4_cast(x[None], 0, None, off), lambda: ops.fp4_cast_dual(x.t()),
                 lambda: ops.gemm_fp4_nt(a, bm), lambda: ops.gemm_fp4_nt(a, ops.fp4_cast(w[:, :32])),
                 lambda: ops.gemm_fp4_nt(r, b), lambda: ops.gemm_fp4_nt_ragged(a, ops.fp4_cast(w[None])),
-                lambda: ops.gemm_fp4_nt_ragged(r, b.with_tensors(b.q, b.sf, None, off)),
+                lambda: ops.gemm_fp4_nt_ragged(r, r),
                 lambda: ops.gemm_fp4_nt_ragged(r, ops.fp4_cast(torch.stack([w, w]))),
                 lambda: ops.gemm_fp4_nt(a, b, accumulate=True),
                 lambda: ops.gemm_fp4_nt(a, b, out=torch.empty((8, 16), dtype=torch.bfloat16, device="cuda"), accumulate=True),
                 lambda: ops.gemm_fp4_nt(a, b, out=torch.empty((8, 15), device="cuda")),
                 lambda: ops.gemm_fp4_nt(a, b, out=torch.empty((16, 8), device="cuda").t()),
+                lambda: ops.fp4_linear(x[0], b), lambda: ops.fp4_linear(x[:, :32], b), lambda: ops.fp4_linear(x, b, offsets=off[:1]),
+                lambda: ops.fp4_linear(x, ops.fp4_cast(torch.stack([w, w]))), lambda: ops.fp4_linear(x, bm, one),
+                lambda: ops.fp4_linear(x, b, out=torch.empty((8, 16), device="cuda")),
                 lambda: ops.gemm_fp4_wgrad_ragged(a, b), lambda: ops.fp4_dequant(r), lambda: fp4.FP4Weight(w[None]),
                 lambda: fp4.dgrad(acts(8, 16, seed=3), fp4.FP4Weight(w, dgrad=False)),
                 lambda: fp4.FP4Linear(64, 16, device="cuda")(acts(8, 63, seed=1))):

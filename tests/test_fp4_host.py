@@ -68,6 +68,18 @@ def test_refused_before_cuda(L):
     assert R(p, 32, p, None, p, 32, p, None, 0, p, 0, 8, p, 0, 4, 8, 64, None) == 1
     assert R(p, 32, p, None, p, 32, p, None, 0, p, 0, 8, p, 600, 4, 8, 64, None) == 2
     assert R(p, 32, p, None, p, 32, p, None, 0, p, 0, 8, p, 2, 4, 8, 0, None) == 2       # k == 0
+    F = L.fp4_linear
+    assert F(p, 0, 64, None, p, 32, p, None, 2, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown format
+    assert F(p, 3, 64, None, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown type
+    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 7, None, 0, 4, 8, 64, None, 0, None) == 1     # D's rows too short
+    assert F(None, 0, 64, None, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1
+    assert F(p, 0, 64, None, p, 40, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 3
+    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, p, 0, 4, 8, 64, None, 0, None) == 1        # offsets, no experts
+    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, p, 600, 4, 8, 64, None, 0, None) == 2
+    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, None, 0, 40, 8, 64, None, 0, None) == 1    # no workspace
+    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, None, 0, 40, 8, 64, p, 10, None) == 1
+    assert L.fp4_linear_workspace_size(16, 7168, 0, 0) == 0
+    assert L.fp4_linear_workspace_size(40, 65, 0, 0) == 40 * 48 + 2 * 512
     W = L.gemm_fp4_wgrad_ragged
     assert W(p, 1024, p, None, p, 1024, p, None, 0, p, 8, None, 2, 4, 4, 8, 0, None) == 1
     assert W(p, 16, p, None, p, 1024, p, None, 0, p, 8, p, 2, 4, 4, 8, 0, None) == 1     # columns too short
