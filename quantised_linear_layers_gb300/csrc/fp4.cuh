@@ -102,31 +102,63 @@ cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int6
                             cudaStream_t st, int num_sms);
 
 #ifdef __CUDACC__
-// Larger of two magnitudes; a NaN operand gives NaN.
+// Larger of two magnitudes; a NaN operand gives NaN. The bf16 form takes two
+// pairs of values of any sign and leaves signs that the caller drops.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t bf16x2_maxabs_nan(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Two fp32 values in one 64-bit register: one instruction, each half rounded
+// as the scalar operation.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f32x2_get(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float rcp_approx(float v) {        // within 1 ulp
+    float d;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
     return d;
 }
 
 // Eight values to eight E2M1 codes (v[0] lowest), round to nearest even, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&v)[4]) {
     uint32_t d;
     asm("{\n"
         ".reg .b8 b0, b1, b2, b3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        ".reg .f32 l0, h0, l1, h1, l2, h2, l3, h3;\n"
+        "mov.b64 {l0, h0}, %1;\n"
+        "mov.b64 {l1, h1}, %2;\n"
+        "mov.b64 {l2, h2}, %3;\n"
+        "mov.b64 {l3, h3}, %4;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, h0, l0;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, h1, l1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, h2, l2;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, h3, l3;\n"
         "mov.b32 %0, {b0, b1, b2, b3};\n"
         "}\n"
         : "=r"(d)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+        : "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]));
     return d;
 }
 
@@ -137,14 +169,30 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 
 // The tensor's scale as the groups' scales use it.
 struct Fp4Tensor {
-    float t, t6;     // t, 6 t
+    float t, t6, r6;     // t, 6 t, 1 / (6 t)
 };
 __device__ __forceinline__ Fp4Tensor fp4_tensor(const float* tscale) {
-    const float t = tscale != nullptr ? __ldg(tscale) : 1.0f;
-    return Fp4Tensor{t, __fmul_rn(6.0f, t)};
+    Fp4Tensor o;
+    o.t = tscale != nullptr ? __ldg(tscale) : 1.0f;
+    o.t6 = __fmul_rn(6.0f, o.t);
+    o.r6 = __frcp_rn(o.t6);
+    return o;
 }
 
-// Scale of one group: its stored byte, its value S and 1 / S (mx: exactly).
+// a / b from r, 1 / b within an ulp: q = a r is within a few ulps, the residual
+// a - q b is exact in an FMA, and q + r (a - q b) is a / b to within 2^-44
+// before it is rounded (the last step of P. Markstein, IBM J. Res. Dev. 34,
+// 1990). A quotient that fp32 holds, such as a halfway case of E2M1, is found
+// exactly; with t a power of two S has four significant bits, no other quotient
+// is that near to a rounding boundary, and the result is the correctly rounded
+// one.
+__device__ __forceinline__ float quot(float a, float b, float r) {
+    const float q = __fmul_rn(a, r);
+    return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
+}
+
+// Scale of one group: its stored byte and what its elements are divided by.
+// nv: S and 1 / S; mx: the power of two 1 / S alone.
 struct Fp4Scale {
     uint32_t byte;
     float s, r;
@@ -155,11 +203,10 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Fp4Tensor& tn) {
     Fp4Scale o;
     o.finite = amax <= 3.402823466e38f;              // false for infinity and NaN
     if constexpr (FMT == kFp4Nv) {
-        float d = __fdiv_rn(amax, tn.t6);
-        d = fminf(fmaxf(d, 0.001953125f), 448.0f);
+        const float d = fminf(fmaxf(quot(amax, tn.t6, tn.r6), 0.001953125f), 448.0f);
         o.byte = static_cast<uint32_t>(__nv_cvt_float_to_fp8(d, __NV_SATFINITE, __NV_E4M3));
         o.s = __fmul_rn(e4m3_value(o.byte), tn.t);
-        o.r = __frcp_rn(o.s);
+        o.r = rcp_approx(o.s);
         if (!o.finite) o.byte = 0x7F;
     } else {
         const uint32_t b = __float_as_uint(amax);
@@ -173,39 +220,31 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Fp4Tensor& tn) {
     return o;
 }
 
-// x / S, correctly rounded. mx: a power of two. nv: one step of Markstein's
-// correction (P. Markstein, IBM J. Res. Dev. 34, 1990): from the correctly
-// rounded reciprocal r, q = x r is within an ulp of x / S, and q + r (x - q S)
-// with the residual exact in an FMA rounds to the quotient. Halfway cases of
-// E2M1 (x = S times a midpoint, common for bf16 x) are therefore kept.
+// Sixteen values of one group (or half an mx group), as pairs, to two words of codes.
 template <int FMT>
-__device__ __forceinline__ float fp4_quot(float x, const Fp4Scale& g) {
-    const float q = __fmul_rn(x, g.r);
-    if constexpr (FMT == kFp4Mx) return q;
-    return __fmaf_rn(__fmaf_rn(-q, g.s, x), g.r, q);
-}
-
-// Sixteen values of one group (or half an mx group) to two words of codes.
-template <int FMT>
-__device__ __forceinline__ uint2 fp4_codes16(const float (&x)[16], const Fp4Scale& g) {
-    float v[8], w[8];
+__device__ __forceinline__ uint2 fp4_codes16(const uint64_t (&x)[8], const Fp4Scale& g) {
+    const uint64_t r = f32x2(g.r, g.r);
+    uint64_t v[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        v[i] = fp4_quot<FMT>(x[i], g);
-        w[i] = fp4_quot<FMT>(x[8 + i], g);
+        uint64_t q = mul2(x[i], r);
+        if constexpr (FMT == kFp4Nv) {
+            const uint64_t ns = f32x2(-g.s, -g.s);
+            q = fma2(fma2(q, ns, x[i]), r, q);
+        }
+        v[i >> 2][i & 3] = q;
     }
-    uint2 o = make_uint2(e2m1x8(v), e2m1x8(w));
+    uint2 o = make_uint2(e2m1x8(v[0]), e2m1x8(v[1]));
     if (!g.finite) o = make_uint2(0u, 0u);
     return o;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+__device__ __forceinline__ uint64_t bf16x2_f32x2(uint32_t w) {
+    return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// The larger magnitude of a pair that bf16x2_maxabs_nan left.
+__device__ __forceinline__ float bf16x2_amax(uint32_t m) {
+    return max_nan(__uint_as_float((m << 16) & 0x7FFFFFFFu), __uint_as_float(m & 0x7FFF0000u));
 }
 
 // Sixteen consecutive elements of a row as they lie in memory.
@@ -233,15 +272,14 @@ struct Raw16<__nv_bfloat16> {
         u[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
     __device__ __forceinline__ float amax() const {
-        const uint32_t k = 0x7FFF7FFFu;
-        uint32_t m = bf16x2_max_nan(bf16x2_max_nan(u[0].x & k, u[0].y & k), bf16x2_max_nan(u[0].z & k, u[0].w & k));
-        m = bf16x2_max_nan(m, bf16x2_max_nan(bf16x2_max_nan(u[1].x & k, u[1].y & k),
-                                             bf16x2_max_nan(u[1].z & k, u[1].w & k)));
-        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        const uint32_t a = bf16x2_maxabs_nan(bf16x2_maxabs_nan(u[0].x, u[0].y), bf16x2_maxabs_nan(u[0].z, u[0].w));
+        const uint32_t b = bf16x2_maxabs_nan(bf16x2_maxabs_nan(u[1].x, u[1].y), bf16x2_maxabs_nan(u[1].z, u[1].w));
+        return bf16x2_amax(bf16x2_maxabs_nan(a, b));
     }
-    __device__ __forceinline__ void values(float (&v)[16]) const {
-        unpack8(u[0], v);
-        unpack8(u[1], v + 8);
+    __device__ __forceinline__ void values(uint64_t (&v)[8]) const {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bf16x2_f32x2(w[i]);
     }
 };
 template <>
@@ -265,9 +303,9 @@ struct Raw16<float> {
         for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(f[i]));
         return m;
     }
-    __device__ __forceinline__ void values(float (&v)[16]) const {
+    __device__ __forceinline__ void values(uint64_t (&v)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = f[i];
+        for (int i = 0; i < 8; ++i) v[i] = f32x2(f[2 * i], f[2 * i + 1]);
     }
 };
 #endif

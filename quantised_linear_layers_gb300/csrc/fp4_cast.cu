@@ -44,56 +44,76 @@ __device__ __forceinline__ int64_t expert_sf_row(const int32_t* offsets, int exp
     return static_cast<int64_t>(blocks) * 128 + (row - start);
 }
 
-// One warp takes a row's 512-column pieces, U of them at a time (their loads
-// are all issued before the first is used); each lane has 16 consecutive
-// columns: an nv group, or half an mx group whose other half is the next
-// lane's. VEC: 16-byte loads along contiguous rows; otherwise element loads
-// with any strides. Rows are taken in the order of the scale blocks' sectors
-// (rows r, r+32, r+64, r+96 of a block are neighbours there).
-template <typename T, int FMT, bool VEC, int U>
+// How the rows of x lie: on 16-byte boundaries, contiguous but starting
+// anywhere, or with any strides.
+constexpr int kRowsVec = 0, kRowsContiguous = 1, kRowsStrided = 2;
+
+// 512 columns of a contiguous row that starts anywhere, one column per lane and
+// load, through the warp's shared memory: 16 columns per lane from there. (A
+// lane loading its own 16 columns one by one touches 32 lines per load:
+// 1003 x 4099 fp32 took 21 us instead of 7.)
+template <typename T>
+__device__ __forceinline__ void load_piece(Raw16<T>& raw, const T* row, int64_t c0, int64_t k, T* buf) {
+    const int lane = threadIdx.x & 31;
+    T v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t c = c0 + i * 32 + lane;
+        v[i] = c < k ? row[c] : T(0.0f);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) buf[i * 32 + lane] = v[i];
+    __syncwarp();
+    const uint4* s = reinterpret_cast<const uint4*>(buf + lane * 16);
+    uint4* d = reinterpret_cast<uint4*>(&raw);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) d[i] = s[i];
+}
+
+// A warp takes a row, in pieces of 512 columns, U of them at a time with their
+// loads issued first; a lane has 16 consecutive columns: an nv group, or half
+// an mx group whose other half is the next lane's. A block's eight rows are
+// those of one 32-byte sector of their scale block (rows r, r+32, r+64, r+96
+// and the next four), whose words its warps write at about the same time; the
+// columns are shared out over blockIdx.y when there are few rows.
+template <typename T, int FMT, int ROWS, int U>
 __global__ void __launch_bounds__(kThreads) fp4_cast_kernel(const Fp4CastArgs p) {
+    __shared__ __align__(16) T s_buf[ROWS == kRowsContiguous ? kThreads / 32 * 512 : 1];
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int lane = threadIdx.x & 31;
-    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t kblocks = fp4_kblocks(p.k, FMT);
     const int pieces = static_cast<int>((p.k + 511) / 512);
     const int steps = (pieces + U - 1) / U;
-    const int64_t seg_blocks = (p.seg_rows + 127) / 128;
-    const int64_t segs = p.seg_rows > 0 ? (p.m / p.seg_rows) : 1;
-    const int64_t rows = p.offsets != nullptr ? p.m : segs * seg_blocks * 128;   // rows in the order taken
+    int64_t row, sf_row;
+    const T* xr = static_cast<const T*>(p.x);
+    if (p.offsets != nullptr) {
+        row = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+        sf_row = row < p.m ? expert_sf_row(p.offsets, p.num_experts, p.m, row) : -1;
+        if (sf_row < 0 || (sf_row >> 7) >= p.sf_row_blocks) return;
+        xr += row * p.sxm;
+    } else {
+        const unsigned block = blockIdx.x >> 4, i = (blockIdx.x & 15u) * 8 + warp;
+        const unsigned seg_blocks = static_cast<unsigned>((p.seg_rows + 127) >> 7);
+        const unsigned seg = block / seg_blocks;
+        sf_row = static_cast<int64_t>(block) * 128 + (i & 3) * 32 + (i >> 2);
+        const int64_t in_seg = sf_row - static_cast<int64_t>(seg) * seg_blocks * 128;
+        if (in_seg >= p.seg_rows) return;
+        row = static_cast<int64_t>(seg) * p.seg_rows + in_seg;
+        xr += seg * p.sxseg + in_seg * p.sxm;
+    }
     const Fp4Tensor tn = fp4_tensor(p.tscale);
-    const int64_t tasks = rows * steps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); t < tasks; t += nwarps) {
-        // eight rows (one 32-byte sector of a scale block) side by side, then the next columns
-        const int64_t r8 = t / (8 * steps);
-        const int in8 = static_cast<int>(t % (8 * steps));
-        int64_t ro, sf_row, row;
-        int step;
-        if (p.offsets != nullptr) {
-            ro = t / steps;
-            step = static_cast<int>(t % steps);
-            row = ro;
-            sf_row = expert_sf_row(p.offsets, p.num_experts, p.m, row);
-            if (sf_row < 0 || (sf_row >> 7) >= p.sf_row_blocks) continue;
-        } else {
-            step = in8 / 8;
-            ro = r8 * 8 + in8 % 8;
-            const int i = static_cast<int>(ro & 127);
-            sf_row = (ro & ~static_cast<int64_t>(127)) + (i & 3) * 32 + (i >> 2);
-            const int64_t seg = (sf_row >> 7) / seg_blocks;
-            const int64_t in_seg = sf_row - seg * seg_blocks * 128;
-            if (in_seg >= p.seg_rows) continue;
-            row = seg * p.seg_rows + in_seg;
-        }
-        const int64_t seg = row / p.seg_rows;
-        const T* xr = static_cast<const T*>(p.x) + seg * p.sxseg + (row - seg * p.seg_rows) * p.sxm;
+    uint8_t* q = p.q + row * p.ldq;
+    uint8_t* sf = p.sf + (sf_row >> 7) * kblocks * kFp4SfBlock + (sf_row & 31) * 16 + ((sf_row >> 5) & 3) * 4;
+    for (int step = blockIdx.y; step < steps; step += gridDim.y) {
         Raw16<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t c = static_cast<int64_t>(step * U + u) * 512 + lane * 16;
-            if (c >= p.k) raw[u].zero();
-            else if (VEC && c + 16 <= p.k) raw[u].load(xr + c);
+            if constexpr (ROWS == kRowsContiguous) load_piece(raw[u], xr, c - lane * 16, p.k, s_buf + warp * 512);
+            else if (c >= p.k) raw[u].zero();
+            else if (ROWS == kRowsVec && c + 16 <= p.k) raw[u].load(xr + c);
             else raw[u].load_some(xr + c * p.sxk, p.sxk, static_cast<int>(p.k - c < 16 ? p.k - c : 16));
         }
 #pragma unroll
@@ -102,23 +122,18 @@ __global__ void __launch_bounds__(kThreads) fp4_cast_kernel(const Fp4CastArgs p)
             float amax = raw[u].amax();
             if constexpr (FMT == kFp4Mx) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             const Fp4Scale g = fp4_scale<FMT>(amax, tn);
-            float v[16];
+            uint64_t v[8];
             raw[u].values(v);
             const uint2 codes = fp4_codes16<FMT>(v, g);
-            if (c < p.k) *reinterpret_cast<uint2*>(p.q + row * p.ldq + (c >> 1)) = codes;
-            // the four bytes of a block's row
+            if (c < p.k) *reinterpret_cast<uint2*>(q + (c >> 1)) = codes;
+            // the four bytes of a scale block's row
             constexpr int lanes = FMT == kFp4Nv ? 1 : 2;           // lanes per group
             const bool live = (c & ~static_cast<int64_t>(fp4_group(FMT) - 1)) < p.k;
             uint32_t w = live ? g.byte << (8 * ((lane / lanes) & 3)) : 0u;
-            if constexpr (lanes == 2) w = (lane & 1) ? 0u : w;
-            if constexpr (lanes == 2) w |= __shfl_xor_sync(0xffffffffu, w, 1);
             w |= __shfl_xor_sync(0xffffffffu, w, lanes);
             w |= __shfl_xor_sync(0xffffffffu, w, 2 * lanes);
             const int64_t kb = c / (4 * fp4_group(FMT));
-            if (lane % (4 * lanes) == 0 && kb < kblocks) {
-                uint8_t* dst = p.sf + ((sf_row >> 7) * kblocks + kb) * kFp4SfBlock + (sf_row & 31) * 16 + ((sf_row >> 5) & 3) * 4;
-                *reinterpret_cast<uint32_t*>(dst) = w;
-            }
+            if (lane % (4 * lanes) == 0 && kb < kblocks) *reinterpret_cast<uint32_t*>(sf + kb * kFp4SfBlock) = w;
         }
     }
 }
@@ -138,7 +153,7 @@ struct DualSmem {
     static constexpr int kBytes = kOffSfc + 2 * kFp4SfBlock;
 };
 
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int ROWS>
 __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     using S = DualSmem<T>;
@@ -180,42 +195,59 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
         }
     }
     __syncthreads();
-    const int64_t rows = s_rows, row0 = s_row0, sfblk = s_sfblk, kcol = s_kcol;
+    const int64_t row0 = s_row0, sfblk = s_sfblk, kcol = s_kcol;
+    const int rows = static_cast<int>(s_rows);
     if (rows < 0 || kcol >= p.kpad) return;
+    const int cols = static_cast<int>(p.k - c0 < 128 ? p.k - c0 : 128);
     const Fp4Tensor tn = fp4_tensor(p.tscale);
-    const T* x = static_cast<const T*>(p.x) + bz * p.sxb;
+    const T* x = static_cast<const T*>(p.x) + bz * p.sxb + row0 * p.sxm + c0;
     const int64_t kblocks_r = fp4_kblocks(p.k, FMT);
     constexpr int kWords = FMT == kFp4Nv ? 2 : 1;             // scale blocks across 128 columns
+    if constexpr (ROWS != kRowsVec) {
+        // rows that start anywhere: one element per lane and load
+        T* tile = reinterpret_cast<T*>(smem);
+        constexpr int pitch = S::kPitch / sizeof(T);
+        const int c = tid & 127;
+#pragma unroll 8
+        for (int r = tid >> 7; r < 128; r += kThreads / 128)
+            tile[r * pitch + c] = (r < rows && c < cols) ? x[r * p.sxm + c] : T(0.0f);
+        __syncthreads();
+    }
     {
         // rows: unit u = (row u / 8, 16 columns u % 8)
         Raw16<T> raw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int u = i * kThreads + tid, r = u >> 3;
-            const int64_t c = c0 + (u & 7) * 16;
-            if (r >= rows || c >= p.k) raw[i].zero();
-            else if (VEC && c + 16 <= p.k) raw[i].load(x + (row0 + r) * p.sxm + c);
-            else raw[i].load_some(x + (row0 + r) * p.sxm + c, 1, static_cast<int>(p.k - c < 16 ? p.k - c : 16));
+            const int u = i * kThreads + tid, r = u >> 3, c = (u & 7) * 16;
+            if constexpr (ROWS != kRowsVec) {
+                const uint4* src = reinterpret_cast<const uint4*>(smem + r * S::kPitch + c * sizeof(T));
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) reinterpret_cast<uint4*>(&raw[i])[j] = src[j];
+            } else {
+                if (r >= rows || c >= cols) raw[i].zero();
+                else if (c + 16 <= cols) raw[i].load(x + r * p.sxm + c);
+                else raw[i].load_some(x + r * p.sxm + c, 1, cols - c);
+            }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int u = i * kThreads + tid, r = u >> 3, cg = u & 7;
-            uint4* dst = reinterpret_cast<uint4*>(smem + r * S::kPitch + cg * 16 * sizeof(T));
-            const uint4* src = reinterpret_cast<const uint4*>(&raw[i]);
+            if constexpr (ROWS == kRowsVec) {
+                uint4* dst = reinterpret_cast<uint4*>(smem + r * S::kPitch + cg * 16 * sizeof(T));
 #pragma unroll
-            for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) dst[j] = src[j];
+                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) dst[j] = reinterpret_cast<const uint4*>(&raw[i])[j];
+            }
             if (p.qr != nullptr) {
                 float amax = raw[i].amax();
                 if constexpr (FMT == kFp4Mx) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 const Fp4Scale g = fp4_scale<FMT>(amax, tn);
-                float v[16];
+                uint64_t v[8];
                 raw[i].values(v);
                 const uint2 codes = fp4_codes16<FMT>(v, g);
-                const int64_t c = c0 + cg * 16;
-                if (r < rows && c < p.k)
-                    *reinterpret_cast<uint2*>(p.qr + bz * p.sqrb + (row0 + r) * p.ldr + (c >> 1)) = codes;
+                if (r < rows && cg * 16 < cols)
+                    *reinterpret_cast<uint2*>(p.qr + bz * p.sqrb + (row0 + r) * p.ldr + ((c0 + cg * 16) >> 1)) = codes;
                 const int gi = FMT == kFp4Nv ? cg : cg >> 1;
-                const bool live = c0 + gi * fp4_group(FMT) < p.k && r < rows;
+                const bool live = gi * fp4_group(FMT) < cols && r < rows;
                 if (FMT == kFp4Nv || (cg & 1) == 0)
                     smem[S::kOffSfr + (gi >> 2) * kFp4SfBlock + (r & 31) * 16 + (r >> 5) * 4 + (gi & 3)] =
                         live ? static_cast<uint8_t>(g.byte) : 0;
@@ -226,52 +258,62 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
     {
         // columns: columns 2 cp and 2 cp + 1, rows 32 tq .. 32 tq + 32
         const int cp = tid & 63, tq = tid >> 6;
-        float v[2][32];
-        float am[2][2];
+        const uint8_t* src = smem + tq * 32 * S::kPitch + cp * 2 * sizeof(T);
+        float am[2][2];                          // column, half
+        uint32_t w[sizeof(T) == 2 ? 32 : 1];     // bf16: the pairs of both columns, kept
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+            for (int j = 0; j < 32; ++j) w[j] = *reinterpret_cast<const uint32_t*>(src + j * S::kPitch);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint8_t* src = smem + (tq * 32 + h * 16 + j) * S::kPitch + cp * 2 * sizeof(T);
-                if constexpr (sizeof(T) == 2) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(src);
-                    v[0][h * 16 + j] = __uint_as_float(w << 16);
-                    v[1][h * 16 + j] = __uint_as_float(w & 0xFFFF0000u);
-                } else {
-                    const float2 w = *reinterpret_cast<const float2*>(src);
-                    v[0][h * 16 + j] = w.x;
-                    v[1][h * 16 + j] = w.y;
-                }
+            for (int h = 0; h < 2; ++h) {
+                uint32_t m = bf16x2_maxabs_nan(w[16 * h], w[16 * h + 1]);
+#pragma unroll
+                for (int j = 2; j < 16; ++j) m = bf16x2_maxabs_nan(m, w[16 * h + j]);
+                am[0][h] = __uint_as_float((m << 16) & 0x7FFFFFFFu);
+                am[1][h] = __uint_as_float(m & 0x7FFF0000u);
             }
+        } else {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                float m = 0.0f;
+            for (int h = 0; h < 2; ++h) {
+                float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) m = max_nan(m, fabsf(v[s][h * 16 + j]));
-                am[s][h] = m;
+                for (int j = 0; j < 16; ++j) {
+                    const float2 e = *reinterpret_cast<const float2*>(src + (16 * h + j) * S::kPitch);
+                    m0 = max_nan(m0, fabsf(e.x));
+                    m1 = max_nan(m1, fabsf(e.y));
+                }
+                am[0][h] = m0;
+                am[1][h] = m1;
             }
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int col = 2 * cp + s;
             if constexpr (FMT == kFp4Mx) am[s][0] = am[s][1] = max_nan(am[s][0], am[s][1]);
-            uint32_t out[4];
+            uint2 out[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const Fp4Scale g = fp4_scale<FMT>(am[s][h], tn);
-                float y[16];
+                uint64_t y[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = v[s][h * 16 + j];
-                const uint2 codes = fp4_codes16<FMT>(y, g);
-                out[2 * h] = codes.x;
-                out[2 * h + 1] = codes.y;
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (sizeof(T) == 2) {
+                        const uint32_t a = w[16 * h + 2 * j], b = w[16 * h + 2 * j + 1];
+                        y[j] = s == 0 ? f32x2(__uint_as_float(a << 16), __uint_as_float(b << 16))
+                                      : f32x2(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u));
+                    } else {
+                        const uint8_t* e = src + (16 * h + 2 * j) * S::kPitch + 4 * s;
+                        y[j] = f32x2(*reinterpret_cast<const float*>(e), *reinterpret_cast<const float*>(e + S::kPitch));
+                    }
+                }
+                out[h] = fp4_codes16<FMT>(y, g);
                 const int gi = FMT == kFp4Nv ? tq * 2 + h : tq;
                 if (FMT == kFp4Nv || h == 0)
                     smem[S::kOffSfc + (gi >> 2) * kFp4SfBlock + (col & 31) * 16 + (col >> 5) * 4 + (gi & 3)] =
                         static_cast<uint8_t>(g.byte);
             }
             *reinterpret_cast<uint4*>(smem + S::kOffCol + col * S::kColPitch + tq * 16) =
-                make_uint4(out[0], out[1], out[2], out[3]);
+                make_uint4(out[0].x, out[0].y, out[1].x, out[1].y);
         }
     }
     __syncthreads();
@@ -279,86 +321,121 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int u = i * kThreads + tid, col = u >> 2, part = u & 3;
-        if (c0 + col < p.k)
+        if (col < cols)
             *reinterpret_cast<uint4*>(p.qc + bz * p.sqcb + (c0 + col) * p.ldc + (kcol >> 1) + part * 16) =
                 *reinterpret_cast<const uint4*>(smem + S::kOffCol + col * S::kColPitch + part * 16);
     }
     // scale blocks
     const int64_t kblocks_c = fp4_kblocks(p.offsets != nullptr ? p.kpad : p.m, FMT);
     if (tid < kWords * 32) {
-        const int w = tid >> 5, l = tid & 31;
-        const int64_t kb = kcol / (4 * fp4_group(FMT)) + w;
+        const int wd = tid >> 5, l = tid & 31;
+        const int64_t kb = kcol / (4 * fp4_group(FMT)) + wd;
         if (kb < kblocks_c)
             *reinterpret_cast<uint4*>(p.sfc + bz * p.sscb + (static_cast<int64_t>(blockIdx.x) * kblocks_c + kb) * kFp4SfBlock + l * 16) =
-                *reinterpret_cast<const uint4*>(smem + S::kOffSfc + w * kFp4SfBlock + l * 16);
+                *reinterpret_cast<const uint4*>(smem + S::kOffSfc + wd * kFp4SfBlock + l * 16);
     } else if (tid >= 128 && tid < 128 + kWords * 32 && p.qr != nullptr && sfblk >= 0 && sfblk < p.sfr_row_blocks) {
-        const int w = (tid - 128) >> 5, l = tid & 31;
-        const int64_t kb = c0 / (4 * fp4_group(FMT)) + w;
+        const int wd = (tid - 128) >> 5, l = tid & 31;
+        const int64_t kb = c0 / (4 * fp4_group(FMT)) + wd;
         if (kb < kblocks_r)
             *reinterpret_cast<uint4*>(p.sfr + bz * p.ssrb + (sfblk * kblocks_r + kb) * kFp4SfBlock + l * 16) =
-                *reinterpret_cast<const uint4*>(smem + S::kOffSfr + w * kFp4SfBlock + l * 16);
+                *reinterpret_cast<const uint4*>(smem + S::kOffSfr + wd * kFp4SfBlock + l * 16);
     }
 }
 
+// The two E2M1 codes of a byte as fp32.
+__device__ __forceinline__ uint64_t e2m1x2_f32x2(uint32_t byte) {
+    uint64_t d;
+    asm("{\n"
+        ".reg .b8 b, z1, z2, z3;\n"
+        ".reg .b32 h;\n"
+        ".reg .b16 l, u;\n"
+        ".reg .f32 fl, fu;\n"
+        "mov.b32 {b, z1, z2, z3}, %1;\n"
+        "cvt.rn.f16x2.e2m1x2 h, b;\n"
+        "mov.b32 {l, u}, h;\n"
+        "cvt.f32.f16 fl, l;\n"
+        "cvt.f32.f16 fu, u;\n"
+        "mov.b64 %0, {fl, fu};\n"
+        "}\n"
+        : "=l"(d)
+        : "r"(byte));
+    return d;
+}
+
 // Codes back to values: fl32(E2M1 * S), S the group's scale as the cast uses
-// it, rounded once more for a bf16 output. A lane has 16 columns.
-template <int FMT, bool OUT_BF16>
+// it, rounded once more for a bf16 output. A warp takes a row (those of a
+// block as in the cast), a lane 16 columns of each piece of 512. Rows of the
+// output that start anywhere are written one column per lane and store.
+template <int FMT, typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantArgs p) {
+    __shared__ __align__(16) T s_buf[VEC ? 1 : kThreads / 32 * 512];
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int lane = threadIdx.x & 31;
-    const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t kblocks = fp4_kblocks(p.k, FMT);
-    const int64_t pieces = (p.k + 511) / 512;
+    const int steps = (static_cast<int>((p.k + 511) / 512) + U - 1) / U;
     const float t = p.tscale != nullptr && FMT == kFp4Nv ? __ldg(p.tscale) : 1.0f;
-    constexpr int es = OUT_BF16 ? 2 : 4;
-    const bool vec = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && (p.ldo * es) % 16 == 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); i < p.m * pieces; i += nwarps) {
-        const int64_t row = i / pieces;
-        const int64_t c = (i % pieces) * 512 + lane * 16;
-        if (c >= p.k) continue;
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p.q + row * p.ldq + (c >> 1)));
-        const int64_t g = c / fp4_group(FMT);
-        const uint32_t b = __ldg(p.sf + ((row >> 7) * kblocks + (g >> 2)) * kFp4SfBlock + (row & 31) * 16 +
-                                 ((row >> 5) & 3) * 4 + (g & 3));
-        float s;
-        if constexpr (FMT == kFp4Nv) s = __fmul_rn(e4m3_value(b), t);
-        else s = b == 0xFFu ? __uint_as_float(0x7FC00000u) : (b == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23));
-        float v[16];
+    const unsigned i8 = (blockIdx.x & 15u) * 8 + warp;
+    const int64_t row = static_cast<int64_t>(blockIdx.x >> 4) * 128 + (i8 & 3) * 32 + (i8 >> 2);
+    if (row >= p.m) return;
+    const uint8_t* q = p.q + row * p.ldq;
+    const uint8_t* sf = p.sf + (row >> 7) * kblocks * kFp4SfBlock + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+    T* out = static_cast<T*>(p.out) + row * p.ldo;
+    for (int step = blockIdx.y; step < steps; step += gridDim.y) {
+        uint2 codes[U];
+        uint32_t b[U];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const uint32_t code = ((j < 8 ? w.x : w.y) >> (4 * (j & 7))) & 0xFu;
-            const uint32_t e = (code >> 1) & 3u, m = code & 1u;
-            // 0, 0.5, then (1 + m / 2) 2^(e - 1)
-            const float mag = e == 0 ? 0.5f * static_cast<float>(m) : __uint_as_float((e + 126u) << 23 | m << 22);
-            v[j] = __fmul_rn((code & 8u) ? -mag : mag, s);
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = static_cast<int64_t>(step * U + u) * 512 + lane * 16;
+            const int64_t g = c / fp4_group(FMT);
+            codes[u] = c < p.k ? __ldg(reinterpret_cast<const uint2*>(q + (c >> 1))) : make_uint2(0, 0);
+            b[u] = c < p.k ? __ldg(sf + (g >> 2) * kFp4SfBlock + (g & 3)) : 0u;
         }
-        if constexpr (OUT_BF16) {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + c;
-            uint32_t h[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                h[j] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            if (vec && c + 16 <= p.k) {
-                reinterpret_cast<uint4*>(o)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                reinterpret_cast<uint4*>(o)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = static_cast<int64_t>(step * U + u) * 512 + lane * 16;
+            float s;
+            if constexpr (FMT == kFp4Nv) s = __fmul_rn(e4m3_value(b[u]), t);
+            else s = b[u] == 0xFFu ? __uint_as_float(0x7FC00000u) : (b[u] == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(b[u] << 23));
+            const uint64_t ss = f32x2(s, s);
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f32x2_get(mul2(e2m1x2_f32x2((j < 4 ? codes[u].x : codes[u].y) >> (8 * (j & 3))), ss), v[2 * j], v[2 * j + 1]);
+            uint4 o[sizeof(T)];
+            if constexpr (sizeof(T) == 2) {
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    h[j] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+                o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                o[1] = make_uint4(h[4], h[5], h[6], h[7]);
             } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + j < p.k) o[j] = __float2bfloat16_rn(v[j]);
-            }
-        } else {
-            float* o = static_cast<float*>(p.out) + row * p.ldo + c;
-            if (vec && c + 16 <= p.k) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<float4*>(o)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            } else {
+                    o[j] = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                      __float_as_uint(v[4 * j + 3]));
+            }
+            if (VEC && c + 16 <= p.k) {
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) reinterpret_cast<uint4*>(out + c)[j] = o[j];
+            } else if (VEC) {
+                const T* e = reinterpret_cast<const T*>(o);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (c + j < p.k) o[j] = v[j];
+                    if (c + j < p.k) out[c + j] = e[j];
+            } else {
+                T* buf = s_buf + warp * 512;
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) reinterpret_cast<uint4*>(buf + lane * 16)[j] = o[j];
+                __syncwarp();
+                const int64_t c0 = c - lane * 16 + lane;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c0 + j * 32 < p.k) out[c0 + j * 32] = buf[j * 32 + lane];
             }
         }
     }
@@ -369,20 +446,36 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantA
 // leaves every s * t and every halfway case of x / (s * t) exact. Each block
 // makes the t of its own part and the largest, as bits, stays in a word that
 // starts at zero: the order of the atomics does not matter.
-template <typename T, bool VEC>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads) fp4_tscale_kernel(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
-                                                            uint32_t* tscale) {
+                                                              uint32_t* tscale) {
+    pdl_launch_dependents();
     pdl_wait_prior();
     float best = 0.0f;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t per_row = (k + 15) / 16;
-    for (int64_t i = first; i < m * per_row; i += stride) {
-        const int64_t row = i / per_row, c = (i - row * per_row) * 16;
-        Raw16<T> raw;
-        if (VEC && c + 16 <= k) raw.load(x + row * sxm + c);
-        else raw.load_some(x + row * sxm + c * sxk, sxk, static_cast<int>(k - c < 16 ? k - c : 16));
-        best = max_nan(best, raw.amax());
+    if constexpr (ROWS == kRowsVec) {
+        const int64_t per_row = (k + 15) / 16;
+        for (int64_t i = first; i < m * per_row; i += stride) {
+            const int64_t row = m == 1 ? 0 : i / per_row, c = (i - row * per_row) * 16;
+            Raw16<T> raw;
+            if (c + 16 <= k) raw.load(x + row * sxm + c);
+            else raw.load_some(x + row * sxm + c, 1, static_cast<int>(k - c));
+            best = max_nan(best, raw.amax());
+        }
+    } else {
+        // one element per lane and load, eight loads in flight
+        constexpr int kPiece = 8 * 32;
+        const int lane = threadIdx.x & 31;
+        const int64_t per_row = (k + kPiece - 1) / kPiece;
+        for (int64_t i = first >> 5; i < m * per_row; i += stride >> 5) {
+            const int64_t row = i / per_row, c0 = (i - row * per_row) * kPiece + lane;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = c0 + j * 32 < k ? static_cast<float>(x[row * sxm + (c0 + j * 32) * sxk]) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) best = max_nan(best, fabsf(v[j]));
+        }
     }
     uint32_t b = __reduce_max_sync(0xffffffffu, __float_as_uint(best) & 0x7FFFFFFFu);
     __shared__ uint32_t s[kThreads / 32];
@@ -417,28 +510,43 @@ bool vec_ok(const void* x, int64_t es, int64_t sxm, int64_t sxk, int64_t sxseg) 
     return (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && sxk == 1 && (sxm * es) % 16 == 0 && (sxseg * es) % 16 == 0;
 }
 
-template <typename T, int FMT, bool VEC>
+int rows_form(const void* x, int64_t es, int64_t sxm, int64_t sxk, int64_t sxseg) {
+    if (vec_ok(x, es, sxm, sxk, sxseg)) return kRowsVec;
+    return sxk == 1 ? kRowsContiguous : kRowsStrided;
+}
+
+// Blocks along the columns: all steps in one when the rows fill the SMs (eight
+// blocks of 256 threads each), as many as there are steps when they do not.
+unsigned column_blocks(int64_t rows, int64_t steps, int num_sms) {
+    const int64_t sets = (rows + 7) / 8;
+    int64_t y = (static_cast<int64_t>(num_sms) * 8 + sets - 1) / sets;
+    if (y > steps) y = steps;
+    return static_cast<unsigned>(y < 1 ? 1 : y);
+}
+
+template <typename T, int FMT, int ROWS>
 cudaError_t cast_u(const Fp4CastArgs& a, cudaStream_t st, int num_sms) {
     const int64_t pieces = (a.k + 511) / 512;
-    const int64_t seg_blocks = (a.seg_rows + 127) / 128;
-    const int64_t rows = a.offsets != nullptr ? a.m : (a.m / a.seg_rows) * seg_blocks * 128;
-    const bool two = a.m * pieces > static_cast<int64_t>(num_sms) * 64;
-    const int64_t tasks = rows * (two ? (pieces + 1) / 2 : pieces);
-    int64_t grid = (tasks + 7) / 8;
-    if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
-    return two ? launch(fp4_cast_kernel<T, FMT, VEC, 2>, dim3(static_cast<unsigned>(grid)), 0, st, a)
-               : launch(fp4_cast_kernel<T, FMT, VEC, 1>, dim3(static_cast<unsigned>(grid)), 0, st, a);
+    const int64_t sets = a.offsets != nullptr ? (a.m + 7) / 8 : (a.m / a.seg_rows) * ((a.seg_rows + 127) / 128) * 16;
+    const unsigned x = static_cast<unsigned>(sets);
+    // two pieces at a time once there is work for several rounds of blocks
+    if (ROWS != kRowsContiguous && a.m * pieces > static_cast<int64_t>(num_sms) * 64)
+        return launch(fp4_cast_kernel<T, FMT, ROWS, 2>, dim3(x, column_blocks(a.m, (pieces + 1) / 2, num_sms)), 0, st, a);
+    return launch(fp4_cast_kernel<T, FMT, ROWS, 1>, dim3(x, column_blocks(a.m, pieces, num_sms)), 0, st, a);
 }
 
 template <typename T, int FMT>
 cudaError_t cast_v(const Fp4CastArgs& a, cudaStream_t st, int num_sms) {
-    return vec_ok(a.x, sizeof(T), a.sxm, a.sxk, a.sxseg) ? cast_u<T, FMT, true>(a, st, num_sms)
-                                                         : cast_u<T, FMT, false>(a, st, num_sms);
+    switch (rows_form(a.x, sizeof(T), a.sxm, a.sxk, a.sxseg)) {
+        case kRowsVec: return cast_u<T, FMT, kRowsVec>(a, st, num_sms);
+        case kRowsContiguous: return cast_u<T, FMT, kRowsContiguous>(a, st, num_sms);
+        default: return cast_u<T, FMT, kRowsStrided>(a, st, num_sms);
+    }
 }
 
-template <typename T, int FMT, bool VEC>
+template <typename T, int FMT, int ROWS>
 cudaError_t dual_v(const Fp4DualArgs& a, cudaStream_t st, dim3 grid) {
-    auto kern = fp4_dual_kernel<T, FMT, VEC>;
+    auto kern = fp4_dual_kernel<T, FMT, ROWS>;
     constexpr int bytes = DualSmem<T>::kBytes;
     if (bytes > 48 * 1024)
         if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), bytes); e != cudaSuccess) return e;
@@ -447,8 +555,34 @@ cudaError_t dual_v(const Fp4DualArgs& a, cudaStream_t st, dim3 grid) {
 
 template <typename T, int FMT>
 cudaError_t dual_t(const Fp4DualArgs& a, cudaStream_t st, dim3 grid) {
-    return vec_ok(a.x, sizeof(T), a.sxm, 1, a.sxb) ? dual_v<T, FMT, true>(a, st, grid)
-                                                   : dual_v<T, FMT, false>(a, st, grid);
+    return vec_ok(a.x, sizeof(T), a.sxm, 1, a.sxb) ? dual_v<T, FMT, kRowsVec>(a, st, grid)
+                                                   : dual_v<T, FMT, kRowsContiguous>(a, st, grid);
+}
+
+template <int FMT, typename T>
+cudaError_t dequant_t(const Fp4DequantArgs& a, cudaStream_t st, int num_sms) {
+    const int64_t pieces = (a.k + 511) / 512;
+    const unsigned x = static_cast<unsigned>((a.m + 127) / 128 * 16);
+    if (!vec_ok(a.out, sizeof(T), a.ldo, 1, 0))
+        return launch(fp4_dequant_kernel<FMT, T, false, 1>, dim3(x, column_blocks(a.m, pieces, num_sms)), 0, st, a);
+    if (a.m * pieces > static_cast<int64_t>(num_sms) * 64)
+        return launch(fp4_dequant_kernel<FMT, T, true, 2>, dim3(x, column_blocks(a.m, (pieces + 1) / 2, num_sms)), 0, st, a);
+    return launch(fp4_dequant_kernel<FMT, T, true, 1>, dim3(x, column_blocks(a.m, pieces, num_sms)), 0, st, a);
+}
+
+template <typename T>
+cudaError_t tscale_t(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk, uint32_t* out, cudaStream_t st, int num_sms) {
+    if (sxk == 1 && sxm == k) {        // one long row: only its end is ragged
+        k *= m;
+        m = 1;
+        sxm = k;
+    }
+    const bool vec = vec_ok(x, sizeof(T), m > 1 ? sxm : 0, sxk, 0);
+    int64_t grid = vec ? (m * ((k + 15) / 16) + kThreads - 1) / kThreads : (m * ((k + 255) / 256) + 7) / 8;
+    if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
+    const dim3 g(static_cast<unsigned>(grid < 1 ? 1 : grid));
+    return vec ? launch(fp4_tscale_kernel<T, kRowsVec>, g, 0, st, x, m, k, sxm, sxk, out)
+               : launch(fp4_tscale_kernel<T, kRowsStrided>, g, 0, st, x, m, k, sxm, sxk, out);
 }
 
 }  // namespace
@@ -469,32 +603,17 @@ cudaError_t launch_fp4_cast_dual(const Fp4DualArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_fp4_dequant(const Fp4DequantArgs& a, cudaStream_t st, int num_sms) {
-    int64_t grid = (a.m * ((a.k + 511) / 512) + 7) / 8;
-    if (grid > static_cast<int64_t>(num_sms) * 16) grid = static_cast<int64_t>(num_sms) * 16;
-    const dim3 g(static_cast<unsigned>(grid));
     if (a.fmt == kFp4Nv)
-        return a.out_bf16 ? launch(fp4_dequant_kernel<kFp4Nv, true>, g, 0, st, a)
-                          : launch(fp4_dequant_kernel<kFp4Nv, false>, g, 0, st, a);
-    return a.out_bf16 ? launch(fp4_dequant_kernel<kFp4Mx, true>, g, 0, st, a)
-                      : launch(fp4_dequant_kernel<kFp4Mx, false>, g, 0, st, a);
+        return a.out_bf16 ? dequant_t<kFp4Nv, __nv_bfloat16>(a, st, num_sms) : dequant_t<kFp4Nv, float>(a, st, num_sms);
+    return a.out_bf16 ? dequant_t<kFp4Mx, __nv_bfloat16>(a, st, num_sms) : dequant_t<kFp4Mx, float>(a, st, num_sms);
 }
 
 cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int64_t k, int64_t sxm, int64_t sxk, float* t,
-                            cudaStream_t st, int num_sms) {
+                                    cudaStream_t st, int num_sms) {
     if (cudaError_t e = cudaMemsetAsync(t, 0, 4, st); e != cudaSuccess) return e;
-    int64_t grid = (m * ((k + 15) / 16) + kThreads - 1) / kThreads;
-    if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
-    if (grid < 1) grid = 1;
-    const dim3 g(static_cast<unsigned>(grid));
     uint32_t* out = reinterpret_cast<uint32_t*>(t);
-    if (is_bf16) {
-        const auto* p = static_cast<const __nv_bfloat16*>(x);
-        return vec_ok(x, 2, sxm, sxk, 0) ? launch(fp4_tscale_kernel<__nv_bfloat16, true>, g, 0, st, p, m, k, sxm, sxk, out)
-                                         : launch(fp4_tscale_kernel<__nv_bfloat16, false>, g, 0, st, p, m, k, sxm, sxk, out);
-    }
-    const auto* p = static_cast<const float*>(x);
-    return vec_ok(x, 4, sxm, sxk, 0) ? launch(fp4_tscale_kernel<float, true>, g, 0, st, p, m, k, sxm, sxk, out)
-                                     : launch(fp4_tscale_kernel<float, false>, g, 0, st, p, m, k, sxm, sxk, out);
+    if (is_bf16) return tscale_t(static_cast<const __nv_bfloat16*>(x), m, k, sxm, sxk, out, st, num_sms);
+    return tscale_t(static_cast<const float*>(x), m, k, sxm, sxk, out, st, num_sms);
 }
 
 }  // namespace ql

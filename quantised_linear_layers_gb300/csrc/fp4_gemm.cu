@@ -196,7 +196,7 @@ __device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, in
             float amax = raw[i].amax();
             if constexpr (FMT == kFp4Mx) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             const Fp4Scale g = fp4_scale<FMT>(amax, tn);
-            float v[16];
+            uint64_t v[8];
             raw[i].values(v);
             *reinterpret_cast<uint2*>(codes + r * 128 + (((cg >> 1) ^ (r & 7)) << 4) + (cg & 1) * 8) = fp4_codes16<FMT>(v, g);
             const int gi = FMT == kFp4Nv ? cg : cg >> 1;

@@ -563,6 +563,9 @@ def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | No
     4 bits. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and
     the cast is the operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
     code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
+    if offsets is None and x.stride(-1) != 1 and x.stride(-2) == 1 and k > 1:
+        # a transposed view: the column-wise cast of the matrix it views
+        return fp4_cast_dual(x.transpose(-1, -2), fmt, tensor_scale, rows=False)[1]
     ld = -(-k // 32) * 16 or 16
     dev = x.device
     a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld, tensor_scale, fmt, batch, m, k, offsets)
