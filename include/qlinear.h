@@ -508,6 +508,9 @@ int64_t fp4_scale_bytes(int64_t rows, int64_t k, int fmt, int experts);
  * all of them). */
 int64_t fp4_column_extent(int64_t m, int experts);
 
+/* Where a call below takes own_scale != 0 (QL_FP4_NV only), it first writes
+ * fp4_tensor_scale(x) to *scale (x_scale), which must then not be NULL. */
+
 /* *scale = the least power of two t with max|x| <= 2688 t (2688 = 6 * 448), at
  * least 2^-80; NaN if x holds an infinity or a NaN. x [m, k], any strides. */
 ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k, int64_t x_stride_m,
@@ -517,15 +520,15 @@ ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k
  * set of scale blocks per batch entry. With offsets (batch must be 1) the scale
  * blocks are by expert; rows of no expert get neither codes nor scales. */
 ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
-                   int64_t x_stride_m, int64_t x_stride_k, int fmt, const float* scale, uint8_t* q, int64_t ldq,
-                   uint8_t* sf, const int32_t* offsets, int experts, ql_stream_t stream);
+                   int64_t x_stride_m, int64_t x_stride_k, int fmt, float* scale, int own_scale, uint8_t* q,
+                   int64_t ldq, uint8_t* sf, const int32_t* offsets, int experts, ql_stream_t stream);
 
 /* Casts x [batch, m, k] (contiguous rows) along its rows and along its columns
  * from one read: (q_rows, sf_rows) as fp4_cast, and (q_cols, sf_cols) the cast
  * of x^T: codes [batch * k][ldc], ldc >= fp4_column_extent(m, experts) / 2.
  * q_rows and sf_rows may both be NULL. */
 ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
-                        int64_t x_stride_m, int fmt, const float* scale, uint8_t* q_rows, int64_t ldr,
+                        int64_t x_stride_m, int fmt, float* scale, int own_scale, uint8_t* q_rows, int64_t ldr,
                         uint8_t* sf_rows, uint8_t* q_cols, int64_t ldc, uint8_t* sf_cols, const int32_t* offsets,
                         int experts, ql_stream_t stream);
 
@@ -552,13 +555,13 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
 /* The forward call: casts X [m, k] (bf16 or fp32, contiguous rows, row stride
  * x_stride_m) and multiplies, D [m, n] bf16 = X W^T, or by expert with offsets
  * (W [experts, n, k]). Equal to fp4_cast and gemm_fp4_nt / gemm_fp4_nt_ragged;
- * up to 16 rows are cast inside the product, in one launch and without a
+ * up to 64 rows are cast inside the product, in one launch and without a
  * workspace. fp4_linear_workspace_size bytes of device memory, 16-byte aligned,
  * are needed otherwise (0: none); they may be reused once the stream is past
  * the call. */
 size_t fp4_linear_workspace_size(int64_t m, int64_t k, int fmt, int experts);
-ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, const float* x_scale, const uint8_t* w,
-                     int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
+ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float* x_scale, int own_scale,
+                     const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
                      const int32_t* offsets, int experts, int64_t m, int64_t n, int64_t k, void* workspace,
                      size_t workspace_bytes, ql_stream_t stream);
 

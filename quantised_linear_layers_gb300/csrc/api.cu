@@ -612,9 +612,17 @@ ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k
                                                  reinterpret_cast<cudaStream_t>(stream), di.num_sms));
 }
 
+// The scale of x [batch, m, k], whose entries must follow one another as rows do.
+static ql_status fp4_own_scale(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
+                               int64_t x_stride_m, int64_t x_stride_k, float* scale, ql_stream_t stream) {
+    if (batch > 1 && x_stride_b != m * x_stride_m) return QL_ERR_UNSUPPORTED;
+    return fp4_tensor_scale(x, x_dtype, batch * m, k, x_stride_m, x_stride_k, scale, stream);
+}
+
 ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
-                   int64_t x_stride_m, int64_t x_stride_k, int fmt, const float* scale, uint8_t* q, int64_t ldq,
-                   uint8_t* sf, const int32_t* offsets, int experts, ql_stream_t stream) {
+                   int64_t x_stride_m, int64_t x_stride_k, int fmt, float* scale, int own_scale, uint8_t* q,
+                   int64_t ldq, uint8_t* sf, const int32_t* offsets, int experts, ql_stream_t stream) {
+    if (own_scale && (scale == nullptr || fmt != QL_FP4_NV)) return QL_ERR_INVALID_ARG;
     if (batch < 0 || m < 0 || k < 0 || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
     if (offsets != nullptr && (batch != 1 || experts < 1)) return QL_ERR_INVALID_ARG;
@@ -644,13 +652,18 @@ ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, in
     a.num_experts = experts;
     a.sf_row_blocks = offsets != nullptr ? fp4_row_blocks(m, experts) : batch * ((m + 127) / 128);
     a.dev_status = di.status;
+    if (own_scale)
+        if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, x_stride_k, scale, stream);
+            s != QL_OK)
+            return s;
     return from_cuda(ql::launch_fp4_cast(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
 }
 
 ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
-                        int64_t x_stride_m, int fmt, const float* scale, uint8_t* q_rows, int64_t ldr,
+                        int64_t x_stride_m, int fmt, float* scale, int own_scale, uint8_t* q_rows, int64_t ldr,
                         uint8_t* sf_rows, uint8_t* q_cols, int64_t ldc, uint8_t* sf_cols, const int32_t* offsets,
                         int experts, ql_stream_t stream) {
+    if (own_scale && (scale == nullptr || fmt != QL_FP4_NV)) return QL_ERR_INVALID_ARG;
     if (batch < 0 || m < 0 || k < 0 || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
     if (offsets != nullptr && (batch != 1 || experts < 1)) return QL_ERR_INVALID_ARG;
@@ -690,6 +703,9 @@ ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t 
     a.num_experts = experts;
     a.kpad = kpad;
     a.dev_status = di.status;
+    if (own_scale)
+        if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, 1, scale, stream); s != QL_OK)
+            return s;
     return from_cuda(ql::launch_fp4_cast_dual(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -804,8 +820,8 @@ size_t fp4_linear_workspace_size(int64_t m, int64_t k, int fmt, int experts) {
     return static_cast<size_t>(m) * ((k + 31) / 32 * 16) + static_cast<size_t>(fp4_scale_bytes(m, k, fmt, experts));
 }
 
-ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, const float* x_scale, const uint8_t* w,
-                     int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
+ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float* x_scale, int own_scale,
+                     const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
                      const int32_t* offsets, int experts, int64_t m, int64_t n, int64_t k, void* workspace,
                      size_t workspace_bytes, ql_stream_t stream) {
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
@@ -817,8 +833,8 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, const 
                                         workspace_bytes < fp4_linear_workspace_size(m, k, fmt, offsets ? experts : 0)))
             return QL_ERR_INVALID_ARG;
         uint8_t* sf = q == nullptr ? nullptr : q + m * ldq;
-        if (ql_status s = fp4_cast(x, x_dtype, 1, m, k, 0, x_stride_m, 1, fmt, x_scale, q, ldq, sf, offsets, experts,
-                                   stream);
+        if (ql_status s = fp4_cast(x, x_dtype, 1, m, k, 0, x_stride_m, 1, fmt, x_scale, own_scale, q, ldq, sf, offsets,
+                                   experts, stream);
             s != QL_OK)
             return s;
         return offsets == nullptr
@@ -830,7 +846,10 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, const 
     if (offsets != nullptr && experts < 1) return QL_ERR_INVALID_ARG;
     if (offsets != nullptr && (experts > ql::kFp4MaxExperts || experts * n >= kInt31)) return QL_ERR_UNSUPPORTED;
     if (x == nullptr || d == nullptr || ldd < n) return QL_ERR_INVALID_ARG;
+    if (own_scale && (x_scale == nullptr || fmt != QL_FP4_NV)) return QL_ERR_INVALID_ARG;
     if (ql_status s = fp4_operand(w, ldw, sfw, k); s != QL_OK) return s;
+    if (own_scale)
+        if (ql_status s = fp4_tensor_scale(x, x_dtype, m, k, x_stride_m, 1, x_scale, stream); s != QL_OK) return s;
     ql::Fp4GemmArgs a{};
     a.xr = x;
     a.xr_bf16 = x_dtype == QL_BF16;

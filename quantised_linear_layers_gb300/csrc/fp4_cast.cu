@@ -445,17 +445,23 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantA
 // 2^11), at least 2^-80; NaN if x has an infinity or a NaN. A power of two
 // leaves every s * t and every halfway case of x / (s * t) exact. Each block
 // makes the t of its own part and the largest, as bits, stays in a word that
-// starts at zero: the order of the atomics does not matter.
-template <typename T, int ROWS>
-__global__ void __launch_bounds__(kThreads) fp4_tscale_kernel(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
+// starts at zero: the order of the atomics does not matter. Up to 2 MB one
+// cluster of eight blocks does it all (CLUSTER): its blocks' maxima meet in shared
+// memory, and no word has to be set to zero by a launch of its own.
+constexpr int kClusterThreads = 1024;
+
+template <typename T, int ROWS, bool CLUSTER>
+__global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kThreads) fp4_tscale_kernel(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
                                                               uint32_t* tscale) {
     pdl_launch_dependents();
     pdl_wait_prior();
+    constexpr int kBlock = CLUSTER ? kClusterThreads : kThreads;
     float best = 0.0f;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlock;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
     if constexpr (ROWS == kRowsVec) {
         const int64_t per_row = (k + 15) / 16;
+#pragma unroll 2
         for (int64_t i = first; i < m * per_row; i += stride) {
             const int64_t row = m == 1 ? 0 : i / per_row, c = (i - row * per_row) * 16;
             Raw16<T> raw;
@@ -478,32 +484,60 @@ __global__ void __launch_bounds__(kThreads) fp4_tscale_kernel(const T* x, int64_
         }
     }
     uint32_t b = __reduce_max_sync(0xffffffffu, __float_as_uint(best) & 0x7FFFFFFFu);
-    __shared__ uint32_t s[kThreads / 32];
+    __shared__ uint32_t s[kBlock / 32], all;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = b;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) b = max(b, s[i]);
+        for (int i = 1; i < kBlock / 32; ++i) b = max(b, s[i]);
+        all = b;
+    }
+    if constexpr (CLUSTER) {
+        __syncwarp();
+        cluster_sync_all();
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            for (unsigned r = 1; r < gridDim.x; ++r) {
+                uint32_t v;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(&all, r)) : "memory");
+                b = max(b, v);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();
+        if (blockIdx.x != 0) return;
+    }
+    if (threadIdx.x == 0) {
         const int e = static_cast<int>(b >> 23) - 11 + ((b & 0x7FFFFFu) > 0x280000u ? 1 : 0);
-        const uint32_t least = 127 - 80;
-        const uint32_t field = e < static_cast<int>(least) ? least : static_cast<uint32_t>(e);
-        atomicMax(tscale, (b >> 23) == 255u ? 0x7FC00000u : field << 23);
+        const int least = 127 - 80;
+        const uint32_t t = (b >> 23) == 255u ? 0x7FC00000u : static_cast<uint32_t>(e < least ? least : e) << 23;
+        if constexpr (CLUSTER) *tscale = t;
+        else atomicMax(tscale, t);
     }
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, size_t smem, cudaStream_t st, const Args&... args) {
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int threads, unsigned cluster, size_t smem, cudaStream_t st,
+                           const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, size_t smem, cudaStream_t st, const Args&... args) {
+    return launch_cluster(kern, grid, kThreads, 1, smem, st, args...);
 }
 
 bool vec_ok(const void* x, int64_t es, int64_t sxm, int64_t sxk, int64_t sxseg) {
@@ -578,11 +612,17 @@ cudaError_t tscale_t(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
         sxm = k;
     }
     const bool vec = vec_ok(x, sizeof(T), m > 1 ? sxm : 0, sxk, 0);
+    // 2 MB, measured: one cluster 3.4 us and 3.1 us less host time than the zeroing and the atomics
+    if (m * k * static_cast<int64_t>(sizeof(T)) <= (2 << 20)) {
+        return vec ? launch_cluster(fp4_tscale_kernel<T, kRowsVec, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out)
+                   : launch_cluster(fp4_tscale_kernel<T, kRowsStrided, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out);
+    }
+    if (cudaError_t e = cudaMemsetAsync(out, 0, 4, st); e != cudaSuccess) return e;
     int64_t grid = vec ? (m * ((k + 15) / 16) + kThreads - 1) / kThreads : (m * ((k + 255) / 256) + 7) / 8;
     if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
     const dim3 g(static_cast<unsigned>(grid < 1 ? 1 : grid));
-    return vec ? launch(fp4_tscale_kernel<T, kRowsVec>, g, 0, st, x, m, k, sxm, sxk, out)
-               : launch(fp4_tscale_kernel<T, kRowsStrided>, g, 0, st, x, m, k, sxm, sxk, out);
+    return vec ? launch(fp4_tscale_kernel<T, kRowsVec, false>, g, 0, st, x, m, k, sxm, sxk, out)
+               : launch(fp4_tscale_kernel<T, kRowsStrided, false>, g, 0, st, x, m, k, sxm, sxk, out);
 }
 
 }  // namespace
@@ -610,7 +650,6 @@ cudaError_t launch_fp4_dequant(const Fp4DequantArgs& a, cudaStream_t st, int num
 
 cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int64_t k, int64_t sxm, int64_t sxk, float* t,
                                     cudaStream_t st, int num_sms) {
-    if (cudaError_t e = cudaMemsetAsync(t, 0, 4, st); e != cudaSuccess) return e;
     uint32_t* out = reinterpret_cast<uint32_t*>(t);
     if (is_bf16) return tscale_t(static_cast<const __nv_bfloat16*>(x), m, k, sxm, sxk, out, st, num_sms);
     return tscale_t(static_cast<const float*>(x), m, k, sxm, sxk, out, st, num_sms);

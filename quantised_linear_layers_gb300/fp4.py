@@ -28,8 +28,9 @@ import torch
 from . import ops
 
 
-def _scale(x: torch.Tensor, fmt: int):
-    return ops.fp4_tensor_scale(x) if fmt == ops.FP4_NV else None
+def _own(fmt: int):
+    """The scale of a training step's casts."""
+    return ops.FP4_OWN_SCALE if fmt == ops.FP4_NV else None
 
 
 def _contiguous_rows(x: torch.Tensor) -> torch.Tensor:
@@ -53,7 +54,9 @@ class FP4Weight:
                              "weight must be 3-D [experts, out_features, in_features]")
         w = _contiguous_rows(w)
         self.shape = tuple(w.shape)
-        scale = _scale(w, self.fmt)
+        scale = _own(self.fmt)
+        if self._dims == 3 and w.stride(0) != w.shape[1] * w.stride(1):
+            w = w.contiguous()
         if self.dgrad:
             self.w, self.wt = ops.fp4_cast_dual(w, self.fmt, scale)
         else:
@@ -72,6 +75,23 @@ def _need_wt(w: FP4Weight) -> ops.FP4Tensor:
     return w.wt
 
 
+# Results are allocated before the first launch of a step: on Grace an
+# allocation right after a launch waits about 3 us for the launch to leave the
+# CPU.
+def _empty(x: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
+    return torch.empty((x.shape[0], cols), dtype=dtype, device=x.device)
+
+
+def _grads(dy: torch.Tensor, w: FP4Weight, need_dx: bool, dw_out: torch.Tensor | None, accumulate: bool):
+    if dw_out is None:
+        if accumulate:
+            raise ValueError("accumulate needs an existing dw_out")
+        dw_out = torch.empty(w.shape, dtype=torch.float32, device=dy.device)
+    elif dw_out.dtype != torch.float32:
+        raise ValueError("dw_out must be fp32")
+    return _empty(dy, w.shape[-1], torch.bfloat16) if need_dx else None, dw_out
+
+
 def forward(x: torch.Tensor, w: FP4Weight, x_scale: torch.Tensor | None = None,
             out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [T, out] = X [T, in] W^T (bf16)."""
@@ -81,8 +101,9 @@ def forward(x: torch.Tensor, w: FP4Weight, x_scale: torch.Tensor | None = None,
 def forward_saving(x: torch.Tensor, w: FP4Weight):
     """Y = X W^T plus X's cast along the tokens for the weight gradient: (Y, cast)."""
     x = _contiguous_rows(x)
-    rows, cols = ops.fp4_cast_dual(x, w.fmt, _scale(x, w.fmt))
-    return ops.gemm_fp4_nt(rows, w.w), cols
+    y = _empty(x, w.shape[-2], torch.bfloat16)
+    rows, cols = ops.fp4_cast_dual(x, w.fmt, _own(w.fmt))
+    return ops.gemm_fp4_nt(rows, w.w, out=y), cols
 
 
 def backward(dy: torch.Tensor, w: FP4Weight, x_cols: ops.FP4Tensor, need_dx: bool = True,
@@ -90,14 +111,16 @@ def backward(dy: torch.Tensor, w: FP4Weight, x_cols: ops.FP4Tensor, need_dx: boo
     """dX = dY W (bf16, or None) and dW (+)= dY^T X (fp32) with dY cast both ways
     from one read and x_cols from ``forward_saving``."""
     dy = _contiguous_rows(dy)
-    rows, cols = ops.fp4_cast_dual(dy, w.fmt, _scale(dy, w.fmt), rows=need_dx)
-    dx = ops.gemm_fp4_nt(rows, _need_wt(w)) if need_dx else None
-    return dx, ops.gemm_fp4_nt(cols, x_cols, out=dw_out, dtype=torch.float32, accumulate=accumulate)
+    dx, dw = _grads(dy, w, need_dx, dw_out, accumulate)
+    rows, cols = ops.fp4_cast_dual(dy, w.fmt, _own(w.fmt), rows=need_dx)
+    if need_dx:
+        ops.gemm_fp4_nt(rows, _need_wt(w), out=dx)
+    return dx, ops.gemm_fp4_nt(cols, x_cols, out=dw, accumulate=accumulate)
 
 
 def dgrad(dy: torch.Tensor, w: FP4Weight, out: torch.Tensor | None = None) -> torch.Tensor:
     """dX [T, in] = dY [T, out] W (bf16)."""
-    return ops.fp4_linear(dy, _need_wt(w), _scale(dy, w.fmt), out=out)
+    return ops.fp4_linear(dy, _need_wt(w), _own(w.fmt), out=out)
 
 
 def experts_forward(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight, x_scale: torch.Tensor | None = None,
@@ -109,22 +132,25 @@ def experts_forward(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight, 
 def experts_forward_saving(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight):
     """experts_forward plus X's cast along each expert's tokens: (Y, cast)."""
     x = _contiguous_rows(x)
-    rows, cols = ops.fp4_cast_dual(x, w.fmt, _scale(x, w.fmt), offsets)
-    return ops.gemm_fp4_nt_ragged(rows, w.w), cols
+    y = _empty(x, w.shape[-2], torch.bfloat16)
+    rows, cols = ops.fp4_cast_dual(x, w.fmt, _own(w.fmt), offsets)
+    return ops.gemm_fp4_nt_ragged(rows, w.w, out=y), cols
 
 
 def experts_backward(dy: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight, x_cols: ops.FP4Tensor,
                      need_dx: bool = True, dw_out: torch.Tensor | None = None, accumulate: bool = False):
     """dX [T, in] (bf16, or None) and dW [experts, out, in] (+)= dY_e^T X_e (fp32)."""
     dy = _contiguous_rows(dy)
-    rows, cols = ops.fp4_cast_dual(dy, w.fmt, _scale(dy, w.fmt), offsets, rows=need_dx)
-    dx = ops.gemm_fp4_nt_ragged(rows, _need_wt(w)) if need_dx else None
-    return dx, ops.gemm_fp4_wgrad_ragged(cols, x_cols, out=dw_out, accumulate=accumulate)
+    dx, dw = _grads(dy, w, need_dx, dw_out, accumulate)
+    rows, cols = ops.fp4_cast_dual(dy, w.fmt, _own(w.fmt), offsets, rows=need_dx)
+    if need_dx:
+        ops.gemm_fp4_nt_ragged(rows, _need_wt(w), out=dx)
+    return dx, ops.gemm_fp4_wgrad_ragged(cols, x_cols, out=dw, accumulate=accumulate)
 
 
 def _forward(x, offsets, w4):
     """A module's forward without a backward: X under its own scale, as in training."""
-    scale = _scale(x, w4.fmt)
+    scale = _own(w4.fmt)
     return forward(x, w4, scale) if offsets is None else experts_forward(x, offsets, w4, scale)
 
 
@@ -139,8 +165,8 @@ class _FP4Fn(torch.autograd.Function):
             ctx.x_cols = None
             return _forward(x, offsets, w4)
         y, cols = forward_saving(x, w4) if offsets is None else experts_forward_saving(x, offsets, w4)
-        ctx.save_for_backward(offsets, cols.buf, cols.scale)
-        ctx.x_cols = cols.set_tensors(None, None, None)
+        ctx.save_for_backward(offsets, cols.buf)
+        ctx.x_cols = (cols.ld, cols._scale, cols.fmt, cols.batch, cols.rows, cols.cols)
         return y
 
     @staticmethod
@@ -154,11 +180,9 @@ class _FP4Fn(torch.autograd.Function):
             if offsets is None:
                 dx = dgrad(dy, w4)
             else:
-                dx = ops.fp4_linear(dy, _need_wt(w4), _scale(dy, w4.fmt), offsets)
+                dx = ops.fp4_linear(dy, _need_wt(w4), _own(w4.fmt), offsets)
             return dx.to(ctx.x_dtype), None, None, None, None
-        _, buf, scale = ctx.saved_tensors
-        cols = ctx.x_cols
-        x_cols = ops.FP4Tensor(buf, cols.ld, scale, cols.fmt, cols.batch, cols.rows, cols.cols, offsets, cols.by_cols)
+        x_cols = ops.FP4Tensor(ctx.saved_tensors[1], *ctx.x_cols, offsets, offsets is not None)
         main = module.main_grad
         kw = dict(need_dx=ctx.needs_input_grad[0], dw_out=main, accumulate=main is not None)
         dx, dw = backward(dy, w4, x_cols, **kw) if offsets is None else experts_backward(dy, offsets, w4, x_cols, **kw)

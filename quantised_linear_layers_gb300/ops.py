@@ -22,6 +22,7 @@ QL_BF16, QL_F32 = 0, 1
 SF_FP32, SF_UE8M0, SF_PACKED_UE8M0 = 0, 1, 2
 CAST_RECIP_OF_SCALE = 0x100
 FP4_NV, FP4_MX = 0, 1
+FP4_OWN_SCALE = "own"       # as a tensor scale: fp4_tensor_scale of the tensor itself
 
 _lock = threading.Lock()
 _lib = None
@@ -51,15 +52,15 @@ _SIGS = {
     "fp4_scale_bytes": [_i64, _i64, _int, _int],
     "fp4_column_extent": [_i64, _int],
     "fp4_tensor_scale": [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp],
-    "fp4_cast": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _vp, _int, _vp],
-    "fp4_cast_dual": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _int,
-                      _vp],
+    "fp4_cast": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _int, _vp, _i64, _vp, _vp, _int, _vp],
+    "fp4_cast_dual": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _int, _vp, _int, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                      _int, _vp],
     "fp4_dequant": [_vp, _i64, _vp, _int, _vp, _i64, _i64, _vp, _int, _i64, _vp],
     "gemm_fp4_nt": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64, _i64, _int, _vp],
     "gemm_fp4_nt_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _int, _i64, _vp, _int, _i64, _i64,
                            _i64, _vp],
     "fp4_linear_workspace_size": [_i64, _i64, _int, _int],
-    "fp4_linear": [_vp, _int, _i64, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp],
+    "fp4_linear": [_vp, _int, _i64, _vp, _int, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp],
     "gemm_fp4_wgrad_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64,
                               _int, _vp],
     "ql_cast_gemm_host_workspace_size": [_i64, _i64, _i64, _int],
@@ -462,22 +463,29 @@ class FP4Tensor:
     it was cast by (``by_cols``: its columns are the experts' rows, each from a
     multiple of 256 on). The layouts are in include/qlinear.h."""
 
-    __slots__ = ("buf", "ld", "scale", "fmt", "batch", "rows", "cols", "offsets", "by_cols", "device", "q_ptr", "sf_ptr",
-                 "scale_ptr")
+    __slots__ = ("buf", "ld", "fmt", "batch", "rows", "cols", "offsets", "by_cols", "device", "q_ptr", "sf_ptr",
+                 "scale_ptr", "_scale")
 
     def __init__(self, buf, ld, scale, fmt, batch, rows, cols, offsets=None, by_cols=False):
+        # scale: a tensor, None, FP4_OWN_SCALE (the last 16 bytes of buf) or the FP4Tensor that has it
         self.ld, self.fmt, self.batch, self.rows, self.cols, self.by_cols = ld, fmt, batch, rows, cols, by_cols
-        self.set_tensors(buf, scale, offsets)
+        self.buf, self.offsets, self.device = buf, offsets, buf.device
+        self.q_ptr = q = buf.data_ptr()
+        self.sf_ptr = q + batch * rows * ld
+        self._scale = scale
+        if scale is None:
+            self.scale_ptr = None
+        elif scale is FP4_OWN_SCALE:
+            self.scale_ptr = q + buf.numel() - 16
+        else:
+            self.scale_ptr = scale.scale_ptr if type(scale) is FP4Tensor else scale.data_ptr()
 
-    def set_tensors(self, buf, scale, offsets):
-        """The tensors that hold it (``buf``, ``scale``, ``offsets``; None or not), as autograd saved them."""
-        self.buf, self.scale, self.offsets = buf, scale, offsets
-        self.scale_ptr = None if scale is None else scale.data_ptr()
-        if buf is not None:
-            self.device = buf.device
-            self.q_ptr = buf.data_ptr()
-            self.sf_ptr = self.q_ptr + self.batch * self.rows * self.ld
-        return self
+    @property
+    def scale(self) -> torch.Tensor | None:
+        s = self._scale
+        if s is FP4_OWN_SCALE:
+            return self.buf[-16:-12].view(torch.float32)
+        return s.scale if type(s) is FP4Tensor else s
 
     @property
     def q(self) -> torch.Tensor:
@@ -497,8 +505,8 @@ def _raw_stream(device) -> int:
 
 
 def _fp4_buf(batch: int, rows: int, ld: int, row_blocks: int, kcols: int, fmt: int, device) -> torch.Tensor:
-    """Room for codes and scale blocks (ld is a multiple of 16, so both are aligned)."""
-    return torch.empty(batch * (rows * ld + row_blocks * -(-kcols // _FP4_WORD[fmt]) * 512), dtype=torch.uint8,
+    """Room for codes, scale blocks (ld is a multiple of 16, so both are aligned) and a scale."""
+    return torch.empty(batch * (rows * ld + row_blocks * -(-kcols // _FP4_WORD[fmt]) * 512) + 16, dtype=torch.uint8,
                        device=device)
 
 
@@ -520,7 +528,12 @@ def _fp4_input(x: torch.Tensor, fmt: int, tensor_scale, offsets):
     if tensor_scale is not None:
         if fmt != FP4_NV:
             raise ValueError("only FP4_NV has a tensor scale")
-        if tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1 or tensor_scale.device != x.device:
+        if tensor_scale is FP4_OWN_SCALE:
+            if dim == 3 and batch > 1 and sb != m * x.stride(1):
+                raise ValueError("x's matrices must follow one another for a scale of their own")
+        elif not isinstance(tensor_scale, torch.Tensor):
+            raise ValueError("tensor_scale must be a tensor, FP4_OWN_SCALE or None")
+        elif tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1 or tensor_scale.device != x.device:
             raise ValueError("tensor_scale must be one fp32 value on x's device")
     experts = 0
     if offsets is not None:
@@ -560,7 +573,8 @@ def fp4_tensor_scale(x: torch.Tensor) -> torch.Tensor:
 def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | None = None,
              offsets: torch.Tensor | None = None) -> FP4Tensor:
     """Casts the rows of x [m, k] or [batch, m, k] (bf16 or fp32, any strides) to
-    4 bits. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and
+    4 bits. ``tensor_scale`` (FP4_NV): one fp32 value on the device, None for 1,
+    or FP4_OWN_SCALE for ``fp4_tensor_scale(x)``, made in the call. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and
     the cast is the operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
     code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
     if offsets is None and x.stride(-1) != 1 and x.stride(-2) == 1 and k > 1:
@@ -570,8 +584,8 @@ def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | No
     dev = x.device
     a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld, tensor_scale, fmt, batch, m, k, offsets)
     st = load_library().fp4_cast(
-        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), x.stride(-1), fmt, a.scale_ptr, a.q_ptr, ld, a.sf_ptr,
-        _ptr(offsets), experts, _raw_stream(dev))
+        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), x.stride(-1), fmt, a.scale_ptr,
+        1 if tensor_scale is FP4_OWN_SCALE else 0, a.q_ptr, ld, a.sf_ptr, _ptr(offsets), experts, _raw_stream(dev))
     if st:
         _check("fp4_cast", st)
     return a
@@ -583,7 +597,7 @@ def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor
     its columns from one read: (cast of x, cast of x^T). The second is the
     operand of products that sum over x's rows; with ``offsets`` each expert's rows
     are columns of their own there (``gemm_fp4_wgrad_ragged``). ``rows=False``
-    leaves the first out (None)."""
+    leaves the first out (None). ``tensor_scale`` as in ``fp4_cast``."""
     code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
     if x.stride(-1) != 1 and k > 1:
         raise ValueError("x must have contiguous rows")
@@ -594,10 +608,11 @@ def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor
     a = None
     if rows:
         ld = -(-k // 32) * 16 or 16
-        a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld, tensor_scale, fmt, batch, m, k,
-                      offsets)
+        a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld,
+                      None if tensor_scale is None else c, fmt, batch, m, k, offsets)
     st = load_library().fp4_cast_dual(
-        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), fmt, c.scale_ptr, a.q_ptr if rows else None,
+        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), fmt, c.scale_ptr,
+        1 if tensor_scale is FP4_OWN_SCALE else 0, a.q_ptr if rows else None,
         a.ld if rows else 0, a.sf_ptr if rows else None, c.q_ptr, c.ld, c.sf_ptr, _ptr(offsets), experts,
         _raw_stream(dev))
     if st:
@@ -680,7 +695,8 @@ def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = Non
     """The forward call, cast and product in one: D [m, n] bf16 = X W^T of
     x [m, k] (bf16 or fp32) and a cast W [n, k]; with ``offsets`` (int32
     [experts + 1]) by expert, W [experts, n, k]. Equal to ``fp4_cast`` followed by
-    ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 16 rows take one launch."""
+    ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 64 rows take one launch.
+    ``x_scale`` as ``fp4_cast``'s tensor_scale."""
     if x.dim() == 2 and x.stride(1) != 1 and x.shape[1] > 1:
         x = x.contiguous()
     code, batch, m, k, _, experts = _fp4_input(x, w.fmt, x_scale, offsets)
@@ -699,13 +715,18 @@ def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = Non
             raise ValueError("out must be bf16")
         ldd = max(out.stride(0), n)
     lib = load_library()
-    size, ws = 0, None
-    if m > 16:
-        size = lib.fp4_linear_workspace_size(m, k, w.fmt, experts)
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    own = x_scale is FP4_OWN_SCALE
+    size = lib.fp4_linear_workspace_size(m, k, w.fmt, experts) if m > 64 else 0
+    ws = None
+    if own or size:
+        ws = torch.empty(size + 16, dtype=torch.uint8, device=dev)      # the scale is at its end
+        ws_ptr = ws.data_ptr()
+    else:
+        ws_ptr = None
     st = lib.fp4_linear(
-        x.data_ptr(), code, x.stride(0), _ptr(x_scale), w.q_ptr, w.ld, w.sf_ptr, w.scale_ptr, w.fmt, out.data_ptr(), ldd,
-        _ptr(offsets), experts, m, n, k, _ptr(ws), size, _raw_stream(dev))
+        x.data_ptr(), code, x.stride(0), ws_ptr + size if own else _ptr(x_scale), 1 if own else 0, w.q_ptr, w.ld,
+        w.sf_ptr, w.scale_ptr, w.fmt, out.data_ptr(), ldd, _ptr(offsets), experts, m, n, k, ws_ptr, size,
+        _raw_stream(dev))
     if st:
         _check("fp4_linear", st)
     return out

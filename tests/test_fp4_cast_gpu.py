@@ -127,6 +127,7 @@ def test_both_ways(ops, m, k, dtype, fmt):
     same(unpack(cols, tv), ref.values(np64(x).T, fmt, tv))
     none, cols2 = ops.fp4_cast_dual(x, fmt, t, rows=False)
     assert none is None and torch.equal(cols2.q, cols.q)
+    same(unpack(ops.fp4_cast(x.t(), fmt, t), tv), ref.values(np64(x).T, fmt, tv))       # a transposed view
     if dtype == torch.bfloat16 and k > 8:                       # rows that do not start on 16 bytes
         y = x[:, 1:]
         rows, cols = ops.fp4_cast_dual(y, fmt, t)
@@ -173,6 +174,25 @@ def test_by_expert(ops, offs, fmt):
         want[:, :hi - lo] = ref.values(np64(x)[lo:hi].T, fmt) if hi > lo else 0
         same(got[:, at:at + n], want)
         at += n
+
+
+@pytest.mark.parametrize("m,k", [(1, 1), (3, 33), (130, 520), (1031, 1031), (1024, 2048)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_own_scale(ops, m, k, dtype):
+    """A scale made in the call is fp4_tensor_scale's, on both sides of the size where that changes its form, and is the
+    casts' own: another call does not change it."""
+    x = acts(m, k, m * k, dtype).cuda()
+    t = ops.fp4_tensor_scale(x)
+    assert float(t) == ref.tensor_scale(np64(x))
+    a, (r, c) = ops.fp4_cast(x, 0, ops.FP4_OWN_SCALE), ops.fp4_cast_dual(x, 0, ops.FP4_OWN_SCALE)
+    big = ops.fp4_cast_dual(x * 64, 0, ops.FP4_OWN_SCALE)[0]
+    for v in (a, r, c):
+        assert float(v.scale) == float(t)
+    assert float(big.scale) == 64 * float(t)
+    want = ops.fp4_dequant(ops.fp4_cast(x, 0, t), torch.float32)
+    assert torch.equal(ops.fp4_dequant(a, torch.float32), want) and torch.equal(ops.fp4_dequant(r, torch.float32), want)
+    w = torch.stack([x, 2 * x])
+    assert float(ops.fp4_cast(w, 0, ops.FP4_OWN_SCALE).scale) == 2 * float(t)
 
 
 def test_past_31_bits(ops):

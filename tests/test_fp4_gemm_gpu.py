@@ -321,9 +321,10 @@ def test_gradients_against_differences(ops, fp4, fmt):
 @FMTS
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 4096, 7168), (3, 300, 515), (16, 257, 2048), (16, 128, 96), (9, 640, 4099),
-                                   (17, 300, 515), (200, 300, 1000)])
+                                   (17, 300, 515), (31, 4096, 2048), (33, 300, 700), (64, 130, 7168), (65, 300, 515),
+                                   (200, 300, 1000)])
 def test_forward_call_equals_cast_and_product(ops, m, n, k, dtype, fmt):
-    """Bit for bit, also where the product casts X itself (up to 16 rows), for rows that start anywhere."""
+    """Bit for bit, also where the product casts X itself (up to 64 rows), for rows that start anywhere."""
     big, w = acts(m, k + 3, seed=m + k, dtype=dtype), acts(n, k, seed=n, mul=0.02)
     b = ops.fp4_cast(w, fmt, ops.fp4_tensor_scale(w) if fmt == 0 else None)
     t = torch.tensor([0.25], device="cuda") if fmt == 0 else None
@@ -331,17 +332,20 @@ def test_forward_call_equals_cast_and_product(ops, m, n, k, dtype, fmt):
         for scale in (None, t):
             want = ops.gemm_fp4_nt(ops.fp4_cast(x, fmt, scale), b)
             assert torch.equal(ops.fp4_linear(x, b, scale), want)
-            if m <= 16:
+            if m <= 64 and k < 3000:
                 check(want, ref.values(np64(x), fmt, 1.0 if scale is None else 0.25),
                       ref.values(np64(w), fmt, 1.0 if b.scale is None else float(b.scale)))
+        if fmt == 0:
+            want = ops.gemm_fp4_nt(ops.fp4_cast(x, fmt, ops.fp4_tensor_scale(x)), b)
+            assert torch.equal(ops.fp4_linear(x, b, ops.FP4_OWN_SCALE), want)
     out = torch.full((m, n + 5), -7.0, dtype=torch.bfloat16, device="cuda")
     ops.fp4_linear(x, b, out=out[:, 2:n + 2])
     assert torch.equal(out[:, 2:n + 2], ops.fp4_linear(x, b)) and bool((out[:, :2] == -7).all()) and bool((out[:, n + 2:] == -7).all())
 
 
 @FMTS
-@pytest.mark.parametrize("offs", [[0, 1], [0, 3, 3, 7, 16], [2, 2, 5, 6], [0, 9, 25], [0, 100, 100, 331]],
-                         ids=["1", "16", "6", "25", "331"])
+@pytest.mark.parametrize("offs", [[0, 1], [0, 3, 3, 7, 16], [2, 2, 5, 6], [0, 9, 25], [0, 1, 40, 64], [0, 100, 100, 331]],
+                         ids=["1", "16", "6", "25", "64", "331"])
 def test_forward_call_by_expert(ops, offs, fmt):
     m, n, k, e = offs[-1], 300, 515, len(offs) - 1
     x, w = acts(m, k, seed=1), acts(e, n, k, seed=2, mul=0.02)
@@ -430,6 +434,8 @@ def test_refusals(ops, fp4):
                 lambda: ops.gemm_fp4_nt(a, b, out=torch.empty((16, 8), device="cuda").t()),
                 lambda: ops.fp4_linear(x[0], b), lambda: ops.fp4_linear(x[:, :32], b), lambda: ops.fp4_linear(x, b, offsets=off[:1]),
                 lambda: ops.fp4_linear(x, ops.fp4_cast(torch.stack([w, w]))), lambda: ops.fp4_linear(x, bm, one),
+                lambda: ops.fp4_cast(x, 1, ops.FP4_OWN_SCALE), lambda: ops.fp4_cast(x, 0, 0.5),
+                lambda: ops.fp4_cast(torch.stack([x, x, x])[::2], 0, ops.FP4_OWN_SCALE),
                 lambda: ops.fp4_linear(x, b, out=torch.empty((8, 16), device="cuda")),
                 lambda: ops.gemm_fp4_wgrad_ragged(a, b), lambda: ops.fp4_dequant(r), lambda: fp4.FP4Weight(w[None]),
                 lambda: fp4.dgrad(acts(8, 16, seed=3), fp4.FP4Weight(w, dgrad=False)),

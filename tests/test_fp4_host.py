@@ -31,25 +31,27 @@ def test_sizes(L):
 def test_refused_before_cuda(L):
     p, u = ctypes.c_void_p(64), ctypes.c_void_p(72)
     C = L.fp4_cast
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 2, None, p, 32, p, None, 0, None) == 1          # unknown format
-    assert C(p, 5, 1, 4, 64, 0, 64, 1, 0, None, p, 32, p, None, 0, None) == 1          # unknown type
-    assert C(p, 0, 1, -4, 64, 0, 64, 1, 0, None, p, 32, p, None, 0, None) == 1         # negative size
-    assert C(None, 0, 1, 4, 64, 0, 64, 1, 0, None, p, 32, p, None, 0, None) == 1       # null input
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, None, 32, p, None, 0, None) == 1       # null codes
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, p, 16, p, None, 0, None) == 1          # codes' rows too short
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, p, 40, p, None, 0, None) == 3          # row stride not of 16 bytes
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, u, 32, p, None, 0, None) == 3          # misaligned codes
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, p, 32, u, None, 0, None) == 3          # misaligned scales
-    assert C(p, 0, 2, 4, 64, 0, 64, 1, 0, None, p, 32, p, p, 2, None) == 1             # offsets with a batch
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, p, 32, p, p, 0, None) == 1             # no experts
-    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, p, 32, p, p, 513, None) == 2           # too many
-    assert C(p, 0, 1, 1 << 31, 64, 0, 64, 1, 0, None, p, 32, p, None, 0, None) == 2
-    assert C(None, 0, 1, 0, 64, 0, 64, 1, 0, None, None, 32, None, None, 0, None) == 0  # nothing to do
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 2, None, 0, p, 32, p, None, 0, None) == 1          # unknown format
+    assert C(p, 5, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, None, 0, None) == 1          # unknown type
+    assert C(p, 0, 1, -4, 64, 0, 64, 1, 0, None, 0, p, 32, p, None, 0, None) == 1         # negative size
+    assert C(None, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, None, 0, None) == 1       # null input
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, None, 32, p, None, 0, None) == 1       # null codes
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 16, p, None, 0, None) == 1          # codes' rows too short
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 40, p, None, 0, None) == 3          # row stride not of 16 bytes
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, u, 32, p, None, 0, None) == 3          # misaligned codes
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, u, None, 0, None) == 3          # misaligned scales
+    assert C(p, 0, 2, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, p, 2, None) == 1             # offsets with a batch
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, p, 0, None) == 1             # no experts
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, p, 513, None) == 2           # too many
+    assert C(p, 0, 1, 1 << 31, 64, 0, 64, 1, 0, None, 0, p, 32, p, None, 0, None) == 2
+    assert C(None, 0, 1, 0, 64, 0, 64, 1, 0, None, 0, None, 32, None, None, 0, None) == 0  # nothing to do
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 1, p, 32, p, None, 0, None) == 1       # own scale, nowhere to put it
+    assert C(p, 0, 1, 4, 64, 0, 64, 1, 1, p, 1, p, 32, p, None, 0, None) == 1          # MX has none
     D = L.fp4_cast_dual
-    assert D(p, 0, 1, 4, 64, 0, 64, 0, None, p, 32, None, p, 64, p, None, 0, None) == 1  # codes without scales
-    assert D(p, 0, 1, 4, 64, 0, 64, 0, None, p, 32, p, p, 48, p, None, 0, None) == 1     # columns too short
-    assert D(p, 0, 1, 4, 64, 0, 64, 7, None, p, 32, p, p, 64, p, None, 0, None) == 1
-    assert D(p, 0, 0, 4, 64, 0, 64, 0, None, p, 32, p, p, 64, p, None, 0, None) == 0
+    assert D(p, 0, 1, 4, 64, 0, 64, 0, None, 0, p, 32, None, p, 64, p, None, 0, None) == 1  # codes without scales
+    assert D(p, 0, 1, 4, 64, 0, 64, 0, None, 0, p, 32, p, p, 48, p, None, 0, None) == 1     # columns too short
+    assert D(p, 0, 1, 4, 64, 0, 64, 7, None, 0, p, 32, p, p, 64, p, None, 0, None) == 1
+    assert D(p, 0, 0, 4, 64, 0, 64, 0, None, 0, p, 32, p, p, 64, p, None, 0, None) == 0
     Q = L.fp4_dequant
     assert Q(p, 32, p, 3, None, 4, 64, p, 0, 64, None) == 1
     assert Q(p, 32, p, 0, None, 4, 64, p, 0, 63, None) == 1
@@ -69,17 +71,17 @@ def test_refused_before_cuda(L):
     assert R(p, 32, p, None, p, 32, p, None, 0, p, 0, 8, p, 600, 4, 8, 64, None) == 2
     assert R(p, 32, p, None, p, 32, p, None, 0, p, 0, 8, p, 2, 4, 8, 0, None) == 2       # k == 0
     F = L.fp4_linear
-    assert F(p, 0, 64, None, p, 32, p, None, 2, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown format
-    assert F(p, 3, 64, None, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown type
-    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 7, None, 0, 4, 8, 64, None, 0, None) == 1     # D's rows too short
-    assert F(None, 0, 64, None, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1
-    assert F(p, 0, 64, None, p, 40, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 3
-    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, p, 0, 4, 8, 64, None, 0, None) == 1        # offsets, no experts
-    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, p, 600, 4, 8, 64, None, 0, None) == 2
-    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, None, 0, 40, 8, 64, None, 0, None) == 1    # no workspace
-    assert F(p, 0, 64, None, p, 32, p, None, 0, p, 8, None, 0, 40, 8, 64, p, 10, None) == 1
-    assert L.fp4_linear_workspace_size(16, 7168, 0, 0) == 0
-    assert L.fp4_linear_workspace_size(40, 65, 0, 0) == 40 * 48 + 2 * 512
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 2, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown format
+    assert F(p, 3, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown type
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 7, None, 0, 4, 8, 64, None, 0, None) == 1     # D's rows too short
+    assert F(None, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1
+    assert F(p, 0, 64, None, 0, p, 40, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 3
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, p, 0, 4, 8, 64, None, 0, None) == 1        # offsets, no experts
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, p, 600, 4, 8, 64, None, 0, None) == 2
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 70, 8, 64, None, 0, None) == 1    # no workspace
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 70, 8, 64, p, 10, None) == 1
+    assert L.fp4_linear_workspace_size(64, 7168, 0, 0) == 0
+    assert L.fp4_linear_workspace_size(70, 65, 0, 0) == 70 * 48 + 2 * 512
     W = L.gemm_fp4_wgrad_ragged
     assert W(p, 1024, p, None, p, 1024, p, None, 0, p, 8, None, 2, 4, 4, 8, 0, None) == 1
     assert W(p, 16, p, None, p, 1024, p, None, 0, p, 8, p, 2, 4, 4, 8, 0, None) == 1     # columns too short
