@@ -2,7 +2,8 @@
 
 Each translation unit is compiled in parallel, then linked as a shared
 library next to this file. No CUDA math shortcuts (--use_fast_math is never
-passed): the cast depends on correctly rounded division.
+passed): the cast depends on correctly rounded division. The module of the 4-bit
+calls over torch tensors (_fp4.so, g++) is compiled beside it.
 """
 from __future__ import annotations
 
@@ -17,6 +18,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqlinear.so")
 SOURCES = ["api.cu", "cast.cu", "fp4_cast.cu", "fp4_gemm.cu", "fp4_gemm_pair.cu", "gemm.cu", "gemm_mx.cu", "gemm_mx2.cu", "gemm_mx_sk.cu", "gemm_pair.cu", "gemm_prom_sk.cu", "noalloc.cu"]
+TORCH_SOURCE = "fp4_torch.cpp"                 # the 4-bit calls over torch tensors (module _fp4)
+TORCH_LIB = os.path.join(HERE, "_fp4.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -63,12 +66,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        module = None if variant else ex.submit(build_torch_module, force)
         for cmd, r in ex.map(run, jobs):
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
             if verbose and (r.stdout or r.stderr):
                 print(r.stdout + r.stderr)
+        if module is not None:
+            module.result()
     if force or jobs or _stale(lib, objs):
         tmp = lib + f".{os.getpid()}.tmp"
         cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static"]
@@ -77,6 +83,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
             raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
     return lib
+
+
+def build_torch_module(force: bool = False) -> str:
+    """Compile the Python module of the 4-bit calls (C++ over torch's tensors and
+    the C ABI, whose entry points it is handed at run time); returns its path."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, TORCH_SOURCE)
+    if not force and not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "qlinear.h")]):
+        return TORCH_LIB
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], cuda):
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
 
 
 def build_bounds_checked(force: bool = False) -> str:

@@ -33,10 +33,6 @@ def _own(fmt: int):
     return ops.FP4_OWN_SCALE if fmt == ops.FP4_NV else None
 
 
-def _contiguous_rows(x: torch.Tensor) -> torch.Tensor:
-    return x if x.stride(-1) == 1 or x.shape[-1] <= 1 else x.contiguous()
-
-
 class FP4Weight:
     """A weight W [out, in] in 4 bits: ``w`` (forward) and, with ``dgrad``, ``wt``
     (the cast of W^T, for the data gradient)."""
@@ -52,7 +48,7 @@ class FP4Weight:
         if w.dim() != self._dims:
             raise ValueError("weight must be 2-D [out_features, in_features]" if self._dims == 2 else
                              "weight must be 3-D [experts, out_features, in_features]")
-        w = _contiguous_rows(w)
+        w = w if w.stride(-1) == 1 or w.shape[-1] <= 1 else w.contiguous()
         self.shape = tuple(w.shape)
         scale = _own(self.fmt)
         if self._dims == 3 and w.stride(0) != w.shape[1] * w.stride(1):
@@ -75,23 +71,6 @@ def _need_wt(w: FP4Weight) -> ops.FP4Tensor:
     return w.wt
 
 
-# Results are allocated before the first launch of a step: on Grace an
-# allocation right after a launch waits about 3 us for the launch to leave the
-# CPU.
-def _empty(x: torch.Tensor, cols: int, dtype: torch.dtype) -> torch.Tensor:
-    return torch.empty((x.shape[0], cols), dtype=dtype, device=x.device)
-
-
-def _grads(dy: torch.Tensor, w: FP4Weight, need_dx: bool, dw_out: torch.Tensor | None, accumulate: bool):
-    if dw_out is None:
-        if accumulate:
-            raise ValueError("accumulate needs an existing dw_out")
-        dw_out = torch.empty(w.shape, dtype=torch.float32, device=dy.device)
-    elif dw_out.dtype != torch.float32:
-        raise ValueError("dw_out must be fp32")
-    return _empty(dy, w.shape[-1], torch.bfloat16) if need_dx else None, dw_out
-
-
 def forward(x: torch.Tensor, w: FP4Weight, x_scale: torch.Tensor | None = None,
             out: torch.Tensor | None = None) -> torch.Tensor:
     """Y [T, out] = X [T, in] W^T (bf16)."""
@@ -100,22 +79,14 @@ def forward(x: torch.Tensor, w: FP4Weight, x_scale: torch.Tensor | None = None,
 
 def forward_saving(x: torch.Tensor, w: FP4Weight):
     """Y = X W^T plus X's cast along the tokens for the weight gradient: (Y, cast)."""
-    x = _contiguous_rows(x)
-    y = _empty(x, w.shape[-2], torch.bfloat16)
-    rows, cols = ops.fp4_cast_dual(x, w.fmt, _own(w.fmt))
-    return ops.gemm_fp4_nt(rows, w.w, out=y), cols
+    return ops.fp4_linear_saving(x, w.w, _own(w.fmt))
 
 
 def backward(dy: torch.Tensor, w: FP4Weight, x_cols: ops.FP4Tensor, need_dx: bool = True,
              dw_out: torch.Tensor | None = None, accumulate: bool = False):
     """dX = dY W (bf16, or None) and dW (+)= dY^T X (fp32) with dY cast both ways
     from one read and x_cols from ``forward_saving``."""
-    dy = _contiguous_rows(dy)
-    dx, dw = _grads(dy, w, need_dx, dw_out, accumulate)
-    rows, cols = ops.fp4_cast_dual(dy, w.fmt, _own(w.fmt), rows=need_dx)
-    if need_dx:
-        ops.gemm_fp4_nt(rows, _need_wt(w), out=dx)
-    return dx, ops.gemm_fp4_nt(cols, x_cols, out=dw, accumulate=accumulate)
+    return ops.fp4_linear_backward(dy, _need_wt(w) if need_dx else None, x_cols, _own(w.fmt), None, dw_out, accumulate)
 
 
 def dgrad(dy: torch.Tensor, w: FP4Weight, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -131,21 +102,14 @@ def experts_forward(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight, 
 
 def experts_forward_saving(x: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight):
     """experts_forward plus X's cast along each expert's tokens: (Y, cast)."""
-    x = _contiguous_rows(x)
-    y = _empty(x, w.shape[-2], torch.bfloat16)
-    rows, cols = ops.fp4_cast_dual(x, w.fmt, _own(w.fmt), offsets)
-    return ops.gemm_fp4_nt_ragged(rows, w.w, out=y), cols
+    return ops.fp4_linear_saving(x, w.w, _own(w.fmt), offsets)
 
 
 def experts_backward(dy: torch.Tensor, offsets: torch.Tensor, w: FP4ExpertWeight, x_cols: ops.FP4Tensor,
                      need_dx: bool = True, dw_out: torch.Tensor | None = None, accumulate: bool = False):
     """dX [T, in] (bf16, or None) and dW [experts, out, in] (+)= dY_e^T X_e (fp32)."""
-    dy = _contiguous_rows(dy)
-    dx, dw = _grads(dy, w, need_dx, dw_out, accumulate)
-    rows, cols = ops.fp4_cast_dual(dy, w.fmt, _own(w.fmt), offsets, rows=need_dx)
-    if need_dx:
-        ops.gemm_fp4_nt_ragged(rows, _need_wt(w), out=dx)
-    return dx, ops.gemm_fp4_wgrad_ragged(cols, x_cols, out=dw, accumulate=accumulate)
+    return ops.fp4_linear_backward(dy, _need_wt(w) if need_dx else None, x_cols, _own(w.fmt), offsets, dw_out,
+                                   accumulate)
 
 
 def _forward(x, offsets, w4):

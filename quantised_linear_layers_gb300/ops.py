@@ -131,10 +131,6 @@ def _dtype_code(x: torch.Tensor) -> int:
     raise TypeError(f"input must be bfloat16 or float32, got {x.dtype}")
 
 
-def _ptr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
-
-
 def _bytes8(t: torch.Tensor) -> torch.Tensor:
     if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError(f"expected an E4M3 (float8_e4m3fn or uint8) tensor, got {t.dtype}")
@@ -463,13 +459,13 @@ class FP4Tensor:
     it was cast by (``by_cols``: its columns are the experts' rows, each from a
     multiple of 256 on). The layouts are in include/qlinear.h."""
 
-    __slots__ = ("buf", "ld", "fmt", "batch", "rows", "cols", "offsets", "by_cols", "device", "q_ptr", "sf_ptr",
+    __slots__ = ("buf", "ld", "fmt", "batch", "rows", "cols", "offsets", "by_cols", "device_index", "q_ptr", "sf_ptr",
                  "scale_ptr", "_scale")
 
     def __init__(self, buf, ld, scale, fmt, batch, rows, cols, offsets=None, by_cols=False):
         # scale: a tensor, None, FP4_OWN_SCALE (the last 16 bytes of buf) or the FP4Tensor that has it
         self.ld, self.fmt, self.batch, self.rows, self.cols, self.by_cols = ld, fmt, batch, rows, cols, by_cols
-        self.buf, self.offsets, self.device = buf, offsets, buf.device
+        self.buf, self.offsets, self.device_index = buf, offsets, buf.get_device()
         self.q_ptr = q = buf.data_ptr()
         self.sf_ptr = q + batch * rows * ld
         self._scale = scale
@@ -497,98 +493,54 @@ class FP4Tensor:
         return self.buf[self.batch * self.rows * self.ld:]
 
 
-_FP4_WORD = {FP4_NV: 64, FP4_MX: 128}       # columns of a scale block
+_fp4 = None
+_FP4_ENTRIES = ("fp4_tensor_scale", "fp4_cast", "fp4_cast_dual", "fp4_dequant", "fp4_linear", "fp4_linear_workspace_size",
+                "gemm_fp4_nt", "gemm_fp4_nt_ragged", "gemm_fp4_wgrad_ragged")
 
 
-def _raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _load_fp4():
+    """The module of the 4-bit calls (_fp4.so), bound to the loaded library's entry
+    points (raises if either is missing: no fallback)."""
+    global _fp4
+    lib = load_library()
+    with _lock:
+        if _fp4 is None:
+            import importlib.util
+            path = os.path.join(_HERE, "_fp4.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"_fp4.so not found at {path}; run quantised_linear_layers_gb300.build.build()")
+            spec = importlib.util.spec_from_file_location("quantised_linear_layers_gb300._fp4", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FP4_ENTRIES), FP4Tensor,
+                     FP4_OWN_SCALE, _check)
+            _fp4 = mod
+    return _fp4
 
 
-def _fp4_buf(batch: int, rows: int, ld: int, row_blocks: int, kcols: int, fmt: int, device) -> torch.Tensor:
-    """Room for codes, scale blocks (ld is a multiple of 16, so both are aligned) and a scale."""
-    return torch.empty(batch * (rows * ld + row_blocks * -(-kcols // _FP4_WORD[fmt]) * 512) + 16, dtype=torch.uint8,
-                       device=device)
-
-
-def _fp4_input(x: torch.Tensor, fmt: int, tensor_scale, offsets):
-    """(type code, batch, m, k, stride between batch entries, experts) of a cast's input, checked."""
-    if fmt not in _FP4_WORD:
-        raise ValueError("fmt must be FP4_NV or FP4_MX")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    dim = x.dim()
-    if dim == 2:
-        m, k = x.shape
-        batch, sb = 1, 0
-    elif dim == 3:
-        batch, m, k = x.shape
-        sb = x.stride(0)
-    else:
-        raise ValueError("x must be 2-D or a batch of 2-D matrices")
-    if tensor_scale is not None:
-        if fmt != FP4_NV:
-            raise ValueError("only FP4_NV has a tensor scale")
-        if tensor_scale is FP4_OWN_SCALE:
-            if dim == 3 and batch > 1 and sb != m * x.stride(1):
-                raise ValueError("x's matrices must follow one another for a scale of their own")
-        elif not isinstance(tensor_scale, torch.Tensor):
-            raise ValueError("tensor_scale must be a tensor, FP4_OWN_SCALE or None")
-        elif tensor_scale.dtype != torch.float32 or tensor_scale.numel() != 1 or tensor_scale.device != x.device:
-            raise ValueError("tensor_scale must be one fp32 value on x's device")
-    experts = 0
-    if offsets is not None:
-        experts = _fp4_experts(offsets, x.device)
-        if dim != 2:
-            raise ValueError("x must be 2-D with offsets")
-    return _dtype_code(x), batch, m, k, sb, experts
-
-
-def _fp4_experts(offsets: torch.Tensor, device) -> int:
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() or offsets.shape[0] < 2 \
-            or offsets.device != device:
-        raise ValueError("offsets must be a contiguous int32 [experts + 1] tensor on x's device")
-    return offsets.shape[0] - 1
+def _is_bf16(dtype: torch.dtype) -> bool:
+    if dtype is torch.bfloat16:
+        return True
+    if dtype is torch.float32:
+        return False
+    raise ValueError("dtype must be bfloat16 or float32")
 
 
 def fp4_tensor_scale(x: torch.Tensor) -> torch.Tensor:
     """The FP4_NV scale of a tensor (any 2-D or 3-D strides, fp32 [1]): the least
     power of two t with max|x| <= 2688 t, at least 2^-80; a power of two leaves
     every group's scale s * t exact. NaN if x has an infinity or a NaN."""
-    dim = x.dim()
-    if dim not in (2, 3) or not x.is_cuda:
-        raise ValueError("x must be a 2-D or 3-D CUDA tensor")
-    m, k = x.shape[-2], x.shape[-1]
-    if dim == 3:
-        if x.stride(0) != m * x.stride(1):
-            x = x.contiguous()
-        m *= x.shape[0]
-    out = torch.empty(1, dtype=torch.float32, device=x.device)
-    st = load_library().fp4_tensor_scale(x.data_ptr(), _dtype_code(x), m, k, x.stride(-2), x.stride(-1), out.data_ptr(),
-                                         _raw_stream(x.device))
-    if st:
-        _check("fp4_tensor_scale", st)
-    return out
+    return (_fp4 or _load_fp4()).tensor_scale(x)
 
 
 def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | None = None,
              offsets: torch.Tensor | None = None) -> FP4Tensor:
     """Casts the rows of x [m, k] or [batch, m, k] (bf16 or fp32, any strides) to
     4 bits. ``tensor_scale`` (FP4_NV): one fp32 value on the device, None for 1,
-    or FP4_OWN_SCALE for ``fp4_tensor_scale(x)``, made in the call. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and
-    the cast is the operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
-    code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
-    if offsets is None and x.stride(-1) != 1 and x.stride(-2) == 1 and k > 1:
-        # a transposed view: the column-wise cast of the matrix it views
-        return fp4_cast_dual(x.transpose(-1, -2), fmt, tensor_scale, rows=False)[1]
-    ld = -(-k // 32) * 16 or 16
-    dev = x.device
-    a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld, tensor_scale, fmt, batch, m, k, offsets)
-    st = load_library().fp4_cast(
-        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), x.stride(-1), fmt, a.scale_ptr,
-        1 if tensor_scale is FP4_OWN_SCALE else 0, a.q_ptr, ld, a.sf_ptr, _ptr(offsets), experts, _raw_stream(dev))
-    if st:
-        _check("fp4_cast", st)
-    return a
+    or FP4_OWN_SCALE for ``fp4_tensor_scale(x)``, made in the call. ``offsets``
+    (int32 [experts + 1]): x's rows are sorted by expert and the cast is the
+    operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
+    return (_fp4 or _load_fp4()).cast(x, fmt, tensor_scale, offsets)
 
 
 def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | None = None,
@@ -598,78 +550,19 @@ def fp4_cast_dual(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor
     operand of products that sum over x's rows; with ``offsets`` each expert's rows
     are columns of their own there (``gemm_fp4_wgrad_ragged``). ``rows=False``
     leaves the first out (None). ``tensor_scale`` as in ``fp4_cast``."""
-    code, batch, m, k, sb, experts = _fp4_input(x, fmt, tensor_scale, offsets)
-    if x.stride(-1) != 1 and k > 1:
-        raise ValueError("x must have contiguous rows")
-    dev = x.device
-    kpad = (-(-m // 256) + experts) * 256 if experts else (-(-m // 128) * 128 or 128)   # fp4_column_extent
-    c = FP4Tensor(_fp4_buf(batch, k, kpad // 2, -(-k // 128), kpad if experts else m, fmt, dev), kpad // 2, tensor_scale,
-                  fmt, batch, k, m, offsets, experts > 0)
-    a = None
-    if rows:
-        ld = -(-k // 32) * 16 or 16
-        a = FP4Tensor(_fp4_buf(batch, m, ld, -(-m // 128) + experts, k, fmt, dev), ld,
-                      None if tensor_scale is None else c, fmt, batch, m, k, offsets)
-    st = load_library().fp4_cast_dual(
-        x.data_ptr(), code, batch, m, k, sb, x.stride(-2), fmt, c.scale_ptr,
-        1 if tensor_scale is FP4_OWN_SCALE else 0, a.q_ptr if rows else None,
-        a.ld if rows else 0, a.sf_ptr if rows else None, c.q_ptr, c.ld, c.sf_ptr, _ptr(offsets), experts,
-        _raw_stream(dev))
-    if st:
-        _check("fp4_cast_dual", st)
-    return a, c
+    return (_fp4 or _load_fp4()).cast_dual(x, fmt, tensor_scale, offsets, rows)
 
 
 def fp4_dequant(a: FP4Tensor, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values [rows, cols] that a cast stands for (bf16 or fp32)."""
-    if a.batch != 1 or a.offsets is not None:
-        raise ValueError("fp4_dequant takes the cast of one matrix")
-    out = _fp4_out(out, (a.rows, a.cols), dtype, a.device, False)
-    st = load_library().fp4_dequant(
-        a.q_ptr, a.ld, a.sf_ptr, a.fmt, a.scale_ptr, a.rows, a.cols, out.data_ptr(), _dtype_code(out),
-        max(out.stride(0), a.cols), _raw_stream(a.device))
-    if st:
-        _check("fp4_dequant", st)
-    return out
-
-
-def _fp4_pair(x: FP4Tensor, w: FP4Tensor):
-    if x.fmt != w.fmt:
-        raise ValueError("the operands' formats differ")
-    if x.cols != w.cols:
-        raise ValueError("the operands must share K")
-    if x.device != w.device:
-        raise ValueError("the operands must be on one device")
-
-
-def _fp4_out(out, shape, dtype, device, accumulate):
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs an existing out")
-        return torch.empty(shape, dtype=dtype, device=device)
-    if out.dtype not in (torch.bfloat16, torch.float32) or tuple(out.shape) != tuple(shape) \
-            or out.device != device or (out.shape[-1] > 1 and out.stride(-1) != 1):
-        raise ValueError(f"out must be bf16 or fp32 {tuple(shape)} with contiguous rows on the operands' device")
-    if accumulate and out.dtype != torch.float32:
-        raise ValueError("accumulate needs an fp32 out")
-    return out
+    return (_fp4 or _load_fp4()).dequant(a, out, _is_bf16(dtype))
 
 
 def gemm_fp4_nt(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
                 accumulate: bool = False) -> torch.Tensor:
     """D [m, n] (+)= X W^T of two row-wise casts of one format: X [m, k], W [n, k];
     D bf16 or fp32 (accumulate: fp32)."""
-    _fp4_pair(x, w)
-    if x.batch != 1 or w.batch != 1 or x.offsets is not None or w.offsets is not None:
-        raise ValueError("gemm_fp4_nt takes casts of one matrix each")
-    out = _fp4_out(out, (x.rows, w.rows), dtype, x.device, accumulate)
-    st = load_library().gemm_fp4_nt(
-        x.q_ptr, x.ld, x.sf_ptr, x.scale_ptr, w.q_ptr, w.ld, w.sf_ptr, w.scale_ptr, x.fmt, out.data_ptr(),
-        _dtype_code(out), max(out.stride(0), w.rows), x.rows, w.rows, x.cols, 1 if accumulate else 0,
-        _raw_stream(x.device))
-    if st:
-        _check("gemm_fp4_nt", st)
-    return out
+    return (_fp4 or _load_fp4()).gemm(x, w, out, _is_bf16(dtype), accumulate)
 
 
 def gemm_fp4_nt_ragged(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = None,
@@ -677,17 +570,15 @@ def gemm_fp4_nt_ragged(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = No
     """Experts' products: rows offsets[e] .. offsets[e+1] of D [m, n] are those
     rows of X [m, k] times W[e]^T; X cast with the offsets, W [experts, n, k] cast
     as a batch. Rows of no expert are left unwritten in ``out``."""
-    _fp4_pair(x, w)
-    if x.offsets is None or x.by_cols or w.offsets is not None or w.batch != x.offsets.shape[0] - 1:
-        raise ValueError("x must be cast by expert and w hold one matrix per expert")
-    out = _fp4_out(out, (x.rows, w.rows), dtype, x.device, False)
-    st = load_library().gemm_fp4_nt_ragged(
-        x.q_ptr, x.ld, x.sf_ptr, x.scale_ptr, w.q_ptr, w.ld, w.sf_ptr, w.scale_ptr, x.fmt, out.data_ptr(),
-        _dtype_code(out), max(out.stride(0), w.rows), x.offsets.data_ptr(), w.batch, x.rows, w.rows, x.cols,
-        _raw_stream(x.device))
-    if st:
-        _check("gemm_fp4_nt_ragged", st)
-    return out
+    return (_fp4 or _load_fp4()).ragged(x, w, out, _is_bf16(dtype))
+
+
+def gemm_fp4_wgrad_ragged(y: FP4Tensor, x: FP4Tensor, out: torch.Tensor | None = None,
+                          accumulate: bool = False) -> torch.Tensor:
+    """Experts' weight gradients D [experts, m, n] (+)= Y_e^T X_e, fp32, from the
+    column-wise casts of Y [tokens, m] and X [tokens, n] by the same offsets. An
+    expert without rows gets zeros."""
+    return (_fp4 or _load_fp4()).wgrad(y, x, out, accumulate)
 
 
 def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = None,
@@ -697,59 +588,27 @@ def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = Non
     [experts + 1]) by expert, W [experts, n, k]. Equal to ``fp4_cast`` followed by
     ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 64 rows take one launch.
     ``x_scale`` as ``fp4_cast``'s tensor_scale."""
-    if x.dim() == 2 and x.stride(1) != 1 and x.shape[1] > 1:
-        x = x.contiguous()
-    code, batch, m, k, _, experts = _fp4_input(x, w.fmt, x_scale, offsets)
-    dev = x.device
-    if x.dim() != 2 or k != w.cols or dev != w.device:
-        raise ValueError("x must be [m, k] with w's k, on w's device")
-    if w.offsets is not None or w.batch != (experts or 1):
-        raise ValueError("w must be the cast of one matrix, or of one per expert with offsets")
-    n = w.rows
-    if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-        ldd = n
-    else:
-        out = _fp4_out(out, (m, n), torch.bfloat16, dev, False)
-        if out.dtype != torch.bfloat16:
-            raise ValueError("out must be bf16")
-        ldd = max(out.stride(0), n)
-    lib = load_library()
-    own = x_scale is FP4_OWN_SCALE
-    size = lib.fp4_linear_workspace_size(m, k, w.fmt, experts) if m > 64 else 0
-    ws = None
-    if own or size:
-        ws = torch.empty(size + 16, dtype=torch.uint8, device=dev)      # the scale is at its end
-        ws_ptr = ws.data_ptr()
-    else:
-        ws_ptr = None
-    st = lib.fp4_linear(
-        x.data_ptr(), code, x.stride(0), ws_ptr + size if own else _ptr(x_scale), 1 if own else 0, w.q_ptr, w.ld,
-        w.sf_ptr, w.scale_ptr, w.fmt, out.data_ptr(), ldd, _ptr(offsets), experts, m, n, k, ws_ptr, size,
-        _raw_stream(dev))
-    if st:
-        _check("fp4_linear", st)
-    return out
+    return (_fp4 or _load_fp4()).linear(_contiguous_rows(x), w, x_scale, offsets, out)
 
 
-def gemm_fp4_wgrad_ragged(y: FP4Tensor, x: FP4Tensor, out: torch.Tensor | None = None,
-                          accumulate: bool = False) -> torch.Tensor:
-    """Experts' weight gradients D [experts, m, n] (+)= Y_e^T X_e, fp32, from the
-    column-wise casts of Y [tokens, m] and X [tokens, n] by the same offsets. An
-    expert without rows gets zeros."""
-    _fp4_pair(y, x)
-    if not y.by_cols or not x.by_cols or y.offsets.shape != x.offsets.shape:
-        raise ValueError("both operands must be column-wise casts by the same experts")
-    experts = y.offsets.shape[0] - 1
-    out = _fp4_out(out, (experts, y.rows, x.rows), torch.float32, y.device, accumulate)
-    if out.dtype != torch.float32 or not out.is_contiguous():
-        raise ValueError("out must be contiguous fp32")
-    st = load_library().gemm_fp4_wgrad_ragged(
-        y.q_ptr, y.ld, y.sf_ptr, y.scale_ptr, x.q_ptr, x.ld, x.sf_ptr, x.scale_ptr, y.fmt, out.data_ptr(), x.rows,
-        y.offsets.data_ptr(), experts, y.cols, y.rows, x.rows, 1 if accumulate else 0, _raw_stream(y.device))
-    if st:
-        _check("gemm_fp4_wgrad_ragged", st)
-    return out
+def fp4_linear_saving(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = None,
+                      offsets: torch.Tensor | None = None):
+    """``fp4_linear`` that also casts x along its columns from the same read:
+    (D, cast of x^T), the second for ``fp4_linear_backward``."""
+    return (_fp4 or _load_fp4()).linear_saving(_contiguous_rows(x), w, x_scale, offsets)
+
+
+def fp4_linear_backward(dy: torch.Tensor, wt: FP4Tensor | None, x_cols: FP4Tensor, dy_scale: torch.Tensor | None = None,
+                        offsets: torch.Tensor | None = None, dw_out: torch.Tensor | None = None,
+                        accumulate: bool = False):
+    """(dX, dW) of ``fp4_linear_saving``'s product: dX [m, k] bf16 = dY W from the
+    cast ``wt`` of W^T (None: no dX), dW [n, k] or [experts, n, k] fp32 (+)= dY^T X,
+    with dY cast both ways from one read."""
+    return (_fp4 or _load_fp4()).linear_backward(_contiguous_rows(dy), wt, x_cols, dy_scale, offsets, dw_out, accumulate)
+
+
+def _contiguous_rows(x: torch.Tensor) -> torch.Tensor:
+    return x if x.stride(-1) == 1 or x.shape[-1] <= 1 else x.contiguous()
 
 
 def set_num_sms(n: int) -> None:

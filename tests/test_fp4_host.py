@@ -101,3 +101,24 @@ def test_reference_closed_forms():
     assert ref.scales(np.array([[6 * 1.0625]]), ref.NV)[0, 0] == 1.0        # E4M3 tie to even: 1, not 1.125
     assert ref.tensor_scale(np.array([[2688.0]])) == 1 and ref.tensor_scale(np.array([[2689.0]])) == 2
     assert np.isnan(ref.values(np.array([[1.0, np.inf]]), ref.NV)).all()
+
+
+def test_module_fails_loudly_when_missing(monkeypatch, tmp_path):
+    from quantised_linear_layers_gb300 import ops
+    monkeypatch.setattr(ops, "_fp4", None)
+    monkeypatch.setattr(ops, "_HERE", str(tmp_path))
+    with pytest.raises(RuntimeError, match="_fp4.so not found"):
+        ops._load_fp4()
+
+
+def test_module_refuses_host_tensors():
+    import torch
+    from quantised_linear_layers_gb300 import ops
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    for call in (lambda: ops.fp4_cast(x), lambda: ops.fp4_cast_dual(x), lambda: ops.fp4_tensor_scale(x),
+                 lambda: ops.fp4_dequant(x), lambda: ops.gemm_fp4_nt(x, x), lambda: ops.fp4_linear(x, x),
+                 lambda: ops.fp4_cast(x, 7), lambda: ops.fp4_dequant(x, torch.float16)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        ops._load_fp4().gemm(x)
