@@ -14,17 +14,18 @@
 // each a part of K; the fp32 partial tiles meet in shared memory, and each CTA
 // sums and stores its share of the rows in the CTAs' order.
 //
-// Up to 64 rows of X (kFp4CastRows) can come as they are, bf16 or fp32: more
-// warps then cast them into the stages, a warp taking up to 32 rows of every
-// eighth stage, and the call is a single launch. Every CTA repeats the cast of
-// its part of K, 64 x 1792 elements at most at K = 7168, while its weights are
-// on their way.
+// Up to 8 rows of X (kFp4CastRows) can come as they are, bf16 or fp32: eight
+// more warps then cast them into the stages, a warp taking every eighth stage,
+// and the call is a single launch. Every CTA repeats the cast of its part of K
+// while its weights are on their way. At 4096 x 7168 (us, weights from HBM)
+// one row takes 7.6 cast inside and 8.8 with a launch for the cast, 8 rows 8.4
+// and 9.2, 16 rows 9.5 and 9.2, 64 rows 15.2 and 10.5.
 //
-// Roles (256 threads, 256 or 512 more with the cast): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
+// Roles (256 threads, 256 more with the cast): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
 // stage's scales into tensor memory, then up to four instructions of K = 64),
-// warps 4-7 epilogue. Two accumulators and two scale slots in tensor memory:
-// the slot of stage i is written when the instructions of stage i - 2, whose
-// completion frees that stage's shared memory, are done.
+// warps 4-7 epilogue. Tensor memory holds two accumulators and a scale slot for
+// every stage of shared memory, so that a stage that has landed can be issued:
+// the instructions that read its slot before are those that freed it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,9 +43,7 @@ namespace ql {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCastStep = 8;                                     // a warp casts every eighth stage
-constexpr int cast_parts(int nt) { return nt <= 32 ? 1 : nt / 32; }
-constexpr int cast_threads(int nt) { return 32 * kCastStep * cast_parts(nt); }
+constexpr int kCastWarps = 8;                // a warp casts every eighth stage
 constexpr int TW = 128;
 constexpr int kMaxSplit = 8;
 
@@ -56,8 +55,8 @@ struct Cfg {
     static constexpr int kStageSf = kWords * kFp4SfBlock;         // per operand
     static constexpr int kBytes = kStageW + kStageX + 2 * kStageSf;
     static constexpr int kSlot = 8 * kWords;                      // tensor-memory columns of a stage's scales
-    static constexpr int kSfCol = NT <= 32 ? 64 : 2 * NT;          // accumulators at 0 and NT
-    static constexpr int kTmem = kSfCol + 2 * kSlot <= 128 ? 128 : (kSfCol + 2 * kSlot <= 256 ? 256 : 512);
+    static constexpr int kSfCol = NT < 32 ? 64 : 2 * NT;          // accumulators at 0 and NT
+    static constexpr int kTmem = 512;
     static constexpr int kMisc = 2304;                            // barriers, offsets
     static constexpr int kMaxStages = (232448 - 1024 - kMisc) / kBytes;
     static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
@@ -68,6 +67,7 @@ struct Cfg {
     static constexpr int kOffOff = kOffBar + 192;
     static constexpr int kSmem = kOffBar + kMisc + 1024;
     static_assert((2 * kStages + 5) * 8 + 16 <= 192, "barriers");
+    static_assert(kSfCol + kStages * kSlot <= kTmem, "tensor memory");
     static_assert(192 + (kFp4MaxExperts + 1) * 4 <= kMisc, "offsets");
     static_assert(kStageX % 1024 == 0 && kSmem <= 232448, "shared memory");
     static_assert(NT * TW * 4 <= kOffSfw, "partial tile fits in the operand ring");
@@ -171,29 +171,29 @@ __device__ __forceinline__ void sum_parts(uint32_t part, const Fp4GemmParams& p,
     }
 }
 
-// One stage of X cast in place of its copy: rows [r0, r1) of 256 columns from
-// column c0 on, codes in the 128-byte swizzle the tensor core reads, scale bytes
-// in a scale block's order. A lane has 16 columns of a row, a warp two rows.
+// One stage of X cast in place of its copy: its rows' 256 columns from column
+// c0 on, codes in the 128-byte swizzle the tensor core reads, scale bytes in a
+// scale block's order. A lane has 16 columns of a row, a warp two rows.
 template <typename T, int FMT>
-__device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, int r0, int r1, int c0, uint8_t* codes,
+__device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, int rows, int c0, uint8_t* codes,
                                            uint8_t* sf, const Fp4Tensor& tn) {
-    constexpr int kAhead = 8 / sizeof(T);        // pairs of rows in flight
+    constexpr int kAhead = 4;                    // pairs of rows in flight
     const int lane = static_cast<int>(threadIdx.x & 31), cg = lane & 15;
     const int c = c0 + cg * 16;
     const T* x = static_cast<const T*>(p.xr) + static_cast<int64_t>(x_row) * p.sxr;
-    for (int rb = r0; rb < r1; rb += 2 * kAhead) {
+    for (int rb = 0; rb < rows; rb += 2 * kAhead) {
         Raw16<T> raw[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int r = rb + 2 * i + (lane >> 4);
-            if (r >= r1 || c >= p.k) raw[i].zero();
+            if (r >= rows || c >= p.k) raw[i].zero();
             else if (p.xr_vec && c + 16 <= p.k) raw[i].load(x + r * p.sxr + c);
             else raw[i].load_some(x + r * p.sxr + c, 1, p.k - c < 16 ? p.k - c : 16);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int r = rb + 2 * i + (lane >> 4);
-            if (rb + 2 * i >= r1) break;
+            if (rb + 2 * i >= rows) break;
             float amax = raw[i].amax();
             if constexpr (FMT == kFp4Mx) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             const Fp4Scale g = fp4_scale<FMT>(amax, tn);
@@ -203,7 +203,7 @@ __device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, in
             const int gi = FMT == kFp4Nv ? cg : cg >> 1;
             if (FMT == kFp4Nv || (cg & 1) == 0) {
                 const bool live = c0 + gi * fp4_group(FMT) < p.k;
-                sf[(gi >> 2) * kFp4SfBlock + (r & 31) * 16 + (r >> 5) * 4 + (gi & 3)] = live ? static_cast<uint8_t>(g.byte) : 0;
+                sf[(gi >> 2) * kFp4SfBlock + r * 16 + (gi & 3)] = live ? static_cast<uint8_t>(g.byte) : 0;
             }
         }
     }
@@ -211,7 +211,7 @@ __device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, in
 
 // T: void when X's codes are copied, else the type of X to cast.
 template <int NT, int FMT, bool OUT_F32, typename T>
-__global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads + cast_threads(NT), 1)
+__global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads + 32 * kCastWarps, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_sfx, const __grid_constant__ CUtensorMap map_sfw,
                     const Fp4GemmParams p) {
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
     const int first = static_cast<int>(cluster_id_x()), step = static_cast<int>(num_clusters_x());
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], kCast ? 1 + cast_parts(NT) : 1); mbar_init(&empty[s], 1); }
+        for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], kCast ? 2 : 1); mbar_init(&empty[s], 1); }
         for (int s = 0; s < 2; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 128); }
         mbar_init(done_bar, 1);
         *abort_flag = 0;
@@ -320,13 +320,9 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
                 const uint32_t x_col = NT < 128 ? static_cast<uint32_t>(t.x_sub >> 5) : 0u;
                 for (int kb = lo; kb < hi; ++kb, ++it) {
                     const uint32_t s = it % C::kStages;
-                    if (it >= 2) {
-                        const uint32_t j = it - 2;
-                        if (!mbar_wait(&empty[j % C::kStages], (j / C::kStages) & 1u, ctl)) { ok = false; break; }
-                    }
                     if (!mbar_wait(&full[s], (it / C::kStages) & 1u, ctl)) { ok = false; break; }
                     tc_fence_after_sync();
-                    const uint32_t sfw = tmem_base + C::kSfCol + (it & 1u) * C::kSlot;
+                    const uint32_t sfw = tmem_base + C::kSfCol + s * C::kSlot;
                     const uint32_t sfx = sfw + 4 * C::kWords;
                     const uint32_t pw = smem_addr(smem + C::kOffSfw + s * C::kStageSf);
                     const uint32_t px = smem_addr(smem + C::kOffSfx + s * C::kStageSf);
@@ -364,15 +360,12 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
             for (int i = first; ok && walk.get(i, p, s_off, t); i += step) {
                 int lo, hi;
                 stages(lo, hi);
-                // this warp's rows, to the pair of rows that a pass writes
-                constexpr int kPart = NT / cast_parts(NT);
-                const int r0 = (warp - 8) / kCastStep * kPart;
-                const int r1 = t.rows < r0 + kPart ? t.rows : r0 + kPart;
+                const int rows = t.rows < NT ? t.rows : NT;
                 for (int kb = lo; kb < hi; ++kb, ++it) {
-                    if (static_cast<int>(it % kCastStep) != (warp - 8) % kCastStep) continue;
+                    if (static_cast<int>(it % kCastWarps) != warp - 8) continue;
                     const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
                     if (!warp_wait(&empty[s], ph ^ 1u, ctl)) { ok = false; break; }
-                    cast_stage<T, FMT>(p, t.x_row, r0, r1, kb * 256, smem + C::kOffX + s * C::kStageX,
+                    cast_stage<T, FMT>(p, t.x_row, rows, kb * 256, smem + C::kOffX + s * C::kStageX,
                                        smem + C::kOffSfx + s * C::kStageSf, tn);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -480,7 +473,7 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     const int64_t most = split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(most * split), 1, 1);
-    cfg.blockDim = dim3(kCast ? kThreads + cast_threads(NT) : kThreads, 1, 1);
+    cfg.blockDim = dim3(kCast ? kThreads + 32 * kCastWarps : kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -544,12 +537,11 @@ void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
-    if (a.xr != nullptr) {
-        if (a.m <= 16) return launch_cast<16>(a, st, num_sms);
-        return a.m <= 32 ? launch_cast<32>(a, st, num_sms) : launch_cast<64>(a, st, num_sms);
-    }
-    if (a.form == kFp4Plain && a.m <= 16) return launch_n<16>(a, st, num_sms);
-    if (a.form == kFp4Plain && a.m <= 64) return launch_n<64>(a, st, num_sms);
+    if (a.xr != nullptr) return launch_cast<16>(a, st, num_sms);
+    if (a.m <= 16) return launch_n<16>(a, st, num_sms);
+    // narrow tiles as long as one covers an expert's rows on average
+    const int64_t per = a.form == kFp4RagRows ? a.m / a.experts : a.m;
+    if (per <= 64) return launch_n<64>(a, st, num_sms);
     return launch_n<128>(a, st, num_sms);
 }
 

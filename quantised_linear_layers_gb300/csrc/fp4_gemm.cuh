@@ -80,7 +80,7 @@ struct Fp4GemmParams {
 };
 
 // Largest m whose X the product casts itself.
-constexpr int kFp4CastRows = 64;
+constexpr int kFp4CastRows = 8;
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);

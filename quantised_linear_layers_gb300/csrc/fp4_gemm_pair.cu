@@ -8,7 +8,9 @@
 // cycles of the tensor core at its rate for K = 64 steps. At that rate the
 // bytes a stage brings into an SM are the tighter limit, hence the widest tile
 // that leaves tensor memory for the scales, with one accumulator; its
-// registers are read out in one go so that the next tile starts at once.
+// registers are read out in one go so that the next tile starts at once. Each
+// stage of shared memory has its scale slot in tensor memory (five of 48
+// columns beside the accumulator's 256).
 //
 // Roles (384 threads per CTA): warp 0 TMA producer, warp 1 of the leader MMA
 // issuer, warps 4-11 epilogue (32 rows x 128 columns of D each, staged in
@@ -55,7 +57,7 @@ struct PairCfg {
     static constexpr int kSmem = kOffOff + (kFp4MaxExperts + 1) * 4 + 12 + 1024;
     static_assert(kOffSf % 1024 == 0 && kSmem <= 232448, "shared memory");
     static_assert((2 * kStages + 3) * 8 + 16 <= 256, "barriers");
-    static_assert(kSfCol + 2 * kSlot <= kTmem, "tensor memory");
+    static_assert(kSfCol + kStages * kSlot <= kTmem, "tensor memory");
 };
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
@@ -211,14 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after_sync();
                     for (int kb = 0; kb < kbs; ++kb, ++it) {
                         const uint32_t s = it % C::kStages;
-                        if (it >= 2) {
-                            // the instructions of stage it - 2 have read the scale slot
-                            const uint32_t j = it - 2;
-                            if (!mbar_wait(&empty[j % C::kStages], (j / C::kStages) & 1u, ctl)) { ok = false; break; }
-                        }
                         if (!mbar_wait_cluster(&full[s], (it / C::kStages) & 1u, ctl)) { ok = false; break; }
                         tc_fence_after_sync();
-                        const uint32_t sfx = tmem_base + C::kSfCol + (it & 1u) * C::kSlot;
+                        const uint32_t sfx = tmem_base + C::kSfCol + s * C::kSlot;
                         const uint32_t sfw = sfx + 4 * C::kWords;      // per word: 4 columns of each W block
                         const uint32_t ps = smem_addr(smem + C::kOffSf + s * C::kStageSf);
 #pragma unroll

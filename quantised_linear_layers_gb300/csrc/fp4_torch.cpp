@@ -22,8 +22,6 @@
 
 namespace {
 
-constexpr int64_t kCastRows = 64;        // fp4_linear casts up to so many rows without a workspace
-
 struct Api {
     decltype(&::fp4_tensor_scale) tensor_scale;
     decltype(&::fp4_cast) cast;
@@ -431,7 +429,7 @@ PyObject* f_linear(Args a) {
     c10::cuda::CUDAGuard guard(in.x->device());
     const Out d = output(a[4], {in.m, w.rows}, at::kBFloat16, w.device, false);
     if (d.code != QL_BF16) value_error("out must be bf16");
-    const int64_t size = in.m > kCastRows ? static_cast<int64_t>(api.linear_ws(in.m, in.k, w.fmt, in.experts)) : 0;
+    const int64_t size = static_cast<int64_t>(api.linear_ws(in.m, in.k, w.fmt, in.experts));
     at::Tensor ws;
     uint8_t* p = nullptr;
     if (size > 0 || in.own) {

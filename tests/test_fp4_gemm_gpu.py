@@ -324,7 +324,7 @@ def test_gradients_against_differences(ops, fp4, fmt):
                                    (17, 300, 515), (31, 4096, 2048), (33, 300, 700), (64, 130, 7168), (65, 300, 515),
                                    (200, 300, 1000)])
 def test_forward_call_equals_cast_and_product(ops, m, n, k, dtype, fmt):
-    """Bit for bit, also where the product casts X itself (up to 64 rows), for rows that start anywhere."""
+    """Bit for bit, also where the product casts X itself (up to 8 rows), for rows that start anywhere."""
     big, w = acts(m, k + 3, seed=m + k, dtype=dtype), acts(n, k, seed=n, mul=0.02)
     b = ops.fp4_cast(w, fmt, ops.fp4_tensor_scale(w) if fmt == 0 else None)
     t = torch.tensor([0.25], device="cuda") if fmt == 0 else None

@@ -80,7 +80,7 @@ def test_refused_before_cuda(L):
     assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, p, 600, 4, 8, 64, None, 0, None) == 2
     assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 70, 8, 64, None, 0, None) == 1    # no workspace
     assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 70, 8, 64, p, 10, None) == 1
-    assert L.fp4_linear_workspace_size(64, 7168, 0, 0) == 0
+    assert L.fp4_linear_workspace_size(8, 7168, 0, 0) == 0
     assert L.fp4_linear_workspace_size(70, 65, 0, 0) == 70 * 48 + 2 * 512
     W = L.gemm_fp4_wgrad_ragged
     assert W(p, 1024, p, None, p, 1024, p, None, 0, p, 8, None, 2, 4, 4, 8, 0, None) == 1
