@@ -8,8 +8,8 @@
 //           for E2M1 * (s * t)
 //   kFp4Mx  32 elements, scale 2^p, p = ceil(log2(amax / 6)) held in
 //           [-127, 127] and stored as p + 127 (UE8M0)
-// A group with an infinity or a NaN gets the scale NaN (0x7F / 0xFF) and codes
-// of zero, so it is NaN in every product and when it is read back.
+// A group with an infinity or a NaN gets the scale NaN (0x7F / 0xFF), so it is
+// NaN in every product and when it is read back, whatever its codes.
 //
 // Layouts. Codes: row-major bytes, element 2j in the low and 2j + 1 in the
 // high half of byte j; rows start on 16-byte boundaries; the unused half byte of an
@@ -191,29 +191,33 @@ __device__ __forceinline__ float quot(float a, float b, float r) {
     return __fmaf_rn(__fmaf_rn(-q, b, a), r, q);
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // Scale of one group: its stored byte and what its elements are divided by.
-// nv: S and 1 / S; mx: the power of two 1 / S alone.
+// nv: S and 1 / S; mx: the power of two 1 / S alone. nv: an amax of infinity or
+// NaN makes the quotient, and with it the byte, NaN.
 struct Fp4Scale {
     uint32_t byte;
     float s, r;
-    bool finite;
 };
 template <int FMT>
 __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Fp4Tensor& tn) {
     Fp4Scale o;
-    o.finite = amax <= 3.402823466e38f;              // false for infinity and NaN
     if constexpr (FMT == kFp4Nv) {
-        const float d = fminf(fmaxf(quot(amax, tn.t6, tn.r6), 0.001953125f), 448.0f);
+        const float d = min_nan(max_nan(quot(amax, tn.t6, tn.r6), 0.001953125f), 448.0f);
         o.byte = static_cast<uint32_t>(__nv_cvt_float_to_fp8(d, __NV_SATFINITE, __NV_E4M3));
         o.s = __fmul_rn(e4m3_value(o.byte), tn.t);
         o.r = rcp_approx(o.s);
-        if (!o.finite) o.byte = 0x7F;
     } else {
         const uint32_t b = __float_as_uint(amax);
-        int e = static_cast<int>((b >> 23) & 0xFFu) - 2 + ((b & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+        // exponent of amax / 6 rounded up: amax > 1.5 * 2^(e + 2) takes the next
+        int e = static_cast<int>((b + 0x3FFFFFu) >> 23) - 2;
         e = e < 0 ? 0 : e;
-        o.byte = static_cast<uint32_t>(e);
-        if (!o.finite) { o.byte = 0xFF; e = 127; }
+        o.byte = b >= 0x7F800000u ? 0xFFu : static_cast<uint32_t>(e);
         o.r = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
         o.s = 0.0f;                                  // not used
     }
@@ -234,9 +238,7 @@ __device__ __forceinline__ uint2 fp4_codes16(const uint64_t (&x)[8], const Fp4Sc
         }
         v[i >> 2][i & 3] = q;
     }
-    uint2 o = make_uint2(e2m1x8(v[0]), e2m1x8(v[1]));
-    if (!g.finite) o = make_uint2(0u, 0u);
-    return o;
+    return make_uint2(e2m1x8(v[0]), e2m1x8(v[1]));
 }
 
 __device__ __forceinline__ uint64_t bf16x2_f32x2(uint32_t w) {

@@ -78,12 +78,12 @@ __device__ __forceinline__ void load_piece(Raw16<T>& raw, const T* row, int64_t 
 // and the next four), whose words its warps write at about the same time; the
 // columns are shared out over blockIdx.y when there are few rows.
 template <typename T, int FMT, int ROWS, int U>
-__global__ void __launch_bounds__(kThreads) fp4_cast_kernel(const Fp4CastArgs p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) fp4_cast_kernel(const Fp4CastArgs p) {
     __shared__ __align__(16) T s_buf[ROWS == kRowsContiguous ? kThreads / 32 * 512 : 1];
     pdl_launch_dependents();
     pdl_wait_prior();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t kblocks = fp4_kblocks(p.k, FMT);
+    const uint32_t kblocks = static_cast<uint32_t>(fp4_kblocks(p.k, FMT));
     const int pieces = static_cast<int>((p.k + 511) / 512);
     const int steps = (pieces + U - 1) / U;
     int64_t row, sf_row;
@@ -106,34 +106,32 @@ __global__ void __launch_bounds__(kThreads) fp4_cast_kernel(const Fp4CastArgs p)
     const Fp4Tensor tn = fp4_tensor(p.tscale);
     uint8_t* q = p.q + row * p.ldq;
     uint8_t* sf = p.sf + (sf_row >> 7) * kblocks * kFp4SfBlock + (sf_row & 31) * 16 + ((sf_row >> 5) & 3) * 4;
+    const uint32_t k = static_cast<uint32_t>(p.k);
     for (int step = blockIdx.y; step < steps; step += gridDim.y) {
+        const uint32_t c0 = static_cast<uint32_t>(step) * (U * 512u) + lane * 16u;
         Raw16<T> raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t c = static_cast<int64_t>(step * U + u) * 512 + lane * 16;
-            if constexpr (ROWS == kRowsContiguous) load_piece(raw[u], xr, c - lane * 16, p.k, s_buf + warp * 512);
-            else if (c >= p.k) raw[u].zero();
-            else if (ROWS == kRowsVec && c + 16 <= p.k) raw[u].load(xr + c);
-            else raw[u].load_some(xr + c * p.sxk, p.sxk, static_cast<int>(p.k - c < 16 ? p.k - c : 16));
+            const uint32_t c = c0 + u * 512u;
+            if constexpr (ROWS == kRowsContiguous) load_piece(raw[u], xr, c - lane * 16, k, s_buf + warp * 512);
+            else if (c >= k) raw[u].zero();
+            else if (ROWS == kRowsVec && c + 16 <= k) raw[u].load(xr + c);
+            else raw[u].load_some(xr + c * p.sxk, p.sxk, static_cast<int>(k - c < 16 ? k - c : 16));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t c = static_cast<int64_t>(step * U + u) * 512 + lane * 16;
+            const uint32_t c = c0 + u * 512u;
             float amax = raw[u].amax();
             if constexpr (FMT == kFp4Mx) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             const Fp4Scale g = fp4_scale<FMT>(amax, tn);
             uint64_t v[8];
             raw[u].values(v);
             const uint2 codes = fp4_codes16<FMT>(v, g);
-            if (c < p.k) *reinterpret_cast<uint2*>(q + (c >> 1)) = codes;
-            // the four bytes of a scale block's row
-            constexpr int lanes = FMT == kFp4Nv ? 1 : 2;           // lanes per group
-            const bool live = (c & ~static_cast<int64_t>(fp4_group(FMT) - 1)) < p.k;
-            uint32_t w = live ? g.byte << (8 * ((lane / lanes) & 3)) : 0u;
-            w |= __shfl_xor_sync(0xffffffffu, w, lanes);
-            w |= __shfl_xor_sync(0xffffffffu, w, 2 * lanes);
-            const int64_t kb = c / (4 * fp4_group(FMT));
-            if (lane % (4 * lanes) == 0 && kb < kblocks) *reinterpret_cast<uint32_t*>(sf + kb * kFp4SfBlock) = w;
+            if (c < k) *reinterpret_cast<uint2*>(q + (c >> 1)) = codes;
+            // the group's byte; the bytes of a block's row past the last group are zero
+            const uint32_t gi = c / fp4_group(FMT);
+            if ((FMT == kFp4Nv || (lane & 1) == 0) && (gi >> 2) < kblocks)
+                sf[static_cast<int64_t>(gi >> 2) * kFp4SfBlock + (gi & 3)] = c < k ? static_cast<uint8_t>(g.byte) : 0;
         }
     }
 }
