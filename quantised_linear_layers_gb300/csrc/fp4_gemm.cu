@@ -21,9 +21,9 @@
 // one row takes 7.6 cast inside and 8.8 with a launch for the cast, 8 rows 8.4
 // and 9.2, 16 rows 9.5 and 9.2, 64 rows 15.2 and 10.5.
 //
-// Roles (256 threads, 256 more with the cast): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
+// Roles (256 or 384 threads, 256 more with the cast): warp 0 TMA producer, warp 1 MMA issuer (tcgen05.cp of a
 // stage's scales into tensor memory, then up to four instructions of K = 64),
-// warps 4-7 epilogue. Tensor memory holds two accumulators and a scale slot for
+// four or eight epilogue warps from warp 4 on. Tensor memory holds two accumulators and a scale slot for
 // every stage of shared memory, so that a stage that has landed can be issued:
 // the instructions that read its slot before are those that freed it.
 #include <cuda.h>
@@ -42,7 +42,6 @@
 namespace ql {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kCastWarps = 8;                // a warp casts every eighth stage
 constexpr int TW = 128;
 constexpr int kMaxSplit = 8;
@@ -54,6 +53,9 @@ struct Cfg {
     static constexpr int kStageX = NT * 128;
     static constexpr int kStageSf = kWords * kFp4SfBlock;         // per operand
     static constexpr int kBytes = kStageW + kStageX + 2 * kStageSf;
+    // epilogue warps: two per lane quarter, each with half the rows, or one when there are 16
+    static constexpr int kEpiWarps = NT >= 64 ? 8 : 4;
+    static constexpr int kThreads = 128 + 32 * kEpiWarps;
     static constexpr int kSlot = 8 * kWords;                      // tensor-memory columns of a stage's scales
     static constexpr int kSfCol = NT < 32 ? 64 : 2 * NT;          // accumulators at 0 and NT
     static constexpr int kTmem = 512;
@@ -131,7 +133,7 @@ __device__ __forceinline__ void store_rows(const Fp4GemmParams& p, int64_t at, i
 // kAhead rows in flight.
 template <int NT, bool OUT_F32>
 __device__ __forceinline__ void sum_parts(uint32_t part, const Fp4GemmParams& p, const Fp4Tile& t, int rank, int split) {
-    constexpr int kAhead = 4, kRowsPer = kThreads / 32;
+    constexpr int kAhead = 4, kRowsPer = 4 + (NT >= 64 ? 8 : 4);
     const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
     const int c4 = (threadIdx.x & 31) * 4, col = t.col + c4;
     const int rows = t.rows < NT ? t.rows : NT;
@@ -211,7 +213,7 @@ __device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, in
 
 // T: void when X's codes are copied, else the type of X to cast.
 template <int NT, int FMT, bool OUT_F32, typename T>
-__global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads + 32 * kCastWarps, 1)
+__global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::value ? 0 : 32 * kCastWarps), 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_sfx, const __grid_constant__ CUtensorMap map_sfw,
                     const Fp4GemmParams p) {
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], kCast ? 2 : 1); mbar_init(&empty[s], 1); }
-        for (int s = 0; s < 2; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 128); }
+        for (int s = 0; s < 2; ++s) { mbar_init(&tfull[s], 1); mbar_init(&tempty[s], 32 * C::kEpiWarps); }
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
             mbar_wait_drain(done_bar, 0, p.wait_limit_ns);
         }
         __syncwarp();
-    } else if (warp >= 8) {
+    } else if (warp >= 4 + C::kEpiWarps) {
         if constexpr (kCast) {
             const Fp4Tensor tn = fp4_tensor(p.tx);
             uint32_t it = 0;
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
                 stages(lo, hi);
                 const int rows = t.rows < NT ? t.rows : NT;
                 for (int kb = lo; kb < hi; ++kb, ++it) {
-                    if (static_cast<int>(it % kCastWarps) != warp - 8) continue;
+                    if (static_cast<int>(it % kCastWarps) != warp - (4 + C::kEpiWarps)) continue;
                     const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
                     if (!warp_wait(&empty[s], ph ^ 1u, ctl)) { ok = false; break; }
                     cast_stage<T, FMT>(p, t.x_row, rows, kb * 256, smem + C::kOffX + s * C::kStageX,
@@ -376,9 +378,11 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
         __syncwarp();
     } else if (warp >= 4) {
         const int q = warp & 3;
+        constexpr int kPart = NT / (C::kEpiWarps / 4);               // rows of the tile this warp stores
+        const int part0 = (warp - 4) / 4 * kPart;
         const float alpha = (p.tx != nullptr ? __ldg(p.tx) : 1.0f) * (p.tw != nullptr ? __ldg(p.tw) : 1.0f);
         uint32_t tc = 0;
-        for (int i = first; walk.get(i, p, s_off, t); i += step) {
+        for (int n = first; walk.get(n, p, s_off, t); n += step) {
             int lo, hi;
             stages(lo, hi);
             const bool any = hi > lo;
@@ -392,7 +396,8 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
             const int rows = t.rows < NT ? t.rows : NT;
             float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-            for (int c0 = 0; c0 < NT; c0 += 16) {
+            for (int i = 0; i < kPart; i += 16) {
+                const int c0 = part0 + i;
                 if (c0 >= rows) break;
                 uint32_t r[16];
                 if (any) {
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? kThreads : kThreads +
         __syncwarp();
         cluster_sync_all();
         Fp4Walk<NT, TW> again;
-        if (warp < 8 && again.get(first, p, s_off, t) && !*abort_flag)
+        if (warp < 4 + C::kEpiWarps && again.get(first, p, s_off, t) && !*abort_flag)
             sum_parts<NT, OUT_F32>(smem_addr(smem), p, t, rank, split);
         __syncwarp();
         cluster_sync_all();
@@ -473,7 +478,7 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     const int64_t most = split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(most * split), 1, 1);
-    cfg.blockDim = dim3(kCast ? kThreads + 32 * kCastWarps : kThreads, 1, 1);
+    cfg.blockDim = dim3(C::kThreads + (kCast ? 32 * kCastWarps : 0), 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
