@@ -14,6 +14,10 @@
 // each a part of K; the fp32 partial tiles meet in shared memory, and each CTA
 // sums and stores its share of the rows in the CTAs' order.
 //
+// (Storing the partial rows straight into their owner's shared memory, with an
+// mbarrier in place of the first cluster barrier, was slower: 64 x 4096 x 7168
+// 8.6 us against 7.8.)
+//
 // Up to 8 rows of X (kFp4CastRows) can come as they are, bf16 or fp32: eight
 // more warps then cast them into the stages, a warp taking every eighth stage,
 // and the call is a single launch. Every CTA repeats the cast of its part of K
@@ -44,7 +48,6 @@ namespace {
 
 constexpr int kCastWarps = 8;                // a warp casts every eighth stage
 constexpr int TW = 128;
-constexpr int kMaxSplit = 8;
 
 template <int NT, int FMT>
 struct Cfg {
@@ -211,8 +214,9 @@ __device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, in
     }
 }
 
-// T: void when X's codes are copied, else the type of X to cast.
-template <int NT, int FMT, bool OUT_F32, typename T>
+// T: void when X's codes are copied, else the type of X to cast. SPLIT: a
+// cluster of CTAs per tile, one tile per cluster.
+template <int NT, int FMT, bool OUT_F32, typename T, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::value ? 0 : 32 * kCastWarps), 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_sfx, const __grid_constant__ CUtensorMap map_sfw,
@@ -231,9 +235,10 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
     int* s_off = reinterpret_cast<int*>(smem + C::kOffOff);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = static_cast<int>(cluster_nctarank());
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int first = static_cast<int>(cluster_id_x()), step = static_cast<int>(num_clusters_x());
+    const int split = SPLIT ? static_cast<int>(cluster_nctarank()) : 1;
+    const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first = SPLIT ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+    const int step = SPLIT ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) { mbar_init(&full[s], kCast ? 2 : 1); mbar_init(&empty[s], 1); }
@@ -394,7 +399,6 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
             }
             const int col = t.col + q * 32 + lane;
             const int rows = t.rows < NT ? t.rows : NT;
-            float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
             for (int i = 0; i < kPart; i += 16) {
                 const int c0 = part0 + i;
@@ -407,7 +411,8 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = 0u;
                 }
-                if (split > 1) {
+                if constexpr (SPLIT) {
+                    float* part = reinterpret_cast<float*>(smem);      // the operand ring, done with
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[(c0 + j) * TW + q * 32 + lane] = __uint_as_float(r[j]);
                 } else if (col < p.n) {
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
             if (any) mbar_arrive(&tempty[as]);
         }
     }
-    if (split > 1) {
+    if constexpr (SPLIT) {
         // one tile per cluster: the partial tiles are in every CTA's shared memory
         __syncwarp();
         cluster_sync_all();
@@ -436,24 +441,34 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
     }
 }
 
-template <int NT, int FMT, bool OUT_F32, typename T = void>
-cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
+// CTAs per tile of a plain product. A cluster costs about as much as some
+// stages of K (measured on 1 x 1024, 64 x 1024 and 128 x 1024 columns with K
+// from 512 to 4096, where a stage takes 0.23 us); the cheapest of 1, 2, 4 and 8
+// that fit on the SMs is taken. In tenths of a stage.
+template <int NT>
+int choose_split(int64_t tiles, int64_t kb, int num_sms) {
+    constexpr int cost[4] = {0, NT <= 16 ? 43 : (NT <= 64 ? 64 : 94), NT <= 16 ? 51 : (NT <= 64 ? 72 : 115),
+                             NT <= 16 ? 51 : (NT <= 64 ? 85 : 149)};
+    int best = 1;
+    int64_t least = 10 * kb;
+    for (int i = 1, s = 2; i < 4 && tiles * s <= num_sms && s <= kb; ++i, s *= 2) {
+        const int64_t c = 10 * ((kb + s - 1) / s) + cost[i];
+        if (c < least) {
+            least = c;
+            best = s;
+        }
+    }
+    return best;
+}
+
+template <int NT, int FMT, bool OUT_F32, typename T, bool SPLIT>
+cudaError_t launch_s(const Fp4GemmArgs& a, Fp4GemmParams& p, int64_t tiles, int split, cudaStream_t st, int num_sms) {
     using C = Cfg<NT, FMT>;
-    Fp4GemmParams p{};
-    fp4_fill_params(a, p);
-    p.tiles_x = static_cast<int>((a.m + NT - 1) / NT);
-    p.tiles_w = static_cast<int>((a.n + TW - 1) / TW);
-    p.group_x = 16;
-    p.vec_store = (reinterpret_cast<uintptr_t>(a.d) & 7u) == 0 && a.ldd % 4 == 0;
+    constexpr bool kCast = !std::is_void<T>::value;
     CUtensorMap mx, mw, msx, msw;
     const int64_t kbytes = (a.k + 1) / 2;
     const int64_t we = a.form == kFp4RagRows ? a.experts : 1;
-    constexpr bool kCast = !std::is_void<T>::value;
     if constexpr (kCast) {
-        p.xr = a.xr;
-        p.sxr = a.sxr;
-        p.k = static_cast<int>(a.k);
-        p.xr_vec = (reinterpret_cast<uintptr_t>(a.xr) & 15u) == 0 && (a.sxr * (a.xr_bf16 ? 2 : 4)) % 16 == 0;
         mx = msx = CUtensorMap{};
     } else if (!fp4_codes_map(&mx, a.x, a.m, kbytes, a.ldx, NT) ||
                !fp4_scales_map(&msx, a.sfx, a.x_row_blocks * p.kblocks, a.fmt)) {
@@ -462,22 +477,13 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     if (!fp4_codes_map(&mw, a.w, a.n * we, kbytes, a.ldw, TW) ||
         !fp4_scales_map(&msw, a.sfw, we * p.w_row_blocks * p.kblocks, a.fmt))
         return cudaErrorInvalidValue;
-    auto kern = fp4_gemm_kernel<NT, FMT, OUT_F32, T>;
+    auto kern = fp4_gemm_kernel<NT, FMT, OUT_F32, T, SPLIT>;
     if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::kSmem); e != cudaSuccess) return e;
-    int64_t tiles = static_cast<int64_t>(p.tiles_x) * p.tiles_w;
-    if (a.form == kFp4RagRows) tiles = (a.m / NT + (a.experts < a.m ? a.experts : a.m)) * p.tiles_w;
-    if (a.form == kFp4RagK) tiles *= a.experts;
-    int split = 1;
-    if (a.form == kFp4Plain) {
-        const int64_t kb = (a.k + 255) / 256;
-        while (split < kMaxSplit && tiles * split * 2 <= num_sms && kb >= split * 4) split *= 2;
-    }
+    const int64_t grid = SPLIT ? tiles * split : (tiles < num_sms ? tiles : num_sms);
     // at most 64 MB of W ahead over the grid, well inside L2
-    const int64_t grid = (split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms)) * split;
     p.ahead = static_cast<int>((int64_t(64) << 20) / (grid * C::kStageW));
-    const int64_t most = split > 1 ? tiles : (tiles < num_sms ? tiles : num_sms);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(most * split), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(C::kThreads + (kCast ? 32 * kCastWarps : 0), 1, 1);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
@@ -489,8 +495,32 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
+    cfg.numAttrs = SPLIT ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, mx, mw, msx, msw, p);
+}
+
+template <int NT, int FMT, bool OUT_F32, typename T = void>
+cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
+    Fp4GemmParams p{};
+    fp4_fill_params(a, p);
+    p.tiles_x = static_cast<int>((a.m + NT - 1) / NT);
+    p.tiles_w = static_cast<int>((a.n + TW - 1) / TW);
+    p.group_x = 16;
+    p.vec_store = (reinterpret_cast<uintptr_t>(a.d) & 7u) == 0 && a.ldd % 4 == 0;
+    if constexpr (!std::is_void<T>::value) {
+        p.xr = a.xr;
+        p.sxr = a.sxr;
+        p.k = static_cast<int>(a.k);
+        p.xr_vec = (reinterpret_cast<uintptr_t>(a.xr) & 15u) == 0 && (a.sxr * (a.xr_bf16 ? 2 : 4)) % 16 == 0;
+    }
+    int64_t tiles = static_cast<int64_t>(p.tiles_x) * p.tiles_w;
+    if (a.form == kFp4Plain) {
+        const int split = choose_split<NT>(tiles, (a.k + 255) / 256, num_sms);
+        if (split > 1) return launch_s<NT, FMT, OUT_F32, T, true>(a, p, tiles, split, st, num_sms);
+    }
+    if (a.form == kFp4RagRows) tiles = (a.m / NT + (a.experts < a.m ? a.experts : a.m)) * p.tiles_w;
+    if (a.form == kFp4RagK) tiles *= a.experts;
+    return launch_s<NT, FMT, OUT_F32, T, false>(a, p, tiles, 1, st, num_sms);
 }
 
 template <int NT>
