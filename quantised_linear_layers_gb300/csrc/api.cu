@@ -608,7 +608,10 @@ ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k
     if (x == nullptr && m > 0 && k > 0) return QL_ERR_INVALID_ARG;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
-    return from_cuda(ql::launch_fp4_tensor_scale(x, x_dtype == QL_BF16, m, k, x_stride_m, x_stride_k, scale,
+    ql::Bounds bnd{};
+    bnd.s[0] = ql::span_of(x, x_dtype == QL_BF16 ? 2 : 4, m, x_stride_m, k, x_stride_k);
+    bnd.status = di.status;
+    return from_cuda(ql::launch_fp4_tensor_scale(x, x_dtype == QL_BF16, m, k, x_stride_m, x_stride_k, scale, bnd,
                                                  reinterpret_cast<cudaStream_t>(stream), di.num_sms));
 }
 
@@ -651,7 +654,11 @@ ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, in
     a.offsets = offsets;
     a.num_experts = experts;
     a.sf_row_blocks = offsets != nullptr ? fp4_row_blocks(m, experts) : batch * ((m + 127) / 128);
-    a.dev_status = di.status;
+    a.bnd.s[0] = ql::span_of(x, a.is_bf16 ? 2 : 4, batch, x_stride_b, m, x_stride_m, k, x_stride_k);
+    a.bnd.s[1] = ql::span_of(q, 1, a.m, ldq, ldq, 1);
+    a.bnd.s[2] = ql::span_of(sf, 1, a.sf_row_blocks * ql::fp4_kblocks(k, fmt) * ql::kFp4SfBlock, 1);
+    a.bnd.s[3] = ql::span_of(offsets, 4, experts + 1, 1);
+    a.bnd.status = di.status;
     if (own_scale)
         if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, x_stride_k, scale, stream);
             s != QL_OK)
@@ -702,7 +709,13 @@ ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t 
     a.offsets = offsets;
     a.num_experts = experts;
     a.kpad = kpad;
-    a.dev_status = di.status;
+    a.bnd.s[0] = ql::span_of(x, a.is_bf16 ? 2 : 4, batch, x_stride_b, m, x_stride_m, k, 1);
+    a.bnd.s[1] = ql::span_of(q_rows, 1, batch * m, ldr, ldr, 1);
+    a.bnd.s[2] = ql::span_of(sf_rows, 1, batch * a.ssrb, 1);
+    a.bnd.s[3] = ql::span_of(offsets, 4, experts + 1, 1);
+    a.bnd.s[4] = ql::span_of(q_cols, 1, batch * k, ldc, ldc, 1);
+    a.bnd.s[5] = ql::span_of(sf_cols, 1, batch * a.sscb, 1);
+    a.bnd.status = di.status;
     if (own_scale)
         if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, 1, scale, stream); s != QL_OK)
             return s;
@@ -730,7 +743,10 @@ ql_status fp4_dequant(const uint8_t* q, int64_t ldq, const uint8_t* sf, int fmt,
     a.out = out;
     a.out_bf16 = out_dtype == QL_BF16;
     a.ldo = ldo;
-    a.dev_status = di.status;
+    a.bnd.s[0] = ql::span_of(out, a.out_bf16 ? 2 : 4, m, ldo, k, 1);
+    a.bnd.s[1] = ql::span_of(q, 1, m, ldq, ldq, 1);
+    a.bnd.s[2] = ql::span_of(sf, 1, fp4_scale_bytes(m, k, fmt, 0), 1);
+    a.bnd.status = di.status;
     return from_cuda(ql::launch_fp4_dequant(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
 }
 

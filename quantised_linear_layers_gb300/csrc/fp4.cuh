@@ -56,7 +56,7 @@ struct Fp4CastArgs {
     const int32_t* offsets;    // row ranges of the experts (num_experts + 1), or null
     int num_experts;
     int64_t sf_row_blocks;     // blocks of 128 rows in sf
-    uint32_t* dev_status;
+    Bounds bnd;                // x, row codes, row scales, offsets, column codes, column scales
 };
 
 // Casts of x along its rows and along its columns from one read.
@@ -79,7 +79,7 @@ struct Fp4DualArgs {
     int num_experts;
     int64_t sfr_row_blocks;    // 128-row blocks in sfr (experts: one more per expert)
     int64_t kpad;              // columns the column cast's codes have room for
-    uint32_t* dev_status;
+    Bounds bnd;                // x, row codes, row scales, offsets, column codes, column scales
 };
 
 struct Fp4DequantArgs {
@@ -92,14 +92,14 @@ struct Fp4DequantArgs {
     void* out;
     bool out_bf16;
     int64_t ldo;
-    uint32_t* dev_status;
+    Bounds bnd;                // out, codes, scales
 };
 
 cudaError_t launch_fp4_cast(const Fp4CastArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_cast_dual(const Fp4DualArgs& a, cudaStream_t st);
 cudaError_t launch_fp4_dequant(const Fp4DequantArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int64_t k, int64_t sxm, int64_t sxk, float* t,
-                            cudaStream_t st, int num_sms);
+                                    const Bounds& bnd, cudaStream_t st, int num_sms);
 
 #ifdef __CUDACC__
 // Larger of two magnitudes; a NaN operand gives NaN. The bf16 form takes two
@@ -255,19 +255,20 @@ struct Raw16;
 template <>
 struct Raw16<__nv_bfloat16> {
     uint4 u[2];
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, const Bounds& b, int i) {
+        if (!QL_IN(b, i, p, 32)) return zero();
         u[0] = __ldg(reinterpret_cast<const uint4*>(p));
         u[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0, 0, 0, 0); }
     // element by element, `n` of them (0 .. 16), `s` elements apart
-    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int64_t s, int n) {
+    __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int64_t s, int n, const Bounds& b, int bi) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t lo = 0, hi = 0;
-            if (2 * i < n) lo = __bfloat16_as_ushort(p[(2 * i) * s]);
-            if (2 * i + 1 < n) hi = __bfloat16_as_ushort(p[(2 * i + 1) * s]);
+            if (2 * i < n && QL_IN(b, bi, p + (2 * i) * s, 2)) lo = __bfloat16_as_ushort(p[(2 * i) * s]);
+            if (2 * i + 1 < n && QL_IN(b, bi, p + (2 * i + 1) * s, 2)) hi = __bfloat16_as_ushort(p[(2 * i + 1) * s]);
             w[i] = lo | (hi << 16);
         }
         u[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -287,7 +288,8 @@ struct Raw16<__nv_bfloat16> {
 template <>
 struct Raw16<float> {
     float f[16];
-    __device__ __forceinline__ void load(const float* p) {
+    __device__ __forceinline__ void load(const float* p, const Bounds& b, int bi) {
+        if (!QL_IN(b, bi, p, 64)) return zero();
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(f + 4 * i) = __ldg(reinterpret_cast<const float4*>(p) + i);
     }
@@ -295,9 +297,9 @@ struct Raw16<float> {
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = 0.0f;
     }
-    __device__ __forceinline__ void load_some(const float* p, int64_t s, int n) {
+    __device__ __forceinline__ void load_some(const float* p, int64_t s, int n, const Bounds& b, int bi) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = i < n ? p[i * s] : 0.0f;
+        for (int i = 0; i < 16; ++i) f[i] = i < n && QL_IN(b, bi, p + i * s, 4) ? p[i * s] : 0.0f;
     }
     __device__ __forceinline__ float amax() const {
         float m = 0.0f;

@@ -24,14 +24,14 @@ constexpr int kThreads = 256;
 
 // Position of `row` among the experts' 128-row scale blocks: its row in the
 // padded order, or -1 if no expert has it. The whole warp calls it.
-__device__ __forceinline__ int64_t expert_sf_row(const int32_t* offsets, int experts, int64_t m, int64_t row) {
+__device__ __forceinline__ int64_t expert_sf_row(const int32_t* offsets, int experts, int64_t row, const Bounds& bnd) {
     const int lane = threadIdx.x & 31;
     int blocks = 0;             // blocks of the experts that end at or before the row
     int start = -1;
     for (int e0 = 0; e0 < experts; e0 += 32) {
         const int e = e0 + lane;
         int b = 0, s = -1;
-        if (e < experts) {
+        if (e < experts && QL_IN(bnd, 3, offsets + e, 8)) {
             const int64_t lo = __ldg(offsets + e), hi = __ldg(offsets + e + 1);
             if (hi <= row) b = static_cast<int>((hi - lo + 127) / 128);
             else if (lo <= row) s = static_cast<int>(lo);
@@ -53,13 +53,13 @@ constexpr int kRowsVec = 0, kRowsContiguous = 1, kRowsStrided = 2;
 // lane loading its own 16 columns one by one touches 32 lines per load:
 // 1003 x 4099 fp32 took 21 us instead of 7.)
 template <typename T>
-__device__ __forceinline__ void load_piece(Raw16<T>& raw, const T* row, int64_t c0, int64_t k, T* buf) {
+__device__ __forceinline__ void load_piece(Raw16<T>& raw, const T* row, int64_t c0, int64_t k, T* buf, const Bounds& bnd) {
     const int lane = threadIdx.x & 31;
     T v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int64_t c = c0 + i * 32 + lane;
-        v[i] = c < k ? row[c] : T(0.0f);
+        v[i] = c < k && QL_IN(bnd, 0, row + c, sizeof(T)) ? row[c] : T(0.0f);
     }
     __syncwarp();
 #pragma unroll
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) fp4_cast_ker
     const T* xr = static_cast<const T*>(p.x);
     if (p.offsets != nullptr) {
         row = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-        sf_row = row < p.m ? expert_sf_row(p.offsets, p.num_experts, p.m, row) : -1;
+        sf_row = row < p.m ? expert_sf_row(p.offsets, p.num_experts, row, p.bnd) : -1;
         if (sf_row < 0 || (sf_row >> 7) >= p.sf_row_blocks) return;
         xr += row * p.sxm;
     } else {
@@ -113,10 +113,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) fp4_cast_ker
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t c = c0 + u * 512u;
-            if constexpr (ROWS == kRowsContiguous) load_piece(raw[u], xr, c - lane * 16, k, s_buf + warp * 512);
+            if constexpr (ROWS == kRowsContiguous) load_piece(raw[u], xr, c - lane * 16, k, s_buf + warp * 512, p.bnd);
             else if (c >= k) raw[u].zero();
-            else if (ROWS == kRowsVec && c + 16 <= k) raw[u].load(xr + c);
-            else raw[u].load_some(xr + c * p.sxk, p.sxk, static_cast<int>(k - c < 16 ? k - c : 16));
+            else if (ROWS == kRowsVec && c + 16 <= k) raw[u].load(xr + c, p.bnd, 0);
+            else raw[u].load_some(xr + c * p.sxk, p.sxk, static_cast<int>(k - c < 16 ? k - c : 16), p.bnd, 0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -127,11 +127,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) fp4_cast_ker
             uint64_t v[8];
             raw[u].values(v);
             const uint2 codes = fp4_codes16<FMT>(v, g);
-            if (c < k) *reinterpret_cast<uint2*>(q + (c >> 1)) = codes;
+            if (c < k && QL_IN(p.bnd, 1, q + (c >> 1), 8)) *reinterpret_cast<uint2*>(q + (c >> 1)) = codes;
             // the group's byte; the bytes of a block's row past the last group are zero
             const uint32_t gi = c / fp4_group(FMT);
-            if ((FMT == kFp4Nv || (lane & 1) == 0) && (gi >> 2) < kblocks)
-                sf[static_cast<int64_t>(gi >> 2) * kFp4SfBlock + (gi & 3)] = c < k ? static_cast<uint8_t>(g.byte) : 0;
+            uint8_t* dst = sf + static_cast<int64_t>(gi >> 2) * kFp4SfBlock + (gi & 3);
+            if ((FMT == kFp4Nv || (lane & 1) == 0) && (gi >> 2) < kblocks && QL_IN(p.bnd, 2, dst, 1))
+                *dst = c < k ? static_cast<uint8_t>(g.byte) : 0;
         }
     }
 }
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
         int64_t left = blockIdx.y, blk = 0, prev = 0;
         s_rows = -1;
         for (int e = 0; e < p.num_experts; ++e) {
+            if (!QL_IN(p.bnd, 3, p.offsets + e, 8)) break;
             int64_t lo = __ldg(p.offsets + e), hi = __ldg(p.offsets + e + 1);
             lo = lo < prev ? prev : (lo > p.m ? p.m : lo);
             hi = hi < lo ? lo : (hi > p.m ? p.m : hi);
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
         const int c = tid & 127;
 #pragma unroll 8
         for (int r = tid >> 7; r < 128; r += kThreads / 128)
-            tile[r * pitch + c] = (r < rows && c < cols) ? x[r * p.sxm + c] : T(0.0f);
+            tile[r * pitch + c] = (r < rows && c < cols && QL_IN(p.bnd, 0, x + r * p.sxm + c, sizeof(T))) ? x[r * p.sxm + c] : T(0.0f);
         __syncthreads();
     }
     {
@@ -223,8 +225,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
                 for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) reinterpret_cast<uint4*>(&raw[i])[j] = src[j];
             } else {
                 if (r >= rows || c >= cols) raw[i].zero();
-                else if (c + 16 <= cols) raw[i].load(x + r * p.sxm + c);
-                else raw[i].load_some(x + r * p.sxm + c, 1, cols - c);
+                else if (c + 16 <= cols) raw[i].load(x + r * p.sxm + c, p.bnd, 0);
+                else raw[i].load_some(x + r * p.sxm + c, 1, cols - c, p.bnd, 0);
             }
         }
 #pragma unroll
@@ -242,8 +244,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
                 uint64_t v[8];
                 raw[i].values(v);
                 const uint2 codes = fp4_codes16<FMT>(v, g);
-                if (r < rows && cg * 16 < cols)
-                    *reinterpret_cast<uint2*>(p.qr + bz * p.sqrb + (row0 + r) * p.ldr + ((c0 + cg * 16) >> 1)) = codes;
+                uint8_t* dst = p.qr + bz * p.sqrb + (row0 + r) * p.ldr + ((c0 + cg * 16) >> 1);
+                if (r < rows && cg * 16 < cols && QL_IN(p.bnd, 1, dst, 8)) *reinterpret_cast<uint2*>(dst) = codes;
                 const int gi = FMT == kFp4Nv ? cg : cg >> 1;
                 const bool live = gi * fp4_group(FMT) < cols && r < rows;
                 if (FMT == kFp4Nv || (cg & 1) == 0)
@@ -319,24 +321,24 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int u = i * kThreads + tid, col = u >> 2, part = u & 3;
-        if (col < cols)
-            *reinterpret_cast<uint4*>(p.qc + bz * p.sqcb + (c0 + col) * p.ldc + (kcol >> 1) + part * 16) =
-                *reinterpret_cast<const uint4*>(smem + S::kOffCol + col * S::kColPitch + part * 16);
+        uint8_t* dst = p.qc + bz * p.sqcb + (c0 + col) * p.ldc + (kcol >> 1) + part * 16;
+        if (col < cols && QL_IN(p.bnd, 4, dst, 16))
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(smem + S::kOffCol + col * S::kColPitch + part * 16);
     }
     // scale blocks
     const int64_t kblocks_c = fp4_kblocks(p.offsets != nullptr ? p.kpad : p.m, FMT);
     if (tid < kWords * 32) {
         const int wd = tid >> 5, l = tid & 31;
         const int64_t kb = kcol / (4 * fp4_group(FMT)) + wd;
-        if (kb < kblocks_c)
-            *reinterpret_cast<uint4*>(p.sfc + bz * p.sscb + (static_cast<int64_t>(blockIdx.x) * kblocks_c + kb) * kFp4SfBlock + l * 16) =
-                *reinterpret_cast<const uint4*>(smem + S::kOffSfc + wd * kFp4SfBlock + l * 16);
+        uint8_t* dst = p.sfc + bz * p.sscb + (static_cast<int64_t>(blockIdx.x) * kblocks_c + kb) * kFp4SfBlock + l * 16;
+        if (kb < kblocks_c && QL_IN(p.bnd, 5, dst, 16))
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(smem + S::kOffSfc + wd * kFp4SfBlock + l * 16);
     } else if (tid >= 128 && tid < 128 + kWords * 32 && p.qr != nullptr && sfblk >= 0 && sfblk < p.sfr_row_blocks) {
         const int wd = (tid - 128) >> 5, l = tid & 31;
         const int64_t kb = c0 / (4 * fp4_group(FMT)) + wd;
-        if (kb < kblocks_r)
-            *reinterpret_cast<uint4*>(p.sfr + bz * p.ssrb + (sfblk * kblocks_r + kb) * kFp4SfBlock + l * 16) =
-                *reinterpret_cast<const uint4*>(smem + S::kOffSfr + wd * kFp4SfBlock + l * 16);
+        uint8_t* dst = p.sfr + bz * p.ssrb + (sfblk * kblocks_r + kb) * kFp4SfBlock + l * 16;
+        if (kb < kblocks_r && QL_IN(p.bnd, 2, dst, 16))
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(smem + S::kOffSfr + wd * kFp4SfBlock + l * 16);
     }
 }
 
@@ -386,8 +388,9 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantA
         for (int u = 0; u < U; ++u) {
             const int64_t c = static_cast<int64_t>(step * U + u) * 512 + lane * 16;
             const int64_t g = c / fp4_group(FMT);
-            codes[u] = c < p.k ? __ldg(reinterpret_cast<const uint2*>(q + (c >> 1))) : make_uint2(0, 0);
-            b[u] = c < p.k ? __ldg(sf + (g >> 2) * kFp4SfBlock + (g & 3)) : 0u;
+            const uint8_t* sb = sf + (g >> 2) * kFp4SfBlock + (g & 3);
+            codes[u] = c < p.k && QL_IN(p.bnd, 1, q + (c >> 1), 8) ? __ldg(reinterpret_cast<const uint2*>(q + (c >> 1))) : make_uint2(0, 0);
+            b[u] = c < p.k && QL_IN(p.bnd, 2, sb, 1) ? __ldg(sb) : 0u;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -418,12 +421,13 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantA
             }
             if (VEC && c + 16 <= p.k) {
 #pragma unroll
-                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j) reinterpret_cast<uint4*>(out + c)[j] = o[j];
+                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j)
+                    if (QL_IN(p.bnd, 0, reinterpret_cast<uint4*>(out + c) + j, 16)) reinterpret_cast<uint4*>(out + c)[j] = o[j];
             } else if (VEC) {
                 const T* e = reinterpret_cast<const T*>(o);
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (c + j < p.k) out[c + j] = e[j];
+                    if (c + j < p.k && QL_IN(p.bnd, 0, out + c + j, sizeof(T))) out[c + j] = e[j];
             } else {
                 T* buf = s_buf + warp * 512;
                 __syncwarp();
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantA
                 const int64_t c0 = c - lane * 16 + lane;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    if (c0 + j * 32 < p.k) out[c0 + j * 32] = buf[j * 32 + lane];
+                    if (c0 + j * 32 < p.k && QL_IN(p.bnd, 0, out + c0 + j * 32, sizeof(T))) out[c0 + j * 32] = buf[j * 32 + lane];
             }
         }
     }
@@ -450,7 +454,7 @@ constexpr int kClusterThreads = 1024;
 
 template <typename T, int ROWS, bool CLUSTER>
 __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kThreads) fp4_tscale_kernel(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
-                                                              uint32_t* tscale) {
+                                                              uint32_t* tscale, const Bounds bnd) {
     pdl_launch_dependents();
     pdl_wait_prior();
     constexpr int kBlock = CLUSTER ? kClusterThreads : kThreads;
@@ -463,8 +467,8 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kThreads) fp4_tsca
         for (int64_t i = first; i < m * per_row; i += stride) {
             const int64_t row = m == 1 ? 0 : i / per_row, c = (i - row * per_row) * 16;
             Raw16<T> raw;
-            if (c + 16 <= k) raw.load(x + row * sxm + c);
-            else raw.load_some(x + row * sxm + c, 1, static_cast<int>(k - c));
+            if (c + 16 <= k) raw.load(x + row * sxm + c, bnd, 0);
+            else raw.load_some(x + row * sxm + c, 1, static_cast<int>(k - c), bnd, 0);
             best = max_nan(best, raw.amax());
         }
     } else {
@@ -476,7 +480,10 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kThreads) fp4_tsca
             const int64_t row = i / per_row, c0 = (i - row * per_row) * kPiece + lane;
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = c0 + j * 32 < k ? static_cast<float>(x[row * sxm + (c0 + j * 32) * sxk]) : 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                const T* e = x + row * sxm + (c0 + j * 32) * sxk;
+                v[j] = c0 + j * 32 < k && QL_IN(bnd, 0, e, sizeof(T)) ? static_cast<float>(*e) : 0.0f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) best = max_nan(best, fabsf(v[j]));
         }
@@ -603,7 +610,7 @@ cudaError_t dequant_t(const Fp4DequantArgs& a, cudaStream_t st, int num_sms) {
 }
 
 template <typename T>
-cudaError_t tscale_t(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk, uint32_t* out, cudaStream_t st, int num_sms) {
+cudaError_t tscale_t(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk, uint32_t* out, const Bounds& bnd, cudaStream_t st, int num_sms) {
     if (sxk == 1 && sxm == k) {        // one long row: only its end is ragged
         k *= m;
         m = 1;
@@ -612,15 +619,15 @@ cudaError_t tscale_t(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
     const bool vec = vec_ok(x, sizeof(T), m > 1 ? sxm : 0, sxk, 0);
     // 2 MB, measured: one cluster 3.4 us and 3.1 us less host time than the zeroing and the atomics
     if (m * k * static_cast<int64_t>(sizeof(T)) <= (2 << 20)) {
-        return vec ? launch_cluster(fp4_tscale_kernel<T, kRowsVec, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out)
-                   : launch_cluster(fp4_tscale_kernel<T, kRowsStrided, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out);
+        return vec ? launch_cluster(fp4_tscale_kernel<T, kRowsVec, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out, bnd)
+                   : launch_cluster(fp4_tscale_kernel<T, kRowsStrided, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out, bnd);
     }
     if (cudaError_t e = cudaMemsetAsync(out, 0, 4, st); e != cudaSuccess) return e;
     int64_t grid = vec ? (m * ((k + 15) / 16) + kThreads - 1) / kThreads : (m * ((k + 255) / 256) + 7) / 8;
     if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
     const dim3 g(static_cast<unsigned>(grid < 1 ? 1 : grid));
-    return vec ? launch(fp4_tscale_kernel<T, kRowsVec, false>, g, 0, st, x, m, k, sxm, sxk, out)
-               : launch(fp4_tscale_kernel<T, kRowsStrided, false>, g, 0, st, x, m, k, sxm, sxk, out);
+    return vec ? launch(fp4_tscale_kernel<T, kRowsVec, false>, g, 0, st, x, m, k, sxm, sxk, out, bnd)
+               : launch(fp4_tscale_kernel<T, kRowsStrided, false>, g, 0, st, x, m, k, sxm, sxk, out, bnd);
 }
 
 }  // namespace
@@ -647,10 +654,10 @@ cudaError_t launch_fp4_dequant(const Fp4DequantArgs& a, cudaStream_t st, int num
 }
 
 cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int64_t k, int64_t sxm, int64_t sxk, float* t,
-                                    cudaStream_t st, int num_sms) {
+                                    const Bounds& bnd, cudaStream_t st, int num_sms) {
     uint32_t* out = reinterpret_cast<uint32_t*>(t);
-    if (is_bf16) return tscale_t(static_cast<const __nv_bfloat16*>(x), m, k, sxm, sxk, out, st, num_sms);
-    return tscale_t(static_cast<const float*>(x), m, k, sxm, sxk, out, st, num_sms);
+    if (is_bf16) return tscale_t(static_cast<const __nv_bfloat16*>(x), m, k, sxm, sxk, out, bnd, st, num_sms);
+    return tscale_t(static_cast<const float*>(x), m, k, sxm, sxk, out, bnd, st, num_sms);
 }
 
 }  // namespace ql

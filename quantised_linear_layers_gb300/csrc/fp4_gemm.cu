@@ -93,9 +93,10 @@ template <bool OUT_F32>
 __device__ __forceinline__ void store_one(const Fp4GemmParams& p, int64_t at, float v) {
     if constexpr (OUT_F32) {
         float* d = static_cast<float*>(p.d) + at;
-        *d = p.accumulate ? *d + v : v;
+        if (QL_IN(p.bnd, 0, d, 4)) *d = p.accumulate ? *d + v : v;
     } else {
-        static_cast<__nv_bfloat16*>(p.d)[at] = __float2bfloat16_rn(v);
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + at;
+        if (QL_IN(p.bnd, 0, d, 2)) *d = __float2bfloat16_rn(v);
     }
 }
 
@@ -114,14 +115,17 @@ __device__ __forceinline__ void store_rows(const Fp4GemmParams& p, int64_t at, i
             if (p.accumulate) {
                 const float* s = d;
 #pragma unroll
-                for (int j = 0; j < 16; ++j, s += p.ldd) v[j] += *s;
+                for (int j = 0; j < 16; ++j, s += p.ldd)
+                    if (QL_IN(p.bnd, 0, s, 4)) v[j] += *s;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j, d += p.ldd) *d = v[j];
+            for (int j = 0; j < 16; ++j, d += p.ldd)
+                if (QL_IN(p.bnd, 0, d, 4)) *d = v[j];
         } else {
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + at;
 #pragma unroll
-            for (int j = 0; j < 16; ++j, d += p.ldd) *d = __float2bfloat16_rn(v[j]);
+            for (int j = 0; j < 16; ++j, d += p.ldd)
+                if (QL_IN(p.bnd, 0, d, 2)) *d = __float2bfloat16_rn(v[j]);
         }
     } else {
 #pragma unroll
@@ -165,8 +169,8 @@ __device__ __forceinline__ void sum_parts(uint32_t part, const Fp4GemmParams& p,
             const float f[4] = {v[j].x * alpha, v[j].y * alpha, v[j].z * alpha, v[j].w * alpha};
             if (!OUT_F32 && p.vec_store && col + 4 <= p.n) {
                 const __nv_bfloat162 h0 = __floats2bfloat162_rn(f[0], f[1]), h1 = __floats2bfloat162_rn(f[2], f[3]);
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.d) + at) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+                if (QL_IN(p.bnd, 0, static_cast<__nv_bfloat16*>(p.d) + at, 8))
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.d) + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -192,8 +196,8 @@ __device__ __forceinline__ void cast_stage(const Fp4GemmParams& p, int x_row, in
         for (int i = 0; i < kAhead; ++i) {
             const int r = rb + 2 * i + (lane >> 4);
             if (r >= rows || c >= p.k) raw[i].zero();
-            else if (p.xr_vec && c + 16 <= p.k) raw[i].load(x + r * p.sxr + c);
-            else raw[i].load_some(x + r * p.sxr + c, 1, p.k - c < 16 ? p.k - c : 16);
+            else if (p.xr_vec && c + 16 <= p.k) raw[i].load(x + r * p.sxr + c, p.bnd, 2);
+            else raw[i].load_some(x + r * p.sxr + c, 1, p.k - c < 16 ? p.k - c : 16, p.bnd, 2);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -569,6 +573,12 @@ void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
     p.dev_status = a.dev_status;
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall_producer = a.stall_producer;
+    // what the kernels read and write with plain loads and stores
+    const int64_t drows = a.m * (a.form == kFp4RagK ? a.experts : 1);
+    p.bnd.s[0] = span_of(a.d, a.out_f32 ? 4 : 2, drows, a.ldd, a.n, 1);
+    p.bnd.s[1] = span_of(a.offsets, 4, a.experts + 1, 1);
+    p.bnd.s[2] = span_of(a.xr, a.xr_bf16 ? 2 : 4, a.m, a.sxr, a.k, 1);
+    p.bnd.status = a.dev_status;
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {

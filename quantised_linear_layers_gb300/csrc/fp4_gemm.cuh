@@ -76,6 +76,7 @@ struct Fp4GemmParams {
     const void* xr;              // X before the cast (the kernel's casting form)
     int64_t sxr;
     int k, xr_vec;               // columns; rows start on 16 bytes
+    Bounds bnd;                  // D, offsets, X before the cast
     int ahead;                   // stages of W brought into L2 before the previous kernel ends
 };
 
@@ -142,7 +143,7 @@ __device__ __forceinline__ void fp4_load_offsets(int* s_off, const Fp4GemmParams
     bool bad = false;
     for (int i0 = 0; i0 <= p.experts; i0 += 32) {
         const int i = i0 + lane;
-        int v = i <= p.experts ? __ldg(p.offsets + i) : 0;
+        int v = i <= p.experts && QL_IN(p.bnd, 1, p.offsets + i, 4) ? __ldg(p.offsets + i) : 0;
         const int raw = v;
         v = v < 0 ? 0 : (v > p.rows ? p.rows : v);
 #pragma unroll

@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_warp_rows(const float* acc, uint8_t* stg, 
 #pragma unroll 4
             for (int r = 0; r < rows; ++r, d += p.ldd) {
                 const float v = *reinterpret_cast<const float*>(stg + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-                if (in0) *d = p.accumulate ? *d + v : v;
+                if (in0 && QL_IN(p.bnd, 0, d, 4)) *d = p.accumulate ? *d + v : v;
             }
         } else {
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + at;
@@ -114,8 +114,8 @@ __device__ __forceinline__ void store_warp_rows(const float* acc, uint8_t* stg, 
                 const uint8_t* row = stg + r * 128 + (lane & 7) * 2;
                 const __nv_bfloat16 v0 = *reinterpret_cast<const __nv_bfloat16*>(row + (((lane >> 3) ^ (r & 7)) << 4));
                 const __nv_bfloat16 v1 = *reinterpret_cast<const __nv_bfloat16*>(row + (((4 + (lane >> 3)) ^ (r & 7)) << 4));
-                if (in0) d[0] = v0;
-                if (in1) d[32] = v1;
+                if (in0 && QL_IN(p.bnd, 0, d, 2)) d[0] = v0;
+                if (in1 && QL_IN(p.bnd, 0, d + 32, 2)) d[32] = v1;
             }
         }
         __syncwarp();
