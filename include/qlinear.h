@@ -555,7 +555,7 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
 /* The forward call: casts X [m, k] (bf16 or fp32, contiguous rows, row stride
  * x_stride_m) and multiplies, D [m, n] bf16 = X W^T, or by expert with offsets
  * (W [experts, n, k]). Equal to fp4_cast and gemm_fp4_nt / gemm_fp4_nt_ragged;
- * up to 8 rows are cast inside the product, in one launch and without a
+ * up to 8 rows (16 with experts) are cast inside the product, in one launch and without a
  * workspace. fp4_linear_workspace_size bytes of device memory, 16-byte aligned,
  * are needed otherwise (0: none); they may be reused once the stream is past
  * the call. */

@@ -832,7 +832,7 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
 }
 
 size_t fp4_linear_workspace_size(int64_t m, int64_t k, int fmt, int experts) {
-    if (m <= ql::kFp4CastRows || k <= 0 || (fmt != QL_FP4_NV && fmt != QL_FP4_MX)) return 0;
+    if (m <= ql::fp4_cast_rows(experts) || k <= 0 || (fmt != QL_FP4_NV && fmt != QL_FP4_MX)) return 0;
     return static_cast<size_t>(m) * ((k + 31) / 32 * 16) + static_cast<size_t>(fp4_scale_bytes(m, k, fmt, experts));
 }
 
@@ -844,7 +844,7 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
     if (x_dtype != QL_BF16 && x_dtype != QL_F32) return QL_ERR_INVALID_ARG;
     const int64_t ldq = (k + 31) / 32 * 16;
     uint8_t* q = static_cast<uint8_t*>(workspace);
-    if (m > ql::kFp4CastRows || m <= 0 || n <= 0 || k <= 0) {
+    if (m > ql::fp4_cast_rows(offsets != nullptr ? experts : 0) || m <= 0 || n <= 0 || k <= 0) {
         if (m > 0 && n > 0 && k > 0 && (workspace == nullptr ||
                                         workspace_bytes < fp4_linear_workspace_size(m, k, fmt, offsets ? experts : 0)))
             return QL_ERR_INVALID_ARG;

@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "bounds.cuh"
 #include "common.cuh"
 #include "fp4.cuh"
@@ -204,13 +206,23 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
     const int64_t kblocks_r = fp4_kblocks(p.k, FMT);
     constexpr int kWords = FMT == kFp4Nv ? 2 : 1;             // scale blocks across 128 columns
     if constexpr (ROWS != kRowsVec) {
-        // rows that start anywhere: one element per lane and load
-        T* tile = reinterpret_cast<T*>(smem);
-        constexpr int pitch = S::kPitch / sizeof(T);
+        // rows that start anywhere: one element per lane and load, kAhead loads in flight
+        using E = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+        E* tile = reinterpret_cast<E*>(smem);
+        constexpr int pitch = S::kPitch / sizeof(T), kAhead = 16, kRowStep = kThreads / 128;
         const int c = tid & 127;
-#pragma unroll 8
-        for (int r = tid >> 7; r < 128; r += kThreads / 128)
-            tile[r * pitch + c] = (r < rows && c < cols && QL_IN(p.bnd, 0, x + r * p.sxm + c, sizeof(T))) ? x[r * p.sxm + c] : T(0.0f);
+        const E* src = reinterpret_cast<const E*>(x) + (tid >> 7) * p.sxm + c;
+#pragma unroll 1
+        for (int r0 = tid >> 7; r0 < 128; r0 += kAhead * kRowStep) {
+            E v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i, src += kRowStep * p.sxm) {
+                v[i] = 0;
+                if (r0 + i * kRowStep < rows && c < cols && QL_IN(p.bnd, 0, src, sizeof(T))) v[i] = *src;
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) tile[(r0 + i * kRowStep) * pitch + c] = v[i];
+        }
         __syncthreads();
     }
     {

@@ -18,7 +18,7 @@
 // mbarrier in place of the first cluster barrier, was slower: 64 x 4096 x 7168
 // 8.6 us against 7.8.)
 //
-// Up to 8 rows of X (kFp4CastRows) can come as they are, bf16 or fp32: eight
+// Up to 8 rows of X, 16 with experts (fp4_cast_rows), can come as they are, bf16 or fp32: eight
 // more warps then cast them into the stages, a warp taking every eighth stage,
 // and the call is a single launch. Every CTA repeats the cast of its part of K
 // while its weights are on their way. At 4096 x 7168 (us, weights from HBM)

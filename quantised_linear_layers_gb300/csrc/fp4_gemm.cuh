@@ -42,7 +42,7 @@ struct Fp4GemmArgs {
     int64_t ldd;
     bool out_f32;
     int accumulate;
-    // X not cast yet (m <= kFp4CastRows): the product casts it itself
+    // X not cast yet (m <= fp4_cast_rows): the product casts it itself
     const void* xr;
     bool xr_bf16;
     int64_t sxr;                 // elements between its rows
@@ -80,8 +80,9 @@ struct Fp4GemmParams {
     int ahead;                   // stages of W brought into L2 before the previous kernel ends
 };
 
-// Largest m whose X the product casts itself.
-constexpr int kFp4CastRows = 8;
+// Largest m whose X the product casts itself: with experts each tile casts its
+// own expert's rows only, so that more rows in all are worth it.
+constexpr int64_t fp4_cast_rows(int experts) { return experts > 0 ? 16 : 8; }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);

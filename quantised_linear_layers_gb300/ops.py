@@ -586,7 +586,7 @@ def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = Non
     """The forward call, cast and product in one: D [m, n] bf16 = X W^T of
     x [m, k] (bf16 or fp32) and a cast W [n, k]; with ``offsets`` (int32
     [experts + 1]) by expert, W [experts, n, k]. Equal to ``fp4_cast`` followed by
-    ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 8 rows take one launch.
+    ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 8 rows (16 with experts) take one launch.
     ``x_scale`` as ``fp4_cast``'s tensor_scale."""
     return (_fp4 or _load_fp4()).linear(_contiguous_rows(x), w, x_scale, offsets, out)
 
