@@ -5,7 +5,9 @@
  * Two operations, each a CUDA kernel launched on the caller's stream:
  *   - the FP8 cast (per token in 1x128 / 1x32 groups, or per 128x128 block),
  *   - the block-scaled FP8 GEMM D = A * B^T (bf16 output for fwd/dgrad,
- *     fp32 output, optionally accumulated, for wgrad).
+ *     fp32 output, optionally accumulated, for wgrad);
+ * and both in microscaled 4-bit floating point, with experts of ragged loads
+ * (the last part of this header).
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller. The library
@@ -477,7 +479,8 @@ int ql_bounds_checked(void);
  *              exponent held in [-127, 127] and stored as UE8M0. No t.
  * E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and E4M3 are rounded to nearest,
  * ties to even; x / (s t) is correctly rounded first (t >= 2^-60). A group that
- * holds an infinity or a NaN is NaN in every product.
+ * holds an infinity or a NaN is NaN in every product, and so is one whose
+ * amax / (6 t) overflows fp32.
  *
  * Layouts:
  *   codes   bytes [rows][ld], element 2j in the low half of byte j; ld a

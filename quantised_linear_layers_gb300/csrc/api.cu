@@ -157,11 +157,24 @@ ql_status fp4_product(ql::Fp4GemmArgs& a, cudaStream_t st) {
     a.stall_producer = g_stall_producer.load();
     const int sms = effective_sms(di);
     const int path = g_gemm_path.load();
-    // 256 x 256 tiles on CTA pairs when there is one for every other pair of
-    // SMs; narrower tiles on one SM otherwise
-    const int64_t per = a.form == ql::kFp4RagRows ? (a.m / a.experts > 0 ? a.m / a.experts : 1) : a.m;
-    const int64_t tiles = ((per + 255) / 256) * ((a.n + 255) / 256) * (a.form == ql::kFp4Plain ? 1 : a.experts);
-    const bool pair = a.xr == nullptr && (path == 3 || (path != 2 && path != 4 && per > 128 && tiles >= sms / 4));
+    // CTA pairs (256 x 256 tiles) or one SM per tile (128 x 128 and narrower).
+    // Pairs need a tile for every other pair of SMs, and either enough of K or
+    // enough tiles to make up for their longer start and end; fp32 output, whose
+    // end is twice as long, needs both. Measured, single / pair in us:
+    //   bf16, 64 tiles (2048 x 2048): K 1024 6.1 / 7.3, 2048 8.0 / 8.5, 2560 9.0 / 9.1, 4096 12.1 / 10.8
+    //   bf16, 128 tiles (4096 x 2048): K 256 7.7 / 7.6, 1024 9.1 / 9.0, 2048 13.1 / 11.6
+    //   fp32, 40 tiles: K 2560 8.9 / 9.9, 4096 11.8 / 11.5; 256 tiles: K 1024 16.2 / 17.9, 2048 21.8 / 21.7;
+    //   512 tiles: K 512 25.0 / 27.1, 1024 30.4 / 28.1
+    //   experts' gradients, 8 x 4096 x 4096: 512 rows each 90 / 99; 8 x 4096 x 7168, 2048 rows each 271 / 224
+    // With experts the rows (or K) are an expert's on average; 128 rows each
+    // are one half of a pair's tile (8 x 4096 x 7168: 25 / 31).
+    const int64_t experts = a.form == ql::kFp4Plain ? 1 : a.experts;
+    const int64_t rows = a.form == ql::kFp4RagRows ? a.m / experts : a.m;
+    const int64_t k = a.form == ql::kFp4RagK ? a.rows / experts : a.k;
+    const int64_t tiles = ((rows + 255) / 256) * ((a.n + 255) / 256) * experts;
+    const bool few = tiles < sms * 4 / 5;
+    const int64_t least_k = a.out_f32 ? (few ? 3584 : (tiles < sms * 5 / 2 ? 2048 : 1024)) : (few ? 2560 : 0);
+    const bool pair = a.xr == nullptr && (path == 3 || (path != 2 && path != 4 && rows > 128 && tiles >= sms / 4 && k >= least_k));
     return from_cuda(pair ? ql::launch_fp4_gemm_pair(a, st, sms) : ql::launch_fp4_gemm(a, st, sms));
 }
 

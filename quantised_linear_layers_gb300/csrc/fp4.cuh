@@ -8,8 +8,9 @@
 //           for E2M1 * (s * t)
 //   kFp4Mx  32 elements, scale 2^p, p = ceil(log2(amax / 6)) held in
 //           [-127, 127] and stored as p + 127 (UE8M0)
-// A group with an infinity or a NaN gets the scale NaN (0x7F / 0xFF), so it is
-// NaN in every product and when it is read back, whatever its codes.
+// A group with an infinity or a NaN (or, nv, whose amax / (6 t) overflows) gets
+// the scale NaN (0x7F / 0xFF), so it is NaN in every product and when it is read
+// back, whatever its codes.
 //
 // Layouts. Codes: row-major bytes, element 2j in the low and 2j + 1 in the
 // high half of byte j; rows start on 16-byte boundaries; the unused half byte of an

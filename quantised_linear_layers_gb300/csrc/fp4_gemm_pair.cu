@@ -3,14 +3,18 @@
 //
 // X's rows are split over the pair (128 per CTA) and so are W's (128 of the
 // 256 columns of D per CTA); each CTA's tensor memory holds the scales of its
-// own X rows and of all W rows of the tile. A stage is 256 columns of K: 32 KB
-// of codes and 6 KB (nv) or 3 KB (mx) of scale blocks per CTA, against 512
-// cycles of the tensor core at its rate for K = 64 steps. At that rate the
-// bytes a stage brings into an SM are the tighter limit, hence the widest tile
-// that leaves tensor memory for the scales, with one accumulator; its
-// registers are read out in one go so that the next tile starts at once. Each
-// stage of shared memory has its scale slot in tensor memory (five of 48
-// columns beside the accumulator's 256).
+// own X rows and of all W rows of the tile, in a slot for every stage of shared
+// memory (five of 48 columns beside the accumulator's 256).
+//
+// What bounds it is an SM's shared memory at 128 bytes a cycle: a stage of 256
+// columns writes 38 KB (nv; mx 35) by TMA, and the instructions read 32 KB of
+// codes, the copies to tensor memory 6 KB (3) of scales: 608 cycles (560) for 512
+// of the tensor core. Hence the widest instruction and tile (256 x 256; halves of
+// 128 columns read X twice: 620 -> 700 us at 16384 x 18432 x 7168), with one
+// accumulator, whose registers are read out in one go so that the next tile
+// starts at once. Measured nv / mx: 8192 x 8192 x 7168 139 / 134 us (6.9 / 7.2
+// PFLOP/s), 16384 x 18432 x 7168 606 / 565 us in a short run, 662 / 603 under the
+// power cap; tensor pipe 79 / 81 % active.
 //
 // Roles (384 threads per CTA): warp 0 TMA producer, warp 1 of the leader MMA
 // issuer, warps 4-11 epilogue (32 rows x 128 columns of D each, staged in

@@ -176,6 +176,16 @@ def test_by_expert(ops, offs, fmt):
         at += n
 
 
+def test_a_scale_far_too_small(ops):
+    """amax / (6 t) beyond fp32 makes its group NaN and no other; beyond the largest group scale it saturates."""
+    x = torch.ones((2, 64), device="cuda")
+    x[0, 20], x[1, 40] = 1e30, 1e10
+    t = torch.tensor([2.0 ** -60], device="cuda")
+    got = np64(ops.fp4_dequant(ops.fp4_cast(x, 0, t), torch.float32))
+    assert np.isnan(got[0, 16:32]).all() and np.isfinite(got[0, :16]).all() and np.isfinite(got[0, 32:]).all()
+    assert got[1, 40] == 6 * 448 * 2.0 ** -60 and got[0, 0] == 6 * 448 * 2.0 ** -60
+
+
 @pytest.mark.parametrize("m,k", [(1, 1), (3, 33), (130, 520), (1031, 1031), (1024, 2048)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_own_scale(ops, m, k, dtype):
