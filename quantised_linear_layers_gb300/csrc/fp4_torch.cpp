@@ -117,8 +117,7 @@ Input input(PyObject* ox, int fmt, PyObject* oscale, PyObject* ooffsets) {
     in.sm = x.stride(-2);
     in.sk = x.stride(-1);
     in.code = dtype_code(x);
-    if (oscale != Py_None) {
-        if (fmt != QL_FP4_NV) value_error("only FP4_NV has a tensor scale");
+    if (oscale != Py_None && fmt == QL_FP4_NV) {        // FP4_MX has none and takes no notice of one
         if (oscale == g_own) {
             in.own = true;
             if (in.batch > 1 && in.sb != in.m * in.sm)
@@ -171,6 +170,7 @@ Room column_room(const Input& in, int fmt) {
 // FP4Tensor(buf, ld, scale, fmt, batch, rows, cols, offsets, by_cols)
 PyObject* wrap(const Room& r, PyObject* scale, int fmt, int64_t batch, int64_t rows, int64_t cols, PyObject* offsets,
                bool by_cols) {
+    if (fmt == QL_FP4_MX) scale = Py_None;
     PyObject* a[9] = {THPVariable_Wrap(r.buf), PyLong_FromLongLong(r.ld), scale, PyLong_FromLong(fmt),
                       PyLong_FromLongLong(batch), PyLong_FromLongLong(rows), PyLong_FromLongLong(cols), offsets,
                       by_cols ? Py_True : Py_False};

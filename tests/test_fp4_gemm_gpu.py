@@ -414,6 +414,20 @@ def test_time_out_is_reported(ops):
     check(ops.gemm_fp4_nt(a, b), ref.values(np64(acts(40, 512, seed=1)), 0), ref.values(np64(acts(300, 512, seed=2)), 0))
 
 
+def test_mx_takes_no_notice_of_a_tensor_scale(ops):
+    x, w = acts(70, 200, seed=1), acts(130, 200, seed=2)
+    b, half = ops.fp4_cast(w, 1), torch.tensor([0.5], device="cuda")
+    want = ops.fp4_cast(x, 1)
+    for scale in (half, ops.FP4_OWN_SCALE):
+        a = ops.fp4_cast(x, 1, scale)
+        r, c = ops.fp4_cast_dual(x, 1, scale)
+        assert a.scale is None and r.scale is None and c.scale is None
+        for v in (a, r):
+            assert torch.equal(ops.fp4_dequant(v), ops.fp4_dequant(want))
+        assert torch.equal(ops.fp4_linear(x, b, scale), ops.gemm_fp4_nt(want, b))
+        assert torch.equal(ops.fp4_linear(x[:3], b, scale), ops.gemm_fp4_nt(want, b)[:3])
+
+
 def test_refusals(ops, fp4):
     x, w = acts(8, 64, seed=1), acts(16, 64, seed=2)
     a, b, bm = ops.fp4_cast(x), ops.fp4_cast(w), ops.fp4_cast(w, 1)
@@ -421,7 +435,7 @@ def test_refusals(ops, fp4):
     r = ops.fp4_cast(x, offsets=off)
     one = torch.ones(1, device="cuda")
     for bad in (lambda: ops.fp4_cast(x, 2), lambda: ops.fp4_cast(x[0]), lambda: ops.fp4_cast(x.cpu()),
-                lambda: ops.fp4_cast(x, 1, one), lambda: ops.fp4_cast(x, 0, one.double()),
+                lambda: ops.fp4_cast(x, 0, one.double()),
                 lambda: ops.fp4_cast(x, 0, one.cpu()), lambda: ops.fp4_cast(x, 0, None, off.long()),
                 lambda: ops.fp4_cast(x[None], 0, None, off), lambda: ops.fp4_cast_dual(x.t()),
                 lambda: ops.gemm_fp4_nt(a, bm), lambda: ops.gemm_fp4_nt(a, ops.fp4_cast(w[:, :32])),
@@ -433,8 +447,8 @@ def test_refusals(ops, fp4):
                 lambda: ops.gemm_fp4_nt(a, b, out=torch.empty((8, 15), device="cuda")),
                 lambda: ops.gemm_fp4_nt(a, b, out=torch.empty((16, 8), device="cuda").t()),
                 lambda: ops.fp4_linear(x[0], b), lambda: ops.fp4_linear(x[:, :32], b), lambda: ops.fp4_linear(x, b, offsets=off[:1]),
-                lambda: ops.fp4_linear(x, ops.fp4_cast(torch.stack([w, w]))), lambda: ops.fp4_linear(x, bm, one),
-                lambda: ops.fp4_cast(x, 1, ops.FP4_OWN_SCALE), lambda: ops.fp4_cast(x, 0, 0.5),
+                lambda: ops.fp4_linear(x, ops.fp4_cast(torch.stack([w, w]))),
+                lambda: ops.fp4_cast(x, 0, 0.5),
                 lambda: ops.fp4_cast(torch.stack([x, x, x])[::2], 0, ops.FP4_OWN_SCALE),
                 lambda: ops.fp4_linear(x, b, out=torch.empty((8, 16), device="cuda")),
                 lambda: ops.gemm_fp4_wgrad_ragged(a, b), lambda: ops.fp4_dequant(r), lambda: fp4.FP4Weight(w[None]),
