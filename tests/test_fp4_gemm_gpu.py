@@ -186,6 +186,66 @@ def test_experts_weight_gradient(ops, offs, path, fmt):
         check(acc[i], yv, xv, d0[i])
 
 
+# Tiles of 256 x 256 on up to 76 pairs of SMs: 38, 49, and 81 and 110 in two rounds; the last tile of columns ends in
+# its first half.
+@FMTS
+@pytest.mark.parametrize("mt,nt", [(1, 38), (7, 7), (9, 9), (11, 10)])
+def test_product_in_rounds_of_tiles(ops, mt, nt, fmt):
+    m, n, k = mt * 256 - 19, nt * 256 - 136, 330
+    x, w = acts(m, k, seed=m + k), acts(n, k, seed=n, mul=0.02)
+    ops.set_gemm_path(3)
+    a, b = ops.fp4_cast(x, fmt), ops.fp4_cast(w, fmt)
+    xv, wv = ref.values(np64(x), fmt), ref.values(np64(w), fmt)
+    check(ops.gemm_fp4_nt(a, b), xv, wv)
+    d = torch.randn((m, n), device="cuda")
+    d0 = np64(d)
+    ops.gemm_fp4_nt(a, b, out=d, accumulate=True)
+    check(d, xv, wv, d0)
+    # rows of D that no 16-byte store can address
+    wide = torch.full((m, n + 5), -7.0, dtype=torch.bfloat16, device="cuda")
+    ops.gemm_fp4_nt(a, b, out=wide[:, 2:2 + n])
+    check(wide[:, 2:2 + n], xv, wv)
+    assert bool((wide[:, :2] == -7).all()) and bool((wide[:, 2 + n:] == -7).all())
+
+
+@FMTS
+@pytest.mark.parametrize("offs", [[0, 700, 700, 2000, 2600], [0, 1, 257, 300, 300, 301, 1999]], ids=["96", "112"])
+def test_experts_product_in_rounds_of_tiles(ops, offs, fmt):
+    m, n, k, e = offs[-1] + 3, 8 * 256 - 136, 200, len(offs) - 1
+    x, w = acts(m, k, seed=1), acts(e, n, k, seed=2, mul=0.02)
+    off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    ops.set_gemm_path(3)
+    out = torch.full((m, n), -7.0, dtype=torch.bfloat16, device="cuda")
+    ops.gemm_fp4_nt_ragged(ops.fp4_cast(x, fmt, offsets=off), ops.fp4_cast(w, fmt), out=out)
+    xv = ref.values(np64(x), fmt)
+    for i, (lo, hi) in enumerate(zip(offs[:-1], offs[1:])):
+        if hi > lo:
+            check(out[lo:hi], xv[lo:hi], ref.values(np64(w[i]), fmt))
+    assert bool((out[offs[-1]:] == -7).all())
+
+
+@FMTS
+@pytest.mark.parametrize("offs", [[0, 300, 300], [0, 5, 333], [0, 90, 91, 400]], ids=["empty", "80", "120"])
+def test_experts_weight_gradient_in_rounds_of_tiles(ops, offs, fmt):
+    t, n, k, e = offs[-1], 8 * 256 - 136, 1100, len(offs) - 1
+    x, dy = acts(t, k, seed=1), acts(t, n, seed=2, mul=1e-3)
+    off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    cx, cy = ops.fp4_cast_dual(x, fmt, None, off)[1], ops.fp4_cast_dual(dy, fmt, None, off)[1]
+    ops.set_gemm_path(3)
+    d = ops.gemm_fp4_wgrad_ragged(cy, cx)
+    acc = torch.randn((e, n, k), device="cuda")
+    d0 = np64(acc)
+    ops.gemm_fp4_wgrad_ragged(cy, cx, out=acc, accumulate=True)
+    for i, (lo, hi) in enumerate(zip(offs[:-1], offs[1:])):
+        if hi == lo:
+            assert bool((d[i] == 0).all())
+            assert np.array_equal(np64(acc[i]), d0[i])
+            continue
+        yv, xv = ref.values(np64(dy)[lo:hi].T, fmt), ref.values(np64(x)[lo:hi].T, fmt)
+        check(d[i], yv, xv)
+        check(acc[i], yv, xv, d0[i])
+
+
 def test_offsets_out_of_order_are_reported_and_stay_inside(ops):
     x, w = acts(100, 64, seed=1), acts(3, 40, 64, seed=2)
     off = torch.tensor([0, 90, 30, 500], dtype=torch.int32, device="cuda")
