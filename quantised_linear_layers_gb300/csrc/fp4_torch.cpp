@@ -237,7 +237,9 @@ Out output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const at::De
     } else {
         r.t = tensor(o, "out must be a tensor");
         const bool type_ok = r.t.scalar_type() == at::kBFloat16 || r.t.scalar_type() == at::kFloat;
-        if (!type_ok || r.t.sizes() != shape || r.t.device() != d || (r.t.size(-1) > 1 && r.t.stride(-1) != 1))
+        // rows that overlap (an expanded tensor's) are no room for them
+        if (!type_ok || r.t.sizes() != shape || r.t.device() != d || (r.t.size(-1) > 1 && r.t.stride(-1) != 1) ||
+            (r.t.size(-2) > 1 && r.t.stride(-2) < r.t.size(-1)))
             value_error("out must be bf16 or fp32 of the result's shape with contiguous rows on the operands' device");
         if (accumulate && r.t.scalar_type() != at::kFloat) value_error("accumulate needs an fp32 out");
     }

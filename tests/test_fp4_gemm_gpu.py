@@ -1,6 +1,9 @@
 """4-bit products and layers on the GPU against the numpy definition in 64
 bits. The casts are exact (test_fp4_cast_gpu.py), so the product's bound is that
 of its fp32 accumulation alone (fp4_reference.bound)."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -518,3 +521,19 @@ def test_refusals(ops, fp4):
             bad()
     with pytest.raises(TypeError):
         ops.fp4_cast(x.half())
+
+
+def test_rows_of_out_that_overlap_are_refused(ops):
+    a, b = ops.fp4_cast(acts(8, 64, seed=1)), ops.fp4_cast(acts(16, 64, seed=2))
+    for dtype in (torch.bfloat16, torch.float32):
+        for out in (torch.zeros((1, 16), dtype=dtype, device="cuda").expand(8, 16),
+                    torch.zeros(100, dtype=dtype, device="cuda").as_strided((8, 16), (8, 1))):
+            with pytest.raises(ValueError):
+                ops.gemm_fp4_nt(a, b, out=out)
+            with pytest.raises(ValueError):
+                ops.fp4_dequant(ops.fp4_cast(acts(8, 16, seed=1)), dtype, out=out)
+    with pytest.raises(ValueError):
+        ops.fp4_linear(acts(8, 64, seed=1), b, out=torch.zeros((1, 16), dtype=torch.bfloat16, device="cuda").expand(8, 16))
+    one = torch.zeros((8, 1), device="cuda")                     # rows of one column: any stride from 1 on
+    ops.gemm_fp4_nt(a, ops.fp4_cast(acts(1, 64, seed=2)), out=one)
+    assert bool((one != 0).any())
