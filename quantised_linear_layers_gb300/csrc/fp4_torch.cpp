@@ -479,7 +479,8 @@ PyObject* f_linear_backward(Args a) {
         check_weight(in, wt);
     }
     if (in.x->dim() != 2 || in.m != xc.cols || in.x->device() != xc.device || xc.batch != 1 ||
-        xc.by_cols != (in.experts > 0) || (in.experts > 0 && xc.offsets->size(0) - 1 != in.experts))
+        xc.by_cols != (in.experts > 0) || (xc.offsets != nullptr) != (in.experts > 0) ||
+        (in.experts > 0 && xc.offsets->size(0) - 1 != in.experts))
         value_error("dy must have the rows, experts and device of the forward call");
     if (in.sk != 1 && in.k > 1) value_error("dy must have contiguous rows");
     c10::cuda::CUDAGuard guard(in.x->device());

@@ -537,3 +537,11 @@ def test_rows_of_out_that_overlap_are_refused(ops):
     one = torch.zeros((8, 1), device="cuda")                     # rows of one column: any stride from 1 on
     ops.gemm_fp4_nt(a, ops.fp4_cast(acts(1, 64, seed=2)), out=one)
     assert bool((one != 0).any())
+
+
+def test_backward_refuses_a_cast_by_experts_without_them(ops):
+    x, off = acts(64, 64, seed=1), torch.tensor([0, 30, 64], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        ops.fp4_linear_backward(acts(64, 32, seed=2), None, ops.fp4_cast(x, offsets=off))
+    with pytest.raises(ValueError):
+        ops.fp4_linear_backward(acts(64, 32, seed=2), None, ops.fp4_cast(x), None, off)
