@@ -645,7 +645,8 @@ ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, in
     if (m >= kInt31 || k >= kInt31 || batch >= kInt31 || batch * m >= kInt31 ||
         (offsets != nullptr && experts > ql::kFp4MaxExperts))
         return QL_ERR_UNSUPPORTED;
-    if (batch == 0 || m == 0 || k == 0) return QL_OK;
+    if (batch == 0 || m == 0 || k == 0)
+        return own_scale ? fp4_tensor_scale(nullptr, x_dtype, 0, 0, 0, 0, scale, stream) : QL_OK;
     if (x == nullptr) return QL_ERR_INVALID_ARG;
     if (ql_status s = fp4_operand(q, ldq, sf, k); s != QL_OK) return s;
     DeviceInfo di;
@@ -689,7 +690,8 @@ ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t 
     if (offsets != nullptr && (batch != 1 || experts < 1)) return QL_ERR_INVALID_ARG;
     if (m >= kInt31 || k >= kInt31 || batch >= 65536 || (offsets != nullptr && experts > ql::kFp4MaxExperts))
         return QL_ERR_UNSUPPORTED;
-    if (batch == 0 || m == 0 || k == 0) return QL_OK;
+    if (batch == 0 || m == 0 || k == 0)
+        return own_scale ? fp4_tensor_scale(nullptr, x_dtype, 0, 0, 0, 0, scale, stream) : QL_OK;
     if (x == nullptr || (q_rows == nullptr) != (sf_rows == nullptr)) return QL_ERR_INVALID_ARG;
     const int64_t kpad = fp4_column_extent(m, offsets != nullptr ? experts : 0);
     if (kpad / 128 >= 65536) return QL_ERR_UNSUPPORTED;

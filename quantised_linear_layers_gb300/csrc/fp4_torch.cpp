@@ -120,7 +120,8 @@ Input input(PyObject* ox, int fmt, PyObject* oscale, PyObject* ooffsets) {
     if (oscale != Py_None && fmt == QL_FP4_NV) {        // FP4_MX has none and takes no notice of one
         if (oscale == g_own) {
             in.own = true;
-            if (in.batch > 1 && in.sb != in.m * in.sm)
+            // one matrix below the other, or (transposed views) one beside the other
+            if (in.batch > 1 && in.sb != in.m * in.sm && !(in.sm == 1 && in.sb == in.k * in.sk))
                 value_error("x's matrices must follow one another for a scale of their own");
         } else {
             const at::Tensor& s = tensor(oscale, "tensor_scale must be a tensor, FP4_OWN_SCALE or None");

@@ -545,3 +545,14 @@ def test_backward_refuses_a_cast_by_experts_without_them(ops):
         ops.fp4_linear_backward(acts(64, 32, seed=2), None, ops.fp4_cast(x, offsets=off))
     with pytest.raises(ValueError):
         ops.fp4_linear_backward(acts(64, 32, seed=2), None, ops.fp4_cast(x), None, off)
+
+
+def test_own_scale_of_nothing_and_of_transposed_batches(ops):
+    least = float(ops.fp4_tensor_scale(torch.empty((0, 5), device="cuda")))
+    for x in (torch.empty((0, 64), device="cuda"), torch.empty((7, 0), dtype=torch.bfloat16, device="cuda")):
+        assert float(ops.fp4_cast(x, 0, ops.FP4_OWN_SCALE).scale) == least
+        assert [float(c.scale) for c in ops.fp4_cast_dual(x, 0, ops.FP4_OWN_SCALE)] == [least, least]
+    x = acts(3, 40, 70, seed=1)
+    got, want = ops.fp4_cast(x.transpose(1, 2), 0, ops.FP4_OWN_SCALE), ops.fp4_cast_dual(x, 0, ops.FP4_OWN_SCALE)[1]
+    assert float(got.scale) == float(want.scale)
+    assert torch.equal(got.q, want.q) and torch.equal(got.sf[:-16], want.sf[:-16])
