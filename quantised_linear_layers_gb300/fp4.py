@@ -24,6 +24,7 @@ activations, and X is read once.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ops
 
@@ -134,6 +135,7 @@ class _FP4Fn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         w4, module = ctx.w4, ctx.module
         offsets = ctx.saved_tensors[0]
@@ -157,7 +159,14 @@ class _FP4Fn(torch.autograd.Function):
 class FP4Linear(torch.nn.Module):
     """nn.Linear (no bias) whose fwd / dgrad / wgrad run through the 4-bit casts
     and products. With ``accumulate_main_grad`` the weight gradient is added into
-    the fp32 buffer ``main_grad`` instead of being returned to autograd."""
+    the fp32 buffer ``main_grad`` instead of being returned to autograd.
+
+    The weight's casts are kept until the weight changes: by an in-place operation
+    or by being given other storage. A write through ``weight.data`` shows in
+    neither; call ``forget_casts`` after one. In a CUDA graph a training step casts
+    the weight anew with every replay, and since replays may change the weight
+    unseen, calls outside the graph keep no casts from then on; a forward without
+    gradients uses the casts kept when it was captured."""
 
     _weight_type = FP4Weight
 
@@ -171,17 +180,52 @@ class FP4Linear(torch.nn.Module):
         torch.nn.init.normal_(self.weight, std=0.02)
         self.fmt = fmt
         self.main_grad = torch.zeros(shape, device=device, dtype=torch.float32) if accumulate_main_grad else None
-        self._w4 = None
-        self._w4_version = None
+        self._w4_in_graphs = []          # casts that captured graphs read
+        self._trained_in_graph = False
+        self.forget_casts()
+
+    def forget_casts(self) -> None:
+        """Has the next forward cast the weight anew."""
+        self._w4 = self._w4_of = self._w4_made = None
+
+    def __getstate__(self):
+        # a copy makes casts of its own
+        return {**self.__dict__, "_w4": None, "_w4_of": None, "_w4_made": None, "_w4_in_graphs": [],
+                "_trained_in_graph": False}
 
     def fp4_weight(self, dgrad: bool = True) -> FP4Weight:
         """The weight's casts, made anew when the weight has changed."""
-        v = self.weight._version
-        if self._w4 is None or self._w4_version != v or (dgrad and not self._w4.dgrad):
-            with torch.no_grad():
-                self._w4 = self._weight_type(self.weight.detach(), self.fmt, dgrad=dgrad)
-            self._w4_version = v
+        w = self.weight
+        capturing = w.is_cuda and torch.cuda.is_current_stream_capturing()
+        of = self._w4_of
+        # `of` keeps the storage that was cast, so that no other can have its address
+        kept = (self._w4 is not None and not self._trained_in_graph and (self._w4.dgrad or not dgrad) and
+                of[0] == w._version and of[1].data_ptr() == w.data_ptr() and of[1].device == w.device and
+                of[1].dtype == w.dtype)
+        training = capturing and torch.is_grad_enabled() and w.requires_grad
+        self._trained_in_graph |= training
+        if training or (capturing and not kept):
+            return self._cast(dgrad)     # part of the graph: not for calls outside it
+        if not kept:
+            self._w4 = self._cast(dgrad)
+            self._w4_of = (w._version, w.detach())
+            stream = torch.cuda.current_stream(w.device)
+            self._w4_made = (stream, stream.record_event())
+        elif capturing:
+            if self._w4 not in self._w4_in_graphs:
+                self._w4_in_graphs.append(self._w4)
+        else:
+            stream = torch.cuda.current_stream(w.device)
+            if stream != self._w4_made[0]:
+                stream.wait_event(self._w4_made[1])
+                for c in (self._w4.w, self._w4.wt):
+                    if c is not None:
+                        c.buf.record_stream(stream)
         return self._w4
+
+    def _cast(self, dgrad: bool) -> FP4Weight:
+        with torch.no_grad():
+            return self._weight_type(self.weight.detach(), self.fmt, dgrad=dgrad)
 
     def _apply_layer(self, x: torch.Tensor, offsets: torch.Tensor | None) -> torch.Tensor:
         if torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad):

@@ -476,6 +476,10 @@ class FP4Tensor:
         else:
             self.scale_ptr = scale.scale_ptr if type(scale) is FP4Tensor else scale.data_ptr()
 
+    def __reduce__(self):        # a copy has addresses of its own
+        return _fp4_tensor, (self.buf, self.ld, self._scale, self.fmt, self.batch, self.rows, self.cols, self.offsets,
+                             self.by_cols)
+
     @property
     def scale(self) -> torch.Tensor | None:
         s = self._scale
@@ -491,6 +495,10 @@ class FP4Tensor:
     @property
     def sf(self) -> torch.Tensor:
         return self.buf[self.batch * self.rows * self.ld:]
+
+
+def _fp4_tensor(buf, ld, scale, *rest):
+    return FP4Tensor(buf, ld, FP4_OWN_SCALE if isinstance(scale, str) else scale, *rest)
 
 
 _fp4 = None

@@ -556,3 +556,120 @@ def test_own_scale_of_nothing_and_of_transposed_batches(ops):
     got, want = ops.fp4_cast(x.transpose(1, 2), 0, ops.FP4_OWN_SCALE), ops.fp4_cast_dual(x, 0, ops.FP4_OWN_SCALE)[1]
     assert float(got.scale) == float(want.scale)
     assert torch.equal(got.q, want.q) and torch.equal(got.sf[:-16], want.sf[:-16])
+
+
+def test_layer_sees_every_change_of_its_weight(fp4):
+    x, w1, w2 = acts(20, 96, seed=1), acts(48, 96, seed=2), acts(48, 96, seed=3)
+    layer = fp4.FP4Linear(96, 48, device="cuda")
+
+    def want(w):
+        return fp4.forward(x, fp4.FP4Weight(w), "own")
+
+    with torch.no_grad():
+        layer.weight.copy_(w1)
+        assert torch.equal(layer(x), want(w1))
+        layer.weight.copy_(w2)
+        assert torch.equal(layer(x), want(w2))
+        layer.weight.data = w1.clone()
+        assert torch.equal(layer(x), want(w1))
+        for w in (w2, w1, w2):                       # storage that comes and goes
+            layer.weight.data = w.clone()
+            assert torch.equal(layer(x), want(w))
+        layer.weight.data.copy_(w1)
+        layer.forget_casts()
+        assert torch.equal(layer(x), want(w1))
+        layer.float()
+        assert torch.equal(layer(x), want(w1))
+        other = copy.deepcopy(layer)
+        other.weight.copy_(w2)
+        assert torch.equal(other(x), want(w2)) and torch.equal(layer(x), want(w1))
+
+
+def test_copies_of_a_cast_stand_by_themselves(ops):
+    x, w = acts(20, 96, seed=1), acts(48, 96, seed=2)
+    rows, cols = ops.fp4_cast_dual(w, 0, ops.FP4_OWN_SCALE)
+    want, a = ops.gemm_fp4_nt(ops.fp4_cast(x), rows), ops.fp4_cast(x)
+    for c in (copy.deepcopy(rows), pickle.loads(pickle.dumps(rows))):
+        assert c.q_ptr == c.buf.data_ptr() != rows.q_ptr and c.scale_ptr != rows.scale_ptr
+        assert float(c.scale) == float(rows.scale)
+        assert torch.equal(ops.gemm_fp4_nt(a, c), want)
+
+
+def test_layer_on_two_streams(fp4):
+    """The casts are made behind other work of a stream and used at once on another one."""
+    x, w = acts(20, 1024, seed=1), acts(2048, 1024, seed=2)
+    layer = fp4.FP4Linear(1024, 2048, device="cuda")
+    with torch.no_grad():
+        layer.weight.copy_(w)
+        want = fp4.forward(x, fp4.FP4Weight(w), "own")
+        big = torch.randn((4096, 4096), device="cuda")
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                big = big @ big * 1e-3
+            first = layer(x)
+        second = layer(x)
+        torch.cuda.synchronize()
+    assert torch.equal(first, want) and torch.equal(second, want)
+
+
+def test_training_step_in_a_graph_follows_its_weight(fp4):
+    x, w, dy = acts(40, 96, seed=1), acts(48, 96, seed=2), acts(40, 48, seed=3, mul=1e-3)
+    layers = []
+    for _ in range(2):
+        layer = fp4.FP4Linear(96, 48, device="cuda")
+        with torch.no_grad():
+            layer.weight.copy_(w)
+        layers.append(layer)
+
+    def step(layer):
+        y = layer(x)
+        grad, = torch.autograd.grad(y, layer.weight, dy)
+        with torch.no_grad():
+            layer.weight.sub_(grad, alpha=1e3)
+        return y.detach()
+
+    eager = [step(layers[0]).clone() for _ in range(3)]
+    assert not torch.equal(eager[0], eager[2])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = [step(layers[1]).clone()]
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step(layers[1])
+    for _ in range(2):
+        graph.replay()
+        got.append(y.clone())
+    assert all(torch.equal(a, b) for a, b in zip(got, eager))
+    for _ in range(2):                               # and a call outside the graph sees what the graph left
+        with torch.no_grad():
+            assert torch.equal(layers[1](x), layers[0](x))
+        graph.replay()
+        step(layers[0])
+
+
+def test_forward_in_a_graph_keeps_its_casts(fp4):
+    x, w1, w2 = acts(5, 96, seed=1), acts(48, 96, seed=2), acts(48, 96, seed=3)
+    layer = fp4.FP4Linear(96, 48, device="cuda")
+    with torch.no_grad():
+        layer.weight.copy_(w1)
+        want = layer(x).clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = layer(x)
+        layer.weight.copy_(w2)
+        layer(x)
+        junk = [torch.full((4096,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        graph.replay()
+        assert torch.equal(y, want)
+        del junk
+
+
+def test_no_second_derivative(fp4):
+    layer = fp4.FP4Linear(96, 48, device="cuda")
+    x = acts(5, 96, seed=1).requires_grad_()
+    dx, = torch.autograd.grad(layer(x).float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.float().sum().backward()
