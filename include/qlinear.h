@@ -541,8 +541,8 @@ ql_status fp4_dequant(const uint8_t* q, int64_t ldq, const uint8_t* sf, int fmt,
                       int64_t k, void* out, ql_dtype out_dtype, int64_t ldo, ql_stream_t stream);
 
 /* D [m, n] = X W^T: X [m, k], W [n, k] row-wise casts of one format, scales
- * x_scale and w_scale (device, NULL is 1); fp32 accumulation, D bf16 or fp32
- * (fp32: accumulate != 0 adds to D). */
+ * x_scale and w_scale (device, NULL is 1), whose product must be a normal fp32
+ * number; fp32 accumulation, D bf16 or fp32 (fp32: accumulate != 0 adds to D). */
 ql_status gemm_fp4_nt(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale, const uint8_t* w,
                       int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, ql_dtype d_dtype,
                       int64_t ldd, int64_t m, int64_t n, int64_t k, int accumulate, ql_stream_t stream);

@@ -642,7 +642,8 @@ ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, in
     if (batch < 0 || m < 0 || k < 0 || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
     if (offsets != nullptr && (batch != 1 || experts < 1)) return QL_ERR_INVALID_ARG;
-    if (m >= kInt31 || k >= kInt31 || batch >= kInt31 || batch * m >= kInt31 ||
+    // (16 blocks of threads take a scale block's rows)
+    if (m >= kInt31 || k >= kInt31 || batch >= kInt31 || batch * m >= kInt31 || batch * ((m + 127) / 128) >= kInt31 / 16 ||
         (offsets != nullptr && experts > ql::kFp4MaxExperts))
         return QL_ERR_UNSUPPORTED;
     if (batch == 0 || m == 0 || k == 0)

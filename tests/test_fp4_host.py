@@ -44,6 +44,7 @@ def test_refused_before_cuda(L):
     assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, p, 0, None) == 1             # no experts
     assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 0, p, 32, p, p, 513, None) == 2           # too many
     assert C(p, 0, 1, 1 << 31, 64, 0, 64, 1, 0, None, 0, p, 32, p, None, 0, None) == 2
+    assert C(p, 0, 1 << 30, 1, 64, 64, 64, 1, 0, None, 0, p, 32, p, None, 0, None) == 2    # more scale blocks than a grid has
     assert C(None, 0, 1, 0, 64, 0, 64, 1, 0, None, 0, None, 32, None, None, 0, None) == 0  # nothing to do
     assert C(p, 0, 1, 4, 64, 0, 64, 1, 0, None, 1, p, 32, p, None, 0, None) == 1       # own scale, nowhere to put it
     assert C(p, 0, 1, 4, 64, 0, 64, 1, 1, p, 1, p, 32, p, None, 0, None) == 1          # MX has none
