@@ -858,10 +858,12 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
                      size_t workspace_bytes, ql_stream_t stream) {
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
     if (x_dtype != QL_BF16 && x_dtype != QL_F32) return QL_ERR_INVALID_ARG;
+    if (m < 0 || n < 0 || k < 0 || (own_scale && (x_scale == nullptr || fmt != QL_FP4_NV))) return QL_ERR_INVALID_ARG;
+    if (n == 0) return own_scale ? fp4_tensor_scale(x, x_dtype, m, k, x_stride_m, 1, x_scale, stream) : QL_OK;
     const int64_t ldq = (k + 31) / 32 * 16;
     uint8_t* q = static_cast<uint8_t*>(workspace);
-    if (m > ql::fp4_cast_rows(offsets != nullptr ? experts : 0) || m <= 0 || n <= 0 || k <= 0) {
-        if (m > 0 && n > 0 && k > 0 && (workspace == nullptr ||
+    if (m > ql::fp4_cast_rows(offsets != nullptr ? experts : 0) || m == 0 || k == 0) {
+        if (m > 0 && k > 0 && (workspace == nullptr ||
                                         workspace_bytes < fp4_linear_workspace_size(m, k, fmt, offsets ? experts : 0)))
             return QL_ERR_INVALID_ARG;
         uint8_t* sf = q == nullptr ? nullptr : q + m * ldq;
@@ -878,7 +880,6 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
     if (offsets != nullptr && experts < 1) return QL_ERR_INVALID_ARG;
     if (offsets != nullptr && (experts > ql::kFp4MaxExperts || experts * n >= kInt31)) return QL_ERR_UNSUPPORTED;
     if (x == nullptr || d == nullptr || ldd < n) return QL_ERR_INVALID_ARG;
-    if (own_scale && (x_scale == nullptr || fmt != QL_FP4_NV)) return QL_ERR_INVALID_ARG;
     if (ql_status s = fp4_operand(w, ldw, sfw, k); s != QL_OK) return s;
     if (own_scale)
         if (ql_status s = fp4_tensor_scale(x, x_dtype, m, k, x_stride_m, 1, x_scale, stream); s != QL_OK) return s;

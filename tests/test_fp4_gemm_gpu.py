@@ -673,3 +673,19 @@ def test_no_second_derivative(fp4):
     dx, = torch.autograd.grad(layer(x).float().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         dx.float().sum().backward()
+
+
+@FMTS
+def test_linear_of_nothing(ops, fmt):
+    x, w = acts(40, 64, seed=1), acts(16, 64, seed=2)
+    own = ops.FP4_OWN_SCALE if fmt == 0 else None
+    for m in (0, 3, 40):
+        for scale in (None, own):
+            assert ops.fp4_linear(x[:m], ops.fp4_cast(w[:0], fmt), scale).shape == (m, 0)
+            d = ops.fp4_linear(x[:m, :0], ops.fp4_cast(w[:, :0], fmt), scale)
+            assert d.shape == (m, 16) and bool((d == 0).all())
+    off = torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda")
+    assert ops.fp4_linear(x[:3], ops.fp4_cast(torch.stack([w, w])[:, :0], fmt), None, off).shape == (3, 0)
+    d, cols = ops.fp4_linear_saving(x[:0], ops.fp4_cast(w, fmt), own)
+    dx, dw = ops.fp4_linear_backward(acts(0, 16, seed=3), ops.fp4_cast_dual(w, fmt, own)[1], cols, own)
+    assert d.shape == (0, 16) and dx.shape == (0, 64) and bool((dw == 0).all()) and dw.shape == (16, 64)

@@ -73,6 +73,9 @@ def test_refused_before_cuda(L):
     assert R(p, 32, p, None, p, 32, p, None, 0, p, 0, 8, p, 2, 4, 8, 0, None) == 2       # k == 0
     F = L.fp4_linear
     assert F(p, 0, 64, None, 0, p, 32, p, None, 2, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown format
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 4, 0, 64, None, 0, None) == 0     # nothing to do
+    assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, -4, 8, 64, None, 0, None) == 1    # negative size
+    assert F(p, 0, 64, None, 1, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # own scale, nowhere to put it
     assert F(p, 3, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1     # unknown type
     assert F(p, 0, 64, None, 0, p, 32, p, None, 0, p, 7, None, 0, 4, 8, 64, None, 0, None) == 1     # D's rows too short
     assert F(None, 0, 64, None, 0, p, 32, p, None, 0, p, 8, None, 0, 4, 8, 64, None, 0, None) == 1
