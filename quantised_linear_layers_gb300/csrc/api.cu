@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -166,6 +167,10 @@ ql_status fp4_product(ql::Fp4GemmArgs& a, cudaStream_t st) {
     //   fp32, 40 tiles: K 2560 8.9 / 9.9, 4096 11.8 / 11.5; 256 tiles: K 1024 16.2 / 17.9, 2048 21.8 / 21.7;
     //   512 tiles: K 512 25.0 / 27.1, 1024 30.4 / 28.1
     //   experts' gradients, 8 x 4096 x 4096: 512 rows each 90 / 99; 8 x 4096 x 7168, 2048 rows each 271 / 224
+    // A D that TMA cannot write, its rows not on 16-byte boundaries, leaves the pairs by
+    // narrower stores and needs more of K to hide them:
+    //   bf16, 2592 x 14539: K 256 29.5 / 34.8, 1024 30.9 / 37.9, 2048 42.8 / 41.1; 4096 x 4098: 1024 14.4 / 16.3, 2048 20.4 / 19.4
+    //   fp32, 2592 x 14539: K 1024 42.0 / 60.4, 2048 51.9 / 61.0, 4096 84.9 / 82.4; 4096 x 4097: 4096 37.6 / 39.7
     // With experts the rows (or K) are an expert's on average; 128 rows each
     // are one half of a pair's tile (8 x 4096 x 7168: 25 / 31).
     const int64_t experts = a.form == ql::kFp4Plain ? 1 : a.experts;
@@ -173,7 +178,8 @@ ql_status fp4_product(ql::Fp4GemmArgs& a, cudaStream_t st) {
     const int64_t k = a.form == ql::kFp4RagK ? a.rows / experts : a.k;
     const int64_t tiles = ((rows + 255) / 256) * ((a.n + 255) / 256) * experts;
     const bool few = tiles < sms * 4 / 5;
-    const int64_t least_k = a.out_f32 ? (few ? 3584 : (tiles < sms * 5 / 2 ? 2048 : 1024)) : (few ? 2560 : 0);
+    int64_t least_k = a.out_f32 ? (few ? 3584 : (tiles < sms * 5 / 2 ? 2048 : 1024)) : (few ? 2560 : 0);
+    if (!ql::fp4_tma_d(a)) least_k = std::max<int64_t>(least_k, a.out_f32 ? 4096 : 2048);
     const bool pair = a.xr == nullptr && (path == 3 || (path != 2 && path != 4 && rows > 128 && tiles >= sms / 4 && k >= least_k));
     return from_cuda(pair ? ql::launch_fp4_gemm_pair(a, st, sms) : ql::launch_fp4_gemm(a, st, sms));
 }

@@ -87,6 +87,10 @@ constexpr int64_t fp4_cast_rows(int experts) { return experts > 0 ? 16 : 8; }
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmArgs& a, cudaStream_t st, int num_sms);
 
+// Whether TMA can write D: rows that start and end on 16-byte boundaries (a copy
+// may write a row's last 16-byte piece whole).
+bool fp4_tma_d(const Fp4GemmArgs& a);
+
 // Tensor maps of an operand's codes (box_rows x 128 bytes = 256 columns) and of
 // its scale blocks (the blocks of 128 rows x 256 columns).
 bool fp4_codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t kbytes, int64_t ld, int box_rows);

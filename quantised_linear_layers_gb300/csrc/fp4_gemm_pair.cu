@@ -68,6 +68,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl)) != 0;
 }
 
+// Eight rows of 64 bf16 columns out of a warp's staging buffer (from its row
+// r0, a multiple of 8) to rows of D that start on 4-byte boundaries.
+__device__ __forceinline__ void store_pairs8(const uint8_t* stg, int r0, __nv_bfloat16* d, int64_t ldd, const Bounds& bnd) {
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        w[j] = *reinterpret_cast<const uint32_t*>(stg + (r0 + j) * 128 + (((lane >> 2) ^ j) << 4) + (lane & 3) * 4);
+    d += 2 * lane;
+#pragma unroll
+    for (int j = 0; j < 8; ++j, d += ldd)
+        if (QL_IN(bnd, 0, d, 4)) *reinterpret_cast<uint32_t*>(d) = w[j];
+}
+
 // The same rows stored by the warp itself, for rows that end inside its 32 and
 // for a D that TMA cannot address: through the warp's staging buffer, so that
 // a store instruction writes neighbouring columns of one row (a lane storing
@@ -112,9 +126,15 @@ __device__ __forceinline__ void store_warp_rows(const float* acc, uint8_t* stg, 
             }
         } else {
             __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.d) + at;
+            int r = 0;
+            // pairs of columns, if all rows start on 4-byte boundaries (2592 x 14540 x 96
+            // 35.2 -> 27.6 us; with rows that start between two, whose ends are stores of
+            // their own, 35.5 -> 58)
+            if (c0 + c + CW <= p.n && (p.ldd & 1) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 2u) == 0)
+                for (; r + 8 <= rows; r += 8, d += 8 * p.ldd) store_pairs8(stg, r, d - lane, p.ldd, p.bnd);
             const bool in1 = c0 + c + lane + 32 < p.n;
 #pragma unroll 4
-            for (int r = 0; r < rows; ++r, d += p.ldd) {
+            for (; r < rows; ++r, d += p.ldd) {
                 const uint8_t* row = stg + r * 128 + (lane & 7) * 2;
                 const __nv_bfloat16 v0 = *reinterpret_cast<const __nv_bfloat16*>(row + (((lane >> 3) ^ (r & 7)) << 4));
                 const __nv_bfloat16 v1 = *reinterpret_cast<const __nv_bfloat16*>(row + (((4 + (lane >> 3)) ^ (r & 7)) << 4));
@@ -338,9 +358,7 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
         !fp4_scales_map(&msw, a.sfw, we * p.w_row_blocks * p.kblocks, a.fmt))
         return cudaErrorInvalidValue;
     constexpr int es = OUT_F32 ? 4 : 2;
-    const bool rows16 = (reinterpret_cast<uintptr_t>(a.d) & 15u) == 0 && (a.ldd * es) % 16 == 0;
-    // a TMA store may write a row's last 16-byte piece whole, so D's rows must end on one
-    if (rows16 && (a.n * es) % 16 == 0 &&
+    if (fp4_tma_d(a) &&
         encode_2d_map(&md, a.d, OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.m * de,
                       a.n, a.ldd * es, 32, 128 / es, 128))
         p.tma_d = 1;
@@ -369,6 +387,11 @@ cudaError_t launch_t(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
 }
 
 }  // namespace
+
+bool fp4_tma_d(const Fp4GemmArgs& a) {
+    const int64_t es = a.out_f32 ? 4 : 2;
+    return (reinterpret_cast<uintptr_t>(a.d) & 15u) == 0 && (a.ldd * es) % 16 == 0 && (a.n * es) % 16 == 0;
+}
 
 cudaError_t launch_fp4_gemm_pair(const Fp4GemmArgs& a, cudaStream_t st, int num_sms) {
     if (a.fmt == kFp4Nv)
