@@ -505,6 +505,11 @@ int ql_bounds_checked(void);
 /* Bytes of the scales of a cast of `rows` rows and k columns; experts > 0: of a
  * row-wise cast by expert. -1 for an unknown format or a negative size. */
 int64_t fp4_scale_bytes(int64_t rows, int64_t k, int fmt, int experts);
+/* A row stride for codes of k columns: a multiple of 128 bytes, so that no piece of
+ * 256 columns straddles a 128-byte line, or of 16 for rows of up to 64 bytes.
+ * Any other multiple of 16 is as right and slower to read: products of 4096 x
+ * 4096 x 7170 took 53.6 us with rows of 3600 bytes and take 41.8 with 3712. */
+int64_t fp4_row_stride(int64_t k);
 /* Columns that the codes of a column-wise cast of m rows have room for: m
  * rounded up to 128; with experts > 0 what any split of m rows over them needs,
  * which is then also the cast's number of columns (its scale blocks run over

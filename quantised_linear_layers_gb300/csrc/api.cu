@@ -616,6 +616,11 @@ int64_t fp4_scale_bytes(int64_t rows, int64_t k, int fmt, int experts) {
     return fp4_row_blocks(rows, experts) * ql::fp4_kblocks(k, fmt) * ql::kFp4SfBlock;
 }
 
+int64_t fp4_row_stride(int64_t k) {
+    const int64_t bytes = k > 0 ? (k + 1) / 2 : 1;
+    return bytes <= 64 ? (bytes + 15) / 16 * 16 : (bytes + 127) / 128 * 128;
+}
+
 int64_t fp4_column_extent(int64_t m, int experts) {
     if (experts <= 0) return (m + 127) / 128 * 128;
     return ((m + ql::kFp4KAlign - 1) / ql::kFp4KAlign + experts) * ql::kFp4KAlign;
@@ -855,7 +860,7 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
 
 size_t fp4_linear_workspace_size(int64_t m, int64_t k, int fmt, int experts) {
     if (m <= ql::fp4_cast_rows(experts) || k <= 0 || (fmt != QL_FP4_NV && fmt != QL_FP4_MX)) return 0;
-    return static_cast<size_t>(m) * ((k + 31) / 32 * 16) + static_cast<size_t>(fp4_scale_bytes(m, k, fmt, experts));
+    return static_cast<size_t>(m) * fp4_row_stride(k) + static_cast<size_t>(fp4_scale_bytes(m, k, fmt, experts));
 }
 
 ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float* x_scale, int own_scale,
@@ -866,7 +871,7 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
     if (x_dtype != QL_BF16 && x_dtype != QL_F32) return QL_ERR_INVALID_ARG;
     if (m < 0 || n < 0 || k < 0 || (own_scale && (x_scale == nullptr || fmt != QL_FP4_NV))) return QL_ERR_INVALID_ARG;
     if (n == 0) return own_scale ? fp4_tensor_scale(x, x_dtype, m, k, x_stride_m, 1, x_scale, stream) : QL_OK;
-    const int64_t ldq = (k + 31) / 32 * 16;
+    const int64_t ldq = fp4_row_stride(k);
     uint8_t* q = static_cast<uint8_t*>(workspace);
     if (m > ql::fp4_cast_rows(offsets != nullptr ? experts : 0) || m == 0 || k == 0) {
         if (m > 0 && k > 0 && (workspace == nullptr ||

@@ -29,6 +29,7 @@ struct Api {
     decltype(&::fp4_dequant) dequant;
     decltype(&::fp4_linear) linear;
     decltype(&::fp4_linear_workspace_size) linear_ws;
+    decltype(&::fp4_row_stride) row_stride;
     decltype(&::gemm_fp4_nt) gemm;
     decltype(&::gemm_fp4_nt_ragged) ragged;
     decltype(&::gemm_fp4_wgrad_ragged) wgrad;
@@ -159,13 +160,12 @@ Room room(int64_t batch, int64_t rows, int64_t ld, int64_t row_blocks, int64_t k
     return r;
 }
 Room row_room(const Input& in, int fmt) {
-    const int64_t ld = in.k > 0 ? ceil_div(in.k, 32) * 16 : 16;
-    return room(in.batch, in.m, ld, ceil_div(in.m, 128) + in.experts, in.k, fmt, in.x->device());
+    return room(in.batch, in.m, api.row_stride(in.k), ceil_div(in.m, 128) + in.experts, in.k, fmt, in.x->device());
 }
 Room column_room(const Input& in, int fmt) {
     const int64_t m1 = in.m > 0 ? in.m : 1;
     const int64_t extent = in.experts > 0 ? (ceil_div(in.m, 256) + in.experts) * 256 : ceil_div(m1, 128) * 128;
-    return room(in.batch, in.k, extent / 2, ceil_div(in.k, 128), in.experts > 0 ? extent : in.m, fmt, in.x->device());
+    return room(in.batch, in.k, api.row_stride(extent), ceil_div(in.k, 128), in.experts > 0 ? extent : in.m, fmt, in.x->device());
 }
 
 // FP4Tensor(buf, ld, scale, fmt, batch, rows, cols, offsets, by_cols)
@@ -540,12 +540,12 @@ PyObject* entry(PyObject*, Args a, Py_ssize_t n) {
 
 // (addresses, FP4Tensor, FP4_OWN_SCALE, error callable)
 PyObject* bind(PyObject*, Args a, Py_ssize_t n) {
-    if (n != 4 || !PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 9) {
+    if (n != 4 || !PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 10) {
         PyErr_SetString(PyExc_TypeError, "bind(addresses, class, own, error)");
         return nullptr;
     }
-    void* p[9];
-    for (int i = 0; i < 9; ++i) {
+    void* p[10];
+    for (int i = 0; i < 10; ++i) {
         p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
         if (p[i] == nullptr) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -558,9 +558,10 @@ PyObject* bind(PyObject*, Args a, Py_ssize_t n) {
     api.dequant = reinterpret_cast<decltype(api.dequant)>(p[3]);
     api.linear = reinterpret_cast<decltype(api.linear)>(p[4]);
     api.linear_ws = reinterpret_cast<decltype(api.linear_ws)>(p[5]);
-    api.gemm = reinterpret_cast<decltype(api.gemm)>(p[6]);
-    api.ragged = reinterpret_cast<decltype(api.ragged)>(p[7]);
-    api.wgrad = reinterpret_cast<decltype(api.wgrad)>(p[8]);
+    api.row_stride = reinterpret_cast<decltype(api.row_stride)>(p[6]);
+    api.gemm = reinterpret_cast<decltype(api.gemm)>(p[7]);
+    api.ragged = reinterpret_cast<decltype(api.ragged)>(p[8]);
+    api.wgrad = reinterpret_cast<decltype(api.wgrad)>(p[9]);
     g_class = Py_NewRef(a[1]);
     g_own = Py_NewRef(a[2]);
     g_error = Py_NewRef(a[3]);

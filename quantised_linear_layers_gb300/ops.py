@@ -50,6 +50,7 @@ _SIGS = {
     "gemm_fp8_nn_bf16": [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp, _i64,
                          _i64, _i64, _i64, _vp],
     "fp4_scale_bytes": [_i64, _i64, _int, _int],
+    "fp4_row_stride": [_i64],
     "fp4_column_extent": [_i64, _int],
     "fp4_tensor_scale": [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp],
     "fp4_cast": [_vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _int, _vp, _int, _vp, _i64, _vp, _vp, _int, _vp],
@@ -108,6 +109,7 @@ def load_library(path: str = LIB_PATH):
             lib.ql_cast_gemm_host_workspace_size.restype = _sz
             lib.fp4_linear_workspace_size.restype = _sz
             lib.fp4_scale_bytes.restype = _i64
+            lib.fp4_row_stride.restype = _i64
             lib.fp4_column_extent.restype = _i64
             _lib = lib
     return _lib
@@ -453,7 +455,7 @@ def cast_gemm_host(x_host: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor, fmt
 # ---------------------------------------------------------------------------
 class FP4Tensor:
     """A matrix (or a batch of them) in 4 bits, as a cast left it: codes and scale
-    blocks in one buffer ``buf`` (``q``: uint8 [batch * rows, ld]; ``sf``), the
+    blocks in one buffer ``buf`` (``q``: uint8, batch * rows rows of stride ld; ``sf``), the
     tensor's scale ``scale`` (fp32 [1], or None for 1), its format and its sizes;
     ``cols`` is the reduction axis. ``offsets`` are the row ranges of the experts
     it was cast by (``by_cols``: its columns are the experts' rows, each from a
@@ -490,7 +492,7 @@ class FP4Tensor:
     @property
     def q(self) -> torch.Tensor:
         n = self.batch * self.rows
-        return self.buf[:n * self.ld].view(n, self.ld)
+        return self.buf[:n * self.ld].view(n, self.ld)[:, :self.ld if self.by_cols else (self.cols + 1) // 2]
 
     @property
     def sf(self) -> torch.Tensor:
@@ -503,7 +505,7 @@ def _fp4_tensor(buf, ld, scale, *rest):
 
 _fp4 = None
 _FP4_ENTRIES = ("fp4_tensor_scale", "fp4_cast", "fp4_cast_dual", "fp4_dequant", "fp4_linear", "fp4_linear_workspace_size",
-                "gemm_fp4_nt", "gemm_fp4_nt_ragged", "gemm_fp4_wgrad_ragged")
+                "fp4_row_stride", "gemm_fp4_nt", "gemm_fp4_nt_ragged", "gemm_fp4_wgrad_ragged")
 
 
 def _load_fp4():

@@ -23,6 +23,8 @@ def test_sizes(L):
     assert L.fp4_scale_bytes(0, 64, 0, 0) == 0
     assert L.fp4_scale_bytes(-1, 64, 0, 0) == -1 and L.fp4_scale_bytes(1, 64, 2, 0) == -1
     assert L.fp4_column_extent(1, 0) == 128 and L.fp4_column_extent(129, 0) == 256
+    assert [L.fp4_row_stride(k) for k in (0, 1, 32, 33, 64, 65, 128, 129, 256, 257, 2051)] == \
+        [16, 16, 16, 32, 32, 48, 64, 128, 128, 256, 1152]
     # any split of 257 rows over 3 experts needs at most 1 + 1 + 2 multiples of 256, and a room for one more
     assert L.fp4_column_extent(257, 3) == 5 * 256
     assert all(sum(-(-c // 256) for c in (a, b, 257 - a - b)) <= 5 for a in range(0, 258, 37) for b in range(0, 258 - a, 29))
