@@ -9,6 +9,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -140,32 +141,55 @@ Input input(PyObject* ox, int fmt, PyObject* oscale, PyObject* ooffsets) {
     return in;
 }
 
-// Codes, scale blocks and (last 16 bytes) a scale of one cast, in one buffer.
+// The layers' calls take x with any strides: `copy` holds one with contiguous
+// rows where x's are not.
+void contiguous_rows(Input& in, at::Tensor& copy) {
+    if (in.sk == 1 || in.k <= 1) return;
+    copy = in.x->contiguous();
+    in.x = &copy;
+    in.sm = copy.stride(-2);
+    in.sk = 1;
+}
+
+// Device memory for the length of a call, from torch's allocator (no tensor
+// around it: 1.0 us less).
+c10::DataPtr scratch(int64_t n) { return c10::cuda::CUDACachingAllocator::get()->allocate(static_cast<size_t>(n)); }
+
+// Codes, scale blocks and (last 16 bytes) a scale of one cast, in one buffer: a
+// tensor for an FP4Tensor, or scratch.
+enum class For { kResult, kCall };
 struct Room {
     at::Tensor buf;
+    c10::DataPtr mem;
     uint8_t* q;
     int64_t ld;
     uint8_t* sf;
     float* own;
 };
-Room room(int64_t batch, int64_t rows, int64_t ld, int64_t row_blocks, int64_t kcols, int fmt, const at::Device& d) {
+Room room(int64_t batch, int64_t rows, int64_t ld, int64_t row_blocks, int64_t kcols, int fmt, const at::Device& d, For use) {
     Room r;
     const int64_t codes = batch * rows * ld;
     const int64_t bytes = codes + batch * row_blocks * ceil_div(kcols, fmt == QL_FP4_NV ? 64 : 128) * 512 + 16;
-    r.buf = new_bytes(bytes, d);
-    r.q = r.buf.data_ptr<uint8_t>();
+    if (use == For::kCall) {
+        r.mem = scratch(bytes);
+        r.q = static_cast<uint8_t*>(r.mem.get());
+    } else {
+        r.buf = new_bytes(bytes, d);
+        r.q = r.buf.data_ptr<uint8_t>();
+    }
     r.ld = ld;
     r.sf = r.q + codes;
     r.own = reinterpret_cast<float*>(r.q + bytes - 16);
     return r;
 }
-Room row_room(const Input& in, int fmt) {
-    return room(in.batch, in.m, api.row_stride(in.k), ceil_div(in.m, 128) + in.experts, in.k, fmt, in.x->device());
+Room row_room(const Input& in, int fmt, For use) {
+    return room(in.batch, in.m, api.row_stride(in.k), ceil_div(in.m, 128) + in.experts, in.k, fmt, in.x->device(), use);
 }
-Room column_room(const Input& in, int fmt) {
+Room column_room(const Input& in, int fmt, For use) {
     const int64_t m1 = in.m > 0 ? in.m : 1;
     const int64_t extent = in.experts > 0 ? (ceil_div(in.m, 256) + in.experts) * 256 : ceil_div(m1, 128) * 128;
-    return room(in.batch, in.k, api.row_stride(extent), ceil_div(in.k, 128), in.experts > 0 ? extent : in.m, fmt, in.x->device());
+    return room(in.batch, in.k, api.row_stride(extent), ceil_div(in.k, 128), in.experts > 0 ? extent : in.m, fmt, in.x->device(),
+                use);
 }
 
 // FP4Tensor(buf, ld, scale, fmt, batch, rows, cols, offsets, by_cols)
@@ -334,11 +358,11 @@ PyObject* f_cast(Args a) {
         Input t = in;
         std::swap(t.m, t.k);
         std::swap(t.sm, t.sk);
-        const Room r = column_room(t, fmt);
+        const Room r = column_room(t, fmt, For::kResult);
         launch_dual(t, fmt, nullptr, r);
         return wrap(r, a[2], fmt, in.batch, in.m, in.k, Py_None, false);
     }
-    const Room r = row_room(in, fmt);
+    const Room r = row_room(in, fmt, For::kResult);
     launch_cast(in, fmt, r);
     return wrap(r, a[2], fmt, in.batch, in.m, in.k, a[3], false);
 }
@@ -350,9 +374,9 @@ PyObject* f_cast_dual(Args a) {
     const bool rows = PyObject_IsTrue(a[4]) == 1;
     if (in.sk != 1 && in.k > 1) value_error("x must have contiguous rows");
     c10::cuda::CUDAGuard guard(in.x->device());
-    const Room c = column_room(in, fmt);
+    const Room c = column_room(in, fmt, For::kResult);
     Room r;
-    if (rows) r = row_room(in, fmt);
+    if (rows) r = row_room(in, fmt, For::kResult);
     launch_dual(in, fmt, rows ? &r : nullptr, c);
     PyObject* oc = wrap(c, a[2], fmt, in.batch, in.k, in.m, a[3], in.experts > 0);
     PyObject* orow = Py_None;
@@ -423,21 +447,22 @@ PyObject* f_wgrad(Args a) {
     return THPVariable_Wrap(d.t);
 }
 
-// (x, w, x_scale, offsets, out): x's rows contiguous
+// (x, w, x_scale, offsets, out)
 PyObject* f_linear(Args a) {
     const Operand w = operand(a[1]);
-    const Input in = input(a[0], w.fmt, a[2], a[3]);
+    Input in = input(a[0], w.fmt, a[2], a[3]);
     check_weight(in, w);
-    if (in.sk != 1 && in.k > 1) value_error("x must have contiguous rows");
     c10::cuda::CUDAGuard guard(in.x->device());
+    at::Tensor copy;
+    contiguous_rows(in, copy);
     const Out d = output(a[4], {in.m, w.rows}, at::kBFloat16, w.device, false);
     if (d.code != QL_BF16) value_error("out must be bf16");
     const int64_t size = static_cast<int64_t>(api.linear_ws(in.m, in.k, w.fmt, in.experts));
-    at::Tensor ws;
+    c10::DataPtr ws;
     uint8_t* p = nullptr;
     if (size > 0 || in.own) {
-        ws = new_bytes(size + 16, w.device);       // the scale is at its end
-        p = ws.data_ptr<uint8_t>();
+        ws = scratch(size + 16);       // the scale is at its end
+        p = static_cast<uint8_t*>(ws.get());
     }
     status("fp4_linear", api.linear(in.x->data_ptr(), in.code, in.sm, in.own ? reinterpret_cast<float*>(p + size) : in.scale,
                                     in.own, w.q, w.ld, w.sf, w.scale, w.fmt, d.t.data_ptr(), d.ld, in.offsets, in.experts,
@@ -448,12 +473,13 @@ PyObject* f_linear(Args a) {
 // (x, w, x_scale, offsets): the product and the cast of x along its columns
 PyObject* f_linear_saving(Args a) {
     const Operand w = operand(a[1]);
-    const Input in = input(a[0], w.fmt, a[2], a[3]);
+    Input in = input(a[0], w.fmt, a[2], a[3]);
     check_weight(in, w);
-    if (in.sk != 1 && in.k > 1) value_error("x must have contiguous rows");
     c10::cuda::CUDAGuard guard(in.x->device());
+    at::Tensor copy;
+    contiguous_rows(in, copy);
     const Out d = output(Py_None, {in.m, w.rows}, at::kBFloat16, w.device, false);
-    const Room c = column_room(in, w.fmt), r = row_room(in, w.fmt);
+    const Room c = column_room(in, w.fmt, For::kResult), r = row_room(in, w.fmt, For::kCall);
     launch_dual(in, w.fmt, &r, c);
     const Operand x = as_operand(in, w.fmt, r, in.own ? c.own : in.scale, false);
     if (in.offsets != nullptr) launch_ragged(x, w, in.offsets, d);
@@ -471,7 +497,7 @@ PyObject* f_linear_saving(Args a) {
 PyObject* f_linear_backward(Args a) {
     const bool need_dx = a[1] != Py_None;
     const Operand xc = operand(a[2]);
-    const Input in = input(a[0], xc.fmt, a[3], a[4]);
+    Input in = input(a[0], xc.fmt, a[3], a[4]);
     const bool acc = PyObject_IsTrue(a[6]) == 1;
     Operand wt;
     if (need_dx) {
@@ -483,17 +509,18 @@ PyObject* f_linear_backward(Args a) {
         xc.by_cols != (in.experts > 0) || (xc.offsets != nullptr) != (in.experts > 0) ||
         (in.experts > 0 && xc.offsets->size(0) - 1 != in.experts))
         value_error("dy must have the rows, experts and device of the forward call");
-    if (in.sk != 1 && in.k > 1) value_error("dy must have contiguous rows");
     c10::cuda::CUDAGuard guard(in.x->device());
+    at::Tensor copy;
+    contiguous_rows(in, copy);
     const Out dw = in.experts > 0 ? output(a[5], {in.experts, in.k, xc.rows}, at::kFloat, xc.device, acc)
                                   : output(a[5], {in.k, xc.rows}, at::kFloat, xc.device, acc);
     if (dw.code != QL_F32) value_error("dw_out must be fp32");
     if (in.experts > 0) check_fp32_whole(dw);
     Out dx;
     if (need_dx) dx = output(Py_None, {in.m, wt.rows}, at::kBFloat16, xc.device, false);
-    const Room c = column_room(in, xc.fmt);
+    const Room c = column_room(in, xc.fmt, For::kCall);
     Room r;
-    if (need_dx) r = row_room(in, xc.fmt);
+    if (need_dx) r = row_room(in, xc.fmt, For::kCall);
     launch_dual(in, xc.fmt, need_dx ? &r : nullptr, c);
     float* scale = in.own ? c.own : in.scale;
     if (need_dx) {

@@ -598,14 +598,14 @@ def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = Non
     [experts + 1]) by expert, W [experts, n, k]. Equal to ``fp4_cast`` followed by
     ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 8 rows (16 with experts) take one launch.
     ``x_scale`` as ``fp4_cast``'s tensor_scale."""
-    return (_fp4 or _load_fp4()).linear(_contiguous_rows(x), w, x_scale, offsets, out)
+    return (_fp4 or _load_fp4()).linear(x, w, x_scale, offsets, out)
 
 
 def fp4_linear_saving(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = None,
                       offsets: torch.Tensor | None = None):
     """``fp4_linear`` that also casts x along its columns from the same read:
     (D, cast of x^T), the second for ``fp4_linear_backward``."""
-    return (_fp4 or _load_fp4()).linear_saving(_contiguous_rows(x), w, x_scale, offsets)
+    return (_fp4 or _load_fp4()).linear_saving(x, w, x_scale, offsets)
 
 
 def fp4_linear_backward(dy: torch.Tensor, wt: FP4Tensor | None, x_cols: FP4Tensor, dy_scale: torch.Tensor | None = None,
@@ -614,11 +614,7 @@ def fp4_linear_backward(dy: torch.Tensor, wt: FP4Tensor | None, x_cols: FP4Tenso
     """(dX, dW) of ``fp4_linear_saving``'s product: dX [m, k] bf16 = dY W from the
     cast ``wt`` of W^T (None: no dX), dW [n, k] or [experts, n, k] fp32 (+)= dY^T X,
     with dY cast both ways from one read."""
-    return (_fp4 or _load_fp4()).linear_backward(_contiguous_rows(dy), wt, x_cols, dy_scale, offsets, dw_out, accumulate)
-
-
-def _contiguous_rows(x: torch.Tensor) -> torch.Tensor:
-    return x if x.stride(-1) == 1 or x.shape[-1] <= 1 else x.contiguous()
+    return (_fp4 or _load_fp4()).linear_backward(dy, wt, x_cols, dy_scale, offsets, dw_out, accumulate)
 
 
 def set_num_sms(n: int) -> None:
