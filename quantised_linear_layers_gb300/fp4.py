@@ -46,14 +46,14 @@ class FP4Weight:
         self.update(w)
 
     def update(self, w: torch.Tensor) -> None:
-        if w.dim() != self._dims:
+        self.shape = tuple(w.shape)
+        if len(self.shape) != self._dims:
             raise ValueError("weight must be 2-D [out_features, in_features]" if self._dims == 2 else
                              "weight must be 3-D [experts, out_features, in_features]")
-        w = w if w.stride(-1) == 1 or w.shape[-1] <= 1 else w.contiguous()
-        self.shape = tuple(w.shape)
-        scale = _own(self.fmt)
-        if self._dims == 3 and w.stride(0) != w.shape[1] * w.stride(1):
+        if not w.is_contiguous() and ((w.stride(-1) != 1 and self.shape[-1] > 1) or
+                                      (self._dims == 3 and w.stride(0) != self.shape[1] * w.stride(1))):
             w = w.contiguous()
+        scale = _own(self.fmt)
         if self.dgrad:
             self.w, self.wt = ops.fp4_cast_dual(w, self.fmt, scale)
         else:
