@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -80,9 +80,11 @@ int format(PyObject* o) {
     return static_cast<int>(f);
 }
 
-at::Tensor new_bytes(int64_t n, const at::Device& d) {
-    return at::empty({n}, at::TensorOptions().dtype(at::kByte).device(d));
+// at::empty without the way through the dispatcher
+at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType type, const at::Device& d) {
+    return at::Tensor(at::detail::empty_cuda(shape, type, d, std::nullopt));
 }
+at::Tensor new_bytes(int64_t n, const at::Device& d) { return new_tensor({n}, at::kByte, d); }
 
 // One cast input: sizes, strides and the experts.
 struct Input {
@@ -258,7 +260,7 @@ Out output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const at::De
     Out r;
     if (o == Py_None) {
         if (accumulate) value_error("accumulate needs an existing out");
-        r.t = at::empty(shape, at::TensorOptions().dtype(type).device(d));
+        r.t = new_tensor(shape, type, d);
     } else {
         r.t = tensor(o, "out must be a tensor");
         const bool type_ok = r.t.scalar_type() == at::kBFloat16 || r.t.scalar_type() == at::kFloat;
@@ -342,7 +344,7 @@ PyObject* f_tensor_scale(Args a) {
         if (x.stride(0) != m * x.stride(1)) x = x.contiguous();
         m *= x.size(0);
     }
-    at::Tensor out = at::empty({1}, at::TensorOptions().dtype(at::kFloat).device(x.device()));
+    at::Tensor out = new_tensor({1}, at::kFloat, x.device());
     status("fp4_tensor_scale", api.tensor_scale(x.data_ptr(), code, m, x.size(-1), x.stride(-2), x.stride(-1),
                                                 out.data_ptr<float>(), stream_of(x.device())));
     return THPVariable_Wrap(out);
