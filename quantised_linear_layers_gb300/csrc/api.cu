@@ -642,6 +642,7 @@ ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k
 // The scale of x [batch, m, k], whose entries must follow one another as rows do.
 static ql_status fp4_own_scale(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
                                int64_t x_stride_m, int64_t x_stride_k, float* scale, ql_stream_t stream) {
+    if (m == 1) x_stride_m = x_stride_b;         // the stride of a single row says nothing
     if (batch > 1 && x_stride_b != m * x_stride_m) return QL_ERR_UNSUPPORTED;
     return fp4_tensor_scale(x, x_dtype, batch * m, k, x_stride_m, x_stride_k, scale, stream);
 }

@@ -97,6 +97,18 @@ struct Input {
     bool own;            // made in the call
 };
 
+// Sizes and strides of a matrix or a batch. A dimension of size one may have any
+// stride (torch calls [4, 1, 64] with strides (64, 256, 1) contiguous): it gets
+// one that holds for whoever takes the batch's rows as one long matrix.
+void layout(const at::Tensor& x, Input& in) {
+    in.batch = x.dim() == 3 ? x.size(0) : 1;
+    in.m = x.size(-2);
+    in.k = x.size(-1);
+    in.sb = in.batch > 1 ? x.stride(0) : 0;
+    in.sm = in.m == 1 ? in.sb : x.stride(-2);
+    in.sk = in.k == 1 ? 1 : x.stride(-1);
+}
+
 int experts_of(const at::Tensor& o, const at::Device& d) {
     if (o.scalar_type() != at::kInt || o.dim() != 1 || !o.is_contiguous() || o.size(0) < 2 || o.device() != d)
         value_error("offsets must be a contiguous int32 [experts + 1] tensor on x's device");
@@ -105,21 +117,10 @@ int experts_of(const at::Tensor& o, const at::Device& d) {
 
 Input input(PyObject* ox, int fmt, PyObject* oscale, PyObject* ooffsets) {
     const at::Tensor& x = cuda_tensor(ox);
+    if (x.dim() != 2 && x.dim() != 3) value_error("x must be 2-D or a batch of 2-D matrices");
     Input in{};
     in.x = &x;
-    if (x.dim() == 2) {
-        in.batch = 1;
-        in.sb = 0;
-    } else if (x.dim() == 3) {
-        in.batch = x.size(0);
-        in.sb = x.stride(0);
-    } else {
-        value_error("x must be 2-D or a batch of 2-D matrices");
-    }
-    in.m = x.size(-2);
-    in.k = x.size(-1);
-    in.sm = x.stride(-2);
-    in.sk = x.stride(-1);
+    layout(x, in);
     in.code = dtype_code(x);
     if (oscale != Py_None && fmt == QL_FP4_NV) {        // FP4_MX has none and takes no notice of one
         if (oscale == g_own) {
@@ -338,14 +339,15 @@ PyObject* f_tensor_scale(Args a) {
     if (x0.dim() != 2 && x0.dim() != 3) value_error("x must be a 2-D or 3-D CUDA tensor");
     const ql_dtype code = dtype_code(x0);
     c10::cuda::CUDAGuard guard(x0.device());
+    Input in{};
+    layout(x0, in);
     at::Tensor x = x0;
-    int64_t m = x.size(-2);
-    if (x.dim() == 3) {
-        if (x.stride(0) != m * x.stride(1)) x = x.contiguous();
-        m *= x.size(0);
+    if (in.batch > 1 && in.sb != in.m * in.sm) {       // its rows do not follow one another: m > 1
+        x = x0.contiguous();
+        layout(x, in);
     }
     at::Tensor out = new_tensor({1}, at::kFloat, x.device());
-    status("fp4_tensor_scale", api.tensor_scale(x.data_ptr(), code, m, x.size(-1), x.stride(-2), x.stride(-1),
+    status("fp4_tensor_scale", api.tensor_scale(x.data_ptr(), code, in.batch * in.m, in.k, in.sm, in.sk,
                                                 out.data_ptr<float>(), stream_of(x.device())));
     return THPVariable_Wrap(out);
 }
@@ -355,8 +357,10 @@ PyObject* f_cast(Args a) {
     const int fmt = format(a[1]);
     Input in = input(a[0], fmt, a[2], a[3]);
     c10::cuda::CUDAGuard guard(in.x->device());
-    if (in.offsets == nullptr && in.sk != 1 && in.sm == 1 && in.k > 1) {
-        // a transposed view: the column-wise cast of the matrix it views
+    const bool turned = in.sk != 1 && in.sm == 1 && in.m > 1;
+    if (in.offsets == nullptr && turned && !(in.own && in.batch > 1 && in.sb != in.k * in.sk)) {
+        // a transposed view: the column-wise cast of the matrix it views (whose scale
+        // needs those matrices to follow one another)
         Input t = in;
         std::swap(t.m, t.k);
         std::swap(t.sm, t.sk);
