@@ -517,7 +517,9 @@ int64_t fp4_row_stride(int64_t k);
 int64_t fp4_column_extent(int64_t m, int experts);
 
 /* Where a call below takes own_scale != 0 (QL_FP4_NV only), it first writes
- * fp4_tensor_scale(x) to *scale (x_scale), which must then not be NULL. */
+ * fp4_tensor_scale(x) to *scale (x_scale), which must then not be NULL; with
+ * offsets, that of the rows [offsets[0], offsets[experts]): what rows of no
+ * expert hold has no influence. */
 
 /* *scale = the least power of two t with max|x| <= 2688 t (2688 = 6 * 448), at
  * least 2^-80; NaN if x holds an infinity or a NaN. x [m, k], any strides. */

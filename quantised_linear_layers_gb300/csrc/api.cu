@@ -626,25 +626,42 @@ int64_t fp4_column_extent(int64_t m, int experts) {
     return ((m + ql::kFp4KAlign - 1) / ql::kFp4KAlign + experts) * ql::kFp4KAlign;
 }
 
-ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k, int64_t x_stride_m,
-                           int64_t x_stride_k, float* scale, ql_stream_t stream) {
+// The scale of x [m, k], or with offsets of its rows that experts have.
+static ql_status fp4_scale_of(const void* x, ql_dtype x_dtype, int64_t m, int64_t k, int64_t x_stride_m, int64_t x_stride_k,
+                              float* scale, const int32_t* offsets, int experts, ql_stream_t stream) {
     if (m < 0 || k < 0 || scale == nullptr || (x_dtype != QL_BF16 && x_dtype != QL_F32)) return QL_ERR_INVALID_ARG;
     if (x == nullptr && m > 0 && k > 0) return QL_ERR_INVALID_ARG;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
-    ql::Bounds bnd{};
-    bnd.s[0] = ql::span_of(x, x_dtype == QL_BF16 ? 2 : 4, m, x_stride_m, k, x_stride_k);
-    bnd.status = di.status;
-    return from_cuda(ql::launch_fp4_tensor_scale(x, x_dtype == QL_BF16, m, k, x_stride_m, x_stride_k, scale, bnd,
-                                                 reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+    ql::Fp4ScaleArgs a{};
+    a.x = x;
+    a.is_bf16 = x_dtype == QL_BF16;
+    a.m = m;
+    a.k = k;
+    a.sxm = x_stride_m;
+    a.sxk = x_stride_k;
+    a.offsets = offsets;
+    a.num_experts = experts;
+    a.t = scale;
+    a.bnd.s[0] = ql::span_of(x, a.is_bf16 ? 2 : 4, m, x_stride_m, k, x_stride_k);
+    a.bnd.s[1] = ql::span_of(offsets, 4, experts + 1, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_fp4_tensor_scale(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
 }
 
-// The scale of x [batch, m, k], whose entries must follow one another as rows do.
+ql_status fp4_tensor_scale(const void* x, ql_dtype x_dtype, int64_t m, int64_t k, int64_t x_stride_m,
+                           int64_t x_stride_k, float* scale, ql_stream_t stream) {
+    return fp4_scale_of(x, x_dtype, m, k, x_stride_m, x_stride_k, scale, nullptr, 0, stream);
+}
+
+// The scale of x [batch, m, k], whose entries must follow one another as rows do
+// (offsets: batch is 1).
 static ql_status fp4_own_scale(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
-                               int64_t x_stride_m, int64_t x_stride_k, float* scale, ql_stream_t stream) {
+                               int64_t x_stride_m, int64_t x_stride_k, float* scale, const int32_t* offsets, int experts,
+                               ql_stream_t stream) {
     if (m == 1) x_stride_m = x_stride_b;         // the stride of a single row says nothing
     if (batch > 1 && x_stride_b != m * x_stride_m) return QL_ERR_UNSUPPORTED;
-    return fp4_tensor_scale(x, x_dtype, batch * m, k, x_stride_m, x_stride_k, scale, stream);
+    return fp4_scale_of(x, x_dtype, batch * m, k, x_stride_m, x_stride_k, scale, offsets, experts, stream);
 }
 
 ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, int64_t k, int64_t x_stride_b,
@@ -687,7 +704,8 @@ ql_status fp4_cast(const void* x, ql_dtype x_dtype, int64_t batch, int64_t m, in
     a.bnd.s[3] = ql::span_of(offsets, 4, experts + 1, 1);
     a.bnd.status = di.status;
     if (own_scale)
-        if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, x_stride_k, scale, stream);
+        if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, x_stride_k, scale, offsets,
+                                        experts, stream);
             s != QL_OK)
             return s;
     return from_cuda(ql::launch_fp4_cast(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
@@ -745,7 +763,8 @@ ql_status fp4_cast_dual(const void* x, ql_dtype x_dtype, int64_t batch, int64_t 
     a.bnd.s[5] = ql::span_of(sf_cols, 1, batch * a.sscb, 1);
     a.bnd.status = di.status;
     if (own_scale)
-        if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, 1, scale, stream); s != QL_OK)
+        if (ql_status s = fp4_own_scale(x, x_dtype, batch, m, k, x_stride_b, x_stride_m, 1, scale, offsets, experts, stream);
+            s != QL_OK)
             return s;
     return from_cuda(ql::launch_fp4_cast_dual(a, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -871,7 +890,9 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
     if (x_dtype != QL_BF16 && x_dtype != QL_F32) return QL_ERR_INVALID_ARG;
     if (m < 0 || n < 0 || k < 0 || (own_scale && (x_scale == nullptr || fmt != QL_FP4_NV))) return QL_ERR_INVALID_ARG;
-    if (n == 0) return own_scale ? fp4_tensor_scale(x, x_dtype, m, k, x_stride_m, 1, x_scale, stream) : QL_OK;
+    if (offsets != nullptr && experts < 1) return QL_ERR_INVALID_ARG;
+    if (n == 0)
+        return own_scale ? fp4_scale_of(x, x_dtype, m, k, x_stride_m, 1, x_scale, offsets, experts, stream) : QL_OK;
     const int64_t ldq = fp4_row_stride(k);
     uint8_t* q = static_cast<uint8_t*>(workspace);
     if (m > ql::fp4_cast_rows(offsets != nullptr ? experts : 0) || m == 0 || k == 0) {
@@ -889,12 +910,11 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
                                         experts, m, n, k, stream);
     }
     if (n >= kInt31 || k >= kInt31) return QL_ERR_UNSUPPORTED;
-    if (offsets != nullptr && experts < 1) return QL_ERR_INVALID_ARG;
     if (offsets != nullptr && (experts > ql::kFp4MaxExperts || experts * n >= kInt31)) return QL_ERR_UNSUPPORTED;
     if (x == nullptr || d == nullptr || ldd < n) return QL_ERR_INVALID_ARG;
     if (ql_status s = fp4_operand(w, ldw, sfw, k); s != QL_OK) return s;
     if (own_scale)
-        if (ql_status s = fp4_tensor_scale(x, x_dtype, m, k, x_stride_m, 1, x_scale, stream); s != QL_OK) return s;
+        if (ql_status s = fp4_scale_of(x, x_dtype, m, k, x_stride_m, 1, x_scale, offsets, experts, stream); s != QL_OK) return s;
     ql::Fp4GemmArgs a{};
     a.xr = x;
     a.xr_bf16 = x_dtype == QL_BF16;

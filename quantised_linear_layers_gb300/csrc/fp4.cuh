@@ -83,6 +83,19 @@ struct Fp4DualArgs {
     Bounds bnd;                // x, row codes, row scales, offsets, column codes, column scales
 };
 
+// The scale t of x [m][k], or of the rows that experts have: [offsets[0],
+// offsets[num_experts]), inside [0, m].
+struct Fp4ScaleArgs {
+    const void* x;
+    bool is_bf16;
+    int64_t m, k;
+    int64_t sxm, sxk;
+    const int32_t* offsets;    // or null
+    int num_experts;
+    float* t;
+    Bounds bnd;                // x, offsets
+};
+
 struct Fp4DequantArgs {
     const uint8_t* q;
     int64_t ldq;
@@ -99,8 +112,7 @@ struct Fp4DequantArgs {
 cudaError_t launch_fp4_cast(const Fp4CastArgs& a, cudaStream_t st, int num_sms);
 cudaError_t launch_fp4_cast_dual(const Fp4DualArgs& a, cudaStream_t st);
 cudaError_t launch_fp4_dequant(const Fp4DequantArgs& a, cudaStream_t st, int num_sms);
-cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int64_t k, int64_t sxm, int64_t sxk, float* t,
-                                    const Bounds& bnd, cudaStream_t st, int num_sms);
+cudaError_t launch_fp4_tensor_scale(const Fp4ScaleArgs& a, cudaStream_t st, int num_sms);
 
 #ifdef __CUDACC__
 // Larger of two magnitudes; a NaN operand gives NaN. The bf16 form takes two

@@ -468,37 +468,57 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const Fp4DequantA
 // memory, and no word has to be set to zero by a launch of its own.
 constexpr int kClusterThreads = 1024;
 
-template <typename T, int ROWS, bool CLUSTER>
-__global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kThreads) fp4_tscale_kernel(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk,
-                                                              uint32_t* tscale, const Bounds bnd) {
+// FLAT: the rows lie one after the other and are taken as one.
+template <typename T, int ROWS, bool FLAT, bool CLUSTER>
+__global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kThreads) fp4_tscale_kernel(const Fp4ScaleArgs p) {
     pdl_launch_dependents();
     pdl_wait_prior();
     constexpr int kBlock = CLUSTER ? kClusterThreads : kThreads;
+    const T* x = static_cast<const T*>(p.x);
+    uint32_t* tscale = reinterpret_cast<uint32_t*>(p.t);
     float best = 0.0f;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlock;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
+    // rows [r0, r1), columns [lo, hi)
+    int64_t r0 = 0, r1 = p.m, lo = 0, hi = p.k;
+    if (p.offsets != nullptr && QL_IN(p.bnd, 1, p.offsets, 4) && QL_IN(p.bnd, 1, p.offsets + p.num_experts, 4)) {
+        const int64_t a = __ldg(p.offsets), b = __ldg(p.offsets + p.num_experts);
+        r0 = a < 0 ? 0 : (a > p.m ? p.m : a);
+        r1 = b < r0 ? r0 : (b > p.m ? p.m : b);
+    }
+    if constexpr (FLAT) {
+        lo = r0 * p.k;
+        hi = r1 * p.k;
+        r0 = 0;
+        r1 = 1;
+    }
     if constexpr (ROWS == kRowsVec) {
-        const int64_t per_row = (k + 15) / 16;
+        const int64_t per_row = (hi + 15) / 16;
 #pragma unroll 2
-        for (int64_t i = first; i < m * per_row; i += stride) {
-            const int64_t row = m == 1 ? 0 : i / per_row, c = (i - row * per_row) * 16;
+        for (int64_t i = r0 * per_row + lo / 16 + first; i < r1 * per_row; i += stride) {
+            const int64_t row = FLAT ? 0 : i / per_row, c = (i - row * per_row) * 16;
             Raw16<T> raw;
-            if (c + 16 <= k) raw.load(x + row * sxm + c, bnd, 0);
-            else raw.load_some(x + row * sxm + c, 1, static_cast<int>(k - c), bnd, 0);
+            if ((!FLAT || c >= lo) && c + 16 <= hi) {
+                raw.load(x + row * p.sxm + c, p.bnd, 0);
+            } else {
+                const int64_t c0 = c < lo ? lo : c, n = hi - c0;
+                raw.load_some(x + row * p.sxm + c0, 1, static_cast<int>(n < c + 16 - c0 ? n : c + 16 - c0), p.bnd, 0);
+            }
             best = max_nan(best, raw.amax());
         }
     } else {
         // one element per lane and load, eight loads in flight
         constexpr int kPiece = 8 * 32;
         const int lane = threadIdx.x & 31;
-        const int64_t per_row = (k + kPiece - 1) / kPiece;
-        for (int64_t i = first >> 5; i < m * per_row; i += stride >> 5) {
-            const int64_t row = i / per_row, c0 = (i - row * per_row) * kPiece + lane;
+        const int64_t per_row = (hi + kPiece - 1) / kPiece;
+        for (int64_t i = r0 * per_row + lo / kPiece + (first >> 5); i < r1 * per_row; i += stride >> 5) {
+            const int64_t row = FLAT ? 0 : i / per_row, c0 = (i - row * per_row) * kPiece + lane;
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const T* e = x + row * sxm + (c0 + j * 32) * sxk;
-                v[j] = c0 + j * 32 < k && QL_IN(bnd, 0, e, sizeof(T)) ? static_cast<float>(*e) : 0.0f;
+                const int64_t c = c0 + j * 32;
+                const T* e = x + row * p.sxm + c * p.sxk;
+                v[j] = c < hi && (!FLAT || c >= lo) && QL_IN(p.bnd, 0, e, sizeof(T)) ? static_cast<float>(*e) : 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) best = max_nan(best, fabsf(v[j]));
@@ -626,25 +646,25 @@ cudaError_t dequant_t(const Fp4DequantArgs& a, cudaStream_t st, int num_sms) {
     return launch(fp4_dequant_kernel<FMT, T, true, 1>, dim3(x, column_blocks(a.m, pieces, num_sms)), 0, st, a);
 }
 
-template <typename T>
-cudaError_t tscale_t(const T* x, int64_t m, int64_t k, int64_t sxm, int64_t sxk, uint32_t* out, const Bounds& bnd, cudaStream_t st, int num_sms) {
-    if (sxk == 1 && sxm == k) {        // one long row: only its end is ragged
-        k *= m;
-        m = 1;
-        sxm = k;
-    }
-    const bool vec = vec_ok(x, sizeof(T), m > 1 ? sxm : 0, sxk, 0);
+template <typename T, int ROWS, bool FLAT>
+cudaError_t tscale_v(const Fp4ScaleArgs& a, cudaStream_t st, int num_sms) {
     // one cluster / zeroing and atomics: 0.5 MB 3.1 / 5.0 us, 1 MB 3.8 / 4.7, 2 MB 5.3 / 6.0, 4 MB 7.9 / 6.2
-    if (m * k * static_cast<int64_t>(sizeof(T)) <= (2 << 20)) {
-        return vec ? launch_cluster(fp4_tscale_kernel<T, kRowsVec, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out, bnd)
-                   : launch_cluster(fp4_tscale_kernel<T, kRowsStrided, true>, dim3(8), kClusterThreads, 8, 0, st, x, m, k, sxm, sxk, out, bnd);
-    }
-    if (cudaError_t e = cudaMemsetAsync(out, 0, 4, st); e != cudaSuccess) return e;
-    int64_t grid = vec ? (m * ((k + 15) / 16) + kThreads - 1) / kThreads : (m * ((k + 255) / 256) + 7) / 8;
+    if (a.m * a.k * static_cast<int64_t>(sizeof(T)) <= (2 << 20))
+        return launch_cluster(fp4_tscale_kernel<T, ROWS, FLAT, true>, dim3(8), kClusterThreads, 8, 0, st, a);
+    if (cudaError_t e = cudaMemsetAsync(a.t, 0, 4, st); e != cudaSuccess) return e;
+    const int64_t rows = FLAT ? 1 : a.m, cols = FLAT ? a.m * a.k : a.k;
+    int64_t grid = ROWS == kRowsVec ? (rows * ((cols + 15) / 16) + kThreads - 1) / kThreads : (rows * ((cols + 255) / 256) + 7) / 8;
     if (grid > static_cast<int64_t>(num_sms) * 8) grid = static_cast<int64_t>(num_sms) * 8;
-    const dim3 g(static_cast<unsigned>(grid < 1 ? 1 : grid));
-    return vec ? launch(fp4_tscale_kernel<T, kRowsVec, false>, g, 0, st, x, m, k, sxm, sxk, out, bnd)
-               : launch(fp4_tscale_kernel<T, kRowsStrided, false>, g, 0, st, x, m, k, sxm, sxk, out, bnd);
+    return launch(fp4_tscale_kernel<T, ROWS, FLAT, false>, dim3(static_cast<unsigned>(grid < 1 ? 1 : grid)), 0, st, a);
+}
+
+template <typename T>
+cudaError_t tscale_t(const Fp4ScaleArgs& a, cudaStream_t st, int num_sms) {
+    // one long row if they follow one another: only its ends are ragged
+    const bool flat = a.sxk == 1 && (a.sxm == a.k || a.m == 1);
+    if (vec_ok(a.x, sizeof(T), flat ? 0 : a.sxm, a.sxk, 0))
+        return flat ? tscale_v<T, kRowsVec, true>(a, st, num_sms) : tscale_v<T, kRowsVec, false>(a, st, num_sms);
+    return flat ? tscale_v<T, kRowsStrided, true>(a, st, num_sms) : tscale_v<T, kRowsStrided, false>(a, st, num_sms);
 }
 
 }  // namespace
@@ -670,11 +690,8 @@ cudaError_t launch_fp4_dequant(const Fp4DequantArgs& a, cudaStream_t st, int num
     return a.out_bf16 ? dequant_t<kFp4Mx, __nv_bfloat16>(a, st, num_sms) : dequant_t<kFp4Mx, float>(a, st, num_sms);
 }
 
-cudaError_t launch_fp4_tensor_scale(const void* x, bool is_bf16, int64_t m, int64_t k, int64_t sxm, int64_t sxk, float* t,
-                                    const Bounds& bnd, cudaStream_t st, int num_sms) {
-    uint32_t* out = reinterpret_cast<uint32_t*>(t);
-    if (is_bf16) return tscale_t(static_cast<const __nv_bfloat16*>(x), m, k, sxm, sxk, out, bnd, st, num_sms);
-    return tscale_t(static_cast<const float*>(x), m, k, sxm, sxk, out, bnd, st, num_sms);
+cudaError_t launch_fp4_tensor_scale(const Fp4ScaleArgs& a, cudaStream_t st, int num_sms) {
+    return a.is_bf16 ? tscale_t<__nv_bfloat16>(a, st, num_sms) : tscale_t<float>(a, st, num_sms);
 }
 
 }  // namespace ql

@@ -17,7 +17,7 @@ the rounding: they are those of the product of the cast operands. Experts
 ``offsets`` on the device; loads may be anything, zero included.
 
 FP4_NV casts of a training step use the tensor's own scale
-(``ops.fp4_tensor_scale``). A forward-only call takes X's scale as given, 1 by
+(``ops.fp4_tensor_scale``; with experts, that of the rows they have). A forward-only call takes X's scale as given, 1 by
 default: group scales then span 2^-9 .. 448, the range of normalised
 activations, and X is read once.
 """

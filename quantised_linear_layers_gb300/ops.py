@@ -547,8 +547,8 @@ def fp4_cast(x: torch.Tensor, fmt: int = FP4_NV, tensor_scale: torch.Tensor | No
              offsets: torch.Tensor | None = None) -> FP4Tensor:
     """Casts the rows of x [m, k] or [batch, m, k] (bf16 or fp32, any strides) to
     4 bits. ``tensor_scale`` (FP4_NV): one fp32 value on the device, None for 1,
-    or FP4_OWN_SCALE for ``fp4_tensor_scale(x)``, made in the call; FP4_MX has none
-    and takes no notice of it. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and the cast is the
+    or FP4_OWN_SCALE for ``fp4_tensor_scale(x)``, made in the call (with offsets, of
+    the experts' rows alone); FP4_MX has none and takes no notice of it. ``offsets`` (int32 [experts + 1]): x's rows are sorted by expert and the cast is the
     operand of ``gemm_fp4_nt_ragged``; rows of no expert are left out."""
     return (_fp4 or _load_fp4()).cast(x, fmt, tensor_scale, offsets)
 
