@@ -501,6 +501,9 @@ int ql_bounds_checked(void);
  * ------------------------------------------------------------------------- */
 #define QL_FP4_NV 0
 #define QL_FP4_MX 1
+/* Added to the fmt of gemm_fp4_nt_ragged and fp4_linear: rows of D that no expert
+ * has become zero. Without it they are not written. */
+#define QL_FP4_ZERO_REST 0x100
 
 /* Bytes of the scales of a cast of `rows` rows and k columns; experts > 0: of a
  * row-wise cast by expert. -1 for an unknown format or a negative size. */
@@ -556,7 +559,7 @@ ql_status gemm_fp4_nt(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const f
 
 /* Experts: rows [offsets[e], offsets[e+1]) of D [m, n] = the same rows of X
  * times W[e]^T. X [m, k] cast with the offsets, W [experts, n, k] cast as a
- * batch. Rows of no expert are not written. k == 0 is refused. */
+ * batch. Rows of no expert: see QL_FP4_ZERO_REST. k == 0 is refused. */
 ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale,
                              const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt,
                              void* d, ql_dtype d_dtype, int64_t ldd, const int32_t* offsets, int experts, int64_t m,
@@ -564,7 +567,8 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
 
 /* The forward call: casts X [m, k] (bf16 or fp32, contiguous rows, row stride
  * x_stride_m) and multiplies, D [m, n] bf16 = X W^T, or by expert with offsets
- * (W [experts, n, k]). Equal to fp4_cast and gemm_fp4_nt / gemm_fp4_nt_ragged;
+ * (W [experts, n, k]; rows of no expert: see QL_FP4_ZERO_REST). Equal to
+ * fp4_cast and gemm_fp4_nt / gemm_fp4_nt_ragged;
  * up to 8 rows (16 with experts) are cast inside the product, in one launch and without a
  * workspace. fp4_linear_workspace_size bytes of device memory, 16-byte aligned,
  * are needed otherwise (0: none); they may be reused once the stream is past

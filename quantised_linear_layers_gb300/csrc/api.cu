@@ -851,6 +851,8 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
                              const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt,
                              void* d, ql_dtype d_dtype, int64_t ldd, const int32_t* offsets, int experts, int64_t m,
                              int64_t n, int64_t k, ql_stream_t stream) {
+    const bool zero_rest = (fmt & QL_FP4_ZERO_REST) != 0;
+    fmt &= ~QL_FP4_ZERO_REST;
     if (m < 0 || n < 0 || k < 0 || experts < 1) return QL_ERR_INVALID_ARG;
     if (m >= kInt31 || n >= kInt31 || k >= kInt31 || experts > ql::kFp4MaxExperts || experts * n >= kInt31)
         return QL_ERR_UNSUPPORTED;
@@ -873,6 +875,7 @@ ql_status gemm_fp4_nt_ragged(const uint8_t* x, int64_t ldx, const uint8_t* sfx, 
     a.n = n;
     a.k = k;
     a.rows = m;
+    a.zero_rest = zero_rest;
     a.d = d;
     a.ldd = ldd;
     return fp4_gemm_common(a, offsets, experts, d_dtype, 0, stream);
@@ -887,6 +890,8 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
                      const uint8_t* w, int64_t ldw, const uint8_t* sfw, const float* w_scale, int fmt, void* d, int64_t ldd,
                      const int32_t* offsets, int experts, int64_t m, int64_t n, int64_t k, void* workspace,
                      size_t workspace_bytes, ql_stream_t stream) {
+    const int zero_rest = fmt & QL_FP4_ZERO_REST;
+    fmt &= ~QL_FP4_ZERO_REST;
     if (fmt != QL_FP4_NV && fmt != QL_FP4_MX) return QL_ERR_INVALID_ARG;
     if (x_dtype != QL_BF16 && x_dtype != QL_F32) return QL_ERR_INVALID_ARG;
     if (m < 0 || n < 0 || k < 0 || (own_scale && (x_scale == nullptr || fmt != QL_FP4_NV))) return QL_ERR_INVALID_ARG;
@@ -906,7 +911,7 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
             return s;
         return offsets == nullptr
                    ? gemm_fp4_nt(q, ldq, sf, x_scale, w, ldw, sfw, w_scale, fmt, d, QL_BF16, ldd, m, n, k, 0, stream)
-                   : gemm_fp4_nt_ragged(q, ldq, sf, x_scale, w, ldw, sfw, w_scale, fmt, d, QL_BF16, ldd, offsets,
+                   : gemm_fp4_nt_ragged(q, ldq, sf, x_scale, w, ldw, sfw, w_scale, fmt | zero_rest, d, QL_BF16, ldd, offsets,
                                         experts, m, n, k, stream);
     }
     if (n >= kInt31 || k >= kInt31) return QL_ERR_UNSUPPORTED;
@@ -929,6 +934,7 @@ ql_status fp4_linear(const void* x, ql_dtype x_dtype, int64_t x_stride_m, float*
     a.offsets = offsets;
     a.experts = offsets == nullptr ? 0 : experts;
     a.rows = m;
+    a.zero_rest = zero_rest != 0;
     a.m = m;
     a.n = n;
     a.k = k;

@@ -430,6 +430,8 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
             tc_fence_before_sync();
             if (any) mbar_arrive(&tempty[as]);
         }
+    } else if (p.zero_rest) {
+        fp4_zero_rest<OUT_F32>(p, s_off);
     }
     if constexpr (SPLIT) {
         // one tile per cluster: the partial tiles are in every CTA's shared memory
@@ -574,6 +576,7 @@ void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
     p.d = a.d;
     p.ldd = a.ldd;
     p.accumulate = a.accumulate;
+    p.zero_rest = a.form == kFp4RagRows && a.zero_rest;
     p.dev_status = a.dev_status;
     p.wait_limit_ns = a.wait_limit_ns;
     p.stall_producer = a.stall_producer;

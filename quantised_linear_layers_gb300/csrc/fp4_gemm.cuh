@@ -42,6 +42,7 @@ struct Fp4GemmArgs {
     int64_t ldd;
     bool out_f32;
     int accumulate;
+    bool zero_rest;              // ragged rows: rows of no expert become zero
     // X not cast yet (m <= fp4_cast_rows): the product casts it itself
     const void* xr;
     bool xr_bf16;
@@ -77,6 +78,7 @@ struct Fp4GemmParams {
     int64_t sxr;
     int k, xr_vec;               // columns; rows start on 16 bytes
     Bounds bnd;                  // D, offsets, X before the cast
+    int zero_rest;
     int ahead;                   // stages of W brought into L2 before the previous kernel ends
 };
 
@@ -164,6 +166,32 @@ __device__ __forceinline__ void fp4_load_offsets(int* s_off, const Fp4GemmParams
         carry = __shfl_sync(0xffffffffu, v, 31);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) atomicOr(p.dev_status, kDevErrBadIndex);
+}
+
+// Zeros in the rows of D before the first and after the last expert's: warps 2
+// and 3 of every CTA, which have nothing else to do by then, a row at a time.
+template <bool OUT_F32>
+__device__ __forceinline__ void fp4_zero_rest(const Fp4GemmParams& p, const int* s_off) {
+    constexpr int es = OUT_F32 ? 4 : 2, kVec = 16 / es;
+    const int lane = threadIdx.x & 31;
+    const int before = s_off[0], after = s_off[p.experts];
+    const int rest = before + p.m - after;
+    uint8_t* d = static_cast<uint8_t*>(p.d);
+    const bool vec = ((reinterpret_cast<uintptr_t>(d) | static_cast<uintptr_t>(p.ldd * es)) & 15u) == 0;
+    for (int64_t i = blockIdx.x * 2 + (threadIdx.x >> 5) - 2; i < rest; i += gridDim.x * 2) {
+        uint8_t* row = d + (i < before ? i : after + (i - before)) * p.ldd * es;
+        int c = 0;
+        if (vec) {
+            for (int j = lane; j < p.n / kVec; j += 32)
+                if (QL_IN(p.bnd, 0, row + 16 * static_cast<int64_t>(j), 16)) *reinterpret_cast<uint4*>(row + 16 * static_cast<int64_t>(j)) = make_uint4(0, 0, 0, 0);
+            c = p.n / kVec * kVec;
+        }
+        for (int64_t j = c + lane; j < p.n; j += 32) {
+            if (!QL_IN(p.bnd, 0, row + j * es, es)) continue;
+            if constexpr (OUT_F32) *reinterpret_cast<float*>(row + j * es) = 0.0f;
+            else *reinterpret_cast<uint16_t*>(row + j * es) = 0;
+        }
+    }
 }
 
 // One tile of D.

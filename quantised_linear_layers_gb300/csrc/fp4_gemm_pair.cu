@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait_drain(done_bar, 0, p.wait_limit_ns);
             }
             __syncwarp();
+        } else if (warp >= 2 && p.zero_rest) {
+            fp4_zero_rest<OUT_F32>(p, s_off);
         }
     } else {
         regs_alloc<184>();

@@ -252,15 +252,18 @@ void same_kind(const Operand& x, const Operand& w) {
 }
 
 // The output: given (checked) or new. D's row stride is its second last stride.
+// Rows that no expert has are left alone in a given one and zero in a new one.
 struct Out {
     at::Tensor t;
     ql_dtype code;
     int64_t ld;
+    int zero_rest;       // QL_FP4_ZERO_REST for a new one
 };
 Out output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const at::Device& d, bool accumulate) {
-    Out r;
+    Out r{};
     if (o == Py_None) {
         if (accumulate) value_error("accumulate needs an existing out");
+        r.zero_rest = QL_FP4_ZERO_REST;
         r.t = new_tensor(shape, type, d);
     } else {
         r.t = tensor(o, "out must be a tensor");
@@ -312,7 +315,7 @@ void launch_gemm(const Operand& x, const Operand& w, const Out& d, bool accumula
 }
 void launch_ragged(const Operand& x, const Operand& w, const int32_t* offsets, const Out& d) {
     status("gemm_fp4_nt_ragged",
-           api.ragged(x.q, x.ld, x.sf, x.scale, w.q, w.ld, w.sf, w.scale, x.fmt, d.t.data_ptr(), d.code, d.ld, offsets,
+           api.ragged(x.q, x.ld, x.sf, x.scale, w.q, w.ld, w.sf, w.scale, x.fmt | d.zero_rest, d.t.data_ptr(), d.code, d.ld, offsets,
                       static_cast<int>(w.batch), x.rows, w.rows, x.cols, stream_of(x.device)));
 }
 void launch_wgrad(const Operand& y, const Operand& x, const int32_t* offsets, int experts, const Out& d, bool accumulate) {
@@ -471,8 +474,8 @@ PyObject* f_linear(Args a) {
         p = static_cast<uint8_t*>(ws.get());
     }
     status("fp4_linear", api.linear(in.x->data_ptr(), in.code, in.sm, in.own ? reinterpret_cast<float*>(p + size) : in.scale,
-                                    in.own, w.q, w.ld, w.sf, w.scale, w.fmt, d.t.data_ptr(), d.ld, in.offsets, in.experts,
-                                    in.m, w.rows, in.k, p, static_cast<size_t>(size), stream_of(w.device)));
+                                    in.own, w.q, w.ld, w.sf, w.scale, w.fmt | d.zero_rest, d.t.data_ptr(), d.ld, in.offsets,
+                                    in.experts, in.m, w.rows, in.k, p, static_cast<size_t>(size), stream_of(w.device)));
     return THPVariable_Wrap(d.t);
 }
 

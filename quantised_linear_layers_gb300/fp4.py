@@ -14,7 +14,9 @@ The tensor core takes 4-bit operands with the summed axis contiguous only, so W,
 X and dY are each cast both ways from one read. Gradients pass straight through
 the rounding: they are those of the product of the cast operands. Experts
 (``FP4ExpertWeight``, ``experts_*``): tokens sorted by expert with int32
-``offsets`` on the device; loads may be anything, zero included.
+``offsets`` on the device; loads may be anything, zero included. Rows before the
+first and after the last expert's, as in a batch padded to a fixed capacity, have
+no influence on any result and are zero in Y and dX (unwritten in a given ``out``).
 
 FP4_NV casts of a training step use the tensor's own scale
 (``ops.fp4_tensor_scale``; with experts, that of the rows they have). A forward-only call takes X's scale as given, 1 by

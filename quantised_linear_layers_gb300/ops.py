@@ -579,7 +579,7 @@ def gemm_fp4_nt_ragged(x: FP4Tensor, w: FP4Tensor, out: torch.Tensor | None = No
                        dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """Experts' products: rows offsets[e] .. offsets[e+1] of D [m, n] are those
     rows of X [m, k] times W[e]^T; X cast with the offsets, W [experts, n, k] cast
-    as a batch. Rows of no expert are left unwritten in ``out``."""
+    as a batch. Rows of no expert are zero, or left unwritten in a given ``out``."""
     return (_fp4 or _load_fp4()).ragged(x, w, out, _is_bf16(dtype))
 
 
@@ -595,7 +595,8 @@ def fp4_linear(x: torch.Tensor, w: FP4Tensor, x_scale: torch.Tensor | None = Non
                offsets: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """The forward call, cast and product in one: D [m, n] bf16 = X W^T of
     x [m, k] (bf16 or fp32) and a cast W [n, k]; with ``offsets`` (int32
-    [experts + 1]) by expert, W [experts, n, k]. Equal to ``fp4_cast`` followed by
+    [experts + 1]) by expert, W [experts, n, k]; rows of no expert are zero, or left
+    unwritten in a given ``out``. Equal to ``fp4_cast`` followed by
     ``gemm_fp4_nt`` or ``gemm_fp4_nt_ragged``; up to 8 rows (16 with experts) take one launch.
     ``x_scale`` as ``fp4_cast``'s tensor_scale."""
     return (_fp4 or _load_fp4()).linear(x, w, x_scale, offsets, out)
