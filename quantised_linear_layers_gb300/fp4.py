@@ -188,42 +188,46 @@ class FP4Linear(torch.nn.Module):
 
     def forget_casts(self) -> None:
         """Has the next forward cast the weight anew."""
-        self._w4 = self._w4_of = self._w4_made = None
+        self._kept = None
 
     def __getstate__(self):
         # a copy makes casts of its own
-        return {**self.__dict__, "_w4": None, "_w4_of": None, "_w4_made": None, "_w4_in_graphs": [],
-                "_trained_in_graph": False}
+        return {**self.__dict__, "_kept": None, "_w4_in_graphs": [], "_trained_in_graph": False}
 
     def fp4_weight(self, dgrad: bool = True) -> FP4Weight:
         """The weight's casts, made anew when the weight has changed."""
         w = self.weight
         capturing = w.is_cuda and torch.cuda.is_current_stream_capturing()
-        of = self._w4_of
-        # `of` keeps the storage that was cast, so that no other can have its address
-        kept = (self._w4 is not None and not self._trained_in_graph and (self._w4.dgrad or not dgrad) and
-                of[0] == w._version and of[1].data_ptr() == w.data_ptr() and of[1].device == w.device and
-                of[1].dtype == w.dtype)
+        # (casts, version and storage of what was cast, stream and event behind the
+        # casts): one object, set and read at once, since other threads do too. It keeps
+        # the storage, so that no other can have its address.
+        kept = self._kept
+        if kept is not None:
+            w4, version, of = kept[:3]
+            if (self._trained_in_graph or (dgrad and not w4.dgrad) or version != w._version or
+                    of.data_ptr() != w.data_ptr() or of.device != w.device or of.dtype != w.dtype):
+                kept = None
         training = capturing and torch.is_grad_enabled() and w.requires_grad
-        self._trained_in_graph |= training
-        if training or (capturing and not kept):
+        if training:
+            self._trained_in_graph = True
+        if training or (capturing and kept is None):
             return self._cast(dgrad)     # part of the graph: not for calls outside it
-        if not kept:
-            self._w4 = self._cast(dgrad)
-            self._w4_of = (w._version, w.detach())
+        if kept is None:
+            version, of = w._version, w.detach()
+            w4 = self._cast(dgrad)
             stream = torch.cuda.current_stream(w.device)
-            self._w4_made = (stream, stream.record_event())
+            self._kept = (w4, version, of, stream, stream.record_event())
         elif capturing:
-            if self._w4 not in self._w4_in_graphs:
-                self._w4_in_graphs.append(self._w4)
+            if w4 not in self._w4_in_graphs:
+                self._w4_in_graphs.append(w4)
         else:
             stream = torch.cuda.current_stream(w.device)
-            if stream != self._w4_made[0]:
-                stream.wait_event(self._w4_made[1])
-                for c in (self._w4.w, self._w4.wt):
+            if stream != kept[3]:
+                stream.wait_event(kept[4])
+                for c in (w4.w, w4.wt):
                     if c is not None:
                         c.buf.record_stream(stream)
-        return self._w4
+        return w4
 
     def _cast(self, dgrad: bool) -> FP4Weight:
         with torch.no_grad():
