@@ -489,7 +489,8 @@ int ql_bounds_checked(void);
  *   scales  uint8 blocks of 128 rows x 4 groups, [ceil(rows/128)]
  *           [ceil(groups/4)][512]: row r, group g of a block at byte
  *           (r % 32) * 16 + (r / 32) * 4 + g; 16-byte aligned. Bytes of groups
- *           past the last are zero; bytes of rows past the last are unspecified.
+ *           past the last are zero, in a column-wise cast by expert also those
+ *           past an expert's last; bytes of rows past the last are unspecified.
  *   experts rows sorted by expert, offsets int32 [experts + 1] on the device:
  *           expert e has rows [offsets[e], offsets[e+1]) of [0, m). A row-wise
  *           cast starts a new 128-row scale block with every expert; a

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dual_kernel(const Fp4DualArgs p)
                 const int gi = FMT == kFp4Nv ? tq * 2 + h : tq;
                 if (FMT == kFp4Nv || h == 0)
                     smem[S::kOffSfc + (gi >> 2) * kFp4SfBlock + (col & 31) * 16 + (col >> 5) * 4 + (gi & 3)] =
-                        static_cast<uint8_t>(g.byte);
+                        gi * fp4_group(FMT) < rows ? static_cast<uint8_t>(g.byte) : 0;
             }
             *reinterpret_cast<uint4*>(smem + S::kOffCol + col * S::kColPitch + tq * 16) =
                 make_uint4(out[0].x, out[0].y, out[1].x, out[1].y);
