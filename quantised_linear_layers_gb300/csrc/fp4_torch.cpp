@@ -14,6 +14,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cuda_runtime_api.h>
+
+#include <atomic>
 #include <cstdint>
 #include <exception>
 #include <stdexcept>
@@ -548,6 +551,56 @@ PyObject* f_linear_backward(Args a) {
     return res;
 }
 
+// Objects that graphs hold, and those whose graphs are gone: a list, since the
+// runtime says so on a thread of its own, which may call neither Python nor CUDA.
+struct Held {
+    PyObject* object;
+    Held* next;
+};
+std::atomic<Held*> g_dropped{nullptr};
+void CUDART_CB graph_gone(void* p) {
+    Held* h = static_cast<Held*>(p);
+    h->next = g_dropped.load(std::memory_order_relaxed);
+    while (!g_dropped.compare_exchange_weak(h->next, h, std::memory_order_release, std::memory_order_relaxed)) {
+    }
+}
+void check_cuda(cudaError_t e) {
+    if (e != cudaSuccess) throw std::runtime_error(cudaGetErrorString(e));
+}
+
+// (object): kept alive by the graph that the current stream captures into, and by
+// every executable made from it.
+PyObject* f_hold(Args a) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaGraph_t graph = nullptr;
+    check_cuda(cudaStreamGetCaptureInfo(c10::cuda::getCurrentCUDAStream().stream(), &status, &id, &graph));
+    if (status != cudaStreamCaptureStatusActive || graph == nullptr) value_error("the current stream captures no graph");
+    Held* h = new Held{Py_NewRef(a[0]), nullptr};
+    cudaUserObject_t object;
+    if (cudaError_t e = cudaUserObjectCreate(&object, h, graph_gone, 1, cudaUserObjectNoDestructorSync); e != cudaSuccess) {
+        Py_DECREF(h->object);
+        delete h;
+        check_cuda(e);
+    }
+    if (cudaError_t e = cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove); e != cudaSuccess) {
+        cudaUserObjectRelease(object, 1);
+        check_cuda(e);
+    }
+    Py_RETURN_NONE;
+}
+
+// (): lets go of what only graphs held that are gone.
+PyObject* f_drop(Args) {
+    for (Held* h = g_dropped.exchange(nullptr, std::memory_order_acquire); h != nullptr;) {
+        Held* next = h->next;
+        Py_DECREF(h->object);
+        delete h;
+        h = next;
+    }
+    Py_RETURN_NONE;
+}
+
 template <PyObject* (*F)(Args), int N>
 PyObject* entry(PyObject*, Args a, Py_ssize_t n) {
     if (n != N) {
@@ -620,6 +673,8 @@ PyMethodDef methods[] = {
     {"wgrad", cfunction(entry<f_wgrad, 4>), METH_FASTCALL, nullptr},
     {"linear", cfunction(entry<f_linear, 5>), METH_FASTCALL, nullptr},
     {"linear_saving", cfunction(entry<f_linear_saving, 4>), METH_FASTCALL, nullptr},
+    {"hold_in_graph", cfunction(entry<f_hold, 1>), METH_FASTCALL, nullptr},
+    {"drop_held", cfunction(entry<f_drop, 0>), METH_FASTCALL, nullptr},
     {"linear_backward", cfunction(entry<f_linear_backward, 7>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

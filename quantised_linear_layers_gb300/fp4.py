@@ -169,7 +169,8 @@ class FP4Linear(torch.nn.Module):
     neither; call ``forget_casts`` after one. In a CUDA graph a training step casts
     the weight anew with every replay, and since replays may change the weight
     unseen, calls outside the graph keep no casts from then on; a forward without
-    gradients uses the casts kept when it was captured."""
+    gradients uses the casts kept when it was captured, which live as long as the
+    graph (their memory is free for others with the first cast after its end)."""
 
     _weight_type = FP4Weight
 
@@ -183,17 +184,17 @@ class FP4Linear(torch.nn.Module):
         torch.nn.init.normal_(self.weight, std=0.02)
         self.fmt = fmt
         self.main_grad = torch.zeros(shape, device=device, dtype=torch.float32) if accumulate_main_grad else None
-        self._w4_in_graphs = []          # casts that captured graphs read
         self._trained_in_graph = False
         self.forget_casts()
 
     def forget_casts(self) -> None:
         """Has the next forward cast the weight anew."""
         self._kept = None
+        ops._drop_held()
 
     def __getstate__(self):
         # a copy makes casts of its own
-        return {**self.__dict__, "_kept": None, "_w4_in_graphs": [], "_trained_in_graph": False}
+        return {**self.__dict__, "_kept": None, "_trained_in_graph": False}
 
     def fp4_weight(self, dgrad: bool = True) -> FP4Weight:
         """The weight's casts, made anew when the weight has changed."""
@@ -214,13 +215,13 @@ class FP4Linear(torch.nn.Module):
         if training or (capturing and kept is None):
             return self._cast(dgrad)     # part of the graph: not for calls outside it
         if kept is None:
+            ops._drop_held()
             version, of = w._version, w.detach()
             w4 = self._cast(dgrad)
             stream = torch.cuda.current_stream(w.device)
             self._kept = (w4, version, of, stream, stream.record_event())
         elif capturing:
-            if w4 not in self._w4_in_graphs:
-                self._w4_in_graphs.append(w4)
+            ops._hold_in_graph(w4)       # the graph reads them, however often the weight changes
         else:
             stream = torch.cuda.current_stream(w.device)
             if stream != kept[3]:

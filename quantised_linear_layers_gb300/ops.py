@@ -528,6 +528,17 @@ def _load_fp4():
     return _fp4
 
 
+def _hold_in_graph(obj) -> None:
+    """Keeps obj alive for as long as the graph being captured, or an executable of it."""
+    (_fp4 or _load_fp4()).hold_in_graph(obj)
+
+
+def _drop_held() -> None:
+    """Lets go of what only graphs held that are gone."""
+    if _fp4 is not None:
+        _fp4.drop_held()
+
+
 def _is_bf16(dtype: torch.dtype) -> bool:
     if dtype is torch.bfloat16:
         return True
