@@ -3,7 +3,8 @@
 Each translation unit is compiled in parallel, then linked as a shared
 library next to this file. No CUDA math shortcuts (--use_fast_math is never
 passed): the cast depends on correctly rounded division. The module of the 4-bit
-calls over torch tensors (_fp4.so, g++) is compiled beside it.
+calls over torch tensors (_fp4.so, g++) is compiled beside it where torch can be
+imported; the library itself needs none.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -45,7 +47,9 @@ def _stale(obj: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: str = "") -> str:
     """Compile the library; returns its path. `variant` (e.g. "bounds" with
     extra_flags=("-DQL_BOUNDS_CHECK",)) builds into its own folder and
-    libqlinear_<variant>.so, leaving the product library as it is."""
+    libqlinear_<variant>.so, leaving the product library as it is. The module over
+    torch's tensors comes with the product library; if it does not compile, that is
+    raised once the library stands."""
     build_dir = BUILD + (f"_{variant}" if variant else "")
     lib = LIB.replace(".so", f"_{variant}.so") if variant else LIB
     os.makedirs(build_dir, exist_ok=True)
@@ -73,40 +77,53 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
                 raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
             if verbose and (r.stdout or r.stderr):
                 print(r.stdout + r.stderr)
+        if force or jobs or _stale(lib, objs):
+            tmp = lib + f".{os.getpid()}.tmp"
+            cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, lib)
         if module is not None:
             module.result()
-    if force or jobs or _stale(lib, objs):
-        tmp = lib + f".{os.getpid()}.tmp"
-        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, lib)
     return lib
 
 
-def build_torch_module(force: bool = False) -> str:
+def build_torch_module(force: bool = False) -> str | None:
     """Compile the Python module of the 4-bit calls (C++ over torch's tensors and
-    the C ABI, whose entry points it is handed at run time); returns its path."""
+    the C ABI, whose entry points it is handed at run time); returns its path, or
+    None without torch. It holds inlined code of torch and Python: another version
+    of either means another module."""
     import sysconfig
 
-    import torch
-    src = os.path.join(CSRC, TORCH_SOURCE)
-    if not force and not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "qlinear.h")]):
-        return TORCH_LIB
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    src = os.path.join(CSRC, TORCH_SOURCE)
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     for d in (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
               sysconfig.get_paths()["include"], cuda):
         cmd += ["-isystem", d]
-    cmd += [src, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    cmd += [src, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    stamp = os.path.join(BUILD, TORCH_SOURCE.replace(".cpp", ".stamp"))
+    made_for = "\n".join([torch.__version__, sys.version, *cmd])
+    if not force and not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "qlinear.h")]) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_for:
+                return TORCH_LIB
+    tmp = TORCH_LIB + f".{os.getpid()}.tmp"
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.makedirs(BUILD, exist_ok=True)
     os.replace(tmp, TORCH_LIB)
+    with open(stamp + f".{os.getpid()}.tmp", "w") as f:
+        f.write(made_for)
+    os.replace(f.name, stamp)
     return TORCH_LIB
 
 
@@ -117,7 +134,6 @@ def build_bounds_checked(force: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     if "--bounds" in sys.argv:
         print(build_bounds_checked(force="--force" in sys.argv))
     else:
