@@ -561,7 +561,6 @@ bool fp4_scales_map(CUtensorMap* map, const uint8_t* sf, int64_t blocks, int fmt
 
 void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
     p.form = a.form;
-    p.fmt = a.fmt;
     p.experts = a.experts;
     p.m = static_cast<int>(a.m);
     p.n = static_cast<int>(a.n);
@@ -569,7 +568,6 @@ void fp4_fill_params(const Fp4GemmArgs& a, Fp4GemmParams& p) {
     p.rows = static_cast<int>(a.rows);
     p.kblocks = static_cast<int>(fp4_kblocks(a.k, a.fmt));
     p.w_row_blocks = static_cast<int>((a.n + 127) / 128);
-    p.x_row_blocks = static_cast<int>(a.x_row_blocks);
     p.offsets = a.offsets;
     p.tx = a.tx;
     p.tw = a.tw;

@@ -54,7 +54,7 @@ struct Fp4GemmArgs {
 
 // Kernel parameters.
 struct Fp4GemmParams {
-    int form, fmt, experts;
+    int form, experts;
     int m, n;                    // D's rows and columns (ragged rows: all rows)
     int k64;                     // steps of 64 along K (plain and ragged rows)
     int rows;                    // upper bound of the offsets
@@ -62,7 +62,6 @@ struct Fp4GemmParams {
     int group_x;                 // tiles of D's rows taken together (pair kernel)
     int kblocks;                 // scale blocks along K of one 128-row block
     int w_row_blocks;            // 128-row scale blocks of one W
-    int x_row_blocks;            // of one X
     const int32_t* offsets;
     const float* tx;
     const float* tw;
