@@ -430,8 +430,9 @@ __global__ void __launch_bounds__(Cfg<NT, FMT>::kThreads + (std::is_void<T>::val
             tc_fence_before_sync();
             if (any) mbar_arrive(&tempty[as]);
         }
-    } else if (p.zero_rest) {
-        fp4_zero_rest<OUT_F32>(p, s_off);
+    } else {
+        if constexpr (!SPLIT)                    // (a product of experts is never split)
+            if (p.zero_rest) fp4_zero_rest<OUT_F32>(p, s_off);
     }
     if constexpr (SPLIT) {
         // one tile per cluster: the partial tiles are in every CTA's shared memory
