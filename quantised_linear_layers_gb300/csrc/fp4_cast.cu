@@ -10,8 +10,8 @@
 // bf16 (nv / mx), with the share of the card's copy rate (6.77 TB/s): cast 46.9 /
 // 45.0 us, 0.95 / 0.97; both ways 71.6 / 65.9 us, 0.76 / 0.80, bound by
 // instruction issue (14 to 16 instructions an element) between its barriers;
-// read-back 60 us in a run of its own outputs, which is this card's rate for
-// writes (235 MB at 4.0 TB/s); scale 37.7 us, 0.92.
+// read-back 66.8 / 66.3 us, 121.7 / 122.0 to fp32, where a fill of the same outputs
+// takes 61.8 and 119.1 (writes alone: 3.8 to 4.1 TB/s); scale 39.0 us, 0.89.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -19,9 +19,10 @@ first and after the last expert's, as in a batch padded to a fixed capacity, hav
 no influence on any result and are zero in Y and dX (unwritten in a given ``out``).
 
 FP4_NV casts of a training step use the tensor's own scale
-(``ops.fp4_tensor_scale``; with experts, that of the rows they have). A forward-only call takes X's scale as given, 1 by
-default: group scales then span 2^-9 .. 448, the range of normalised
-activations, and X is read once.
+(``ops.fp4_tensor_scale``; with experts, that of the rows they have). A
+forward-only call takes X's scale as given, 1 by default: group scales then span
+2^-9 .. 448, the range of normalised activations, and X is read once. The modules
+take X's own scale with and without gradients.
 """
 from __future__ import annotations
 
