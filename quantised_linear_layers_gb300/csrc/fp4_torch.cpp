@@ -568,14 +568,27 @@ void check_cuda(cudaError_t e) {
     if (e != cudaSuccess) throw std::runtime_error(cudaGetErrorString(e));
 }
 
-// (object): kept alive by the graph that the current stream captures into, and by
-// every executable made from it.
+// (object, event): object is kept alive by the graph that the current stream
+// captures into, and by every executable made from it; the host waits for the event
+// behind the work that made it, which a capture cannot.
 PyObject* f_hold(Args a) {
+    void* event = PyLong_AsVoidPtr(a[1]);
+    if (event == nullptr && PyErr_Occurred()) throw Raised{};
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
     cudaGraph_t graph = nullptr;
     check_cuda(cudaStreamGetCaptureInfo(c10::cuda::getCurrentCUDAStream().stream(), &status, &id, &graph));
     if (status != cudaStreamCaptureStatusActive || graph == nullptr) value_error("the current stream captures no graph");
+    if (event != nullptr) {
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;       // else a wait ends the capture
+        check_cuda(cudaThreadExchangeStreamCaptureMode(&mode));
+        cudaError_t e;
+        Py_BEGIN_ALLOW_THREADS
+        e = cudaEventSynchronize(static_cast<cudaEvent_t>(event));
+        Py_END_ALLOW_THREADS
+        check_cuda(cudaThreadExchangeStreamCaptureMode(&mode));
+        check_cuda(e);
+    }
     Held* h = new Held{Py_NewRef(a[0]), nullptr};
     cudaUserObject_t object;
     if (cudaError_t e = cudaUserObjectCreate(&object, h, graph_gone, 1, cudaUserObjectNoDestructorSync); e != cudaSuccess) {
@@ -673,7 +686,7 @@ PyMethodDef methods[] = {
     {"wgrad", cfunction(entry<f_wgrad, 4>), METH_FASTCALL, nullptr},
     {"linear", cfunction(entry<f_linear, 5>), METH_FASTCALL, nullptr},
     {"linear_saving", cfunction(entry<f_linear_saving, 4>), METH_FASTCALL, nullptr},
-    {"hold_in_graph", cfunction(entry<f_hold, 1>), METH_FASTCALL, nullptr},
+    {"hold_in_graph", cfunction(entry<f_hold, 2>), METH_FASTCALL, nullptr},
     {"drop_held", cfunction(entry<f_drop, 0>), METH_FASTCALL, nullptr},
     {"linear_backward", cfunction(entry<f_linear_backward, 7>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -222,7 +222,7 @@ class FP4Linear(torch.nn.Module):
             stream = torch.cuda.current_stream(w.device)
             self._kept = (w4, version, of, stream, stream.record_event())
         elif capturing:
-            ops._hold_in_graph(w4)       # the graph reads them, however often the weight changes
+            ops._hold_in_graph(w4, kept[4])  # the graph reads them, however often the weight changes
         else:
             stream = torch.cuda.current_stream(w.device)
             if stream != kept[3]:

@@ -528,9 +528,10 @@ def _load_fp4():
     return _fp4
 
 
-def _hold_in_graph(obj) -> None:
-    """Keeps obj alive for as long as the graph being captured, or an executable of it."""
-    (_fp4 or _load_fp4()).hold_in_graph(obj)
+def _hold_in_graph(obj, event: torch.cuda.Event) -> None:
+    """Keeps obj alive for as long as the graph being captured, or an executable of it,
+    and waits for the event behind the work that made it."""
+    (_fp4 or _load_fp4()).hold_in_graph(obj, event.cuda_event)
 
 
 def _drop_held() -> None:
