@@ -90,7 +90,8 @@ def draw(rng):
             c["renormalise"] = False                   # one weight renormalised is constant: no gradient
     else:
         c |= {"n": _log(rng, 33, 7168), "experts": _log(rng, 2, 512, odd=1.0), "k": rng.randint(1, 8)}
-        c["m"] = _log(rng, 1, min(16384, 60_000_000 // (c["n"] * c["k"])))
+        token = c["n"] * (2 * c["k"] + 2) * _size(c["dtype"]) * (2 if op == "exchange_train" else 1)
+        c["m"] = _log(rng, 1, min(16384, 1_000_000_000 // token))
         c |= {"skew": round(rng.uniform(0.0, 1.5), 2), "padded": rng.choice([0.0, 0.0, 0.1])}
     return c
 
