@@ -6,8 +6,9 @@
  *   - the FP8 cast (per token in 1x128 / 1x32 groups, or per 128x128 block),
  *   - the block-scaled FP8 GEMM D = A * B^T (bf16 output for fwd/dgrad,
  *     fp32 output, optionally accumulated, for wgrad);
- * and both in microscaled 4-bit floating point, with experts of ragged loads
- * (the last part of this header).
+ * and both in microscaled 4-bit floating point, with experts of ragged loads;
+ * then what stands around the experts' products: layer norm, routing and the
+ * exchange of rows (the last part of this header).
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller. The library
@@ -588,6 +589,92 @@ ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sf
                                 const uint8_t* x, int64_t ldx, const uint8_t* sfx, const float* x_scale, int fmt,
                                 float* d, int64_t ldd, const int32_t* offsets, int experts, int64_t tokens, int64_t m,
                                 int64_t n, int accumulate, ql_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the experts' products: layer norm, routing and the exchange of rows.
+ *
+ * All take bf16 or fp32 rows (contiguous, any row stride; rows on 16-byte
+ * boundaries are faster) and compute in fp32, rounding once. Outputs' rows must not
+ * overlap. No results depend on timing: sums have a fixed order. No call allocates;
+ * a workspace is 16-byte aligned device memory, free for others once the stream is
+ * past the call.
+ * ------------------------------------------------------------------------- */
+
+/* Y [m, n] = (x - mean) / sqrt(var + eps) * weight + bias over the rows of X, mean
+ * and var (the mean of (x - mean)^2, whose squares must fit fp32) of each row.
+ * weight and bias [n] of one type, each may be NULL. mean and rstd = 1 / sqrt(var +
+ * eps), fp32 [m], for the backward call, or both NULL. eps >= 0. A row with an
+ * infinity or a NaN becomes NaN. */
+ql_status layer_norm(const void* x, ql_dtype x_dtype, int64_t m, int64_t n, int64_t x_stride_m, const void* weight,
+                     const void* bias, ql_dtype w_dtype, float eps, void* y, ql_dtype y_dtype, int64_t y_stride_m, float* mean,
+                     float* rstd, ql_stream_t stream);
+
+/* With h = (x - mean) rstd and g = dy weight: dX = rstd (g - mean(g) - h mean(g h))
+ * of X's type, dweight [n] = sum of dy h and dbias [n] = sum of dy over the rows, fp32
+ * (both NULL: neither, and no workspace). */
+size_t layer_norm_backward_workspace_size(int64_t m, int64_t n);
+ql_status layer_norm_backward(const void* dy, ql_dtype dy_dtype, int64_t dy_stride_m, const void* x, ql_dtype x_dtype,
+                              int64_t x_stride_m, const float* mean, const float* rstd, const void* weight, ql_dtype w_dtype,
+                              int64_t m, int64_t n, void* dx, int64_t dx_stride_m, float* dweight, float* dbias,
+                              void* workspace, size_t workspace_bytes, ql_stream_t stream);
+
+/* Which k of the experts each of m tokens goes to, and with which weights.
+ *   logits   [m, experts]; scores s = softmax or sigmoid of a token's
+ *   bias     fp32 [experts] or NULL: experts are chosen by c = s + bias and weighted
+ *            by s
+ *   groups   the experts in equal runs, of which the `kept` best are chosen from; a
+ *            group's score is the sum of its group_best (1 or 2) largest c
+ *   weights  fp32 [m, k] = s * scale, with renormalise the shares s / sum(s) of the
+ *            token's chosen * scale
+ *   chosen   int32 [m, k], by falling c
+ * Comparisons are those of 64 bits (without a bias between logits); ties go to the
+ * lower index. An expert with logit or bias -inf is out of reach and counts for
+ * nothing; where fewer than k are left the rest of chosen is -1 with weight 0. A NaN
+ * is chosen last, and the weights of a token with one among its logits or the bias are
+ * NaN; so are those of a token with logit +inf under the softmax. experts <= 512,
+ * k <= 32, groups <= 32. */
+#define QL_SCORE_SOFTMAX 0
+#define QL_SCORE_SIGMOID 1
+ql_status expert_route(const void* logits, ql_dtype logits_dtype, int64_t m, int experts, int64_t stride_m, const float* bias,
+                       int k, int score, int groups, int kept, int group_best, int renormalise, float scale, float* weights,
+                       int32_t* chosen, ql_stream_t stream);
+
+/* dlogits [m, experts], of the logits' type, from the gradient of expert_route's
+ * weights (the choice has none, nor has the bias). Entries of chosen outside
+ * [0, experts) count for nothing. */
+ql_status expert_route_backward(const float* dweights, const void* logits, ql_dtype logits_dtype, int64_t m, int experts,
+                                int64_t stride_m, const int32_t* chosen, int k, int score, int renormalise, float scale,
+                                void* dlogits, int64_t d_stride_m, ql_stream_t stream);
+
+/* The order of the slots (entries of chosen, int32 [slots]) by expert, and within an
+ * expert as they are: rows [slots] is each slot's place, -1 for a slot of no expert
+ * (chosen -1); offsets [experts + 1] is where each expert's places begin, as the 4-bit
+ * experts' calls take it (offsets[0] is 0, offsets[experts] the number of slots that
+ * have an expert). Any other value of chosen counts as -1 and makes ql_device_status
+ * return QL_ERR_INVALID_ARG. slots <= 2^26, experts <= 512. */
+size_t expert_plan_workspace_size(int64_t slots, int experts);
+ql_status expert_plan(const int32_t* chosen, int64_t slots, int experts, int32_t* offsets, int32_t* rows, void* workspace,
+                      size_t workspace_bytes, ql_stream_t stream);
+
+/* XS [m * k, n]: row rows[t * k + j] = row t of X [m, n]; rows from offsets[experts] on
+ * are zero. rows and offsets are expert_plan's; rows outside [0, m * k) are none. */
+ql_status expert_dispatch(const void* x, ql_dtype dtype, int64_t m, int64_t n, int64_t x_stride_m, const int32_t* rows,
+                          const int32_t* offsets, int experts, int k, void* xs, int64_t xs_stride_m, ql_stream_t stream);
+
+/* Y [m, n]: row t = add[t] + sum over j of weights[t, j] * row rows[t * k + j] of YS
+ * [m * k, n], summed in fp32 in the order of j and rounded once; a slot without a row
+ * counts for nothing. weights fp32 [m, k] (NULL: 1, the gradient of expert_dispatch),
+ * add [m, n] or NULL. */
+ql_status expert_combine(const void* ys, ql_dtype dtype, int64_t ys_stride_m, const int32_t* rows, const float* weights,
+                         const void* add, int64_t add_stride_m, int64_t m, int64_t n, int k, void* y, int64_t y_stride_m,
+                         ql_stream_t stream);
+
+/* Its gradients: row rows[t * k + j] of DYS [m * k, n] = weights[t, j] * dy[t], rows from
+ * offsets[experts] on are zero; dweights fp32 [m, k] = dy[t] . that row of YS, 0 for a
+ * slot without one. */
+ql_status expert_combine_backward(const void* dy, ql_dtype dtype, int64_t dy_stride_m, const void* ys, int64_t ys_stride_m,
+                                  const int32_t* rows, const int32_t* offsets, int experts, const float* weights, int64_t m,
+                                  int64_t n, int k, void* dys, int64_t dys_stride_m, float* dweights, ql_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -2,8 +2,8 @@
 
 Each translation unit is compiled in parallel, then linked as a shared
 library next to this file. No CUDA math shortcuts (--use_fast_math is never
-passed): the cast depends on correctly rounded division. The module of the 4-bit
-calls over torch tensors (_fp4.so, g++) is compiled beside it where torch can be
+passed): the cast depends on correctly rounded division. The module of the calls
+over torch tensors (_fp4.so, g++) is compiled beside it where torch can be
 imported; the library itself needs none.
 """
 from __future__ import annotations
@@ -19,8 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqlinear.so")
-SOURCES = ["api.cu", "cast.cu", "fp4_cast.cu", "fp4_gemm.cu", "fp4_gemm_pair.cu", "gemm.cu", "gemm_mx.cu", "gemm_mx2.cu", "gemm_mx_sk.cu", "gemm_pair.cu", "gemm_prom_sk.cu", "noalloc.cu"]
-TORCH_SOURCE = "fp4_torch.cpp"                 # the 4-bit calls over torch tensors (module _fp4)
+SOURCES = ["api.cu", "cast.cu", "exchange.cu", "fp4_cast.cu", "fp4_gemm.cu", "fp4_gemm_pair.cu", "gemm.cu", "gemm_mx.cu", "gemm_mx2.cu", "gemm_mx_sk.cu", "gemm_pair.cu", "gemm_prom_sk.cu", "noalloc.cu", "norm.cu", "route.cu"]
+TORCH_SOURCE = "fp4_torch.cpp"                 # the calls over torch tensors (module _fp4)
+TORCH_HEADERS = ["layers_torch.h"]             # what it includes of this folder
 TORCH_LIB = os.path.join(HERE, "_fp4.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -53,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
     build_dir = BUILD + (f"_{variant}" if variant else "")
     lib = LIB.replace(".so", f"_{variant}.so") if variant else LIB
     os.makedirs(build_dir, exist_ok=True)
-    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")) and f not in TORCH_HEADERS]
     headers.append(os.path.join(INCLUDE, "qlinear.h"))
     objs, jobs = [], []
     for src in SOURCES:
@@ -90,7 +91,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), variant: s
 
 
 def build_torch_module(force: bool = False) -> str | None:
-    """Compile the Python module of the 4-bit calls (C++ over torch's tensors and
+    """Compile the Python module of the 4-bit calls and those around the experts (C++ over torch's tensors and
     the C ABI, whose entry points it is handed at run time); returns its path, or
     None without torch. It holds inlined code of torch and Python: another version
     of either means another module."""
@@ -111,7 +112,8 @@ def build_torch_module(force: bool = False) -> str | None:
     cmd += [src, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     stamp = os.path.join(BUILD, TORCH_SOURCE.replace(".cpp", ".stamp"))
     made_for = "\n".join([torch.__version__, sys.version, *cmd])
-    if not force and not _stale(TORCH_LIB, [src, os.path.join(INCLUDE, "qlinear.h")]) and os.path.exists(stamp):
+    deps = [src, os.path.join(INCLUDE, "qlinear.h")] + [os.path.join(CSRC, f) for f in TORCH_HEADERS]
+    if not force and not _stale(TORCH_LIB, deps) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read() == made_for:
                 return TORCH_LIB

@@ -14,6 +14,8 @@
 #include "fp4.cuh"
 #include "fp4_gemm.cuh"
 #include "gemm.cuh"
+#include "norm.cuh"
+#include "route.cuh"
 
 namespace {
 
@@ -139,6 +141,8 @@ ql_status gemm_common(const uint8_t* a, int64_t lda, const void* sfa, int64_t sa
 // 4-bit operators: shared argument checks and the launch of a product.
 // ---------------------------------------------------------------------------
 constexpr int64_t kInt31 = int64_t(1) << 31;
+constexpr int64_t kMaxSlots = int64_t(1) << 26;     // of an exchange: every chunk of a plan reads the counts of all
+constexpr int64_t kMaxColumns = int64_t(1) << 22;   // 65535 pieces of 128 columns and less
 
 // Codes of `rows` rows of `k` columns: alignment and row stride.
 ql_status fp4_operand(const uint8_t* q, int64_t ld, const uint8_t* sf, int64_t k) {
@@ -977,6 +981,317 @@ ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sf
     a.d = d;
     a.ldd = ldd;
     return fp4_gemm_common(a, offsets, experts, QL_F32, accumulate, stream);
+}
+
+static bool known_type(ql_dtype t) { return t == QL_BF16 || t == QL_F32; }
+static int64_t bytes_of(ql_dtype t) { return t == QL_BF16 ? 2 : 4; }
+// An output's rows, which must not overlap.
+static bool rows_fit(const void* p, int64_t rows, int64_t n, int64_t stride) { return p != nullptr && (rows <= 1 || stride >= n); }
+
+ql_status layer_norm(const void* x, ql_dtype x_dtype, int64_t m, int64_t n, int64_t x_stride_m, const void* weight,
+                     const void* bias, ql_dtype w_dtype, float eps, void* y, ql_dtype y_dtype, int64_t y_stride_m, float* mean,
+                     float* rstd, ql_stream_t stream) {
+    if (m < 0 || n < 0 || !known_type(x_dtype) || !known_type(y_dtype) || !(eps >= 0.0f)) return QL_ERR_INVALID_ARG;
+    if ((weight != nullptr || bias != nullptr) && !known_type(w_dtype)) return QL_ERR_INVALID_ARG;
+    if ((mean == nullptr) != (rstd == nullptr)) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || n >= kInt31) return QL_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return QL_OK;
+    if (x == nullptr || !rows_fit(y, m, n, y_stride_m)) return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::NormArgs a{};
+    a.x = x;
+    a.x_bf16 = x_dtype == QL_BF16;
+    a.m = m;
+    a.n = n;
+    a.sx = x_stride_m;
+    a.w = weight;
+    a.b = bias;
+    a.w_bf16 = w_dtype == QL_BF16;
+    a.eps = eps;
+    a.y = y;
+    a.y_bf16 = y_dtype == QL_BF16;
+    a.sy = y_stride_m;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.bnd.s[0] = ql::span_of(x, bytes_of(x_dtype), m, x_stride_m, n, 1);
+    a.bnd.s[1] = ql::span_of(weight, bytes_of(w_dtype), n, 1);
+    a.bnd.s[2] = ql::span_of(bias, bytes_of(w_dtype), n, 1);
+    a.bnd.s[3] = ql::span_of(y, bytes_of(y_dtype), m, y_stride_m, n, 1);
+    a.bnd.s[4] = ql::span_of(mean, 4, m, 1);
+    a.bnd.s[5] = ql::span_of(rstd, 4, m, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_norm(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+}
+
+size_t layer_norm_backward_workspace_size(int64_t m, int64_t n) {
+    return m <= 0 || n <= 0 ? 0 : ql::norm_back_workspace(m, n);
+}
+
+ql_status layer_norm_backward(const void* dy, ql_dtype dy_dtype, int64_t dy_stride_m, const void* x, ql_dtype x_dtype,
+                              int64_t x_stride_m, const float* mean, const float* rstd, const void* weight, ql_dtype w_dtype,
+                              int64_t m, int64_t n, void* dx, int64_t dx_stride_m, float* dweight, float* dbias,
+                              void* workspace, size_t workspace_bytes, ql_stream_t stream) {
+    if (m < 0 || n < 0 || !known_type(x_dtype) || !known_type(dy_dtype)) return QL_ERR_INVALID_ARG;
+    if (weight != nullptr && !known_type(w_dtype)) return QL_ERR_INVALID_ARG;
+    if ((dweight == nullptr) != (dbias == nullptr)) return QL_ERR_INVALID_ARG;
+    if (m >= kInt31 || n >= kInt31) return QL_ERR_UNSUPPORTED;
+    if (n == 0) return QL_OK;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (m == 0) {                      // sums over no rows
+        if (dweight == nullptr) return QL_OK;
+        const cudaError_t e = cudaMemsetAsync(dweight, 0, static_cast<size_t>(n) * 4, st);
+        return from_cuda(e != cudaSuccess ? e : cudaMemsetAsync(dbias, 0, static_cast<size_t>(n) * 4, st));
+    }
+    if (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || !rows_fit(dx, m, n, dx_stride_m))
+        return QL_ERR_INVALID_ARG;
+    if (dweight != nullptr) {
+        if (workspace == nullptr || workspace_bytes < layer_norm_backward_workspace_size(m, n)) return QL_ERR_INVALID_ARG;
+        if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
+    }
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::NormBackArgs a{};
+    a.dy = dy;
+    a.dy_bf16 = dy_dtype == QL_BF16;
+    a.sdy = dy_stride_m;
+    a.x = x;
+    a.x_bf16 = x_dtype == QL_BF16;
+    a.m = m;
+    a.n = n;
+    a.sx = x_stride_m;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.w = weight;
+    a.w_bf16 = w_dtype == QL_BF16;
+    a.dx = dx;
+    a.sdx = dx_stride_m;
+    a.dw = dweight;
+    a.db = dbias;
+    a.part = static_cast<float*>(workspace);
+    a.bnd.s[0] = ql::span_of(dy, bytes_of(dy_dtype), m, dy_stride_m, n, 1);
+    a.bnd.s[1] = ql::span_of(x, bytes_of(x_dtype), m, x_stride_m, n, 1);
+    a.bnd.s[2] = ql::span_of(mean, 4, m, 1);
+    a.bnd.s[3] = ql::span_of(rstd, 4, m, 1);
+    a.bnd.s[4] = ql::span_of(weight, bytes_of(w_dtype), n, 1);
+    a.bnd.s[5] = ql::span_of(dx, bytes_of(x_dtype), m, dx_stride_m, n, 1);
+    a.bnd.s[6] = ql::span_of(workspace, 1, static_cast<int64_t>(layer_norm_backward_workspace_size(m, n)), 1);
+    a.bnd.s[7] = ql::span_of(dweight, 4, n, 1);
+    a.bnd.s[8] = ql::span_of(dbias, 4, n, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_norm_back(a, st, di.num_sms));
+}
+
+static ql_status route_sizes(int64_t m, int experts, int k, int score) {
+    if (m < 0 || experts < 1 || k < 1 || k > experts || (score != QL_SCORE_SOFTMAX && score != QL_SCORE_SIGMOID))
+        return QL_ERR_INVALID_ARG;
+    return m >= kInt31 || experts > ql::kRouteMaxExperts || k > ql::kRouteMaxK ? QL_ERR_UNSUPPORTED : QL_OK;
+}
+
+ql_status expert_route(const void* logits, ql_dtype logits_dtype, int64_t m, int experts, int64_t stride_m, const float* bias,
+                       int k, int score, int groups, int kept, int group_best, int renormalise, float scale, float* weights,
+                       int32_t* chosen, ql_stream_t stream) {
+    if (!known_type(logits_dtype)) return QL_ERR_INVALID_ARG;
+    if (ql_status s = route_sizes(m, experts, k, score); s != QL_OK) return s;
+    if (groups < 1 || experts % groups != 0 || kept < 1 || kept > groups || (group_best != 1 && group_best != 2))
+        return QL_ERR_INVALID_ARG;
+    if (groups > ql::kRouteMaxGroups) return QL_ERR_UNSUPPORTED;
+    if (m == 0) return QL_OK;
+    if (logits == nullptr || weights == nullptr || chosen == nullptr) return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::RouteArgs a{};
+    a.logits = logits;
+    a.bf16 = logits_dtype == QL_BF16;
+    a.m = m;
+    a.sl = stride_m;
+    a.experts = experts;
+    a.bias = bias;
+    a.k = k;
+    a.groups = groups;
+    a.kept = kept;
+    a.group_best = group_best;
+    a.sigmoid = score == QL_SCORE_SIGMOID;
+    a.renormalise = renormalise != 0;
+    a.scale = scale;
+    a.weights = weights;
+    a.chosen = chosen;
+    a.bnd.s[0] = ql::span_of(logits, bytes_of(logits_dtype), m, stride_m, experts, 1);
+    a.bnd.s[1] = ql::span_of(bias, 4, experts, 1);
+    a.bnd.s[2] = ql::span_of(weights, 4, m * k, 1);
+    a.bnd.s[3] = ql::span_of(chosen, 4, m * k, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_route(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ql_status expert_route_backward(const float* dweights, const void* logits, ql_dtype logits_dtype, int64_t m, int experts,
+                                int64_t stride_m, const int32_t* chosen, int k, int score, int renormalise, float scale,
+                                void* dlogits, int64_t d_stride_m, ql_stream_t stream) {
+    if (!known_type(logits_dtype)) return QL_ERR_INVALID_ARG;
+    if (ql_status s = route_sizes(m, experts, k, score); s != QL_OK) return s;
+    if (m == 0) return QL_OK;
+    if (dweights == nullptr || logits == nullptr || chosen == nullptr || !rows_fit(dlogits, m, experts, d_stride_m))
+        return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::RouteBackArgs a{};
+    a.dweights = dweights;
+    a.logits = logits;
+    a.bf16 = logits_dtype == QL_BF16;
+    a.m = m;
+    a.sl = stride_m;
+    a.experts = experts;
+    a.chosen = chosen;
+    a.k = k;
+    a.sigmoid = score == QL_SCORE_SIGMOID;
+    a.renormalise = renormalise != 0;
+    a.scale = scale;
+    a.dlogits = dlogits;
+    a.sd = d_stride_m;
+    a.bnd.s[0] = ql::span_of(dweights, 4, m * k, 1);
+    a.bnd.s[1] = ql::span_of(logits, bytes_of(logits_dtype), m, stride_m, experts, 1);
+    a.bnd.s[2] = ql::span_of(chosen, 4, m * k, 1);
+    a.bnd.s[3] = ql::span_of(dlogits, bytes_of(logits_dtype), m, d_stride_m, experts, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_route_back(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t expert_plan_workspace_size(int64_t slots, int experts) {
+    return slots <= 0 || experts <= 0 ? 0 : ql::plan_workspace(slots, experts);
+}
+
+ql_status expert_plan(const int32_t* chosen, int64_t slots, int experts, int32_t* offsets, int32_t* rows, void* workspace,
+                      size_t workspace_bytes, ql_stream_t stream) {
+    if (slots < 0 || experts < 1) return QL_ERR_INVALID_ARG;
+    if (slots > kMaxSlots || experts > ql::kRouteMaxExperts) return QL_ERR_UNSUPPORTED;
+    if (offsets == nullptr || (slots > 0 && (chosen == nullptr || rows == nullptr))) return QL_ERR_INVALID_ARG;
+    const size_t need = expert_plan_workspace_size(slots, experts);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QL_ERR_INVALID_ARG;
+    if (need > 0 && !aligned16(workspace)) return QL_ERR_ALIGNMENT;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::PlanArgs a{};
+    a.chosen = chosen;
+    a.slots = slots;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.counts = need > 0 ? static_cast<int32_t*>(workspace) : nullptr;
+    a.chunk = ql::plan_chunk(slots);
+    a.dev_status = di.status;
+    a.bnd.s[0] = ql::span_of(chosen, 4, slots, 1);
+    a.bnd.s[1] = ql::span_of(offsets, 4, experts + 1, 1);
+    a.bnd.s[2] = ql::span_of(rows, 4, slots, 1);
+    a.bnd.s[3] = ql::span_of(a.counts, 1, static_cast<int64_t>(need), 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_plan(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of an exchange of rows of n columns between m tokens and m k places.
+static ql_status exchange_sizes(int64_t m, int64_t n, int k, ql_dtype dtype) {
+    if (m < 0 || n < 0 || k < 1 || !known_type(dtype)) return QL_ERR_INVALID_ARG;
+    return m >= kInt31 || n > kMaxColumns || m * k > kMaxSlots ? QL_ERR_UNSUPPORTED : QL_OK;
+}
+
+ql_status expert_dispatch(const void* x, ql_dtype dtype, int64_t m, int64_t n, int64_t x_stride_m, const int32_t* rows,
+                          const int32_t* offsets, int experts, int k, void* xs, int64_t xs_stride_m, ql_stream_t stream) {
+    if (ql_status s = exchange_sizes(m, n, k, dtype); s != QL_OK) return s;
+    if (experts < 1) return QL_ERR_INVALID_ARG;
+    if (experts > ql::kRouteMaxExperts) return QL_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return QL_OK;
+    if (x == nullptr || rows == nullptr || offsets == nullptr || !rows_fit(xs, m * k, n, xs_stride_m)) return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::DispatchArgs a{};
+    a.x = x;
+    a.m = m;
+    a.n = n;
+    a.sx = x_stride_m;
+    a.es = static_cast<int>(bytes_of(dtype));
+    a.rows = rows;
+    a.offsets = offsets;
+    a.experts = experts;
+    a.k = k;
+    a.xs = xs;
+    a.sxs = xs_stride_m;
+    a.bnd.s[0] = ql::span_of(x, a.es, m, x_stride_m, n, 1);
+    a.bnd.s[1] = ql::span_of(rows, 4, m * k, 1);
+    a.bnd.s[2] = ql::span_of(offsets, 4, experts + 1, 1);
+    a.bnd.s[3] = ql::span_of(xs, a.es, m * k, xs_stride_m, n, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_dispatch(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+}
+
+ql_status expert_combine(const void* ys, ql_dtype dtype, int64_t ys_stride_m, const int32_t* rows, const float* weights,
+                         const void* add, int64_t add_stride_m, int64_t m, int64_t n, int k, void* y, int64_t y_stride_m,
+                         ql_stream_t stream) {
+    if (ql_status s = exchange_sizes(m, n, k, dtype); s != QL_OK) return s;
+    if (m == 0 || n == 0) return QL_OK;
+    if (ys == nullptr || rows == nullptr || !rows_fit(y, m, n, y_stride_m)) return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::CombineArgs a{};
+    a.ys = ys;
+    a.bf16 = dtype == QL_BF16;
+    a.m = m;
+    a.n = n;
+    a.sys = ys_stride_m;
+    a.k = k;
+    a.rows = rows;
+    a.weights = weights;
+    a.add = add;
+    a.sadd = add_stride_m;
+    a.y = y;
+    a.sy = y_stride_m;
+    a.bnd.s[0] = ql::span_of(ys, bytes_of(dtype), m * k, ys_stride_m, n, 1);
+    a.bnd.s[1] = ql::span_of(rows, 4, m * k, 1);
+    a.bnd.s[2] = ql::span_of(weights, 4, m * k, 1);
+    a.bnd.s[3] = ql::span_of(add, bytes_of(dtype), m, add_stride_m, n, 1);
+    a.bnd.s[4] = ql::span_of(y, bytes_of(dtype), m, y_stride_m, n, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+}
+
+ql_status expert_combine_backward(const void* dy, ql_dtype dtype, int64_t dy_stride_m, const void* ys, int64_t ys_stride_m,
+                                  const int32_t* rows, const int32_t* offsets, int experts, const float* weights, int64_t m,
+                                  int64_t n, int k, void* dys, int64_t dys_stride_m, float* dweights, ql_stream_t stream) {
+    if (ql_status s = exchange_sizes(m, n, k, dtype); s != QL_OK) return s;
+    if (experts < 1) return QL_ERR_INVALID_ARG;
+    if (experts > ql::kRouteMaxExperts) return QL_ERR_UNSUPPORTED;
+    if (m == 0) return QL_OK;
+    if (dweights == nullptr) return QL_ERR_INVALID_ARG;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (n == 0) return from_cuda(cudaMemsetAsync(dweights, 0, static_cast<size_t>(m) * k * 4, st));
+    if (dy == nullptr || ys == nullptr || rows == nullptr || offsets == nullptr || weights == nullptr ||
+        !rows_fit(dys, m * k, n, dys_stride_m))
+        return QL_ERR_INVALID_ARG;
+    DeviceInfo di;
+    if (ql_status s = device_info(di); s != QL_OK) return s;
+    ql::CombineBackArgs a{};
+    a.dy = dy;
+    a.bf16 = dtype == QL_BF16;
+    a.m = m;
+    a.n = n;
+    a.sdy = dy_stride_m;
+    a.ys = ys;
+    a.sys = ys_stride_m;
+    a.k = k;
+    a.rows = rows;
+    a.offsets = offsets;
+    a.experts = experts;
+    a.weights = weights;
+    a.dys = dys;
+    a.sdys = dys_stride_m;
+    a.dweights = dweights;
+    a.bnd.s[0] = ql::span_of(dy, bytes_of(dtype), m, dy_stride_m, n, 1);
+    a.bnd.s[1] = ql::span_of(ys, bytes_of(dtype), m * k, ys_stride_m, n, 1);
+    a.bnd.s[2] = ql::span_of(rows, 4, m * k, 1);
+    a.bnd.s[3] = ql::span_of(offsets, 4, experts + 1, 1);
+    a.bnd.s[4] = ql::span_of(weights, 4, m * k, 1);
+    a.bnd.s[5] = ql::span_of(dys, bytes_of(dtype), m * k, dys_stride_m, n, 1);
+    a.bnd.s[6] = ql::span_of(dweights, 4, m * k, 1);
+    a.bnd.status = di.status;
+    return from_cuda(ql::launch_combine_back(a, st));
 }
 
 ql_status ql_set_num_sms(int num_sms) {

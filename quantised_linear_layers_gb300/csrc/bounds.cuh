@@ -26,10 +26,12 @@ constexpr int kMaxSpans = 6;
 // The ranges of the buffers one kernel touches with plain loads and stores,
 // and the device status word (bits at status[0], first offending address as
 // a 64-bit word at status + 2).
-struct Bounds {
-    Span s[kMaxSpans];
+template <int N>
+struct BoundsOf {
+    Span s[N];
     uint32_t* status;
 };
+using Bounds = BoundsOf<kMaxSpans>;
 
 // Byte range of a [d0 x d1 x d2] view of es-byte elements with element
 // strides s0, s1, s2 (any sign) at base; empty when base is null or any
@@ -49,7 +51,8 @@ inline Span span_of(const void* base, int64_t es, int64_t d0, int64_t s0, int64_
 
 #ifdef __CUDACC__
 #ifdef QL_BOUNDS_CHECK
-__device__ __forceinline__ bool in_span(const Bounds& b, int i, const void* p, uint32_t bytes) {
+template <int N>
+__device__ __forceinline__ bool in_span(const BoundsOf<N>& b, int i, const void* p, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     if (a >= b.s[i].lo && a + bytes <= b.s[i].hi) return true;
     if (b.status != nullptr) {

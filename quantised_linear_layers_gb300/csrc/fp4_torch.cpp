@@ -1,5 +1,5 @@
-// The 4-bit calls as a Python module over torch tensors: argument checks,
-// output and workspace allocation, and the C ABI's entry points
+// The 4-bit calls, and those around the experts' products (layers_torch.h), as a
+// Python module over torch tensors: argument checks, output and workspace allocation, and the C ABI's entry points
 // (include/qlinear.h), which it is handed as addresses. At these sizes a call's
 // host time is most of its cost; done in Python it was twice this.
 //
@@ -551,6 +551,8 @@ PyObject* f_linear_backward(Args a) {
     return res;
 }
 
+#include "layers_torch.h"
+
 // Objects that graphs hold, and those whose graphs are gone: a list, since the
 // runtime says so on a thread of its own, which may call neither Python nor CUDA.
 struct Held {
@@ -635,19 +637,20 @@ PyObject* entry(PyObject*, Args a, Py_ssize_t n) {
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown error in a 4-bit call");
+        PyErr_SetString(PyExc_RuntimeError, "unknown error in a call over torch tensors");
     }
     return nullptr;
 }
 
-// (addresses, FP4Tensor, FP4_OWN_SCALE, error callable)
+// (addresses, FP4Tensor, FP4_OWN_SCALE, ExpertPlan, error callable)
 PyObject* bind(PyObject*, Args a, Py_ssize_t n) {
-    if (n != 4 || !PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 10) {
-        PyErr_SetString(PyExc_TypeError, "bind(addresses, class, own, error)");
+    constexpr int kEntries = 10 + kLayerEntries;
+    if (n != 5 || !PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != kEntries) {
+        PyErr_SetString(PyExc_TypeError, "bind(addresses, class, own, plan class, error)");
         return nullptr;
     }
-    void* p[10];
-    for (int i = 0; i < 10; ++i) {
+    void* p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
         if (p[i] == nullptr) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -664,9 +667,11 @@ PyObject* bind(PyObject*, Args a, Py_ssize_t n) {
     api.gemm = reinterpret_cast<decltype(api.gemm)>(p[7]);
     api.ragged = reinterpret_cast<decltype(api.ragged)>(p[8]);
     api.wgrad = reinterpret_cast<decltype(api.wgrad)>(p[9]);
+    bind_layers(p + 10);
     g_class = Py_NewRef(a[1]);
     g_own = Py_NewRef(a[2]);
-    g_error = Py_NewRef(a[3]);
+    g_plan_class = Py_NewRef(a[3]);
+    g_error = Py_NewRef(a[4]);
     Py_RETURN_NONE;
 }
 
@@ -689,6 +694,14 @@ PyMethodDef methods[] = {
     {"hold_in_graph", cfunction(entry<f_hold, 2>), METH_FASTCALL, nullptr},
     {"drop_held", cfunction(entry<f_drop, 0>), METH_FASTCALL, nullptr},
     {"linear_backward", cfunction(entry<f_linear_backward, 7>), METH_FASTCALL, nullptr},
+    {"layer_norm", cfunction(entry<f_layer_norm, 7>), METH_FASTCALL, nullptr},
+    {"layer_norm_backward", cfunction(entry<f_layer_norm_backward, 5>), METH_FASTCALL, nullptr},
+    {"route", cfunction(entry<f_route, 9>), METH_FASTCALL, nullptr},
+    {"route_backward", cfunction(entry<f_route_backward, 6>), METH_FASTCALL, nullptr},
+    {"plan", cfunction(entry<f_plan, 2>), METH_FASTCALL, nullptr},
+    {"dispatch", cfunction(entry<f_dispatch, 3>), METH_FASTCALL, nullptr},
+    {"combine", cfunction(entry<f_combine, 5>), METH_FASTCALL, nullptr},
+    {"combine_backward", cfunction(entry<f_combine_backward, 4>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp4", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
@@ -696,10 +709,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp4", nullptr, -1, methods, nullp
 }  // namespace
 
 PyMODINIT_FUNC PyInit__fp4() {
-    PyObject** names[] = {&n_q, &n_sf, &n_scale, &n_ld, &n_fmt, &n_batch, &n_rows, &n_cols, &n_offsets, &n_by_cols, &n_device};
+    PyObject** names[] = {&n_q, &n_sf, &n_scale, &n_ld, &n_fmt, &n_batch, &n_rows, &n_cols, &n_offsets, &n_by_cols, &n_device,
+                          &n_plan_rows, &n_plan_offsets};
     const char* text[] = {"q_ptr", "sf_ptr", "scale_ptr", "ld", "fmt", "batch", "rows", "cols", "offsets", "by_cols",
-                          "device_index"};
-    for (int i = 0; i < 11; ++i)
+                          "device_index", "rows", "offsets"};
+    for (int i = 0; i < 13; ++i)
         if ((*names[i] = PyUnicode_InternFromString(text[i])) == nullptr) return nullptr;
     return PyModule_Create(&module);
 }

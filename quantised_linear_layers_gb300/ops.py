@@ -22,6 +22,7 @@ QL_BF16, QL_F32 = 0, 1
 SF_FP32, SF_UE8M0, SF_PACKED_UE8M0 = 0, 1, 2
 CAST_RECIP_OF_SCALE = 0x100
 FP4_NV, FP4_MX = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}     # of a router, as expert_route takes them
 FP4_OWN_SCALE = "own"       # as a tensor scale: fp4_tensor_scale of the tensor itself
 
 _lock = threading.Lock()
@@ -64,6 +65,17 @@ _SIGS = {
     "fp4_linear": [_vp, _int, _i64, _vp, _int, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp],
     "gemm_fp4_wgrad_ragged": [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64,
                               _int, _vp],
+    "layer_norm": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, ctypes.c_float, _vp, _int, _i64, _vp, _vp, _vp],
+    "layer_norm_backward_workspace_size": [_i64, _i64],
+    "layer_norm_backward": [_vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _sz,
+                            _vp],
+    "expert_route": [_vp, _int, _i64, _int, _i64, _vp, _int, _int, _int, _int, _int, _int, ctypes.c_float, _vp, _vp, _vp],
+    "expert_route_backward": [_vp, _vp, _int, _i64, _int, _i64, _vp, _int, _int, _int, ctypes.c_float, _vp, _i64, _vp],
+    "expert_plan_workspace_size": [_i64, _int],
+    "expert_plan": [_vp, _i64, _int, _vp, _vp, _vp, _sz, _vp],
+    "expert_dispatch": [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, _int, _vp, _i64, _vp],
+    "expert_combine": [_vp, _int, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _i64, _vp],
+    "expert_combine_backward": [_vp, _int, _i64, _vp, _i64, _vp, _vp, _int, _vp, _i64, _i64, _int, _vp, _i64, _vp, _vp],
     "ql_cast_gemm_host_workspace_size": [_i64, _i64, _i64, _int],
     "ql_cast_gemm_host": [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp, _i64, _i64, _i64, _i64, _i64,
                           _vp, _sz, _vp],
@@ -108,6 +120,8 @@ def load_library(path: str = LIB_PATH):
             lib.ql_gemm_workspace_size.restype = _sz
             lib.ql_cast_gemm_host_workspace_size.restype = _sz
             lib.fp4_linear_workspace_size.restype = _sz
+            lib.layer_norm_backward_workspace_size.restype = _sz
+            lib.expert_plan_workspace_size.restype = _sz
             lib.fp4_scale_bytes.restype = _i64
             lib.fp4_row_stride.restype = _i64
             lib.fp4_column_extent.restype = _i64
@@ -506,10 +520,24 @@ def _fp4_tensor(buf, ld, scale, *rest):
 _fp4 = None
 _FP4_ENTRIES = ("fp4_tensor_scale", "fp4_cast", "fp4_cast_dual", "fp4_dequant", "fp4_linear", "fp4_linear_workspace_size",
                 "fp4_row_stride", "gemm_fp4_nt", "gemm_fp4_nt_ragged", "gemm_fp4_wgrad_ragged")
+_LAYER_ENTRIES = ("layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size", "expert_route",
+                  "expert_route_backward", "expert_plan", "expert_plan_workspace_size", "expert_dispatch", "expert_combine",
+                  "expert_combine_backward")
+
+
+class ExpertPlan:
+    """Where the rows of a batch go among its experts (``expert_plan``): ``offsets`` int32
+    [experts + 1], as the 4-bit experts take them, and ``rows`` int32 [tokens, k], the
+    place of each slot in the order by expert (-1: none)."""
+
+    __slots__ = ("offsets", "rows")
+
+    def __init__(self, offsets: torch.Tensor, rows: torch.Tensor):
+        self.offsets, self.rows = offsets, rows
 
 
 def _load_fp4():
-    """The module of the 4-bit calls (_fp4.so), bound to the loaded library's entry
+    """The module of the calls over torch tensors (_fp4.so), bound to the loaded library's entry
     points (raises if either is missing: no fallback)."""
     global _fp4
     lib = load_library()
@@ -522,8 +550,8 @@ def _load_fp4():
             spec = importlib.util.spec_from_file_location("quantised_linear_layers_gb300._fp4", path)
             mod = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(mod)
-            mod.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FP4_ENTRIES), FP4Tensor,
-                     FP4_OWN_SCALE, _check)
+            mod.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FP4_ENTRIES + _LAYER_ENTRIES),
+                     FP4Tensor, FP4_OWN_SCALE, ExpertPlan, _check)
             _fp4 = mod
     return _fp4
 
@@ -628,6 +656,93 @@ def fp4_linear_backward(dy: torch.Tensor, wt: FP4Tensor | None, x_cols: FP4Tenso
     cast ``wt`` of W^T (None: no dX), dW [n, k] or [experts, n, k] fp32 (+)= dY^T X,
     with dY cast both ways from one read."""
     return (_fp4 or _load_fp4()).linear_backward(dy, wt, x_cols, dy_scale, offsets, dw_out, accumulate)
+
+
+# ---------------------------------------------------------------------------
+# Around the experts' products: layer norm, routing and the exchange of rows
+# ---------------------------------------------------------------------------
+def _type_code(dtype: torch.dtype | None) -> int:
+    if dtype is None:
+        return 2
+    return QL_BF16 if _is_bf16(dtype) else QL_F32
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, eps: float = 1e-5,
+               out: torch.Tensor | None = None, dtype: torch.dtype | None = None) -> torch.Tensor:
+    """(x - mean) / sqrt(var + eps) * weight + bias over the rows of x [m, n] (bf16 or
+    fp32), in fp32 and rounded once to ``dtype`` (default: out's or x's). weight and
+    bias [n], bf16 or fp32, each may be None."""
+    return (_fp4 or _load_fp4()).layer_norm(x, weight, bias, eps, out, _type_code(dtype), False)
+
+
+def layer_norm_saving(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                      eps: float = 1e-5, out: torch.Tensor | None = None, dtype: torch.dtype | None = None):
+    """``layer_norm`` that keeps its rows' statistics: (y, stats), stats fp32 [2, m]
+    (mean, 1 / sqrt(var + eps)) for ``layer_norm_backward``."""
+    return (_fp4 or _load_fp4()).layer_norm(x, weight, bias, eps, out, _type_code(dtype), True)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, weight: torch.Tensor | None = None,
+                        sums: bool | None = None):
+    """(dx, dweight, dbias) of ``layer_norm_saving``: dx of x's type, dweight and dbias
+    fp32 [n], which are None without ``sums`` (default: with a weight)."""
+    return (_fp4 or _load_fp4()).layer_norm_backward(dy, x, stats, weight, weight is not None if sums is None else sums)
+
+
+def _score_code(score: str) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}")
+    return SCORES[score]
+
+
+def route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
+          kept: int = 1, group_best: int = 1, renormalise: bool = True, scale: float = 1.0):
+    """Which k experts each token goes to: (weights fp32 [tokens, k], experts int32
+    [tokens, k]) from logits [tokens, experts] (bf16 or fp32).
+
+    Scores s are the ``score`` ("softmax" or "sigmoid") of a token's logits. Experts are
+    chosen by s + bias (fp32 [experts], for balance) from the ``kept`` best of ``groups``
+    equal runs of experts, where a group's score is the sum of its ``group_best`` (1 or
+    2) largest; ties go to the lower index, as in 64 bits. Weights are s, or with
+    ``renormalise`` its share among the token's chosen, times ``scale``. An expert with
+    logit or bias -inf is out of reach; a token that reaches fewer than k has experts -1
+    with weight 0 for the rest."""
+    return (_fp4 or _load_fp4()).route(logits, k, bias, _score_code(score), groups, kept, group_best, renormalise, scale)
+
+
+def route_backward(dweights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, score: str = "softmax",
+                   renormalise: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """dlogits (of the logits' type) from the gradient of ``route``'s weights. The choice
+    has no gradient, nor has the bias."""
+    return (_fp4 or _load_fp4()).route_backward(dweights, logits, experts, _score_code(score), renormalise, scale)
+
+
+def expert_plan(experts: torch.Tensor, num_experts: int) -> ExpertPlan:
+    """The order by expert of the slots of ``experts`` (int32 [tokens, k], -1: none), the
+    slots of one expert in their own order: an ``ExpertPlan``. Everything stays on the
+    device. An index outside [-1, num_experts) counts as -1 and shows in
+    ``device_status``."""
+    return (_fp4 or _load_fp4()).plan(experts, num_experts)
+
+
+def expert_dispatch(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
+    """xs [tokens * k, n]: x's rows sorted by expert, one for each slot; zeros past the
+    last expert's. Its gradient is ``expert_combine(dxs, plan)``."""
+    return (_fp4 or _load_fp4()).dispatch(x, plan, out)
+
+
+def expert_combine(ys: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor | None = None, add: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """y [tokens, n] = add + the sum over a token's slots of weights (fp32 [tokens, k],
+    None: 1) times their rows of ys [tokens * k, n], in fp32 and rounded once to ys's
+    type; slots of no expert count for nothing."""
+    return (_fp4 or _load_fp4()).combine(ys, plan, weights, add, out)
+
+
+def expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor):
+    """(dys, dweights) of ``expert_combine``: dys [tokens * k, n] of ys's type, zeros
+    past the last expert's rows; dweights fp32 [tokens, k]. The gradient of ``add`` is dy."""
+    return (_fp4 or _load_fp4()).combine_backward(dy, ys, plan, weights)
 
 
 def set_num_sms(n: int) -> None:

@@ -1,0 +1,204 @@
+"""Routing and its gradient against 64 bits: the choice equal, weights within fp32."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import layer_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from quantised_linear_layers_gb300 import ops
+    return ops
+
+
+def logits_of(m, n, dtype, seed=0, size=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (size * torch.randn((m, n), generator=g) + 0.7 * torch.randn((1, n), generator=g)).to(dtype).cuda()
+
+
+def bias_of(n, seed=1, size=0.1):
+    return (size * torch.randn(n, generator=torch.Generator().manual_seed(seed))).cuda()
+
+
+def check(ops, logits, k, bias=None, score="softmax", groups=1, kept=1, group_best=1, renormalise=True, scale=1.0, dw_seed=5):
+    w, e = ops.route(logits, k, bias, score=score, groups=groups, kept=kept, group_best=group_best, renormalise=renormalise, scale=scale)
+    assert w.dtype == F and e.dtype == torch.int32 and w.shape == e.shape == (logits.shape[0], k)
+    want = ref.choose(logits, k, bias, score, groups, kept, group_best)
+    assert torch.equal(e.cpu(), want), f"{int((e.cpu() != want).any(1).sum())} tokens choose otherwise"
+    ref.close(w, *ref.route_weights(logits, want, score, renormalise, scale), "weights")
+    dw = torch.randn((logits.shape[0], k), generator=torch.Generator().manual_seed(dw_seed)).cuda()
+    d = ops.route_backward(dw, logits, e, score, renormalise, scale)
+    assert d.dtype == logits.dtype and d.shape == logits.shape
+    ref.close(d, *ref.route_backward(dw, logits, want, score, renormalise, scale, logits.dtype), "dlogits")
+    assert ops.device_status() == 0
+    return w, e
+
+
+WAYS = list(itertools.product(["softmax", "sigmoid"], [False, True], [False, True]))
+
+
+@pytest.mark.parametrize("score,biased,renormalise", WAYS)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (5, 2, 2), (33, 8, 2), (7, 31, 31), (9, 32, 32), (20, 33, 5), (12, 64, 6), (6, 100, 8),
+                                   (10, 128, 1), (11, 162, 6), (9, 256, 8), (5, 257, 32), (4, 512, 16), (3, 511, 4)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_sizes(ops, m, n, k, score, biased, renormalise, dtype):
+    check(ops, logits_of(m, n, dtype, n + k), k, bias_of(n) if biased else None, score, renormalise=renormalise, scale=2.5)
+
+
+@pytest.mark.parametrize("score,biased,renormalise", WAYS)
+@pytest.mark.parametrize("n,groups,kept,best,k", [(256, 8, 4, 2, 8), (162, 9, 3, 1, 6), (162, 9, 3, 2, 6), (64, 32, 5, 2, 8), (32, 32, 3, 2, 3),
+                                                  (512, 2, 1, 2, 8), (96, 4, 4, 2, 5), (60, 3, 2, 1, 20), (40, 8, 1, 2, 7)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_groups(ops, n, groups, kept, best, k, score, biased, renormalise, dtype):
+    check(ops, logits_of(12, n, dtype, n), k, bias_of(n) if biased else None, score, groups, kept, best, renormalise)
+
+
+def test_strides(ops):
+    wide = logits_of(9, 600, F)
+    for x in (wide[:, :256], wide[:, 1:257], wide[:, 2:258], wide[::2, 4:260], wide[:, ::2][:, :256], wide[:1].expand(4, -1)[:, :256],
+              wide.t()[:9].t()):
+        check(ops, x, 8 if x.shape[1] > 9 else 3, None, "sigmoid")
+    check(ops, wide.to(BF)[:, 1:163], 6)
+    check(ops, wide.to(BF)[:, 8:136], 6)
+
+
+def test_ties_go_to_the_lower_index(ops):
+    n, k = 40, 7
+    for value in (0.0, -0.0, 3.25, -60.0, 80.0):
+        x = torch.full((3, n), value, device="cuda")
+        x[1, 11] = 90.0
+        x[2, ::2] = -x[2, ::2]
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, torch.zeros(n, device="cuda"), torch.full((n,), 0.25, device="cuda")):
+                for how in ({}, {"groups": 8, "kept": 3, "group_best": 2}, {"groups": 5, "kept": 2}):
+                    _, e = check(ops, x, k, bias, score, **how)
+    # logits of few values: ties inside and at the border, with groups of equal sums
+    g = torch.Generator().manual_seed(2)
+    x = torch.randint(-2, 3, (64, 64), generator=g).float().cuda()
+    b = (torch.randint(-1, 2, (64,), generator=g) * 0.125).cuda()
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, b):
+            for how in ({}, {"groups": 8, "kept": 4, "group_best": 2}, {"groups": 8, "kept": 4}):
+                check(ops, x, 8, bias, score, **how)
+
+
+def test_choices_that_fp32_cannot_tell_apart(ops):
+    """Scores that differ by less than fp32 arithmetic's errors are told apart in 64 bits."""
+    n = 64
+    g = torch.Generator().manual_seed(4)
+    for score in ("softmax", "sigmoid"):
+        base = torch.randn((200, 1), generator=g)
+        x = (base + torch.randint(-6, 7, (200, n), generator=g) * 2.0 ** -23).cuda()
+        for how in ({}, {"groups": 8, "kept": 4, "group_best": 2}):
+            check(ops, x, 6, None, score, **how)
+            check(ops, x, 6, torch.zeros(n, device="cuda"), score, **how)
+            check(ops, x, 6, (torch.randint(-2, 3, (n,), generator=g) * 2.0 ** -25).cuda(), score, **how)
+
+
+def test_saturated_scores(ops):
+    """Without a bias the logits decide, also where both scores round to 1 or to 0."""
+    x = torch.tensor([[40.0, 60.0, 50.0, 45.0], [-200.0, -150.0, -170.0, -300.0], [100.0, -100.0, 99.0, -99.0]], device="cuda")
+    for renormalise in (False, True):
+        _, e = check(ops, x, 2, None, "sigmoid", renormalise=renormalise)
+        assert e.tolist() == [[1, 2], [1, 2], [0, 2]]
+        check(ops, x, 3, None, "softmax", renormalise=renormalise)
+    w, _ = ops.route(x, 2, None, "sigmoid")
+    assert torch.allclose(w.sum(1), torch.ones(3, device="cuda"))       # -150 and -170 underflow each, not their shares
+
+
+LOW = {BF: torch.finfo(BF).min, F: torch.finfo(F).min}
+
+
+@pytest.mark.parametrize("score,biased,renormalise", WAYS)
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_masks(ops, score, biased, renormalise, dtype):
+    n, k = 48, 6
+    bias = bias_of(n) if biased else None
+    for how in ({}, {"groups": 6, "kept": 3, "group_best": 2}, {"groups": 6, "kept": 2}):
+        x = logits_of(8, n, dtype, 9)
+        x[0] = -math.inf                            # reaches none
+        x[1, :45] = -math.inf                       # reaches three
+        x[2, 8:] = -math.inf                        # one group
+        x[3, ::2] = -math.inf
+        x[4, 5:] = LOW[dtype]                       # a mask of the type's lowest value can be chosen
+        x[5] = LOW[dtype]
+        x[6, 1:] = -math.inf
+        w, e = check(ops, x, k, bias, score, renormalise=renormalise, **how)
+        assert (e[0] == -1).all() and (w[0] == 0).all()
+        if biased:                                   # a bias of -inf puts an expert out of everyone's reach
+            off = bias.clone()
+            off[:20] = -math.inf
+            _, e = check(ops, x, k, off, score, renormalise=renormalise, **how)
+            assert ((e == -1) | (e >= 20)).all()
+
+
+@pytest.mark.parametrize("score,biased,renormalise", WAYS)
+def test_nan_is_seen_and_stays_in_its_row(ops, score, biased, renormalise):
+    n, k = 40, 4
+    bias = bias_of(n) if biased else None
+    x = logits_of(6, n, F)
+    clean, ce = ops.route(x, k, bias, score, renormalise=renormalise)
+    x[2, 7] = math.nan
+    x[4] = math.nan
+    for how in ({}, {"groups": 4, "kept": 2, "group_best": 2}):
+        w, e = ops.route(x, k, bias, score, renormalise=renormalise, **how)
+        assert torch.isnan(w[2]).all() and torch.isnan(w[4]).all()
+        assert ((e >= 0) & (e < n)).all() and (e[2] != 7).all()
+        assert all(len(set(r)) == k for r in e.tolist())
+    w, e = ops.route(x, k, bias, score, renormalise=renormalise)
+    keep = [0, 1, 3, 5]
+    assert torch.equal(w[keep], clean[keep]) and torch.equal(e[keep], ce[keep])
+    x = logits_of(2, n, F)
+    x[1, 3] = math.inf
+    w, e = ops.route(x, k, bias, score, renormalise=renormalise)
+    assert torch.isfinite(w[0]).all()
+    if score == "softmax":
+        assert torch.isnan(w[1]).all()
+    else:
+        # 1, and the best only where no bias counts against it
+        assert torch.isfinite(w[1]).all() and torch.equal(e.cpu(), ref.choose(x, k, bias, score)) and (biased or e[1, 0] == 3)
+    if biased:
+        bias[5] = math.nan
+        assert torch.isnan(ops.route(x, k, bias, score, renormalise=renormalise)[0]).all()
+
+
+def test_backward_takes_an_expert_twice_and_none(ops):
+    x = logits_of(3, 20, F)
+    e = torch.tensor([[4, 4, -1], [19, 0, 19], [-1, -1, -1]], dtype=torch.int32, device="cuda")
+    dw = torch.randn((3, 3), generator=torch.Generator().manual_seed(3)).cuda()
+    for score, _, renormalise in WAYS:
+        d = ops.route_backward(dw, x, e, score, renormalise, 1.5)
+        ref.close(d, *ref.route_backward(dw, x, e.cpu(), score, renormalise, 1.5, F), "dlogits")
+        assert (d[2] == 0).all()
+
+
+@pytest.mark.parametrize("score,_,renormalise", WAYS[::2] + WAYS[1::2][:2])
+def test_gradient_against_differences(ops, score, _, renormalise):
+    n, k, step = 12, 4, 1e-6
+    x = logits_of(3, n, F, 8)
+    w, e = ops.route(x, k, None, score, renormalise=renormalise, scale=2.0)
+    v = torch.randn((3, k), generator=torch.Generator().manual_seed(1))
+    d = ops.route_backward(v.cuda(), x, e, score, renormalise, 2.0).cpu().double()
+
+    def f(l):
+        return (ref.route_weights(l, e.cpu(), score, renormalise, 2.0)[0] * v.double()).sum(1)
+    xd = x.cpu().double()
+    for i in range(n):
+        h = torch.zeros(n, dtype=torch.float64)
+        h[i] = step
+        assert torch.allclose(d[:, i], (f(xd + h) - f(xd - h)) / (2 * step), rtol=1e-5, atol=1e-6)
+
+
+def test_no_tokens(ops):
+    x = torch.empty((0, 16), device="cuda")
+    w, e = ops.route(x, 3)
+    assert w.shape == e.shape == (0, 3)
+    assert ops.route_backward(w, x, e).shape == (0, 16)
