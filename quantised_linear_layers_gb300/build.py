@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqlinear.so")
-SOURCES = ["api.cu", "cast.cu", "exchange.cu", "fp4_cast.cu", "fp4_gemm.cu", "fp4_gemm_pair.cu", "gemm.cu", "gemm_mx.cu", "gemm_mx2.cu", "gemm_mx_sk.cu", "gemm_pair.cu", "gemm_prom_sk.cu", "noalloc.cu", "norm.cu", "route.cu"]
+SOURCES = ["api.cu", "cast.cu", "exchange.cu", "fp4_cast.cu", "fp4_gemm.cu", "fp4_gemm_pair.cu", "gemm.cu", "gemm_mx.cu", "gemm_mx2.cu", "gemm_mx_sk.cu", "gemm_pair.cu", "gemm_prom_sk.cu", "noalloc.cu", "norm.cu", "norm_back.cu", "route.cu"]
 TORCH_SOURCE = "fp4_torch.cpp"                 # the calls over torch tensors (module _fp4)
 TORCH_HEADERS = ["layers_torch.h"]             # what it includes of this folder
 TORCH_LIB = os.path.join(HERE, "_fp4.so")

@@ -1,25 +1,286 @@
-// Layer norm: y = (x - mean) rstd w + b over the rows of x, and its gradients.
+// Layer norm: y = (x - mean) rstd w + b over the rows of x. Backward: norm_back.cu.
 //
 // mean and variance are those of the row's own elements in fp32: a first sum for
 // the mean, then sums of d = x - mean and of d^2, whose first corrects the mean's
-// rounding (so rows far from zero lose nothing to it).
-//
-// Backward, with h = (x - mean) rstd and g = dy w:
-//   dx = rstd (g - sum(g) / n - h sum(g h) / n),  dw = sum_rows dy h,  db = sum_rows dy
+// rounding (so rows far from zero lose nothing to it). A row is read once and stays
+// in its threads' registers, as pairs of fp32; bound by memory, and by instructions
+// next to it.
+#include "gemm.cuh"
 #include "norm.cuh"
-
-#include "rows.cuh"
+#include "norm_rows.cuh"
 
 namespace ql {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kSms = 152;             // for sizes that a caller asks for without a device
 
-template <typename B>
-__device__ __forceinline__ float weight_at(const void* w, bool bf16, int64_t i, const B& b, int span) {
-    return bf16 ? to_f32(load_one(static_cast<const __nv_bfloat16*>(w) + i, b, span, from_f32<__nv_bfloat16>(0.0f)))
-                : load_one(static_cast<const float*>(w) + i, b, span, 0.0f);
+// A run's deviations from `about`, in its place, and the sums of them and of their squares;
+// elements past the row's ends stay zero.
+template <int W, bool EDGE>
+__device__ __forceinline__ void deviations(F2* v, float about, int c, int n, F2& s1, F2& s2) {
+    const F2 off = f2(-about, -about);
+    if (EDGE && (c < 0 || c + W > n)) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            float a, b;
+            unpack(v[i], a, b);
+            v[i] = f2(c + 2 * i >= 0 && c + 2 * i < n ? a - about : 0.0f, c + 2 * i + 1 >= 0 && c + 2 * i + 1 < n ? b - about : 0.0f);
+        }
+    } else if (EDGE || c < n) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[i] = add2(v[i], off);
+    }
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+        s1 = add2(s1, v[i]);
+        s2 = fma2(v[i], v[i], s2);
+    }
+}
+
+// Two sums over a warp's or a block's row.
+template <bool WARP>
+__device__ __forceinline__ void team_sum(float& a, float& b, float* s) {
+    if constexpr (WARP) {
+        const float v = sums_over_warp(a, b);
+        a = __shfl_sync(0xffffffffu, v, 0);
+        b = __shfl_sync(0xffffffffu, v, 16);
+    } else {
+        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        float v = sums_over_warp(a, b);
+        if ((lane & 15) == 0) s[(lane >> 4) * 32 + (threadIdx.x >> 5)] = v;
+        __syncthreads();
+        a = lane < warps ? s[lane] : 0.0f;
+        b = lane < warps ? s[32 + lane] : 0.0f;
+        v = sums_over_warp(a, b);
+        a = __shfl_sync(0xffffffffu, v, 0);
+        b = __shfl_sync(0xffffffffu, v, 16);
+    }
+}
+
+// ---------------------------------------------------------------- rows in registers
+// Element i of run u of thread t: whole vectors, or (SPREAD) elements a team apart, which
+// take any boundary and any length and are whole lines to a warp all the same.
+template <int W, bool SPREAD>
+__device__ __forceinline__ int column(int u, int i, int t, int team) {
+    return SPREAD ? (u * W + i) * team + t : (u * team + t) * W + i;
+}
+template <int W, bool SPREAD, typename T, typename B>
+__device__ __forceinline__ void load_columns(F2* v, const T* row, int u, int t, int team, int n, const B& bnd, int span) {
+    Pack<T, W> p = zero_pack<T, W>();
+    if constexpr (SPREAD) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (column<W, true>(u, i, t, team) < n) p.v[i] = load_one(row + column<W, true>(u, i, t, team), bnd, span, p.v[i]);
+    } else if (column<W, false>(u, 0, t, team) < n) {
+        p = load_pack<T, W>(row + column<W, false>(u, 0, t, team), bnd, span);
+    }
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) v[i] = pair_of<W>(p, i);
+}
+template <int W, bool SPREAD, typename B>
+__device__ __forceinline__ void load_weight_columns(F2* v, const void* p, bool bf16, float other, int u, int t, int team, int n, const B& bnd, int span) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[i] = f2(other, other);
+    } else if (bf16) {
+        load_columns<W, SPREAD>(v, static_cast<const __nv_bfloat16*>(p), u, t, team, n, bnd, span);
+    } else {
+        load_columns<W, SPREAD>(v, static_cast<const float*>(p), u, t, team, n, bnd, span);
+    }
+}
+
+// A row to a warp (eight rows to a block) or to a block.
+template <typename T, typename O, int W, int E, bool WARP, bool SPREAD>
+__global__ void __launch_bounds__(WARP ? 256 : (E <= 8 ? 1024 : 512)) norm_kernel(const NormArgs p) {
+    constexpr int U = E / W, H = W / 2;
+    __shared__ float s_sum[WARP ? 1 : 2 * 64];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int t = WARP ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x);
+    const int team = WARP ? 32 : static_cast<int>(blockDim.x);
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x);
+    if (row >= p.m) return;
+    const int n = static_cast<int>(p.n);
+    const T* x = static_cast<const T*>(p.x) + row * p.sx;
+    F2 v[E / 2], sum = 0ull;
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_columns<W, SPREAD>(v + u * H, x, u, t, team, n, p.bnd, 0);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) sum = add2(sum, v[e]);
+    const float inv_n = 1.0f / static_cast<float>(n);
+    float about = sum2(sum), none = 0.0f;
+    team_sum<WARP>(about, none, s_sum);
+    about *= inv_n;
+    F2 s1 = 0ull, s2 = 0ull;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < H; ++i) {                      // elements past the row's end stay zero
+            F2& d = v[u * H + i];
+            if constexpr (SPREAD) {
+                float a, b;
+                unpack(d, a, b);
+                d = f2(column<W, true>(u, 2 * i, t, team) < n ? a - about : 0.0f, column<W, true>(u, 2 * i + 1, t, team) < n ? b - about : 0.0f);
+            } else if (column<W, false>(u, 0, t, team) < n) {
+                d = add2(d, f2(-about, -about));
+            }
+            s1 = add2(s1, d);
+            s2 = fma2(d, d, s2);
+        }
+    float m1 = sum2(s1), m2 = sum2(s2);
+    team_sum<WARP>(m1, m2, s_sum + (WARP ? 0 : 64));
+    m1 *= inv_n;
+    const float rstd = rsqrtf(fmaxf(m2 * inv_n - m1 * m1, 0.0f) + p.eps);
+    if (p.mean != nullptr && t == 0) {
+        store_one(p.mean + row, about + m1, p.bnd, 4);
+        store_one(p.rstd + row, rstd, p.bnd, 5);
+    }
+    const F2 r2 = f2(rstd, rstd), back = f2(-m1 * rstd, -m1 * rstd);
+    O* y = static_cast<O*>(p.y) + row * p.sy;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (column<W, SPREAD>(u, 0, t, team) >= n) continue;
+        F2 w[H], b[H];
+        load_weight_columns<W, SPREAD>(w, p.w, p.w_bf16, 1.0f, u, t, team, n, p.bnd, 1);
+        load_weight_columns<W, SPREAD>(b, p.b, p.w_bf16, 0.0f, u, t, team, n, p.bnd, 2);
+        Pack<O, W> o;
+#pragma unroll
+        for (int i = 0; i < H; ++i) set_pair<W>(o, i, fma2(fma2(v[u * H + i], r2, back), w[i], b[i]));
+        if constexpr (SPREAD) {
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                if (column<W, true>(u, i, t, team) < n) store_one(y + column<W, true>(u, i, t, team), o.v[i], p.bnd, 3);
+        } else {
+            store_pack<O, W>(y + column<W, false>(u, 0, t, team), o, p.bnd, 3);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- many rows
+// The same by teams with their rows on the way through shared memory, R rows at a time
+// so that their sums share exchanges and barriers: a row's arithmetic is 6 instructions
+// an element, and a thread's part of the sums 100 a row were it alone.
+template <typename T, typename O, int E, bool EDGE>
+__global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const NormArgs p, const Teams f, bool y_vec, bool w_vec) {
+    constexpr int W = 16 / sizeof(T), U = E / W, H = W / 2, XB = 16;
+    constexpr int R = E <= 16 ? 2 : 1;                     // (32 elements twice: no registers left)
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    __shared__ float s_sum[2][128];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int id = static_cast<int>(threadIdx.x) / f.team, t = static_cast<int>(threadIdx.x) - id * f.team;
+    const int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * id, step = static_cast<int64_t>(gridDim.x) * f.teams;
+    const int n = static_cast<int>(p.n), all = static_cast<int>(blockDim.x);
+    const int shift = EDGE ? static_cast<int>((f.at.base + static_cast<int64_t>(blockIdx.x) * f.at.stride) % W) : 0;
+    const int c0 = t * W - shift, cu = f.team * W;         // run u starts at column c0 + u * cu
+
+    // [stage][R][U] runs, a thread's side by side; then a team's weights and biases, [2][E]
+    const int line = all * E * static_cast<int>(sizeof(T)), stage = R * line;
+    uint8_t* my_x = s_mem + threadIdx.x * XB;
+    ulonglong2* my_w = reinterpret_cast<ulonglong2*>(s_mem + f.stages * stage) + t;               // + i * team
+    if (EDGE || n < U * cu)
+        for (int s = 0; s < f.stages * R * U; ++s) *reinterpret_cast<uint4*>(my_x + s * all * XB) = make_uint4(0u, 0u, 0u, 0u);
+    const T *lo = static_cast<const T*>(p.x), *hi = lo + (p.m - 1) * p.sx + n;
+    const T* x_next = lo + first * p.sx;
+    int64_t row_next = first;
+    auto fetch = [&](int at) {                             // R rows into the stage that begins at byte `at`
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row_next < p.m) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) fetch_run<W, EDGE>(my_x + at + r * line + u * all * XB, x_next, c0 + u * cu, n, true, lo, hi, p.bnd, 0);
+            }
+            row_next += step;
+            x_next += step * p.sx;
+        }
+        copy_commit();                                     // a group for every stage, also past the last row
+    };
+    for (int s = 0; s < f.stages; ++s) fetch(s * stage);
+    if (id == 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            F2 w[H], b[H];
+            weight_run<W, EDGE>(w, p.w, p.w_bf16, 1.0f, c0 + u * cu, n, w_vec && shift == 0, p.bnd, 1);
+            weight_run<W, EDGE>(b, p.b, p.w_bf16, 0.0f, c0 + u * cu, n, w_vec && shift == 0, p.bnd, 2);
+#pragma unroll
+            for (int i = 0; i < H / 2; ++i) {
+                my_w[(u * (H / 2) + i) * f.team] = make_ulonglong2(w[2 * i], w[2 * i + 1]);
+                my_w[(E / 4 + u * (H / 2) + i) * f.team] = make_ulonglong2(b[2 * i], b[2 * i + 1]);
+            }
+        }
+    }
+    __syncthreads();
+    const float inv_n = 1.0f / static_cast<float>(n);
+    O* y = static_cast<O*>(p.y) + first * p.sy;
+    float *mean = p.mean + first, *rstd_to = p.rstd + first;
+    int at = 0;
+    for (int64_t row = first; row < p.m; row += R * step) {
+        copy_wait(f.stages);
+        F2 v[R][E / 2];
+        float about[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            F2 sum = 0ull;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + r * line + u * all * XB);
+                if (EDGE && (c0 + u * cu < 0 || c0 + u * cu + W > n)) mask_run<W>(x, c0 + u * cu, n);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    v[r][u * H + i] = pair_of<W>(x, i);
+                    sum = add2(sum, v[r][u * H + i]);
+                }
+            }
+            about[r] = sum2(sum);
+        }
+        fetch(at);                                         // the rows are in registers
+        at = at + stage == f.stages * stage ? 0 : at + stage;
+        sum_over_team(about[0], about[1], s_sum[0], f.team, id);
+        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};             // sums of d, then of d^2
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            about[r] *= inv_n;
+            F2 s1 = 0ull, s2 = 0ull;
+#pragma unroll
+            for (int u = 0; u < U; ++u) deviations<W, EDGE>(v[r] + u * H, about[r], c0 + u * cu, n, s1, s2);
+            m[r] = sum2(s1);
+            m[2 + r] = sum2(s2);
+        }
+        if constexpr (R == 2) sum4_over_team(m, s_sum[1], f.team, id);
+        else sum_over_team(m[0], m[2], s_sum[1], f.team, id);
+        F2 r2[R], back[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float m1 = m[r] * inv_n, rstd = rsqrtf(fmaxf(m[2 + r] * inv_n - m1 * m1, 0.0f) + p.eps);
+            if (p.mean != nullptr && t == 0 && row + r * step < p.m) {
+                store_one(mean + r * step, about[r] + m1, p.bnd, 4);
+                store_one(rstd_to + r * step, rstd, p.bnd, 5);
+            }
+            r2[r] = f2(rstd, rstd);
+            back[r] = f2(-m1 * rstd, -m1 * rstd);
+        }
+        mean += R * step;
+        rstd_to += R * step;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * cu;
+            if (c >= n) continue;
+            F2 o[R][H];
+#pragma unroll
+            for (int i = 0; i < H / 2; ++i) {
+                const ulonglong2 w = my_w[(u * (H / 2) + i) * f.team], b = my_w[(E / 4 + u * (H / 2) + i) * f.team];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    o[r][2 * i] = fma2(fma2(v[r][u * H + 2 * i], r2[r], back[r]), w.x, b.x);
+                    o[r][2 * i + 1] = fma2(fma2(v[r][u * H + 2 * i + 1], r2[r], back[r]), w.y, b.y);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r == 0 || row + r * step < p.m) store_run<W, EDGE>(y + r * step * p.sy, o[r], c, n, y_vec, p.bnd, 3);
+        }
+        y += R * step * p.sy;
+    }
 }
 
 // ---------------------------------------------------------------- any length
@@ -46,135 +307,93 @@ __global__ void __launch_bounds__(kThreads) norm_any_kernel(const NormArgs p) {
         }
         sum_over_row<2, false>(two, s_sum + 32);
         const float off = two[0] / n;
-        const float rstd = 1.0f / sqrtf(fmaxf(two[1] / n - off * off, 0.0f) + p.eps);
+        const float rstd = rsqrtf(fmaxf(two[1] / n - off * off, 0.0f) + p.eps);
         if (p.mean != nullptr && threadIdx.x == 0) {
             store_one(p.mean + row, about + off, p.bnd, 4);
             store_one(p.rstd + row, rstd, p.bnd, 5);
         }
         for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
-            float h = (to_f32(load_one(x + i, p.bnd, 0, zero)) - about - off) * rstd;
-            if (p.w != nullptr) h *= weight_at(p.w, p.w_bf16, i, p.bnd, 1);
-            if (p.b != nullptr) h += weight_at(p.b, p.w_bf16, i, p.bnd, 2);
-            store_one(y + i, from_f32<O>(h), p.bnd, 3);
+            const float h = (to_f32(load_one(x + i, p.bnd, 0, zero)) - about - off) * rstd;
+            float w[1], b[1];
+            load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 1);
+            load_weights<1>(b, p.b, p.w_bf16, i, 0.0f, p.bnd, 2);
+            store_one(y + i, from_f32<O>(fmaf(h, w[0], b[0])), p.bnd, 3);
         }
     }
 }
 
-template <typename T, typename D>
-__global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(const NormBackArgs p) {
-    __shared__ float s_sum[2 * 32];
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const float n = static_cast<float>(p.n);
-    for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x) {
-        const T* x = static_cast<const T*>(p.x) + row * p.sx;
-        const D* dy = static_cast<const D*>(p.dy) + row * p.sdy;
-        T* dx = static_cast<T*>(p.dx) + row * p.sdx;
-        const float mean = load_one(p.mean + row, p.bnd, 2, 0.0f), rstd = load_one(p.rstd + row, p.bnd, 3, 0.0f);
-        float c[2] = {0.0f, 0.0f};
-        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
-            float g = to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f)));
-            if (p.w != nullptr) g *= weight_at(p.w, p.w_bf16, i, p.bnd, 4);
-            c[0] += g;
-            c[1] = fmaf(g, (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd, c[1]);
-        }
-        __syncthreads();
-        sum_over_row<2, false>(c, s_sum);
-        const float c1 = c[0] / n, c2 = c[1] / n;
-        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
-            float g = to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f)));
-            if (p.w != nullptr) g *= weight_at(p.w, p.w_bf16, i, p.bnd, 4);
-            const float h = (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd;
-            store_one(dx + i, from_f32<T>(rstd * (g - c1 - h * c2)), p.bnd, 5);
-        }
-    }
+// Whether a call's rows are whole aligned vectors.
+template <typename T, typename O>
+bool whole_vectors(const NormArgs& a) {
+    constexpr int W = 16 / sizeof(T);
+    const Boundary x = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
+    return x.base == 0 && x.stride == 0 && a.n % W == 0 && same_boundary(x, boundary_of(a.y, sizeof(O), a.sy, a.m, W)) &&
+           aligned_to(a.w, 16) && aligned_to(a.b, 16);
 }
 
-// Sums of dy h and dy over the rows of a part, a column per thread of a row of
-// threads; part blockIdx.y has rows [y * rows, (y + 1) * rows).
-template <typename T, typename D>
-__global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(const NormBackArgs p, int64_t rows) {
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (col >= p.n) return;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows, r1 = r0 + rows < p.m ? r0 + rows : p.m;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        const float dy = to_f32(load_one(static_cast<const D*>(p.dy) + r * p.sdy + col, p.bnd, 0, from_f32<D>(0.0f)));
-        const float x = to_f32(load_one(static_cast<const T*>(p.x) + r * p.sx + col, p.bnd, 1, from_f32<T>(0.0f)));
-        dw = fmaf(dy, (x - load_one(p.mean + r, p.bnd, 2, 0.0f)) * load_one(p.rstd + r, p.bnd, 3, 0.0f), dw);
-        db += dy;
-    }
-    float* part = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.n;
-    store_one(part + col, dw, p.bnd, 6);
-    store_one(part + p.n + col, db, p.bnd, 6);
+template <typename T, typename O, int E, bool WARP>
+cudaError_t norm_e(const NormArgs& a, bool whole, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    const dim3 grid(static_cast<unsigned>(WARP ? (a.m + 7) / 8 : a.m));
+    const int threads = WARP ? 256 : team_of(a.n, E, false, W);
+    if (whole) return launch_after(norm_kernel<T, O, W, E, WARP, false>, grid, threads, 0, st, a);
+    return launch_after(norm_kernel<T, O, W, E, WARP, true>, grid, threads, 0, st, a);
 }
 
-// dw and db: the parts' sums, 32 columns by 8 shares of the parts per block, in a
-// fixed order.
-__global__ void __launch_bounds__(kThreads) norm_dw_join_kernel(const NormBackArgs p, int parts) {
-    __shared__ float s[8][33];
-    pdl_launch_dependents();
-    pdl_wait_prior();
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + tx;      // of 2 n
-    float v = 0.0f;
-    if (col < 2 * p.n)
-#pragma unroll 4
-        for (int i = ty; i < parts; i += 8) v += load_one(p.part + i * 2 * p.n + col, p.bnd, 6, 0.0f);
-    s[ty][tx] = v;
-    __syncthreads();
-    if (ty == 0 && col < 2 * p.n) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][tx];
-        if (col < p.n) store_one(p.dw + col, v, p.bnd, 7);
-        else store_one(p.db + col - p.n, v, p.bnd, 8);
-    }
+// Rows to a team from which the ring pays for its start. Measured, teams / a row to a
+// block or warp, us:
+//   whole vectors  2048 x 2048 (2 rows) 6.3 / 6.2, 1003 x 4096 fp32 (3) 11.0 / 9.1, 1024 x 8000 fp32 (7) 18.3 / 19.4,
+//                  16384 x 1024 (8) 18.0 / 20.3, 4096 x 4096 (9) 20.7 / 18.9, 4096 x 7168 (13) 27.5 / 31.7,
+//                  16384 x 7168 (54) 82 / 108
+//   others         1003 x 4099 fp32 (2) 14.0 / 13.0, 16384 x 1023 (8) 29.2 / 35.4, 4096 x 4095 (9) 28.2 / 45.5
+// and never for the shortest rows: 16384 x 96 (7) 5.3 / 5.0, 16384 x 97 8.4 / 5.8.
+constexpr int kLeastRows = 6;
+
+// Rows by teams: false where that many rows are too few for it.
+template <typename T, typename O, int E>
+bool rows_e(const NormArgs& a, bool whole, cudaStream_t st, int num_sms, cudaError_t& e) {
+    constexpr int W = 16 / sizeof(T);
+    Teams f;
+    f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
+    const bool y_vec = same_boundary(f.at, boundary_of(a.y, sizeof(O), a.sy, a.m, W)), w_vec = aligned_to(a.w, 16) && aligned_to(a.b, 16);
+    auto kern = whole ? norm_rows_kernel<T, O, E, false> : norm_rows_kernel<T, O, E, true>;
+    f.team = team_of(a.n, E, !whole, W);
+    const int64_t blocks = blocks_of(a.m, num_sms, f.at);
+    f.teams = teams_of(a.m, blocks, f.team, E <= 16 ? 896 : 512);
+    if (a.m < blocks * f.teams * kLeastRows) return false;
+    const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T)) * (E <= 16 ? 2 : 1), weights = f.team * E * 8;
+    f.stages = (kNormRoom - weights) / stage;
+    if (f.stages > 4) f.stages = 4;
+    const int smem = f.stages * stage + weights;
+    e = cudaSuccess;
+    if (smem > 46 * 1024)                                  // 48 KB without being asked for
+        e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kNormRoom);
+    if (e == cudaSuccess) e = launch_after(kern, dim3(static_cast<unsigned>(blocks)), threads, static_cast<size_t>(smem), st, a, f, y_vec, w_vec);
+    return true;
 }
-
-unsigned grid_of(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 1 : (n < most ? n : most)); }
-
-// Parts of the rows for the column sums: enough blocks for every SM to have four.
-int64_t any_parts(int64_t m, int64_t n) {
-    const int64_t cols = (n + kThreads - 1) / kThreads;
-    int64_t parts = (kSms * 4 + cols - 1) / cols;
-    if (parts > (m + 15) / 16) parts = (m + 15) / 16;
-    return parts < 1 ? 1 : parts;
-}
-
 template <typename T, typename O>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t st, int num_sms) {
-    return launch_after(norm_any_kernel<T, O>, dim3(grid_of(a.m, static_cast<int64_t>(num_sms) * 8)), kThreads, 0, st, a);
-}
-
-template <typename T, typename D>
-cudaError_t back_t(const NormBackArgs& a, cudaStream_t st, int num_sms) {
-    if (cudaError_t e = launch_after(norm_dx_any_kernel<T, D>, dim3(grid_of(a.m, static_cast<int64_t>(num_sms) * 8)), kThreads, 0, st, a);
-        e != cudaSuccess || a.dw == nullptr)
-        return e;
-    const int64_t parts = any_parts(a.m, a.n), rows = (a.m + parts - 1) / parts;
-    if (cudaError_t e = launch_after(norm_dw_any_kernel<T, D>, dim3(static_cast<unsigned>((a.n + kThreads - 1) / kThreads), static_cast<unsigned>(parts)),
-                                     kThreads, 0, st, a, rows);
-        e != cudaSuccess)
-        return e;
-    return launch_after(norm_dw_join_kernel, dim3(static_cast<unsigned>((2 * a.n + 31) / 32)), kThreads, 0, st, a, static_cast<int>(parts));
+    constexpr int W = 16 / sizeof(T);
+    if (a.n > kNormLongest) {
+        const int64_t most = static_cast<int64_t>(num_sms) * 8;
+        return launch_after(norm_any_kernel<T, O>, dim3(static_cast<unsigned>(a.m < most ? a.m : most)), kThreads, 0, st, a);
+    }
+    const bool whole = whole_vectors<T, O>(a);
+    cudaError_t e;
+    if (a.n <= 256 - W) return norm_e<T, O, 8, true>(a, whole, st);
+    if (a.n <= 8192 - W ? rows_e<T, O, 16>(a, whole, st, num_sms, e) : rows_e<T, O, 32>(a, whole, st, num_sms, e)) return e;
+    if (a.n <= 1024 - W) return norm_e<T, O, 32, true>(a, whole, st);
+    // few elements to a thread where few rows leave a block alone on its SM (1 x 7168 2.8 us, 12.6 by a
+    // loop of 256 threads) and where elements go one by one; 4096 x 7168 takes 31.7 with 32 and 67 with 8
+    if (a.n <= 8192 - W && (a.m <= num_sms || !whole)) return norm_e<T, O, 8, false>(a, whole, st);
+    return norm_e<T, O, 32, false>(a, whole, st);
 }
 
 }  // namespace
 
-size_t norm_back_workspace(int64_t m, int64_t n) {
-    return static_cast<size_t>(any_parts(m, n)) * 2 * static_cast<size_t>(n) * sizeof(float);
-}
-
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st, int num_sms) {
     if (a.x_bf16) return a.y_bf16 ? norm_t<__nv_bfloat16, __nv_bfloat16>(a, st, num_sms) : norm_t<__nv_bfloat16, float>(a, st, num_sms);
     return a.y_bf16 ? norm_t<float, __nv_bfloat16>(a, st, num_sms) : norm_t<float, float>(a, st, num_sms);
-}
-
-cudaError_t launch_norm_back(const NormBackArgs& a, cudaStream_t st, int num_sms) {
-    if (a.x_bf16) return a.dy_bf16 ? back_t<__nv_bfloat16, __nv_bfloat16>(a, st, num_sms) : back_t<__nv_bfloat16, float>(a, st, num_sms);
-    return a.dy_bf16 ? back_t<float, __nv_bfloat16>(a, st, num_sms) : back_t<float, float>(a, st, num_sms);
 }
 
 }  // namespace ql

@@ -1,0 +1,363 @@
+// Layer norm's gradients. With h = (x - mean) rstd and g = dy w:
+//   dx = rstd (g - sum(g) / n - h sum(g h) / n),  dw = sum_rows dy h,  db = sum_rows dy
+//
+// Bound by memory: x and dy are read once for all three. Every block goes over rows
+// with a fixed set of columns to each thread, which adds up their dw and db in
+// registers; a second kernel joins the blocks' sums in a fixed order.
+#include "gemm.cuh"
+#include "norm.cuh"
+#include "norm_rows.cuh"
+
+namespace ql {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowThreads = 512;          // of a block with whole rows
+constexpr int64_t kSms = 152;             // for sizes that a caller asks for without a device
+
+// ---------------------------------------------------------------- rows of up to 16368 columns
+// With d = x - mean, q = dy rstd and g = q w (that is rstd dy w):
+//   dx = g - d rstd^2 sum(g d) / n - sum(g) / n,  dw += q d,  db += dy
+// Elements past a row's ends have x = dy = w = 0 and add nothing.
+//
+// The rows to come are on their way into a ring of `stages` rows in shared memory, in
+// which each thread copies and reads only what is its own: no thread waits for
+// another's copy, and a row's threads for one another only at its two sums.
+template <typename T, typename D, int E, bool EDGE>
+__global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackArgs p, const Teams f, bool dy_vec, bool dx_vec, bool w_vec) {
+    constexpr int W = 16 / sizeof(T), U = E / W, H = W / 2, XB = W * sizeof(T), DB = W * sizeof(D);
+    constexpr bool KEEP = E <= 16;                         // a row's d and g in registers, and the weights
+    extern __shared__ __align__(16) uint8_t s_mem[];
+    __shared__ float s_sum[2][64];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int id = static_cast<int>(threadIdx.x) / f.team, t = static_cast<int>(threadIdx.x) - id * f.team;
+    const int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * id, step = static_cast<int64_t>(gridDim.x) * f.teams;
+    const int n = static_cast<int>(p.n), all = static_cast<int>(blockDim.x);
+    const int shift = EDGE ? static_cast<int>((f.at.base + static_cast<int64_t>(blockIdx.x) * f.at.stride) % W) : 0;
+    const int c0 = t * W - shift, cu = f.team * W;         // run u starts at column c0 + u * cu
+
+    // [stage][U] runs of x and of dy, then (not KEEP) [E] weights, a thread's side by side
+    const int stage = all * U * (XB + DB);
+    uint8_t* my_x = s_mem + threadIdx.x * XB;
+    uint8_t* my_dy = s_mem + all * U * XB + threadIdx.x * DB;
+    ulonglong2* my_w = reinterpret_cast<ulonglong2*>(s_mem + f.stages * stage) + threadIdx.x;     // + i * all
+    for (int s = 0; s < f.stages; ++s)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            *reinterpret_cast<Pack<T, W>*>(my_x + s * stage + u * all * XB) = zero_pack<T, W>();
+            *reinterpret_cast<Pack<D, W>*>(my_dy + s * stage + u * all * DB) = zero_pack<D, W>();
+        }
+    const T *x_lo = static_cast<const T*>(p.x), *x_hi = x_lo + (p.m - 1) * p.sx + n;
+    const D *dy_lo = static_cast<const D*>(p.dy), *dy_hi = dy_lo + (p.m - 1) * p.sdy + n;
+    const T* x_next = x_lo + first * p.sx;
+    const D* dy_next = dy_lo + first * p.sdy;
+    int64_t row_next = first;
+    auto fetch = [&](int at) {                             // into the stage that begins at byte `at`
+        if (row_next < p.m) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                fetch_run<W, EDGE>(my_x + at + u * all * XB, x_next, c0 + u * cu, n, true, x_lo, x_hi, p.bnd, 1);
+                fetch_run<W, EDGE>(my_dy + at + u * all * DB, dy_next, c0 + u * cu, n, dy_vec, dy_lo, dy_hi, p.bnd, 0);
+            }
+        }
+        copy_commit();                                     // a group for every row, also past the last
+        row_next += step;
+        x_next += step * p.sx;
+        dy_next += step * p.sdy;
+    };
+    for (int s = 0; s < f.stages; ++s) fetch(s * stage);
+    F2 w[KEEP ? E / 2 : H];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        F2* v = w + (KEEP ? u * H : 0);
+        weight_run<W, EDGE>(v, p.w, p.w_bf16, 1.0f, c0 + u * cu, n, w_vec && shift == 0, p.bnd, 4);
+        if constexpr (!KEEP) {
+#pragma unroll
+            for (int i = 0; i < H / 2; ++i) my_w[(u * (H / 2) + i) * all] = make_ulonglong2(v[2 * i], v[2 * i + 1]);
+        }
+    }
+    auto weights = [&](int u, F2 (&v)[H]) {                // of run u
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) v[i] = w[u * H + i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < H / 2; ++i) {
+                const ulonglong2 two = my_w[(u * (H / 2) + i) * all];
+                v[2 * i] = two.x;
+                v[2 * i + 1] = two.y;
+            }
+        }
+    };
+    F2 dw[E / 2], db[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = 0ull;
+    const float *mean_next = p.mean + first, *rstd_next = p.rstd + first;
+    float mean = 0.0f, rstd = 0.0f;
+    if (first < p.m) {
+        mean = load_one(mean_next, p.bnd, 2, 0.0f);
+        rstd = load_one(rstd_next, p.bnd, 3, 0.0f);
+    }
+    T* dx = static_cast<T*>(p.dx) + first * p.sdx;
+    const float inv_n = 1.0f / static_cast<float>(n);
+    int at = 0, turn = 0;
+    for (int64_t row = first; row < p.m; row += step, dx += step * p.sdx) {
+        float mean2 = 0.0f, rstd2 = 0.0f;                  // the next row's
+        mean_next += step;
+        rstd_next += step;
+        if (row + step < p.m) {
+            mean2 = load_one(mean_next, p.bnd, 2, 0.0f);
+            rstd2 = load_one(rstd_next, p.bnd, 3, 0.0f);
+        }
+        copy_wait(f.stages);
+        const F2 off = f2(-mean, -mean), r2 = f2(rstd, rstd);
+        F2 d[KEEP ? E / 2 : 1], g[KEEP ? E / 2 : 1];
+        F2 sg = 0ull, sgd = 0ull;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + u * all * XB);
+            Pack<D, W> dy = *reinterpret_cast<const Pack<D, W>*>(my_dy + at + u * all * DB);
+            if (EDGE && (c0 + u * cu < 0 || c0 + u * cu + W > n)) {
+                mask_run<W>(x, c0 + u * cu, n);
+                mask_run<W>(dy, c0 + u * cu, n);
+            }
+            F2 wu[H];
+            weights(u, wu);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int e = u * H + i;
+                const F2 v = pair_of<W>(dy, i), de = add2(pair_of<W>(x, i), off), q = mul2(v, r2), ge = mul2(q, wu[i]);
+                dw[e] = fma2(q, de, dw[e]);
+                db[e] = add2(db[e], v);
+                sg = add2(sg, ge);
+                sgd = fma2(ge, de, sgd);
+                if constexpr (KEEP) {
+                    d[e] = de;
+                    g[e] = ge;
+                }
+            }
+        }
+        if constexpr (KEEP) fetch(at);
+        float a = sum2(sg), b = sum2(sgd);
+        sum_over_team(a, b, s_sum[turn], f.team, id);
+        turn ^= 1;
+        const float k1 = -a * inv_n, k2 = -rstd * rstd * (b * inv_n);
+        const F2 k1k1 = f2(k1, k1), k2k2 = f2(k2, k2);
+        asm volatile("" ::: "memory");                     // what is not kept is read again
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * cu;
+            if (c >= n) continue;
+            F2 o[H];
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) o[i] = add2(g[u * H + i], fma2(d[u * H + i], k2k2, k1k1));
+            } else {
+                const Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + u * all * XB);
+                const Pack<D, W> dy = *reinterpret_cast<const Pack<D, W>*>(my_dy + at + u * all * DB);
+                F2 wu[H];
+                weights(u, wu);
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    o[i] = fma2(mul2(pair_of<W>(dy, i), r2), wu[i], fma2(add2(pair_of<W>(x, i), off), k2k2, k1k1));
+            }
+            store_run<W, EDGE>(dx, o, c, n, dx_vec, p.bnd, 5);
+        }
+        if constexpr (!KEEP) fetch(at);
+        at = at + stage == f.stages * stage ? 0 : at + stage;
+        mean = mean2;
+        rstd = rstd2;
+    }
+    if (p.dw == nullptr) return;
+    // the block's teams one after the other, in the rows' room
+    ulonglong2* sum = reinterpret_cast<ulonglong2*>(s_mem) + t;           // [E / 2] pairs of dw, then of db: + i * team
+    if (f.teams > 1) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int i = 0; i < f.teams; ++i) {
+            __syncthreads();
+            if (id == i)
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    ulonglong2* to = sum + e * f.team;
+                    if (i > 0) {
+                        const ulonglong2 v = *to;
+                        dw[e] = add2(v.x, dw[e]);
+                        db[e] = add2(v.y, db[e]);
+                    }
+                    if (i < f.teams - 1) *to = make_ulonglong2(dw[e], db[e]);
+                }
+        }
+    }
+    if (id != f.teams - 1) return;                         // the last team has the sums of all of them
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * cu;
+        if (c >= n) continue;
+        store_run<W, true>(part, dw + u * H, c, n, !EDGE, p.bnd, 6);
+        store_run<W, true>(part + p.n, db + u * H, c, n, !EDGE, p.bnd, 6);
+    }
+}
+
+// ---------------------------------------------------------------- any length
+template <typename T, typename D>
+__global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(const NormBackArgs p) {
+    __shared__ float s_sum[2 * 32];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const float n = static_cast<float>(p.n);
+    for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x) {
+        const T* x = static_cast<const T*>(p.x) + row * p.sx;
+        const D* dy = static_cast<const D*>(p.dy) + row * p.sdy;
+        T* dx = static_cast<T*>(p.dx) + row * p.sdx;
+        const float mean = load_one(p.mean + row, p.bnd, 2, 0.0f), rstd = load_one(p.rstd + row, p.bnd, 3, 0.0f);
+        float c[2] = {0.0f, 0.0f};
+        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
+            float w[1];
+            load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 4);
+            const float g = to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))) * w[0];
+            c[0] += g;
+            c[1] = fmaf(g, (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd, c[1]);
+        }
+        __syncthreads();
+        sum_over_row<2, false>(c, s_sum);
+        const float c1 = c[0] / n, c2 = c[1] / n;
+        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
+            float w[1];
+            load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 4);
+            const float g = to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))) * w[0];
+            const float h = (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd;
+            store_one(dx + i, from_f32<T>(rstd * (g - c1 - h * c2)), p.bnd, 5);
+        }
+    }
+}
+
+// Sums of dy h and dy over the rows of a part, a column per thread of a row of
+// threads; part blockIdx.y has rows [y * rows, (y + 1) * rows).
+template <typename T, typename D>
+__global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(const NormBackArgs p, int64_t rows) {
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (col >= p.n) return;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows, r1 = r0 + rows < p.m ? r0 + rows : p.m;
+    float dw = 0.0f, db = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        const float dy = to_f32(load_one(static_cast<const D*>(p.dy) + r * p.sdy + col, p.bnd, 0, from_f32<D>(0.0f)));
+        const float x = to_f32(load_one(static_cast<const T*>(p.x) + r * p.sx + col, p.bnd, 1, from_f32<T>(0.0f)));
+        dw = fmaf(dy, (x - load_one(p.mean + r, p.bnd, 2, 0.0f)) * load_one(p.rstd + r, p.bnd, 3, 0.0f), dw);
+        db += dy;
+    }
+    float* part = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.n;
+    store_one(part + col, dw, p.bnd, 6);
+    store_one(part + p.n + col, db, p.bnd, 6);
+}
+
+// dw and db: the parts' sums, 32 columns by 16 shares of the parts per block, in a
+// fixed order. At most 152 parts (10 of long rows): all of a thread's loads at once.
+__global__ void __launch_bounds__(512) norm_dw_join_kernel(const NormBackArgs p, int parts) {
+    __shared__ float s[16][33];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + tx;      // of 2 n
+    float v[10];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) v[i] = col < 2 * p.n && ty + 16 * i < parts ? load_one(p.part + (ty + 16 * i) * 2 * p.n + col, p.bnd, 6, 0.0f) : 0.0f;
+#pragma unroll
+    for (int i = 1; i < 10; ++i) v[0] += v[i];
+    s[ty][tx] = v[0];
+    __syncthreads();
+    if (ty == 0 && col < 2 * p.n) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += s[i][tx];
+        if (col < p.n) store_one(p.dw + col, sum, p.bnd, 7);
+        else store_one(p.db + col - p.n, sum, p.bnd, 8);
+    }
+}
+
+unsigned grid_of(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 1 : (n < most ? n : most)); }
+
+// Parts of the rows for the column sums of long rows: enough blocks for every SM to have four.
+int64_t any_parts(int64_t m, int64_t n) {
+    const int64_t cols = (n + kThreads - 1) / kThreads;
+    int64_t parts = (kSms * 4 + cols - 1) / cols;
+    if (parts > (m + 15) / 16) parts = (m + 15) / 16;
+    return parts < 1 ? 1 : parts;
+}
+
+cudaError_t join(const NormBackArgs& a, int64_t parts, cudaStream_t st) {
+    if (a.dw == nullptr) return cudaSuccess;
+    return launch_after(norm_dw_join_kernel, dim3(static_cast<unsigned>((2 * a.n + 31) / 32)), 512, 0, st, a, static_cast<int>(parts));
+}
+
+// Most parts of the rows: the blocks of the kernel above, a multiple of 8 where rows
+// start differently.
+int64_t most_parts(int64_t m) {
+    const int64_t least = m < 8 ? 8 : m;
+    return least < kSms ? least : kSms;
+}
+
+template <typename T, typename D, int E>
+cudaError_t back_e(const NormBackArgs& a, cudaStream_t st, int num_sms) {
+    constexpr int W = 16 / sizeof(T);
+    Teams f;
+    f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
+    const bool dy_vec = same_boundary(f.at, boundary_of(a.dy, sizeof(D), a.sdy, a.m, W)),
+               dx_vec = same_boundary(f.at, boundary_of(a.dx, sizeof(T), a.sdx, a.m, W)), w_vec = aligned_to(a.w, 16);
+    const bool edge = f.at.base != 0 || f.at.stride != 0 || a.n % W != 0 || !dy_vec || !dx_vec || !w_vec;
+    auto kern = edge ? norm_back_kernel<T, D, E, true> : norm_back_kernel<T, D, E, false>;
+    f.team = team_of(a.n, E, edge, W);
+    const int64_t blocks = blocks_of(a.m, num_sms < kSms ? num_sms : kSms, f.at);
+    f.teams = teams_of(a.m, blocks, f.team, kRowThreads);
+    const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T) + sizeof(D)), weights = E <= 16 ? 0 : threads * E * 4;
+    f.stages = (kNormRoom - weights) / stage;
+    if (f.stages > 4) f.stages = 4;
+    const int sums = f.teams > 1 ? f.team * E * 8 : 0, rows = f.stages * stage + weights, smem = sums > rows ? sums : rows;
+    if (smem > 47 * 1024)                                  // 48 KB without being asked for
+        if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kNormRoom); e != cudaSuccess) return e;
+    if (cudaError_t e = launch_after(kern, dim3(static_cast<unsigned>(blocks)), threads, static_cast<size_t>(smem), st, a, f, dy_vec, dx_vec, w_vec);
+        e != cudaSuccess)
+        return e;
+    return join(a, blocks, st);
+}
+
+// Elements per thread of a team.
+template <typename T, typename D>
+cudaError_t back_rows(const NormBackArgs& a, cudaStream_t st, int num_sms) {
+    constexpr int W = 16 / sizeof(T);
+    if (a.n <= 256 - W) return back_e<T, D, 8>(a, st, num_sms);
+    if (a.n <= 8192 - W) return back_e<T, D, 16>(a, st, num_sms);
+    return back_e<T, D, 32>(a, st, num_sms);
+}
+
+template <typename T, typename D>
+cudaError_t back_t(const NormBackArgs& a, cudaStream_t st, int num_sms) {
+    if (a.n > kNormLongest) {
+        if (cudaError_t e = launch_after(norm_dx_any_kernel<T, D>, dim3(grid_of(a.m, static_cast<int64_t>(num_sms) * 8)), kThreads, 0, st, a);
+            e != cudaSuccess || a.dw == nullptr)
+            return e;
+        const int64_t parts = any_parts(a.m, a.n), rows = (a.m + parts - 1) / parts;
+        if (cudaError_t e = launch_after(norm_dw_any_kernel<T, D>, dim3(static_cast<unsigned>((a.n + kThreads - 1) / kThreads), static_cast<unsigned>(parts)),
+                                         kThreads, 0, st, a, rows);
+            e != cudaSuccess)
+            return e;
+        return join(a, parts, st);
+    }
+    return back_rows<T, D>(a, st, num_sms);
+}
+
+}  // namespace
+
+size_t norm_back_workspace(int64_t m, int64_t n) {
+    return static_cast<size_t>(n > kNormLongest ? any_parts(m, n) : most_parts(m)) * 2 * static_cast<size_t>(n) * sizeof(float);
+}
+
+cudaError_t launch_norm_back(const NormBackArgs& a, cudaStream_t st, int num_sms) {
+    if (a.x_bf16) return a.dy_bf16 ? back_t<__nv_bfloat16, __nv_bfloat16>(a, st, num_sms) : back_t<__nv_bfloat16, float>(a, st, num_sms);
+    return a.dy_bf16 ? back_t<float, __nv_bfloat16>(a, st, num_sms) : back_t<float, float>(a, st, num_sms);
+}
+
+}  // namespace ql

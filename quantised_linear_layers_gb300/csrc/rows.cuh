@@ -72,6 +72,24 @@ __device__ __forceinline__ void store_one(T* p, T v, const B& b, int span) {
     if (QL_IN(b, span, p, sizeof(T))) *p = v;
 }
 
+// W elements of a vector of bf16 or fp32 that may be missing (then `other`), from
+// element c on; 16-byte aligned where W > 1.
+template <int W, typename B>
+__device__ __forceinline__ void load_weights(float (&w)[W], const void* p, bool bf16, int64_t c, float other, const B& b, int span) {
+    if (p == nullptr) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = other;
+    } else if (bf16) {
+        const Pack<__nv_bfloat16, W> v = load_pack<__nv_bfloat16, W>(static_cast<const __nv_bfloat16*>(p) + c, b, span);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = to_f32(v.v[i]);
+    } else {
+        const Pack<float, W> v = load_pack<float, W>(static_cast<const float*>(p) + c, b, span);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = v.v[i];
+    }
+}
+
 // v[0 .. N) summed over the threads of a row: a warp, or a whole block by way of
 // s [N * 32] in shared memory (which the caller may use again only after a barrier).
 // Every thread gets the sums; their order does not depend on timing.

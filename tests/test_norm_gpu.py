@@ -54,7 +54,8 @@ def check(ops, x, w, b, out, eps=1e-5, dy=None):
 
 
 SIZES = [(1, 1), (1, 2), (3, 7), (5, 31), (2, 32), (7, 33), (300, 64), (130, 257), (9, 1000), (33, 1003), (40, 2048), (3, 2056),
-         (17, 4099), (5, 7168), (700, 776), (2, 8192), (3, 8200), (2, 16384), (2, 16391), (1, 40000), (1300, 96)]
+         (17, 4099), (5, 7168), (700, 776), (2, 8192), (3, 8200), (2, 16384), (2, 16391), (1, 40000), (1300, 96), (2000, 1032),
+         (1501, 1027)]
 
 
 @pytest.mark.parametrize("m,n", SIZES)
@@ -94,13 +95,15 @@ def test_out_is_written_and_nothing_else(ops):
     x = acts(6, 776, BF)
     w, b = params(776, F)
     for dtype in (BF, F):
-        room = torch.full((8, 800), 7.0, dtype=dtype, device="cuda")
-        view = room[1:7, 5:781]
-        got = ops.layer_norm(x, w, b, out=view)
-        assert got.data_ptr() == view.data_ptr()
-        assert torch.equal(view, ops.layer_norm(x, w, b, dtype=dtype))
-        view.fill_(7.0)
-        assert torch.equal(room, torch.full_like(room, 7.0))
+        for first in (8, 5):                           # on a 16-byte boundary, where sums run in the order of the new tensor's, and off it
+            room = torch.full((8, 800), 7.0, dtype=dtype, device="cuda")
+            view = room[1:7, first:first + 776]
+            got = ops.layer_norm(x, w, b, out=view)
+            assert got.data_ptr() == view.data_ptr() and got.dtype == dtype
+            ref.close(view, *ref.norm(x, w, b, 1e-5, dtype)[:2], "y")
+            assert first != 8 or torch.equal(view, ops.layer_norm(x, w, b, dtype=dtype))
+            view.fill_(7.0)
+            assert torch.equal(room, torch.full_like(room, 7.0))
 
 
 @pytest.mark.parametrize("n", [8, 1003, 7168])
