@@ -382,10 +382,11 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t st, int num_sms) {
     cudaError_t e;
     if (a.n <= 256 - W) return norm_e<T, O, 8, true>(a, whole, st);
     if (a.n <= 8192 - W ? rows_e<T, O, 16>(a, whole, st, num_sms, e) : rows_e<T, O, 32>(a, whole, st, num_sms, e)) return e;
-    if (a.n <= 1024 - W) return norm_e<T, O, 32, true>(a, whole, st);
+    // a row to a warp / to a block, us: 200 x 1000 3.3 / 2.2, 2048 x 1000 5.0 / 4.7, 4000 x 1000 5.5 / 6.9, 8000 x 500 8.7 / 10.5
+    if (a.n <= 1024 - W && a.m > 10 * num_sms) return norm_e<T, O, 32, true>(a, whole, st);
     // few elements to a thread where few rows leave a block alone on its SM (1 x 7168 2.8 us, 12.6 by a
     // loop of 256 threads) and where elements go one by one; 4096 x 7168 takes 31.7 with 32 and 67 with 8
-    if (a.n <= 8192 - W && (a.m <= num_sms || !whole)) return norm_e<T, O, 8, false>(a, whole, st);
+    if (a.n <= 8192 - W && (a.m <= num_sms || a.n <= 1024 - W || !whole)) return norm_e<T, O, 8, false>(a, whole, st);
     return norm_e<T, O, 32, false>(a, whole, st);
 }
 

@@ -66,140 +66,209 @@ __device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int exper
     }
 }
 
-// The k best of a token in 64 bits: lane j gets the j-th one's index, or -1.
-// c: 512 doubles of shared memory, the warp's own.
-template <int NV>
-__device__ __noinline__ int choose_exact(const RouteArgs& p, const float (&l)[NV], const float (&b)[NV], float top, int magic,
-                                         double* c) {
-    const int lane = threadIdx.x & 31;
-    const double lowest = -1e300;
-    double total = 1.0;
-    double v[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) : exp(static_cast<double>(l[i]) - static_cast<double>(top));
+// ---------------------------------------------------------------- in 64 bits
+// What a token's scores in 64 bits need: the softmax's largest logit and sum.
+struct Score64 {
+    double top, total;
+    bool sigmoid;
+    __device__ double operator()(float l) const {
+        return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp(static_cast<double>(l) - top) / total;
+    }
+};
+template <typename T>
+__device__ __noinline__ Score64 score64(const RouteArgs& p, const T* row, float top) {
+    Score64 r{static_cast<double>(top), 1.0, p.sigmoid};
     if (!p.sigmoid) {
-        total = 0.0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) total += v[i];
-        total = warp_sum(total);
+        double sum = 0.0;
+        for (int e = threadIdx.x & 31; e < p.experts; e += 32) sum += exp(static_cast<double>(to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f)))) - r.top);
+        r.total = warp_sum(sum);
     }
+    return r;
+}
+// The choice c of expert e: -inf out of reach.
+template <typename T>
+__device__ __forceinline__ double choice64(const RouteArgs& p, const T* row, const Score64& s, int e) {
+    const float l = to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))), b = p.bias != nullptr ? load_one(p.bias + e, p.bnd, 1, 0.0f) : 0.0f;
+    return l == -INFINITY || b == -INFINITY ? -INFINITY : s(l) + static_cast<double>(b);
+}
+// The largest of a warp's values and the lowest place that has it.
+__device__ __forceinline__ void best_of_warp(double& v, int& at) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool reached = l[i] != -INFINITY && b[i] != -INFINITY;
-        double x = v[i] / total + static_cast<double>(b[i]);
-        if (x != x) x = lowest;
-        c[lane * NV + i] = reached ? x : -INFINITY;
-        v[i] = !reached ? -INFINITY : (p.bias != nullptr ? x : static_cast<double>(l[i]));
-    }
-    __syncwarp();
-    if (p.kept < p.groups) {
-        const int size = p.experts / p.groups;
-        double score = -INFINITY;
-        if (lane < p.groups) {
-            double best = -INFINITY, next = -INFINITY;
-            for (int i = 0; i < size; ++i) {
-                const double x = c[lane * size + i];
-                if (x > best) {
-                    next = best;
-                    best = x;
-                } else if (x > next) {
-                    next = x;
-                }
-            }
-            score = p.group_best > 1 && next != -INFINITY ? best + next : best;
+    for (int o = 16; o > 0; o >>= 1) {
+        const double v2 = __shfl_xor_sync(kAll, v, o);
+        const int at2 = __shfl_xor_sync(kAll, at, o);
+        if (v2 > v || (v2 == v && at2 < at)) {
+            v = v2;
+            at = at2;
         }
-        uint32_t kept = 0;
-        for (int r = 0; r < p.kept; ++r) {
-            double s = (kept >> lane) & 1u ? -INFINITY : score;
-            int at = lane;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const double s2 = __shfl_xor_sync(kAll, s, o);
-                const int at2 = __shfl_xor_sync(kAll, at, o);
-                if (s2 > s || (s2 == s && at2 < at)) {
-                    s = s2;
-                    at = at2;
-                }
-            }
-            if (s == -INFINITY) break;
-            kept |= 1u << at;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (((kept >> (over(lane * NV + i, magic) & 31)) & 1u) == 0u) v[i] = -INFINITY;
     }
-    int mine = -1;
-    for (int r = 0; r < p.k; ++r) {
-        double s = -INFINITY;
-        int at = 1 << 20;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (v[i] > s) {
-                s = v[i];
-                at = lane * NV + i;
-            }
+}
+
+// The best `need` of the groups in `which`, as a mask.
+template <typename T>
+__device__ __noinline__ uint32_t groups_exact(const RouteArgs& p, const T* row, float top, uint32_t which, int need) {
+    const Score64 s = score64(p, row, top);
+    const int lane = threadIdx.x & 31, size = p.experts / p.groups;
+    double mine = -INFINITY;                               // lane g: group g's score
+    for (uint32_t left = which; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        double best = -INFINITY, next = -INFINITY;
+        for (int i = lane; i < size; i += 32) {
+            const double c = choice64(p, row, s, g * size + i);
+            next = fmax(next, fmin(best, c));
+            best = fmax(best, c);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const double s2 = __shfl_xor_sync(kAll, s, o);
-            const int at2 = __shfl_xor_sync(kAll, at, o);
-            if (s2 > s || (s2 == s && at2 < at)) {
-                s = s2;
-                at = at2;
-            }
+            const double b2 = __shfl_xor_sync(kAll, best, o), n2 = __shfl_xor_sync(kAll, next, o);
+            next = fmax(fmin(best, b2), fmax(next, n2));
+            best = fmax(best, b2);
         }
-        if (s == -INFINITY) break;
+        if (lane == g) mine = p.group_best > 1 && next != -INFINITY ? best + next : best;
+    }
+    uint32_t kept = 0;
+    for (; need > 0; --need) {
+        double v = mine;
+        int at = lane;
+        best_of_warp(v, at);
+        if (v == -INFINITY) break;
+        kept |= 1u << at;
+        if (lane == at) mine = -INFINITY;
+    }
+    return kept;
+}
+
+// The k best of the experts whose bit is set in the lanes' `which` (bit i of a lane: expert
+// lane * nv + i): lane j gets the j-th one's index, or -1. list: 64 ints of shared memory.
+template <typename T>
+__device__ __noinline__ int choose_exact(const RouteArgs& p, const T* row, float top, uint32_t which, int nv, int* list) {
+    const Score64 s = score64(p, row, top);
+    const int lane = threadIdx.x & 31;
+    int mine = -1;
+    int all = __popc(which), before = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, before, o);
+        if (lane >= o) before += v;
+    }
+    const int count = __shfl_sync(kAll, before, 31);
+    if (count <= 32) {                                     // a lane each, ranked against one another
+        for (before -= all; which != 0; which &= which - 1) list[before++] = lane * nv + __ffs(which) - 1;
+        list[32 + lane] = -1;
+        __syncwarp();
+        const int e = lane < count ? list[lane] : -1;
+        const double c = e >= 0 ? choice64(p, row, s, e) : -INFINITY;
+        int rank = 0;
+        for (int i = 0; i < count; ++i) {
+            const double c2 = __shfl_sync(kAll, c, i);
+            const int e2 = __shfl_sync(kAll, e, i);
+            rank += c2 > c || (c2 == c && e2 < e);
+        }
+        if (e >= 0 && c != -INFINITY && rank < p.k) list[32 + rank] = e;
+        __syncwarp();
+        return lane < p.k ? list[32 + lane] : -1;
+    }
+    double c[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[i] = (which >> i) & 1u ? choice64(p, row, s, lane * nv + i) : -INFINITY;
+    for (int r = 0; r < p.k; ++r) {
+        double v = -INFINITY;
+        int at = 1 << 20;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c[i] > v) {
+                v = c[i];
+                at = lane * nv + i;
+            }
+        best_of_warp(v, at);
+        if (v == -INFINITY) break;
         if (lane == r) mine = at;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (at == lane * NV + i) v[i] = -INFINITY;
+        for (int i = 0; i < 16; ++i)
+            if (at == lane * nv + i) c[i] = -INFINITY;
     }
     return mine;
 }
 
+// ---------------------------------------------------------------- the choice
+// Sorts a lane's keys, largest first (Batcher's odd-even merges).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+            for (int j = d % p; j + d < N; j += 2 * d)
+#pragma unroll
+                for (int i = 0; i < d; ++i)
+                    if (i + j + d < N && (i + j) / (2 * p) == (i + j + d) / (2 * p)) {
+                        const uint32_t a = k[i + j], b = k[i + j + d];
+                        k[i + j] = max(a, b);
+                        k[i + j + d] = min(a, b);
+                    }
+}
+
+// The least key that is not surely below one by more than `wide`.
+__device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
+    const float v = value_of(key) - wide;
+    return v == v ? key_of(v) : kNanKey + 1;
+}
+
+// A token's k best take k rounds: the lanes' keys are sorted once, a round takes the
+// largest of the lanes' next ones, the lowest lane first, and that lane goes on to its
+// next. Which expert it was follows from the key and its place among the lane's, all
+// rounds at once.
 template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
-    __shared__ double s_row[kWarps][NV * 32];
+    __shared__ __align__(16) uint32_t s_keys[kWarps][2][NV * 32];      // as they are; sorted, by lane
+    __shared__ int s_list[kWarps][64];
     pdl_launch_dependents();
     pdl_wait_prior();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= p.m) return;
     const T* row = static_cast<const T*>(p.logits) + t * p.sl;
-    float l[NV], b[NV];
-    load_row<T, NV, VEC>(l, row, p.experts, p.bnd, 0);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane * NV + i;
-        b[i] = p.bias != nullptr && e < p.experts ? load_one(p.bias + e, p.bnd, 1, 0.0f) : 0.0f;
-    }
     const bool grouped = p.kept < p.groups, sums = grouped && p.group_best > 1;
     const bool biased = p.bias != nullptr, scored = biased || sums;
+    const bool whole = !p.sigmoid && (scored || !p.renormalise);       // the softmax over all experts is needed
     const int size = p.experts / p.groups;
     const int magic = ((1 << 20) + size - 1) / size;
+    const int e0 = lane * NV;
+    auto in = [&](int i) { return VEC ? e0 < p.experts : e0 + i < p.experts; };
 
-    bool nan = false;
-    float top = -INFINITY;
+    float l[NV], b[NV];
+    load_row<T, NV, VEC>(l, row, p.experts, p.bnd, 0);
+    float odd = 0.0f, b_most = 0.0f;                       // odd: NaN if anything is not finite
+    if (biased) {
+        if (VEC && aligned_to(p.bias, 16)) load_row<float, NV, true>(b, p.bias, p.experts, p.bnd, 1);
+        else load_row<float, NV, false>(b, p.bias, p.experts, p.bnd, 1);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        nan |= l[i] != l[i] || b[i] != b[i];
-        top = fmaxf(top, l[i]);
+        if (!biased) b[i] = 0.0f;
+        if (!in(i)) l[i] = b[i] = 0.0f;                    // its key is 0 below
+        odd = fmaf(l[i], 0.0f, odd);
+        odd = fmaf(b[i], 0.0f, odd);
+        b_most = fmaxf(b_most, fabsf(b[i]));
     }
-    nan = __any_sync(kAll, nan);
-    // row sums of the softmax are only needed where a score is
-    const bool whole = !p.sigmoid && (scored || !p.renormalise);
-    float total = 1.0f;
-    if (whole) top = warp_max(top);
-    const float base = top == -INFINITY ? 0.0f : top;
+    const bool special = __any_sync(kAll, odd != 0.0f);
 
-    uint32_t key[NV];
+    float top = 0.0f, total = 1.0f;
+    if (whole) {
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) top = fmaxf(top, in(i) ? l[i] : -INFINITY);
+        top = warp_max(top);
+        if (top == -INFINITY) top = 0.0f;
+    }
     float s[NV];
-    float bound = 0.0f;                                    // of a choice's error
     if (whole || scored) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            s[i] = p.sigmoid ? 1.0f / (1.0f + expf(-l[i])) : expf(l[i] - base);
-            sum += s[i];
+            s[i] = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top);
+            sum += in(i) ? s[i] : 0.0f;
         }
         if (!p.sigmoid) {
             total = warp_sum(sum);
@@ -208,117 +277,161 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
             for (int i = 0; i < NV; ++i) s[i] *= inv;
         }
     }
+    uint32_t key[NV];
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const bool reached = l[i] != -INFINITY && b[i] != -INFINITY;
         const float c = biased ? s[i] + b[i] : l[i];
-        key[i] = !reached ? kUnreached : (c != c ? kNanKey : key_of(c));
+        key[i] = in(i) ? key_of(c) : kUnreached;
+        if (special && in(i)) {
+            nan |= l[i] != l[i] || b[i] != b[i] || (!p.sigmoid && l[i] == INFINITY);
+            if (c != c) key[i] = kNanKey;
+            if (l[i] == -INFINITY || b[i] == -INFINITY) key[i] = kUnreached;
+        }
     }
+    if (special) nan = __any_sync(kAll, nan);
+    // How far a choice in fp32 may be off. A sigmoid's exp is within (2 + 1.2 |l|) 2^-23 of
+    // itself, by which s moves 2^-23.6 at most; the sum and the quotient add 2^-24 and
+    // 2^-22 of s: 2^-21.3. A softmax's term at x below the largest is off by
+    // (2 + 1.7 x) 2^-23 exp(-x), 2 * 2^-23 at most, its sum of up to 512 by 21 roundings and
+    // 8 * 2^-23 of itself, so s by 2^-18.5 of the largest. c's own rounding is 2^-24 of
+    // s + |b|.
+    float bound = 0.0f;
     if (scored) {
-        // relative to the largest score: expf 2^-22, 1 + e and the division 2^-24 each, a
-        // softmax's sum at most 21 roundings; one rounding of c, of s + |b| at most
-        const float unit = p.sigmoid ? 0x1p-20f : 0x1p-18f;
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (key[i] > kNanKey) most = fmaxf(most, fmaf(s[i], unit, fabsf(b[i]) * 0x1p-23f));
-        bound = warp_max(most);
+        b_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_most)));
+        bound = (p.sigmoid ? 0x1p-21f : __fdividef(0x1p-18f, total)) + b_most * 0x1p-23f;
     }
 
-    bool unsure = false;
     if (grouped) {
-        // scores of the groups: lane g has that of group g
-        uint32_t group = kUnreached;
-        float* c = reinterpret_cast<float*>(s_row[warp]);
-        uint32_t* ck = reinterpret_cast<uint32_t*>(c);
+        uint32_t best = 0, next = 0;
+        const int lanes = size / NV;
+        if (lanes * NV == size && (lanes & (lanes - 1)) == 0) {        // a group is a power of two of lanes
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            uint32_t v = key[i];
-            if (sums && !biased) v = v <= kNanKey ? v : key_of(s[i]);
-            ck[lane * NV + i] = v;
-        }
-        __syncwarp();
-        if (lane < p.groups) {
-            uint32_t best = 0, next = 0;
-            const uint32_t* of = ck + lane * size;
-            for (int i = 0, at = lane; i < size; ++i, ++at) {
-                while (at >= size) at -= size;             // lanes start at different banks
-                const uint32_t v = of[at];
+            for (int i = 0; i < NV; ++i) {
+                const uint32_t v = sums && !biased && key[i] > kNanKey ? key_of(s[i]) : key[i];
                 next = max(next, min(best, v));
                 best = max(best, v);
             }
-            group = best;
-            if (p.group_best > 1 && next > kNanKey) group = key_of(value_of(best) + value_of(next));
-        }
-        uint32_t kept = 0, last = 0;
-        for (int r = 0; r <= p.kept; ++r) {
-            const uint32_t v = (kept >> lane) & 1u ? 0u : group;
-            const uint32_t best = __reduce_max_sync(kAll, v);
-            if (r == p.kept) {                             // the best that stays out
-                if (scored && best > kNanKey) unsure = value_of(last) - value_of(best) <= 6.0f * bound;      // two sums of two
-                break;
+            for (int o = 1; o < lanes; o <<= 1) {
+                const uint32_t b2 = __shfl_xor_sync(kAll, best, o), n2 = __shfl_xor_sync(kAll, next, o);
+                next = max(min(best, b2), max(next, n2));
+                best = max(best, b2);
             }
-            if (best == 0) break;
-            kept |= 1u << (__ffs(__ballot_sync(kAll, v == best)) - 1);
-            last = best;
+            best = __shfl_sync(kAll, best, (lane * lanes) & 31);
+            next = __shfl_sync(kAll, next, (lane * lanes) & 31);
+        } else {
+            // through shared memory, `per` lanes to a group
+            uint32_t* keys = s_keys[warp][0];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) keys[e0 + i] = sums && !biased && key[i] > kNanKey ? key_of(s[i]) : key[i];
+            __syncwarp();
+            int per = 1;
+            while (2 * per * p.groups <= 32) per *= 2;
+            const int g = lane / per;
+            if (g < p.groups)
+                for (int i = lane & (per - 1); i < size; i += per) {
+                    const uint32_t v = keys[g * size + i];
+                    next = max(next, min(best, v));
+                    best = max(best, v);
+                }
+            for (int o = 1; o < per; o <<= 1) {
+                const uint32_t b2 = __shfl_xor_sync(kAll, best, o), n2 = __shfl_xor_sync(kAll, next, o);
+                next = max(min(best, b2), max(next, n2));
+                best = max(best, b2);
+            }
+            best = __shfl_sync(kAll, best, (lane * per) & 31);
+            next = __shfl_sync(kAll, next, (lane * per) & 31);
+            __syncwarp();
+        }
+        // lane g has group g's
+        uint32_t group = lane < p.groups ? best : kUnreached;
+        if (sums && lane < p.groups && next > kNanKey) group = key_of(value_of(best) + value_of(next));
+        uint32_t kept = 0, last = 0;
+        for (int r = 0; r < p.kept; ++r) {
+            const uint32_t v = (kept >> lane) & 1u ? kUnreached : group;
+            const uint32_t most = __reduce_max_sync(kAll, v);
+            if (most == kUnreached) break;
+            kept |= 1u << (__ffs(__ballot_sync(kAll, v == most)) - 1);
+            last = most;
+        }
+        if (scored && !nan) {
+            // sums of two choices are within two bounds and their own rounding; the best that stays out
+            const uint32_t out = __reduce_max_sync(kAll, (kept >> lane) & 1u ? kUnreached : group);
+            const float wide = 6.0f * bound;
+            if (out > kNanKey && !(value_of(last) - value_of(out) > wide)) {
+                const bool in = group > kNanKey && value_of(group) - value_of(out) > wide;
+                const bool open = group > kNanKey && !in && !(value_of(last) - value_of(group) > wide);
+                const uint32_t sure = __ballot_sync(kAll, in), which = __ballot_sync(kAll, open);
+                kept = sure | groups_exact(p, row, top, which, p.kept - __popc(sure));
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (((kept >> (over(lane * NV + i, magic) & 31)) & 1u) == 0u) key[i] = kUnreached;
+            if (((kept >> (over(e0 + i, magic) & 31)) & 1u) == 0u) key[i] = kUnreached;
     }
 
-    int mine = -1;                                         // lane j: the j-th choice
-    uint32_t my_key = 0;
+    uint32_t* keys = s_keys[warp][0];
+    uint32_t* sorted = s_keys[warp][1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) keys[e0 + i] = key[i];
+    sort_keys<NV>(key);
+#pragma unroll
+    for (int i = 1; i < NV; ++i) sorted[i * 32 + lane] = key[i];
+    __syncwarp();
+    uint32_t head = key[0], my_key = kUnreached, last = kUnreached;
+    int place = 0, my_place = 0, my_lane = 0;
     for (int r = 0; r < p.k; ++r) {
-        uint32_t best = key[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-        const uint32_t most = __reduce_max_sync(kAll, best);
-        if (most == 0) break;
-        const int from = __ffs(__ballot_sync(kAll, best == most)) - 1;
-        int at = 0;
-        if (lane == from) {
-            bool found = false;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (!found && key[i] == most) {
-                    found = true;
-                    key[i] = 0;
-                    at = lane * NV + i;
-                }
-        }
-        at = __shfl_sync(kAll, at, from);
+        last = __reduce_max_sync(kAll, head);
+        if (last == kUnreached) break;
+        const int from = __ffs(__ballot_sync(kAll, head == last)) - 1;
+        const int at = __shfl_sync(kAll, place, from);
         if (lane == r) {
-            mine = at;
-            my_key = most;
+            my_key = last;
+            my_lane = from;
+            my_place = at;
+        }
+        if (lane == from) {
+            ++place;
+            head = place < NV ? sorted[place * 32 + lane] : kUnreached;
         }
     }
+    int mine = -1;                                         // lane j: the j-th choice
+    if (my_key != kUnreached) {
+        // the (place - greater ones)-th of the lane's experts with that key
+        int skip = my_place;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) skip -= keys[my_lane * NV + i] > my_key;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (keys[my_lane * NV + i] == my_key && skip-- == 0) mine = my_lane * NV + i;
+    }
     float lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
-    if (biased) {
+    if (biased && !nan) {
         // gaps between choices next to one another, and from the last to what stays out;
         // the same logit and bias are a tie in any precision
+        const float wide = 3.0f * bound;
         const float b1 = mine >= 0 ? load_one(p.bias + mine, p.bnd, 1, 0.0f) : 0.0f;
         const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
         const float lg2 = __shfl_down_sync(kAll, lg, 1), b2 = __shfl_down_sync(kAll, b1, 1);
-        if (lane < p.k - 1 && key2 > kNanKey && value_of(my_key) - value_of(key2) <= 3.0f * bound && (lg != lg2 || b1 != b2))
-            unsure = true;
-        const uint32_t last = __shfl_sync(kAll, my_key, p.k - 1);
-        const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
+        bool unsure = lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide) && (lg != lg2 || b1 != b2);
         if (last > kNanKey) {
+            const uint32_t least = near_key(last, wide);
+            const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
+            bool near = false;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (key[i] > kNanKey && value_of(last) - value_of(key[i]) <= 3.0f * bound && (l[i] != llast || b[i] != blast))
-                    unsure = true;
+            for (int i = 0; i < NV; ++i) near |= keys[e0 + i] >= least && (l[i] != llast || b[i] != blast);
+            // the k chosen are near too: only a lane's next one can be another
+            if (head >= least && near) unsure = true;
         }
-    }
-    if (__any_sync(kAll, unsure) && !nan) {
-        __syncwarp();
-        if (!biased) {
+        if (__any_sync(kAll, unsure)) {
+            const uint32_t least = last > kNanKey ? near_key(last, wide) : kNanKey + 1;
+            uint32_t which = 0;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) b[i] = 0.0f;
+            for (int i = 0; i < NV; ++i) which |= (keys[e0 + i] >= least ? 1u : 0u) << i;
+            __syncwarp();
+            mine = choose_exact(p, row, top, which, NV, s_list[warp]);
+            lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
         }
-        mine = choose_exact<NV>(p, l, b, whole ? base : 0.0f, magic, s_row[warp]);
-        lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
     }
 
     float w;
@@ -337,7 +450,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
     } else if (mine < 0) {
         w = 0.0f;
     } else {
-        w = (p.sigmoid ? 1.0f / (1.0f + expf(-lg)) : expf(lg - base) / total) * p.scale;
+        w = (p.sigmoid ? 1.0f / (1.0f + expf(-lg)) : expf(lg - top) / total) * p.scale;
     }
     if (nan && mine >= 0) w = __int_as_float(0x7fffffff);
     if (lane < p.k) {

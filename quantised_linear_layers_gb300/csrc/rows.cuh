@@ -131,7 +131,7 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, size_t 
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-inline bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+__host__ __device__ inline bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
 // Rows of es-byte elements, row stride in elements, that start on multiples of `bytes`.
 inline bool rows_aligned(const void* p, int64_t es, int64_t stride, int64_t rows, int64_t bytes) {
     return aligned_to(p, bytes) && (rows <= 1 || (stride * es) % bytes == 0);
