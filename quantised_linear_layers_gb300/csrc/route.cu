@@ -46,9 +46,9 @@ __device__ __forceinline__ double warp_sum(double v) {
 // e / size for e < 512: magic = ceil(2^20 / size); e size < 2^20.
 __device__ __forceinline__ int over(int e, int magic) { return (e * magic) >> 20; }
 
-// A token's logits, NV to a lane; -inf past the last.
+// A row's elements, NV to a lane; `other` past the last.
 template <typename T, int NV, bool VEC>
-__device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int experts, const Bounds& bnd, int span) {
+__device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int experts, float other, const Bounds& bnd, int span) {
     const int e0 = (threadIdx.x & 31) * NV;
     if constexpr (VEC) {                                   // NV elements or none
         if (e0 < experts) {
@@ -57,12 +57,12 @@ __device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int exper
             for (int i = 0; i < NV; ++i) l[i] = to_f32(v.v[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
+            for (int i = 0; i < NV; ++i) l[i] = other;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            l[i] = e0 + i < experts ? to_f32(load_one(row + e0 + i, bnd, span, from_f32<T>(0.0f))) : -INFINITY;
+            l[i] = e0 + i < experts ? to_f32(load_one(row + e0 + i, bnd, span, from_f32<T>(0.0f))) : other;
     }
 }
 
@@ -139,9 +139,10 @@ __device__ __noinline__ uint32_t groups_exact(const RouteArgs& p, const T* row, 
 }
 
 // The k best of the experts whose bit is set in the lanes' `which` (bit i of a lane: expert
-// lane * nv + i): lane j gets the j-th one's index, or -1. list: 64 ints of shared memory.
+// lane * nv + i): lane j gets the j-th one's index, or -1. list: 64 ints of shared memory,
+// c: nv * 32 doubles.
 template <typename T>
-__device__ __noinline__ int choose_exact(const RouteArgs& p, const T* row, float top, uint32_t which, int nv, int* list) {
+__device__ __noinline__ int choose_exact(const RouteArgs& p, const T* row, float top, uint32_t which, int nv, int* list, double* c_at) {
     const Score64 s = score64(p, row, top);
     const int lane = threadIdx.x & 31;
     int mine = -1;
@@ -168,24 +169,19 @@ __device__ __noinline__ int choose_exact(const RouteArgs& p, const T* row, float
         __syncwarp();
         return lane < p.k ? list[32 + lane] : -1;
     }
-    double c[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) c[i] = (which >> i) & 1u ? choice64(p, row, s, lane * nv + i) : -INFINITY;
+    for (int i = 0; i < nv; ++i) c_at[i * 32 + lane] = (which >> i) & 1u ? choice64(p, row, s, lane * nv + i) : -INFINITY;
     for (int r = 0; r < p.k; ++r) {
         double v = -INFINITY;
         int at = 1 << 20;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c[i] > v) {
-                v = c[i];
+        for (int i = 0; i < nv; ++i)
+            if (c_at[i * 32 + lane] > v) {
+                v = c_at[i * 32 + lane];
                 at = lane * nv + i;
             }
         best_of_warp(v, at);
         if (v == -INFINITY) break;
         if (lane == r) mine = at;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (at == lane * nv + i) c[i] = -INFINITY;
+        if (at / nv == lane) c_at[at % nv * 32 + lane] = -INFINITY;
     }
     return mine;
 }
@@ -209,6 +205,66 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[N]) {
                     }
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// NV keys of a lane to or from its run of a warp's keys.
+template <int NV>
+__device__ __forceinline__ void store_keys(uint32_t* to, const uint32_t (&k)[NV]) {
+    if constexpr (NV % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) *reinterpret_cast<uint4*>(to + i) = make_uint4(k[i], k[i + 1], k[i + 2], k[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) to[i] = k[i];
+    }
+}
+template <int NV>
+__device__ __forceinline__ void load_keys(uint32_t (&k)[NV], const uint32_t* from) {
+    if constexpr (NV % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + i);
+            k[i] = v.x;
+            k[i + 1] = v.y;
+            k[i + 2] = v.z;
+            k[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) k[i] = from[i];
+    }
+}
+
+// Terms of the chosen's shares, and their sum: s itself, or where they would underflow s
+// over the largest of them. Lanes with `on` have a chosen expert's logit.
+__device__ __forceinline__ float share_terms(bool sigmoid, bool on, float l, float& e) {
+    float most = 0.0f;
+    if (!sigmoid || !__any_sync(kAll, on && !(l < -64.0f))) {
+        most = warp_max(on ? l : -INFINITY);
+        if (most == -INFINITY) most = 0.0f;
+    }
+    e = 0.0f;
+    if (on) {
+        if (!sigmoid) {
+            e = expf(l - most);
+        } else if (most < 0.0f) {
+            e = expf(l - most);                            // s = e^l to all of fp32's digits
+        } else {
+            const float a = expf(-fabsf(l));
+            e = (l < 0.0f ? a : 1.0f) / (1.0f + a);
+        }
+    }
+    return warp_sum(e);
+}
+
 // The least key that is not surely below one by more than `wide`.
 __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
     const float v = value_of(key) - wide;
@@ -219,10 +275,12 @@ __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
 // largest of the lanes' next ones, the lowest lane first, and that lane goes on to its
 // next. Which expert it was follows from the key and its place among the lane's, all
 // rounds at once.
-template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
-    __shared__ __align__(16) uint32_t s_keys[kWarps][2][NV * 32];      // as they are; sorted, by lane
+template <typename T, int NV, bool VEC, bool SIGMOID>
+__global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const RouteArgs p) {
+    // a warp's keys as they are, and sorted, lane by lane, with a last 0
+    __shared__ __align__(16) uint32_t s_keys[kWarps][NV * 32], s_sorted[kWarps][NV * 32 + 32];
     __shared__ int s_list[kWarps][64];
+    __shared__ double s_wide[kWarps][NV * 32];
     pdl_launch_dependents();
     pdl_wait_prior();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -231,75 +289,95 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
     const T* row = static_cast<const T*>(p.logits) + t * p.sl;
     const bool grouped = p.kept < p.groups, sums = grouped && p.group_best > 1;
     const bool biased = p.bias != nullptr, scored = biased || sums;
-    const bool whole = !p.sigmoid && (scored || !p.renormalise);       // the softmax over all experts is needed
+    const bool whole = !SIGMOID && (scored || !p.renormalise);         // the softmax over all experts is needed
     const int size = p.experts / p.groups;
     const int magic = ((1 << 20) + size - 1) / size;
     const int e0 = lane * NV;
     auto in = [&](int i) { return VEC ? e0 < p.experts : e0 + i < p.experts; };
 
     float l[NV], b[NV];
-    load_row<T, NV, VEC>(l, row, p.experts, p.bnd, 0);
+    load_row<T, NV, VEC>(l, row, p.experts, 0.0f, p.bnd, 0);
     float odd = 0.0f, b_most = 0.0f;                       // odd: NaN if anything is not finite
-    if (biased) {
-        if (VEC && aligned_to(p.bias, 16)) load_row<float, NV, true>(b, p.bias, p.experts, p.bnd, 1);
-        else load_row<float, NV, false>(b, p.bias, p.experts, p.bnd, 1);
-    }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (!biased) b[i] = 0.0f;
-        if (!in(i)) l[i] = b[i] = 0.0f;                    // its key is 0 below
-        odd = fmaf(l[i], 0.0f, odd);
-        odd = fmaf(b[i], 0.0f, odd);
-        b_most = fmaxf(b_most, fabsf(b[i]));
+    for (int i = 0; i < NV; ++i) odd = fmaf(l[i], 0.0f, odd);
+    if (biased) {
+        if (VEC && aligned_to(p.bias, 16)) load_row<float, NV, true>(b, p.bias, p.experts, 0.0f, p.bnd, 1);
+        else load_row<float, NV, false>(b, p.bias, p.experts, 0.0f, p.bnd, 1);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            odd = fmaf(b[i], 0.0f, odd);
+            b_most = fmaxf(b_most, fabsf(b[i]));
+        }
     }
     const bool special = __any_sync(kAll, odd != 0.0f);
 
-    float top = 0.0f, total = 1.0f;
-    if (whole) {
+    float top = 0.0f, total = 1.0f, s[NV];
+    if (SIGMOID) {
+        if (scored) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) s[i] = rcp_fast(1.0f + exp2_fast(l[i] * -1.442695041f));      // e^x as 2^(x log2 e)
+        }
+    } else if (whole) {
         top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) top = fmaxf(top, in(i) ? l[i] : -INFINITY);
         top = warp_max(top);
         if (top == -INFINITY) top = 0.0f;
-    }
-    float s[NV];
-    if (whole || scored) {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            s[i] = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top);
+            s[i] = exp2_fast((l[i] - top) * 1.442695041f);
             sum += in(i) ? s[i] : 0.0f;
         }
-        if (!p.sigmoid) {
-            total = warp_sum(sum);
-            const float inv = 1.0f / total;
+        total = warp_sum(sum);
+        const float inv = 1.0f / total;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s[i] *= inv;
-        }
+        for (int i = 0; i < NV; ++i) s[i] *= inv;
     }
     uint32_t key[NV];
-    bool nan = false;
+    if (biased) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const float c = biased ? s[i] + b[i] : l[i];
-        key[i] = in(i) ? key_of(c) : kUnreached;
-        if (special && in(i)) {
-            nan |= l[i] != l[i] || b[i] != b[i] || (!p.sigmoid && l[i] == INFINITY);
-            if (c != c) key[i] = kNanKey;
-            if (l[i] == -INFINITY || b[i] == -INFINITY) key[i] = kUnreached;
-        }
+        for (int i = 0; i < NV; ++i) key[i] = key_of(s[i] + b[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = key_of(l[i]);
     }
-    if (special) nan = __any_sync(kAll, nan);
-    // How far a choice in fp32 may be off. A sigmoid's exp is within (2 + 1.2 |l|) 2^-23 of
-    // itself, by which s moves 2^-23.6 at most; the sum and the quotient add 2^-24 and
-    // 2^-22 of s: 2^-21.3. A softmax's term at x below the largest is off by
-    // (2 + 1.7 x) 2^-23 exp(-x), 2 * 2^-23 at most, its sum of up to 512 by 21 roundings and
-    // 8 * 2^-23 of itself, so s by 2^-18.5 of the largest. c's own rounding is 2^-24 of
-    // s + |b|.
+    bool nan = false;
+    if (special) {
+#pragma unroll 1
+        for (int i = 0; i < NV; ++i) {
+            float li = l[0], bi = biased ? b[0] : 0.0f;
+            uint32_t k = key[0];
+#pragma unroll
+            for (int j = 1; j < NV; ++j)
+                if (j == i) {
+                    li = l[j];
+                    bi = biased ? b[j] : 0.0f;
+                    k = key[j];
+                }
+            if (e0 + i < p.experts) nan |= li != li || bi != bi || (!SIGMOID && li == INFINITY);
+            if (k > key_of(INFINITY) || k < key_of(-INFINITY)) k = kNanKey;            // a NaN of either sign
+            if (li == -INFINITY || bi == -INFINITY) k = kUnreached;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j == i) key[j] = k;
+        }
+        nan = __any_sync(kAll, nan);
+    }
+    if (p.experts < NV * 32) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = in(i) ? key[i] : kUnreached;
+    }
+    // How far a choice in fp32 may be off. 2^(x log2 e) is within 2^-22.5 + 1.5 |x| 2^-24 of
+    // e^x (the approximation; the product and the constant in it): by that a sigmoid moves
+    // by 2^-24 at most, the sum and the reciprocal add 2^-24 and 2^-23 of it, 2^-22 in all. A
+    // softmax's term at x below the largest is off by (1.5 + 1.5 x / 2) 2^-22 exp(-x), 2^-21.4
+    // at most, its sum of up to 512 by 21 roundings and 2^-19.7 of itself, so s by 2^-18.5 of
+    // the largest. c's own rounding is 2^-24 of s + |b|.
     float bound = 0.0f;
     if (scored) {
         b_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_most)));
-        bound = (p.sigmoid ? 0x1p-21f : __fdividef(0x1p-18f, total)) + b_most * 0x1p-23f;
+        bound = (SIGMOID ? 0x1p-21f : 0x1p-18f / total) + b_most * 0x1p-23f;
     }
 
     if (grouped) {
@@ -321,7 +399,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
             next = __shfl_sync(kAll, next, (lane * lanes) & 31);
         } else {
             // through shared memory, `per` lanes to a group
-            uint32_t* keys = s_keys[warp][0];
+            uint32_t* keys = s_keys[warp];
 #pragma unroll
             for (int i = 0; i < NV; ++i) keys[e0 + i] = sums && !biased && key[i] > kNanKey ? key_of(s[i]) : key[i];
             __syncwarp();
@@ -365,21 +443,28 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
                 kept = sure | groups_exact(p, row, top, which, p.kept - __popc(sure));
             }
         }
+        if (lanes * NV == size) {                          // a lane's experts are of one group
+            if (((kept >> (over(e0, magic) & 31)) & 1u) == 0u) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (((kept >> (over(e0 + i, magic) & 31)) & 1u) == 0u) key[i] = kUnreached;
+                for (int i = 0; i < NV; ++i) key[i] = kUnreached;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (((kept >> (over(e0 + i, magic) & 31)) & 1u) == 0u) key[i] = kUnreached;
+        }
     }
 
-    uint32_t* keys = s_keys[warp][0];
-    uint32_t* sorted = s_keys[warp][1];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) keys[e0 + i] = key[i];
+    uint32_t* keys = s_keys[warp];
+    uint32_t* sorted = s_sorted[warp];
+    store_keys<NV>(keys + e0, key);
     sort_keys<NV>(key);
 #pragma unroll
     for (int i = 1; i < NV; ++i) sorted[i * 32 + lane] = key[i];
+    sorted[NV * 32 + lane] = kUnreached;
     __syncwarp();
     uint32_t head = key[0], my_key = kUnreached, last = kUnreached;
-    int place = 0, my_place = 0, my_lane = 0;
+    int place = lane, my_place = 0;                        // of the lane's next key in `sorted`
     for (int r = 0; r < p.k; ++r) {
         last = __reduce_max_sync(kAll, head);
         if (last == kUnreached) break;
@@ -387,23 +472,25 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
         const int at = __shfl_sync(kAll, place, from);
         if (lane == r) {
             my_key = last;
-            my_lane = from;
             my_place = at;
         }
         if (lane == from) {
-            ++place;
-            head = place < NV ? sorted[place * 32 + lane] : kUnreached;
+            place += 32;
+            head = sorted[place];
         }
     }
     int mine = -1;                                         // lane j: the j-th choice
     if (my_key != kUnreached) {
-        // the (place - greater ones)-th of the lane's experts with that key
-        int skip = my_place;
+        // the (place - greater ones)-th of its lane's experts with that key
+        const int first = (my_place & 31) * NV;
+        int skip = my_place >> 5;
+        uint32_t of[NV];
+        load_keys<NV>(of, keys + first);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) skip -= keys[my_lane * NV + i] > my_key;
+        for (int i = 0; i < NV; ++i) skip -= of[i] > my_key;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (keys[my_lane * NV + i] == my_key && skip-- == 0) mine = my_lane * NV + i;
+            if (of[i] == my_key && skip-- == 0) mine = first + i;
     }
     float lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
     if (biased && !nan) {
@@ -417,40 +504,31 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs p) {
         if (last > kNanKey) {
             const uint32_t least = near_key(last, wide);
             const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
-            bool near = false;
+            // a lane's next key is near; and is any of its experts' another than the last choice
+            if (head >= least) {
+                load_keys<NV>(key, keys + e0);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) near |= keys[e0 + i] >= least && (l[i] != llast || b[i] != blast);
-            // the k chosen are near too: only a lane's next one can be another
-            if (head >= least && near) unsure = true;
+                for (int i = 0; i < NV; ++i) unsure |= key[i] >= least && (l[i] != llast || b[i] != blast);
+            }
         }
         if (__any_sync(kAll, unsure)) {
             const uint32_t least = last > kNanKey ? near_key(last, wide) : kNanKey + 1;
             uint32_t which = 0;
+            load_keys<NV>(key, keys + e0);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) which |= (keys[e0 + i] >= least ? 1u : 0u) << i;
+            for (int i = 0; i < NV; ++i) which |= (key[i] >= least ? 1u : 0u) << i;
             __syncwarp();
-            mine = choose_exact(p, row, top, which, NV, s_list[warp]);
+            mine = choose_exact(p, row, top, which, NV, s_list[warp], s_wide[warp]);
             lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
         }
     }
 
-    float w;
+    float w = 0.0f;
     if (p.renormalise) {
-        // shares of the chosen: every term is taken relative to the largest, so that
-        // none of them underflows with it
-        const float most = warp_max(lg);
-        const float ref = p.sigmoid ? fminf(most, 0.0f) : (most == -INFINITY ? 0.0f : most);
-        float e = 0.0f;
-        if (mine >= 0) {
-            if (!p.sigmoid) e = expf(lg - ref);
-            else e = lg <= 0.0f ? expf(lg - ref) / (1.0f + expf(lg)) : 1.0f / (1.0f + expf(-lg));
-        }
-        const float all = warp_sum(e);
-        w = mine >= 0 ? e / all * p.scale : 0.0f;
-    } else if (mine < 0) {
-        w = 0.0f;
-    } else {
-        w = (p.sigmoid ? 1.0f / (1.0f + expf(-lg)) : expf(lg - top) / total) * p.scale;
+        const float all = share_terms(SIGMOID, mine >= 0, lg, w);
+        w = mine >= 0 ? w / all * p.scale : 0.0f;
+    } else if (mine >= 0) {
+        w = (SIGMOID ? 1.0f / (1.0f + expf(-lg)) : expf(lg - top) / total) * p.scale;
     }
     if (nan && mine >= 0) w = __int_as_float(0x7fffffff);
     if (lane < p.k) {
@@ -488,7 +566,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_back_kernel(const RouteBack
     const bool dense = !p.sigmoid && !p.renormalise;
     float l[NV], base = 0.0f, total = 1.0f;
     if (dense) {
-        load_row<T, NV, VEC>(l, row, p.experts, p.bnd, 1);
+        load_row<T, NV, VEC>(l, row, p.experts, -INFINITY, p.bnd, 1);
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) top = fmaxf(top, l[i]);
@@ -505,20 +583,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_back_kernel(const RouteBack
     }
     float v = 0.0f, mean = 0.0f;
     if (p.renormalise) {
-        const float most = warp_max(lg);
-        const float ref = p.sigmoid ? fminf(most, 0.0f) : (most == -INFINITY ? 0.0f : most);
-        float q = 0.0f, rest = 1.0f;                       // rest: 1 - s
-        if (e >= 0) {
-            if (!p.sigmoid) {
-                q = expf(lg - ref);
-            } else {
-                const float a = expf(-fabsf(lg)), small = a / (1.0f + a), large = 1.0f / (1.0f + a);
-                q = lg <= 0.0f ? expf(lg - ref) * large : large;
-                rest = lg <= 0.0f ? large : small;
-            }
-        }
-        const float all = warp_sum(q);
+        float q;
+        const float all = share_terms(p.sigmoid, e >= 0, lg, q);
         q = all == 0.0f ? 0.0f : q / all;
+        float rest = 1.0f;                                 // 1 - s
+        if (p.sigmoid) {
+            const float a = expf(-fabsf(lg));
+            rest = (lg < 0.0f ? 1.0f : a) / (1.0f + a);
+        }
         mean = warp_sum(e >= 0 ? q * g : 0.0f);
         if (e >= 0) v = q * rest * (g - mean);
     } else if (p.sigmoid) {
@@ -564,11 +636,15 @@ bool vec_rows(const void* p, int64_t es, int64_t stride, int64_t m, int experts,
     return experts % nv == 0 && rows_aligned(p, es, stride, m, bytes);
 }
 
+template <typename T, int NV, bool SIGMOID>
+cudaError_t route_s(const RouteArgs& a, cudaStream_t st) {
+    if (vec_rows(a.logits, sizeof(T), a.sl, a.m, a.experts, NV))
+        return launch_after(route_kernel<T, NV, true, SIGMOID>, dim3(blocks(a.m)), kWarps * 32, 0, st, a);
+    return launch_after(route_kernel<T, NV, false, SIGMOID>, dim3(blocks(a.m)), kWarps * 32, 0, st, a);
+}
 template <typename T, int NV>
 cudaError_t route_nv(const RouteArgs& a, cudaStream_t st) {
-    if (vec_rows(a.logits, sizeof(T), a.sl, a.m, a.experts, NV))
-        return launch_after(route_kernel<T, NV, true>, dim3(blocks(a.m)), kWarps * 32, 0, st, a);
-    return launch_after(route_kernel<T, NV, false>, dim3(blocks(a.m)), kWarps * 32, 0, st, a);
+    return a.sigmoid ? route_s<T, NV, true>(a, st) : route_s<T, NV, false>(a, st);
 }
 template <typename T>
 cudaError_t route_t(const RouteArgs& a, cudaStream_t st) {
