@@ -271,6 +271,17 @@ __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
     return v == v ? key_of(v) : kNanKey + 1;
 }
 
+// Whether the choice with logit l1 and bias b1 is surely greater than the one with l2, b2,
+// told by differences, which fp32 has to a share of themselves:
+//   s1 - s2 = s1 (1 - s2) (1 - e^(l2 - l1)) for a sigmoid, s1 (1 - e^(l2 - l1)) for a softmax
+// within 2^-20 and 2^-17 of it, against b2 - b1.
+template <bool SIGMOID>
+__device__ __noinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {
+    const float ds = -expm1f(l2 - l1) * (SIGMOID ? 1.0f / ((1.0f + expf(-l1)) * (1.0f + expf(l2))) : expf(l1 - top) / total);
+    const float db = b2 - b1;
+    return ds - db > fabsf(ds) * (SIGMOID ? 0x1p-20f : 0x1p-17f) + fabsf(db) * 0x1p-22f;
+}
+
 // A token's k best take k rounds: the lanes' keys are sorted once, a round takes the
 // largest of the lanes' next ones, the lowest lane first, and that lane goes on to its
 // next. Which expert it was follows from the key and its place among the lane's, all
@@ -501,14 +512,17 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const RouteArgs p
         const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
         const float lg2 = __shfl_down_sync(kAll, lg, 1), b2 = __shfl_down_sync(kAll, b1, 1);
         bool unsure = lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide) && (lg != lg2 || b1 != b2);
+        if (unsure) unsure = !surely_greater<SIGMOID>(lg, b1, lg2, b2, top, total);
         if (last > kNanKey) {
             const uint32_t least = near_key(last, wide);
             const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
-            // a lane's next key is near; and is any of its experts' another than the last choice
             if (head >= least) {
-                load_keys<NV>(key, keys + e0);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) unsure |= key[i] >= least && (l[i] != llast || b[i] != blast);
+#pragma unroll 1
+                for (int e = e0; e < e0 + NV; ++e)
+                    if (keys[e] >= least && keys[e] <= last) {
+                        const float li = to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))), bi = load_one(p.bias + e, p.bnd, 1, 0.0f);
+                        if (li != llast || bi != blast) unsure |= !surely_greater<SIGMOID>(llast, blast, li, bi, top, total);
+                    }
             }
         }
         if (__any_sync(kAll, unsure)) {
