@@ -66,124 +66,44 @@ __device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int exper
     }
 }
 
-// ---------------------------------------------------------------- in 64 bits
-// What a token's scores in 64 bits need: the softmax's largest logit and sum.
-struct Score64 {
-    double top, total;
-    bool sigmoid;
-    __device__ double operator()(float l) const {
-        return sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp(static_cast<double>(l) - top) / total;
+// Terms of the chosen's shares, and their sum: s itself, or where they would underflow s
+// over the largest of them. Lanes with `on` have a chosen expert's logit.
+__device__ __forceinline__ float share_terms(bool sigmoid, bool on, float l, float& e) {
+    float most = 0.0f;
+    if (!sigmoid || !__any_sync(kAll, on && !(l < -64.0f))) {
+        most = warp_max(on ? l : -INFINITY);
+        if (most == -INFINITY) most = 0.0f;
     }
-};
-template <typename T>
-__device__ __noinline__ Score64 score64(const RouteArgs& p, const T* row, float top) {
-    Score64 r{static_cast<double>(top), 1.0, p.sigmoid};
-    if (!p.sigmoid) {
-        double sum = 0.0;
-        for (int e = threadIdx.x & 31; e < p.experts; e += 32) sum += exp(static_cast<double>(to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f)))) - r.top);
-        r.total = warp_sum(sum);
-    }
-    return r;
-}
-// The choice c of expert e: -inf out of reach.
-template <typename T>
-__device__ __forceinline__ double choice64(const RouteArgs& p, const T* row, const Score64& s, int e) {
-    const float l = to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))), b = p.bias != nullptr ? load_one(p.bias + e, p.bnd, 1, 0.0f) : 0.0f;
-    return l == -INFINITY || b == -INFINITY ? -INFINITY : s(l) + static_cast<double>(b);
-}
-// The largest of a warp's values and the lowest place that has it.
-__device__ __forceinline__ void best_of_warp(double& v, int& at) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const double v2 = __shfl_xor_sync(kAll, v, o);
-        const int at2 = __shfl_xor_sync(kAll, at, o);
-        if (v2 > v || (v2 == v && at2 < at)) {
-            v = v2;
-            at = at2;
+    e = 0.0f;
+    if (on) {
+        if (!sigmoid) {
+            e = expf(l - most);
+        } else if (most < 0.0f) {
+            e = expf(l - most);                            // s = e^l to all of fp32's digits
+        } else {
+            const float a = expf(-fabsf(l));
+            e = (l < 0.0f ? a : 1.0f) / (1.0f + a);
         }
     }
+    return warp_sum(e);
 }
 
-// The best `need` of the groups in `which`, as a mask.
-template <typename T>
-__device__ __noinline__ uint32_t groups_exact(const RouteArgs& p, const T* row, float top, uint32_t which, int need) {
-    const Score64 s = score64(p, row, top);
-    const int lane = threadIdx.x & 31, size = p.experts / p.groups;
-    double mine = -INFINITY;                               // lane g: group g's score
-    for (uint32_t left = which; left != 0; left &= left - 1) {
-        const int g = __ffs(left) - 1;
-        double best = -INFINITY, next = -INFINITY;
-        for (int i = lane; i < size; i += 32) {
-            const double c = choice64(p, row, s, g * size + i);
-            next = fmax(next, fmin(best, c));
-            best = fmax(best, c);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double b2 = __shfl_xor_sync(kAll, best, o), n2 = __shfl_xor_sync(kAll, next, o);
-            next = fmax(fmin(best, b2), fmax(next, n2));
-            best = fmax(best, b2);
-        }
-        if (lane == g) mine = p.group_best > 1 && next != -INFINITY ? best + next : best;
+// Lane j has the token's j-th expert and its logit, or -1: weights and experts.
+template <bool SIGMOID>
+__device__ __forceinline__ void put_weights(const RouteArgs& p, int64_t t, int mine, float lg, float top, float total, bool nan) {
+    float w = 0.0f;
+    if (p.renormalise) {
+        const float all = share_terms(SIGMOID, mine >= 0, lg, w);
+        w = mine >= 0 ? w / all * p.scale : 0.0f;
+    } else if (mine >= 0) {
+        w = (SIGMOID ? 1.0f / (1.0f + expf(-lg)) : expf(lg - top) / total) * p.scale;
     }
-    uint32_t kept = 0;
-    for (; need > 0; --need) {
-        double v = mine;
-        int at = lane;
-        best_of_warp(v, at);
-        if (v == -INFINITY) break;
-        kept |= 1u << at;
-        if (lane == at) mine = -INFINITY;
-    }
-    return kept;
-}
-
-// The k best of the experts whose bit is set in the lanes' `which` (bit i of a lane: expert
-// lane * nv + i): lane j gets the j-th one's index, or -1. list: 64 ints of shared memory,
-// c: nv * 32 doubles.
-template <typename T>
-__device__ __noinline__ int choose_exact(const RouteArgs& p, const T* row, float top, uint32_t which, int nv, int* list, double* c_at) {
-    const Score64 s = score64(p, row, top);
+    if (nan && mine >= 0) w = __int_as_float(0x7fffffff);
     const int lane = threadIdx.x & 31;
-    int mine = -1;
-    int all = __popc(which), before = all;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, before, o);
-        if (lane >= o) before += v;
+    if (lane < p.k) {
+        store_one(p.weights + t * p.k + lane, w, p.bnd, 2);
+        store_one(p.chosen + t * p.k + lane, mine, p.bnd, 3);
     }
-    const int count = __shfl_sync(kAll, before, 31);
-    if (count <= 32) {                                     // a lane each, ranked against one another
-        for (before -= all; which != 0; which &= which - 1) list[before++] = lane * nv + __ffs(which) - 1;
-        list[32 + lane] = -1;
-        __syncwarp();
-        const int e = lane < count ? list[lane] : -1;
-        const double c = e >= 0 ? choice64(p, row, s, e) : -INFINITY;
-        int rank = 0;
-        for (int i = 0; i < count; ++i) {
-            const double c2 = __shfl_sync(kAll, c, i);
-            const int e2 = __shfl_sync(kAll, e, i);
-            rank += c2 > c || (c2 == c && e2 < e);
-        }
-        if (e >= 0 && c != -INFINITY && rank < p.k) list[32 + rank] = e;
-        __syncwarp();
-        return lane < p.k ? list[32 + lane] : -1;
-    }
-    for (int i = 0; i < nv; ++i) c_at[i * 32 + lane] = (which >> i) & 1u ? choice64(p, row, s, lane * nv + i) : -INFINITY;
-    for (int r = 0; r < p.k; ++r) {
-        double v = -INFINITY;
-        int at = 1 << 20;
-        for (int i = 0; i < nv; ++i)
-            if (c_at[i * 32 + lane] > v) {
-                v = c_at[i * 32 + lane];
-                at = lane * nv + i;
-            }
-        best_of_warp(v, at);
-        if (v == -INFINITY) break;
-        if (lane == r) mine = at;
-        if (at / nv == lane) c_at[at % nv * 32 + lane] = -INFINITY;
-    }
-    return mine;
 }
 
 // ---------------------------------------------------------------- the choice
@@ -243,28 +163,6 @@ __device__ __forceinline__ void load_keys(uint32_t (&k)[NV], const uint32_t* fro
     }
 }
 
-// Terms of the chosen's shares, and their sum: s itself, or where they would underflow s
-// over the largest of them. Lanes with `on` have a chosen expert's logit.
-__device__ __forceinline__ float share_terms(bool sigmoid, bool on, float l, float& e) {
-    float most = 0.0f;
-    if (!sigmoid || !__any_sync(kAll, on && !(l < -64.0f))) {
-        most = warp_max(on ? l : -INFINITY);
-        if (most == -INFINITY) most = 0.0f;
-    }
-    e = 0.0f;
-    if (on) {
-        if (!sigmoid) {
-            e = expf(l - most);
-        } else if (most < 0.0f) {
-            e = expf(l - most);                            // s = e^l to all of fp32's digits
-        } else {
-            const float a = expf(-fabsf(l));
-            e = (l < 0.0f ? a : 1.0f) / (1.0f + a);
-        }
-    }
-    return warp_sum(e);
-}
-
 // The least key that is not surely below one by more than `wide`.
 __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
     const float v = value_of(key) - wide;
@@ -276,10 +174,182 @@ __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
 //   s1 - s2 = s1 (1 - s2) (1 - e^(l2 - l1)) for a sigmoid, s1 (1 - e^(l2 - l1)) for a softmax
 // within 2^-20 and 2^-17 of it, against b2 - b1.
 template <bool SIGMOID>
-__device__ __noinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {
+__device__ __forceinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {
     const float ds = -expm1f(l2 - l1) * (SIGMOID ? 1.0f / ((1.0f + expf(-l1)) * (1.0f + expf(l2))) : expf(l1 - top) / total);
     const float db = b2 - b1;
     return ds - db > fabsf(ds) * (SIGMOID ? 0x1p-20f : 0x1p-17f) + fabsf(db) * 0x1p-22f;
+}
+
+// ---------------------------------------------------------------- what fp32 leaves open
+// Choices in 64 bits: -inf out of reach.
+template <typename T, bool SIGMOID>
+struct Choice64 {
+    const RouteArgs& p;
+    const T* row;
+    double top, total;
+    __device__ __forceinline__ float logit(int e) const { return to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))); }
+    __device__ __forceinline__ float bias(int e) const { return p.bias != nullptr ? load_one(p.bias + e, p.bnd, 1, 0.0f) : 0.0f; }
+    __device__ __forceinline__ double of(float l, float b) const {
+        if (l == -INFINITY || b == -INFINITY) return -INFINITY;
+        const double x = static_cast<double>(l), s = SIGMOID ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / total;
+        return s + static_cast<double>(b);
+    }
+    __device__ void prepare(float most) {
+        top = static_cast<double>(most);
+        total = 1.0;
+        if (!SIGMOID) {
+            total = 0.0;
+            for (int e = threadIdx.x & 31; e < p.experts; e += 32) total += exp(static_cast<double>(logit(e)) - top);
+            total = warp_sum(total);
+        }
+    }
+};
+// The largest of a warp's values and the lowest place that has it.
+__device__ __forceinline__ void best_of_warp(double& v, int& at) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const double v2 = __shfl_xor_sync(kAll, v, o);
+        const int at2 = __shfl_xor_sync(kAll, at, o);
+        if (v2 > v || (v2 == v && at2 < at)) {
+            v = v2;
+            at = at2;
+        }
+    }
+}
+
+// A token whose choice hangs on gaps within the bound: one in a thousand, so the kernel ends
+// with this call and keeps no register for it. keys: its experts' keys; sure: the
+// groups that stay; open: those of which the best join them; top, total: its softmax's. A
+// warp has few lanes for 64 bits (16 cycles an instruction): they see only the open groups, and
+// of the experts those near the border, if differences do not tell those apart.
+// list: 64 ints of shared memory.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t* keys, int* list, float bound, float top, float total, uint32_t sure,
+                                        uint32_t open) {
+    const int lane = threadIdx.x & 31, size = p.experts / p.groups;
+    Choice64<T, SIGMOID> c64{p, static_cast<const T*>(p.logits) + t * p.sl};
+    bool ready = false;
+    uint32_t kept = sure;
+    if (open != 0) {
+        c64.prepare(top);
+        ready = true;
+        double mine = -INFINITY;                           // lane g: group g's score
+        for (uint32_t left = open; left != 0; left &= left - 1) {
+            const int g = __ffs(left) - 1;
+            double best = -INFINITY, next = -INFINITY;
+            for (int i = lane; i < size; i += 32) {
+                const double c = c64.of(c64.logit(g * size + i), c64.bias(g * size + i));
+                next = fmax(next, fmin(best, c));
+                best = fmax(best, c);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const double b2 = __shfl_xor_sync(kAll, best, o), n2 = __shfl_xor_sync(kAll, next, o);
+                next = fmax(fmin(best, b2), fmax(next, n2));
+                best = fmax(best, b2);
+            }
+            if (lane == g) mine = p.group_best > 1 && next != -INFINITY ? best + next : best;
+        }
+        for (int need = p.kept - __popc(sure); need > 0; --need) {
+            double v = mine;
+            int at = lane;
+            best_of_warp(v, at);
+            if (v == -INFINITY) break;
+            kept |= 1u << at;
+            if (lane == at) mine = -INFINITY;
+        }
+        for (int e = lane; e < p.experts; e += 32)
+            if (((kept >> (e / size & 31)) & 1u) == 0u) keys[e] = kUnreached;
+        __syncwarp();
+    }
+    // the k best by keys, then whatever is near the last of them
+    int count = 0, first = 0;                              // first: of those near
+    uint32_t last = kUnreached;
+    for (int r = 0; r < p.k; ++r) {
+        uint32_t best = kUnreached;
+        int at = 0x7fffffff;
+        for (int e = lane; e < p.experts; e += 32)
+            if (keys[e] > best) {
+                best = keys[e];
+                at = e;
+            }
+        const uint32_t most = __reduce_max_sync(kAll, best);
+        if (most == kUnreached) break;
+        at = __reduce_min_sync(kAll, best == most ? at : 0x7fffffff);
+        __syncwarp();
+        if (lane == 0) {
+            keys[at] = kUnreached;
+            list[r] = at;
+        }
+        __syncwarp();
+        last = most;
+        count = r + 1;
+    }
+    first = count;
+    bool few = true;
+    if (p.bias != nullptr && count == p.k && last > kNanKey) {
+        const uint32_t least = near_key(last, 3.0f * bound);
+        for (int e0 = 0; e0 < p.experts && few; e0 += 32) {
+            const bool near = e0 + lane < p.experts && keys[e0 + lane] >= least;
+            const uint32_t all = __ballot_sync(kAll, near);
+            few = count + __popc(all) <= 32;
+            if (few && near) list[count + __popc(all & ((1u << lane) - 1u))] = e0 + lane;
+            count += __popc(all);
+        }
+        __syncwarp();
+    }
+    int mine = -1;
+    float lg = -INFINITY;
+    if (few) {
+        const int e = lane < count ? list[lane] : -1;
+        const float l = e >= 0 ? c64.logit(e) : -INFINITY, b = e >= 0 ? c64.bias(e) : 0.0f;
+        mine = lane < first ? e : -1;
+        if (p.bias != nullptr) {                           // without one the keys are the logits'
+            // the chosen against the one before, the others against the last chosen
+            const int to = lane < first ? lane - 1 : first - 1;
+            const float l1 = __shfl_sync(kAll, l, to & 31), b1 = __shfl_sync(kAll, b, to & 31);
+            const bool told = lane == 0 || e < 0 || (l == l1 && b == b1) || surely_greater<SIGMOID>(l1, b1, l, b, top, total);
+            if (!__all_sync(kAll, told)) {
+                if (!ready) c64.prepare(top);
+                const double c = e >= 0 ? c64.of(l, b) : -INFINITY;
+                int rank = 0;
+                for (int i = 0; i < count; ++i) {
+                    const double c2 = __shfl_sync(kAll, c, i);
+                    const int e2 = __shfl_sync(kAll, e, i);
+                    rank += c2 > c || (c2 == c && e2 < e);
+                }
+                __syncwarp();
+                if (e >= 0 && rank < p.k) list[32 + rank] = e;
+                __syncwarp();
+                mine = lane < first ? list[32 + lane] : -1;
+            }
+        }
+    } else {
+        // more than a warp's worth: every round in 64 bits, those that were taken by keys among them
+        if (lane < first) keys[list[lane]] = last;
+        __syncwarp();
+        const uint32_t least = near_key(last, 3.0f * bound);
+        if (!ready) c64.prepare(top);
+        for (int r = 0; r < p.k; ++r) {
+            double v = -INFINITY;
+            int at = 1 << 20;
+            for (int e = lane; e < p.experts; e += 32)
+                if (keys[e] >= least) {
+                    const double c = c64.of(c64.logit(e), c64.bias(e));
+                    if (c > v) {
+                        v = c;
+                        at = e;
+                    }
+                }
+            best_of_warp(v, at);
+            if (v == -INFINITY) break;
+            if (lane == r) mine = at;
+            if (lane == 0) keys[at] = kUnreached;
+            __syncwarp();
+        }
+    }
+    if (mine >= 0) lg = c64.logit(mine);
+    put_weights<SIGMOID>(p, t, mine, lg, top, total, false);
 }
 
 // A token's k best take k rounds: the lanes' keys are sorted once, a round takes the
@@ -287,11 +357,10 @@ __device__ __noinline__ bool surely_greater(float l1, float b1, float l2, float 
 // next. Which expert it was follows from the key and its place among the lane's, all
 // rounds at once.
 template <typename T, int NV, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const RouteArgs p) {
+__global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_constant__ RouteArgs p) {
     // a warp's keys as they are, and sorted, lane by lane, with a last 0
     __shared__ __align__(16) uint32_t s_keys[kWarps][NV * 32], s_sorted[kWarps][NV * 32 + 32];
     __shared__ int s_list[kWarps][64];
-    __shared__ double s_wide[kWarps][NV * 32];
     pdl_launch_dependents();
     pdl_wait_prior();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -444,14 +513,17 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const RouteArgs p
             last = most;
         }
         if (scored && !nan) {
-            // sums of two choices are within two bounds and their own rounding; the best that stays out
+            // sums of two choices are within two bounds and their own rounding of the best that stays out
             const uint32_t out = __reduce_max_sync(kAll, (kept >> lane) & 1u ? kUnreached : group);
             const float wide = 6.0f * bound;
             if (out > kNanKey && !(value_of(last) - value_of(out) > wide)) {
-                const bool in = group > kNanKey && value_of(group) - value_of(out) > wide;
-                const bool open = group > kNanKey && !in && !(value_of(last) - value_of(group) > wide);
-                const uint32_t sure = __ballot_sync(kAll, in), which = __ballot_sync(kAll, open);
-                kept = sure | groups_exact(p, row, top, which, p.kept - __popc(sure));
+                const bool above = group > kNanKey && value_of(group) - value_of(out) > wide;
+                const bool near = group > kNanKey && !above && !(value_of(last) - value_of(group) > wide);
+                const uint32_t sure = __ballot_sync(kAll, above), open = __ballot_sync(kAll, near);
+                store_keys<NV>(s_keys[warp] + e0, key);
+                __syncwarp();
+                route_open<T, SIGMOID>(p, t, s_keys[warp], s_list[warp], bound, top, total, sure, open);
+                return;
             }
         }
         if (lanes * NV == size) {                          // a lane's experts are of one group
@@ -505,50 +577,30 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const RouteArgs p
     }
     float lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
     if (biased && !nan) {
-        // gaps between choices next to one another, and from the last to what stays out;
-        // the same logit and bias are a tie in any precision
+        // gaps between choices next to one another, and from the last to what stays out
         const float wide = 3.0f * bound;
-        const float b1 = mine >= 0 ? load_one(p.bias + mine, p.bnd, 1, 0.0f) : 0.0f;
         const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
-        const float lg2 = __shfl_down_sync(kAll, lg, 1), b2 = __shfl_down_sync(kAll, b1, 1);
-        bool unsure = lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide) && (lg != lg2 || b1 != b2);
-        if (unsure) unsure = !surely_greater<SIGMOID>(lg, b1, lg2, b2, top, total);
-        if (last > kNanKey) {
-            const uint32_t least = near_key(last, wide);
+        bool unsure = lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide);
+        unsure |= last > kNanKey && head >= near_key(last, wide);
+        if (__any_sync(kAll, unsure)) {
+            // the same logit and bias are a tie in any precision
+            const float b1 = mine >= 0 ? load_one(p.bias + mine, p.bnd, 1, 0.0f) : 0.0f;
+            const float lg2 = __shfl_down_sync(kAll, lg, 1), b2 = __shfl_down_sync(kAll, b1, 1);
             const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
-            if (head >= least) {
+            unsure = unsure && lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide) && (lg != lg2 || b1 != b2);
+            if (last > kNanKey && head >= near_key(last, wide))
 #pragma unroll 1
                 for (int e = e0; e < e0 + NV; ++e)
-                    if (keys[e] >= least && keys[e] <= last) {
-                        const float li = to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))), bi = load_one(p.bias + e, p.bnd, 1, 0.0f);
-                        if (li != llast || bi != blast) unsure |= !surely_greater<SIGMOID>(llast, blast, li, bi, top, total);
-                    }
+                    if (keys[e] >= near_key(last, wide) && keys[e] <= last)
+                        unsure |= to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))) != llast || load_one(p.bias + e, p.bnd, 1, 0.0f) != blast;
+            if (__any_sync(kAll, unsure)) {
+                __syncwarp();
+                route_open<T, SIGMOID>(p, t, keys, s_list[warp], bound, top, total, kAll, 0u);
+                return;
             }
         }
-        if (__any_sync(kAll, unsure)) {
-            const uint32_t least = last > kNanKey ? near_key(last, wide) : kNanKey + 1;
-            uint32_t which = 0;
-            load_keys<NV>(key, keys + e0);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) which |= (key[i] >= least ? 1u : 0u) << i;
-            __syncwarp();
-            mine = choose_exact(p, row, top, which, NV, s_list[warp], s_wide[warp]);
-            lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
-        }
     }
-
-    float w = 0.0f;
-    if (p.renormalise) {
-        const float all = share_terms(SIGMOID, mine >= 0, lg, w);
-        w = mine >= 0 ? w / all * p.scale : 0.0f;
-    } else if (mine >= 0) {
-        w = (SIGMOID ? 1.0f / (1.0f + expf(-lg)) : expf(lg - top) / total) * p.scale;
-    }
-    if (nan && mine >= 0) w = __int_as_float(0x7fffffff);
-    if (lane < p.k) {
-        store_one(p.weights + t * p.k + lane, w, p.bnd, 2);
-        store_one(p.chosen + t * p.k + lane, mine, p.bnd, 3);
-    }
+    put_weights<SIGMOID>(p, t, mine, lg, top, total, nan);
 }
 
 // Gradient with respect to the logits. With dw' = scale dw:
