@@ -46,11 +46,43 @@ __device__ __forceinline__ double warp_sum(double v) {
 // e / size for e < 512: magic = ceil(2^20 / size); e size < 2^20.
 __device__ __forceinline__ int over(int e, int magic) { return (e * magic) >> 20; }
 
-// A row's elements, NV to a lane; `other` past the last.
+// NV words of a lane to or from its run of a warp's.
+template <int NV, typename E>
+__device__ __forceinline__ void store_words(E* to, const E (&k)[NV]) {
+    if constexpr (NV % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            Pack<E, 4> v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v.v[j] = k[i + j];
+            *reinterpret_cast<Pack<E, 4>*>(to + i) = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) to[i] = k[i];
+    }
+}
+template <int NV, typename E>
+__device__ __forceinline__ void load_words(E (&k)[NV], const E* from) {
+    if constexpr (NV % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+            const Pack<E, 4> v = *reinterpret_cast<const Pack<E, 4>*>(from + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k[i + j] = v.v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) k[i] = from[i];
+    }
+}
+
+// A row's elements, NV to a lane; `other` past the last. VEC: a lane's are one vector or
+// none; else they come as whole lines by way of buf, NV * 32 floats of the warp's own.
 template <typename T, int NV, bool VEC>
-__device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int experts, float other, const Bounds& bnd, int span) {
-    const int e0 = (threadIdx.x & 31) * NV;
-    if constexpr (VEC) {                                   // NV elements or none
+__device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int experts, float other, float* buf, const Bounds& bnd, int span) {
+    const int lane = threadIdx.x & 31, e0 = lane * NV;
+    if constexpr (VEC) {
         if (e0 < experts) {
             const Pack<T, NV> v = load_pack<T, NV>(row + e0, bnd, span);
 #pragma unroll
@@ -61,8 +93,16 @@ __device__ __forceinline__ void load_row(float (&l)[NV], const T* row, int exper
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            l[i] = e0 + i < experts ? to_f32(load_one(row + e0 + i, bnd, span, from_f32<T>(0.0f))) : other;
+        for (int i = 0; i < NV; ++i) {
+            const int e = i * 32 + lane;
+            l[i] = e < experts ? to_f32(load_one(row + e, bnd, span, from_f32<T>(0.0f))) : other;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) buf[i * 32 + lane] = l[i];
+        __syncwarp();
+        load_words<NV>(l, buf + e0);
+        __syncwarp();
     }
 }
 
@@ -135,49 +175,70 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// NV keys of a lane to or from its run of a warp's keys.
-template <int NV>
-__device__ __forceinline__ void store_keys(uint32_t* to, const uint32_t (&k)[NV]) {
-    if constexpr (NV % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < NV; i += 4) *reinterpret_cast<uint4*>(to + i) = make_uint4(k[i], k[i + 1], k[i + 2], k[i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) to[i] = k[i];
-    }
-}
-template <int NV>
-__device__ __forceinline__ void load_keys(uint32_t (&k)[NV], const uint32_t* from) {
-    if constexpr (NV % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < NV; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(from + i);
-            k[i] = v.x;
-            k[i + 1] = v.y;
-            k[i + 2] = v.z;
-            k[i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) k[i] = from[i];
-    }
-}
-
 // The least key that is not surely below one by more than `wide`.
 __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
     const float v = value_of(key) - wide;
     return v == v ? key_of(v) : kNanKey + 1;
 }
 
-// Whether the choice with logit l1 and bias b1 is surely greater than the one with l2, b2,
-// told by differences, which fp32 has to a share of themselves:
+// By how much the choice with logit l1 and bias b1 is greater than the one with l2, b2, told
+// by differences, which fp32 has to a share of themselves, and how far off that may be:
 //   s1 - s2 = s1 (1 - s2) (1 - e^(l2 - l1)) for a sigmoid, s1 (1 - e^(l2 - l1)) for a softmax
 // within 2^-20 and 2^-17 of it, against b2 - b1.
 template <bool SIGMOID>
-__device__ __forceinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {
+__device__ __forceinline__ void add_difference(float l1, float b1, float l2, float b2, float top, float total, float& by, float& off) {
     const float ds = -expm1f(l2 - l1) * (SIGMOID ? 1.0f / ((1.0f + expf(-l1)) * (1.0f + expf(l2))) : expf(l1 - top) / total);
     const float db = b2 - b1;
-    return ds - db > fabsf(ds) * (SIGMOID ? 0x1p-20f : 0x1p-17f) + fabsf(db) * 0x1p-22f;
+    by += ds - db;
+    off += fabsf(ds) * (SIGMOID ? 0x1p-20f : 0x1p-17f) + fabsf(db) * 0x1p-22f;
+}
+template <bool SIGMOID>
+__device__ __forceinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {
+    float by = 0.0f, off = 0.0f;
+    add_difference<SIGMOID>(l1, b1, l2, b2, top, total, by, off);
+    return by > off;
+}
+
+// The largest of keys[first .. first + size), the lowest place first; every lane gets both.
+// It is taken out.
+__device__ __forceinline__ int take_best(uint32_t* keys, int first, int size, uint32_t& best) {
+    uint32_t mine = kUnreached;
+    int at = 0x7fffffff;
+#pragma unroll 1
+    for (int e = first + static_cast<int>(threadIdx.x & 31); e < first + size; e += 32)
+        if (keys[e] > mine) {
+            mine = keys[e];
+            at = e;
+        }
+    best = __reduce_max_sync(kAll, mine);
+    at = __reduce_min_sync(kAll, mine == best ? at : 0x7fffffff);
+    __syncwarp();
+    if (best != kUnreached && (threadIdx.x & 31) == 0) keys[at] = kUnreached;
+    __syncwarp();
+    return at;
+}
+// Whether group a's score is surely greater than group z's, by the differences of their best
+// experts, whom no other of their groups is near. Takes those out of keys.
+template <typename T, bool SIGMOID>
+__device__ __noinline__ bool surely_greater_group(const RouteArgs& p, const T* row, uint32_t* keys, int a, int z, float bound, float top, float total) {
+    const int size = p.experts / p.groups;
+    float by = 0.0f, off = 0.0f;
+    uint32_t ka = kUnreached, kz = kUnreached;
+#pragma unroll 1
+    for (int r = 0; r < p.group_best; ++r) {
+        const int ea = take_best(keys, a * size, size, ka), ez = take_best(keys, z * size, size, kz);
+        if (ka <= kNanKey || kz <= kNanKey) return false;
+        add_difference<SIGMOID>(to_f32(load_one(row + ea, p.bnd, 0, from_f32<T>(0.0f))), p.bias != nullptr ? load_one(p.bias + ea, p.bnd, 1, 0.0f) : 0.0f,
+                                to_f32(load_one(row + ez, p.bnd, 0, from_f32<T>(0.0f))), p.bias != nullptr ? load_one(p.bias + ez, p.bnd, 1, 0.0f) : 0.0f,
+                                top, total, by, off);
+    }
+    if (p.bias != nullptr) {                               // without one the keys are the logits'
+        uint32_t ra, rz;
+        take_best(keys, a * size, size, ra);
+        take_best(keys, z * size, size, rz);
+        if ((ra > kNanKey && !(value_of(ka) - value_of(ra) > 2.05f * bound)) || (rz > kNanKey && !(value_of(kz) - value_of(rz) > 2.05f * bound))) return false;
+    }
+    return by > off;
 }
 
 // ---------------------------------------------------------------- what fp32 leaves open
@@ -288,7 +349,7 @@ __device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t*
     first = count;
     bool few = true;
     if (p.bias != nullptr && count == p.k && last > kNanKey) {
-        const uint32_t least = near_key(last, 3.0f * bound);
+        const uint32_t least = near_key(last, 2.05f * bound);
         for (int e0 = 0; e0 < p.experts && few; e0 += 32) {
             const bool near = e0 + lane < p.experts && keys[e0 + lane] >= least;
             const uint32_t all = __ballot_sync(kAll, near);
@@ -328,7 +389,7 @@ __device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t*
         // more than a warp's worth: every round in 64 bits, those that were taken by keys among them
         if (lane < first) keys[list[lane]] = last;
         __syncwarp();
-        const uint32_t least = near_key(last, 3.0f * bound);
+        const uint32_t least = near_key(last, 2.05f * bound);
         if (!ready) c64.prepare(top);
         for (int r = 0; r < p.k; ++r) {
             double v = -INFINITY;
@@ -357,7 +418,7 @@ __device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t*
 // next. Which expert it was follows from the key and its place among the lane's, all
 // rounds at once.
 template <typename T, int NV, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_constant__ RouteArgs p) {
+__global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_constant__ RouteArgs p) {
     // a warp's keys as they are, and sorted, lane by lane, with a last 0
     __shared__ __align__(16) uint32_t s_keys[kWarps][NV * 32], s_sorted[kWarps][NV * 32 + 32];
     __shared__ int s_list[kWarps][64];
@@ -376,13 +437,14 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
     auto in = [&](int i) { return VEC ? e0 < p.experts : e0 + i < p.experts; };
 
     float l[NV], b[NV];
-    load_row<T, NV, VEC>(l, row, p.experts, 0.0f, p.bnd, 0);
+    float* buf = reinterpret_cast<float*>(s_keys[warp]);
+    load_row<T, NV, VEC>(l, row, p.experts, 0.0f, buf, p.bnd, 0);
     float odd = 0.0f, b_most = 0.0f;                       // odd: NaN if anything is not finite
 #pragma unroll
     for (int i = 0; i < NV; ++i) odd = fmaf(l[i], 0.0f, odd);
     if (biased) {
-        if (VEC && aligned_to(p.bias, 16)) load_row<float, NV, true>(b, p.bias, p.experts, 0.0f, p.bnd, 1);
-        else load_row<float, NV, false>(b, p.bias, p.experts, 0.0f, p.bnd, 1);
+        if (VEC && aligned_to(p.bias, 16)) load_row<float, NV, true>(b, p.bias, p.experts, 0.0f, buf, p.bnd, 1);
+        else load_row<float, NV, false>(b, p.bias, p.experts, 0.0f, buf, p.bnd, 1);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             odd = fmaf(b[i], 0.0f, odd);
@@ -448,17 +510,21 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < NV; ++i) key[i] = in(i) ? key[i] : kUnreached;
     }
-    // How far a choice in fp32 may be off. 2^(x log2 e) is within 2^-22.5 + 1.5 |x| 2^-24 of
-    // e^x (the approximation; the product and the constant in it): by that a sigmoid moves
-    // by 2^-24 at most, the sum and the reciprocal add 2^-24 and 2^-23 of it, 2^-22 in all. A
-    // softmax's term at x below the largest is off by (1.5 + 1.5 x / 2) 2^-22 exp(-x), 2^-21.4
-    // at most, its sum of up to 512 by 21 roundings and 2^-19.7 of itself, so s by 2^-18.5 of
-    // the largest. c's own rounding is 2^-24 of s + |b|.
+    // How far a choice in fp32 may be off. 2^(x log2 e) is within 2^-22 + 1.5 |x| 2^-24 of e^x
+    // (the approximation; the product and the constant in it): by that a sigmoid moves by
+    // 0.29 * 2^-22 at most, the sum and the reciprocal add 2^-24 and 2^-23 of it: 1.04 * 2^-22
+    // (measured over 2^30 logits in [-60, 60]: 0.49 * 2^-22). A
+    // softmax's term at x below the largest is off by (2 + 0.75 x) 2^-23 exp(-x), 2^-22 at
+    // most, its sum of up to 512 by 21 roundings and 2^-20 of itself, so s by 2^-18.5 of
+    // the largest. c's own rounding is 2^-24 of s + |b|. Two choices differ as they seem to
+    // where that is by more than `wide`; two sums of two of them, each rounded once more, by
+    // more than 5 bounds.
     float bound = 0.0f;
     if (scored) {
         b_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_most)));
-        bound = (SIGMOID ? 0x1p-21f : 0x1p-18f / total) + b_most * 0x1p-23f;
+        bound = (SIGMOID ? 0x1.4p-22f + 0x1p-24f : 0x1p-18f / total) + b_most * 0x1p-24f;
     }
+    const float wide = 2.05f * bound;
 
     if (grouped) {
         uint32_t best = 0, next = 0;
@@ -513,17 +579,26 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
             last = most;
         }
         if (scored && !nan) {
-            // sums of two choices are within two bounds and their own rounding of the best that stays out
+            // the groups near the border: `five` around the best that stays out and the last that stays
             const uint32_t out = __reduce_max_sync(kAll, (kept >> lane) & 1u ? kUnreached : group);
-            const float wide = 6.0f * bound;
-            if (out > kNanKey && !(value_of(last) - value_of(out) > wide)) {
-                const bool above = group > kNanKey && value_of(group) - value_of(out) > wide;
-                const bool near = group > kNanKey && !above && !(value_of(last) - value_of(group) > wide);
+            const float five = 5.0f * bound;
+            if (out > kNanKey && !(value_of(last) - value_of(out) > five)) {
+                const bool above = group > kNanKey && value_of(group) - value_of(out) > five;
+                const bool near = group > kNanKey && !above && !(value_of(last) - value_of(group) > five);
                 const uint32_t sure = __ballot_sync(kAll, above), open = __ballot_sync(kAll, near);
-                store_keys<NV>(s_keys[warp] + e0, key);
+                store_words<NV>(s_keys[warp] + e0, key);
                 __syncwarp();
-                route_open<T, SIGMOID>(p, t, s_keys[warp], s_list[warp], bound, top, total, sure, open);
-                return;
+                const uint32_t kept_near = open & kept, out_near = open & ~kept;
+                const bool told = __popc(kept_near) == 1 && __popc(out_near) == 1 &&
+                                  surely_greater_group<T, SIGMOID>(p, row, s_keys[warp], __ffs(kept_near) - 1, __ffs(out_near) - 1, bound, top, total);
+                if (!told) {
+                    __syncwarp();
+                    store_words<NV>(s_keys[warp] + e0, key);
+                    __syncwarp();
+                    route_open<T, SIGMOID>(p, t, s_keys[warp], s_list[warp], bound, top, total, sure, open);
+                    return;
+                }
+                __syncwarp();
             }
         }
         if (lanes * NV == size) {                          // a lane's experts are of one group
@@ -540,7 +615,7 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
 
     uint32_t* keys = s_keys[warp];
     uint32_t* sorted = s_sorted[warp];
-    store_keys<NV>(keys + e0, key);
+    store_words<NV>(keys + e0, key);
     sort_keys<NV>(key);
 #pragma unroll
     for (int i = 1; i < NV; ++i) sorted[i * 32 + lane] = key[i];
@@ -568,7 +643,7 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
         const int first = (my_place & 31) * NV;
         int skip = my_place >> 5;
         uint32_t of[NV];
-        load_keys<NV>(of, keys + first);
+        load_words<NV>(of, keys + first);
 #pragma unroll
         for (int i = 0; i < NV; ++i) skip -= of[i] > my_key;
 #pragma unroll
@@ -578,21 +653,32 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
     float lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
     if (biased && !nan) {
         // gaps between choices next to one another, and from the last to what stays out
-        const float wide = 3.0f * bound;
         const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
         bool unsure = lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide);
         unsure |= last > kNanKey && head >= near_key(last, wide);
         if (__any_sync(kAll, unsure)) {
-            // the same logit and bias are a tie in any precision
+            // the same logit and bias are a tie in any precision; others by their differences
             const float b1 = mine >= 0 ? load_one(p.bias + mine, p.bnd, 1, 0.0f) : 0.0f;
             const float lg2 = __shfl_down_sync(kAll, lg, 1), b2 = __shfl_down_sync(kAll, b1, 1);
             const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
-            unsure = unsure && lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide) && (lg != lg2 || b1 != b2);
-            if (last > kNanKey && head >= near_key(last, wide))
+            // my own next in line, then my lane's experts that stay out against the last choice
+            float l1 = lg, bb1 = b1, l2 = lg2, bb2 = b2;
+            bool ask = unsure && lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide);
+            const bool near = last > kNanKey && head >= near_key(last, wide);
+            unsure = false;
 #pragma unroll 1
-                for (int e = e0; e < e0 + NV; ++e)
-                    if (keys[e] >= near_key(last, wide) && keys[e] <= last)
-                        unsure |= to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f))) != llast || load_one(p.bias + e, p.bnd, 1, 0.0f) != blast;
+            for (int i = -1; i < (near ? NV : 0); ++i) {
+                if (i >= 0) {
+                    const int e = e0 + i;
+                    ask = keys[e] >= near_key(last, wide) && keys[e] <= last;
+                    if (!ask) continue;
+                    l1 = llast;
+                    bb1 = blast;
+                    l2 = to_f32(load_one(row + e, p.bnd, 0, from_f32<T>(0.0f)));
+                    bb2 = load_one(p.bias + e, p.bnd, 1, 0.0f);
+                }
+                if (ask && (l1 != l2 || bb1 != bb2)) unsure |= !surely_greater<SIGMOID>(l1, bb1, l2, bb2, top, total);
+            }
             if (__any_sync(kAll, unsure)) {
                 __syncwarp();
                 route_open<T, SIGMOID>(p, t, keys, s_list[warp], bound, top, total, kAll, 0u);
@@ -612,7 +698,7 @@ __global__ void __launch_bounds__(kWarps * 32, 6) route_kernel(const __grid_cons
 // by slot, so that an expert named twice gets both.
 template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_back_kernel(const RouteBackArgs p) {
-    __shared__ float s_row[kWarps][NV * 32];
+    __shared__ __align__(16) float s_row[kWarps][NV * 32];
     pdl_launch_dependents();
     pdl_wait_prior();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -632,7 +718,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_back_kernel(const RouteBack
     const bool dense = !p.sigmoid && !p.renormalise;
     float l[NV], base = 0.0f, total = 1.0f;
     if (dense) {
-        load_row<T, NV, VEC>(l, row, p.experts, -INFINITY, p.bnd, 1);
+        load_row<T, NV, VEC>(l, row, p.experts, -INFINITY, s_row[warp], p.bnd, 1);
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) top = fmaxf(top, l[i]);
@@ -666,19 +752,21 @@ __global__ void __launch_bounds__(kWarps * 32) route_back_kernel(const RouteBack
         v = g;
         mean = warp_sum(e >= 0 ? g * (expf(lg - base) / total) : 0.0f);
     }
+    float d[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s_row[warp][lane * NV + i] = 0.0f;
+    for (int i = 0; i < NV; ++i) d[i] = 0.0f;
+    store_words<NV>(s_row[warp] + lane * NV, d);
     __syncwarp();
     for (int j = 0; j < p.k; ++j) {
         if (lane == j && e >= 0) s_row[warp][e] += v;
         __syncwarp();
     }
     T* out = static_cast<T*>(p.dlogits) + t * p.sd;
-    float d[NV];
+    load_words<NV>(d, s_row[warp] + lane * NV);
+    if (dense) {
+        const float inv = 1.0f / total;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        d[i] = s_row[warp][lane * NV + i];
-        if (dense) d[i] = l[i] / total * (d[i] - mean);
+        for (int i = 0; i < NV; ++i) d[i] = l[i] * inv * (d[i] - mean);
     }
     if constexpr (VEC) {
         if (lane * NV < p.experts) {
@@ -687,10 +775,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_back_kernel(const RouteBack
             for (int i = 0; i < NV; ++i) o.v[i] = from_f32<T>(d[i]);
             store_pack<T, NV>(out + lane * NV, o, p.bnd, 3);
         }
-    } else {
+    } else {                                               // as whole lines
+        __syncwarp();
+        store_words<NV>(s_row[warp] + lane * NV, d);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (lane * NV + i < p.experts) store_one(out + lane * NV + i, from_f32<T>(d[i]), p.bnd, 3);
+            if (i * 32 + lane < p.experts) store_one(out + i * 32 + lane, from_f32<T>(s_row[warp][i * 32 + lane]), p.bnd, 3);
     }
 }
 
