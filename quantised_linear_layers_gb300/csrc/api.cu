@@ -1219,7 +1219,7 @@ ql_status expert_dispatch(const void* x, ql_dtype dtype, int64_t m, int64_t n, i
     a.bnd.s[2] = ql::span_of(offsets, 4, experts + 1, 1);
     a.bnd.s[3] = ql::span_of(xs, a.es, m * k, xs_stride_m, n, 1);
     a.bnd.status = di.status;
-    return from_cuda(ql::launch_dispatch(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+    return from_cuda(ql::launch_dispatch(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ql_status expert_combine(const void* ys, ql_dtype dtype, int64_t ys_stride_m, const int32_t* rows, const float* weights,
@@ -1249,7 +1249,7 @@ ql_status expert_combine(const void* ys, ql_dtype dtype, int64_t ys_stride_m, co
     a.bnd.s[3] = ql::span_of(add, bytes_of(dtype), m, add_stride_m, n, 1);
     a.bnd.s[4] = ql::span_of(y, bytes_of(dtype), m, y_stride_m, n, 1);
     a.bnd.status = di.status;
-    return from_cuda(ql::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
+    return from_cuda(ql::launch_combine(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ql_status expert_combine_backward(const void* dy, ql_dtype dtype, int64_t dy_stride_m, const void* ys, int64_t ys_stride_m,

@@ -115,164 +115,294 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
 }
 
 // ---------------------------------------------------------------- rows there and back
+// A token is a team's: a power of two of threads, up to a block. A thread has runs of W
+// columns: whole 16-byte vectors, or (SPREAD) elements a team apart, which take any
+// boundary and any length and are whole lines all the same. What hides the memory's
+// latency is threads: each has few loads, all at once, and is soon gone.
 constexpr int kThreads = 128;
+constexpr int kSlots = 8;                                  // of a token at a time
 
-// A row that `rows` names, or -1: what lies outside [0, all) is none.
-template <typename B>
-__device__ __forceinline__ int64_t row_at(const int32_t* rows, int64_t slot, int64_t all, const B& b, int span) {
-    const int64_t r = load_one(rows + slot, b, span, -1);
-    return r < all ? r : -1;
+// Columns of run u of a team's thread.
+template <int W, bool SPREAD>
+__device__ __forceinline__ int64_t column(int u, int i, int lane, int team) {
+    return SPREAD ? (static_cast<int64_t>(u) * W + i) * team + lane : (static_cast<int64_t>(u) * team + lane) * W + i;
+}
+template <typename T, int W, bool SPREAD, typename B>
+__device__ __forceinline__ Pack<T, W> load_columns(const T* row, int u, int lane, int team, int64_t n, const B& b, int span) {
+    if constexpr (!SPREAD) {
+        return load_pack<T, W>(row + column<W, false>(u, 0, lane, team), b, span);
+    } else {
+        Pack<T, W> v = zero_pack<T, W>();
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int64_t c = column<W, true>(u, i, lane, team);
+            if (c < n) v.v[i] = load_one(row + c, b, span, v.v[i]);
+        }
+        return v;
+    }
+}
+template <typename T, int W, bool SPREAD, typename B>
+__device__ __forceinline__ void store_columns(T* row, const Pack<T, W>& v, int u, int lane, int team, int64_t n, const B& b, int span) {
+    if constexpr (!SPREAD) {
+        store_pack<T, W>(row + column<W, false>(u, 0, lane, team), v, b, span);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int64_t c = column<W, true>(u, i, lane, team);
+            if (c < n) store_one(row + c, v.v[i], b, span);
+        }
+    }
 }
 
-// A block has a token and a piece of its columns, held in registers and written to
-// each of the token's k rows. E: an element, or 16 bytes of them (n and strides then
-// count those). Row t k + j of xs is this token's to clear if no slot has it.
-template <typename E>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs p) {
-    constexpr int U = 4;
+// The rows of K slots of a token from slot j0 on: -1 for none, and for what lies outside
+// [0, all).
+template <int K, typename B>
+__device__ __forceinline__ void rows_of(int32_t (&r)[K], const int32_t* rows, int64_t t, int j0, int k, int64_t all, const B& b, int span) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        r[j] = j0 + j < k ? load_one(rows + t * k + j0 + j, b, span, -1) : -1;
+        if (r[j] >= all) r[j] = -1;
+    }
+}
+template <int K, typename B>
+__device__ __forceinline__ void weights_of(float (&w)[K], const float* weights, int64_t t, int j0, int k, const B& b, int span) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j] = weights == nullptr ? 1.0f : (j0 + j < k ? load_one(weights + t * k + j0 + j, b, span, 0.0f) : 0.0f);
+}
+
+// Row t k + j of xs is token t's to clear if no slot has it.
+template <typename T, int W, bool SPREAD>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs p, int team, unsigned pieces) {
+    constexpr int U = 4, K = 4;
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int64_t t = blockIdx.x, all = p.m * p.k;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (kThreads * U) + threadIdx.x;
-    const E* x = static_cast<const E*>(p.x) + t * p.sx;
-    E v[U];
+    const unsigned group = blockIdx.x / pieces;
+    const int lane = threadIdx.x & (team - 1), u0 = static_cast<int>(blockIdx.x - group * pieces) * U;
+    const int64_t t = static_cast<int64_t>(group) * (kThreads / team) + threadIdx.x / team, all = p.m * p.k;
+    if (t >= p.m) return;
+    const T* x = static_cast<const T*>(p.x) + t * p.sx;
+    Pack<T, W> v[U];
+    int32_t r[K];
+    rows_of<K>(r, p.rows, t, 0, p.k, all, p.bnd, 1);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t c = c0 + u * kThreads;
-        v[u] = c < p.n ? load_one(x + c, p.bnd, 0, E{}) : E{};
+        v[u] = zero_pack<T, W>();
+        if (column<W, SPREAD>(u0 + u, 0, lane, team) < p.n) v[u] = load_columns<T, W, SPREAD>(x, u0 + u, lane, team, p.n, p.bnd, 0);
     }
     const int64_t used = load_one(p.offsets + p.experts, p.bnd, 2, 0);
-    for (int j = 0; j < p.k; ++j) {
-        const int64_t r = row_at(p.rows, t * p.k + j, all, p.bnd, 1);
-        if (r >= 0) {
-            E* xs = static_cast<E*>(p.xs) + r * p.sxs;
+    for (int j0 = 0; j0 < p.k; j0 += K) {
+        int32_t next[K];
+        if (j0 + K < p.k) rows_of<K>(next, p.rows, t, j0 + K, p.k, all, p.bnd, 1);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + u * kThreads < p.n) store_one(xs + c0 + u * kThreads, v[u], p.bnd, 3);
-        }
-        if (t * p.k + j >= used) {
-            E* xs = static_cast<E*>(p.xs) + (t * p.k + j) * p.sxs;
+        for (int j = 0; j < K; ++j)
+            if (r[j] >= 0)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + u * kThreads < p.n) store_one(xs + c0 + u * kThreads, E{}, p.bnd, 3);
-        }
+                for (int u = 0; u < U; ++u)
+                    if (column<W, SPREAD>(u0 + u, 0, lane, team) < p.n)
+                        store_columns<T, W, SPREAD>(static_cast<T*>(p.xs) + r[j] * p.sxs, v[u], u0 + u, lane, team, p.n, p.bnd, 3);
+#pragma unroll
+        for (int j = 0; j < K; ++j) r[j] = next[j];
     }
+    if (t * p.k + p.k > used)
+        for (int j = 0; j < p.k; ++j)
+            if (t * p.k + j >= used)
+                for (int u = u0; u < u0 + U; ++u)
+                    if (column<W, SPREAD>(u, 0, lane, team) < p.n)
+                        store_columns<T, W, SPREAD>(static_cast<T*>(p.xs) + (t * p.k + j) * p.sxs, zero_pack<T, W>(), u, lane, team, p.n, p.bnd, 3);
 }
 
-// A block has a token and a piece of its columns; a thread W columns, whose k terms it
-// adds up in fp32 in the order of j, eight loads at a time.
-template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs p) {
-    constexpr int J = 8;
+// Runs of a thread: enough loads for few slots, sums that registers hold.
+__host__ __device__ constexpr int combine_runs(int k) { return k == 1 ? 4 : (k == 2 ? 2 : 1); }
+
+// A thread adds up its columns' k terms in fp32 in the order of j: U runs of K slots are on
+// their way at a time.
+template <typename T, int W, int K, bool SPREAD>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs p, int team, unsigned pieces) {
+    constexpr int U = combine_runs(K);
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int64_t t = blockIdx.x, all = p.m * p.k;
-    const int64_t c = (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x) * W;
-    if (c >= p.n) return;
-    float sum[W];
+    const unsigned group = blockIdx.x / pieces;
+    const int lane = threadIdx.x & (team - 1), u0 = static_cast<int>(blockIdx.x - group * pieces) * U;
+    const int64_t t = static_cast<int64_t>(group) * (kThreads / team) + threadIdx.x / team, all = p.m * p.k;
+    if (t >= p.m) return;
+    float sum[U][W];
 #pragma unroll
-    for (int i = 0; i < W; ++i) sum[i] = 0.0f;
-    if (p.add != nullptr) {
-        const Pack<T, W> a = load_pack<T, W>(static_cast<const T*>(p.add) + t * p.sadd + c, p.bnd, 3);
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) sum[i] = to_f32(a.v[i]);
-    }
-    for (int j0 = 0; j0 < p.k; j0 += J) {
-        Pack<T, W> v[J];
-        float w[J];
+        for (int i = 0; i < W; ++i) sum[u][i] = 0.0f;
+        if (p.add != nullptr && column<W, SPREAD>(u0 + u, 0, lane, team) < p.n) {
+            const Pack<T, W> a = load_columns<T, W, SPREAD>(static_cast<const T*>(p.add) + t * p.sadd, u0 + u, lane, team, p.n, p.bnd, 3);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int64_t r = j0 + j < p.k ? row_at(p.rows, t * p.k + j0 + j, all, p.bnd, 1) : -1;
-            w[j] = r < 0 ? 0.0f : (p.weights != nullptr ? load_one(p.weights + t * p.k + j0 + j, p.bnd, 2, 0.0f) : 1.0f);
-            v[j] = r < 0 ? zero_pack<T, W>() : load_pack<T, W>(static_cast<const T*>(p.ys) + r * p.sys + c, p.bnd, 0);
+            for (int i = 0; i < W; ++i) sum[u][i] = to_f32(a.v[i]);
         }
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int i = 0; i < W; ++i) sum[i] = fmaf(w[j], to_f32(v[j].v[i]), sum[i]);
     }
-    Pack<T, W> o;
+    for (int j0 = 0; j0 < p.k; j0 += K) {
+        int32_t r[K];
+        float w[K];
+        rows_of<K>(r, p.rows, t, j0, p.k, all, p.bnd, 1);
+        weights_of<K>(w, p.weights, t, j0, p.k, p.bnd, 2);
+        Pack<T, W> v[U][K];
 #pragma unroll
-    for (int i = 0; i < W; ++i) o.v[i] = from_f32<T>(sum[i]);
-    store_pack<T, W>(static_cast<T*>(p.y) + t * p.sy + c, o, p.bnd, 4);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (r[j] >= 0 && column<W, SPREAD>(u0 + u, 0, lane, team) < p.n)
+                    v[u][j] = load_columns<T, W, SPREAD>(static_cast<const T*>(p.ys) + r[j] * p.sys, u0 + u, lane, team, p.n, p.bnd, 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (r[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < W; ++i) sum[u][i] = fmaf(w[j], to_f32(v[u][j].v[i]), sum[u][i]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (column<W, SPREAD>(u0 + u, 0, lane, team) < p.n) {
+            Pack<T, W> o;
+#pragma unroll
+            for (int i = 0; i < W; ++i) o.v[i] = from_f32<T>(sum[u][i]);
+            store_columns<T, W, SPREAD>(static_cast<T*>(p.y) + t * p.sy, o, u0 + u, lane, team, p.n, p.bnd, 4);
+        }
 }
 
-// A block has a token: for up to eight of its slots at a time it goes over dy[t] once,
-// writes their rows of dys and sums up their dots.
-template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) combine_back_kernel(const CombineBackArgs p) {
-    constexpr int J = 8;
-    __shared__ float s_sum[J * 32];
+// For up to K of a token's slots at a time a team goes over dy[t] once, writes their rows
+// of dys and sums up their dots. Teams are parts of a warp, or (BLOCK) a block.
+template <typename T, int W, int K, bool SPREAD, bool BLOCK>
+__global__ void __launch_bounds__(kThreads) combine_back_kernel(const CombineBackArgs p, int team) {
+    constexpr int U = K >= 4 ? 1 : 4 / K;
+    __shared__ float s_sum[BLOCK ? K * 32 : 1];
     pdl_launch_dependents();
     pdl_wait_prior();
-    const int64_t t = blockIdx.x, all = p.m * p.k;
-    const T* dy = static_cast<const T*>(p.dy) + t * p.sdy;
+    const int lane = threadIdx.x & (team - 1), runs = static_cast<int>((p.n + team * W - 1) / (team * W));
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / team) + threadIdx.x / team, all = p.m * p.k;
+    const bool here = t < p.m;                             // a warp's teams sum up together
     const int64_t used = load_one(p.offsets + p.experts, p.bnd, 3, 0);
-    for (int j0 = 0; j0 < p.k; j0 += J) {
-        int64_t r[J];
-        float w[J], dot[J];
+    const T* dy = static_cast<const T*>(p.dy) + t * p.sdy;
+    for (int j0 = 0; j0 < p.k; j0 += K) {
+        int32_t r[K];
+        float w[K], dot[K];
+        rows_of<K>(r, p.rows, t, j0, here ? p.k : 0, all, p.bnd, 2);
+        weights_of<K>(w, p.weights, t, j0, here ? p.k : 0, p.bnd, 4);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            r[j] = j0 + j < p.k ? row_at(p.rows, t * p.k + j0 + j, all, p.bnd, 2) : -1;
-            w[j] = r[j] < 0 ? 0.0f : load_one(p.weights + t * p.k + j0 + j, p.bnd, 4, 0.0f);
-            dot[j] = 0.0f;
-        }
-        for (int64_t c = static_cast<int64_t>(threadIdx.x) * W; c < p.n; c += kThreads * W) {
-            const Pack<T, W> g = load_pack<T, W>(dy + c, p.bnd, 0);
-            Pack<T, W> v[J];
+        for (int j = 0; j < K; ++j) dot[j] = 0.0f;
+        for (int u0 = 0; u0 < runs && here; u0 += U) {
+            Pack<T, W> g[U], v[U][K];
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (r[j] >= 0) v[j] = load_pack<T, W>(static_cast<const T*>(p.ys) + r[j] * p.sys + c, p.bnd, 1);
+            for (int u = 0; u < U; ++u)
+                if (column<W, SPREAD>(u0 + u, 0, lane, team) < p.n) {
+                    g[u] = load_columns<T, W, SPREAD>(dy, u0 + u, lane, team, p.n, p.bnd, 0);
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (r[j] >= 0) {
-                    Pack<T, W> o;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        const float d = to_f32(g.v[i]);
-                        dot[j] = fmaf(d, to_f32(v[j].v[i]), dot[j]);
-                        o.v[i] = from_f32<T>(d * w[j]);
-                    }
-                    store_pack<T, W>(static_cast<T*>(p.dys) + r[j] * p.sdys + c, o, p.bnd, 5);
+                    for (int j = 0; j < K; ++j)
+                        if (r[j] >= 0) v[u][j] = load_columns<T, W, SPREAD>(static_cast<const T*>(p.ys) + r[j] * p.sys, u0 + u, lane, team, p.n, p.bnd, 1);
                 }
 #pragma unroll
-            for (int j = 0; j < J; ++j)
-                if (j0 + j < p.k && t * p.k + j0 + j >= used)
-                    store_pack<T, W>(static_cast<T*>(p.dys) + (t * p.k + j0 + j) * p.sdys + c, zero_pack<T, W>(), p.bnd, 5);
-        }
-        __syncthreads();                                   // the last slots' sums have been read
-        sum_over_row<J, false>(dot, s_sum);
+            for (int u = 0; u < U; ++u)
+                if (column<W, SPREAD>(u0 + u, 0, lane, team) < p.n)
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-            if (threadIdx.x == j && j0 + j < p.k) store_one(p.dweights + t * p.k + j0 + j, dot[j], p.bnd, 6);
+                    for (int j = 0; j < K; ++j)
+                        if (r[j] >= 0) {
+                            Pack<T, W> o;
+#pragma unroll
+                            for (int i = 0; i < W; ++i) {
+                                const float d = to_f32(g[u].v[i]);
+                                dot[j] = fmaf(d, to_f32(v[u][j].v[i]), dot[j]);
+                                o.v[i] = from_f32<T>(d * w[j]);
+                            }
+                            store_columns<T, W, SPREAD>(static_cast<T*>(p.dys) + r[j] * p.sdys, o, u0 + u, lane, team, p.n, p.bnd, 5);
+                        }
+        }
+        if constexpr (BLOCK) {
+            if (j0 > 0) __syncthreads();                   // the last sums have been read
+            sum_over_row<K, false>(dot, s_sum);
+        } else {
+            for (int o = team >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < K; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+        }
+        if (here && lane == 0)
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (j0 + j < p.k) store_one(p.dweights + t * p.k + j0 + j, dot[j], p.bnd, 6);
     }
+    if (here && t * p.k + p.k > used)
+        for (int j = 0; j < p.k; ++j)
+            if (t * p.k + j >= used)
+                for (int u = 0; u < runs; ++u)
+                    if (column<W, SPREAD>(u, 0, lane, team) < p.n)
+                        store_columns<T, W, SPREAD>(static_cast<T*>(p.dys) + (t * p.k + j) * p.sdys, zero_pack<T, W>(), u, lane, team, p.n, p.bnd, 5);
 }
 
-unsigned pieces(int64_t n, int64_t each) { return static_cast<unsigned>((n + each - 1) / each); }
+// The team for rows of n columns, `most` threads at most.
+int team_of(int64_t n, int w, int most) {
+    int team = 1;
+    while (team < most && static_cast<int64_t>(team) * w < n) team *= 2;
+    return team;
+}
+// Pieces of a row of n columns, and blocks for m tokens: those of one token follow one
+// another, so that a row's pieces are on their way together (the other way round 4096 x 8
+// rows of 7168 took 171 us to combine).
+unsigned pieces_of(int64_t n, int w, int team, int runs) {
+    const int64_t each = static_cast<int64_t>(team) * w * runs;
+    return static_cast<unsigned>((n + each - 1) / each);
+}
+bool blocks_of(int64_t m, int team, unsigned pieces, dim3& grid) {
+    const int64_t per = kThreads / team, blocks = (m + per - 1) / per * pieces;
+    grid = dim3(static_cast<unsigned>(blocks));
+    return blocks < (int64_t(1) << 31);
+}
 
+template <typename T, bool SPREAD>
+cudaError_t dispatch_s(const DispatchArgs& a, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    const int team = team_of(a.n, W, kThreads);
+    const unsigned pieces = pieces_of(a.n, W, team, 4);
+    dim3 grid;
+    if (!blocks_of(a.m, team, pieces, grid)) return cudaErrorInvalidValue;
+    return launch_after(dispatch_kernel<T, W, SPREAD>, grid, kThreads, 0, st, a, team, pieces);
+}
+template <typename T, int K, bool SPREAD>
+cudaError_t combine_k(const CombineArgs& a, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    const int team = team_of(a.n, W, kThreads);
+    const unsigned pieces = pieces_of(a.n, W, team, combine_runs(K));
+    dim3 grid;
+    if (!blocks_of(a.m, team, pieces, grid)) return cudaErrorInvalidValue;
+    return launch_after(combine_kernel<T, W, K, SPREAD>, grid, kThreads, 0, st, a, team, pieces);
+}
+template <typename T, int K, bool SPREAD>
+cudaError_t combine_back_k(const CombineBackArgs& a, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    if (a.n > 32 * 4 * W)
+        return launch_after(combine_back_kernel<T, W, K, SPREAD, true>, dim3(static_cast<unsigned>(a.m)), kThreads, 0, st, a, kThreads);
+    const int team = team_of(a.n, W, 32), per = kThreads / team;
+    return launch_after(combine_back_kernel<T, W, K, SPREAD, false>, dim3(static_cast<unsigned>((a.m + per - 1) / per)), kThreads, 0, st, a, team);
+}
+// Slots at a time: k's own number where it is small.
+#define QL_BY_SLOTS(F, T, SPREAD, a, ...)                               \
+    ((a).k == 1 ? F<T, 1, SPREAD>(a, __VA_ARGS__)                       \
+                : ((a).k == 2 ? F<T, 2, SPREAD>(a, __VA_ARGS__)         \
+                              : ((a).k <= 4 ? F<T, 4, SPREAD>(a, __VA_ARGS__) : F<T, kSlots, SPREAD>(a, __VA_ARGS__))))
+
+template <typename T>
+cudaError_t dispatch_t(const DispatchArgs& a, cudaStream_t st) {
+    constexpr int W = 16 / sizeof(T);
+    const bool vec = a.n % W == 0 && rows_aligned(a.x, sizeof(T), a.sx, a.m, 16) && rows_aligned(a.xs, sizeof(T), a.sxs, a.m * a.k, 16);
+    return vec ? dispatch_s<T, false>(a, st) : dispatch_s<T, true>(a, st);
+}
 template <typename T>
 cudaError_t combine_t(const CombineArgs& a, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const bool vec = a.n % W == 0 && rows_aligned(a.ys, sizeof(T), a.sys, a.m * a.k, 16) && rows_aligned(a.y, sizeof(T), a.sy, a.m, 16) &&
                      (a.add == nullptr || rows_aligned(a.add, sizeof(T), a.sadd, a.m, 16));
-    if (vec)
-        return launch_after(combine_kernel<T, W>, dim3(static_cast<unsigned>(a.m), pieces(a.n, kThreads * W)), kThreads, 0, st, a);
-    return launch_after(combine_kernel<T, 1>, dim3(static_cast<unsigned>(a.m), pieces(a.n, kThreads)), kThreads, 0, st, a);
+    return vec ? QL_BY_SLOTS(combine_k, T, false, a, st) : QL_BY_SLOTS(combine_k, T, true, a, st);
 }
 template <typename T>
 cudaError_t combine_back_t(const CombineBackArgs& a, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const bool vec = a.n % W == 0 && rows_aligned(a.ys, sizeof(T), a.sys, a.m * a.k, 16) && rows_aligned(a.dy, sizeof(T), a.sdy, a.m, 16) &&
                      rows_aligned(a.dys, sizeof(T), a.sdys, a.m * a.k, 16);
-    if (vec) return launch_after(combine_back_kernel<T, W>, dim3(static_cast<unsigned>(a.m)), kThreads, 0, st, a);
-    return launch_after(combine_back_kernel<T, 1>, dim3(static_cast<unsigned>(a.m)), kThreads, 0, st, a);
-}
-template <typename E>
-cudaError_t dispatch_e(DispatchArgs a, int64_t per, cudaStream_t st) {
-    a.n /= per;
-    a.sx /= per;
-    a.sxs /= per;
-    return launch_after(dispatch_kernel<E>, dim3(static_cast<unsigned>(a.m), pieces(a.n, kThreads * 4)), kThreads, 0, st, a);
+    return vec ? QL_BY_SLOTS(combine_back_k, T, false, a, st) : QL_BY_SLOTS(combine_back_k, T, true, a, st);
 }
 
 }  // namespace
@@ -297,18 +427,10 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
     return launch_after(plan_place_kernel, dim3(chunks), kPlanThreads, 0, st, a);
 }
 
-cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t st, int num_sms) {
-    (void)num_sms;
-    if ((a.n * a.es) % 16 == 0 && rows_aligned(a.x, a.es, a.sx, a.m, 16) && rows_aligned(a.xs, a.es, a.sxs, a.m * a.k, 16)) {
-        DispatchArgs v = a;
-        if (a.m <= 1) v.sx = 0;
-        if (a.m * a.k <= 1) v.sxs = 0;
-        return dispatch_e<uint4>(v, 16 / a.es, st);
-    }
-    return a.es == 2 ? dispatch_e<uint16_t>(a, 1, st) : dispatch_e<uint32_t>(a, 1, st);
+cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t st) {
+    return a.es == 2 ? dispatch_t<__nv_bfloat16>(a, st) : dispatch_t<float>(a, st);
 }
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st, int num_sms) {
-    (void)num_sms;
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
     return a.bf16 ? combine_t<__nv_bfloat16>(a, st) : combine_t<float>(a, st);
 }
 cudaError_t launch_combine_back(const CombineBackArgs& a, cudaStream_t st) {
