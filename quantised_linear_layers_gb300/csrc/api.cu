@@ -1249,7 +1249,7 @@ ql_status expert_combine(const void* ys, ql_dtype dtype, int64_t ys_stride_m, co
     a.bnd.s[3] = ql::span_of(add, bytes_of(dtype), m, add_stride_m, n, 1);
     a.bnd.s[4] = ql::span_of(y, bytes_of(dtype), m, y_stride_m, n, 1);
     a.bnd.status = di.status;
-    return from_cuda(ql::launch_combine(a, reinterpret_cast<cudaStream_t>(stream)));
+    return from_cuda(ql::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), di.num_sms));
 }
 
 ql_status expert_combine_backward(const void* dy, ql_dtype dtype, int64_t dy_stride_m, const void* ys, int64_t ys_stride_m,
@@ -1291,7 +1291,7 @@ ql_status expert_combine_backward(const void* dy, ql_dtype dtype, int64_t dy_str
     a.bnd.s[5] = ql::span_of(dys, bytes_of(dtype), m * k, dys_stride_m, n, 1);
     a.bnd.s[6] = ql::span_of(dweights, 4, m * k, 1);
     a.bnd.status = di.status;
-    return from_cuda(ql::launch_combine_back(a, st));
+    return from_cuda(ql::launch_combine_back(a, st, di.num_sms));
 }
 
 ql_status ql_set_num_sms(int num_sms) {

@@ -1,8 +1,8 @@
 // The exchange of rows with the experts: the order of the slots (token, j) by
 // expert (a stable counting sort), rows to their places, and the weighted sums
 // back, with the gradients of both.
+#include "gemm.cuh"
 #include "route.cuh"
-
 #include "rows.cuh"
 
 namespace ql {
@@ -333,6 +333,138 @@ __global__ void __launch_bounds__(kThreads) combine_back_kernel(const CombineBac
                         store_columns<T, W, SPREAD>(static_cast<T*>(p.dys) + (t * p.k + j) * p.sdys, zero_pack<T, W>(), u, lane, team, p.n, p.bnd, 5);
 }
 
+// ---------------------------------------------------------------- many tokens
+// The same for many tokens: a team is a warp or a block and goes from token to token, with
+// the runs to come on their way into a ring of S in shared memory, in which each thread
+// copies and reads only what is its own. A token's rows are known one token ahead.
+constexpr int kRingThreads = 256;
+constexpr int ring_stages(int k) { return k >= 8 ? 3 : (k >= 4 ? 5 : 8); }
+
+struct RingArgs {
+    const void *one, *many;    // a row of each token: add (or null), dy; the experts' rows: ys
+    int64_t m, n, s_one, s_many;
+    int k;
+    const int32_t* rows;
+    const float* weights;      // or null: 1
+    void* out;                 // y, or dys
+    int64_t s_out;
+    const int32_t* offsets;    // back: past offsets[experts] dys is zero
+    int experts;
+    float* dweights;
+    BoundsOf<7> bnd;           // one, many, rows, weights, out, offsets, dweights
+};
+
+template <typename T, int K, bool BACK, bool BLOCK>
+__global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const RingArgs p) {
+    constexpr int W = 16 / sizeof(T), S = ring_stages(K), L = K + 1, TEAM = BLOCK ? kRingThreads : 32;
+    extern __shared__ __align__(16) uint8_t s_ring[];      // [S][L][threads] runs: the token's, the experts'
+    __shared__ float s_sum[2][BACK && BLOCK ? K * 32 : 1];
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    const int lane = threadIdx.x & (TEAM - 1), runs = static_cast<int>((p.n + TEAM * W - 1) / (TEAM * W));
+    const int64_t all = p.m * p.k, step = static_cast<int64_t>(gridDim.x) * (kRingThreads / TEAM);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRingThreads / TEAM) + threadIdx.x / TEAM;
+    uint8_t* mine = s_ring + threadIdx.x * 16;
+    auto slot = [&](int s, int l) { return mine + (s * L + l) * kRingThreads * 16; };
+    const int64_t used = BACK ? load_one(p.offsets + p.experts, p.bnd, 5, 0) : 0;
+
+    // the copies' place in the sequence of runs
+    int64_t f_token = first;
+    int f_run = 0;
+    int32_t f_rows[K], f_next[K];
+    auto rows_at = [&](int32_t (&r)[K], int64_t t) { rows_of<K>(r, p.rows, t, 0, t < p.m ? p.k : 0, all, p.bnd, 2); };
+    rows_at(f_rows, first);
+    rows_at(f_next, first + step);
+    auto fetch = [&](int s) {
+        const int64_t c = (static_cast<int64_t>(f_run) * TEAM + lane) * W;
+        if (f_token < p.m && c < p.n) {
+            const T* one = static_cast<const T*>(p.one) + f_token * p.s_one + c;
+            if (p.one != nullptr && QL_IN(p.bnd, 0, one, 16)) copy_async<16>(slot(s, 0), one);
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (f_rows[j] >= 0) {
+                    const T* many = static_cast<const T*>(p.many) + f_rows[j] * p.s_many + c;
+                    if (QL_IN(p.bnd, 1, many, 16)) copy_async<16>(slot(s, 1 + j), many);
+                }
+        }
+        copy_commit();                                     // a group for every run, also past the last
+        if (++f_run == runs) {
+            f_run = 0;
+            f_token += step;
+#pragma unroll
+            for (int j = 0; j < K; ++j) f_rows[j] = f_next[j];
+            rows_at(f_next, f_token + step);
+        }
+    };
+    for (int s = 0; s < S; ++s) fetch(s);
+    int32_t next[K];
+    float w_next[K];
+    rows_at(next, first);
+    weights_of<K>(w_next, p.weights, first, 0, first < p.m ? p.k : 0, p.bnd, 3);
+    int s = 0, turn = 0;
+    for (int64_t t = first; t < p.m; t += step) {
+        int32_t r[K];
+        float w[K], dot[K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            r[j] = next[j];
+            w[j] = w_next[j];
+            dot[j] = 0.0f;
+        }
+        rows_at(next, t + step);
+        weights_of<K>(w_next, p.weights, t + step, 0, t + step < p.m ? p.k : 0, p.bnd, 3);
+        for (int u = 0; u < runs; ++u) {
+            copy_wait<S - 1>();
+            const int64_t c = (static_cast<int64_t>(u) * TEAM + lane) * W;
+            if (c < p.n) {
+                Pack<T, W> one = zero_pack<T, W>();
+                if (p.one != nullptr) one = *reinterpret_cast<const Pack<T, W>*>(slot(s, 0));
+                float sum[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) sum[i] = to_f32(one.v[i]);
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (r[j] >= 0) {
+                        const Pack<T, W> v = *reinterpret_cast<const Pack<T, W>*>(slot(s, 1 + j));
+                        if constexpr (BACK) {
+                            Pack<T, W> o;
+#pragma unroll
+                            for (int i = 0; i < W; ++i) {
+                                dot[j] = fmaf(sum[i], to_f32(v.v[i]), dot[j]);
+                                o.v[i] = from_f32<T>(sum[i] * w[j]);
+                            }
+                            store_pack<T, W>(static_cast<T*>(p.out) + r[j] * p.s_out + c, o, p.bnd, 4);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < W; ++i) sum[i] = fmaf(w[j], to_f32(v.v[i]), sum[i]);
+                        }
+                    }
+                if constexpr (!BACK) {
+                    Pack<T, W> o;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) o.v[i] = from_f32<T>(sum[i]);
+                    store_pack<T, W>(static_cast<T*>(p.out) + t * p.s_out + c, o, p.bnd, 4);
+                }
+            }
+            fetch(s);                                      // what it copies over has been read
+            if (++s == S) s = 0;
+        }
+        if constexpr (BACK) {
+            sum_over_row<K, !BLOCK>(dot, s_sum[turn]);
+            turn ^= 1;                                     // the next token's sums go elsewhere
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (j < p.k) store_one(p.dweights + t * p.k + j, dot[j], p.bnd, 6);
+            if (t * p.k + p.k > used)
+                for (int j = 0; j < p.k; ++j)
+                    if (t * p.k + j >= used)
+                        for (int64_t c = lane * W; c < p.n; c += TEAM * W)
+                            store_pack<T, W>(static_cast<T*>(p.out) + (t * p.k + j) * p.s_out + c, zero_pack<T, W>(), p.bnd, 4);
+        }
+    }
+}
+
 // The team for rows of n columns, `most` threads at most.
 int team_of(int64_t n, int w, int most) {
     int team = 1;
@@ -384,6 +516,32 @@ cudaError_t combine_back_k(const CombineBackArgs& a, cudaStream_t st) {
                 : ((a).k == 2 ? F<T, 2, SPREAD>(a, __VA_ARGS__)         \
                               : ((a).k <= 4 ? F<T, 4, SPREAD>(a, __VA_ARGS__) : F<T, kSlots, SPREAD>(a, __VA_ARGS__))))
 
+// The ring for calls with several tokens to a team: true if it was launched, with e.
+template <typename T, int K, bool BACK, bool BLOCK>
+bool ring_b(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
+    constexpr int TEAM = BLOCK ? kRingThreads : 32, smem = ring_stages(K) * (K + 1) * kRingThreads * 16;
+    auto kern = exchange_ring_kernel<T, K, BACK, BLOCK>;
+    const int64_t most = static_cast<int64_t>(num_sms) * 2;
+    if (a.m * TEAM < 4 * most * kRingThreads) return false;
+    e = smem > 46 * 1024 ? ensure_smem_attr(reinterpret_cast<const void*>(kern), smem) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_after(kern, dim3(static_cast<unsigned>(most)), kRingThreads, smem, st, a);
+    return true;
+}
+template <typename T, int K, bool BACK>
+bool ring_k(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
+    constexpr int W = 16 / sizeof(T);
+    return a.n >= kRingThreads * W ? ring_b<T, K, BACK, true>(a, st, num_sms, e) : ring_b<T, K, BACK, false>(a, st, num_sms, e);
+}
+template <typename T, bool BACK>
+bool ring(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
+    constexpr int W = 16 / sizeof(T);
+    if (a.k > 8 || a.n < 32 * W) return false;
+    if (a.k == 1) return ring_k<T, 1, BACK>(a, st, num_sms, e);
+    if (a.k == 2) return ring_k<T, 2, BACK>(a, st, num_sms, e);
+    if (a.k <= 4) return ring_k<T, 4, BACK>(a, st, num_sms, e);
+    return ring_k<T, 8, BACK>(a, st, num_sms, e);
+}
+
 template <typename T>
 cudaError_t dispatch_t(const DispatchArgs& a, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
@@ -391,17 +549,27 @@ cudaError_t dispatch_t(const DispatchArgs& a, cudaStream_t st) {
     return vec ? dispatch_s<T, false>(a, st) : dispatch_s<T, true>(a, st);
 }
 template <typename T>
-cudaError_t combine_t(const CombineArgs& a, cudaStream_t st) {
+cudaError_t combine_t(const CombineArgs& a, cudaStream_t st, int num_sms) {
     constexpr int W = 16 / sizeof(T);
     const bool vec = a.n % W == 0 && rows_aligned(a.ys, sizeof(T), a.sys, a.m * a.k, 16) && rows_aligned(a.y, sizeof(T), a.sy, a.m, 16) &&
                      (a.add == nullptr || rows_aligned(a.add, sizeof(T), a.sadd, a.m, 16));
+    cudaError_t e;
+    if (vec && ring<T, false>(RingArgs{a.add, a.ys, a.m, a.n, a.sadd, a.sys, a.k, a.rows, a.weights, a.y, a.sy, nullptr, 0, nullptr,
+                                       {{a.bnd.s[3], a.bnd.s[0], a.bnd.s[1], a.bnd.s[2], a.bnd.s[4], Span{0, 0}, Span{0, 0}}, a.bnd.status}},
+                              st, num_sms, e))
+        return e;
     return vec ? QL_BY_SLOTS(combine_k, T, false, a, st) : QL_BY_SLOTS(combine_k, T, true, a, st);
 }
 template <typename T>
-cudaError_t combine_back_t(const CombineBackArgs& a, cudaStream_t st) {
+cudaError_t combine_back_t(const CombineBackArgs& a, cudaStream_t st, int num_sms) {
     constexpr int W = 16 / sizeof(T);
     const bool vec = a.n % W == 0 && rows_aligned(a.ys, sizeof(T), a.sys, a.m * a.k, 16) && rows_aligned(a.dy, sizeof(T), a.sdy, a.m, 16) &&
                      rows_aligned(a.dys, sizeof(T), a.sdys, a.m * a.k, 16);
+    cudaError_t e;
+    if (vec && ring<T, true>(RingArgs{a.dy, a.ys, a.m, a.n, a.sdy, a.sys, a.k, a.rows, a.weights, a.dys, a.sdys, a.offsets, a.experts, a.dweights,
+                                      {{a.bnd.s[0], a.bnd.s[1], a.bnd.s[2], a.bnd.s[4], a.bnd.s[5], a.bnd.s[3], a.bnd.s[6]}, a.bnd.status}},
+                             st, num_sms, e))
+        return e;
     return vec ? QL_BY_SLOTS(combine_back_k, T, false, a, st) : QL_BY_SLOTS(combine_back_k, T, true, a, st);
 }
 
@@ -430,11 +598,11 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
 cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t st) {
     return a.es == 2 ? dispatch_t<__nv_bfloat16>(a, st) : dispatch_t<float>(a, st);
 }
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st) {
-    return a.bf16 ? combine_t<__nv_bfloat16>(a, st) : combine_t<float>(a, st);
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st, int num_sms) {
+    return a.bf16 ? combine_t<__nv_bfloat16>(a, st, num_sms) : combine_t<float>(a, st, num_sms);
 }
-cudaError_t launch_combine_back(const CombineBackArgs& a, cudaStream_t st) {
-    return a.bf16 ? combine_back_t<__nv_bfloat16>(a, st) : combine_back_t<float>(a, st);
+cudaError_t launch_combine_back(const CombineBackArgs& a, cudaStream_t st, int num_sms) {
+    return a.bf16 ? combine_back_t<__nv_bfloat16>(a, st, num_sms) : combine_back_t<float>(a, st, num_sms);
 }
 
 }  // namespace ql

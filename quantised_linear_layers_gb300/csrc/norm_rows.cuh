@@ -173,25 +173,6 @@ inline int team_of(int64_t n, int e, bool edge, int w) { return static_cast<int>
 
 
 // ---------------------------------------------------------------- rows through shared memory
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
-    if constexpr (BYTES > 16) {
-        copy_async<16>(to, from);
-        copy_async<BYTES - 16>(static_cast<uint8_t*>(to) + 16, static_cast<const uint8_t*>(from) + 16);
-    } else if constexpr (BYTES == 16) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
-    } else {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
-    }
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most `stages` - 1 of the thread's groups are on their way.
-__device__ __forceinline__ void copy_wait(int stages) {
-    if (stages >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
 // A run into a thread's own place in shared memory. A run that sticks out of the row is
 // copied whole where that stays between the tensor's first and last element, [lo, hi):
 // mask_run takes out what is other rows'. At those ends it goes element by element.

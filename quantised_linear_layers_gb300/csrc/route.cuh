@@ -107,7 +107,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
 cudaError_t launch_route_back(const RouteBackArgs& a, cudaStream_t st);
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st);
 cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t st);
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st);
-cudaError_t launch_combine_back(const CombineBackArgs& a, cudaStream_t st);
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t st, int num_sms);
+cudaError_t launch_combine_back(const CombineBackArgs& a, cudaStream_t st, int num_sms);
 
 }  // namespace ql

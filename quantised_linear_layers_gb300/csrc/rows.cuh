@@ -114,6 +114,30 @@ __device__ __forceinline__ void sum_over_row(float (&v)[N], float* s) {
     }
 }
 
+// Asynchronous copies into a thread's own place in shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    if constexpr (BYTES > 16) {
+        copy_async<16>(to, from);
+        copy_async<BYTES - 16>(static_cast<uint8_t*>(to) + 16, static_cast<const uint8_t*>(from) + 16);
+    } else if constexpr (BYTES == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES) : "memory");
+    }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of the thread's groups are on their way; `stages` - 1 of them.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copy_wait(int stages) {
+    if (stages >= 4) copy_wait<3>();
+    else if (stages == 3) copy_wait<2>();
+    else if (stages == 2) copy_wait<1>();
+    else copy_wait<0>();
+}
 // Launch with programmatic stream serialization: the kernel may start before its
 // predecessor ends and waits for it (griddepcontrol.wait) before its first access.
 template <typename... KArgs, typename... Args>
