@@ -10,7 +10,7 @@ namespace {
 
 // ---------------------------------------------------------------- plan
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanRoom = kRouteMaxExperts + 1;            // and a place for no expert
+constexpr int kPlanRoom = kRouteMaxExperts + 2;            // and a place for no expert
 
 // The expert of a slot; `experts` for none.
 __device__ __forceinline__ int expert_of(const PlanArgs& p, int64_t slot) {
@@ -40,13 +40,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanArgs
 // the chunk's slots, so the order among an expert's slots is the slots' own. Every
 // chunk adds up the counts of all of them: no chunk waits for another.
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs p) {
-    __shared__ uint16_t s_warp[kPlanWarps][kPlanRoom];     // slots of a warp, then of the warps before
+    __shared__ __align__(16) uint16_t s_warp[kPlanWarps][kPlanRoom];   // slots of a warp, then of the warps before
     __shared__ int s_total[kRouteMaxExperts], s_before[kRouteMaxExperts];
     __shared__ int s_sum[kPlanWarps];
     pdl_launch_dependents();
     pdl_wait_prior();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kPlanWarps * kPlanRoom; i += kPlanThreads) (&s_warp[0][0])[i] = 0;
+    for (int i = lane; i < (p.experts + 2) / 2; i += 32) reinterpret_cast<uint32_t*>(s_warp[warp])[i] = 0;
     for (int e = threadIdx.x; e < kRouteMaxExperts; e += kPlanThreads) s_total[e] = s_before[e] = 0;
     __syncthreads();
     const int64_t run = p.chunk / kPlanWarps;              // a multiple of 32
@@ -61,12 +61,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.experts; e += kPlanThreads) {
-        int sum = 0;
-#pragma unroll 8
+        int c[kPlanWarps], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; ++w) c[w] = s_warp[w][e];
+#pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) {
-            const int c = s_warp[w][e];
             s_warp[w][e] = static_cast<uint16_t>(sum);
-            sum += c;
+            sum += c[w];
         }
         if (p.counts == nullptr) s_total[e] = sum;         // one chunk
     }
@@ -97,8 +98,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanArgs
     }
     if (lane == 31) s_sum[warp] = sum;
     __syncthreads();
-    int ahead = 0;
-    for (int w = 0; w < warp; ++w) ahead += s_sum[w];
+    int ahead = lane < warp ? s_sum[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
     const int start = ahead + sum - mine;
     if (threadIdx.x < p.experts) s_before[threadIdx.x] += start;
     if (blockIdx.x == 0 && threadIdx.x <= p.experts) store_one(p.offsets + threadIdx.x, start, p.bnd, 1);
@@ -357,7 +359,7 @@ struct RingArgs {
 template <typename T, int K, bool BACK, bool BLOCK>
 __global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const RingArgs p) {
     constexpr int W = 16 / sizeof(T), S = ring_stages(K), L = K + 1, TEAM = BLOCK ? kRingThreads : 32;
-    extern __shared__ __align__(16) uint8_t s_ring[];      // [S][L][threads] runs: the token's, the experts'
+    extern __shared__ __align__(16) uint8_t s_ring[];      // [S][L][threads] runs: the token's if there is one, the experts'
     __shared__ float s_sum[2][BACK && BLOCK ? K * 32 : 1];
     pdl_launch_dependents();
     pdl_wait_prior();
@@ -516,21 +518,25 @@ cudaError_t combine_back_k(const CombineBackArgs& a, cudaStream_t st) {
                 : ((a).k == 2 ? F<T, 2, SPREAD>(a, __VA_ARGS__)         \
                               : ((a).k <= 4 ? F<T, 4, SPREAD>(a, __VA_ARGS__) : F<T, kSlots, SPREAD>(a, __VA_ARGS__))))
 
-// The ring for calls with several tokens to a team: true if it was launched, with e.
-template <typename T, int K, bool BACK, bool BLOCK>
-bool ring_b(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
-    constexpr int TEAM = BLOCK ? kRingThreads : 32, smem = ring_stages(K) * (K + 1) * kRingThreads * 16;
-    auto kern = exchange_ring_kernel<T, K, BACK, BLOCK>;
-    const int64_t most = static_cast<int64_t>(num_sms) * 2;
-    if (a.m * TEAM < 4 * most * kRingThreads) return false;
-    e = smem > 46 * 1024 ? ensure_smem_attr(reinterpret_cast<const void*>(kern), smem) : cudaSuccess;
-    if (e == cudaSuccess) e = launch_after(kern, dim3(static_cast<unsigned>(most)), kRingThreads, smem, st, a);
-    return true;
-}
+// Two blocks of ring on every SM, with a token to every warp at least; with fewer, a
+// token to a block if it has work for one. Measured, ring by warps / by blocks / no ring, us:
+//   sums       4096 x 8 of 7168 88 / 85 / 136, 4096 x 2 of 4096 18.7 / 22.9 / 21.9, 16384 x 1 of 4096 51 / 66 / 53,
+//              8192 x 2 of 1024 12.7 / - / 18.5
+//   gradients  163 / 163 / 177, 30.2 / 35.1 / 39.4, 71 / 100 / 116, 17.0 / - / 19.4
+// fewer tokens, by blocks / no ring:
+//   sums       1500 x 8 of 7168 34 / 52, 400 x 8 of 7168 14.4 / 16.8, 512 x 8 of 4096 10.2 / 12.6, 2400 x 2 of 8192 22.4 / 25.0,
+//              1024 x 2 of 4096 7.3 / 5.6
+//   gradients  63 / 73, 20.2 / 21.3, 15.5 / 21.2, 32.4 / 41.8, 12.0 / 12.4
 template <typename T, int K, bool BACK>
 bool ring_k(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
-    constexpr int W = 16 / sizeof(T);
-    return a.n >= kRingThreads * W ? ring_b<T, K, BACK, true>(a, st, num_sms, e) : ring_b<T, K, BACK, false>(a, st, num_sms, e);
+    constexpr int smem = ring_stages(K) * (K + 1) * kRingThreads * 16;
+    const int64_t blocks = static_cast<int64_t>(num_sms) * 2;
+    const bool by_warps = a.m >= blocks * (kRingThreads / 32);
+    if (!by_warps && (a.m < blocks || a.k * a.n * static_cast<int64_t>(sizeof(T)) < 32 * 1024)) return false;
+    auto kern = by_warps ? exchange_ring_kernel<T, K, BACK, false> : exchange_ring_kernel<T, K, BACK, true>;
+    e = smem > 46 * 1024 ? ensure_smem_attr(reinterpret_cast<const void*>(kern), smem) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_after(kern, dim3(static_cast<unsigned>(blocks)), kRingThreads, smem, st, a);
+    return true;
 }
 template <typename T, bool BACK>
 bool ring(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
