@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(const NormBackArg
         for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
             float w[1];
             load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 4);
-            const float g = to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))) * w[0];
+            const float g = __fmul_rn(to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))), w[0]);
             c[0] += g;
             c[1] = fmaf(g, (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd, c[1]);
         }
@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(const NormBackArg
         for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
             float w[1];
             load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 4);
-            const float g = to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))) * w[0];
+            const float g = __fmul_rn(to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))), w[0]);
             const float h = (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd;
-            store_one(dx + i, from_f32<T>(rstd * (g - c1 - h * c2)), p.bnd, 5);
+            store_one(dx + i, from_f32<T>(rstd * fmaf(-h, c2, g - c1)), p.bnd, 5);
         }
     }
 }

@@ -661,6 +661,13 @@ def fp4_linear_backward(dy: torch.Tensor, wt: FP4Tensor | None, x_cols: FP4Tenso
 # ---------------------------------------------------------------------------
 # Around the experts' products: layer norm, routing and the exchange of rows
 # ---------------------------------------------------------------------------
+def _refuse_forward_mode(what: str, *tensors: torch.Tensor | None) -> None:
+    """The calls go past autograd, which would refuse (the level by itself first: it is quick)."""
+    from torch.autograd import forward_ad
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{what} has no forward-mode derivatives")
+
+
 def _type_code(dtype: torch.dtype | None) -> int:
     if dtype is None:
         return 2
