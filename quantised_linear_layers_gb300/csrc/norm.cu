@@ -353,7 +353,7 @@ constexpr int kLeastRows = 6;
 template <typename T, typename O, int E>
 bool rows_e(const NormArgs& a, bool whole, cudaStream_t st, int num_sms, cudaError_t& e) {
     constexpr int W = 16 / sizeof(T);
-    Teams f;
+    Teams f{};
     f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
     const bool y_vec = same_boundary(f.at, boundary_of(a.y, sizeof(O), a.sy, a.m, W)), w_vec = aligned_to(a.w, 16) && aligned_to(a.b, 16);
     auto kern = whole ? norm_rows_kernel<T, O, E, false> : norm_rows_kernel<T, O, E, true>;

@@ -13,9 +13,28 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRowThreads = 512;          // of a block with whole rows
+constexpr int kCluster = 8;               // blocks that join their sums themselves
 constexpr int64_t kSms = 152;             // for sizes that a caller asks for without a device
 
 // ---------------------------------------------------------------- rows of up to 16368 columns
+// The sums of a cluster's blocks, V of the 2 n columns at a time (V divides 2 n).
+template <int V>
+__device__ __forceinline__ void join_columns(const NormBackArgs& p, int n, int first, int step) {
+    for (int c = first * V; c < 2 * n; c += step * V) {
+        Pack<float, V> v[kCluster];
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) v[i] = load_pack<float, V>(p.part + static_cast<int64_t>(i) * 2 * n + c, p.bnd, 6);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kCluster; ++i) sum += v[i].v[k];
+            if (c + k < n) store_one(p.dw + c + k, sum, p.bnd, 7);
+            else store_one(p.db + c + k - n, sum, p.bnd, 8);
+        }
+    }
+}
+
 // With d = x - mean, q = dy rstd and g = q w (that is rstd dy w):
 //   dx = g - d rstd^2 sum(g d) / n - sum(g) / n,  dw += q d,  db += dy
 // Elements past a row's ends have x = dy = w = 0 and add nothing.
@@ -170,33 +189,47 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
         rstd = rstd2;
     }
     if (p.dw == nullptr) return;
-    // the block's teams one after the other, in the rows' room
-    ulonglong2* sum = reinterpret_cast<ulonglong2*>(s_mem) + t;           // [E / 2] pairs of dw, then of db: + i * team
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
     if (f.teams > 1) {
+        // the block's teams in the rows' room: [team][E / 2][threads] pairs of dw and db
+        ulonglong2* sums = reinterpret_cast<ulonglong2*>(s_mem);
         asm volatile("cp.async.wait_all;" ::: "memory");
-        for (int i = 0; i < f.teams; ++i) {
-            __syncthreads();
-            if (id == i)
+        __syncthreads();
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    ulonglong2* to = sum + e * f.team;
-                    if (i > 0) {
-                        const ulonglong2 v = *to;
-                        dw[e] = add2(v.x, dw[e]);
-                        db[e] = add2(v.y, db[e]);
-                    }
-                    if (i < f.teams - 1) *to = make_ulonglong2(dw[e], db[e]);
+        for (int e = 0; e < E / 2; ++e) sums[(id * (E / 2) + e) * f.team + t] = make_ulonglong2(dw[e], db[e]);
+        __syncthreads();
+        const int pairs = E / 2 * f.team;
+        for (int j = threadIdx.x; j < pairs; j += all) {   // columns 2 j - shift and the next, those of run j / H
+            const int run = j / H, u = run / f.team, c = 2 * j - shift, i = (u * H + j % H) * f.team + run - u * f.team;
+            ulonglong2 v = sums[i];
+            for (int k = 1; k < f.teams; ++k) {
+                const ulonglong2 o = sums[k * pairs + i];
+                v.x = add2(v.x, o.x);
+                v.y = add2(v.y, o.y);
+            }
+            float a[4];
+            unpack(v.x, a[0], a[1]);
+            unpack(v.y, a[2], a[3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (c + k >= 0 && c + k < n) {
+                    store_one(part + c + k, a[k], p.bnd, 6);
+                    store_one(part + n + c + k, a[2 + k], p.bnd, 6);
                 }
         }
-    }
-    if (id != f.teams - 1) return;                         // the last team has the sums of all of them
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * cu;
-        if (c >= n) continue;
-        store_run<W, true>(part, dw + u * H, c, n, !EDGE, p.bnd, 6);
-        store_run<W, true>(part + p.n, db + u * H, c, n, !EDGE, p.bnd, 6);
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * cu;
+            if (c >= n) continue;
+            store_run<W, true>(part, dw + u * H, c, n, !EDGE, p.bnd, 6);
+            store_run<W, true>(part + p.n, db + u * H, c, n, !EDGE, p.bnd, 6);
+        }
+    }
+    if (f.cluster) {                                       // few rows: joined at once, by all blocks
+        cluster_sync_all();
+        if (n % 2 == 0) join_columns<4>(p, n, static_cast<int>(blockIdx.x) * all + static_cast<int>(threadIdx.x), kCluster * all);
+        else join_columns<1>(p, n, static_cast<int>(blockIdx.x) * all + static_cast<int>(threadIdx.x), kCluster * all);
     }
 }
 
@@ -296,30 +329,35 @@ cudaError_t join(const NormBackArgs& a, int64_t parts, cudaStream_t st) {
 // Most parts of the rows: the blocks of the kernel above, a multiple of 8 where rows
 // start differently.
 int64_t most_parts(int64_t m) {
-    const int64_t least = m < 8 ? 8 : m;
+    const int64_t least = m < kCluster ? kCluster : m;
     return least < kSms ? least : kSms;
 }
 
 template <typename T, typename D, int E>
 cudaError_t back_e(const NormBackArgs& a, cudaStream_t st, int num_sms) {
     constexpr int W = 16 / sizeof(T);
-    Teams f;
+    Teams f{};
     f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
     const bool dy_vec = same_boundary(f.at, boundary_of(a.dy, sizeof(D), a.sdy, a.m, W)),
                dx_vec = same_boundary(f.at, boundary_of(a.dx, sizeof(T), a.sdx, a.m, W)), w_vec = aligned_to(a.w, 16);
     const bool edge = f.at.base != 0 || f.at.stride != 0 || a.n % W != 0 || !dy_vec || !dx_vec || !w_vec;
     auto kern = edge ? norm_back_kernel<T, D, E, true> : norm_back_kernel<T, D, E, false>;
     f.team = team_of(a.n, E, edge, W);
-    const int64_t blocks = blocks_of(a.m, num_sms < kSms ? num_sms : kSms, f.at);
+    // With up to two rows to a team of eight blocks, these join their sums as a cluster: one launch less,
+    // which takes the host longer than the rows' spread over the SMs saves (one row: 9.3 us of host time
+    // with a second kernel, 5.8 without).
+    f.cluster = a.dw != nullptr && a.m <= 2 * kCluster * (kRowThreads / f.team);
+    const int64_t blocks = f.cluster ? kCluster : blocks_of(a.m, num_sms < kSms ? num_sms : kSms, f.at);
     f.teams = teams_of(a.m, blocks, f.team, kRowThreads);
     const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T) + sizeof(D)), weights = E <= 16 ? 0 : threads * E * 4;
     f.stages = (kNormRoom - weights) / stage;
     if (f.stages > 4) f.stages = 4;
-    const int sums = f.teams > 1 ? f.team * E * 8 : 0, rows = f.stages * stage + weights, smem = sums > rows ? sums : rows;
+    const int sums = f.teams > 1 ? threads * E * 8 : 0, rows = f.stages * stage + weights, smem = sums > rows ? sums : rows;
     if (smem > 47 * 1024)                                  // 48 KB without being asked for
         if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kNormRoom); e != cudaSuccess) return e;
-    if (cudaError_t e = launch_after(kern, dim3(static_cast<unsigned>(blocks)), threads, static_cast<size_t>(smem), st, a, f, dy_vec, dx_vec, w_vec);
-        e != cudaSuccess)
+    if (cudaError_t e = launch_cluster_after(kern, dim3(static_cast<unsigned>(blocks)), threads, f.cluster ? kCluster : 1, static_cast<size_t>(smem), st, a, f,
+                                             dy_vec, dx_vec, w_vec);
+        e != cudaSuccess || f.cluster)
         return e;
     return join(a, blocks, st);
 }

@@ -208,6 +208,7 @@ __device__ __forceinline__ void mask_run(Pack<T, W>& v, int c, int n) {
 struct Teams {
     int team, teams, stages;
     Boundary at;
+    bool cluster;              // the blocks are one cluster
 };
 // Blocks of a launch over m rows, `most` at most (a multiple of 8), and their teams of
 // `team` threads, `threads` at most in all: rows first to blocks, then to teams.
