@@ -92,10 +92,11 @@ def combine(ys: torch.Tensor, plan: ops.ExpertPlan, weights: torch.Tensor, add: 
 class Router(torch.nn.Module):
     """Scores of every token for every expert, and the k it goes to.
 
-    The scores' weights and products are fp32. With ``balance`` the buffer ``bias`` (fp32
-    [experts], zero at first) is added to the scores that choose, not to the weights;
-    ``balance_step`` moves it against the load of a batch. The other arguments are
-    ``ops.route``'s."""
+    The scores' products are fp32, and so are their weights unless the module is cast. With
+    ``balance`` the buffer ``bias`` ([experts], zero at first; keep it in fp32, whose steps
+    are finer than ``balance_step``'s) is added to the scores that choose, not to the
+    weights; ``balance_step`` moves it against the load of a batch. The other arguments
+    are ``ops.route``'s."""
 
     def __init__(self, features: int, experts: int, k: int, balance: bool = False, device=None, score: str = "softmax",
                  groups: int = 1, kept: int = 1, group_best: int = 1, renormalise: bool = True, scale: float = 1.0):
@@ -116,15 +117,16 @@ class Router(torch.nn.Module):
         """x [tokens, features] -> (weights fp32 [tokens, k], experts int32 [tokens, k])."""
         if x.dim() != 2 or x.shape[1] != self.features:
             raise ValueError(f"expected [tokens, {self.features}], got {tuple(x.shape)}")
-        return route(torch.nn.functional.linear(x.float(), self.weight), self.k, self.bias, **self.how)
+        bias = None if self.bias is None else self.bias.float()
+        return route(torch.nn.functional.linear(x.float(), self.weight.float()), self.k, bias, **self.how)
 
     @torch.no_grad()
     def balance_step(self, plan: ops.ExpertPlan, rate: float = 1e-3) -> None:
         """bias += rate for experts with fewer rows than the mean, -= rate for those with more."""
         if self.bias is None:
             raise ValueError("the router was made without balance=True")
-        load = plan.offsets.diff().to(self.bias.dtype)
-        self.bias += rate * torch.sign(load.mean() - load)
+        load = plan.offsets.diff().float()
+        self.bias += (rate * torch.sign(load.mean() - load)).to(self.bias.dtype)
 
 
 class FP4MoE(torch.nn.Module):

@@ -134,6 +134,11 @@ def test_layer(pkg, tokens, fmt):
     twin = copy.deepcopy(layer)
     with torch.no_grad():
         assert torch.equal(twin(x), layer(x))
+    layer.zero_grad()
+    layer.to(BF)                                    # a model cast as a whole: every parameter in bf16
+    y3 = layer(x)
+    y3.float().square().mean().backward()
+    assert torch.isfinite(y3).all() and layer.router.weight.grad.dtype == BF
     assert pkg.ops.device_status() == 0
 
 
