@@ -595,7 +595,9 @@ ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sf
  *
  * All take bf16 or fp32 rows (contiguous, any row stride; rows on 16-byte
  * boundaries are faster) and compute in fp32, rounding once. Outputs' rows must not
- * overlap. No results depend on timing: sums have a fixed order. No call allocates;
+ * overlap, nor an output an input (but layer_norm's Y may be X, and expert_combine's Y
+ * its add, of the same type and stride). No results depend on timing: sums have a fixed
+ * order. A pointer off its elements' boundary is QL_ERR_ALIGNMENT. No call allocates;
  * a workspace is 16-byte aligned device memory, free for others once the stream is
  * past the call.
  * ------------------------------------------------------------------------- */
@@ -604,7 +606,7 @@ ql_status gemm_fp4_wgrad_ragged(const uint8_t* y, int64_t ldy, const uint8_t* sf
  * and var (the mean of (x - mean)^2, whose squares must fit fp32) of each row.
  * weight and bias [n] of one type, each may be NULL. mean and rstd = 1 / sqrt(var +
  * eps), fp32 [m], for the backward call, or both NULL. eps >= 0. A row with an
- * infinity or a NaN becomes NaN. */
+ * infinity or a NaN becomes NaN; mean and rstd of rows of no columns are NaN. */
 ql_status layer_norm(const void* x, ql_dtype x_dtype, int64_t m, int64_t n, int64_t x_stride_m, const void* weight,
                      const void* bias, ql_dtype w_dtype, float eps, void* y, ql_dtype y_dtype, int64_t y_stride_m, float* mean,
                      float* rstd, ql_stream_t stream);

@@ -144,6 +144,12 @@ constexpr int64_t kInt31 = int64_t(1) << 31;
 constexpr int64_t kMaxSlots = int64_t(1) << 26;     // of an exchange: every chunk of a plan reads the counts of all
 constexpr int64_t kMaxColumns = int64_t(1) << 22;   // 65535 pieces of 128 columns and less
 
+// Pointers of elements of `bytes`.
+template <typename... P>
+bool on_elements(int64_t bytes, P... p) {
+    return ((reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0) && ...);
+}
+
 // Codes of `rows` rows of `k` columns: alignment and row stride.
 ql_status fp4_operand(const uint8_t* q, int64_t ld, const uint8_t* sf, int64_t k) {
     if (q == nullptr || sf == nullptr || ld < (k + 1) / 2) return QL_ERR_INVALID_ARG;
@@ -995,8 +1001,17 @@ ql_status layer_norm(const void* x, ql_dtype x_dtype, int64_t m, int64_t n, int6
     if ((weight != nullptr || bias != nullptr) && !known_type(w_dtype)) return QL_ERR_INVALID_ARG;
     if ((mean == nullptr) != (rstd == nullptr)) return QL_ERR_INVALID_ARG;
     if (m >= kInt31 || n >= kInt31) return QL_ERR_UNSUPPORTED;
-    if (m == 0 || n == 0) return QL_OK;
+    if (m == 0) return QL_OK;
+    if (n == 0) {                      // the statistics of nothing: NaN
+        if (mean == nullptr) return QL_OK;
+        cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+        const cudaError_t e = cudaMemsetAsync(mean, 0xff, static_cast<size_t>(m) * 4, st);
+        return from_cuda(e != cudaSuccess ? e : cudaMemsetAsync(rstd, 0xff, static_cast<size_t>(m) * 4, st));
+    }
     if (x == nullptr || !rows_fit(y, m, n, y_stride_m)) return QL_ERR_INVALID_ARG;
+    if (!on_elements(bytes_of(x_dtype), x) || !on_elements(bytes_of(w_dtype), weight, bias) || !on_elements(bytes_of(y_dtype), y) ||
+        !on_elements(4, mean, rstd))
+        return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::NormArgs a{};
@@ -1049,6 +1064,9 @@ ql_status layer_norm_backward(const void* dy, ql_dtype dy_dtype, int64_t dy_stri
         if (workspace == nullptr || workspace_bytes < layer_norm_backward_workspace_size(m, n)) return QL_ERR_INVALID_ARG;
         if (!aligned16(workspace)) return QL_ERR_ALIGNMENT;
     }
+    if (!on_elements(bytes_of(dy_dtype), dy) || !on_elements(bytes_of(x_dtype), x, dx) || !on_elements(bytes_of(w_dtype), weight) ||
+        !on_elements(4, mean, rstd, dweight, dbias))
+        return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::NormBackArgs a{};
@@ -1098,6 +1116,7 @@ ql_status expert_route(const void* logits, ql_dtype logits_dtype, int64_t m, int
     if (groups > ql::kRouteMaxGroups) return QL_ERR_UNSUPPORTED;
     if (m == 0) return QL_OK;
     if (logits == nullptr || weights == nullptr || chosen == nullptr) return QL_ERR_INVALID_ARG;
+    if (!on_elements(bytes_of(logits_dtype), logits) || !on_elements(4, bias, weights, chosen)) return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::RouteArgs a{};
@@ -1132,6 +1151,7 @@ ql_status expert_route_backward(const float* dweights, const void* logits, ql_dt
     if (m == 0) return QL_OK;
     if (dweights == nullptr || logits == nullptr || chosen == nullptr || !rows_fit(dlogits, m, experts, d_stride_m))
         return QL_ERR_INVALID_ARG;
+    if (!on_elements(bytes_of(logits_dtype), logits, dlogits) || !on_elements(4, dweights, chosen)) return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::RouteBackArgs a{};
@@ -1167,7 +1187,7 @@ ql_status expert_plan(const int32_t* chosen, int64_t slots, int experts, int32_t
     if (offsets == nullptr || (slots > 0 && (chosen == nullptr || rows == nullptr))) return QL_ERR_INVALID_ARG;
     const size_t need = expert_plan_workspace_size(slots, experts);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QL_ERR_INVALID_ARG;
-    if (need > 0 && !aligned16(workspace)) return QL_ERR_ALIGNMENT;
+    if ((need > 0 && !aligned16(workspace)) || !on_elements(4, chosen, offsets, rows)) return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::PlanArgs a{};
@@ -1200,6 +1220,7 @@ ql_status expert_dispatch(const void* x, ql_dtype dtype, int64_t m, int64_t n, i
     if (experts > ql::kRouteMaxExperts) return QL_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return QL_OK;
     if (x == nullptr || rows == nullptr || offsets == nullptr || !rows_fit(xs, m * k, n, xs_stride_m)) return QL_ERR_INVALID_ARG;
+    if (!on_elements(bytes_of(dtype), x, xs) || !on_elements(4, rows, offsets)) return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::DispatchArgs a{};
@@ -1228,6 +1249,7 @@ ql_status expert_combine(const void* ys, ql_dtype dtype, int64_t ys_stride_m, co
     if (ql_status s = exchange_sizes(m, n, k, dtype); s != QL_OK) return s;
     if (m == 0 || n == 0) return QL_OK;
     if (ys == nullptr || rows == nullptr || !rows_fit(y, m, n, y_stride_m)) return QL_ERR_INVALID_ARG;
+    if (!on_elements(bytes_of(dtype), ys, add, y) || !on_elements(4, rows, weights)) return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::CombineArgs a{};
@@ -1265,6 +1287,7 @@ ql_status expert_combine_backward(const void* dy, ql_dtype dtype, int64_t dy_str
     if (dy == nullptr || ys == nullptr || rows == nullptr || offsets == nullptr || weights == nullptr ||
         !rows_fit(dys, m * k, n, dys_stride_m))
         return QL_ERR_INVALID_ARG;
+    if (!on_elements(bytes_of(dtype), dy, ys, dys) || !on_elements(4, rows, offsets, weights, dweights)) return QL_ERR_ALIGNMENT;
     DeviceInfo di;
     if (ql_status s = device_info(di); s != QL_OK) return s;
     ql::CombineBackArgs a{};

@@ -91,6 +91,11 @@ int small_integer(PyObject* o) {
     if (v < INT32_MIN || v > INT32_MAX) value_error("integer out of range");
     return static_cast<int>(v);
 }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v == 1;
+}
 float real(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw Raised{};
@@ -133,7 +138,7 @@ PyObject* f_layer_norm(Args a) {
         out_type = tensor(a[4], "out must be a tensor").scalar_type();
         if (out_type != at::kBFloat16 && out_type != at::kFloat) value_error("out must be bfloat16 or float32");
     }
-    const bool saving = PyObject_IsTrue(a[6]) == 1;
+    const bool saving = truth(a[6]);
     c10::cuda::CUDAGuard guard(d);
     const Matrix y = result(a[4], x.m, x.n, out_type, d);
     at::Tensor stats;
@@ -158,7 +163,7 @@ PyObject* f_layer_norm_backward(Args a) {
     const at::Tensor& stats = table(a[2], at::kFloat, 2, x.m, d, "stats must be those of the forward call");
     Weights w;
     w.w = weight_of(a[3], x.n, d, w, true);
-    const bool sums = PyObject_IsTrue(a[4]) == 1;
+    const bool sums = truth(a[4]);
     const Matrix dx = result(nullptr, x.m, x.n, x.t.scalar_type(), d);
     at::Tensor dw, db;
     c10::DataPtr ws;
@@ -200,7 +205,7 @@ PyObject* f_route(Args a) {
     const int experts = static_cast<int>(l.n < INT32_MAX ? l.n : INT32_MAX);
     at::Tensor w = new_tensor({l.m, k}, at::kFloat, d), e = new_tensor({l.m, k}, at::kInt, d);
     status("expert_route", layers.route(l.t.data_ptr(), l.code, l.m, experts, l.ld, bias, k, small_integer(a[3]), groups, kept, best,
-                                        PyObject_IsTrue(a[7]) == 1, real(a[8]), w.data_ptr<float>(), e.data_ptr<int32_t>(),
+                                        truth(a[7]), real(a[8]), w.data_ptr<float>(), e.data_ptr<int32_t>(),
                                         stream_of(d)));
     return pair(THPVariable_Wrap(w), THPVariable_Wrap(e));
 }
@@ -216,7 +221,7 @@ PyObject* f_route_backward(Args a) {
     const int experts = static_cast<int>(l.n < INT32_MAX ? l.n : INT32_MAX);
     status("expert_route_backward",
            layers.route_back(dw.data_ptr<float>(), l.t.data_ptr(), l.code, l.m, experts, l.ld, e.data_ptr<int32_t>(),
-                             static_cast<int>(e.size(1)), small_integer(a[3]), PyObject_IsTrue(a[4]) == 1, real(a[5]),
+                             static_cast<int>(e.size(1)), small_integer(a[3]), truth(a[4]), real(a[5]),
                              o.t.data_ptr(), o.ld, stream_of(d)));
     return THPVariable_Wrap(o.t);
 }

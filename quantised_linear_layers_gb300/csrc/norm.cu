@@ -37,6 +37,12 @@ __device__ __forceinline__ void deviations(F2* v, float about, int c, int n, F2&
     }
 }
 
+// From the mean of the deviations and that of their squares; NaN stays NaN.
+__device__ __forceinline__ float rstd_of(float m1, float m2, float eps) {
+    const float var = fmaf(-m1, m1, m2);
+    return rsqrtf((var < 0.0f ? 0.0f : var) + eps);
+}
+
 // Two sums over a warp's or a block's row.
 template <bool WARP>
 __device__ __forceinline__ void team_sum(float& a, float& b, float* s) {
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(WARP ? 256 : (E <= 8 ? 1024 : 512)) norm_kerne
     float m1 = sum2(s1), m2 = sum2(s2);
     team_sum<WARP>(m1, m2, s_sum + (WARP ? 0 : 64));
     m1 *= inv_n;
-    const float rstd = rsqrtf(fmaxf(fmaf(-m1, m1, m2 * inv_n), 0.0f) + p.eps);
+    const float rstd = rstd_of(m1, m2 * inv_n, p.eps);
     if (p.mean != nullptr && t == 0) {
         store_one(p.mean + row, about + m1, p.bnd, 4);
         store_one(p.rstd + row, rstd, p.bnd, 5);
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
         F2 r2[R], back[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float m1 = m[r] * inv_n, rstd = rsqrtf(fmaxf(fmaf(-m1, m1, m[2 + r] * inv_n), 0.0f) + p.eps);
+            const float m1 = m[r] * inv_n, rstd = rstd_of(m1, m[2 + r] * inv_n, p.eps);
             if (p.mean != nullptr && t == 0 && row + r * step < p.m) {
                 store_one(mean + r * step, about[r] + m1, p.bnd, 4);
                 store_one(rstd_to + r * step, rstd, p.bnd, 5);
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) norm_any_kernel(const NormArgs p) {
         }
         sum_over_row<2, false>(two, s_sum + 32);
         const float off = two[0] / n;
-        const float rstd = rsqrtf(fmaxf(fmaf(-off, off, two[1] / n), 0.0f) + p.eps);
+        const float rstd = rstd_of(off, two[1] / n, p.eps);
         if (p.mean != nullptr && threadIdx.x == 0) {
             store_one(p.mean + row, about + off, p.bnd, 4);
             store_one(p.rstd + row, rstd, p.bnd, 5);

@@ -118,7 +118,9 @@ class Router(torch.nn.Module):
         if x.dim() != 2 or x.shape[1] != self.features:
             raise ValueError(f"expected [tokens, {self.features}], got {tuple(x.shape)}")
         bias = None if self.bias is None else self.bias.float()
-        return route(torch.nn.functional.linear(x.float(), self.weight.float()), self.k, bias, **self.how)
+        with torch.autocast(x.device.type, enabled=False):
+            logits = torch.nn.functional.linear(x.float(), self.weight.float())
+        return route(logits, self.k, bias, **self.how)
 
     @torch.no_grad()
     def balance_step(self, plan: ops.ExpertPlan, rate: float = 1e-3) -> None:

@@ -678,7 +678,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
                out: torch.Tensor | None = None, dtype: torch.dtype | None = None) -> torch.Tensor:
     """(x - mean) / sqrt(var + eps) * weight + bias over the rows of x [m, n] (bf16 or
     fp32), in fp32 and rounded once to ``dtype`` (default: out's or x's). weight and
-    bias [n], bf16 or fp32, each may be None."""
+    bias [n], bf16 or fp32, each may be None; out may be x."""
     return (_fp4 or _load_fp4()).layer_norm(x, weight, bias, eps, out, _type_code(dtype), False)
 
 
@@ -742,7 +742,7 @@ def expert_combine(ys: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor | N
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """y [tokens, n] = add + the sum over a token's slots of weights (fp32 [tokens, k],
     None: 1) times their rows of ys [tokens * k, n], in fp32 and rounded once to ys's
-    type; slots of no expert count for nothing."""
+    type; slots of no expert count for nothing. out may be add."""
     return (_fp4 or _load_fp4()).combine(ys, plan, weights, add, out)
 
 

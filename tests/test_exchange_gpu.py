@@ -169,3 +169,26 @@ def test_nothing_to_do(ops):
     x = torch.empty((8, 0), dtype=BF, device="cuda")
     assert ops.expert_combine(x, p).shape == (4, 0)
     assert not ops.expert_combine_backward(x[:4], x, p, torch.ones((4, 2), device="cuda"))[1].any()
+
+
+@pytest.mark.parametrize("m,k,n,apart", [(2500, 2, 520, 1 << 19), (2500, 2, 521, (1 << 19) + 1), (600, 8, 2048, 1 << 19)])
+def test_rows_past_32_bits(ops, m, k, n, apart):
+    """Rows far apart equal the same rows side by side."""
+    def far(rows):
+        return torch.empty((rows - 1) * apart + n, dtype=BF, device="cuda").as_strided((rows, n), (apart, 1))
+    p = ops.expert_plan(experts_of(m, k, 16), 16)
+    x, ys, dy, w = rand((m, n), BF, 1), rand((m * k, n), BF, 2), rand((m, n), BF, 3), rand((m, k), F, 4)
+    there = far(m * k)
+    assert torch.equal(ops.expert_dispatch(x, p, out=there), ops.expert_dispatch(x, p))
+    there.copy_(ys)
+    assert torch.equal(ops.expert_combine(there, p, w, x), ops.expert_combine(ys, p, w, x))
+    for a, b in zip(ops.expert_combine_backward(dy, there, p, w), ops.expert_combine_backward(dy, ys, p, w)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,k,n", [(5, 2, 40), (5, 2, 41), (2500, 2, 520), (600, 8, 2048)])
+def test_sums_onto_what_they_are_added_to(ops, m, k, n):
+    p = ops.expert_plan(experts_of(m, k, 16), 16)
+    ys, add, w = rand((m * k, n), BF, 2), rand((m, n), BF, 3), rand((m, k), F, 4)
+    want = ops.expert_combine(ys, p, w, add)
+    assert torch.equal(ops.expert_combine(ys, p, w, add, out=add), want) and torch.equal(add, want)

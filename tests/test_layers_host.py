@@ -98,6 +98,37 @@ def test_exchange_refuses(L):
     assert grad(m=0, dw=None) == 0
 
 
+def test_elements_off_their_boundaries_are_refused(L):
+    odd, two = ctypes.c_void_p(65), ctypes.c_void_p(66)
+
+    def norm(x=P, w=P, b=P, y=P, mean=P, rstd=P):
+        return L.layer_norm(x, 0, 4, 64, 64, w, b, 1, 1e-5, y, 1, 64, mean, rstd, None)
+    assert norm(x=odd) == norm(w=two) == norm(b=two) == norm(y=two) == norm(mean=two) == norm(rstd=two) == ALI
+
+    def back(dy=P, x=P, mean=P, rstd=P, w=P, dx=P, dw=P, db=P):
+        return L.layer_norm_backward(dy, 1, 64, x, 0, 64, mean, rstd, w, 0, 4, 64, dx, 64, dw, db, P, 1 << 20, None)
+    assert back(dy=two) == back(x=odd) == back(mean=two) == back(rstd=two) == back(w=odd) == back(dx=odd) == back(dw=two) == back(db=two) == ALI
+
+    def route(l=P, bias=None, w=P, e=P):
+        return L.expert_route(l, 0, 4, 16, 16, bias, 2, 0, 1, 1, 1, 1, 1.0, w, e, None)
+    assert route(l=odd) == route(bias=two) == route(w=two) == route(e=two) == ALI
+
+    def route_back(dw=P, l=P, e=P, d=P):
+        return L.expert_route_backward(dw, l, 0, 4, 16, 16, e, 2, 0, 1, 1.0, d, 16, None)
+    assert route_back(dw=two) == route_back(l=odd) == route_back(e=two) == route_back(d=odd) == ALI
+    for e, o, r in ((two, P, P), (P, two, P), (P, P, two)):
+        assert L.expert_plan(e, 8, 4, o, r, None, 0, None) == ALI
+    for x, r, o, xs in ((two, P, P, P), (P, two, P, P), (P, P, two, P), (P, P, P, two)):
+        assert L.expert_dispatch(x, 1, 4, 64, 64, r, o, 8, 2, xs, 64, None) == ALI
+    for ys, r, w, add, y in ((odd, P, P, P, P), (P, two, P, P, P), (P, P, two, P, P), (P, P, P, odd, P), (P, P, P, P, odd)):
+        assert L.expert_combine(ys, 0, 64, r, w, add, 64, 4, 64, 2, y, 64, None) == ALI
+    for i in range(7):
+        p = [P] * 7
+        p[i] = two
+        dy, ys, r, o, w, dys, dw = p
+        assert L.expert_combine_backward(dy, 1, 64, ys, 64, r, o, 8, w, 4, 64, 2, dys, 64, dw, None) == ALI
+
+
 def test_calls_refuse_host_tensors(L):
     from quantised_linear_layers_gb300 import ops
     x, e = torch.zeros(4, 8), torch.zeros((4, 2), dtype=torch.int32)

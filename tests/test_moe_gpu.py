@@ -148,6 +148,38 @@ def test_layer_without_tokens(pkg):
         assert layer(torch.empty((0, 64), dtype=BF, device="cuda")).shape == (0, 64)
 
 
+def test_layer_of_no_tokens_has_gradients(pkg):
+    layer = pkg.moe.FP4MoE(64, 32, 4, 2, device="cuda")
+    x = torch.empty((0, 64), dtype=BF, device="cuda", requires_grad=True)
+    layer(x).sum().backward()
+    assert x.grad.shape == (0, 64)
+    for p in layer.parameters():
+        assert p.grad is None or not p.grad.any()
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_tokens_that_reach_no_expert_stay_as_they_are(pkg, tokens):
+    layer = pkg.moe.FP4MoE(64, 32, 4, 2, device="cuda", balance=True)
+    layer.router.bias.fill_(float("-inf"))
+    x = rand((tokens, 64), BF, 1).requires_grad_()
+    y = layer(x)
+    assert torch.equal(y, x) and layer.plan.offsets.tolist() == [0] * 5
+    y.sum().backward()
+    assert torch.equal(x.grad, torch.ones_like(x))
+    for p in layer.parameters():
+        assert p.grad is None or not p.grad.any()
+    assert pkg.ops.device_status() == 0
+
+
+def test_router_keeps_fp32_under_autocast(pkg):
+    router = pkg.moe.Router(64, 16, 4, device="cuda")
+    x = rand((50, 64), BF, 1)
+    want = router(x)
+    with torch.autocast("cuda", dtype=BF):
+        got = router(x)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def calls(pkg, x, w, b, logits, bias, ys, dy, dw):
     ops = pkg.ops
     y, stats = ops.layer_norm_saving(x, w, b)

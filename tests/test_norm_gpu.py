@@ -170,3 +170,37 @@ def test_gradients_against_differences(ops, n):
                        (db[i].cpu().double(), (f(xd, wd, bd + e) - f(xd, wd, bd - e)).sum() / (2 * step))):
             # differences of values of size ~1e3 in 64 bits over 2e-5, and fp32's own 1e-5
             assert torch.allclose(got, d, rtol=2e-5, atol=1e-4 * float(v.abs().max()))
+
+
+@pytest.mark.parametrize("m,n,dtype", [(5, 40, BF), (3, 7168, BF), (2000, 1032, BF), (2000, 1027, F), (2000, 1027, BF), (2, 16391, F)])
+def test_in_place(ops, m, n, dtype):
+    w, b = params(n, F)
+    x = acts(m, n, dtype)
+    y = ops.layer_norm(x, w, b)
+    assert ops.layer_norm(x, w, b, out=x).data_ptr() == x.data_ptr()
+    assert torch.equal(x, y)
+
+
+def test_statistics_of_what_has_none(ops):
+    x = acts(4, 1003, F)
+    x[1, 5] = float("nan")
+    _, stats = ops.layer_norm_saving(x)
+    assert torch.isnan(stats[:, 1]).all() and torch.isfinite(stats[:, [0, 2, 3]]).all()
+    _, stats = ops.layer_norm_saving(torch.empty((5, 0), device="cuda"))
+    assert torch.isnan(stats).all()
+
+
+@pytest.mark.parametrize("n", [7168, 264])
+def test_rows_past_32_bits(ops, n):
+    """Rows 2^20 elements apart equal the same rows side by side."""
+    m = 2049
+    room = [torch.empty((m - 1 << 20) + n, dtype=BF, device="cuda").as_strided((m, n), (1 << 20, 1)) for _ in range(3)]
+    x, dy, y = room
+    x.copy_(acts(m, n, BF))
+    dy.copy_(acts(m, n, BF, 1))
+    w, b = params(n, F)
+    want, stats = ops.layer_norm_saving(x.contiguous(), w, b)
+    got, far = ops.layer_norm_saving(x, w, b, out=y)
+    assert torch.equal(got, want) and torch.equal(far, stats)
+    for a, c in zip(ops.layer_norm_backward(dy, x, stats, w), ops.layer_norm_backward(dy.contiguous(), x.contiguous(), stats, w)):
+        assert torch.equal(a, c)

@@ -202,3 +202,22 @@ def test_no_tokens(ops):
     w, e = ops.route(x, 3)
     assert w.shape == e.shape == (0, 3)
     assert ops.route_backward(w, x, e).shape == (0, 16)
+
+
+@pytest.mark.parametrize("n", [256, 161])
+def test_rows_past_32_bits(ops, n):
+    """Rows 2^20 elements apart equal the same rows side by side."""
+    near = torch.randn((2049, n), generator=torch.Generator().manual_seed(5)).cuda()
+    far = torch.empty((2048 << 20) + n, device="cuda").as_strided((2049, n), (1 << 20, 1))
+    far.copy_(near)
+    for a, b in zip(ops.route(far, 6), ops.route(near, 6)):
+        assert torch.equal(a, b)
+    w, e = ops.route(near, 6)
+    assert torch.equal(ops.route_backward(w, far, e, renormalise=False), ops.route_backward(w, near, e, renormalise=False))
+
+
+def test_a_truth_that_has_none_is_an_error(ops):
+    x = torch.zeros((2, 8), device="cuda")
+    with pytest.raises(RuntimeError):
+        ops.route(x, 2, renormalise=torch.ones(2))
+    assert ops.route(x, 2)[1].tolist() == [[0, 1]] * 2
