@@ -414,11 +414,12 @@ __global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const Ri
             rows_at(f_next, f_token + step);
         }
     };
-    for (int s = 0; s < S; ++s) fetch(s);
     int32_t next[K];
-    float w_next[K];
-    rows_at(next, first);
+    float w_next[K];                                       // (behind the copies they would wait for the ring to fill)
+#pragma unroll
+    for (int j = 0; j < K; ++j) next[j] = f_rows[j];
     weights_of<K>(w_next, p.weights, first, 0, first < p.m ? p.k : 0, p.bnd, 3);
+    for (int s = 0; s < S; ++s) fetch(s);
     int s = 0, turn = 0;
     for (int64_t t = first; t < p.m; t += step) {
         int32_t r[K];

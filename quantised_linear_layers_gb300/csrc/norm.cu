@@ -111,6 +111,16 @@ __global__ void __launch_bounds__(WARP ? 256 : (E <= 8 ? 1024 : 512)) norm_kerne
     F2 v[E / 2], sum = 0ull;
 #pragma unroll
     for (int u = 0; u < U; ++u) load_columns<W, SPREAD>(v + u * H, x, u, t, team, n, p.bnd, 0);
+    // where registers hold them, the weights are on their way beside the row: 1003 x 4099 fp32 13.0 -> 11.7 us
+    constexpr bool EARLY = E <= 8;
+    F2 w0[EARLY ? E / 2 : 1], b0[EARLY ? E / 2 : 1];
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            load_weight_columns<W, SPREAD>(w0 + u * H, p.w, p.w_bf16, 1.0f, u, t, team, n, p.bnd, 1);
+            load_weight_columns<W, SPREAD>(b0 + u * H, p.b, p.w_bf16, 0.0f, u, t, team, n, p.bnd, 2);
+        }
+    }
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) sum = add2(sum, v[e]);
     const float inv_n = 1.0f / static_cast<float>(n);
@@ -147,8 +157,16 @@ __global__ void __launch_bounds__(WARP ? 256 : (E <= 8 ? 1024 : 512)) norm_kerne
     for (int u = 0; u < U; ++u) {
         if (column<W, SPREAD>(u, 0, t, team) >= n) continue;
         F2 w[H], b[H];
-        load_weight_columns<W, SPREAD>(w, p.w, p.w_bf16, 1.0f, u, t, team, n, p.bnd, 1);
-        load_weight_columns<W, SPREAD>(b, p.b, p.w_bf16, 0.0f, u, t, team, n, p.bnd, 2);
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                w[i] = w0[u * H + i];
+                b[i] = b0[u * H + i];
+            }
+        } else {
+            load_weight_columns<W, SPREAD>(w, p.w, p.w_bf16, 1.0f, u, t, team, n, p.bnd, 1);
+            load_weight_columns<W, SPREAD>(b, p.b, p.w_bf16, 0.0f, u, t, team, n, p.bnd, 2);
+        }
         Pack<O, W> o;
 #pragma unroll
         for (int i = 0; i < H; ++i) set_pair<W>(o, i, fma2(fma2(v[u * H + i], r2, back), w[i], b[i]));
@@ -201,7 +219,8 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
         }
         copy_commit();                                     // a group for every stage, also past the last row
     };
-    for (int s = 0; s < f.stages; ++s) fetch(s * stage);
+    // the weights between the first stage and the rest: behind all of them they wait for the ring to fill
+    fetch(0);
     if (id == 0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -215,6 +234,7 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
             }
         }
     }
+    for (int s = 1; s < f.stages; ++s) fetch(s * stage);
     __syncthreads();
     const float inv_n = 1.0f / static_cast<float>(n);
     O* y = static_cast<O*>(p.y) + first * p.sy;
@@ -348,12 +368,13 @@ cudaError_t norm_e(const NormArgs& a, bool whole, cudaStream_t st) {
 
 // Rows to a team from which the ring pays for its start. Measured, teams / a row to a
 // block or warp, us:
-//   whole vectors  2048 x 2048 (2 rows) 6.3 / 6.2, 1003 x 4096 fp32 (3) 11.0 / 9.1, 1024 x 8000 fp32 (7) 18.3 / 19.4,
-//                  16384 x 1024 (8) 18.0 / 20.3, 4096 x 4096 (9) 20.7 / 18.9, 4096 x 7168 (13) 27.5 / 31.7,
-//                  16384 x 7168 (54) 82 / 108
-//   others         1003 x 4099 fp32 (2) 14.0 / 13.0, 16384 x 1023 (8) 29.2 / 35.4, 4096 x 4095 (9) 28.2 / 45.5
-// and never for the shortest rows: 16384 x 96 (7) 5.3 / 5.0, 16384 x 97 8.4 / 5.8.
-constexpr int kLeastRows = 6;
+//   whole vectors, fp32   2048 x 2048 (2 rows) 6.0 / 6.2, 1003 x 4096 fp32 (3) 10.8 / 8.1, 1024 x 8000 fp32 (7) 18.8 / 19.3,
+//                         2000 x 7168 (7) 17.6 / 18.5, 16384 x 1024 (8) 16.9 / 20.5, 4096 x 4096 (9) 19.3 / 18.8,
+//                         4096 x 7168 (13) 26.3 / 31.6, 16384 x 7168 (54) 82.9 / 108, 1003 x 4099 fp32 (2) 13.7 / 11.7,
+//                         2000 x 2049 fp32 (2) 14.8 / 10.7
+//   others of bf16        300 x 7167 (1) 7.2 / 6.9, 600 x 4099 (1.3) 8.1 / 7.2, 512 x 7167 (1.7) 9.9 / 12.1, 2000 x 2049 (2.2) 10.5 / 10.8,
+//                         1003 x 7167 (3.3) 15.9 / 21.7, 16384 x 1023 (8) 28.7 / 33.8, 4096 x 4095 (9) 26.8 / 42.3
+constexpr double kLeastRows = 6, kLeastRowsOdd = 1.5;
 
 // Rows by teams: false where that many rows are too few for it.
 template <typename T, typename O, int E>
@@ -366,7 +387,7 @@ bool rows_e(const NormArgs& a, bool whole, cudaStream_t st, int num_sms, cudaErr
     f.team = team_of(a.n, E, !whole, W);
     const int64_t blocks = blocks_of(a.m, num_sms, f.at);
     f.teams = teams_of(a.m, blocks, f.team, E <= 16 ? 896 : 512);
-    if (a.m < blocks * f.teams * kLeastRows) return false;
+    if (static_cast<double>(a.m) < static_cast<double>(blocks * f.teams) * (whole || sizeof(T) == 4 ? kLeastRows : kLeastRowsOdd)) return false;
     const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T)) * (E <= 16 ? 2 : 1), weights = f.team * E * 8;
     f.stages = (kNormRoom - weights) / stage;
     if (f.stages > 4) f.stages = 4;
@@ -391,7 +412,8 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t st, int num_sms) {
     // a row to a warp / to a block, us: 200 x 1000 3.3 / 2.2, 2048 x 1000 5.0 / 4.7, 4000 x 1000 5.5 / 6.9, 8000 x 500 8.7 / 10.5
     if (a.n <= 1024 - W && a.m > 10 * num_sms) return norm_e<T, O, 32, true>(a, whole, st);
     // few elements to a thread where few rows leave a block alone on its SM (1 x 7168 2.8 us, 12.6 by a
-    // loop of 256 threads) and where elements go one by one; 4096 x 7168 takes 31.7 with 32 and 67 with 8
+    // loop of 256 threads) and where elements go one by one; 4096 x 7168 takes 31.7 with 32 and 67 with 8,
+    // 1003 x 4099 fp32 12.8 with 32, 14.9 with 16 and 11.7 with 8
     if (a.n <= 8192 - W && (a.m <= num_sms || a.n <= 1024 - W || !whole)) return norm_e<T, O, 8, false>(a, whole, st);
     return norm_e<T, O, 32, false>(a, whole, st);
 }

@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
         x_next += step * p.sx;
         dy_next += step * p.sdy;
     };
-    for (int s = 0; s < f.stages; ++s) fetch(s * stage);
+    // what the first row needs besides, before the other stages: behind them it waits for the ring to fill
+    fetch(0);
     F2 w[KEEP ? E / 2 : H];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -96,6 +97,13 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
             for (int i = 0; i < H / 2; ++i) my_w[(u * (H / 2) + i) * all] = make_ulonglong2(v[2 * i], v[2 * i + 1]);
         }
     }
+    const float *mean_next = p.mean + first, *rstd_next = p.rstd + first;
+    float mean = 0.0f, rstd = 0.0f;
+    if (first < p.m) {
+        mean = load_one(mean_next, p.bnd, 2, 0.0f);
+        rstd = load_one(rstd_next, p.bnd, 3, 0.0f);
+    }
+    for (int s = 1; s < f.stages; ++s) fetch(s * stage);
     auto weights = [&](int u, F2 (&v)[H]) {                // of run u
         if constexpr (KEEP) {
 #pragma unroll
@@ -112,12 +120,6 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
     F2 dw[E / 2], db[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = 0ull;
-    const float *mean_next = p.mean + first, *rstd_next = p.rstd + first;
-    float mean = 0.0f, rstd = 0.0f;
-    if (first < p.m) {
-        mean = load_one(mean_next, p.bnd, 2, 0.0f);
-        rstd = load_one(rstd_next, p.bnd, 3, 0.0f);
-    }
     T* dx = static_cast<T*>(p.dx) + first * p.sdx;
     const float inv_n = 1.0f / static_cast<float>(n);
     int at = 0, turn = 0;
