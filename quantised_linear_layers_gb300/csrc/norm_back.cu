@@ -192,8 +192,10 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
     }
     if (p.dw == nullptr) return;
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
-    if (f.teams > 1) {
-        // the block's teams in the rows' room: [team][E / 2][threads] pairs of dw and db
+    if ((EDGE && W > 4) || f.teams > 1) {
+        // the block's teams in the rows' room: [team][E / 2][threads] pairs of dw and db. (From here stores
+        // are whole lines: 512 x 7167 13.5 us, 20.2 by each thread's runs, whose elements go one by one; but
+        // 1003 x 4099 fp32, with runs of 4, 18.3 and 17.6.)
         ulonglong2* sums = reinterpret_cast<ulonglong2*>(s_mem);
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
@@ -224,8 +226,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * cu;
             if (c >= n) continue;
-            store_run<W, true>(part, dw + u * H, c, n, !EDGE, p.bnd, 6);
-            store_run<W, true>(part + p.n, db + u * H, c, n, !EDGE, p.bnd, 6);
+            store_run<W, EDGE>(part, dw + u * H, c, n, false, p.bnd, 6);
+            store_run<W, EDGE>(part + p.n, db + u * H, c, n, false, p.bnd, 6);
         }
     }
     if (f.cluster) {                                       // few rows: joined at once, by all blocks
@@ -354,7 +356,7 @@ cudaError_t back_e(const NormBackArgs& a, cudaStream_t st, int num_sms) {
     const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T) + sizeof(D)), weights = E <= 16 ? 0 : threads * E * 4;
     f.stages = (kNormRoom - weights) / stage;
     if (f.stages > 4) f.stages = 4;
-    const int sums = f.teams > 1 ? threads * E * 8 : 0, rows = f.stages * stage + weights, smem = sums > rows ? sums : rows;
+    const int sums = a.dw != nullptr && ((edge && W > 4) || f.teams > 1) ? threads * E * 8 : 0, rows = f.stages * stage + weights, smem = sums > rows ? sums : rows;
     if (smem > 47 * 1024)                                  // 48 KB without being asked for
         if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kNormRoom); e != cudaSuccess) return e;
     if (cudaError_t e = launch_cluster_after(kern, dim3(static_cast<unsigned>(blocks)), threads, f.cluster ? kCluster : 1, static_cast<size_t>(smem), st, a, f,
