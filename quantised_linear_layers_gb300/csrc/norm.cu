@@ -15,18 +15,11 @@ namespace {
 constexpr int kThreads = 256;
 
 // A run's deviations from `about`, in its place, and the sums of them and of their squares;
-// elements past the row's ends stay zero.
-template <int W, bool EDGE>
+// runs from column n on stay zero.
+template <int W>
 __device__ __forceinline__ void deviations(F2* v, float about, int c, int n, F2& s1, F2& s2) {
     const F2 off = f2(-about, -about);
-    if (EDGE && (c < 0 || c + W > n)) {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            float a, b;
-            unpack(v[i], a, b);
-            v[i] = f2(c + 2 * i >= 0 && c + 2 * i < n ? a - about : 0.0f, c + 2 * i + 1 >= 0 && c + 2 * i + 1 < n ? b - about : 0.0f);
-        }
-    } else if (EDGE || c < n) {
+    if (c < n) {
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) v[i] = add2(v[i], off);
     }
@@ -193,40 +186,43 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
     pdl_launch_dependents();
     pdl_wait_prior();
     const int id = static_cast<int>(threadIdx.x) / f.team, t = static_cast<int>(threadIdx.x) - id * f.team;
-    const int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * id, step = static_cast<int64_t>(gridDim.x) * f.teams;
-    const int n = static_cast<int>(p.n), all = static_cast<int>(blockDim.x);
-    const int shift = EDGE ? static_cast<int>((f.at.base + static_cast<int64_t>(blockIdx.x) * f.at.stride) % W) : 0;
-    const int c0 = t * W - shift, cu = f.team * W;         // run u starts at column c0 + u * cu
+    const uint32_t rows = static_cast<uint32_t>(p.m), first = blockIdx.x + gridDim.x * id, step = gridDim.x * f.teams;
+    const int all = static_cast<int>(blockDim.x);
+    Ends end{0, static_cast<int>(p.n), -1};
+    if constexpr (EDGE) end = ends_of<W>(static_cast<int>((f.at.base + static_cast<int64_t>(blockIdx.x) * f.at.stride) % W), static_cast<int>(p.n), t >= f.team - 32);
+    const int n = end.tail;                                // of the runs
+    const int c0 = end.head + t * W, cu = f.team * W;      // run u starts at column c0 + u * cu
 
-    // [stage][R][U] runs, a thread's side by side; then a team's weights and biases, [2][E]
+    // [stage][R][U] runs, a thread's side by side; then a team's weights and biases, [2][E];
+    // then (EDGE) [stage][R][teams] words of the lanes that have a row's ends
     const int line = all * E * static_cast<int>(sizeof(T)), stage = R * line;
     uint8_t* my_x = s_mem + threadIdx.x * XB;
     ulonglong2* my_w = reinterpret_cast<ulonglong2*>(s_mem + f.stages * stage) + t;               // + i * team
-    if (EDGE || n < U * cu)
+    uint32_t* my_end = reinterpret_cast<uint32_t*>(s_mem + f.stages * stage + f.team * E * 8) + id * 32 + (t & 31);
+    const int end_row = f.teams * 32;                      // words
+    if (n < U * cu)
         for (int s = 0; s < f.stages * R * U; ++s) *reinterpret_cast<uint4*>(my_x + s * all * XB) = make_uint4(0u, 0u, 0u, 0u);
-    const T *lo = static_cast<const T*>(p.x), *hi = lo + (p.m - 1) * p.sx + n;
-    const T* x_next = lo + first * p.sx;
-    int64_t row_next = first;
-    auto fetch = [&](int at) {                             // R rows into the stage that begins at byte `at`
+    const T* x = static_cast<const T*>(p.x);
+    const OneOf<T> one_of(x + first * p.sx, end.col, static_cast<int>(p.n), p.sx);
+    auto fetch = [&](int at, int turn, uint32_t row) {     // R rows from that on into the turn-th stage, which begins at byte `at`
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (row_next < p.m) {
+        for (int r = 0; r < R; ++r, row += step)
+            if (row < rows) {
+                const T* from = x + row * p.sx;
 #pragma unroll
-                for (int u = 0; u < U; ++u) fetch_run<W, EDGE>(my_x + at + r * line + u * all * XB, x_next, c0 + u * cu, n, true, lo, hi, p.bnd, 0);
+                for (int u = 0; u < U; ++u) fetch_run<W>(my_x + at + r * line + u * all * XB, from, c0 + u * cu, n, true, p.bnd, 0);
+                if (EDGE && end.col >= 0) one_of.fetch(my_end + (turn * R + r) * end_row, from + end.col, row, rows, p.bnd, 0);
             }
-            row_next += step;
-            x_next += step * p.sx;
-        }
         copy_commit();                                     // a group for every stage, also past the last row
     };
     // the weights between the first stage and the rest: behind all of them they wait for the ring to fill
-    fetch(0);
+    fetch(0, 0, first);
     if (id == 0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             F2 w[H], b[H];
-            weight_run<W, EDGE>(w, p.w, p.w_bf16, 1.0f, c0 + u * cu, n, w_vec && shift == 0, p.bnd, 1);
-            weight_run<W, EDGE>(b, p.b, p.w_bf16, 0.0f, c0 + u * cu, n, w_vec && shift == 0, p.bnd, 2);
+            weight_run<W>(w, p.w, p.w_bf16, 1.0f, c0 + u * cu, n, !EDGE || (w_vec && end.head == 0), p.bnd, 1);
+            weight_run<W>(b, p.b, p.w_bf16, 0.0f, c0 + u * cu, n, !EDGE || (w_vec && end.head == 0), p.bnd, 2);
 #pragma unroll
             for (int i = 0; i < H / 2; ++i) {
                 my_w[(u * (H / 2) + i) * f.team] = make_ulonglong2(w[2 * i], w[2 * i + 1]);
@@ -234,23 +230,26 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
             }
         }
     }
-    for (int s = 1; s < f.stages; ++s) fetch(s * stage);
+    float end_w = 0.0f, end_b = 0.0f;
+    if (EDGE && end.col >= 0) {
+        end_w = weight_one(p.w, p.w_bf16, 1.0f, end.col, p.bnd, 1);
+        end_b = weight_one(p.b, p.w_bf16, 0.0f, end.col, p.bnd, 2);
+    }
+    for (int s = 1; s < f.stages; ++s) fetch(s * stage, s, first + s * R * step);
     __syncthreads();
-    const float inv_n = 1.0f / static_cast<float>(n);
-    O* y = static_cast<O*>(p.y) + first * p.sy;
-    float *mean = p.mean + first, *rstd_to = p.rstd + first;
-    int at = 0;
-    for (int64_t row = first; row < p.m; row += R * step) {
+    const float inv_n = 1.0f / static_cast<float>(p.n);
+    int at = 0, turn = 0;
+    for (uint32_t row = first; row < rows; row += R * step) {
         copy_wait(f.stages);
         F2 v[R][E / 2];
+        float one[R];                                      // of the row's ends
         float about[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             F2 sum = 0ull;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + r * line + u * all * XB);
-                if (EDGE && (c0 + u * cu < 0 || c0 + u * cu + W > n)) mask_run<W>(x, c0 + u * cu, n);
+                const Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + r * line + u * all * XB);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     v[r][u * H + i] = pair_of<W>(x, i);
@@ -258,9 +257,14 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
                 }
             }
             about[r] = sum2(sum);
+            if (EDGE && end.col >= 0) {
+                one[r] = one_of.value(my_end + (turn * R + r) * end_row);
+                about[r] += one[r];
+            }
         }
-        fetch(at);                                         // the rows are in registers
-        at = at + stage == f.stages * stage ? 0 : at + stage;
+        fetch(at, turn, row + f.stages * R * step);                                   // the rows are in registers
+        at += stage;
+        if (++turn == f.stages) at = turn = 0;
         sum_over_team(about[0], about[1], s_sum[0], f.team, id);
         float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};             // sums of d, then of d^2
 #pragma unroll
@@ -268,9 +272,14 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
             about[r] *= inv_n;
             F2 s1 = 0ull, s2 = 0ull;
 #pragma unroll
-            for (int u = 0; u < U; ++u) deviations<W, EDGE>(v[r] + u * H, about[r], c0 + u * cu, n, s1, s2);
+            for (int u = 0; u < U; ++u) deviations<W>(v[r] + u * H, about[r], c0 + u * cu, n, s1, s2);
             m[r] = sum2(s1);
             m[2 + r] = sum2(s2);
+            if (EDGE && end.col >= 0) {
+                one[r] -= about[r];
+                m[r] += one[r];
+                m[2 + r] = fmaf(one[r], one[r], m[2 + r]);
+            }
         }
         if constexpr (R == 2) sum4_over_team(m, s_sum[1], f.team, id);
         else sum_over_team(m[0], m[2], s_sum[1], f.team, id);
@@ -278,15 +287,16 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float m1 = m[r] * inv_n, rstd = rstd_of(m1, m[2 + r] * inv_n, p.eps);
-            if (p.mean != nullptr && t == 0 && row + r * step < p.m) {
-                store_one(mean + r * step, about[r] + m1, p.bnd, 4);
-                store_one(rstd_to + r * step, rstd, p.bnd, 5);
+            if (p.mean != nullptr && t == 0 && row + r * step < rows) {
+                store_one(p.mean + row + r * step, about[r] + m1, p.bnd, 4);
+                store_one(p.rstd + row + r * step, rstd, p.bnd, 5);
             }
             r2[r] = f2(rstd, rstd);
             back[r] = f2(-m1 * rstd, -m1 * rstd);
+            if (EDGE && end.col >= 0 && row + r * step < rows)
+                store_one(static_cast<O*>(p.y) + (row + r * step) * p.sy + end.col, from_f32<O>(fmaf(fmaf(one[r], rstd, -m1 * rstd), end_w, end_b)), p.bnd, 3);
         }
-        mean += R * step;
-        rstd_to += R * step;
+        O* y = static_cast<O*>(p.y) + row * p.sy;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * cu;
@@ -303,9 +313,8 @@ __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const No
             }
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (r == 0 || row + r * step < p.m) store_run<W, EDGE>(y + r * step * p.sy, o[r], c, n, y_vec, p.bnd, 3);
+                if (r == 0 || row + r * step < rows) store_run<W>(y + r * step * p.sy, o[r], c, n, !EDGE || y_vec, p.bnd, 3);
         }
-        y += R * step * p.sy;
     }
 }
 
@@ -361,7 +370,7 @@ template <typename T, typename O, int E, bool WARP>
 cudaError_t norm_e(const NormArgs& a, bool whole, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const dim3 grid(static_cast<unsigned>(WARP ? (a.m + 7) / 8 : a.m));
-    const int threads = WARP ? 256 : team_of(a.n, E, false, W);
+    const int threads = WARP ? 256 : team_of(a.n, E);
     if (whole) return launch_after(norm_kernel<T, O, W, E, WARP, false>, grid, threads, 0, st, a);
     return launch_after(norm_kernel<T, O, W, E, WARP, true>, grid, threads, 0, st, a);
 }
@@ -384,14 +393,15 @@ bool rows_e(const NormArgs& a, bool whole, cudaStream_t st, int num_sms, cudaErr
     f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
     const bool y_vec = same_boundary(f.at, boundary_of(a.y, sizeof(O), a.sy, a.m, W)), w_vec = aligned_to(a.w, 16) && aligned_to(a.b, 16);
     auto kern = whole ? norm_rows_kernel<T, O, E, false> : norm_rows_kernel<T, O, E, true>;
-    f.team = team_of(a.n, E, !whole, W);
-    const int64_t blocks = blocks_of(a.m, num_sms, f.at);
+    f.team = team_of(a.n, E);
+    const int64_t blocks = blocks_of(a.m, num_sms, f.at.stride == 0);
     f.teams = teams_of(a.m, blocks, f.team, E <= 16 ? 896 : 512);
     if (static_cast<double>(a.m) < static_cast<double>(blocks * f.teams) * (whole || sizeof(T) == 4 ? kLeastRows : kLeastRowsOdd)) return false;
     const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T)) * (E <= 16 ? 2 : 1), weights = f.team * E * 8;
-    f.stages = (kNormRoom - weights) / stage;
+    const int ends = whole ? 0 : f.teams * 128 * (E <= 16 ? 2 : 1);     // of a stage
+    f.stages = (kNormRoom - weights) / (stage + ends);
     if (f.stages > 4) f.stages = 4;
-    const int smem = f.stages * stage + weights;
+    const int smem = f.stages * (stage + ends) + weights;
     e = cudaSuccess;
     if (smem > 46 * 1024)                                  // 48 KB without being asked for
         e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kNormRoom);

@@ -37,7 +37,8 @@ __device__ __forceinline__ void join_columns(const NormBackArgs& p, int n, int f
 
 // With d = x - mean, q = dy rstd and g = q w (that is rstd dy w):
 //   dx = g - d rstd^2 sum(g d) / n - sum(g) / n,  dw += q d,  db += dy
-// Elements past a row's ends have x = dy = w = 0 and add nothing.
+// Runs past a row's last have x = dy = 0 and are not stored; they add nothing to its sums,
+// whose g is 0 there.
 //
 // The rows to come are on their way into a ring of `stages` rows in shared memory, in
 // which each thread copies and reads only what is its own: no thread waits for
@@ -51,59 +52,65 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
     pdl_launch_dependents();
     pdl_wait_prior();
     const int id = static_cast<int>(threadIdx.x) / f.team, t = static_cast<int>(threadIdx.x) - id * f.team;
-    const int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * id, step = static_cast<int64_t>(gridDim.x) * f.teams;
-    const int n = static_cast<int>(p.n), all = static_cast<int>(blockDim.x);
-    const int shift = EDGE ? static_cast<int>((f.at.base + static_cast<int64_t>(blockIdx.x) * f.at.stride) % W) : 0;
-    const int c0 = t * W - shift, cu = f.team * W;         // run u starts at column c0 + u * cu
+    const uint32_t m = static_cast<uint32_t>(p.m), first = blockIdx.x + gridDim.x * id, step = gridDim.x * f.teams;
+    const int all = static_cast<int>(blockDim.x);
+    Ends end{0, static_cast<int>(p.n), -1};
+    if constexpr (EDGE) end = ends_of<W>(static_cast<int>((f.at.base + static_cast<int64_t>(blockIdx.x) * f.at.stride) % W), static_cast<int>(p.n), t >= f.team - 32);
+    const int n = end.tail;                                // of the runs
+    const int c0 = end.head + t * W, cu = f.team * W;      // run u starts at column c0 + u * cu
 
-    // [stage][U] runs of x and of dy, then (not KEEP) [E] weights, a thread's side by side
+    // [stage][U] runs of x and of dy, then (not KEEP) [E] weights, a thread's side by side;
+    // then (EDGE) [stage][2][teams] words of the lanes that have a row's ends
     const int stage = all * U * (XB + DB);
     uint8_t* my_x = s_mem + threadIdx.x * XB;
     uint8_t* my_dy = s_mem + all * U * XB + threadIdx.x * DB;
     ulonglong2* my_w = reinterpret_cast<ulonglong2*>(s_mem + f.stages * stage) + threadIdx.x;     // + i * all
+    uint32_t* my_end = reinterpret_cast<uint32_t*>(s_mem + f.stages * stage + (KEEP ? 0 : all * E * 4)) + id * 32 + (t & 31);
+    const int end_row = f.teams * 32;                      // words
     for (int s = 0; s < f.stages; ++s)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             *reinterpret_cast<Pack<T, W>*>(my_x + s * stage + u * all * XB) = zero_pack<T, W>();
             *reinterpret_cast<Pack<D, W>*>(my_dy + s * stage + u * all * DB) = zero_pack<D, W>();
         }
-    const T *x_lo = static_cast<const T*>(p.x), *x_hi = x_lo + (p.m - 1) * p.sx + n;
-    const D *dy_lo = static_cast<const D*>(p.dy), *dy_hi = dy_lo + (p.m - 1) * p.sdy + n;
-    const T* x_next = x_lo + first * p.sx;
-    const D* dy_next = dy_lo + first * p.sdy;
-    int64_t row_next = first;
-    auto fetch = [&](int at) {                             // into the stage that begins at byte `at`
-        if (row_next < p.m) {
+    const OneOf<T> x_one(static_cast<const T*>(p.x) + first * p.sx, end.col, static_cast<int>(p.n), p.sx);
+    const OneOf<D> dy_one(static_cast<const D*>(p.dy) + first * p.sdy, end.col, static_cast<int>(p.n), p.sdy);
+    auto fetch = [&](int at, int stage_no, uint32_t row) { // that row into that stage, which begins at byte `at`
+        if (row < m) {
+            const T* x = static_cast<const T*>(p.x) + row * p.sx;
+            const D* dy = static_cast<const D*>(p.dy) + row * p.sdy;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                fetch_run<W, EDGE>(my_x + at + u * all * XB, x_next, c0 + u * cu, n, true, x_lo, x_hi, p.bnd, 1);
-                fetch_run<W, EDGE>(my_dy + at + u * all * DB, dy_next, c0 + u * cu, n, dy_vec, dy_lo, dy_hi, p.bnd, 0);
+                fetch_run<W>(my_x + at + u * all * XB, x, c0 + u * cu, n, true, p.bnd, 1);
+                fetch_run<W>(my_dy + at + u * all * DB, dy, c0 + u * cu, n, !EDGE || dy_vec, p.bnd, 0);
+            }
+            if (EDGE && end.col >= 0) {
+                x_one.fetch(my_end + 2 * stage_no * end_row, x + end.col, row, m, p.bnd, 1);
+                dy_one.fetch(my_end + (2 * stage_no + 1) * end_row, dy + end.col, row, m, p.bnd, 0);
             }
         }
         copy_commit();                                     // a group for every row, also past the last
-        row_next += step;
-        x_next += step * p.sx;
-        dy_next += step * p.sdy;
     };
     // what the first row needs besides, before the other stages: behind them it waits for the ring to fill
-    fetch(0);
+    fetch(0, 0, first);
     F2 w[KEEP ? E / 2 : H];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         F2* v = w + (KEEP ? u * H : 0);
-        weight_run<W, EDGE>(v, p.w, p.w_bf16, 1.0f, c0 + u * cu, n, w_vec && shift == 0, p.bnd, 4);
+        weight_run<W>(v, p.w, p.w_bf16, 1.0f, c0 + u * cu, n, !EDGE || (w_vec && end.head == 0), p.bnd, 4);
         if constexpr (!KEEP) {
 #pragma unroll
             for (int i = 0; i < H / 2; ++i) my_w[(u * (H / 2) + i) * all] = make_ulonglong2(v[2 * i], v[2 * i + 1]);
         }
     }
-    const float *mean_next = p.mean + first, *rstd_next = p.rstd + first;
     float mean = 0.0f, rstd = 0.0f;
-    if (first < p.m) {
-        mean = load_one(mean_next, p.bnd, 2, 0.0f);
-        rstd = load_one(rstd_next, p.bnd, 3, 0.0f);
+    if (first < m) {
+        mean = load_one(p.mean + first, p.bnd, 2, 0.0f);
+        rstd = load_one(p.rstd + first, p.bnd, 3, 0.0f);
     }
-    for (int s = 1; s < f.stages; ++s) fetch(s * stage);
+    float end_w = 0.0f, end_dw = 0.0f, end_db = 0.0f;
+    if (EDGE && end.col >= 0) end_w = weight_one(p.w, p.w_bf16, 1.0f, end.col, p.bnd, 4);
+    for (int s = 1; s < f.stages; ++s) fetch(s * stage, s, first + s * step);
     auto weights = [&](int u, F2 (&v)[H]) {                // of run u
         if constexpr (KEEP) {
 #pragma unroll
@@ -120,16 +127,13 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
     F2 dw[E / 2], db[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dw[e] = db[e] = 0ull;
-    T* dx = static_cast<T*>(p.dx) + first * p.sdx;
-    const float inv_n = 1.0f / static_cast<float>(n);
-    int at = 0, turn = 0;
-    for (int64_t row = first; row < p.m; row += step, dx += step * p.sdx) {
+    const float inv_n = 1.0f / static_cast<float>(p.n);
+    int at = 0, turn = 0, stage_no = 0;
+    for (uint32_t row = first; row < m; row += step) {
         float mean2 = 0.0f, rstd2 = 0.0f;                  // the next row's
-        mean_next += step;
-        rstd_next += step;
-        if (row + step < p.m) {
-            mean2 = load_one(mean_next, p.bnd, 2, 0.0f);
-            rstd2 = load_one(rstd_next, p.bnd, 3, 0.0f);
+        if (row + step < m) {
+            mean2 = load_one(p.mean + row + step, p.bnd, 2, 0.0f);
+            rstd2 = load_one(p.rstd + row + step, p.bnd, 3, 0.0f);
         }
         copy_wait(f.stages);
         const F2 off = f2(-mean, -mean), r2 = f2(rstd, rstd);
@@ -137,12 +141,8 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
         F2 sg = 0ull, sgd = 0ull;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + u * all * XB);
-            Pack<D, W> dy = *reinterpret_cast<const Pack<D, W>*>(my_dy + at + u * all * DB);
-            if (EDGE && (c0 + u * cu < 0 || c0 + u * cu + W > n)) {
-                mask_run<W>(x, c0 + u * cu, n);
-                mask_run<W>(dy, c0 + u * cu, n);
-            }
+            const Pack<T, W> x = *reinterpret_cast<const Pack<T, W>*>(my_x + at + u * all * XB);
+            const Pack<D, W> dy = *reinterpret_cast<const Pack<D, W>*>(my_dy + at + u * all * DB);
             F2 wu[H];
             weights(u, wu);
 #pragma unroll
@@ -159,13 +159,23 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
                 }
             }
         }
-        if constexpr (KEEP) fetch(at);
-        float a = sum2(sg), b = sum2(sgd);
+        float a = sum2(sg), b = sum2(sgd), end_d = 0.0f, end_g = 0.0f;
+        if (EDGE && end.col >= 0) {
+            const float v = dy_one.value(my_end + (2 * stage_no + 1) * end_row), q = v * rstd;
+            end_d = x_one.value(my_end + 2 * stage_no * end_row) - mean;
+            end_g = q * end_w;
+            end_dw = fmaf(q, end_d, end_dw);
+            end_db += v;
+            a += end_g;
+            b = fmaf(end_g, end_d, b);
+        }
+        if constexpr (KEEP) fetch(at, stage_no, row + f.stages * step);
         sum_over_team(a, b, s_sum[turn], f.team, id);
         turn ^= 1;
         const float k1 = -a * inv_n, k2 = -rstd * rstd * (b * inv_n);
         const F2 k1k1 = f2(k1, k1), k2k2 = f2(k2, k2);
         asm volatile("" ::: "memory");                     // what is not kept is read again
+        T* dx = static_cast<T*>(p.dx) + row * p.sdx;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * cu;
@@ -183,17 +193,19 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
                 for (int i = 0; i < H; ++i)
                     o[i] = fma2(mul2(pair_of<W>(dy, i), r2), wu[i], fma2(add2(pair_of<W>(x, i), off), k2k2, k1k1));
             }
-            store_run<W, EDGE>(dx, o, c, n, dx_vec, p.bnd, 5);
+            store_run<W>(dx, o, c, n, !EDGE || dx_vec, p.bnd, 5);
         }
-        if constexpr (!KEEP) fetch(at);
-        at = at + stage == f.stages * stage ? 0 : at + stage;
+        if (EDGE && end.col >= 0) store_one(dx + end.col, from_f32<T>(end_g + fmaf(end_d, k2, k1)), p.bnd, 5);
+        if constexpr (!KEEP) fetch(at, stage_no, row + f.stages * step);
+        at += stage;
+        if (++stage_no == f.stages) at = stage_no = 0;
         mean = mean2;
         rstd = rstd2;
     }
     if (p.dw == nullptr) return;
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 2 * p.n;
     if ((EDGE && W > 4) || f.teams > 1) {
-        // the block's teams in the rows' room: [team][E / 2][threads] pairs of dw and db. (From here stores
+        // the block's teams in the rows' room: [team][E / 2][threads] pairs of dw and db, [team][32] of the ends'. (From here stores
         // are whole lines: 512 x 7167 13.5 us, 20.2 by each thread's runs, whose elements go one by one; but
         // 1003 x 4099 fp32, with runs of 4, 18.3 and 17.6.)
         ulonglong2* sums = reinterpret_cast<ulonglong2*>(s_mem);
@@ -201,10 +213,20 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) sums[(id * (E / 2) + e) * f.team + t] = make_ulonglong2(dw[e], db[e]);
+        F2* end_sums = reinterpret_cast<F2*>(sums + all * (E / 2));
+        if (EDGE && end.col >= 0) end_sums[id * 32 + (t & 31)] = f2(end_dw, end_db);
         __syncthreads();
+        if (EDGE && id == 0 && end.col >= 0) {
+            F2 v = end_sums[t & 31];
+            for (int k = 1; k < f.teams; ++k) v = add2(v, end_sums[k * 32 + (t & 31)]);
+            float a, b;
+            unpack(v, a, b);
+            store_one(part + end.col, a, p.bnd, 6);
+            store_one(part + p.n + end.col, b, p.bnd, 6);
+        }
         const int pairs = E / 2 * f.team;
-        for (int j = threadIdx.x; j < pairs; j += all) {   // columns 2 j - shift and the next, those of run j / H
-            const int run = j / H, u = run / f.team, c = 2 * j - shift, i = (u * H + j % H) * f.team + run - u * f.team;
+        for (int j = threadIdx.x; j < pairs; j += all) {   // columns head + 2 j and the next, those of run j / H
+            const int run = j / H, u = run / f.team, c = end.head + 2 * j, i = (u * H + j % H) * f.team + run - u * f.team;
             ulonglong2 v = sums[i];
             for (int k = 1; k < f.teams; ++k) {
                 const ulonglong2 o = sums[k * pairs + i];
@@ -214,26 +236,32 @@ __global__ void __launch_bounds__(kRowThreads) norm_back_kernel(const NormBackAr
             float a[4];
             unpack(v.x, a[0], a[1]);
             unpack(v.y, a[2], a[3]);
+            if (c < n) {                                   // and c + 1 with it
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (c + k >= 0 && c + k < n) {
+                for (int k = 0; k < 2; ++k) {
                     store_one(part + c + k, a[k], p.bnd, 6);
-                    store_one(part + n + c + k, a[2 + k], p.bnd, 6);
+                    store_one(part + p.n + c + k, a[2 + k], p.bnd, 6);
                 }
+            }
         }
     } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * cu;
             if (c >= n) continue;
-            store_run<W, EDGE>(part, dw + u * H, c, n, false, p.bnd, 6);
-            store_run<W, EDGE>(part + p.n, db + u * H, c, n, false, p.bnd, 6);
+            store_run<W>(part, dw + u * H, c, n, !EDGE, p.bnd, 6);
+            store_run<W>(part + p.n, db + u * H, c, n, !EDGE, p.bnd, 6);
+        }
+        if (EDGE && end.col >= 0) {
+            store_one(part + end.col, end_dw, p.bnd, 6);
+            store_one(part + p.n + end.col, end_db, p.bnd, 6);
         }
     }
     if (f.cluster) {                                       // few rows: joined at once, by all blocks
         cluster_sync_all();
-        if (n % 2 == 0) join_columns<4>(p, n, static_cast<int>(blockIdx.x) * all + static_cast<int>(threadIdx.x), kCluster * all);
-        else join_columns<1>(p, n, static_cast<int>(blockIdx.x) * all + static_cast<int>(threadIdx.x), kCluster * all);
+        const int cols = static_cast<int>(p.n);
+        if (cols % 2 == 0) join_columns<4>(p, cols, static_cast<int>(blockIdx.x) * all + static_cast<int>(threadIdx.x), kCluster * all);
+        else join_columns<1>(p, cols, static_cast<int>(blockIdx.x) * all + static_cast<int>(threadIdx.x), kCluster * all);
     }
 }
 
@@ -342,21 +370,24 @@ cudaError_t back_e(const NormBackArgs& a, cudaStream_t st, int num_sms) {
     constexpr int W = 16 / sizeof(T);
     Teams f{};
     f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
-    const bool dy_vec = same_boundary(f.at, boundary_of(a.dy, sizeof(D), a.sdy, a.m, W)),
+    const Boundary dy_at = boundary_of(a.dy, sizeof(D), a.sdy, a.m, W);
+    const bool dy_vec = same_boundary(f.at, dy_at),
                dx_vec = same_boundary(f.at, boundary_of(a.dx, sizeof(T), a.sdx, a.m, W)), w_vec = aligned_to(a.w, 16);
     const bool edge = f.at.base != 0 || f.at.stride != 0 || a.n % W != 0 || !dy_vec || !dx_vec || !w_vec;
     auto kern = edge ? norm_back_kernel<T, D, E, true> : norm_back_kernel<T, D, E, false>;
-    f.team = team_of(a.n, E, edge, W);
+    f.team = team_of(a.n, E);
     // With up to two rows to a team of eight blocks, these join their sums as a cluster: one launch less,
     // which takes the host longer than the rows' spread over the SMs saves (one row: 9.3 us of host time
     // with a second kernel, 5.8 without).
     f.cluster = a.dw != nullptr && a.m <= 2 * kCluster * (kRowThreads / f.team);
-    const int64_t blocks = f.cluster ? kCluster : blocks_of(a.m, num_sms < kSms ? num_sms : kSms, f.at);
+    const int64_t blocks = f.cluster ? kCluster : blocks_of(a.m, num_sms < kSms ? num_sms : kSms, f.at.stride == 0 && dy_at.stride == 0);
     f.teams = teams_of(a.m, blocks, f.team, kRowThreads);
     const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T) + sizeof(D)), weights = E <= 16 ? 0 : threads * E * 4;
-    f.stages = (kNormRoom - weights) / stage;
+    const int ends = edge ? f.teams * 256 : 0;             // of a stage
+    f.stages = (kNormRoom - weights) / (stage + ends);
     if (f.stages > 4) f.stages = 4;
-    const int sums = a.dw != nullptr && ((edge && W > 4) || f.teams > 1) ? threads * E * 8 : 0, rows = f.stages * stage + weights, smem = sums > rows ? sums : rows;
+    const int sums = a.dw != nullptr && ((edge && W > 4) || f.teams > 1) ? threads * E * 8 + f.teams * 256 : 0;
+    const int rows = f.stages * (stage + ends) + weights, smem = sums > rows ? sums : rows;
     if (smem > 47 * 1024)                                  // 48 KB without being asked for
         if (cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), kNormRoom); e != cudaSuccess) return e;
     if (cudaError_t e = launch_cluster_after(kern, dim3(static_cast<unsigned>(blocks)), threads, f.cluster ? kCluster : 1, static_cast<size_t>(smem), st, a, f,

@@ -1,10 +1,10 @@
 // What the layer norm kernels share: packed fp32 arithmetic, sums over the threads of a
-// row, and vectors that may stick out over a row's ends.
+// row, and rows that start anywhere.
 //
-// A row is a team's: `team` threads of whole warps. A thread has U runs of W elements,
-// run u of thread t those from column (u * team + t) * W - shift on, where shift is
-// what the row's first element is past a boundary of W elements: all its accesses are
-// whole vectors but those of a row's first and last run, which go element by element.
+// A row is a team's: `team` threads of whole warps. A thread has U runs of W elements, on
+// boundaries of W elements and inside the row: run u of thread t those from column
+// head + (u * team + t) * W on. What a row has before the first run and behind the last,
+// up to W - 1 elements each, is the team's last warp's, an element to a lane (Ends).
 #pragma once
 
 #include "rows.cuh"
@@ -117,46 +117,64 @@ __device__ __forceinline__ void sum4_over_team(float (&a)[4], float* s, int team
 }
 
 // ---------------------------------------------------------------- runs
-// W elements from column c of a row of n on as pairs, zeros past its ends. EDGE: a run
-// may stick out or be off its boundary (vec says that whole ones are on it).
-template <int W, bool EDGE, typename T, typename B>
+// W elements from column c of a row on as pairs, zeros from column n on. vec: on a boundary.
+template <int W, typename T, typename B>
 __device__ __forceinline__ void load_run(F2* v, const T* row, int c, int n, bool vec, const B& bnd, int span) {
     Pack<T, W> p = zero_pack<T, W>();
-    if (!EDGE || (vec && c >= 0 && c + W <= n)) {
+    if (vec) {
         if (c < n) p = load_pack<T, W>(row + c, bnd, span);
-    } else if (c > -W && c < n) {
+    } else if (c < n) {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (c + i >= 0 && c + i < n) p.v[i] = load_one(row + c + i, bnd, span, p.v[i]);
+        for (int i = 0; i < W; ++i) p.v[i] = load_one(row + c + i, bnd, span, p.v[i]);
     }
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) v[i] = pair_of<W>(p, i);
 }
-// And back: the elements inside the row.
-template <int W, bool EDGE, typename T, typename B>
+// And back, where c < n.
+template <int W, typename T, typename B>
 __device__ __forceinline__ void store_run(T* row, const F2* v, int c, int n, bool vec, const B& bnd, int span) {
     Pack<T, W> p;
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) set_pair<W>(p, i, v[i]);
-    if (!EDGE || (vec && c >= 0 && c + W <= n)) {
+    if (vec) {
         if (c < n) store_pack<T, W>(row + c, p, bnd, span);
-    } else {
+    } else if (c < n) {
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (c + i >= 0 && c + i < n) store_one(row + c + i, p.v[i], bnd, span);
+        for (int i = 0; i < W; ++i) store_one(row + c + i, p.v[i], bnd, span);
     }
 }
-// A run of weights of bf16 or fp32 that may be missing (`other`).
-template <int W, bool EDGE, typename B>
+// A run of weights of bf16 or fp32 that may be missing (`other`), and one of them.
+template <int W, typename B>
 __device__ __forceinline__ void weight_run(F2* v, const void* p, bool bf16, float other, int c, int n, bool vec, const B& bnd, int span) {
     if (p == nullptr) {
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) v[i] = f2(other, other);
     } else if (bf16) {
-        load_run<W, EDGE>(v, static_cast<const __nv_bfloat16*>(p), c, n, vec, bnd, span);
+        load_run<W>(v, static_cast<const __nv_bfloat16*>(p), c, n, vec, bnd, span);
     } else {
-        load_run<W, EDGE>(v, static_cast<const float*>(p), c, n, vec, bnd, span);
+        load_run<W>(v, static_cast<const float*>(p), c, n, vec, bnd, span);
     }
+}
+template <typename B>
+__device__ __forceinline__ float weight_one(const void* p, bool bf16, float other, int c, const B& bnd, int span) {
+    float w[1];
+    load_weights<1>(w, p, bf16, c, other, bnd, span);
+    return w[0];
+}
+
+// A row of n >= W columns whose first is `shift` past a boundary: whole runs of the columns
+// [head, tail), and the lane's column of the others, or -1.
+struct Ends {
+    int head, tail, col;
+};
+template <int W>
+__device__ __forceinline__ Ends ends_of(int shift, int n, bool last_warp) {
+    Ends e;
+    e.head = shift == 0 ? 0 : W - shift;
+    e.tail = e.head + (n - e.head) / W * W;
+    const int lane = static_cast<int>(threadIdx.x & 31), c = lane < W ? e.head - W + lane : e.tail + lane - W;
+    e.col = last_warp && lane < 2 * W && c >= 0 && c < n && (c < e.head || c >= e.tail) ? c : -1;
+    return e;
 }
 
 // Where a tensor's rows start past boundaries of w elements: row r at (base + r * stride) % w.
@@ -168,52 +186,67 @@ inline Boundary boundary_of(const void* p, int64_t es, int64_t stride, int64_t m
                     m > 1 ? static_cast<int>(((stride % w) + w) % w) : 0};
 }
 inline bool same_boundary(const Boundary& a, const Boundary& b) { return a.base == b.base && a.stride == b.stride; }
-// Threads of a team for rows of n columns, E elements each, wherever the rows start.
-inline int team_of(int64_t n, int e, bool edge, int w) { return static_cast<int>((n + (edge ? w - 1 : 0) + 32 * e - 1) / (32 * e)) * 32; }
-
+// Threads of a team for rows of n columns, E elements each.
+inline int team_of(int64_t n, int e) { return static_cast<int>((n + 32 * e - 1) / (32 * e)) * 32; }
 
 // ---------------------------------------------------------------- rows through shared memory
-// A run into a thread's own place in shared memory. A run that sticks out of the row is
-// copied whole where that stays between the tensor's first and last element, [lo, hi):
-// mask_run takes out what is other rows'. At those ends it goes element by element.
-template <int W, bool EDGE, typename T, typename B>
-__device__ __forceinline__ void fetch_run(void* place, const T* row, int c, int n, bool vec, const T* lo, const T* hi, const B& bnd, int span) {
+// A run into a thread's own place in shared memory, where c < n.
+template <int W, typename T, typename B>
+__device__ __forceinline__ void fetch_run(void* place, const T* row, int c, int n, bool vec, const B& bnd, int span) {
     T* to = static_cast<T*>(place);
-    if (!EDGE) {
+    if (vec) {
         if (c < n && QL_IN(bnd, span, row + c, W * sizeof(T))) copy_async<W * sizeof(T)>(to, row + c);
-    } else if (c > -W && c < n) {
-        if (vec && row + c >= lo && row + c + W <= hi) {
-            if (QL_IN(bnd, span, row + c, W * sizeof(T))) copy_async<W * sizeof(T)>(to, row + c);
-        } else {
+    } else if (c < n) {
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                if (c + i >= 0 && c + i < n && QL_IN(bnd, span, row + c + i, sizeof(T))) {
-                    if constexpr (sizeof(T) == 4) copy_async<4>(to + i, row + c + i);
-                    else to[i] = row[c + i];
-                }
-        }
+        for (int i = 0; i < W; ++i)
+            if (QL_IN(bnd, span, row + c + i, sizeof(T))) {
+                if constexpr (sizeof(T) == 4) copy_async<4>(to + i, row + c + i);
+                else to[i] = row[c + i];
+            }
     }
 }
-// The run with zeros for what is not the row's.
-template <int W, typename T>
-__device__ __forceinline__ void mask_run(Pack<T, W>& v, int c, int n) {
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-        if (c + i < 0 || c + i >= n) v.v[i] = from_f32<T>(0.0f);
-}
+// Column c of a tensor's rows by a lane with a word of its own, where it comes in the word of
+// memory that it is in: with a neighbour of bf16, which may be the row before's or behind's
+// (or what lies between them), but not past the tensor. first: a row of the lane's, n its
+// columns, stride that between rows; all the lane's rows start alike.
+template <typename T>
+struct OneOf {
+    bool high, before, behind;                             // the second half; with a neighbour of another row, or (both) none
+    __device__ __forceinline__ OneOf(const T* first, int c, int n, int64_t stride) {
+        high = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(first + c) & 2) != 0;
+        before = sizeof(T) == 2 && high && c == 0;
+        behind = sizeof(T) == 2 && !high && c == n - 1;
+        if ((before || behind) && stride <= 0) before = behind = true;
+    }
+    template <typename B>
+    __device__ __forceinline__ void fetch(uint32_t* word, const T* p, uint32_t row, uint32_t m, const B& bnd, int span) const {
+        if constexpr (sizeof(T) == 4) {
+            if (QL_IN(bnd, span, p, 4)) copy_async<4>(word, p);
+        } else if ((before && row == 0) || (behind && row == m - 1) || (before && behind)) {
+            reinterpret_cast<T*>(word)[high] = load_one(p, bnd, span, from_f32<T>(0.0f));
+        } else if (QL_IN(bnd, span, p - high, 4)) {
+            copy_async<4>(word, p - high);
+        }
+    }
+    __device__ __forceinline__ float value(const uint32_t* word) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(*word);
+        else return __uint_as_float(high ? *word & 0xffff0000u : *word << 16);
+    }
+};
 
 // How the rows go to the teams of warps of the blocks. Every row of a block has the same
 // shift (row = block + blocks * (team + teams * i), blocks a multiple of 8 unless all
-// rows start alike), so a thread's columns stay its own.
+// rows start alike, x's and dy's), so a thread's columns stay its own.
 struct Teams {
     int team, teams, stages;
     Boundary at;
     bool cluster;              // the blocks are one cluster
 };
-// Blocks of a launch over m rows, `most` at most (a multiple of 8), and their teams of
-// `team` threads, `threads` at most in all: rows first to blocks, then to teams.
-inline int64_t blocks_of(int64_t m, int64_t most, const Boundary& at) {
-    if (at.stride == 0) return m < most ? m : most;
+// Blocks of a launch over m rows (alike: all start alike), `most` at most (a multiple of
+// 8), and their teams of `team` threads, `threads` at most in all: rows first to blocks,
+// then to teams.
+inline int64_t blocks_of(int64_t m, int64_t most, bool alike) {
+    if (alike) return m < most ? m : most;
     const int64_t blocks = (m < 8 ? 8 : m) / 8 * 8;
     return blocks < most ? blocks : most / 8 * 8;
 }
