@@ -375,15 +375,15 @@ cudaError_t norm_e(const NormArgs& a, bool whole, cudaStream_t st) {
     return launch_after(norm_kernel<T, O, W, E, WARP, true>, grid, threads, 0, st, a);
 }
 
-// Rows to a team from which the ring pays for its start. Measured, teams / a row to a
-// block or warp, us:
-//   whole vectors, fp32   2048 x 2048 (2 rows) 6.0 / 6.2, 1003 x 4096 fp32 (3) 10.8 / 8.1, 1024 x 8000 fp32 (7) 18.8 / 19.3,
-//                         2000 x 7168 (7) 17.6 / 18.5, 16384 x 1024 (8) 16.9 / 20.5, 4096 x 4096 (9) 19.3 / 18.8,
-//                         4096 x 7168 (13) 26.3 / 31.6, 16384 x 7168 (54) 82.9 / 108, 1003 x 4099 fp32 (2) 13.7 / 11.7,
-//                         2000 x 2049 fp32 (2) 14.8 / 10.7
-//   others of bf16        300 x 7167 (1) 7.2 / 6.9, 600 x 4099 (1.3) 8.1 / 7.2, 512 x 7167 (1.7) 9.9 / 12.1, 2000 x 2049 (2.2) 10.5 / 10.8,
-//                         1003 x 7167 (3.3) 15.9 / 21.7, 16384 x 1023 (8) 28.7 / 33.8, 4096 x 4095 (9) 26.8 / 42.3
-constexpr double kLeastRows = 6, kLeastRowsOdd = 1.5;
+// Rows to a team from which the ring pays for its start (for fp32 it is half as many rows
+// deep). Measured, teams / a row to a block or warp, us:
+//   bf16  300 x 7167 (1 row) 6.9 / 6.9, 600 x 4099 (1.3) 6.8 / 7.2, 512 x 7168 (1.7) 5.8 / 5.7, 512 x 7167 8.0 / 12.3, 2048 x 2048 (1.9)
+//         5.4 / 6.1, 800 x 7168 (2.6) 8.3 / 9.4, 2000 x 7168 (7) 15.8 / 18.5, 16384 x 1024 (8) 15.9 / 20.9, 4096 x 4096 (9) 17.3 / 19.0,
+//         4096 x 4095 (9) 21.0 / 42.4, 4096 x 7168 (13) 24.0 / 31.6, 16384 x 7168 (54) 75 / 108
+//   fp32  1003 x 4096 (2.2) 10.3 / 8.9, 1003 x 4099 (2.2) 11.6 / 11.9, 2000 x 2049 (2.2) 12.0 / 10.8, 2000 x 4096 (4.4) 15.5 / 16.8,
+//         1024 x 8000 (7) 16.1 / 19.4
+// and never for the shortest rows: 16384 x 96 5.3 / 5.0, 16384 x 97 8.4 / 5.8.
+constexpr double kLeastRows = 1.25, kLeastRows32 = 3;
 
 // Rows by teams: false where that many rows are too few for it.
 template <typename T, typename O, int E>
@@ -396,7 +396,7 @@ bool rows_e(const NormArgs& a, bool whole, cudaStream_t st, int num_sms, cudaErr
     f.team = team_of(a.n, E);
     const int64_t blocks = blocks_of(a.m, num_sms, f.at.stride == 0);
     f.teams = teams_of(a.m, blocks, f.team, E <= 16 ? 896 : 512);
-    if (static_cast<double>(a.m) < static_cast<double>(blocks * f.teams) * (whole || sizeof(T) == 4 ? kLeastRows : kLeastRowsOdd)) return false;
+    if (static_cast<double>(a.m) < static_cast<double>(blocks * f.teams) * (sizeof(T) == 4 ? kLeastRows32 : kLeastRows)) return false;
     const int threads = f.team * f.teams, stage = threads * E * static_cast<int>(sizeof(T)) * (E <= 16 ? 2 : 1), weights = f.team * E * 8;
     const int ends = whole ? 0 : f.teams * 128 * (E <= 16 ? 2 : 1);     // of a stage
     f.stages = (kNormRoom - weights) / (stage + ends);
@@ -419,7 +419,8 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t st, int num_sms) {
     cudaError_t e;
     if (a.n <= 256 - W) return norm_e<T, O, 8, true>(a, whole, st);
     if (a.n <= 8192 - W ? rows_e<T, O, 16>(a, whole, st, num_sms, e) : rows_e<T, O, 32>(a, whole, st, num_sms, e)) return e;
-    // a row to a warp / to a block, us: 200 x 1000 3.3 / 2.2, 2048 x 1000 5.0 / 4.7, 4000 x 1000 5.5 / 6.9, 8000 x 500 8.7 / 10.5
+    // a row to a warp / to a block, us: 200 x 1000 3.3 / 2.2, 2048 x 1000 5.1 / 4.5, 4000 x 504 3.9 / 4.9, fp32 4000 x 1000 8.0 / 9.3,
+    // 8000 x 504 8.4 / 10.2
     if (a.n <= 1024 - W && a.m > 10 * num_sms) return norm_e<T, O, 32, true>(a, whole, st);
     // few elements to a thread where few rows leave a block alone on its SM (1 x 7168 2.8 us, 12.6 by a
     // loop of 256 threads) and where elements go one by one; 4096 x 7168 takes 31.7 with 32 and 67 with 8,
