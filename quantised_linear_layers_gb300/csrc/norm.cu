@@ -393,7 +393,7 @@ bool rows_e(const NormArgs& a, bool whole, cudaStream_t st, int num_sms, cudaErr
     f.at = boundary_of(a.x, sizeof(T), a.sx, a.m, W);
     const bool y_vec = same_boundary(f.at, boundary_of(a.y, sizeof(O), a.sy, a.m, W)), w_vec = aligned_to(a.w, 16) && aligned_to(a.b, 16);
     auto kern = whole ? norm_rows_kernel<T, O, E, false> : norm_rows_kernel<T, O, E, true>;
-    f.team = team_of(a.n, E);
+    f.team = runs_team_of(a.n, E, W);
     const int64_t blocks = blocks_of(a.m, num_sms, f.at.stride == 0);
     f.teams = teams_of(a.m, blocks, f.team, E <= 16 ? 896 : 512);
     if (static_cast<double>(a.m) < static_cast<double>(blocks * f.teams) * (sizeof(T) == 4 ? kLeastRows32 : kLeastRows)) return false;

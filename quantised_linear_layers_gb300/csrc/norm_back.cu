@@ -381,7 +381,7 @@ cudaError_t back_e(const NormBackArgs& a, cudaStream_t st, int num_sms) {
                dx_vec = same_boundary(f.at, boundary_of(a.dx, sizeof(T), a.sdx, a.m, W)), w_vec = aligned_to(a.w, 16);
     const bool edge = f.at.base != 0 || f.at.stride != 0 || a.n % W != 0 || !dy_vec || !dx_vec || !w_vec;
     auto kern = edge ? norm_back_kernel<T, D, E, true> : norm_back_kernel<T, D, E, false>;
-    f.team = team_of(a.n, E);
+    f.team = runs_team_of(a.n, E, W);
     // With up to two rows to a team of eight blocks, these join their sums as a cluster: one launch less,
     // which takes the host longer than the rows' spread over the SMs saves (one row: 9.3 us of host time
     // with a second kernel, 5.8 without).

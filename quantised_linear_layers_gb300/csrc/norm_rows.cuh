@@ -242,6 +242,8 @@ struct Teams {
     Boundary at;
     bool cluster;              // the blocks are one cluster
 };
+// And for rows in runs of w with Ends.
+inline int runs_team_of(int64_t n, int e, int w) { return n < w ? 32 : team_of(n / w * w, e); }
 // Blocks of a launch over m rows (alike: all start alike), `most` at most (a multiple of
 // 8), and their teams of `team` threads, `threads` at most in all: rows first to blocks,
 // then to teams.
