@@ -354,14 +354,16 @@ __global__ void __launch_bounds__(kThreads) combine_back_kernel(const CombineBac
 // ---------------------------------------------------------------- many tokens
 // The same for many tokens: a team is a warp or a block and goes from token to token, with
 // the runs to come on their way into a ring of S in shared memory, in which each thread
-// copies and reads only what is its own. A token's rows are known one token ahead.
+// copies and reads only what is its own. A token's rows are known one token ahead. For sums of
+// many slots "token" is one of its 2^split pieces of columns, so that all teams have about as
+// much to do.
 constexpr int kRingThreads = 256;
 constexpr int ring_stages(int k) { return k >= 8 ? 3 : (k >= 4 ? 5 : 8); }
 
 struct RingArgs {
     const void *one, *many;    // a row of each token: add (or null), dy; the experts' rows: ys
     int64_t m, n, s_one, s_many;
-    int k;
+    int k, split;
     const int32_t* rows;
     const float* weights;      // or null: 1
     void* out;                 // y, or dys
@@ -380,6 +382,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const Ri
     pdl_launch_dependents();
     pdl_wait_prior();
     const int lane = threadIdx.x & (TEAM - 1), runs = static_cast<int>((p.n + TEAM * W - 1) / (TEAM * W));
+    const int split = !BACK && K > 2 ? p.split : 0, piece = (runs + (1 << split) - 1) >> split;       // runs of a piece; none is empty
+    const int64_t items = p.m << split;
     const int64_t all = p.m * p.k, step = static_cast<int64_t>(gridDim.x) * (kRingThreads / TEAM);
     const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRingThreads / TEAM) + threadIdx.x / TEAM;
     uint8_t* mine = s_ring + threadIdx.x * 16;
@@ -387,16 +391,18 @@ __global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const Ri
     const int64_t used = BACK ? load_one(p.offsets + p.experts, p.bnd, 5, 0) : 0;
 
     // the copies' place in the sequence of runs
-    int64_t f_token = first;
-    int f_run = 0;
+    auto run_of = [&](int64_t i) { return static_cast<int>(i & ((1 << split) - 1)) * piece; };
+    auto end_of = [&](int run) { return run + piece < runs ? run + piece : runs; };
+    int64_t f_item = first;
+    int f_run = run_of(first), f_end = end_of(f_run);
     int32_t f_rows[K], f_next[K];
-    auto rows_at = [&](int32_t (&r)[K], int64_t t) { rows_of<K>(r, p.rows, t, 0, t < p.m ? p.k : 0, all, p.bnd, 2); };
+    auto rows_at = [&](int32_t (&r)[K], int64_t i) { rows_of<K>(r, p.rows, i >> split, 0, i < items ? p.k : 0, all, p.bnd, 2); };
     rows_at(f_rows, first);
     rows_at(f_next, first + step);
     auto fetch = [&](int s) {
         const int64_t c = (static_cast<int64_t>(f_run) * TEAM + lane) * W;
-        if (f_token < p.m && c < p.n) {
-            const T* one = static_cast<const T*>(p.one) + f_token * p.s_one + c;
+        if (f_item < items && c < p.n) {
+            const T* one = static_cast<const T*>(p.one) + (f_item >> split) * p.s_one + c;
             if (p.one != nullptr && QL_IN(p.bnd, 0, one, 16)) copy_async<16>(slot(s, 0), one);
 #pragma unroll
             for (int j = 0; j < K; ++j)
@@ -406,22 +412,24 @@ __global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const Ri
                 }
         }
         copy_commit();                                     // a group for every run, also past the last
-        if (++f_run == runs) {
-            f_run = 0;
-            f_token += step;
+        if (++f_run == f_end) {
+            f_item += step;
+            f_run = run_of(f_item);
+            f_end = end_of(f_run);
 #pragma unroll
             for (int j = 0; j < K; ++j) f_rows[j] = f_next[j];
-            rows_at(f_next, f_token + step);
+            rows_at(f_next, f_item + step);
         }
     };
     int32_t next[K];
     float w_next[K];                                       // (behind the copies they would wait for the ring to fill)
 #pragma unroll
     for (int j = 0; j < K; ++j) next[j] = f_rows[j];
-    weights_of<K>(w_next, p.weights, first, 0, first < p.m ? p.k : 0, p.bnd, 3);
+    weights_of<K>(w_next, p.weights, first >> split, 0, first < items ? p.k : 0, p.bnd, 3);
     for (int s = 0; s < S; ++s) fetch(s);
     int s = 0, turn = 0;
-    for (int64_t t = first; t < p.m; t += step) {
+    for (int64_t item = first; item < items; item += step) {
+        const int64_t t = item >> split;
         int32_t r[K];
         float w[K], dot[K];
 #pragma unroll
@@ -430,9 +438,10 @@ __global__ void __launch_bounds__(kRingThreads, 2) exchange_ring_kernel(const Ri
             w[j] = w_next[j];
             dot[j] = 0.0f;
         }
-        rows_at(next, t + step);
-        weights_of<K>(w_next, p.weights, t + step, 0, t + step < p.m ? p.k : 0, p.bnd, 3);
-        for (int u = 0; u < runs; ++u) {
+        rows_at(next, item + step);
+        weights_of<K>(w_next, p.weights, (item + step) >> split, 0, item + step < items ? p.k : 0, p.bnd, 3);
+        const int u0 = run_of(item), u1 = end_of(u0);
+        for (int u = u0; u < u1; ++u) {
             copy_wait<S - 1>();
             const int64_t c = (static_cast<int64_t>(u) * TEAM + lane) * W;
             if (c < p.n) {
@@ -537,19 +546,26 @@ cudaError_t combine_back_k(const CombineBackArgs& a, cudaStream_t st) {
 
 // Two blocks of ring on every SM, with a token to every warp at least; with fewer, a
 // token to a block if it has work for one. Measured, ring by warps / by blocks / no ring, us:
-//   sums       4096 x 8 of 7168 88 / 85 / 136, 4096 x 2 of 4096 18.7 / 22.9 / 21.9, 16384 x 1 of 4096 51 / 66 / 53,
+//   sums       4096 x 8 of 7168 85 / 84 / 136, 4096 x 2 of 4096 18.7 / 22.9 / 21.9, 16384 x 1 of 4096 51 / 66 / 53,
 //              8192 x 2 of 1024 12.7 / - / 18.5
 //   gradients  163 / 163 / 177, 30.2 / 35.1 / 39.4, 71 / 100 / 116, 17.0 / - / 19.4
 // fewer tokens, by blocks / no ring:
-//   sums       1500 x 8 of 7168 34 / 52, 400 x 8 of 7168 14.4 / 16.8, 512 x 8 of 4096 10.2 / 12.6, 2400 x 2 of 8192 22.4 / 25.0,
+//   sums       1500 x 8 of 7168 34 / 52, 400 x 8 of 7168 13.2 / 16.8, 512 x 8 of 4096 10.2 / 12.6, 2400 x 2 of 8192 22.4 / 25.0,
 //              1024 x 2 of 4096 7.3 / 5.6
 //   gradients  63 / 73, 20.2 / 21.3, 15.5 / 21.2, 32.4 / 41.8, 12.0 / 12.4
 template <typename T, int K, bool BACK>
-bool ring_k(const RingArgs& a, cudaStream_t st, int num_sms, cudaError_t& e) {
+bool ring_k(RingArgs a, cudaStream_t st, int num_sms, cudaError_t& e) {
     constexpr int smem = ring_stages(K) * (K + 1) * kRingThreads * 16;
     const int64_t blocks = static_cast<int64_t>(num_sms) * 2;
     const bool by_warps = a.m >= blocks * (kRingThreads / 32);
     if (!by_warps && (a.m < blocks || a.k * a.n * static_cast<int64_t>(sizeof(T)) < 32 * 1024)) return false;
+    const int64_t teams = blocks * (by_warps ? kRingThreads / 32 : 1), run = (by_warps ? 32 : kRingThreads) * 16 / static_cast<int64_t>(sizeof(T));
+    const int64_t runs = (a.n + run - 1) / run;
+    // pieces: 4096 x 8 of 7168 85 us, by whole tokens 88, 3000 x 4 of 2048 14.4 and 15.7; but with fewer
+    // slots their looking up costs more: 4096 x 2 of 4096 20.5 and 18.7
+    a.split = 0;
+    if (!BACK && K > 2)
+        while (a.split < 3 && (a.m << a.split) < 6 * teams && runs >> a.split >= 4 && runs % (2 << a.split) == 0) ++a.split;
     auto kern = by_warps ? exchange_ring_kernel<T, K, BACK, false> : exchange_ring_kernel<T, K, BACK, true>;
     e = smem > 46 * 1024 ? ensure_smem_attr(reinterpret_cast<const void*>(kern), smem) : cudaSuccess;
     if (e == cudaSuccess) e = launch_after(kern, dim3(static_cast<unsigned>(blocks)), kRingThreads, smem, st, a);
@@ -577,7 +593,7 @@ cudaError_t combine_t(const CombineArgs& a, cudaStream_t st, int num_sms) {
     const bool vec = a.n % W == 0 && rows_aligned(a.ys, sizeof(T), a.sys, a.m * a.k, 16) && rows_aligned(a.y, sizeof(T), a.sy, a.m, 16) &&
                      (a.add == nullptr || rows_aligned(a.add, sizeof(T), a.sadd, a.m, 16));
     cudaError_t e;
-    if (vec && ring<T, false>(RingArgs{a.add, a.ys, a.m, a.n, a.sadd, a.sys, a.k, a.rows, a.weights, a.y, a.sy, nullptr, 0, nullptr,
+    if (vec && ring<T, false>(RingArgs{a.add, a.ys, a.m, a.n, a.sadd, a.sys, a.k, 0, a.rows, a.weights, a.y, a.sy, nullptr, 0, nullptr,
                                        {{a.bnd.s[3], a.bnd.s[0], a.bnd.s[1], a.bnd.s[2], a.bnd.s[4], Span{0, 0}, Span{0, 0}}, a.bnd.status}},
                               st, num_sms, e))
         return e;
@@ -589,7 +605,7 @@ cudaError_t combine_back_t(const CombineBackArgs& a, cudaStream_t st, int num_sm
     const bool vec = a.n % W == 0 && rows_aligned(a.ys, sizeof(T), a.sys, a.m * a.k, 16) && rows_aligned(a.dy, sizeof(T), a.sdy, a.m, 16) &&
                      rows_aligned(a.dys, sizeof(T), a.sdys, a.m * a.k, 16);
     cudaError_t e;
-    if (vec && ring<T, true>(RingArgs{a.dy, a.ys, a.m, a.n, a.sdy, a.sys, a.k, a.rows, a.weights, a.dys, a.sdys, a.offsets, a.experts, a.dweights,
+    if (vec && ring<T, true>(RingArgs{a.dy, a.ys, a.m, a.n, a.sdy, a.sys, a.k, 0, a.rows, a.weights, a.dys, a.sdys, a.offsets, a.experts, a.dweights,
                                       {{a.bnd.s[0], a.bnd.s[1], a.bnd.s[2], a.bnd.s[4], a.bnd.s[5], a.bnd.s[3], a.bnd.s[6]}, a.bnd.status}},
                              st, num_sms, e))
         return e;
