@@ -192,3 +192,17 @@ def test_sums_onto_what_they_are_added_to(ops, m, k, n):
     ys, add, w = rand((m * k, n), BF, 2), rand((m, n), BF, 3), rand((m, k), F, 4)
     want = ops.expert_combine(ys, p, w, add)
     assert torch.equal(ops.expert_combine(ys, p, w, add, out=add), want) and torch.equal(add, want)
+
+
+@pytest.mark.parametrize("m,k,n,dtype", [(2500, 8, 2048, BF), (2500, 7, 2040, BF), (2600, 4, 1000, BF), (2433, 3, 1024, F), (400, 8, 7168, BF), (305, 5, 8200, F),
+                                         (2500, 2, 2048, BF), (2500, 1, 264, BF)])
+def test_many_tokens_take_the_same_sums(ops, m, k, n, dtype):
+    """Whole vectors of many tokens against rows off their boundaries, whose elements go one by
+    one: the same terms in the same order."""
+    p = ops.expert_plan(experts_of(m, k, 16, none=0.2), 16)
+    ys, add, w = rand((m * k, n), dtype, 2), rand((m, n), dtype, 3), rand((m, k), F, 4)
+    room = torch.empty((m * k, n + 1), dtype=dtype, device="cuda")
+    room[:, 1:].copy_(ys)
+    for ww in (w, None):
+        assert torch.equal(ops.expert_combine(ys, p, ww, add), ops.expert_combine(room[:, 1:], p, ww, add))
+    assert torch.equal(ops.expert_combine_backward(add, ys, p, w)[0], ops.expert_combine_backward(add, room[:, 1:], p, w)[0])
