@@ -4,7 +4,7 @@
 // the mean, then sums of d = x - mean and of d^2, whose first corrects the mean's
 // rounding (so rows far from zero lose nothing to it). A row is read once and stays
 // in its threads' registers, as pairs of fp32; bound by memory, and by instructions
-// next to it.
+// next to it. 16384 x 7168 bf16: 75.4 us, 0.92 of a copy's rate; one row 2.8 us, a launch.
 #include "gemm.cuh"
 #include "norm.cuh"
 #include "norm_rows.cuh"
@@ -176,7 +176,10 @@ __global__ void __launch_bounds__(WARP ? 256 : (E <= 8 ? 1024 : 512)) norm_kerne
 // ---------------------------------------------------------------- many rows
 // The same by teams with their rows on the way through shared memory, R rows at a time
 // so that their sums share exchanges and barriers: a row's arithmetic is 6 instructions
-// an element, and a thread's part of the sums 100 a row were it alone.
+// an element, and a thread's part of the sums 100 a row were it alone. Rows are found by
+// index: of the 72 registers that 896 threads have none is left for addresses, and what
+// spills goes to L2, with so little L1 beside the ring (16384 x 7168 75 us, 83 with
+// addresses kept; 4096 x 7167 32 and 37).
 template <typename T, typename O, int E, bool EDGE>
 __global__ void __launch_bounds__(E <= 16 ? 896 : 512) norm_rows_kernel(const NormArgs p, const Teams f, bool y_vec, bool w_vec) {
     constexpr int W = 16 / sizeof(T), U = E / W, H = W / 2, XB = 16;

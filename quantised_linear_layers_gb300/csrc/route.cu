@@ -9,6 +9,10 @@
 // logits, since both scores rise with them: exact. With one, or where a group's
 // score is a sum, fp32 scores with a bound on their error decide wherever the gaps
 // that matter are wider than it; the other tokens are done again in 64 bits.
+//
+// Bound by instructions, 500 to 1000 a token (memory would take 16384 x 256 fp32 2.6 us): 8 of
+// 256 experts for 16384 tokens 11.5 us, with a bias 13.2, by groups of sums 17.4, the
+// gradient 8 to 12; one token 3 us, a launch.
 #include "route.cuh"
 
 #include "rows.cuh"
