@@ -223,6 +223,67 @@ def test_captured_graphs_follow_their_inputs(pkg, m, n):
                 assert torch.equal(a, b)
 
 
+def captured_step(step):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    return g, out
+
+
+@pytest.mark.parametrize("m,n", [(5, 96), (700, 1032)])
+def test_a_captured_training_step(pkg, m, n):
+    """Forward and gradients of norm, routing and the exchange in one graph, on new inputs."""
+    def values(seed):
+        return [rand((m, n), F, seed), 1 + rand((n,), F, seed + 1, 0.2), rand((n,), F, seed + 2, 0.1), rand((16, n), F, seed + 3, n ** -0.5), rand((n,), F, seed + 4)]
+    leaves = [t.requires_grad_() for t in values(0)]
+
+    def step():
+        x, gamma, beta, router, mix = leaves
+        h = pkg.norm.layer_norm(x, gamma, beta)
+        weights, experts = pkg.moe.route(torch.nn.functional.linear(h, router), 4, score="sigmoid")
+        plan = pkg.ops.expert_plan(experts, 16)
+        y = pkg.moe.combine(pkg.moe.dispatch(h, plan) * mix, plan, weights, x)
+        return [y.detach(), *torch.autograd.grad(y.square().mean(), leaves)]
+    g, out = captured_step(step)
+    for seed in (10, 20):
+        with torch.no_grad():
+            for t, v in zip(leaves, values(seed)):
+                t.copy_(v)
+        want = step()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
+def test_the_layer_in_a_captured_training_step(pkg):
+    torch.manual_seed(0)
+    layer = pkg.moe.FP4MoE(64, 96, 8, 2, device="cuda")
+    x = rand((70, 64), BF, 1).requires_grad_()
+    leaves = [x, layer.norm.weight, layer.norm.bias, layer.router.weight, layer.up.weight, layer.down.weight]
+
+    def step():
+        y = layer(x)
+        return [y.detach(), *torch.autograd.grad(y.float().square().mean(), leaves)]
+    g, out = captured_step(step)
+    for seed in (2, 3):
+        with torch.no_grad():
+            x.copy_(rand((70, 64), BF, seed))
+            layer.up.weight.mul_(1.25)
+        want = step()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+    assert pkg.ops.device_status() == 0
+
+
 def test_streams_and_threads(pkg):
     """Calls at once from threads with streams of their own equal the same calls alone."""
     sets = [inputs(m, n, s) for s, (m, n) in enumerate(((1000, 1032), (300, 520), (2500, 264), (40, 4096)))]
