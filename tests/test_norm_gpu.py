@@ -204,3 +204,17 @@ def test_rows_past_32_bits(ops, n):
     assert torch.equal(got, want) and torch.equal(far, stats)
     for a, c in zip(ops.layer_norm_backward(dy, x, stats, w), ops.layer_norm_backward(dy.contiguous(), x.contiguous(), stats, w)):
         assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("m,n", [(700, 1003), (1300, 520), (2000, 261), (400, 8201)])
+@pytest.mark.parametrize("x_dtype,out", [(BF, BF), (F, F), (F, BF), (BF, F)])
+def test_many_rows_that_start_anywhere(ops, m, n, x_dtype, out):
+    """x and dy with starts of their own, alike in all rows or in none, and the first and the last
+    element of their memory among them."""
+    w, b = params(n, F)
+    for i, (x_first, x_wide, dy_first, dy_wide) in enumerate(((1, n + 1, 0, n), (0, n, 1, n + 1), (3, n + 8 - n % 8, 5, n + 9), (7, n + 7, 7, n + 7))):
+        x, dy = (torch.empty(f + (m - 1) * s + n, dtype=d, device="cuda")[f:].as_strided((m, n), (s, 1), f)
+                 for f, s, d in ((x_first, x_wide, x_dtype), (dy_first, dy_wide, out)))
+        x.copy_(acts(m, n, x_dtype, i))
+        dy.copy_(1e-3 * acts(m, n, out, i + 9))
+        check(ops, x, w, b, out, dy=dy)
