@@ -69,6 +69,21 @@ Matrix result(PyObject* o, int64_t m, int64_t n, at::ScalarType type, const at::
     r.ld = m > 1 ? r.t.stride(0) : n;
     return r;
 }
+// Two new tensors of 4-byte elements that live and die together, in one storage: an allocation
+// is a fifth of a small call's host time (routing of one token 4.5 -> 3.6 us, a plan 4.7 -> 3.7).
+struct Two {
+    at::Tensor a, b;
+};
+Two new_two(at::IntArrayRef a_shape, at::ScalarType a_type, at::IntArrayRef b_shape, at::ScalarType b_type, const at::Device& d) {
+    const int64_t room = (c10::multiply_integers(a_shape) + 3) / 4 * 4;
+    Two r;
+    r.a = new_tensor({room + c10::multiply_integers(b_shape)}, a_type, d);
+    r.b = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(r.a.storage()), r.a.key_set(), c10::scalarTypeToTypeMeta(b_type));
+    r.b.unsafeGetTensorImpl()->set_storage_offset(room);
+    r.b.unsafeGetTensorImpl()->set_sizes_contiguous(b_shape);
+    r.a.unsafeGetTensorImpl()->set_sizes_contiguous(a_shape);
+    return r;
+}
 bool cuda_contiguous(PyObject* o, at::ScalarType type, const at::Device& d) {
     if (!THPVariable_Check(o)) return false;
     const at::Tensor& t = THPVariable_Unpack(o);
@@ -169,8 +184,9 @@ PyObject* f_layer_norm_backward(Args a) {
     c10::DataPtr ws;
     size_t size = 0;
     if (sums) {
-        dw = new_tensor({x.n}, at::kFloat, d);
-        db = new_tensor({x.n}, at::kFloat, d);
+        const Two two = new_two({x.n}, at::kFloat, {x.n}, at::kFloat, d);
+        dw = two.a;
+        db = two.b;
         size = layers.norm_back_ws(x.m, x.n);
         if (size > 0) ws = scratch(static_cast<int64_t>(size));
     }
@@ -203,7 +219,8 @@ PyObject* f_route(Args a) {
         value_error("groups must divide the experts, kept be between 1 and groups, group_best 1 or 2");
     c10::cuda::CUDAGuard guard(d);
     const int experts = static_cast<int>(l.n < INT32_MAX ? l.n : INT32_MAX);
-    at::Tensor w = new_tensor({l.m, k}, at::kFloat, d), e = new_tensor({l.m, k}, at::kInt, d);
+    const Two o = new_two({l.m, k}, at::kFloat, {l.m, k}, at::kInt, d);
+    const at::Tensor &w = o.a, &e = o.b;
     status("expert_route", layers.route(l.t.data_ptr(), l.code, l.m, experts, l.ld, bias, k, small_integer(a[3]), groups, kept, best,
                                         truth(a[7]), real(a[8]), w.data_ptr<float>(), e.data_ptr<int32_t>(),
                                         stream_of(d)));
@@ -239,7 +256,8 @@ PyObject* f_plan(Args a) {
     const size_t size = layers.plan_ws(slots, experts);
     c10::DataPtr ws;
     if (size > 0) ws = scratch(static_cast<int64_t>(size));
-    at::Tensor offsets = new_tensor({static_cast<int64_t>(experts) + 1}, at::kInt, d), rows = new_tensor(e.sizes(), at::kInt, d);
+    const Two two = new_two({static_cast<int64_t>(experts) + 1}, at::kInt, e.sizes(), at::kInt, d);
+    const at::Tensor &offsets = two.a, &rows = two.b;
     status("expert_plan", layers.plan(e.data_ptr<int32_t>(), slots, experts, offsets.data_ptr<int32_t>(), rows.data_ptr<int32_t>(),
                                       ws.get(), size, stream_of(d)));
     PyObject* args[2] = {THPVariable_Wrap(offsets), THPVariable_Wrap(rows)};
