@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
             const uint32_t v = (kept >> lane) & 1u ? kUnreached : group;
             const uint32_t most = __reduce_max_sync(kAll, v);
             if (most == kUnreached) break;
-            kept |= 1u << (__ffs(__ballot_sync(kAll, v == most)) - 1);
+            const uint32_t all = __ballot_sync(kAll, v == most);
+            kept |= all & (0u - all);                      // the first of them
             last = most;
         }
         if (scored && !nan) {
@@ -626,25 +627,26 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
     sorted[NV * 32 + lane] = kUnreached;
     __syncwarp();
     uint32_t head = key[0], my_key = kUnreached, last = kUnreached;
-    int place = lane, my_place = 0;                        // of the lane's next key in `sorted`
+    int place = lane;                                      // of the lane's next key in `sorted`
+    int* places = s_list[warp];                            // of the choices
+    const uint32_t below = (1u << lane) - 1u;
     for (int r = 0; r < p.k; ++r) {
         last = __reduce_max_sync(kAll, head);
         if (last == kUnreached) break;
-        const int from = __ffs(__ballot_sync(kAll, head == last)) - 1;
-        const int at = __shfl_sync(kAll, place, from);
-        if (lane == r) {
-            my_key = last;
-            my_place = at;
-        }
-        if (lane == from) {
+        const bool has = head == last;
+        const uint32_t all = __ballot_sync(kAll, has);
+        if (lane == r) my_key = last;
+        if (has && (all & below) == 0) {                   // the first of them
+            places[r] = place;
             place += 32;
             head = sorted[place];
         }
     }
+    __syncwarp();
     int mine = -1;                                         // lane j: the j-th choice
     if (my_key != kUnreached) {
         // the (place - greater ones)-th of its lane's experts with that key
-        const int first = (my_place & 31) * NV;
+        const int my_place = places[lane], first = (my_place & 31) * NV;
         int skip = my_place >> 5;
         uint32_t of[NV];
         load_words<NV>(of, keys + first);
