@@ -187,15 +187,22 @@ __device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
 }
 
 // By how much the choice with logit l1 and bias b1 is greater than the one with l2, b2, told
-// by differences, which fp32 has to a share of themselves, and how far off that may be:
-//   s1 - s2 = s1 (1 - s2) (1 - e^(l2 - l1)) for a sigmoid, s1 (1 - e^(l2 - l1)) for a softmax
-// within 2^-20 and 2^-17 of it, against b2 - b1.
+// by differences, which fp32 has to a share of themselves, and how far off that may be. With
+// hi the greater logit and x = lo - hi, never positive,
+//   s(hi) - s(lo) = s(hi) (1 - s(lo)) (1 - e^x) for a sigmoid, s(hi) (1 - e^x) for a softmax
+// against b2 - b1. x's rounding moves 1 - e^x by 2^-24 of itself (x e^x / (1 - e^x) is 1 at
+// most; for the lesser logit first it would go whole into the exponential). expf is within 2^-22
+// of itself, expm1f within 2^-23, and divisions, products and sums add 2^-24 each:
+// 16 * 2^-24 for the sigmoid; for the softmax 11 * 2^-24, the 37 * 2^-24 of its total (below) and
+// the rounding of hi - top. `off` has a quarter more, for the roundings of `by` and of itself;
+// db's own is 2^-24 of it. What underflows or overflows on the way is below 2^-126.
 template <bool SIGMOID>
 __device__ __forceinline__ void add_difference(float l1, float b1, float l2, float b2, float top, float total, float& by, float& off) {
-    const float ds = -expm1f(l2 - l1) * (SIGMOID ? 1.0f / ((1.0f + expf(-l1)) * (1.0f + expf(l2))) : expf(l1 - top) / total);
-    const float db = b2 - b1;
+    const float hi = fmaxf(l1, l2), lo = fminf(l1, l2);
+    const float gap = -expm1f(lo - hi) * (SIGMOID ? 1.0f / ((1.0f + expf(-hi)) * (1.0f + expf(lo))) : expf(hi - top) / total);
+    const float ds = l1 < l2 ? -gap : gap, db = b2 - b1;
     by += ds - db;
-    off += fabsf(ds) * (SIGMOID ? 0x1p-20f : 0x1p-17f) + fabsf(db) * 0x1p-22f;
+    off += gap * (SIGMOID ? 0x1.4p-20f : fmaf(top - hi, 0x1.2p-24f, 0x1p-18f)) + fabsf(db) * 0x1p-22f + 0x1p-126f;
 }
 template <bool SIGMOID>
 __device__ __forceinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {

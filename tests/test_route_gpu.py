@@ -221,3 +221,78 @@ def test_a_truth_that_has_none_is_an_error(ops):
     with pytest.raises(RuntimeError):
         ops.route(x, 2, renormalise=torch.ones(2))
     assert ops.route(x, 2)[1].tolist() == [[0, 1]] * 2
+
+
+def far_pairs(lo, hi, n, seed):
+    """[rounds * n / 2, n] logits that reach one pair of experts each, (p, n / 2 + p), of opposite signs
+    and lo to hi from zero, and a bias whose difference takes back that of their scores but for a few
+    2^-24."""
+    g = torch.Generator().manual_seed(seed)
+    half, rounds = n // 2, 64
+    size = lo + (hi - lo) * torch.rand((2, half), generator=g)
+    bias = torch.cat([torch.ones(half), torch.zeros(half)])
+    x = torch.full((rounds, half, n), -math.inf)
+    p = torch.arange(half)
+    low = -size[0]
+    bias[half:] = (torch.sigmoid(low.double()) + 1 - torch.sigmoid(size[1].double())).float()
+    for r in range(rounds):
+        x[r, p, p] = low + torch.randint(-8, 9, (half,), generator=g) * 2.0 ** -21
+        x[r, p, half + p] = size[1] + torch.randint(-8, 9, (half,), generator=g) * 2.0 ** -20
+    bias[half:] += torch.randint(-3, 4, (half,), generator=g) * 2.0 ** -24
+    turned = torch.rand(half, generator=g) < 0.5                  # the far one on the other side
+    swap = torch.where(turned, half + p, p)
+    order = torch.cat([swap, (swap + half) % n])
+    return x.view(-1, n)[:, order].cuda(), bias[order].cuda()
+
+
+@pytest.mark.parametrize("lo,hi", [(0.5, 8), (8, 12), (12, 16), (16, 20), (20, 42), (42, 100)])
+@pytest.mark.parametrize("n,how", [(64, {}), (512, {}), (64, dict(groups=2, kept=1)), (64, dict(groups=2, kept=1, group_best=2))])
+def test_far_logits_whose_bias_brings_them_together(ops, lo, hi, n, how):
+    """A choice between logits far apart on both sides of zero, whose scores with the bias differ by
+    less than fp32 can tell: as in 64 bits."""
+    x, bias = far_pairs(lo, hi, n, n + int(lo))
+    for k in (1, 2):
+        _, e = ops.route(x, k, bias, "sigmoid", **how)
+        c = (torch.sigmoid(x.double()) + bias.double()).masked_fill(torch.isneginf(x), -math.inf)
+        order = torch.sort(c, dim=1, descending=True, stable=True)[1][:, :k].to(torch.int32)
+        if how and k == 2:                                        # the other group's is out of reach
+            order[:, 1] = -1
+        wrong = (e != order).any(1)
+        assert not wrong.any(), f"{int(wrong.sum())} of {len(wrong)} tokens choose otherwise"
+    # the same pair as the best of groups of two
+    if not how:
+        size = 4
+        both = x.new_zeros((x.shape[0], size))
+        pair = torch.sort(torch.isneginf(x).to(torch.int8), dim=1, stable=True)[1][:, :2]
+        both[:, 0::2] = torch.gather(x, 1, pair)                  # experts 0 and 2; 1 and 3 alike
+        for i in range(0, x.shape[0], max(1, x.shape[0] // 64)):
+            b = torch.zeros(size, device="cuda")
+            b[0::2] = bias[pair[i]]
+            check(ops, both[i:i + 1], 2, b, "sigmoid", 2, 1, 2)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_softmax_scores_far_apart(ops, seed):
+    """The same for a softmax: experts far below the best, whose scores a bias brings together."""
+    n = 32
+    g = torch.Generator().manual_seed(seed)
+    x = torch.full((400, n), -math.inf)
+    x[:, 0] = 0.0
+    x[:, 1] = -2 * torch.rand(400, generator=g)
+    x[:, 2] = -(1 + 60 * torch.rand(400, generator=g))
+    x[:, 3] = -(1 + 60 * torch.rand(400, generator=g))
+    s = torch.softmax(x.double(), 1)
+    for a, b in ((0, 2), (1, 3), (2, 3)):
+        for t in range(0, 400, 10):
+            bias = torch.zeros(n)
+            bias[a], bias[b] = 0.0, float(s[t, a] - s[t, b]) + int(torch.randint(-2, 3, (1,), generator=g)) * 2.0 ** -25
+            check(ops, x[t:t + 1].cuda(), 2, bias.cuda(), "softmax")
+
+
+def test_pairs_that_differences_told_wrongly(ops):
+    """c is (1.00000000, 1.00000001) and (0.99980920, 0.99980920), the second 1e-9 above the first."""
+    for l, b, best in (((-19.763317, 17.257856), (1.0, 4.191575e-08), 1), ((-8.113878, 8.564082), (0.99950993, 0.0), 1)):
+        x, bias = torch.tensor([l], device="cuda"), torch.tensor(b, device="cuda")
+        assert check(ops, x, 1, bias, "sigmoid")[1].item() == best
+        check(ops, x, 2, bias, "sigmoid")
+        check(ops, x.flip(1), 1, bias.flip(0), "sigmoid")
