@@ -180,10 +180,18 @@ __device__ __forceinline__ float rcp_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// The least key that is not surely below one by more than `wide`.
-__device__ __forceinline__ uint32_t near_key(uint32_t key, float wide) {
-    const float v = value_of(key) - wide;
+// A choice c = s + b is off by what its score is (`off` at most) and by its own rounding, 2^-24
+// of it, whatever the other experts' biases are. c1 is greater than c2 in earnest where it
+// seems so by more than this: c2's rounding is 2^-24 (|c1| + c1 - c2) at most.
+__device__ __forceinline__ float wide_of(float c1, float off) { return 2.05f * fmaf(fabsf(c1), 0x1p-24f, off); }
+// The least key that is not surely below one.
+__device__ __forceinline__ uint32_t near_key(uint32_t key, float off) {
+    const float v = value_of(key) - wide_of(value_of(key), off);
     return v == v ? key_of(v) : kNanKey + 1;
+}
+// Whether the choice with key k1 is not surely greater than the one with k2.
+__device__ __forceinline__ bool close_keys(uint32_t k1, uint32_t k2, float off) {
+    return !(value_of(k1) - value_of(k2) > wide_of(value_of(k1), off));
 }
 
 // By how much the choice with logit l1 and bias b1 is greater than the one with l2, b2, told
@@ -232,7 +240,7 @@ __device__ __forceinline__ int take_best(uint32_t* keys, int first, int size, ui
 // Whether group a's score is surely greater than group z's, by the differences of their best
 // experts, whom no other of their groups is near. Takes those out of keys.
 template <typename T, bool SIGMOID>
-__device__ __noinline__ bool surely_greater_group(const RouteArgs& p, const T* row, uint32_t* keys, int a, int z, float bound, float top, float total) {
+__device__ __noinline__ bool surely_greater_group(const RouteArgs& p, const T* row, uint32_t* keys, int a, int z, float score_off, float top, float total) {
     const int size = p.experts / p.groups;
     float by = 0.0f, off = 0.0f;
     uint32_t ka = kUnreached, kz = kUnreached;
@@ -248,7 +256,7 @@ __device__ __noinline__ bool surely_greater_group(const RouteArgs& p, const T* r
         uint32_t ra, rz;
         take_best(keys, a * size, size, ra);
         take_best(keys, z * size, size, rz);
-        if ((ra > kNanKey && !(value_of(ka) - value_of(ra) > 2.05f * bound)) || (rz > kNanKey && !(value_of(kz) - value_of(rz) > 2.05f * bound))) return false;
+        if ((ra > kNanKey && close_keys(ka, ra, score_off)) || (rz > kNanKey && close_keys(kz, rz, score_off))) return false;
     }
     return by > off;
 }
@@ -297,7 +305,7 @@ __device__ __forceinline__ void best_of_warp(double& v, int& at) {
 // of the experts those near the border, if differences do not tell those apart.
 // list: 64 ints of shared memory.
 template <typename T, bool SIGMOID>
-__device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t* keys, int* list, float bound, float top, float total, uint32_t sure,
+__device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t* keys, int* list, float score_off, float top, float total, uint32_t sure,
                                         uint32_t open) {
     const int lane = threadIdx.x & 31, size = p.experts / p.groups;
     Choice64<T, SIGMOID> c64{p, static_cast<const T*>(p.logits) + t * p.sl};
@@ -361,7 +369,7 @@ __device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t*
     first = count;
     bool few = true;
     if (p.bias != nullptr && count == p.k && last > kNanKey) {
-        const uint32_t least = near_key(last, 2.05f * bound);
+        const uint32_t least = near_key(last, score_off);
         for (int e0 = 0; e0 < p.experts && few; e0 += 32) {
             const bool near = e0 + lane < p.experts && keys[e0 + lane] >= least;
             const uint32_t all = __ballot_sync(kAll, near);
@@ -401,7 +409,7 @@ __device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t*
         // more than a warp's worth: every round in 64 bits, those that were taken by keys among them
         if (lane < first) keys[list[lane]] = last;
         __syncwarp();
-        const uint32_t least = near_key(last, 2.05f * bound);
+        const uint32_t least = near_key(last, score_off);
         if (!ready) c64.prepare(top);
         for (int r = 0; r < p.k; ++r) {
             double v = -INFINITY;
@@ -451,17 +459,14 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
     float l[NV], b[NV];
     float* buf = reinterpret_cast<float*>(s_keys[warp]);
     load_row<T, NV, VEC>(l, row, p.experts, 0.0f, buf, p.bnd, 0);
-    float odd = 0.0f, b_most = 0.0f;                       // odd: NaN if anything is not finite
+    float odd = 0.0f;                                      // NaN if anything is not finite
 #pragma unroll
     for (int i = 0; i < NV; ++i) odd = fmaf(l[i], 0.0f, odd);
     if (biased) {
         if (VEC && aligned_to(p.bias, 16)) load_row<float, NV, true>(b, p.bias, p.experts, 0.0f, buf, p.bnd, 1);
         else load_row<float, NV, false>(b, p.bias, p.experts, 0.0f, buf, p.bnd, 1);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            odd = fmaf(b[i], 0.0f, odd);
-            b_most = fmaxf(b_most, fabsf(b[i]));
-        }
+        for (int i = 0; i < NV; ++i) odd = fmaf(b[i], 0.0f, odd);
     }
     const bool special = __any_sync(kAll, odd != 0.0f);
 
@@ -522,21 +527,14 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < NV; ++i) key[i] = in(i) ? key[i] : kUnreached;
     }
-    // How far a choice in fp32 may be off. 2^(x log2 e) is within 2^-22 + 1.5 |x| 2^-24 of e^x
+    // How far a score in fp32 may be off. 2^(x log2 e) is within 2^-22 + 1.5 |x| 2^-24 of e^x
     // (the approximation; the product and the constant in it): by that a sigmoid moves by
     // 0.29 * 2^-22 at most, the sum and the reciprocal add 2^-24 and 2^-23 of it: 1.04 * 2^-22
     // (measured over 2^30 logits in [-60, 60]: 0.49 * 2^-22). A
-    // softmax's term at x below the largest is off by (2 + 0.75 x) 2^-23 exp(-x), 2^-22 at
+    // softmax's term at x below the largest is off by (2 + 1.13 x) 2^-23 exp(-x), 2^-22 at
     // most, its sum of up to 512 by 21 roundings and 2^-20 of itself, so s by 2^-18.5 of
-    // the largest. c's own rounding is 2^-24 of s + |b|. Two choices differ as they seem to
-    // where that is by more than `wide`; two sums of two of them, each rounded once more, by
-    // more than 5 bounds.
-    float bound = 0.0f;
-    if (scored) {
-        b_most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b_most)));
-        bound = (SIGMOID ? 0x1.4p-22f + 0x1p-24f : 0x1p-18f / total) + b_most * 0x1p-24f;
-    }
-    const float wide = 2.05f * bound;
+    // the largest.
+    const float score_off = SIGMOID ? 0x1.4p-22f : 0x1p-18f / total;
 
     if (grouped) {
         uint32_t best = 0, next = 0;
@@ -582,33 +580,37 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
         // lane g has group g's
         uint32_t group = lane < p.groups ? best : kUnreached;
         if (sums && lane < p.groups && next > kNanKey) group = key_of(value_of(best) + value_of(next));
-        uint32_t kept = 0, last = 0;
+        uint32_t kept = 0;
         for (int r = 0; r < p.kept; ++r) {
             const uint32_t v = (kept >> lane) & 1u ? kUnreached : group;
             const uint32_t most = __reduce_max_sync(kAll, v);
             if (most == kUnreached) break;
             const uint32_t all = __ballot_sync(kAll, v == most);
             kept |= all & (0u - all);                      // the first of them
-            last = most;
         }
         if (scored && !nan) {
-            // the groups near the border: `five` around the best that stays out and the last that stays
-            const uint32_t out = __reduce_max_sync(kAll, (kept >> lane) & 1u ? kUnreached : group);
-            const float five = 5.0f * bound;
-            if (out > kNanKey && !(value_of(last) - value_of(out) > five)) {
-                const bool above = group > kNanKey && value_of(group) - value_of(out) > five;
-                const bool near = group > kNanKey && !above && !(value_of(last) - value_of(group) > five);
+            // what a group's score may be: its choices' errors, its sum's rounding and the ends' own
+            const bool in_reach = group > kNanKey, stays = ((kept >> lane) & 1u) != 0u;
+            const float score = value_of(group);
+            const float off = fmaf(fabsf(value_of(best)) + (sums && next > kNanKey ? fabsf(value_of(next)) : 0.0f), 0x1p-22f, 2.1f * score_off);
+            const float low = score - off, high = score + off;
+            const uint32_t least = low == low ? key_of(low) : kNanKey + 1, most = high == high ? key_of(high) : kAll;
+            // the groups near the border between the best that stays out and the last that stays
+            const uint32_t out = __reduce_max_sync(kAll, in_reach && !stays ? most : kUnreached);
+            const uint32_t last = __reduce_min_sync(kAll, stays ? least : kAll);
+            if (out >= last) {
+                const bool above = stays && least > out, near = in_reach && !above && most >= last;
                 const uint32_t sure = __ballot_sync(kAll, above), open = __ballot_sync(kAll, near);
                 store_words<NV>(s_keys[warp] + e0, key);
                 __syncwarp();
                 const uint32_t kept_near = open & kept, out_near = open & ~kept;
                 const bool told = __popc(kept_near) == 1 && __popc(out_near) == 1 &&
-                                  surely_greater_group<T, SIGMOID>(p, row, s_keys[warp], __ffs(kept_near) - 1, __ffs(out_near) - 1, bound, top, total);
+                                  surely_greater_group<T, SIGMOID>(p, row, s_keys[warp], __ffs(kept_near) - 1, __ffs(out_near) - 1, score_off, top, total);
                 if (!told) {
                     __syncwarp();
                     store_words<NV>(s_keys[warp] + e0, key);
                     __syncwarp();
-                    route_open<T, SIGMOID>(p, t, s_keys[warp], s_list[warp], bound, top, total, sure, open);
+                    route_open<T, SIGMOID>(p, t, s_keys[warp], s_list[warp], score_off, top, total, sure, open);
                     return;
                 }
                 __syncwarp();
@@ -668,23 +670,22 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
     if (biased && !nan) {
         // gaps between choices next to one another, and from the last to what stays out
         const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
-        bool unsure = lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide);
-        unsure |= last > kNanKey && head >= near_key(last, wide);
-        if (__any_sync(kAll, unsure)) {
+        const bool ahead = lane < p.k - 1 && key2 > kNanKey && close_keys(my_key, key2, score_off);
+        const uint32_t least = near_key(last, score_off);
+        const bool near = last > kNanKey && head >= least;
+        if (__any_sync(kAll, ahead || near)) {
             // the same logit and bias are a tie in any precision; others by their differences
             const float b1 = mine >= 0 ? load_one(p.bias + mine, p.bnd, 1, 0.0f) : 0.0f;
             const float lg2 = __shfl_down_sync(kAll, lg, 1), b2 = __shfl_down_sync(kAll, b1, 1);
             const float llast = __shfl_sync(kAll, lg, p.k - 1), blast = __shfl_sync(kAll, b1, p.k - 1);
             // my own next in line, then my lane's experts that stay out against the last choice
             float l1 = lg, bb1 = b1, l2 = lg2, bb2 = b2;
-            bool ask = unsure && lane < p.k - 1 && key2 > kNanKey && !(value_of(my_key) - value_of(key2) > wide);
-            const bool near = last > kNanKey && head >= near_key(last, wide);
-            unsure = false;
+            bool ask = ahead, unsure = false;
 #pragma unroll 1
             for (int i = -1; i < (near ? NV : 0); ++i) {
                 if (i >= 0) {
                     const int e = e0 + i;
-                    ask = keys[e] >= near_key(last, wide) && keys[e] <= last;
+                    ask = keys[e] >= least && keys[e] <= last;
                     if (!ask) continue;
                     l1 = llast;
                     bb1 = blast;
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
             }
             if (__any_sync(kAll, unsure)) {
                 __syncwarp();
-                route_open<T, SIGMOID>(p, t, keys, s_list[warp], bound, top, total, kAll, 0u);
+                route_open<T, SIGMOID>(p, t, keys, s_list[warp], score_off, top, total, kAll, 0u);
                 return;
             }
         }

@@ -296,3 +296,46 @@ def test_pairs_that_differences_told_wrongly(ops):
         assert check(ops, x, 1, bias, "sigmoid")[1].item() == best
         check(ops, x, 2, bias, "sigmoid")
         check(ops, x.flip(1), 1, bias.flip(0), "sigmoid")
+
+
+def test_a_large_bias_tells_with_its_own_error(ops):
+    """Biases of any size beside small ones: a choice is as uncertain as its own scores are."""
+    n, g = 64, torch.Generator().manual_seed(12)
+    x = logits_of(300, n, F, 3)
+    for big in (-1e9, 1e9, -math.inf, -1e38, 3e38, 2.0 ** 23, -2.0 ** 24):
+        bias = 0.1 * torch.randn(n, generator=g)
+        bias[torch.randperm(n, generator=g)[:9]] = big
+        for score in ("sigmoid", "softmax"):
+            for how in ({}, {"groups": 8, "kept": 4, "group_best": 2}, {"groups": 8, "kept": 3}):
+                check(ops, x, 6, bias.cuda(), score, **how)
+    # a group's two that cancel
+    bias = 0.1 * torch.randn(n, generator=g)
+    bias[0:8:4] = torch.tensor([2.0 ** 24, -2.0 ** 24])
+    bias[1:4] = bias[5:8] = -math.inf
+    for score in ("sigmoid", "softmax"):
+        check(ops, x, 6, bias.cuda(), score, groups=8, kept=4, group_best=2)
+
+
+@pytest.mark.parametrize("how", [{}, dict(groups=8, kept=4, group_best=2)])
+def test_an_expert_out_of_reach_costs_the_others_nothing(ops, how):
+    """A bias that masks an expert leaves the others to fp32: 16384 tokens in at most three times the time (70 if the mask made all choices uncertain)."""
+    x = logits_of(16384, 256, F, 1)
+    clean = bias_of(256, 2, 0.02)
+
+    def time(bias):
+        call = lambda: ops.route(x, 8, bias, "sigmoid", **how)      # noqa: E731
+        call()
+        best = math.inf
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(20):
+                call()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    for off in (-math.inf, -1e9, 1e9):
+        bias = clean.clone()
+        bias[17] = off
+        assert time(bias) < 3 * time(clean), off
