@@ -69,16 +69,17 @@ Matrix result(PyObject* o, int64_t m, int64_t n, at::ScalarType type, const at::
     r.ld = m > 1 ? r.t.stride(0) : n;
     return r;
 }
-// Two new tensors of 4-byte elements that live and die together, in one storage: an allocation
-// is a fifth of a small call's host time (routing of one token 4.5 -> 3.6 us, a plan 4.7 -> 3.7).
+// Two new tensors of one type that live and die together, in one storage: an allocation is a fifth
+// of a small call's host time (a plan 4.7 -> 3.7 us). Of two types they could not be saved: torch
+// refuses a storage that is read as both.
 struct Two {
     at::Tensor a, b;
 };
-Two new_two(at::IntArrayRef a_shape, at::ScalarType a_type, at::IntArrayRef b_shape, at::ScalarType b_type, const at::Device& d) {
+Two new_two(at::IntArrayRef a_shape, at::IntArrayRef b_shape, at::ScalarType type, const at::Device& d) {
     const int64_t room = (c10::multiply_integers(a_shape) + 3) / 4 * 4;
     Two r;
-    r.a = new_tensor({room + c10::multiply_integers(b_shape)}, a_type, d);
-    r.b = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(r.a.storage()), r.a.key_set(), c10::scalarTypeToTypeMeta(b_type));
+    r.a = new_tensor({room + c10::multiply_integers(b_shape)}, type, d);
+    r.b = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(r.a.storage()), r.a.key_set(), r.a.dtype());
     r.b.unsafeGetTensorImpl()->set_storage_offset(room);
     r.b.unsafeGetTensorImpl()->set_sizes_contiguous(b_shape);
     r.a.unsafeGetTensorImpl()->set_sizes_contiguous(a_shape);
@@ -184,7 +185,7 @@ PyObject* f_layer_norm_backward(Args a) {
     c10::DataPtr ws;
     size_t size = 0;
     if (sums) {
-        const Two two = new_two({x.n}, at::kFloat, {x.n}, at::kFloat, d);
+        const Two two = new_two({x.n}, {x.n}, at::kFloat, d);
         dw = two.a;
         db = two.b;
         size = layers.norm_back_ws(x.m, x.n);
@@ -219,8 +220,7 @@ PyObject* f_route(Args a) {
         value_error("groups must divide the experts, kept be between 1 and groups, group_best 1 or 2");
     c10::cuda::CUDAGuard guard(d);
     const int experts = static_cast<int>(l.n < INT32_MAX ? l.n : INT32_MAX);
-    const Two o = new_two({l.m, k}, at::kFloat, {l.m, k}, at::kInt, d);
-    const at::Tensor &w = o.a, &e = o.b;
+    const at::Tensor w = new_tensor({l.m, k}, at::kFloat, d), e = new_tensor({l.m, k}, at::kInt, d);
     status("expert_route", layers.route(l.t.data_ptr(), l.code, l.m, experts, l.ld, bias, k, small_integer(a[3]), groups, kept, best,
                                         truth(a[7]), real(a[8]), w.data_ptr<float>(), e.data_ptr<int32_t>(),
                                         stream_of(d)));
@@ -256,7 +256,7 @@ PyObject* f_plan(Args a) {
     const size_t size = layers.plan_ws(slots, experts);
     c10::DataPtr ws;
     if (size > 0) ws = scratch(static_cast<int64_t>(size));
-    const Two two = new_two({static_cast<int64_t>(experts) + 1}, at::kInt, e.sizes(), at::kInt, d);
+    const Two two = new_two({static_cast<int64_t>(experts) + 1}, e.sizes(), at::kInt, d);
     const at::Tensor &offsets = two.a, &rows = two.b;
     status("expert_plan", layers.plan(e.data_ptr<int32_t>(), slots, experts, offsets.data_ptr<int32_t>(), rows.data_ptr<int32_t>(),
                                       ws.get(), size, stream_of(d)));

@@ -339,3 +339,14 @@ def test_an_expert_out_of_reach_costs_the_others_nothing(ops, how):
         bias = clean.clone()
         bias[17] = off
         assert time(bias) < 3 * time(clean), off
+
+
+def test_a_batchs_routing_can_be_saved(ops):
+    import io
+    w, e = ops.route(logits_of(5, 20, F), 3)
+    room = io.BytesIO()
+    torch.save({"weights": w, "experts": e}, room)
+    room.seek(0)
+    back = torch.load(room)
+    assert torch.equal(back["weights"], w) and torch.equal(back["experts"], e)
+    assert w.untyped_storage().nbytes() == w.numel() * 4 == e.untyped_storage().nbytes()
