@@ -67,6 +67,7 @@ Matrix result(PyObject* o, int64_t m, int64_t n, at::ScalarType type, const at::
         (n > 1 && r.t.stride(1) != 1) || (m > 1 && r.t.stride(0) < n))
         value_error("out must be of the result's type and shape with contiguous rows on the inputs' device");
     r.ld = m > 1 ? r.t.stride(0) : n;
+    if (!r.t.is_inference()) r.t.unsafeGetTensorImpl()->bump_version();     // autograd sees that what it saved is written over
     return r;
 }
 // Two new tensors of one type that live and die together, in one storage: an allocation is a fifth

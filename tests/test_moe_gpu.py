@@ -341,3 +341,23 @@ def test_calls_refuse_what_does_not_fit(pkg):
     with pytest.raises(ops.QLError):
         ops.layer_norm(x, eps=-1.0)
     assert ops.device_status() == 0
+
+
+def test_a_given_out_counts_as_written(pkg):
+    """Autograd sees that a tensor it saved has been written over; tensors without a version are taken as they are."""
+    ops = pkg.ops
+    p = ops.expert_plan(torch.zeros((4, 1), dtype=torch.int32, device="cuda"), 2)
+    ys = rand((4, 32), F, 2)
+    for write in (lambda t: ops.layer_norm(t, out=t), lambda t: ops.layer_norm_saving(t, out=t), lambda t: ops.expert_dispatch(ys, p, out=t),
+                  lambda t: ops.expert_combine(ys, p, out=t), lambda t: ops.expert_combine(ys, p, None, t, out=t)):
+        a = rand((4, 32), F, 1).requires_grad_() * 2
+        y = a.square().sum()
+        before = a._version
+        write(a.detach())
+        assert a._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    with torch.inference_mode():
+        t = rand((4, 32), F, 1)
+    want = ops.layer_norm(t)
+    assert torch.equal(ops.layer_norm(t, out=t), want)
