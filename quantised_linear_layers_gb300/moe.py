@@ -43,16 +43,21 @@ def route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score:
     return ops.route(logits, k, bias, score, groups, kept, group_best, renormalise, scale)
 
 
+def _tables(plan: ops.ExpertPlan) -> tuple[torch.Tensor, ...]:
+    """A plan's tables as autograd can save them (ExpertPlan(*tables) is the plan again)."""
+    return tuple(t.clone() if t.is_inference() else t for t in (plan.offsets, plan.rows))
+
+
 class _DispatchFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, plan):
-        ctx.plan = plan
+        ctx.save_for_backward(*_tables(plan))
         return ops.expert_dispatch(x, plan)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dxs):
-        return ops.expert_combine(dxs, ctx.plan), None
+        return ops.expert_combine(dxs, ops.ExpertPlan(*ctx.saved_tensors)), None
 
 
 def dispatch(x: torch.Tensor, plan: ops.ExpertPlan) -> torch.Tensor:
@@ -66,18 +71,17 @@ def dispatch(x: torch.Tensor, plan: ops.ExpertPlan) -> torch.Tensor:
 class _CombineFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ys, plan, weights, add):
-        ctx.plan = plan
-        ctx.save_for_backward(ys, weights)
+        ctx.save_for_backward(ys, weights, *_tables(plan))
         return ops.expert_combine(ys, plan, weights, add)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        ys, weights = ctx.saved_tensors
+        ys, weights, *tables = ctx.saved_tensors
         need_ys, _, need_w, need_add = ctx.needs_input_grad
         dys = dw = None
         if need_ys or need_w:
-            dys, dw = ops.expert_combine_backward(dy, ys, ctx.plan, weights)
+            dys, dw = ops.expert_combine_backward(dy, ys, ops.ExpertPlan(*tables), weights)
         return dys if need_ys else None, None, dw if need_w else None, dy if need_add else None
 
 

@@ -361,3 +361,32 @@ def test_a_given_out_counts_as_written(pkg):
         t = rand((4, 32), F, 1)
     want = ops.layer_norm(t)
     assert torch.equal(ops.layer_norm(t, out=t), want)
+
+
+def test_autograd_keeps_the_plan(pkg):
+    """A plan's tables are saved tensors: hooks see them, and tables written again are noticed."""
+    m, k, n = 6, 2, 4
+    e = torch.randint(-1, n, (m, k), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    x, ys, w = rand((m, 32), F, 1), rand((m * k, 32), F, 2), rand((m, k), F, 3)
+    for call, leaf in ((lambda t, p: pkg.moe.dispatch(t, p), x), (lambda t, p: pkg.moe.combine(t, p, w), ys)):
+        leaf = leaf.clone().requires_grad_()
+        plan = pkg.ops.expert_plan(e, n)
+        seen = []
+
+        def pack(t):
+            seen.append(t)
+            return t.cpu()
+        with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.cuda()):
+            y = call(leaf, plan)
+        assert any(t is plan.rows or t.data_ptr() == plan.rows.data_ptr() for t in seen)
+        v = rand(tuple(y.shape), F, 4)
+        got, = torch.autograd.grad(y, leaf, v)
+        want, = torch.autograd.grad(call(leaf, plan), leaf, v)
+        assert torch.equal(got, want)
+        y = call(leaf, plan)
+        plan.rows.fill_(-1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+        with torch.inference_mode():
+            frozen = pkg.ops.expert_plan(e, n)
+        assert torch.equal(torch.autograd.grad(call(leaf, frozen), leaf, v)[0], want)
