@@ -80,12 +80,14 @@ class _CombineFn(torch.autograd.Function):
         ys, weights, *tables = ctx.saved_tensors
         need_ys, _, need_w, need_add = ctx.needs_input_grad
         dys = dw = None
-        if need_ys or need_w:
+        if need_ys and weights is None:
+            dys = ops.expert_dispatch(dy, ops.ExpertPlan(*tables))
+        elif need_ys or need_w:
             dys, dw = ops.expert_combine_backward(dy, ys, ops.ExpertPlan(*tables), weights)
         return dys if need_ys else None, None, dw if need_w else None, dy if need_add else None
 
 
-def combine(ys: torch.Tensor, plan: ops.ExpertPlan, weights: torch.Tensor, add: torch.Tensor | None = None) -> torch.Tensor:
+def combine(ys: torch.Tensor, plan: ops.ExpertPlan, weights: torch.Tensor | None = None, add: torch.Tensor | None = None) -> torch.Tensor:
     """``ops.expert_combine``, differentiable once in ys, weights and add."""
     ops._refuse_forward_mode("combine", ys, weights, add)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (ys, weights, add)):

@@ -390,3 +390,16 @@ def test_autograd_keeps_the_plan(pkg):
         with torch.inference_mode():
             frozen = pkg.ops.expert_plan(e, n)
         assert torch.equal(torch.autograd.grad(call(leaf, frozen), leaf, v)[0], want)
+
+
+def test_sums_without_weights_have_gradients(pkg):
+    m, k, n = 9, 3, 5
+    e = torch.randint(-1, n, (m, k), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    plan = pkg.ops.expert_plan(e, n)
+    ys, add = rand((m * k, 40), F, 2).requires_grad_(), rand((m, 40), F, 3).requires_grad_()
+    v = rand((m, 40), F, 4)
+    y = pkg.moe.combine(ys, plan, None, add)
+    one = pkg.moe.combine(ys, plan, torch.ones((m, k), device="cuda"), add)
+    assert torch.equal(y, one)
+    for a, b in zip(torch.autograd.grad(y, (ys, add), v), torch.autograd.grad(one, (ys, add), v)):
+        assert torch.equal(a, b)
