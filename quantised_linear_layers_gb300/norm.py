@@ -36,7 +36,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     """(x - mean) / sqrt(var + eps) * weight + bias over the last axis of x (bf16 or
     fp32), of ``dtype`` (default: x's). Differentiable once in x, weight and bias."""
     ops._refuse_forward_mode("layer_norm", x, weight, bias)
-    x2 = x.reshape(-1, x.shape[-1])
+    x2 = x.reshape(x.shape[:-1].numel(), x.shape[-1])                  # (no -1: rows may have no columns)
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         y = _LayerNormFn.apply(x2, weight, bias, eps, dtype)
     else:

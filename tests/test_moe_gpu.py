@@ -403,3 +403,15 @@ def test_sums_without_weights_have_gradients(pkg):
     assert torch.equal(y, one)
     for a, b in zip(torch.autograd.grad(y, (ys, add), v), torch.autograd.grad(one, (ys, add), v)):
         assert torch.equal(a, b)
+
+
+def test_norm_of_no_columns(pkg):
+    for shape in ((5, 0), (2, 3, 0), (0, 0), (0, 7), (2, 0, 7)):
+        x = torch.empty(shape, device="cuda", requires_grad=True)
+        w = torch.ones(shape[-1], device="cuda", requires_grad=True)
+        y = pkg.norm.layer_norm(x, w)
+        assert y.shape == shape
+        y.sum().backward()
+        assert x.grad.shape == shape and not w.grad.any()
+        with torch.no_grad():
+            assert pkg.norm.LayerNorm(shape[-1], device="cuda")(x).shape == shape
