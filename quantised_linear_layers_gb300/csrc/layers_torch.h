@@ -67,8 +67,27 @@ Matrix result(PyObject* o, int64_t m, int64_t n, at::ScalarType type, const at::
         (n > 1 && r.t.stride(1) != 1) || (m > 1 && r.t.stride(0) < n))
         value_error("out must be of the result's type and shape with contiguous rows on the inputs' device");
     r.ld = m > 1 ? r.t.stride(0) : n;
-    if (!r.t.is_inference()) r.t.unsafeGetTensorImpl()->bump_version();     // autograd sees that what it saved is written over
     return r;
+}
+// A given out is written while other rows are still read: it may not meet an input in memory, but
+// (in_place) be it, with the same type and stride. Rows side by side in one buffer do not meet.
+void refuse_overlap(const Matrix& out, const Matrix& in, bool in_place, const char* msg) {
+    if (out.m == 0 || out.n == 0 || in.m == 0 || in.n == 0) return;
+    const int64_t eo = out.code == QL_BF16 ? 2 : 4, ei = in.code == QL_BF16 ? 2 : 4;
+    const int64_t po = reinterpret_cast<intptr_t>(out.t.data_ptr()), pi = reinterpret_cast<intptr_t>(in.t.data_ptr());
+    const int64_t wo = out.n * eo, wi = in.n * ei;
+    if (po + (out.m - 1) * out.ld * eo + wo <= pi || pi + (in.m - 1) * in.ld * ei + wi <= po) return;
+    if (in_place && po == pi && out.code == in.code && out.m == in.m && out.n == in.n && out.ld == in.ld) return;
+    const int64_t row = out.m > 1 ? out.ld * eo : in.ld * ei;
+    if (row > 0 && (out.m == 1 || in.m == 1 || out.ld * eo == in.ld * ei)) {
+        const int64_t d = ((pi - po) % row + row) % row;      // from a row of out to the next of in
+        if (d >= wo && d + wi <= row) return;
+    }
+    value_error(msg);
+}
+// A given out has been written: autograd sees where it had saved it.
+void count_write(PyObject* given, const Matrix& out) {
+    if (given != Py_None && !out.t.is_inference()) out.t.unsafeGetTensorImpl()->bump_version();
 }
 // Two new tensors of one type that live and die together, in one storage: an allocation is a fifth
 // of a small call's host time (a plan 4.7 -> 3.7 us). Of two types they could not be saved: torch
@@ -158,6 +177,7 @@ PyObject* f_layer_norm(Args a) {
     const bool saving = truth(a[6]);
     c10::cuda::CUDAGuard guard(d);
     const Matrix y = result(a[4], x.m, x.n, out_type, d);
+    if (a[4] != Py_None) refuse_overlap(y, x, true, "out must be x or away from it");
     at::Tensor stats;
     float* mean = nullptr;
     if (saving) {
@@ -166,6 +186,7 @@ PyObject* f_layer_norm(Args a) {
     }
     status("layer_norm", layers.norm(x.t.data_ptr(), x.code, x.m, x.n, x.ld, w.w, w.b, w.code, eps, y.t.data_ptr(), y.code, y.ld,
                                      saving && x.m > 0 ? mean : nullptr, saving && x.m > 0 ? mean + x.m : nullptr, stream_of(d)));
+    count_write(a[4], y);
     PyObject* oy = THPVariable_Wrap(y.t);
     return saving ? pair(oy, THPVariable_Wrap(stats)) : oy;
 }
@@ -303,8 +324,10 @@ PyObject* f_dispatch(Args a) {
     if (p.m != x.m) value_error("x must have the plan's tokens");
     c10::cuda::CUDAGuard guard(d);
     const Matrix o = result(a[2], p.m * p.k, x.n, x.t.scalar_type(), d);
+    if (a[2] != Py_None) refuse_overlap(o, x, false, "out must be away from x");
     status("expert_dispatch", layers.dispatch(x.t.data_ptr(), x.code, x.m, x.n, x.ld, p.rows.data_ptr<int32_t>(), p.offsets.data_ptr<int32_t>(),
                                               p.experts, static_cast<int>(p.k), o.t.data_ptr(), o.ld, stream_of(d)));
+    count_write(a[2], o);
     return THPVariable_Wrap(o.t);
 }
 
@@ -323,9 +346,14 @@ PyObject* f_combine(Args a) {
         if (add.m != p.m || add.n != ys.n || add.code != ys.code) value_error("add must be a matrix of the result's shape and type on its device");
     }
     const Matrix y = result(a[4], p.m, ys.n, ys.t.scalar_type(), d);
+    if (a[4] != Py_None) {
+        refuse_overlap(y, ys, false, "out must be away from ys");
+        if (a[3] != Py_None) refuse_overlap(y, add, true, "out must be add or away from it");
+    }
     status("expert_combine", layers.combine(ys.t.data_ptr(), ys.code, ys.ld, p.rows.data_ptr<int32_t>(), w,
                                             a[3] != Py_None ? add.t.data_ptr() : nullptr, a[3] != Py_None ? add.ld : 0, p.m, ys.n,
                                             static_cast<int>(p.k), y.t.data_ptr(), y.ld, stream_of(d)));
+    count_write(a[4], y);
     return THPVariable_Wrap(y.t);
 }
 

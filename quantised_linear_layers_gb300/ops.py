@@ -678,7 +678,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
                out: torch.Tensor | None = None, dtype: torch.dtype | None = None) -> torch.Tensor:
     """(x - mean) / sqrt(var + eps) * weight + bias over the rows of x [m, n] (bf16 or
     fp32), in fp32 and rounded once to ``dtype`` (default: out's or x's). weight and
-    bias [n], bf16 or fp32, each may be None; out may be x."""
+    bias [n], bf16 or fp32, each may be None. out may be x, but not overlap it otherwise."""
     return (_fp4 or _load_fp4()).layer_norm(x, weight, bias, eps, out, _type_code(dtype), False)
 
 
@@ -734,7 +734,7 @@ def expert_plan(experts: torch.Tensor, num_experts: int) -> ExpertPlan:
 
 def expert_dispatch(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """xs [tokens * k, n]: x's rows sorted by expert, one for each slot; zeros past the
-    last expert's. Its gradient is ``expert_combine(dxs, plan)``."""
+    last expert's. out may not overlap x. Its gradient is ``expert_combine(dxs, plan)``."""
     return (_fp4 or _load_fp4()).dispatch(x, plan, out)
 
 
@@ -742,7 +742,8 @@ def expert_combine(ys: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor | N
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """y [tokens, n] = add + the sum over a token's slots of weights (fp32 [tokens, k],
     None: 1) times their rows of ys [tokens * k, n], in fp32 and rounded once to ys's
-    type; slots of no expert count for nothing. out may be add."""
+    type; slots of no expert count for nothing. out may be add, but not overlap it otherwise,
+    nor ys."""
     return (_fp4 or _load_fp4()).combine(ys, plan, weights, add, out)
 
 

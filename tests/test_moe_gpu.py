@@ -415,3 +415,28 @@ def test_norm_of_no_columns(pkg):
         assert x.grad.shape == shape and not w.grad.any()
         with torch.no_grad():
             assert pkg.norm.LayerNorm(shape[-1], device="cuda")(x).shape == shape
+
+
+def test_outs_over_inputs_are_refused(pkg):
+    """Rows that others are still read from are not written: but a norm's may be x's own, sums' add's."""
+    ops = pkg.ops
+    room = rand((12, 64), F, 1)
+    p = ops.expert_plan(torch.zeros((4, 1), dtype=torch.int32, device="cuda"), 2)
+    x, ys = room[:4], room[4:8]
+    half, tall = room.view(24, 32)[:4], room.to(BF)
+    for call in (lambda: ops.expert_dispatch(x, p, out=x), lambda: ops.expert_dispatch(x, p, out=room[1:5]), lambda: ops.expert_combine(ys, p, out=ys),
+                 lambda: ops.expert_combine(ys, p, out=room[6:10]), lambda: ops.expert_combine(ys, p, None, x, out=room[1:5]),
+                 lambda: ops.layer_norm(x, out=room[2:6]), lambda: ops.layer_norm(room[:, :32][:4], out=room[:, 16:48][:4]),
+                 lambda: ops.layer_norm(room[:, :32][:4], out=half), lambda: ops.layer_norm(room[:1], out=room[:1].view(BF)[:, :64]),
+                 lambda: ops.layer_norm_saving(tall[:4].view(F), out=tall[:4, :32])):
+        with pytest.raises(ValueError):
+            call()
+    # side by side and row by row in one buffer
+    want = ops.layer_norm(room[:, :32].contiguous())
+    keep = room.clone()
+    assert torch.equal(ops.layer_norm(room[:, :32], out=room[:, 32:]), want) and torch.equal(room[:, :32], keep[:, :32])
+    room.copy_(keep)
+    want = ops.expert_dispatch(room[0:8:2].contiguous(), p)
+    assert torch.equal(ops.expert_dispatch(room[0:8:2], p, out=room[1:8:2]), want) and torch.equal(room[0:8:2], keep[0:8:2])
+    room.copy_(keep)
+    assert torch.equal(ops.expert_combine(x[:, ::2], p, out=room[:4, :32]), ops.expert_combine(keep[:4, ::2], p))      # of a copy
