@@ -659,7 +659,9 @@ ql_status expert_plan(const int32_t* chosen, int64_t slots, int experts, int32_t
                       size_t workspace_bytes, ql_stream_t stream);
 
 /* XS [m * k, n]: row rows[t * k + j] = row t of X [m, n]; rows from offsets[experts] on
- * are zero. rows and offsets are expert_plan's; rows outside [0, m * k) are none. */
+ * are zero. rows and offsets are expert_plan's; rows outside [0, m * k) are none. As in
+ * the calls below m * k <= 2^26, n <= 2^22 and m * ceil(n / 512) < 2^31, or the call is
+ * QL_ERR_UNSUPPORTED. */
 ql_status expert_dispatch(const void* x, ql_dtype dtype, int64_t m, int64_t n, int64_t x_stride_m, const int32_t* rows,
                           const int32_t* offsets, int experts, int k, void* xs, int64_t xs_stride_m, ql_stream_t stream);
 

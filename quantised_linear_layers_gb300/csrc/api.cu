@@ -142,7 +142,7 @@ ql_status gemm_common(const uint8_t* a, int64_t lda, const void* sfa, int64_t sa
 // ---------------------------------------------------------------------------
 constexpr int64_t kInt31 = int64_t(1) << 31;
 constexpr int64_t kMaxSlots = int64_t(1) << 26;     // of an exchange: every chunk of a plan reads the counts of all
-constexpr int64_t kMaxColumns = int64_t(1) << 22;   // 65535 pieces of 128 columns and less
+constexpr int64_t kMaxColumns = int64_t(1) << 22;   // of its rows, whose runs are counted in 32 bits
 
 // Pointers of elements of `bytes`.
 template <typename... P>
@@ -1210,7 +1210,9 @@ ql_status expert_plan(const int32_t* chosen, int64_t slots, int experts, int32_t
 // Sizes of an exchange of rows of n columns between m tokens and m k places.
 static ql_status exchange_sizes(int64_t m, int64_t n, int k, ql_dtype dtype) {
     if (m < 0 || n < 0 || k < 1 || !known_type(dtype)) return QL_ERR_INVALID_ARG;
-    return m >= kInt31 || n > kMaxColumns || m * k > kMaxSlots ? QL_ERR_UNSUPPORTED : QL_OK;
+    if (m >= kInt31 || n > kMaxColumns || m * k > kMaxSlots) return QL_ERR_UNSUPPORTED;
+    // a block has 512 columns of a token, or all: the first outputs that no grid fits have 2 TB
+    return m * ((n + 511) / 512) >= kInt31 ? QL_ERR_UNSUPPORTED : QL_OK;
 }
 
 ql_status expert_dispatch(const void* x, ql_dtype dtype, int64_t m, int64_t n, int64_t x_stride_m, const int32_t* rows,

@@ -507,10 +507,9 @@ unsigned pieces_of(int64_t n, int w, int team, int runs) {
     const int64_t each = static_cast<int64_t>(team) * w * runs;
     return static_cast<unsigned>((n + each - 1) / each);
 }
-bool blocks_of(int64_t m, int team, unsigned pieces, dim3& grid) {
-    const int64_t per = kThreads / team, blocks = (m + per - 1) / per * pieces;
-    grid = dim3(static_cast<unsigned>(blocks));
-    return blocks < (int64_t(1) << 31);
+dim3 blocks_of(int64_t m, int team, unsigned pieces) {
+    const int64_t per = kThreads / team;
+    return dim3(static_cast<unsigned>((m + per - 1) / per * pieces));
 }
 
 template <typename T, bool SPREAD>
@@ -518,18 +517,14 @@ cudaError_t dispatch_s(const DispatchArgs& a, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const int team = team_of(a.n, W, kThreads);
     const unsigned pieces = pieces_of(a.n, W, team, 4);
-    dim3 grid;
-    if (!blocks_of(a.m, team, pieces, grid)) return cudaErrorInvalidValue;
-    return launch_after(dispatch_kernel<T, W, SPREAD>, grid, kThreads, 0, st, a, team, pieces);
+    return launch_after(dispatch_kernel<T, W, SPREAD>, blocks_of(a.m, team, pieces), kThreads, 0, st, a, team, pieces);
 }
 template <typename T, int K, bool SPREAD>
 cudaError_t combine_k(const CombineArgs& a, cudaStream_t st) {
     constexpr int W = 16 / sizeof(T);
     const int team = team_of(a.n, W, kThreads);
     const unsigned pieces = pieces_of(a.n, W, team, combine_runs(K));
-    dim3 grid;
-    if (!blocks_of(a.m, team, pieces, grid)) return cudaErrorInvalidValue;
-    return launch_after(combine_kernel<T, W, K, SPREAD>, grid, kThreads, 0, st, a, team, pieces);
+    return launch_after(combine_kernel<T, W, K, SPREAD>, blocks_of(a.m, team, pieces), kThreads, 0, st, a, team, pieces);
 }
 template <typename T, int K, bool SPREAD>
 cudaError_t combine_back_k(const CombineBackArgs& a, cudaStream_t st) {

@@ -183,3 +183,11 @@ def test_reference_closed_forms():
     w, _ = ref.route_weights(l, ref.choose(l, 2), "softmax", True, 3.0)
     assert torch.allclose(w, torch.tensor([[1.5, 1.5], [0.0, 0.0], [1.5, 1.5]], dtype=torch.float64))
     assert ref.plan(torch.tensor([[1, 0], [-1, 1]], dtype=torch.int32), 3) == ([0, 1, 3, 3], [1, 0, -1, 2])
+
+
+def test_exchanges_of_more_blocks_than_a_grid_are_unsupported(L):
+    """Rows for which no device has memory: refused as too large before any launch."""
+    m, n = 1 << 26, 1 << 22
+    assert L.expert_dispatch(P, 0, m, n, n, P, P, 8, 1, P, n, None) == UNS
+    assert L.expert_combine(P, 0, n, P, None, None, 0, m, n, 1, P, n, None) == UNS
+    assert L.expert_combine_backward(P, 0, n, P, n, P, P, 8, P, m, n, 1, P, n, P, None) == UNS
