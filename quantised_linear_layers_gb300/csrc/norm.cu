@@ -332,17 +332,32 @@ __global__ void __launch_bounds__(kThreads) norm_any_kernel(const NormArgs p) {
         const T* x = static_cast<const T*>(p.x) + row * p.sx;
         O* y = static_cast<O*>(p.y) + row * p.sy;
         const T zero = from_f32<T>(0.0f);
-        float one[1] = {0.0f};
-        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) one[0] += to_f32(load_one(x + i, p.bnd, 0, zero));
+        LongSum sum;
+        for (int64_t i0 = threadIdx.x; i0 < p.n; i0 += kLongRun * kThreads) {
+            const int64_t i1 = i0 + long_run(i0, p.n, kThreads) * kThreads;
+            float run = 0.0f;
+#pragma unroll 16
+            for (int64_t i = i0; i < i1; i += kThreads) run += to_f32(load_one(x + i, p.bnd, 0, zero));
+            sum.add(run);
+        }
+        float one[1] = {sum.value()};
         __syncthreads();                     // the last row's sums have been read
         sum_over_row<1, false>(one, s_sum);
         const float about = one[0] / n;
-        float two[2] = {0.0f, 0.0f};
-        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
-            const float d = to_f32(load_one(x + i, p.bnd, 0, zero)) - about;
-            two[0] += d;
-            two[1] = fmaf(d, d, two[1]);
+        LongSum s1, s2;
+        for (int64_t i0 = threadIdx.x; i0 < p.n; i0 += kLongRun * kThreads) {
+            const int64_t i1 = i0 + long_run(i0, p.n, kThreads) * kThreads;
+            float r1 = 0.0f, r2 = 0.0f;
+#pragma unroll 16
+            for (int64_t i = i0; i < i1; i += kThreads) {
+                const float d = to_f32(load_one(x + i, p.bnd, 0, zero)) - about;
+                r1 += d;
+                r2 = fmaf(d, d, r2);
+            }
+            s1.add(r1);
+            s2.add(r2);
         }
+        float two[2] = {s1.value(), s2.value()};
         sum_over_row<2, false>(two, s_sum + 32);
         const float off = two[0] / n;
         const float rstd = rstd_of(off, two[1] / n, p.eps);

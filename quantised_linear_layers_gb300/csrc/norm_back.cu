@@ -284,14 +284,23 @@ __global__ void __launch_bounds__(kThreads) norm_dx_any_kernel(const NormBackArg
         const D* dy = static_cast<const D*>(p.dy) + row * p.sdy;
         T* dx = static_cast<T*>(p.dx) + row * p.sdx;
         const float mean = load_one(p.mean + row, p.bnd, 2, 0.0f), rstd = load_one(p.rstd + row, p.bnd, 3, 0.0f);
-        float c[2] = {0.0f, 0.0f};
-        for (int64_t i = threadIdx.x; i < p.n; i += kThreads) {
-            float w[1];
-            load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 4);
-            const float g = __fmul_rn(to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))), w[0]);
-            c[0] += g;
-            c[1] = fmaf(g, (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd, c[1]);
+        LongSum s1, s2;
+        for (int64_t i0 = threadIdx.x; i0 < p.n; i0 += kLongRun * kThreads) {
+            const int count = long_run(i0, p.n, kThreads);
+            float r1 = 0.0f, r2 = 0.0f;
+#pragma unroll 8
+            for (int j = 0; j < count; ++j) {
+                const int64_t i = i0 + j * kThreads;
+                float w[1];
+                load_weights<1>(w, p.w, p.w_bf16, i, 1.0f, p.bnd, 4);
+                const float g = __fmul_rn(to_f32(load_one(dy + i, p.bnd, 0, from_f32<D>(0.0f))), w[0]);
+                r1 += g;
+                r2 = fmaf(g, (to_f32(load_one(x + i, p.bnd, 1, from_f32<T>(0.0f))) - mean) * rstd, r2);
+            }
+            s1.add(r1);
+            s2.add(r2);
         }
+        float c[2] = {s1.value(), s2.value()};
         __syncthreads();
         sum_over_row<2, false>(c, s_sum);
         const float c1 = c[0] / n, c2 = c[1] / n;
@@ -314,16 +323,24 @@ __global__ void __launch_bounds__(kThreads) norm_dw_any_kernel(const NormBackArg
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     if (col >= p.n) return;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows, r1 = r0 + rows < p.m ? r0 + rows : p.m;
-    float dw = 0.0f, db = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        const float dy = to_f32(load_one(static_cast<const D*>(p.dy) + r * p.sdy + col, p.bnd, 0, from_f32<D>(0.0f)));
-        const float x = to_f32(load_one(static_cast<const T*>(p.x) + r * p.sx + col, p.bnd, 1, from_f32<T>(0.0f)));
-        dw = fmaf(dy, (x - load_one(p.mean + r, p.bnd, 2, 0.0f)) * load_one(p.rstd + r, p.bnd, 3, 0.0f), dw);
-        db += dy;
+    LongSum dw, db;
+    for (int64_t first = r0; first < r1; first += kLongRun) {
+        const int count = long_run(first, r1, 1);
+        float run_w = 0.0f, run_b = 0.0f;
+#pragma unroll 8
+        for (int j = 0; j < count; ++j) {
+            const int64_t r = first + j;
+            const float dy = to_f32(load_one(static_cast<const D*>(p.dy) + r * p.sdy + col, p.bnd, 0, from_f32<D>(0.0f)));
+            const float x = to_f32(load_one(static_cast<const T*>(p.x) + r * p.sx + col, p.bnd, 1, from_f32<T>(0.0f)));
+            run_w = fmaf(dy, (x - load_one(p.mean + r, p.bnd, 2, 0.0f)) * load_one(p.rstd + r, p.bnd, 3, 0.0f), run_w);
+            run_b += dy;
+        }
+        dw.add(run_w);
+        db.add(run_b);
     }
     float* part = p.part + static_cast<int64_t>(blockIdx.y) * 2 * p.n;
-    store_one(part + col, dw, p.bnd, 6);
-    store_one(part + p.n + col, db, p.bnd, 6);
+    store_one(part + col, dw.value(), p.bnd, 6);
+    store_one(part + p.n + col, db.value(), p.bnd, 6);
 }
 
 // dw and db: the parts' sums, 32 columns by 16 shares of the parts per block, in a

@@ -13,6 +13,24 @@ namespace ql {
 
 constexpr int kNormRoom = 224 * 1024;     // shared memory of a block
 constexpr int64_t kNormLongest = 16384 - 16;       // columns of a row in a team's registers
+// Terms that a thread adds up one after the other where a sum may have any number of them; the
+// runs' sums are added up with what each addition rounds off (Neumaier), so that the error does
+// not grow with their number.
+constexpr int kLongRun = 64;
+struct LongSum {
+    float all = 0.0f, off = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float t = all + v;
+        off += fabsf(all) >= fabsf(v) ? (all - t) + v : (v - t) + all;
+        all = t;
+    }
+    __device__ __forceinline__ float value() const { return fabsf(all) < INFINITY ? all + off : all; }
+};
+// Terms of the run that begins at first and goes on by `step`, up to end.
+__device__ __forceinline__ int long_run(int64_t first, int64_t end, int step) {
+    const int64_t count = (end - first + step - 1) / step;
+    return count < kLongRun ? static_cast<int>(count) : kLongRun;
+}
 
 // ---------------------------------------------------------------- pairs of fp32
 using F2 = unsigned long long;

@@ -30,8 +30,8 @@ def close(got, want, tol, what=""):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, by {float(off[bad].max()):.3e} at most"
 
 
-def norm(x, w, b, eps, out_dtype):
-    """(y, its tolerance, h, mean, rstd, h's tolerance)."""
+def norm(x, w, b, eps, out_dtype, c=None):
+    """(y, its tolerance, h, mean, rstd, h's tolerance); c: additions that a term passes."""
     x = x.detach().cpu().double()
     n = x.shape[1]
     w = torch.ones(n, dtype=torch.float64) if w is None else w.detach().cpu().double()
@@ -40,7 +40,7 @@ def norm(x, w, b, eps, out_dtype):
     rstd = 1 / torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + eps)
     h = (x - mean) * rstd
     y = h * w + b
-    c = adds(n)
+    c = adds(n) if c is None else c
     # the mean within c U of the mean |x - mean| (one standard deviation at most), the
     # variance within 2 c U, six roundings on the way
     dh = U * (c + (c + 6) * h.abs())
@@ -48,15 +48,15 @@ def norm(x, w, b, eps, out_dtype):
     return y, tol * (1 + 2 ** -7), h, mean, rstd, dh
 
 
-def norm_backward(dy, x, w, eps, dx_dtype):
+def norm_backward(dy, x, w, eps, dx_dtype, c=None):
     """{name: (value, tolerance)} of dx, dw, db."""
-    _, _, h, mean, rstd, dh = norm(x, None, None, eps, torch.float32)
+    _, _, h, mean, rstd, dh = norm(x, None, None, eps, torch.float32, c)
     dy = dy.detach().cpu().double()
     n = h.shape[1]
     g = dy if w is None else dy * w.detach().cpu().double()
     c1, c2 = g.mean(1, keepdim=True), (g * h).mean(1, keepdim=True)
     dx = rstd * (g - c1 - h * c2)
-    c = adds(n)
+    c = adds(n) if c is None else c
     # h from the kept mean, which is rounded once more
     dh = dh + 2 * U * mean.abs() * rstd
     ga, gh = g.abs().mean(1, keepdim=True), (g * h).abs().mean(1, keepdim=True)

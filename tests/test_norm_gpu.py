@@ -218,3 +218,48 @@ def test_many_rows_that_start_anywhere(ops, m, n, x_dtype, out):
         x.copy_(acts(m, n, x_dtype, i))
         dy.copy_(1e-3 * acts(m, n, out, i + 9))
         check(ops, x, w, b, out, dy=dy)
+
+
+@pytest.mark.parametrize("n", [(1 << 20) + 3, 1 << 22])
+@pytest.mark.parametrize("x_dtype,out", [(BF, BF), (F, F), (F, BF), (BF, F)])
+def test_sums_of_long_rows_stay_exact(ops, n, x_dtype, out):
+    """Rows whose terms all err the same way: errors that do not grow with the row's length. A term
+    passes a run of 64 and two trees of 32."""
+    c = 80
+    g = torch.Generator().manual_seed(1)
+    x = (torch.where(torch.rand((2, n), generator=g) < 0.5, -1.1, 1.1) + torch.tensor([[0.3], [300.0]])).to(x_dtype).cuda()
+    dy = (1.1e-3 + 1e-5 * torch.randn((2, n), generator=g)).to(out).cuda()
+    y, stats = ops.layer_norm_saving(x, dtype=out)
+    want, tol, _, mean, rstd, _ = ref.norm(x, None, None, 1e-5, out, c)
+    ref.close(y, want, tol, "y")
+    ref.close(stats[0][:, None], mean, ref.U * (2 * mean.abs() + c / rstd), "mean")
+    ref.close(stats[1][:, None], rstd, ref.U * (c + 6) * rstd, "rstd")
+    dx, _, _ = ops.layer_norm_backward(dy, x, stats)
+    ref.close(dx, *ref.norm_backward(dy, x, None, 1e-5, x_dtype, c)["dx"], "dx")
+
+
+def test_sums_of_many_long_rows_stay_exact(ops):
+    """The gradients of weight and bias over 65536 rows alike: a term passes a run of 64 and the joins of
+    at most 10 parts."""
+    m, n, c = 65536, 16391, 80
+    x = acts(1, n, F)
+    dy = torch.full((1, n), 1.1e-3, device="cuda")
+    _, stats = ops.layer_norm_saving(x)
+    _, dw, db = ops.layer_norm_backward(dy.to(BF).expand(m, n), x.to(BF).expand(m, n), stats.expand(2, m).contiguous(), sums=True)
+    v = dy.to(BF).cpu().double()
+    h = (x.to(BF).cpu().double() - stats[0].cpu().double()) * stats[1].cpu().double()
+    # two roundings of h, one of the product
+    ref.close(db[None], m * v, c * ref.U * m * v, "db")
+    ref.close(dw[None], m * v * h, (c + 3) * ref.U * m * v * h.abs(), "dw")
+
+
+def test_an_infinity_in_long_rows_stays_one(ops):
+    m, n = 300, 16400
+    x, dy = acts(m, n, F), torch.ones((m, n), device="cuda")
+    dy[7, 3], dy[9, 5] = float("inf"), float("nan")
+    _, stats = ops.layer_norm_saving(x)
+    dx, _, db = ops.layer_norm_backward(dy, x, stats, sums=True)
+    assert db[3] == float("inf") and torch.isnan(db[5]) and torch.equal(db[10:], torch.full_like(db[10:], m))
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    bad[[7, 9]] = True
+    assert torch.isnan(dx[bad]).all() and torch.isfinite(dx[~bad]).all()
