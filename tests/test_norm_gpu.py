@@ -262,4 +262,4 @@ def test_an_infinity_in_long_rows_stays_one(ops):
     assert db[3] == float("inf") and torch.isnan(db[5]) and torch.equal(db[10:], torch.full_like(db[10:], m))
     bad = torch.zeros(m, dtype=torch.bool, device="cuda")
     bad[[7, 9]] = True
-    assert torch.isnan(dx[bad]).all() and torch.isfinite(dx[~bad]).all()
+    assert not torch.isfinite(dx[bad]).any() and torch.isfinite(dx[~bad]).all()       # g - mean(g) - h mean(g h): NaN or an infinity
