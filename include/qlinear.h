@@ -633,8 +633,8 @@ ql_status layer_norm_backward(const void* dy, ql_dtype dy_dtype, int64_t dy_stri
  * lower index. An expert with logit or bias -inf is out of reach and counts for
  * nothing; where fewer than k are left the rest of chosen is -1 with weight 0. A NaN
  * is chosen last, and the weights of a token with one among its logits or the bias are
- * NaN; so are those of a token with logit +inf under the softmax. experts <= 512,
- * k <= 32, groups <= 32. */
+ * NaN (the rest of its choice is fp32's); so are those of a token with logit +inf under
+ * the softmax. experts <= 512, k <= 32, groups <= 32. */
 #define QL_SCORE_SOFTMAX 0
 #define QL_SCORE_SIGMOID 1
 ql_status expert_route(const void* logits, ql_dtype logits_dtype, int64_t m, int experts, int64_t stride_m, const float* bias,

@@ -98,7 +98,9 @@ def combine(ys: torch.Tensor, plan: ops.ExpertPlan, weights: torch.Tensor | None
 class Router(torch.nn.Module):
     """Scores of every token for every expert, and the k it goes to.
 
-    The scores' products are fp32, and so are their weights unless the module is cast. With
+    The scores' products are torch's in fp32, under autocast too, and so are their weights unless
+    the module is cast. (Where the process lets fp32 products be TF32, by
+    torch.set_float32_matmul_precision, these are, and the choices follow them.) With
     ``balance`` the buffer ``bias`` ([experts], zero at first; keep it in fp32, whose steps
     are finer than ``balance_step``'s) is added to the scores that choose, not to the
     weights; ``balance_step`` moves it against the load of a batch. The other arguments
