@@ -200,9 +200,10 @@ __device__ __forceinline__ bool close_keys(uint32_t k1, uint32_t k2, float off) 
 //   s(hi) - s(lo) = s(hi) (1 - s(lo)) (1 - e^x) for a sigmoid, s(hi) (1 - e^x) for a softmax
 // against b2 - b1. x's rounding moves 1 - e^x by 2^-24 of itself (x e^x / (1 - e^x) is 1 at
 // most; for the lesser logit first it would go whole into the exponential). expf is within 2^-22
-// of itself, expm1f within 2^-23, and divisions, products and sums add 2^-24 each:
-// 16 * 2^-24 for the sigmoid; for the softmax 11 * 2^-24, the 37 * 2^-24 of its total (below) and
-// the rounding of hi - top. `off` has a quarter more, for the roundings of `by` and of itself;
+// of itself, which moves the sigmoid's factors by 1 - s(hi) and s(lo) of it, together by no more
+// than all of it; expm1f is within 2^-23, and divisions, products and sums add 2^-24 each:
+// 12 * 2^-24 for the sigmoid; for the softmax 9 * 2^-24, the 37 * 2^-24 of its total (below) and
+// the rounding of hi - top. `off` has a third more, for the roundings of `by` and of itself;
 // db's own is 2^-24 of it. What underflows or overflows on the way is below 2^-126.
 template <bool SIGMOID>
 __device__ __forceinline__ void add_difference(float l1, float b1, float l2, float b2, float top, float total, float& by, float& off) {
@@ -210,7 +211,7 @@ __device__ __forceinline__ void add_difference(float l1, float b1, float l2, flo
     const float gap = -expm1f(lo - hi) * (SIGMOID ? 1.0f / ((1.0f + expf(-hi)) * (1.0f + expf(lo))) : expf(hi - top) / total);
     const float ds = l1 < l2 ? -gap : gap, db = b2 - b1;
     by += ds - db;
-    off += gap * (SIGMOID ? 0x1.4p-20f : fmaf(top - hi, 0x1.2p-24f, 0x1p-18f)) + fabsf(db) * 0x1p-22f + 0x1p-126f;
+    off += gap * (SIGMOID ? 0x1p-20f : fmaf(top - hi, 0x1.2p-24f, 0x1p-18f)) + fabsf(db) * 0x1p-22f + 0x1p-126f;
 }
 template <bool SIGMOID>
 __device__ __forceinline__ bool surely_greater(float l1, float b1, float l2, float b2, float top, float total) {
@@ -589,10 +590,10 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
             kept |= all & (0u - all);                      // the first of them
         }
         if (scored && !nan) {
-            // what a group's score may be: its choices' errors, its sum's rounding and the ends' own
+            // what a group's score may be: its choices' errors, its sum's rounding and that of the ends
             const bool in_reach = group > kNanKey, stays = ((kept >> lane) & 1u) != 0u;
             const float score = value_of(group);
-            const float off = fmaf(fabsf(value_of(best)) + (sums && next > kNanKey ? fabsf(value_of(next)) : 0.0f), 0x1p-22f, 2.1f * score_off);
+            const float off = fmaf(fabsf(value_of(best)) + (sums && next > kNanKey ? fabsf(value_of(next)) : 0.0f), 0x1.8p-23f, 2.1f * score_off);
             const float low = score - off, high = score + off;
             const uint32_t least = low == low ? key_of(low) : kNanKey + 1, most = high == high ? key_of(high) : kAll;
             // the groups near the border between the best that stays out and the last that stays
