@@ -11,8 +11,8 @@
 // that matter are wider than it; the other tokens are done again in 64 bits.
 //
 // Bound by instructions, 500 to 1000 a token (memory would take 16384 x 256 fp32 2.6 us): 8 of
-// 256 experts for 16384 tokens 11.3 us, with a bias 13.0, by groups of sums 17.1, the
-// gradient 8 to 12; of 512 32, 41 and 43 (sixteen keys a lane, some of them spilled: 35 to 40
+// 256 experts for 16384 tokens 11.2 us, with a bias 12.7, by groups of sums 17.4, the
+// gradient 7 to 10; of 512 31, 42 and 43 (sixteen keys a lane, some of them spilled: 35 to 40
 // with the registers of four blocks an SM instead of eight); one token 3 us, a launch.
 #include "route.cuh"
 
@@ -207,9 +207,10 @@ __device__ __forceinline__ bool close_keys(uint32_t k1, uint32_t k2, float off) 
 // db's own is 2^-24 of it. What underflows or overflows on the way is below 2^-126.
 template <bool SIGMOID>
 __device__ __forceinline__ void add_difference(float l1, float b1, float l2, float b2, float top, float total, float& by, float& off) {
-    const float hi = fmaxf(l1, l2), lo = fminf(l1, l2);
+    const bool up = l1 < l2;
+    const float hi = up ? l2 : l1, lo = up ? l1 : l2;
     const float gap = -expm1f(lo - hi) * (SIGMOID ? 1.0f / ((1.0f + expf(-hi)) * (1.0f + expf(lo))) : expf(hi - top) / total);
-    const float ds = l1 < l2 ? -gap : gap, db = b2 - b1;
+    const float ds = up ? -gap : gap, db = b2 - b1;
     by += ds - db;
     off += gap * (SIGMOID ? 0x1p-20f : fmaf(top - hi, 0x1.2p-24f, 0x1p-18f)) + fabsf(db) * 0x1p-22f + 0x1p-126f;
 }
@@ -299,7 +300,7 @@ __device__ __forceinline__ void best_of_warp(double& v, int& at) {
     }
 }
 
-// A token whose choice hangs on gaps within the bound: one in a thousand, so the kernel ends
+// A token whose choice hangs on gaps within the bounds: one in 17000 of random ones, so the kernel ends
 // with this call and keeps no register for it. keys: its experts' keys; sure: the
 // groups that stay; open: those of which the best join them; top, total: its softmax's. A
 // warp has few lanes for 64 bits (16 cycles an instruction): they see only the open groups, and
