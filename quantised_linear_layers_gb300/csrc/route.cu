@@ -42,6 +42,20 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
+// Of unsigned integers by exchanges too. __reduce_max_sync is one instruction, but as it is
+// compiled here it has given a maximum of values that lanes no longer had (the last round's,
+// once in 100000 tokens of up to 32 experts, on other tokens every time): it is used only
+// where the outcome is looked over (16384 x 256 by groups 22.4 us without it).
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+__device__ __forceinline__ uint32_t warp_min(uint32_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -232,8 +246,8 @@ __device__ __forceinline__ int take_best(uint32_t* keys, int first, int size, ui
             mine = keys[e];
             at = e;
         }
-    best = __reduce_max_sync(kAll, mine);
-    at = __reduce_min_sync(kAll, mine == best ? at : 0x7fffffff);
+    best = warp_max(mine);
+    at = static_cast<int>(warp_min(mine == best ? static_cast<uint32_t>(at) : 0x7fffffffu));
     __syncwarp();
     if (best != kUnreached && (threadIdx.x & 31) == 0) keys[at] = kUnreached;
     __syncwarp();
@@ -261,6 +275,33 @@ __device__ __noinline__ bool surely_greater_group(const RouteArgs& p, const T* r
         if ((ra > kNanKey && close_keys(ka, ra, score_off)) || (rz > kNanKey && close_keys(kz, rz, score_off))) return false;
     }
     return by > off;
+}
+
+// The k best of a token's keys, the lowest index first, without the sorted runs: lane j gets the
+// j-th, its key, and all lanes the last one's key (kUnreached: fewer than k); `head` is the
+// largest of the lane's own nv that stay out. list: k ints.
+__device__ __noinline__ int choose_again(uint32_t* keys, int* list, int k, int nv, uint32_t& my_key, uint32_t& last, uint32_t& head) {
+    const int lane = threadIdx.x & 31;
+    my_key = kUnreached;
+    __syncwarp();
+    for (int r = 0; r < k; ++r) {
+        const int at = take_best(keys, 0, nv * 32, last);
+        if (last == kUnreached) break;
+        if (lane == r) {
+            my_key = last;
+            list[r] = at;
+        }
+    }
+    head = kUnreached;
+    for (int i = 0; i < nv; ++i) head = max(head, keys[lane * nv + i]);
+    __syncwarp();
+    int mine = -1;
+    if (my_key != kUnreached) {
+        mine = list[lane];
+        keys[mine] = my_key;
+    }
+    __syncwarp();
+    return mine;
 }
 
 // ---------------------------------------------------------------- what fp32 leaves open
@@ -356,9 +397,9 @@ __device__ __noinline__ void route_open(const RouteArgs& p, int64_t t, uint32_t*
                 best = keys[e];
                 at = e;
             }
-        const uint32_t most = __reduce_max_sync(kAll, best);
+        const uint32_t most = warp_max(best);
         if (most == kUnreached) break;
-        at = __reduce_min_sync(kAll, best == most ? at : 0x7fffffff);
+        at = static_cast<int>(warp_min(best == most ? static_cast<uint32_t>(at) : 0x7fffffffu));
         __syncwarp();
         if (lane == 0) {
             keys[at] = kUnreached;
@@ -582,14 +623,21 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
         // lane g has group g's
         uint32_t group = lane < p.groups ? best : kUnreached;
         if (sums && lane < p.groups && next > kNanKey) group = key_of(value_of(best) + value_of(next));
+        auto best_groups = [&](auto max_of) {
+            uint32_t kept = 0;
+            for (int r = 0; r < p.kept; ++r) {
+                const uint32_t v = (kept >> lane) & 1u ? kUnreached : group;
+                const uint32_t most = max_of(v);
+                if (most == kUnreached) break;
+                const uint32_t all = __ballot_sync(kAll, v == most);
+                kept |= all & (0u - all);                  // the first of them
+            }
+            return kept;
+        };
         uint32_t kept = 0;
-        for (int r = 0; r < p.kept; ++r) {
-            const uint32_t v = (kept >> lane) & 1u ? kUnreached : group;
-            const uint32_t most = __reduce_max_sync(kAll, v);
-            if (most == kUnreached) break;
-            const uint32_t all = __ballot_sync(kAll, v == most);
-            kept |= all & (0u - all);                      // the first of them
-        }
+        // (with scores a wrong group among them shows below: its bounds meet those of a better one that stays out)
+        if (scored && !nan) kept = best_groups([](uint32_t v) { return __reduce_max_sync(kAll, v); });
+        if (__popc(kept) != p.kept) kept = best_groups([](uint32_t v) { return warp_max(v); });
         if (scored && !nan) {
             // what a group's score may be: its choices' errors, its sum's rounding and that of the ends
             const bool in_reach = group > kNanKey, stays = ((kept >> lane) & 1u) != 0u;
@@ -598,8 +646,11 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
             const float low = score - off, high = score + off;
             const uint32_t least = low == low ? key_of(low) : kNanKey + 1, most = high == high ? key_of(high) : kAll;
             // the groups near the border between the best that stays out and the last that stays
-            const uint32_t out = __reduce_max_sync(kAll, in_reach && !stays ? most : kUnreached);
-            const uint32_t last = __reduce_min_sync(kAll, stays ? least : kAll);
+            uint32_t last = __reduce_min_sync(kAll, stays ? least : kAll), out = kUnreached;
+            if (__any_sync(kAll, stays ? least < last : in_reach && most >= last)) {
+                out = warp_max(in_reach && !stays ? most : kUnreached);
+                last = warp_min(stays ? least : kAll);
+            }
             if (out >= last) {
                 const bool above = stays && least > out, near = in_reach && !above && most >= last;
                 const uint32_t sure = __ballot_sync(kAll, above), open = __ballot_sync(kAll, near);
@@ -668,10 +719,23 @@ __global__ void __launch_bounds__(kWarps * 32, 8) route_kernel(const __grid_cons
         for (int i = 0; i < NV; ++i)
             if (of[i] == my_key && skip-- == 0) mine = first + i;
     }
+    // looked over: every choice is an expert's, behind the one before, and before all that stay out
+    uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
+    const int mine2 = __shfl_down_sync(kAll, mine, 1), mine_last = __shfl_sync(kAll, mine, p.k - 1);
+    bool wrong = my_key != kUnreached && mine < 0;
+    wrong |= lane < p.k - 1 && key2 != kUnreached && !(my_key > key2 || (my_key == key2 && mine < mine2));
+    wrong |= head > last || (head == last && last != kUnreached && e0 + NV <= mine_last);
+    if (__any_sync(kAll, wrong)) {
+        uint32_t k1, k2, k3;
+        mine = choose_again(keys, places, p.k, NV, k1, k2, k3);
+        my_key = k1;
+        last = k2;
+        head = k3;
+        key2 = __shfl_down_sync(kAll, my_key, 1);
+    }
     float lg = mine >= 0 ? to_f32(load_one(row + mine, p.bnd, 0, from_f32<T>(0.0f))) : -INFINITY;
     if (biased && !nan) {
         // gaps between choices next to one another, and from the last to what stays out
-        const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
         const bool ahead = lane < p.k - 1 && key2 > kNanKey && close_keys(my_key, key2, score_off);
         const uint32_t least = near_key(last, score_off);
         const bool near = last > kNanKey && head >= least;

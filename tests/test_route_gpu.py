@@ -350,3 +350,33 @@ def test_a_batchs_routing_can_be_saved(ops):
     back = torch.load(room)
     assert torch.equal(back["weights"], w) and torch.equal(back["experts"], e)
     assert w.untyped_storage().nbytes() == w.numel() * 4 == e.untyped_storage().nbytes()
+
+
+@pytest.mark.parametrize("n,k,dtype", [(20, 7, F), (32, 8, F), (32, 2, F), (32, 8, BF), (64, 6, F), (128, 8, F), (256, 8, F)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_choices_do_not_depend_on_timing(ops, n, k, dtype, score):
+    """Many tokens many times: every choice is a sort's."""
+    x = torch.randn((1 << 19, n), generator=torch.Generator(device="cuda").manual_seed(n), device="cuda").mul_(3).to(dtype)
+    want = torch.sort(x, dim=1, descending=True, stable=True)[1][:, :k].to(torch.int32)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(25):
+        wrong += (ops.route(x, k, None, score)[1] != want).any(1).sum()
+        wrong += (ops.route(x, k, None, score, 2, 2)[1] != want).any(1).sum()
+    assert wrong == 0
+
+
+@pytest.mark.parametrize("best", [1, 2])
+def test_groups_do_not_depend_on_timing(ops, best):
+    x = torch.randn((1 << 18, 32), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").mul_(2)
+    bias = 0.05 * torch.randn(32, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    for b in (None, bias):
+        c = torch.sigmoid(x.double()) if b is None else torch.sigmoid(x.double()) + b.double()
+        groups = torch.sort(c.view(-1, 8, 4), dim=2, descending=True)[0][:, :, :best].sum(2)
+        order = torch.sort(groups, dim=1, descending=True, stable=True)[1]
+        kept = torch.zeros_like(groups, dtype=torch.bool).scatter_(1, order[:, :3], True)
+        by = (x.double() if b is None else c).masked_fill(~kept.repeat_interleave(4, 1), -math.inf)
+        want = torch.sort(by, dim=1, descending=True, stable=True)[1][:, :4].to(torch.int32)
+        wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+        for _ in range(50):
+            wrong += (ops.route(x, 4, b, "sigmoid", 8, 3, best)[1] != want).any(1).sum()
+        assert wrong == 0
