@@ -3,7 +3,7 @@
 // A warp has a token; a lane has NV consecutive experts in registers. Choices are
 // compared as unsigned integers in the order of the numbers that they stand for:
 // 0 for an expert out of reach (logit or bias -inf), 1 for a NaN. Each of k rounds
-// takes the largest key of the warp, the lowest index first.
+// takes the largest key of the warp, the lowest index first; the outcome is looked over.
 //
 // The choice is what 64 bits say. Without a bias experts are compared by their
 // logits, since both scores rise with them: exact. With one, or where a group's
@@ -11,8 +11,8 @@
 // that matter are wider than it; the other tokens are done again in 64 bits.
 //
 // Bound by instructions, 500 to 1000 a token (memory would take 16384 x 256 fp32 2.6 us): 8 of
-// 256 experts for 16384 tokens 11.2 us, with a bias 12.7, by groups of sums 17.4, the
-// gradient 7 to 10; of 512 31, 42 and 43 (sixteen keys a lane, some of them spilled: 35 to 40
+// 256 experts for 16384 tokens 11.9 us, with a bias 13.4, by groups of sums 18.3, the
+// gradient 7 to 10; of 512 31, 43 and 44 (sixteen keys a lane, some of them spilled: 35 to 40
 // with the registers of four blocks an SM instead of eight); one token 3 us, a launch.
 #include "route.cuh"
 
@@ -45,7 +45,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Of unsigned integers by exchanges too. __reduce_max_sync is one instruction, but as it is
 // compiled here it has given a maximum of values that lanes no longer had (the last round's,
 // once in 100000 tokens of up to 32 experts, on other tokens every time): it is used only
-// where the outcome is looked over (16384 x 256 by groups 22.4 us without it).
+// where the outcome is looked over (8 % less time than by exchanges alone).
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
